@@ -93,6 +93,8 @@ def draw(rng):
     count = _log_size(rng, 1, 24)
     top = int(math.sqrt((2 ** 32 if op == "attend" else 2 ** 31) / (count * q_heads)))
     lens = [_log_size(rng, 1, min(top, 8192)) for _ in range(count)]
+    if op == "attend_step":  # a lone token has no gradient but dv: a training batch holds at least one longer sequence
+        lens[rng.randrange(count)] = _log_size(rng, 64, min(top, 8192))
     return _attend(op, ",".join(map(str, lens)), q_heads, kv_heads, head_dim)
 
 
