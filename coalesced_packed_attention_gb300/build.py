@@ -20,7 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libzl.so")
 SOURCES = ["zl_plan.cpp", "zl_placement.cpp", "zl_api.cu", "zl_fwd2.cu", "zl_bwd.cu", "zl_rowops.cu",
-           "zl_noalloc.cu"]
+           "zl_noalloc.cu", "zl_rope.cu", "zl_causal_plan.cpp", "zl_causal_api.cu", "zl_causal_fwd.cu",
+           "zl_causal_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
           "--expt-relaxed-constexpr", "-I", os.path.join(HERE, "..", "include")]

@@ -1,0 +1,122 @@
+// Internal tables and launch interfaces of the causal attention (host planner and kernels).
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <vector>
+
+#include "../../include/zl.h"
+
+namespace zl {
+
+// Query rows are packed by key head: the `group` query heads that share a key head are neighbours, so a
+// block of up to 128 rows is (tokens x group) with row r = token r / group, head r % group.  A block holds
+// tokens_per_block(group) whole tokens; its rows past tokens x group are never stored.
+constexpr int kCausalRows = 128;
+__host__ __device__ inline int tokens_per_block(int group) { return kCausalRows / group; }
+
+struct CausalSeq {
+  int64_t q_offset, kv_offset;
+  int32_t q_len, kv_len;
+  int64_t acc_block;  // first 128-row block of the sequence in the dQ accumulator: [kv head][query block]
+};
+
+// One forward tile: up to two query blocks of one (sequence, key head) over a range of key blocks.
+struct CausalTile {
+  int32_t seq, head, block;  // first query block (block, block + 1)
+  int32_t kv_lo, kv_hi;      // key blocks [kv_lo, kv_hi) of 128, as far as the rows see them
+  int32_t part;              // -1: final output; else the tile's slot of partial results
+};
+// One backward tile: 128 keys of one (sequence, key head).
+struct CausalBwdTile {
+  int32_t seq, head, block, pad;
+};
+// Rows whose key range was split: the combine of `parts` slots from `slot` on.
+struct CausalMerge {
+  int32_t seq, head, block, slot, parts, pad[3];
+};
+
+struct CausalFwdParams {
+  const CausalSeq* seqs;
+  const CausalTile* tiles;
+  const int32_t* tile_ptr;  // tiles of thread block b: [tile_ptr[b], tile_ptr[b + 1])
+  int32_t* status;
+  long long wait_limit;
+  int32_t withhold_load;
+  int32_t n_q_heads, group;
+  __nv_bfloat16* o;
+  float* lse;
+  float* part_o;    // [slot][256][d]
+  float* part_lse;  // [slot][256]
+  float scale_log2;
+};
+
+struct CausalMergeParams {
+  const CausalSeq* seqs;
+  const CausalMerge* groups;
+  int32_t n_groups, n_q_heads, group;
+  const float* part_o;
+  const float* part_lse;
+  __nv_bfloat16* o;
+  float* lse;
+};
+
+struct CausalBwdParams {
+  const CausalSeq* seqs;
+  const CausalBwdTile* tiles;
+  const int32_t* tile_ptr;
+  int32_t* status;
+  long long wait_limit;
+  int32_t withhold_load;
+  int32_t n_q_heads, n_kv_heads, group;
+  const float* lse;
+  const float* row_d;  // D, [q tokens][q heads]
+  float* acc;          // fp32 dQ accumulator, [block][d / 4][128][4]
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  int64_t dk_stride, dv_stride;
+  float scale, scale_log2;
+};
+
+cudaError_t launch_causal_fwd(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CausalFwdParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_causal_merge(int head_dim, const CausalMergeParams& p, int num_sms, cudaStream_t stream);
+// D = rowsum(dO * O) over every row of the query tensor, and zeroing of the dQ accumulator.
+cudaError_t launch_causal_bwd_pre(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* row_d,
+                                  int64_t rows, float* acc, int64_t acc_floats, int num_sms, cudaStream_t stream);
+cudaError_t launch_causal_bwd(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& tdo, const CausalBwdParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_causal_dq(int head_dim, const CausalSeq* seqs, int32_t n_seqs, int32_t n_q_heads,
+                             int32_t n_kv_heads, int64_t acc_blocks, const float* acc, __nv_bfloat16* dq,
+                             int64_t dq_stride, float scale, int num_sms, cudaStream_t stream);
+
+}  // namespace zl
+
+struct zl_causal_plan {
+  int32_t n_q_heads = 0, n_kv_heads = 0, head_dim = 0, group = 0;
+  int64_t q_tokens = 0, kv_tokens = 0;
+  int device = -1, num_sms = 0;
+  bool host_only = false, test_withhold = false;
+  bool shared_keys = false;  // two sequences read the same key rows: no backward
+
+  std::vector<zl::CausalSeq> seqs;
+  std::vector<zl::CausalTile> fwd_tiles;
+  std::vector<int32_t> fwd_ptr;
+  std::vector<zl::CausalBwdTile> bwd_tiles;
+  std::vector<int32_t> bwd_ptr;
+  std::vector<zl::CausalMerge> merges;
+  int32_t slots = 0;
+  int64_t acc_blocks = 0;
+  int64_t fwd_bytes = 0, bwd_bytes = 0;
+
+  void* dev_blob = nullptr;
+  zl::CausalSeq* d_seqs = nullptr;
+  zl::CausalTile* d_fwd_tiles = nullptr;
+  int32_t* d_fwd_ptr = nullptr;
+  zl::CausalBwdTile* d_bwd_tiles = nullptr;
+  int32_t* d_bwd_ptr = nullptr;
+  zl::CausalMerge* d_merges = nullptr;
+  int32_t* d_status = nullptr;
+};

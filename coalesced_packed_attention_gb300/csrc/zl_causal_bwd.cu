@@ -1,0 +1,736 @@
+// Backward of the causal attention over packed sequences with grouped heads (sm_103a).
+//
+// With P = exp(scale q k^T - LSE) over the visible keys and D_i = rowsum(dO_i * O_i):
+//   dV_j = sum_i P_ij dO_i,  dS_ij = P_ij (dO_i . V_j - D_i),
+//   dK_j = scale sum_i dS_ij Q_i,  dQ_i = scale sum_j dS_ij K_j,
+// the sums over i running over every query head of the key head's group.
+//
+// Query rows are packed as in the forward (row r = token r / group, head r % group), so the group's sum is the
+// product's own sum over rows: a tile is 128 keys of one key head and keeps K, V in shared memory and dK, dV in
+// TMEM while it walks the query blocks from the first that sees one of its keys to the sequence's last.  Every
+// dK, dV element is formed by one CTA in a fixed order.  Per block:
+//   S^T  = K Q_i^T      (SMEM x SMEM -> TMEM R0)   lanes = keys, columns = query rows
+//   dP^T = V dO_i^T     (SMEM x SMEM -> TMEM R1)
+//   softmax warpgroups (thread = key; each takes 64 columns): P^T (bf16) to TMEM over S^T, dS^T (bf16) to
+//   shared memory; a key sees the columns from `first` on, so the causal mask is one comparison a column and
+//   only blocks on the diagonal carry it
+//   dV  += P^T dO_i     (TMEM x SMEM)
+//   dQ_i = dS K         (SMEM x SMEM -> TMEM R1)
+//   dK  += dS^T Q_i     (SMEM x SMEM)
+//   the dQ warpgroup reads dQ_i, stages it 16 KB at a time and hands each chunk to the bulk-copy engine as one
+//   reduce-add into the fp32 accumulator, which a last kernel scales, rounds and writes out.
+// The key tiles of one head reach a query block in an order that may differ from run to run, so dQ may differ
+// in the last bits of its fp32 sum before it is rounded; dK, dV never do.
+//
+// Query rows past the sequence (other tokens of the packed tensors) and past tokens x group (never loaded) are
+// zeroed in shared memory: their P is 0, but the products over rows would still multiply what lies there, and
+// 0 x NaN is NaN.  So are key rows past the sequence.
+// Rounding: P and dS are bf16 operands of their products (relative 2^-9 each, independent from pair to pair);
+// S, dP, D and every sum are fp32; dQ, dK, dV are rounded once.
+// Roles and budget: warps 0-7 softmax (two warpgroups), 8-11 dQ drain, 12 TMA, 13 MMA, 14-15 idle; launched with
+// 128 registers a thread, traded with setmaxnreg to 136 / 152 / 88, per sub-partition 2 x 136 + 152 + 88 = 4 x 128,
+// exactly the launch allocation.  TMEM (512 columns): R0 [0,128), R1 [128,256), dV [256,256+d), dK [384,384+d).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "zl_causal.h"
+#include "zl_internal.h"
+#include "zl_ptx.cuh"
+
+namespace zl {
+
+namespace {
+
+template <int D>
+struct CausalBwdLayout {
+  static constexpr int kBox = 128 * 128;
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kK = 0;
+  static constexpr int kV = kK + kTile;
+  static constexpr int kQ = kV + kTile;             // 2 stages
+  static constexpr int kDO = kQ + 2 * kTile;        // 1 stage (free once dV has read it)
+  static constexpr int kDS = kDO + kTile;           // [128 keys][128 rows] bf16, two 128-byte-swizzled boxes
+  static constexpr int kStageBytes = 128 * 32 * 4;  // one 32-column chunk of a block's dQ, fp32
+  static constexpr int kStage = kDS + 2 * kBox;     // 2 staging buffers of the dQ drain
+  static constexpr int kLD = kStage + 2 * kStageBytes;  // [2 block parities] -LSE*log2(e) and -D of a block's rows
+  static constexpr int kBar = kLD + 2 * 2 * 128 * 4;
+  static constexpr int kNumBars = 21;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kBytes = kMisc + 32;
+};
+
+constexpr float kLog2eC = 1.44269504088896340736f;
+constexpr float kInfC = __builtin_huge_valf();
+
+__device__ __forceinline__ bool cbwait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit,
+                                       int32_t* status) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (mbar_try_wait(a, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > limit) {
+      *abort_flag = 1;
+      atomicCAS(status, 0, ZL_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// Bulk reduce-add of fp32 from shared into global memory, tracked by this thread's bulk groups.
+__device__ __forceinline__ void bulk_add_f32(float* gdst, uint32_t ssrc, uint32_t bytes) {
+  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(gdst), "r"(ssrc),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// until at most one of this thread's bulk groups still has to read its source
+__device__ __forceinline__ void bulk_read_all_but_1() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_all_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// TMEM column of the packed bf16 P^T in R0 for K-step kk (16 rows): rows 0-63 are packed by warpgroup 0 into
+// columns [0,32), rows 64-127 by warpgroup 1 into [64,96), each over S^T columns it has already read.
+__device__ __forceinline__ uint32_t p_col(int kk) { return (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8); }
+
+constexpr uint32_t kLaunchRegs = 128;
+constexpr uint32_t kSoftmaxRegs = 136, kDrainRegs = 152, kMiscRegs = 88;
+static_assert(2 * kSoftmaxRegs + kDrainRegs + kMiscRegs == 4 * kLaunchRegs,
+              "register split must equal the launch allocation");
+template <uint32_t N>
+__device__ __forceinline__ void set_regs() {
+  static_assert(N % 8 == 0 && N >= 24 && N <= 256, "setmaxnreg takes a multiple of 8 in [24, 256]");
+  if constexpr (N > kLaunchRegs)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else if constexpr (N < kLaunchRegs)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void tma_rows(void* dst, const void* map, uint64_t* bar, int c0, int head, int tok) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(0), "r"(head), "r"(tok), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The query blocks that a key tile walks: [first, end).
+struct BwdSpan {
+  int first, n, nqb;
+};
+__device__ __forceinline__ BwdSpan walk_of(int block, int q_len, int kv_len, int tb) {
+  BwdSpan s;
+  s.nqb = (q_len + tb - 1) / tb;
+  const int t0 = max(0, block * 128 - (kv_len - q_len));  // first token that sees the tile's first key
+  s.first = min(s.nqb, t0 / tb);
+  s.n = s.nqb - s.first;
+  return s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(512, 1)
+    zl_causal_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                         const CausalBwdParams p) {
+  using L = CausalBwdLayout<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* kv_full = bar + 0;
+  uint64_t* kv_empty = bar + 1;
+  uint64_t* q_full = bar + 2;   // [2]
+  uint64_t* q_empty = bar + 4;  // [2]
+  uint64_t* do_full = bar + 6;
+  uint64_t* do_empty = bar + 7;     // dV (the last reader of dO) complete
+  uint64_t* s_full = bar + 8;       // S^T of the block in TMEM R0
+  uint64_t* ds_ready = bar + 9;     // dS^T in shared memory, dP^T read out of R1 (256 arrivals)
+  uint64_t* dq_full = bar + 10;
+  uint64_t* dq_empty = bar + 11;
+  uint64_t* kv_done = bar + 12;
+  uint64_t* drain = bar + 13;
+  uint64_t* ld_full = bar + 14;     // LSE / D of a query block staged in shared memory
+  uint64_t* p_ready = bar + 15;     // P^T in TMEM R0 (256 arrivals): the dV product may start
+  uint64_t* dp_full = bar + 16;     // dP^T of the block in TMEM R1
+  uint64_t* stage_full = bar + 17;  // [2] a dQ chunk written to staging buffer b (128 arrivals)
+  uint64_t* stage_free = bar + 19;  // [2] the reduce-add of buffer b has read it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);
+  float* sLD = reinterpret_cast<float*>(smem + L::kLD);  // block parity b: LSE at 256 b, D at 256 b + 128
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need a 1024-byte aligned base
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, ZL_ERR_UNSUPPORTED);
+    return;
+  }
+  const int tb = tokens_per_block(p.group), box_rows = tb * p.group;
+  // rows past the box are never loaded: zero once what lies there
+  for (int b = 0; b < 3 * (D / 64); ++b) {
+    uint8_t* box = smem + L::kQ + b * L::kBox;  // Q stage 0, Q stage 1, dO
+    for (int i = box_rows * 8 + threadIdx.x; i < 128 * 8; i += 512)
+      reinterpret_cast<uint4*>(box)[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
+      mbar_init(stage_full + i, 128);
+      mbar_init(stage_free + i, 1);
+    }
+    mbar_init(do_full, 1);
+    mbar_init(do_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_ready, 256);
+    mbar_init(ds_ready, 256);
+    mbar_init(dq_full, 1);
+    mbar_init(dq_empty, 128);
+    mbar_init(kv_done, 1);
+    mbar_init(drain, 1);
+    mbar_init(ld_full, 256);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_do);
+  }
+  if (warp == 13) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  uint8_t* sK = smem + L::kK;
+  uint8_t* sV = smem + L::kV;
+  uint8_t* sQ = smem + L::kQ;
+  uint8_t* sDO = smem + L::kDO;
+  uint8_t* sDS = smem + L::kDS;
+  const int t_begin = p.tile_ptr[blockIdx.x], t_end = p.tile_ptr[blockIdx.x + 1];
+
+  if (warp >= 12) {
+    set_regs<kMiscRegs>();
+    if (warp == 12) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        const uint32_t row_bytes = (uint32_t)(D / 64) * (uint32_t)box_rows * 128u;
+        uint32_t kt = 0, qit = 0, dit = 0;
+        bool ok = true;
+        for (int t = t_begin; t < t_end && ok; ++t) {
+          const CausalBwdTile tl = p.tiles[t];
+          const CausalSeq sq = p.seqs[tl.seq];
+          const BwdSpan sp = walk_of(tl.block, sq.q_len, sq.kv_len, tb);
+          if (sp.n == 0) continue;
+          if (!cbwait(kv_empty, (kt & 1) ^ 1, abort_flag, p.wait_limit, p.status)) break;
+          ++kt;
+          const int kvrow = (int)(sq.kv_offset + (int64_t)tl.block * 128);
+          mbar_arrive_expect_tx(kv_full, 2 * L::kTile);
+          if (p.withhold_load && kt == 1) {
+            // test hook: the announced bytes never arrive; a bounded wait runs out
+          } else {
+            for (int c = 0; c < D / 64; ++c) {
+              tma_load_3d(sK + c * L::kBox, &tm_k, kv_full, 64 * c, tl.head, kvrow);
+              tma_load_3d(sV + c * L::kBox, &tm_v, kv_full, 64 * c, tl.head, kvrow);
+            }
+          }
+          for (int is = 0; is < sp.n; ++is) {
+            const int tok = (int)(sq.q_offset + (int64_t)(sp.first + is) * tb);
+            const uint32_t st = qit & 1, ph = (qit >> 1) & 1;
+            if (!cbwait(q_empty + st, ph ^ 1, abort_flag, p.wait_limit, p.status)) { ok = false; break; }
+            mbar_arrive_expect_tx(q_full + st, row_bytes);
+            for (int c = 0; c < D / 64; ++c)
+              tma_rows(sQ + st * L::kTile + c * L::kBox, &tm_q, q_full + st, 64 * c, tl.head, tok);
+            ++qit;
+            if (!cbwait(do_empty, (dit & 1) ^ 1, abort_flag, p.wait_limit, p.status)) { ok = false; break; }
+            mbar_arrive_expect_tx(do_full, row_bytes);
+            for (int c = 0; c < D / 64; ++c) tma_rows(sDO + c * L::kBox, &tm_do, do_full, 64 * c, tl.head, tok);
+            ++dit;
+          }
+        }
+        if (*abort_flag) {
+          // the copies in flight land before the block's shared memory goes back (a bounded wait each)
+          auto settle = [](uint64_t* b, uint32_t parity) {
+            const long long t0 = clock64();
+            while (!mbar_try_wait(smem_u32(b), parity) && clock64() - t0 < 2000000) {
+            }
+          };
+          if (kt) settle(kv_full, (kt - 1) & 1);
+          if (dit) settle(do_full, (dit - 1) & 1);
+          for (uint32_t b = 1; b <= 2; ++b)
+            if (qit >= b) settle(q_full + ((qit - b) & 1), ((qit - b) >> 1) & 1);
+        }
+      }
+    } else if (warp == 13) {
+      // ------------------------------------------------------------ MMA issuer (warp-uniform; one elected lane)
+      constexpr uint32_t kIdSq = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t kIdKV = idesc_bf16(128, D, false, true);
+      constexpr uint32_t kIdDQ = idesc_bf16(128, D, true, true);
+      const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), aQ = smem_u32(sQ), aDO = smem_u32(sDO), aDS = smem_u32(sDS);
+      const uint32_t tR0 = tmem, tR1 = tmem + 128, tdV = tmem + 256, tdK = tmem + 384;
+      auto wait_w = [&](uint64_t* b, uint32_t parity) {
+        return __all_sync(0xffffffffu, cbwait(b, parity, abort_flag, p.wait_limit, p.status));
+      };
+      // low words of the operand descriptors (K-major: LBO 16 B; MN-major: LBO one 16 KB box)
+      const uint32_t kK = sdesc_lo(aK, 16), kV = sdesc_lo(aV, 16), kQ = sdesc_lo(aQ, 16), kDO = sdesc_lo(aDO, 16);
+      const uint32_t kDS = sdesc_lo(aDS, 16);
+      const uint32_t mK = sdesc_lo(aK, L::kBox), mQ = sdesc_lo(aQ, L::kBox), mDO = sdesc_lo(aDO, L::kBox);
+      const uint32_t mDS = sdesc_lo(aDS, L::kBox);
+      auto dsc = [](uint32_t lo, uint32_t bytes) { return sdesc_join(lo + (bytes >> 4)); };
+      uint32_t kt = 0, qit = 0, nblocks = 0;
+      bool ok = true;
+      for (int t = t_begin; t < t_end && ok; ++t) {
+        const CausalBwdTile tl = p.tiles[t];
+        const CausalSeq sq = p.seqs[tl.seq];
+        const BwdSpan sp = walk_of(tl.block, sq.q_len, sq.kv_len, tb);
+        if (sp.n == 0) continue;
+        if (!wait_w(kv_full, kt & 1)) break;
+        ++kt;
+        const int kvrows = sq.kv_len - tl.block * 128;
+        if (kvrows < 128) {
+          zero_tile_rows<D>(aK, kvrows, lane);
+          zero_tile_rows<D>(aV, kvrows, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        // rows of the walk's last block that belong to the sequence
+        const int last_rows = (sq.q_len - (sp.nqb - 1) * tb) * p.group;
+        auto fix_rows = [&](int is, uint32_t tile) {
+          if (is == sp.n - 1 && last_rows < box_rows) {
+            zero_tile_rows<D>(tile, last_rows, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        };
+        tc_fence_after();
+        auto issue_s = [&](uint32_t st) {  // S^T = K Q^T of the query block in stage st
+          const uint32_t dq = kQ + ((st * L::kTile) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
+            mma_ss_w(tR0, dsc(kK, off), dsc(dq, off), kIdSq, kk > 0);
+          }
+          mma_commit_w(s_full);
+        };
+        if (!wait_w(q_full + (qit & 1), (qit >> 1) & 1)) break;
+        fix_rows(0, aQ + (qit & 1) * L::kTile);
+        tc_fence_after();
+        issue_s(qit & 1);
+        for (int is = 0; is < sp.n; ++is) {
+          const uint32_t st = qit & 1;
+          if (!wait_w(do_full, qit & 1)) { ok = false; break; }
+          fix_rows(is, aDO);
+          if (nblocks > 0 && !wait_w(dq_empty, (nblocks - 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {  // dP^T = V dO^T
+            const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
+            mma_ss_w(tR1, dsc(kV, off), dsc(kDO, off), kIdSq, kk > 0);
+          }
+          mma_commit_w(dp_full);
+          if (!wait_w(p_ready, nblocks & 1)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)  // dV += P^T dO
+            mma_ts_w(tdV, tR0 + p_col(kk), dsc(mDO, kk * 2048), kIdKV, (is > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_w(do_empty);
+          if (is + 1 < sp.n) {
+            // S^T of the next block as soon as dV has read P^T out of R0 (products run in issue order)
+            const uint32_t st2 = (qit + 1) & 1, ph2 = ((qit + 1) >> 1) & 1;
+            if (!wait_w(q_full + st2, ph2)) { ok = false; break; }
+            fix_rows(is + 1, aQ + st2 * L::kTile);
+            tc_fence_after();
+            issue_s(st2);
+          }
+          if (!wait_w(ds_ready, nblocks & 1)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)  // dQ = dS K (both operands MN-major), first: the drain starts on it
+            mma_ss_w(tR1, dsc(mDS, kk * 2048), dsc(mK, kk * 2048), kIdDQ, kk > 0);
+          mma_commit_w(dq_full);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {  // dK += dS^T Q
+            const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
+            mma_ss_w(tdK, dsc(kDS, off), dsc(mQ, st * L::kTile + kk * 2048), kIdKV, (is > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit_w(q_empty + st);
+          ++qit;
+          ++nblocks;
+        }
+        if (!ok) break;
+        mma_commit_w(kv_done);
+        mma_commit_w(kv_empty);
+      }
+      mma_commit_w(drain);
+      wait_w(drain, 0);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ dQ drain warpgroup (thread = query row)
+    set_regs<kDrainRegs>();
+    constexpr int kChunks = D / 32;
+    const int t_row = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t aStage = smem_u32(smem + L::kStage);
+    uint32_t nblocks = 0, sit = 0;  // sit: chunks staged so far
+    bool ok = true;
+    for (int t = t_begin; t < t_end && ok; ++t) {
+      const CausalBwdTile tl = p.tiles[t];
+      const CausalSeq sq = p.seqs[tl.seq];
+      const BwdSpan sp = walk_of(tl.block, sq.q_len, sq.kv_len, tb);
+      float* acc_hd = p.acc + (sq.acc_block + (int64_t)tl.head * sp.nqb) * (128 * D);
+      for (int is = 0; is < sp.n; ++is) {
+        if (!__all_sync(0xffffffffu, cbwait(dq_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
+        tc_fence_after();
+        uint32_t u[kChunks][32];  // all of the row: R1 is released before any reduction is issued
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) tmem_ld32(tmem + lane_base + 128 + 32 * c, u[c]);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(dq_empty);  // the next block's dP^T may overwrite R1
+        // chunk c (columns 32c..32c+31) of a block is 16 KB contiguous in the accumulator, [8 column
+        // groups][128 rows][4]; two buffers, so one chunk is staged while the previous one is read
+        float* blk = acc_hd + (int64_t)(sp.first + is) * (128 * D);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const uint32_t b = sit & 1, use = sit >> 1;
+          if (!__all_sync(0xffffffffu, cbwait(stage_free + b, (use & 1) ^ 1, abort_flag, p.wait_limit, p.status))) {
+            ok = false;
+            break;
+          }
+          const uint32_t sb = aStage + b * L::kStageBytes;
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            sts_v4(sb + (g * 128 + t_row) * 16, u[c][4 * g], u[c][4 * g + 1], u[c][4 * g + 2], u[c][4 * g + 3]);
+          fence_proxy_async_smem();
+          mbar_arrive(stage_full + b);
+          if (warp == 8 && lane == 0 && cbwait(stage_full + b, use & 1, abort_flag, p.wait_limit, p.status)) {
+            bulk_add_f32(blk + c * (32 * 128), sb, L::kStageBytes);
+            bulk_commit_group();
+            bulk_read_all_but_1();  // the other buffer's reduce-add has read it
+            if (sit > 0) mbar_arrive(stage_free + (b ^ 1));
+          }
+          ++sit;
+        }
+        if (!ok) break;
+        ++nblocks;
+      }
+    }
+    if (warp == 8 && lane == 0) bulk_all_done();
+  } else {
+    // ------------------------------------------------------------ softmax warpgroups
+    // Two warpgroups share the TMEM lanes (lane = key) and split the columns: warpgroup wg takes query rows
+    // [64wg, 64wg+64) of S^T and dP^T and channels [wg d/2, (wg+1) d/2) of dK and dV.
+    set_regs<kSoftmaxRegs>();
+    constexpr int kHalfD = D / 2;
+    const int wg = warp >> 2;
+    const int t_key = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int qc0 = 64 * wg;
+    const int dc0 = kHalfD * wg;
+    const float sl2 = p.scale_log2;
+    const uint32_t aDSrow = smem_u32(sDS) + wg * L::kBox + t_key * 128;
+    // warpgroup 0 stages LSE and D: thread t_key holds packed row t_key
+    const int rt = t_key / p.group, rh = t_key - rt * p.group;
+    uint32_t nblocks = 0, ntiles = 0;
+    for (int t = t_begin; t < t_end; ++t) {
+      const CausalBwdTile tl = p.tiles[t];
+      const CausalSeq sq = p.seqs[tl.seq];
+      const BwdSpan sp = walk_of(tl.block, sq.q_len, sq.kv_len, tb);
+      const int key = tl.block * 128 + t_key;
+      const bool key_ok = key < sq.kv_len;
+      const int64_t ld_base = sq.q_offset * p.n_q_heads + (int64_t)tl.head * p.group + rh;
+      bool ok = true;
+      float lse_n = -kInfC, d_n = 0.f;
+      // rows past the sequence and rows that see no key (LSE = -inf) get exp2(-inf) = 0 everywhere
+      auto fetch = [&](int blk) {
+        const int tok = blk * tb + rt;
+        lse_n = -kInfC;
+        d_n = 0.f;
+        if (rt < tb && tok < sq.q_len) {
+          const int64_t i = ld_base + (int64_t)tok * p.n_q_heads;
+          const float l = __ldg(p.lse + i);
+          if (l != -kInfC) {
+            lse_n = -l * kLog2eC;
+            d_n = -__ldg(p.row_d + i);
+          }
+        }
+      };
+      if (wg == 0 && sp.n > 0) fetch(sp.first);
+      for (int is = 0; is < sp.n; ++is) {
+        if (wg == 0) {
+          sLD[256 * (nblocks & 1) + t_key] = lse_n;
+          sLD[256 * (nblocks & 1) + 128 + t_key] = d_n;
+        }
+        mbar_arrive(ld_full);  // bounded stand-in for a barrier of both warpgroups
+        if (!__all_sync(0xffffffffu, cbwait(ld_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
+        if (wg == 0 && is + 1 < sp.n) fetch(sp.first + is + 1);
+
+        const float* sLSE = sLD + 256 * (nblocks & 1);
+        const float* sD = sLSE + 128;
+        // first column (query row of the block) that sees this key; 128: none
+        const int first = key_ok ? max(0, (key - (sq.kv_len - sq.q_len) - (sp.first + is) * tb) * p.group) : 128;
+        if (!__all_sync(0xffffffffu, cbwait(s_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
+        tc_fence_after();
+        float pr[64];
+        {
+          uint32_t u0[32], u1[32];
+          tmem_ld32(tmem + lane_base + qc0, u0);
+          tmem_ld32(tmem + lane_base + qc0 + 32, u1);
+          tmem_ld_wait();
+          const float2 sl2v = make_float2(sl2, sl2);
+          const float2* nl2 = reinterpret_cast<const float2*>(sLSE + qc0);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x0 = fma2(make_float2(__uint_as_float(u0[2 * e]), __uint_as_float(u0[2 * e + 1])), sl2v, nl2[e]);
+            const float2 x1 =
+                fma2(make_float2(__uint_as_float(u1[2 * e]), __uint_as_float(u1[2 * e + 1])), sl2v, nl2[16 + e]);
+            pr[2 * e] = ex2(x0.x);
+            pr[2 * e + 1] = ex2(x0.y);
+            pr[32 + 2 * e] = ex2(x1.x);
+            pr[32 + 2 * e + 1] = ex2(x1.y);
+          }
+          if (first > qc0) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (qc0 + e < first) pr[e] = 0.f;
+          }
+        }
+        {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(pr[2 * e], pr[2 * e + 1]);
+          tmem_st32(tmem + lane_base + qc0, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_ready);
+
+        // dP^T of this block is issued after the previous block's dQ product, which read the dS^T buffer:
+        // once dP^T is complete the buffer may be rewritten
+        if (!__all_sync(0xffffffffu, cbwait(dp_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t u[32];
+          tmem_ld32(tmem + lane_base + 128 + qc0 + 32 * c, u);
+          tmem_ld_wait();
+          uint32_t pk[16];
+          const float2* nd2 = reinterpret_cast<const float2*>(sD + qc0 + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 ds = mul2(add2(make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])), nd2[e]),
+                                   make_float2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]));
+            pk[e] = pack_bf16(ds.x, ds.y);
+          }
+          // dS^T row t_key -> box wg of shared memory, 128-byte swizzle
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int chunk = 4 * c + g;
+            sts_v4(aDSrow + ((chunk ^ (t_key & 7)) << 4), pk[4 * g], pk[4 * g + 1], pk[4 * g + 2], pk[4 * g + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();  // the dP^T loads are complete: dQ may overwrite R1
+        mbar_arrive(ds_ready);
+        ++nblocks;
+      }
+      if (!ok) break;
+      // ---- dK, dV of this tile's keys (this warpgroup's channels)
+      if (sp.n > 0) {
+        if (!__all_sync(0xffffffffu, cbwait(kv_done, ntiles & 1, abort_flag, p.wait_limit, p.status))) break;
+        ++ntiles;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int c = 0; c < kHalfD / 32; ++c) {
+        uint32_t uv[32], uk[32];
+        if (sp.n > 0) {
+          tmem_ld32(tmem + lane_base + 256 + dc0 + 32 * c, uv);
+          tmem_ld32(tmem + lane_base + 384 + dc0 + 32 * c, uk);
+          tmem_ld_wait();
+        } else {  // no query: the keys' gradients are empty sums
+#pragma unroll
+          for (int e = 0; e < 32; ++e) uv[e] = uk[e] = 0u;
+        }
+        if (key_ok) {
+          const int64_t row = sq.kv_offset + key, col = (int64_t)tl.head * D + dc0 + 32 * c;
+          uint4* dv4 = reinterpret_cast<uint4*>(p.dv + row * p.dv_stride + col);
+          uint4* dk4 = reinterpret_cast<uint4*>(p.dk + row * p.dk_stride + col);
+          auto f = [](uint32_t x) { return __uint_as_float(x); };
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dv4[i] = make_uint4(pack_bf16(f(uv[8 * i]), f(uv[8 * i + 1])), pack_bf16(f(uv[8 * i + 2]), f(uv[8 * i + 3])),
+                                pack_bf16(f(uv[8 * i + 4]), f(uv[8 * i + 5])), pack_bf16(f(uv[8 * i + 6]), f(uv[8 * i + 7])));
+            dk4[i] = make_uint4(pack_bf16(f(uk[8 * i]) * p.scale, f(uk[8 * i + 1]) * p.scale),
+                                pack_bf16(f(uk[8 * i + 2]) * p.scale, f(uk[8 * i + 3]) * p.scale),
+                                pack_bf16(f(uk[8 * i + 4]) * p.scale, f(uk[8 * i + 5]) * p.scale),
+                                pack_bf16(f(uk[8 * i + 6]) * p.scale, f(uk[8 * i + 7]) * p.scale));
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// D = rowsum(dO * O): d / 8 lanes per row of the [tokens, heads, d] tensors, four rows' loads in flight; each
+// block first zeroes its share of the dQ accumulator.  HBM-bound: 4 d bytes read and 4 + 4 d written a row.
+template <int D>
+__global__ void __launch_bounds__(256) zl_causal_pre_kernel(const __nv_bfloat16* __restrict__ o,
+                                                            const __nv_bfloat16* __restrict__ d_o,
+                                                            float* __restrict__ row_d, int64_t rows,
+                                                            float* __restrict__ acc, int64_t acc4) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = 4;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, piece = lane % kLanes;
+  const int64_t nthreads = (int64_t)gridDim.x * blockDim.x;
+  float4* z4 = reinterpret_cast<float4*>(acc);
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < acc4; i += nthreads)
+    z4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int64_t nwarps = nthreads / 32;
+  for (int64_t base = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * (kRows * kUnroll); base < rows;
+       base += nwarps * (kRows * kUnroll)) {
+    uint4 a[kUnroll], b[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t row = base + u * kRows + sub;
+      a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows) {
+        a[u] = __ldg(reinterpret_cast<const uint4*>(o + row * D) + piece);
+        b[u] = __ldg(reinterpret_cast<const uint4*>(d_o + row * D) + piece);
+      }
+    }
+    auto dot2 = [](uint32_t x, uint32_t y, float s) {
+      s = fmaf(__uint_as_float(x << 16), __uint_as_float(y << 16), s);
+      return fmaf(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u), s);
+    };
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float s = dot2(a[u].w, b[u].w, dot2(a[u].z, b[u].z, dot2(a[u].y, b[u].y, dot2(a[u].x, b[u].x, 0.f))));
+#pragma unroll
+      for (int k = kLanes / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+      const int64_t row = base + u * kRows + sub;
+      if (piece == 0 && row < rows) row_d[row] = s;
+    }
+  }
+}
+
+// dQ: one block per 128-row accumulator block and 64-channel half, read in storage order, turned over in shared
+// memory, scaled, rounded to bf16 and written to the rows of its tokens.
+template <int D>
+__global__ void __launch_bounds__(256) zl_causal_dq_kernel(const CausalSeq* __restrict__ seqs, int32_t n_seqs,
+                                                           int32_t n_q_heads, int32_t n_kv_heads, int64_t n_slabs,
+                                                           const float* __restrict__ acc,
+                                                           __nv_bfloat16* __restrict__ dq, int64_t dq_stride,
+                                                           float scale) {
+  constexpr int kHalves = D / 64;
+  __shared__ float4 tile[128][17];
+  const int group = n_q_heads / n_kv_heads, tb = tokens_per_block(group);
+  for (int64_t sl = blockIdx.x; sl < n_slabs; sl += gridDim.x) {
+    const int64_t blk = sl / kHalves;
+    const int half = (int)(sl % kHalves);
+    int lo = 0, hi = n_seqs - 1;  // last sequence whose first block is <= blk (empty ones share their start)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (seqs[mid].acc_block <= blk) lo = mid; else hi = mid - 1;
+    }
+    const CausalSeq sq = seqs[lo];
+    const int nqb = (sq.q_len + tb - 1) / tb;
+    const int64_t in_seq = blk - sq.acc_block;
+    const int head = (int)(in_seq / nqb), qb = (int)(in_seq % nqb);
+    const float4* src = reinterpret_cast<const float4*>(acc) + sl * (128 * 16);
+    float4 x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = __ldg(src + u * 256 + threadIdx.x);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int k = u * 256 + threadIdx.x;  // piece (column group k / 128, row k % 128)
+      tile[k & 127][k >> 7] = x[u];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = u * 256 + threadIdx.x;  // row k / 8, 8 channels from 8 (k % 8) on
+      const int r = k >> 3, c = k & 7;
+      const int rt = r / group, tok = qb * tb + rt;
+      if (rt < tb && tok < sq.q_len) {
+        const float4 v = tile[r][2 * c], w = tile[r][2 * c + 1];
+        *reinterpret_cast<uint4*>(dq + (sq.q_offset + tok) * dq_stride +
+                                  ((int64_t)head * group + (r - rt * group)) * D + half * 64 + 8 * c) =
+            make_uint4(pack_bf16(v.x * scale, v.y * scale), pack_bf16(v.z * scale, v.w * scale),
+                       pack_bf16(w.x * scale, w.y * scale), pack_bf16(w.z * scale, w.w * scale));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Blocks of a grid-stride kernel of 256 threads: as many as can be resident at once, or fewer.
+template <typename K>
+int resident_grid(K kernel, int64_t blocks, int num_sms) {
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 256, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
+  const int64_t cap = (int64_t)num_sms * per_sm;
+  return (int)(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
+}
+
+}  // namespace
+
+cudaError_t launch_causal_bwd_pre(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* row_d,
+                                  int64_t rows, float* acc, int64_t acc_floats, int num_sms, cudaStream_t stream) {
+  auto k = head_dim == 128 ? zl_causal_pre_kernel<128> : zl_causal_pre_kernel<64>;
+  const int64_t by_rows = (rows + 8 * 4 * (256 / head_dim) - 1) / (8 * 4 * (256 / head_dim));
+  const int64_t by_acc = (acc_floats / 4 + 255) / 256;
+  k<<<resident_grid(k, by_rows > by_acc ? by_rows : by_acc, num_sms), 256, 0, stream>>>(o, d_o, row_d, rows, acc,
+                                                                                       acc_floats / 4);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_causal_bwd(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& tdo, const CausalBwdParams& p, int grid, cudaStream_t stream) {
+  const int smem = head_dim == 128 ? CausalBwdLayout<128>::kBytes : CausalBwdLayout<64>::kBytes;
+  const int smem_launch = smem > 120 * 1024 ? smem : 120 * 1024;  // one CTA per SM (TMEM 512 columns)
+  auto k = head_dim == 128 ? zl_causal_bwd_kernel<128> : zl_causal_bwd_kernel<64>;
+  static PerDeviceOnce configured[2];
+  cudaError_t e = configured[head_dim == 128].run([&] {
+    cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_launch);
+    if (r != cudaSuccess) return r;
+    // the register split adds up to exactly the launch allocation: a kernel built with another per-thread count
+    // would leave an increase waiting for registers forever
+    cudaFuncAttributes fa;
+    r = cudaFuncGetAttributes(&fa, k);
+    if (r != cudaSuccess) return r;
+    return fa.numRegs == (int)kLaunchRegs ? cudaSuccess : cudaErrorInvalidKernelImage;
+  });
+  if (e != cudaSuccess) return e;
+  k<<<grid, 512, smem_launch, stream>>>(tq, tk, tv, tdo, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_causal_dq(int head_dim, const CausalSeq* seqs, int32_t n_seqs, int32_t n_q_heads,
+                             int32_t n_kv_heads, int64_t acc_blocks, const float* acc, __nv_bfloat16* dq,
+                             int64_t dq_stride, float scale, int num_sms, cudaStream_t stream) {
+  const int64_t slabs = acc_blocks * (head_dim / 64);
+  if (slabs == 0) return cudaSuccess;
+  auto k = head_dim == 128 ? zl_causal_dq_kernel<128> : zl_causal_dq_kernel<64>;
+  k<<<resident_grid(k, slabs, num_sms), 256, 0, stream>>>(seqs, n_seqs, n_q_heads, n_kv_heads, slabs, acc, dq,
+                                                          dq_stride, scale);
+  return cudaGetLastError();
+}
+
+}  // namespace zl

@@ -37,6 +37,18 @@ class zl_work_item(ctypes.Structure):
                 ("out_offset", ctypes.c_int64), ("lse_offset", ctypes.c_int64)]
 
 
+class zl_qk_rope_desc(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("rot_dim", ctypes.c_int32), ("half_layout", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("axis_pairs", ctypes.c_int32 * 3), ("amplitude", ctypes.c_float)]
+
+
+class zl_causal_seq(ctypes.Structure):
+    _fields_ = [("q_offset", ctypes.c_int64), ("kv_offset", ctypes.c_int64),
+                ("q_len", ctypes.c_int32), ("kv_len", ctypes.c_int32)]
+
+
 class zl_bucket(ctypes.Structure):
     _fields_ = [("seq_len", ctypes.c_int64), ("count", ctypes.c_int32), ("time", ctypes.c_double),
                 ("mem", ctypes.c_double)]
@@ -77,6 +89,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "zl_get_device_status": (I32, [P, P, pI32]),
         "zl_status_string": (ctypes.c_char_p, [I32]),
         "zl_version": (I32, []),
+        "zl_rope_frequencies": (I32, [pD, I32, ctypes.POINTER(ctypes.c_uint64)]),
+        "zl_qk_rope_workspace": (I32, [ctypes.POINTER(zl_qk_rope_desc), pI64]),
+        "zl_qk_rope_fwd": (I32, [ctypes.POINTER(zl_qk_rope_desc), P, I64, P, I64, P, P, P, P, P, I64, P, I64, P]),
+        "zl_qk_rope_bwd": (I32, [ctypes.POINTER(zl_qk_rope_desc), P, I64, P, I64, P, P, P, P, P, I64, P, I64, P, I64,
+                                 P, I64, P, P, P, P]),
+        "zl_plan_causal": (I32, [ctypes.POINTER(zl_causal_seq), I32, I32, I32, I32, I64, I64, U32, ctypes.POINTER(P)]),
+        "zl_causal_plan_destroy": (None, [P]),
+        "zl_causal_plan_workspace": (I32, [P, pI64, pI64]),
+        "zl_causal_plan_tiles": (I32, [P, I32, pI32, I64, pI64]),
+        "zl_causal_attn_fwd": (I32, [P, P, I64, P, I64, P, I64, P, P, P, F, P]),
+        "zl_causal_attn_bwd": (I32, [P, P, I64, P, I64, P, I64, P, P, P, P, I64, P, I64, P, I64, P, F, P]),
+        "zl_causal_get_device_status": (I32, [P, P, pI32]),
         "zl_catalog_cut": (I32, [ctypes.POINTER(zl_bucket), I32, pI32, ctypes.POINTER(ctypes.c_double)]),
         "zl_pack_fillers": (I32, [pD, pD, I32, I32, pD, pD, ctypes.c_double, ctypes.c_double, pI32, pD, pD, pI32, pD]),
     }
@@ -382,7 +406,347 @@ def exported_symbols() -> List[str]:
             "zl_plan_count",
             "zl_plan_tiles", "zl_plan_group", "zl_coalesced_attn_fwd", "zl_merge_partials",
             "zl_coalesced_attn_bwd", "zl_bwd_preprocess", "zl_bwd_main", "zl_bwd_finalize",
-            "zl_get_device_status", "zl_status_string", "zl_version", "zl_catalog_cut", "zl_pack_fillers"]
+            "zl_get_device_status", "zl_status_string", "zl_version", "zl_catalog_cut", "zl_pack_fillers",
+            "zl_rope_frequencies", "zl_qk_rope_workspace", "zl_qk_rope_fwd", "zl_qk_rope_bwd", "zl_plan_causal",
+            "zl_causal_plan_destroy", "zl_causal_plan_workspace", "zl_causal_plan_tiles", "zl_causal_attn_fwd",
+            "zl_causal_attn_bwd", "zl_causal_get_device_status"]
+
+
+# ---------------------------------------------------------------- causal sequences
+def _heads(t, what, shape=None, dtype=None):
+    """(pointer, token stride) of a bf16 [tokens, heads, d] CUDA tensor whose heads are
+    contiguous; the token stride is free, so views of a fused projection pass."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise TypeError(f"{what}: expected a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what}: expected shape {shape or '[tokens, heads, d]'}, got {tuple(t.shape)}")
+    n, h, d = t.shape
+    if n == 0 or h == 0:
+        return None, h * d
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{what}: the heads of a token must be contiguous, got strides {t.stride()}")
+    stride = t.stride(0) if n > 1 else h * d  # a lone token has no next one
+    if stride < h * d:
+        raise ValueError(f"{what}: token stride {stride} below heads * d = {h * d}")
+    return t.data_ptr(), stride
+
+
+def _on_current_device(*tensors):
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.device.index != dev:
+            raise ValueError(f"tensor on cuda:{t.device.index}, current device is cuda:{dev}")
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                       original_len: int = 4096, slow: float = 1.0, fast: float = 32.0):
+    """(radians per position of the rot_dim / 2 pairs, amplitude) of a rotary embedding,
+    base^(-2i / rot_dim), optionally scaled for contexts `factor` times the original:
+      "linear"  every frequency divided by the factor (positions pressed together);
+      "ntk"     the base raised so that the slowest pair is divided by the factor, the
+                fastest kept;
+      "yarn"    pairs that turn more than `fast` times in original_len positions kept, those
+                under `slow` turns divided by the factor, a ramp over the turns between;
+                amplitude 0.1 ln(factor) + 1."""
+    import math
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim: expected an even number from 2 on, got {rot_dim}")
+    if not (base > 0 and factor >= 1 and original_len > 0 and fast > slow):
+        raise ValueError("expected base > 0, factor >= 1, original_len > 0 and fast > slow")
+    if scaling == "ntk":
+        base = base * factor ** (rot_dim / max(1, rot_dim - 2))
+    freqs = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    if scaling in (None, "ntk"):
+        return freqs, 1.0
+    if scaling == "linear":
+        return [f / factor for f in freqs], 1.0
+    if scaling == "yarn":
+        out = []
+        for f in freqs:
+            keep = min(1.0, max(0.0, (original_len * f / (2 * math.pi) - slow) / (fast - slow)))
+            out.append(f * keep + f / factor * (1 - keep))
+        return out, 0.1 * math.log(factor) + 1.0
+    raise ValueError(f"scaling: expected None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+
+
+@dataclass
+class RotaryTable:
+    """Frequencies of a rotation on one device, and how the pairs are laid out."""
+    freq: "object"  # int64 tensor holding the 64-bit fractions of a turn per position
+    rot_dim: int
+    half: bool
+    axis_pairs: List[int]
+    amplitude: float
+
+
+def rotary_table(inv_freq: Sequence[float], layout: str = "half", axis_pairs: Optional[Sequence[int]] = None,
+                 amplitude: float = 1.0, device="cuda") -> RotaryTable:
+    """Table for zl_qk_rope_fwd / bwd from radians per position, pair by pair.  layout: "half"
+    (channels p and p + pairs) or "interleaved" (2p and 2p + 1).  axis_pairs: how many pairs each
+    position axis turns, in order (default: one axis turns them all)."""
+    import torch
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"layout: expected 'half' or 'interleaved', got {layout!r}")
+    radians = [float(f) for f in inv_freq]
+    n = len(radians)
+    pairs = [int(a) for a in axis_pairs] if axis_pairs is not None else [n]
+    if not 1 <= len(pairs) <= 3 or min(pairs) < 0 or sum(pairs) != n:
+        raise ValueError(f"axis_pairs: expected one to three counts that add up to {n}, got {pairs}")
+    out = (ctypes.c_uint64 * max(1, n))()
+    _check(load_library().zl_rope_frequencies((ctypes.c_double * max(1, n))(*radians), n, out), "zl_rope_frequencies")
+    freq = torch.tensor([ctypes.c_int64(x).value for x in out[:n]], dtype=torch.int64).to(device)
+    return RotaryTable(freq, 2 * n, layout == "half", pairs, float(amplitude))
+
+
+def zl_qk_rope_workspace_bytes(n_tokens: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    """Scratch bytes of a zl_qk_rope_bwd that returns weight gradients."""
+    b = ctypes.c_int64()
+    desc = zl_qk_rope_desc(n_tokens, n_q_heads, n_kv_heads, head_dim, 1, 0.0, 0, 0, 0, (ctypes.c_int32 * 3)(), 1.0)
+    _check(load_library().zl_qk_rope_workspace(ctypes.byref(desc), ctypes.byref(b)), "zl_qk_rope_workspace")
+    return b.value
+
+
+def _rope_args(q, k, positions, table, norm, eps, q_weight, k_weight, others):
+    """Descriptor, and the pointers of positions, frequencies and weights."""
+    import torch
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError("q and k: at least one is needed")
+    if lead.dim() != 3:
+        raise ValueError(f"expected [tokens, heads, d], got {tuple(lead.shape)}")
+    n, _, d = lead.shape
+    hq, hk = (t.shape[1] if t is not None and t.dim() == 3 else 0 for t in (q, k))
+    _on_current_device(q, k, positions, q_weight, k_weight, table.freq if table is not None else None, *others)
+    if table is not None and table.rot_dim > 0:
+        axes = len(table.axis_pairs)
+        if positions is None:
+            raise ValueError("positions: a rotation needs them")
+        pos = _ptr(positions, torch.int32, "positions")
+        if tuple(positions.shape) not in ((n, axes),) + (((n,),) if axes == 1 else ()):
+            raise ValueError(f"positions: expected shape {(n, axes)}, got {tuple(positions.shape)}")
+        freq = _ptr(table.freq, torch.int64, "table", table.rot_dim // 2)
+        desc = zl_qk_rope_desc(n, hq, hk, d, int(norm), eps, table.rot_dim, int(table.half), axes,
+                               (ctypes.c_int32 * 3)(*table.axis_pairs), table.amplitude)
+    else:
+        pos = freq = None
+        desc = zl_qk_rope_desc(n, hq, hk, d, int(norm), eps, 0, 0, 0, (ctypes.c_int32 * 3)(), 1.0)
+    return desc, n, hq, hk, d, pos, freq, _ptr(q_weight, torch.float32, "q_weight", d), _ptr(k_weight, torch.float32, "k_weight", d)
+
+
+def _maybe_heads(t, what, n, h, d):
+    if t is None and h == 0:
+        return None, 0
+    return _heads(t, what, (n, h, d))
+
+
+def zl_qk_rope_fwd(q, k, q_out, k_out, positions, table: Optional[RotaryTable], norm: bool = False, q_weight=None,
+                   k_weight=None, eps: float = 1e-6, stream=None):
+    """Every head of q [tokens, Hq, d] and k [tokens, Hkv, d] (either may be None) normalised
+    (norm=True) and rotated at its token's positions (int32 [tokens, axes]; table None: no
+    rotation) into q_out, k_out, which may be q and k themselves."""
+    desc, n, hq, hk, d, pos, freq, qw, kw = _rope_args(q, k, positions, table, norm, eps, q_weight, k_weight,
+                                                       (q_out, k_out))
+    _check(load_library().zl_qk_rope_fwd(
+        ctypes.byref(desc), *_maybe_heads(q, "q", n, hq, d), *_maybe_heads(k, "k", n, hk, d), qw, kw, pos, freq,
+        *_maybe_heads(q_out, "q_out", n, hq, d), *_maybe_heads(k_out, "k_out", n, hk, d), _stream(stream)),
+        "zl_qk_rope_fwd")
+
+
+def zl_qk_rope_bwd(q, k, dq_out, dk_out, dq, dk, positions, table: Optional[RotaryTable], norm: bool = False,
+                   q_weight=None, k_weight=None, dq_weight=None, dk_weight=None, workspace=None, eps: float = 1e-6,
+                   stream=None):
+    """Gradient of zl_qk_rope_fwd: dq, dk from dq_out, dk_out.  With norm=True q and k are the
+    forward's inputs (else None will do) and dq_weight, dk_weight, where given, receive the
+    weights' gradients (workspace: zl_qk_rope_workspace_bytes)."""
+    import torch
+    desc, n, hq, hk, d, pos, freq, qw, kw = _rope_args(dq_out, dk_out, positions, table, norm, eps, q_weight, k_weight,
+                                                       (q, k, dq, dk, dq_weight, dk_weight, workspace))
+    if norm:
+        xq, xk = _maybe_heads(q, "q", n, hq, d), _maybe_heads(k, "k", n, hk, d)
+    else:
+        xq = xk = (None, 0)
+    need = None
+    if dq_weight is not None or dk_weight is not None:
+        need = zl_qk_rope_workspace_bytes(n, hq, hk, d)
+    _check(load_library().zl_qk_rope_bwd(
+        ctypes.byref(desc), *xq, *xk, qw, kw, pos, freq, *_maybe_heads(dq_out, "dq_out", n, hq, d),
+        *_maybe_heads(dk_out, "dk_out", n, hk, d), *_maybe_heads(dq, "dq", n, hq, d), *_maybe_heads(dk, "dk", n, hk, d),
+        _ptr(dq_weight, torch.float32, "dq_weight", d), _ptr(dk_weight, torch.float32, "dk_weight", d),
+        _ptr(workspace, torch.uint8, "workspace", need), _stream(stream)), "zl_qk_rope_bwd")
+
+
+class CausalPlan:
+    """Owner of one zl_causal_plan*.  Created by zl_plan_causal()."""
+
+    def __init__(self, handle: int, n_q_heads: int, n_kv_heads: int, head_dim: int, q_tokens: int, kv_tokens: int,
+                 device: Optional[int]):
+        self.handle = ctypes.c_void_p(handle)
+        self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
+        self.q_tokens, self.kv_tokens = q_tokens, kv_tokens
+        self.device = device  # CUDA device index the plan was built on (None: host-only plan)
+        f, b = ctypes.c_int64(), ctypes.c_int64()
+        _check(load_library().zl_causal_plan_workspace(self.handle, ctypes.byref(f), ctypes.byref(b)),
+               "zl_causal_plan_workspace")
+        self.fwd_workspace_bytes, self.bwd_workspace_bytes = f.value, b.value
+
+    def tiles(self, which: int = 0):
+        """Schedule as (sequence, key head, block, first key block, end key block, part, thread
+        block) tuples; which = 0 forward, 1 backward."""
+        n = ctypes.c_int64()
+        L = load_library()
+        _check(L.zl_causal_plan_tiles(self.handle, which, None, 0, ctypes.byref(n)), "zl_causal_plan_tiles")
+        buf = (ctypes.c_int32 * (7 * max(1, n.value)))()
+        _check(L.zl_causal_plan_tiles(self.handle, which, buf, n.value, ctypes.byref(n)), "zl_causal_plan_tiles")
+        return [tuple(buf[7 * i:7 * i + 7]) for i in range(n.value)]
+
+    def destroy(self):
+        if self.handle is not None and self.handle.value:
+            load_library().zl_causal_plan_destroy(self.handle)
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def causal_seqs(lengths: Sequence[int]):
+    """Sequences of self-attention packed one behind the other: (q_offset, q_len, kv_offset,
+    kv_len) each, for zl_plan_causal."""
+    out, at = [], 0
+    for n in lengths:
+        out.append((at, n, at, n))
+        at += n
+    return out
+
+
+def zl_plan_causal(seqs: Sequence, n_q_heads: int, n_kv_heads: int, head_dim: int, q_tokens: int, kv_tokens: int,
+                   flags: int = 0) -> CausalPlan:
+    """Plan over seqs = [(q_offset, q_len, kv_offset, kv_len), ...] on the current device."""
+    L = load_library()
+    arr = (zl_causal_seq * max(1, len(seqs)))()
+    for i, (qo, ql, ko, kl) in enumerate(seqs):
+        for name, x, bits in (("q_offset", qo, 63), ("q_len", ql, 31), ("kv_offset", ko, 63), ("kv_len", kl, 31)):
+            if not -(1 << bits) <= x < (1 << bits):
+                raise ValueError(f"sequence {i}: {name} {x} does not fit {bits + 1} bits")
+        arr[i] = zl_causal_seq(qo, ko, ql, kl)
+    h = ctypes.c_void_p()
+    device = _plan_device(flags)
+    _check(L.zl_plan_causal(arr, len(seqs), n_q_heads, n_kv_heads, head_dim, q_tokens, kv_tokens, flags,
+                            ctypes.byref(h)), "zl_plan_causal")
+    return CausalPlan(h.value, n_q_heads, n_kv_heads, head_dim, q_tokens, kv_tokens, device)
+
+
+def allocate_causal(plan: CausalPlan, device="cuda", backward: bool = False) -> Dict[str, "object"]:
+    """Outputs, workspace and (backward) gradients of a causal plan, uninitialised."""
+    import torch
+    bf = dict(dtype=torch.bfloat16, device=device)
+    ws = max(plan.fwd_workspace_bytes, plan.bwd_workspace_bytes if backward else 0)
+    out = {"o": torch.empty(plan.q_tokens, plan.n_q_heads, plan.head_dim, **bf),
+           "lse": torch.empty(plan.q_tokens, plan.n_q_heads, dtype=torch.float32, device=device),
+           "workspace": torch.empty(max(16, ws), dtype=torch.uint8, device=device)}
+    if backward:
+        out["dq"] = torch.empty(plan.q_tokens, plan.n_q_heads, plan.head_dim, **bf)
+        out["dk"] = torch.empty(plan.kv_tokens, plan.n_kv_heads, plan.head_dim, **bf)
+        out["dv"] = torch.empty(plan.kv_tokens, plan.n_kv_heads, plan.head_dim, **bf)
+    return out
+
+
+def _causal_shapes(plan: CausalPlan):
+    return ((plan.q_tokens, plan.n_q_heads, plan.head_dim), (plan.kv_tokens, plan.n_kv_heads, plan.head_dim))
+
+
+def _whole(t, what, shape, dtype):
+    """Pointer of a contiguous CUDA tensor of exactly this shape (None where it is empty)."""
+    p = _ptr(t, dtype, what)
+    if p is None or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {None if t is None else tuple(t.shape)}")
+    return p if t.numel() else None
+
+
+def zl_causal_attn_fwd(plan: CausalPlan, q, k, v, o, lse, workspace, scale: float, stream=None):
+    import torch
+    _on_plan_device(plan, q, k, v, o, lse, workspace)
+    sq, sk = _causal_shapes(plan)
+    st = load_library().zl_causal_attn_fwd(
+        plan.handle, *_heads(q, "q", sq), *_heads(k, "k", sk), *_heads(v, "v", sk), _whole(o, "o", sq, torch.bfloat16),
+        _whole(lse, "lse", sq[:2], torch.float32),
+        _ptr(workspace, torch.uint8, "workspace", plan.fwd_workspace_bytes), ctypes.c_float(scale), _stream(stream))
+    _check(st, "zl_causal_attn_fwd")
+
+
+def zl_causal_attn_bwd(plan: CausalPlan, q, k, v, o, d_o, lse, dq, dk, dv, workspace, scale: float, stream=None):
+    import torch
+    _on_plan_device(plan, q, k, v, o, d_o, lse, dq, dk, dv, workspace)
+    sq, sk = _causal_shapes(plan)
+    st = load_library().zl_causal_attn_bwd(
+        plan.handle, *_heads(q, "q", sq), *_heads(k, "k", sk), *_heads(v, "v", sk), _whole(o, "o", sq, torch.bfloat16),
+        _whole(d_o, "d_o", sq, torch.bfloat16), _whole(lse, "lse", sq[:2], torch.float32), *_heads(dq, "dq", sq),
+        *_heads(dk, "dk", sk), *_heads(dv, "dv", sk),
+        _ptr(workspace, torch.uint8, "workspace", plan.bwd_workspace_bytes), ctypes.c_float(scale), _stream(stream))
+    _check(st, "zl_causal_attn_bwd")
+
+
+def zl_causal_get_device_status(plan: CausalPlan, stream=None) -> int:
+    s = ctypes.c_int32()
+    _check(load_library().zl_causal_get_device_status(plan.handle, _stream(stream), ctypes.byref(s)),
+           "zl_causal_get_device_status")
+    return s.value
+
+
+def _qkv_views(plan: CausalPlan, qkv, what="qkv"):
+    hq, hk = plan.n_q_heads, plan.n_kv_heads
+    if plan.q_tokens != plan.kv_tokens:
+        raise ValueError("a fused projection needs as many key rows as query rows")
+    shape = (plan.q_tokens, hq + 2 * hk, plan.head_dim)
+    if tuple(qkv.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(qkv.shape)}")
+    return qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+
+
+def allocate_qkv_attention(plan: CausalPlan, device="cuda", backward: bool = False) -> Dict[str, "object"]:
+    """allocate_causal plus the normalised, rotated queries and keys, and the weights' gradients."""
+    import torch
+    sq, sk = _causal_shapes(plan)
+    out = allocate_causal(plan, device, backward)
+    out["q"], out["k"] = (torch.empty(s, dtype=torch.bfloat16, device=device) for s in (sq, sk))
+    if backward:
+        out["dq_weight"], out["dk_weight"] = (torch.empty(plan.head_dim, dtype=torch.float32, device=device) for _ in range(2))
+        out["rope_workspace"] = torch.empty(
+            zl_qk_rope_workspace_bytes(plan.q_tokens, plan.n_q_heads, plan.n_kv_heads, plan.head_dim), dtype=torch.uint8,
+            device=device)
+    return out
+
+
+def qkv_attention_forward(plan: CausalPlan, qkv, positions, table: Optional[RotaryTable], scale: float, bufs: dict,
+                          q_weight=None, k_weight=None, eps: float = 1e-6, stream=None) -> dict:
+    """Causal self-attention from a projection's output qkv [tokens, Hq + 2 Hkv, d]: queries and keys
+    normalised where weights are given, rotated, attended; the values are read where they lie."""
+    q, k, v = _qkv_views(plan, qkv)
+    norm = q_weight is not None or k_weight is not None
+    zl_qk_rope_fwd(q, k, bufs["q"], bufs["k"], positions, table, norm, q_weight, k_weight, eps, stream)
+    zl_causal_attn_fwd(plan, bufs["q"], bufs["k"], v, bufs["o"], bufs["lse"], bufs["workspace"], scale, stream)
+    return bufs
+
+
+def qkv_attention_backward(plan: CausalPlan, qkv, d_o, dqkv, positions, table: Optional[RotaryTable], scale: float,
+                           bufs: dict, q_weight=None, k_weight=None, eps: float = 1e-6, stream=None) -> dict:
+    """Gradient of qkv_attention_forward into dqkv (as qkv) and, with weights, bufs["dq_weight"] and
+    bufs["dk_weight"]."""
+    q, k, v = _qkv_views(plan, qkv)
+    dq, dk, dv = _qkv_views(plan, dqkv, "dqkv")
+    norm = q_weight is not None or k_weight is not None
+    zl_causal_attn_bwd(plan, bufs["q"], bufs["k"], v, bufs["o"], d_o, bufs["lse"], bufs["dq"], bufs["dk"], dv,
+                       bufs["workspace"], scale, stream)
+    zl_qk_rope_bwd(q, k, bufs["dq"], bufs["dk"], dq, dk, positions, table, norm, q_weight, k_weight,
+                   bufs["dq_weight"] if q_weight is not None else None,
+                   bufs["dk_weight"] if k_weight is not None else None, bufs["rope_workspace"], eps, stream)
+    return bufs
 
 
 # ---------------------------------------------------------------- host placement slice

@@ -382,6 +382,142 @@ ZL_API zl_status zl_pack_fillers(const double* filler_time, const double* filler
                                  double M_cap, int32_t* assign, double* final_time, double* final_mem,
                                  int32_t* n_overflow, double* makespan);
 
+/* ----------------------------------------------------------------------------------
+ * Causal sequences: rotary positions and head norms of queries and keys, and causal
+ * attention with grouped heads.  Operators beside the engine's bidirectional attention
+ * (library mechanics; no passage): an autoregressive model trains or serves on the same
+ * packed tokens.  Tensors are bf16 [tokens, heads, d] whose heads are contiguous
+ * (head stride d) and whose token stride is an argument, in elements, a multiple of 8:
+ * queries, keys and values may be views of one projection's [tokens, (Hq + 2 Hkv) d]
+ * output, and their gradients views of its gradient.  d is 64 or 128.
+ * ---------------------------------------------------------------------------------- */
+
+/* What zl_qk_rope_fwd / bwd do to every head of every token. */
+typedef struct {
+  int64_t n_tokens;      /* >= 0 */
+  int32_t n_q_heads;     /* heads of q (>= 0) and of k (>= 0), not both 0 */
+  int32_t n_kv_heads;
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t norm;          /* 1: RMS norm over the head before the rotation */
+  float eps;             /* added to the mean square; >= 0 */
+  int32_t rot_dim;       /* leading channels that are rotated: 0 .. d, a multiple of 2
+                            (interleaved) or 16 (half); the rest passes through */
+  int32_t half_layout;   /* pair p is channels (p, p + rot_dim / 2); 0: (2p, 2p + 1) */
+  int32_t n_axes;        /* position axes, 1 .. 3 (rot_dim > 0) */
+  int32_t axis_pairs[3]; /* pairs turned by each axis, in order; they add up to rot_dim / 2 */
+  float amplitude;       /* factor on the rotated channels (long-context scaling); 1 */
+} zl_qk_rope_desc;
+
+/* Radians per position -> the 64-bit fixed-point fraction of a turn per position that
+ * zl_qk_rope_fwd / bwd take: round down of frac(radians / (2 pi)) * 2^64.  Host arrays.
+ * Position times that number modulo 2^64 is the turn's fraction at any 32-bit position,
+ * with no error beyond the frequency's own 53 bits. */
+ZL_API zl_status zl_rope_frequencies(const double* radians, int32_t n, uint64_t* out);
+
+/* Workspace of zl_qk_rope_bwd when it returns weight gradients. */
+ZL_API zl_status zl_qk_rope_workspace(const zl_qk_rope_desc* desc, int64_t* bytes);
+
+/* Per head row x at the token's positions, with the tensor's weights w:
+ *   y = x w / sqrt(mean(x^2) + eps)   (norm = 1; w = 1 where the pointer is NULL)
+ *   pair (a, b) of y, angle t f:  (a cos - b sin, b cos + a sin) * amplitude.
+ *   q, k: inputs; q_out, k_out: outputs (each may be its input, with the same stride; no
+ *   other overlap).  A tensor with 0 heads may be NULL.
+ *   q_weight, k_weight: fp32 [d] or NULL.  positions: int32 [n_tokens, n_axes], any
+ *   value.  freq: uint64 [rot_dim / 2] from zl_rope_frequencies, in device memory.
+ * One pass; fp32 arithmetic, rounded once.  Uses no state: calls on different streams
+ * are independent.  ZL_ERR_INVALID_ARG for a bad descriptor, a missing pointer, a stride
+ * below heads * d, or weights without norm; ZL_ERR_ALIGN for a base that is not 16-byte
+ * aligned or a stride that is not a multiple of 8. */
+ZL_API zl_status zl_qk_rope_fwd(const zl_qk_rope_desc* desc, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const float* q_weight, const float* k_weight,
+                                const int32_t* positions, const uint64_t* freq, void* q_out, int64_t q_out_stride,
+                                void* k_out, int64_t k_out_stride, void* stream);
+
+/* Gradient of zl_qk_rope_fwd: dq_out, dk_out are the gradients of its outputs, dq, dk (bf16)
+ * those of its inputs; q, k are the forward's INPUTS (read with norm = 1 only; NULL
+ * otherwise).  dq_weight, dk_weight (fp32 [d], written; NULL: not wanted) need the
+ * weight, and workspace of zl_qk_rope_workspace bytes.  dq may be dq_out, dk may be dk_out
+ * (same stride).  The weights' sums over tokens and heads are taken in a fixed order.
+ * Errors as zl_qk_rope_fwd. */
+ZL_API zl_status zl_qk_rope_bwd(const zl_qk_rope_desc* desc, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const float* q_weight, const float* k_weight,
+                                const int32_t* positions, const uint64_t* freq, const void* dq_out,
+                                int64_t dq_out_stride, const void* dk_out, int64_t dk_out_stride, void* dq,
+                                int64_t dq_stride, void* dk, int64_t dk_stride, float* dq_weight, float* dk_weight,
+                                void* workspace, void* stream);
+
+/* One sequence: queries [q_offset, q_offset + q_len) of the query tensors over keys
+ * [kv_offset, kv_offset + kv_len) of the key and value tensors.  Query i sees keys
+ * j <= kv_len - q_len + i: the last query sees every key, so a chunk of a prompt, or one
+ * new token, stands behind the keys already there.  With kv_len < q_len the first
+ * q_len - kv_len queries see none. */
+typedef struct {
+  int64_t q_offset, kv_offset;
+  int32_t q_len, kv_len;
+} zl_causal_seq;
+
+typedef struct zl_causal_plan zl_causal_plan;
+
+/* Plan of the causal attention over n_seqs sequences (host memory, not retained), on the
+ * current device: tiles, their static schedule over the SMs, and where few rows face
+ * many keys the split of the key range.  n_q_heads must be a multiple of n_kv_heads, query head
+ * h reads key head h / (n_q_heads / n_kv_heads); at most 128 query heads share a key head.
+ * The query tensors have q_tokens rows, the key tensors kv_tokens (below 2^31 - 512).
+ * Sequences may come in any order and leave gaps; their query rows must be disjoint.
+ * They may share key rows (a common prefix): the plan then has no backward.
+ * flags: ZL_PLAN_HOST_ONLY, ZL_PLAN_TEST_WITHHOLD_LOAD.
+ * The plan is read-only once built: launches from one plan may run at the same time on
+ * several streams (each with its own outputs and workspace).  Building allocates and
+ * copies, so it is not for a stream under capture; launches are.
+ * Errors: ZL_ERR_INVALID_ARG for a range outside its tensor, overlapping query rows, a bad head
+ * count or flag; ZL_ERR_UNSUPPORTED for another head_dim, group, size or device;
+ * ZL_ERR_NO_MEMORY, ZL_ERR_CUDA.  On error *out is NULL. */
+ZL_API zl_status zl_plan_causal(const zl_causal_seq* seqs, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                int32_t head_dim, int64_t q_tokens, int64_t kv_tokens, uint32_t flags,
+                                zl_causal_plan** out);
+/* Free a plan; NULL is ignored.  No launch that uses it may still be running. */
+ZL_API void zl_causal_plan_destroy(zl_causal_plan* plan);
+/* Device scratch that the forward (0 where no key range is split) and the backward need;
+ * one buffer of the larger size serves both in turn.  Any pointer may be NULL. */
+ZL_API zl_status zl_causal_plan_workspace(const zl_causal_plan* plan, int64_t* fwd_bytes, int64_t* bwd_bytes);
+/* The schedule: which = 0 forward, 1 backward.  *n = tiles; up to cap tiles as 7 int32
+ * {sequence, key head, block, first key block, end key block, part, thread block}: forward
+ * tiles are two blocks of 128 / group tokens from `block` on, over 128-key blocks, part >= 0 where
+ * the key range is split; backward tiles are 128 keys. */
+ZL_API zl_status zl_causal_plan_tiles(const zl_causal_plan* plan, int32_t which, int32_t* out, int64_t cap, int64_t* n);
+
+/* Causal attention: O = softmax(scale q k^T) V over the visible keys and LSE, the natural
+ * log of the sum of exponents; O = 0 and LSE = -inf for a query that sees no key.
+ *   q: bf16 [q_tokens, n_q_heads, d], k, v: [kv_tokens, n_kv_heads, d], token strides given.
+ *   o: bf16 [q_tokens, n_q_heads, d] contiguous; lse: fp32 [q_tokens, n_q_heads].
+ *   workspace: as zl_causal_plan_workspace (NULL where it says 0).
+ *   scale: positive, normal.
+ * Rows of o and lse that belong to no sequence are left as they were.  Tokens outside the
+ * sequences may hold anything, NaN included.  Within a sequence a value row that is not finite
+ * makes the rows that see it not finite, and may do so to earlier rows that share its 128-key block
+ * (their weight for it is 0, and 0 x Inf is NaN, as in a plain product).
+ * Errors: ZL_ERR_INVALID_ARG, ZL_ERR_ALIGN, ZL_ERR_CUDA as for the other launches. */
+ZL_API zl_status zl_causal_attn_fwd(const zl_causal_plan* plan, const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride, void* o, float* lse,
+                                    void* workspace, float scale, void* stream);
+
+/* Gradient of zl_causal_attn_fwd: q, k, v, o, lse as the forward took and left them, d_o
+ * (bf16, contiguous like o); dq, dk, dv: bf16 with token strides, written for every row of every
+ * sequence (zero where no query sees a key), other rows left as they were.
+ * With P = exp(scale q k^T - LSE), D = rowsum(dO * O), dS = P (dO V^T - D):
+ *   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO, keys' gradients summed over their group.
+ * dQ is summed in fp32 over 128-key tiles in an order that may vary between runs (its last fp32
+ * bits may, before the rounding); dK and dV are formed in one order.
+ * ZL_ERR_INVALID_ARG also for a plan whose sequences share key rows. */
+ZL_API zl_status zl_causal_attn_bwd(const zl_causal_plan* plan, const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride, const void* o, const void* d_o,
+                                    const float* lse, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                                    void* dv, int64_t dv_stride, void* workspace, float scale, void* stream);
+
+/* As zl_get_device_status: reads and clears the plan's status word (a bounded device wait that
+ * gave up), synchronising the stream. */
+ZL_API zl_status zl_causal_get_device_status(const zl_causal_plan* plan, void* stream, int32_t* device_status);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,411 @@
+"""Causal attention with grouped heads on the GPU against the 64-bit reference.
+
+Tolerances are bounds by arithmetic, element by element, with a = 2^-8 the half step of bf16 relative to a value:
+  scores     a dot of d bf16 products summed in fp32: e_s = d 2^-24 scale |q|.|k|; P is off by e_s + 2^-20, relative
+  O          P rounded to bf16 (a) and off by that much, O rounded (a):   a |O| + (a + e_P) P |V|
+  LSE        max e_s + 2^-20 (1 + |LSE|)
+  D          dO . O with the O that the forward stored:                   |dO| . tol(O) + d 2^-24 |dO|.|O|
+  dS         P (dP - D):                 e_P |dS| + P (tol(D) + d 2^-24 |dO|.|V|), then rounded to bf16 (a)
+  dV, dK, dQ the products of those with |dO|, |Q|, |K|, and rounded (a)
+Normwise, the same roundings are independent of one another and each is a / sqrt(3) of its value at most in the root
+mean square, so the expected square of the error is at most (b = a^2 / 3, c the group's rows)
+  O   b (O^2 + P^2 V^2)      D   dO^2 . that      dV  b (dV^2 + P^2' dO^2)
+  dQ  b (dQ^2 + scale^2 dS^2 K^2) + var(D) (scale P K)^2      dK  b dK^2 + scale^2 (b dS^2 + P^2 var(D))' Q^2
+(D's error is one number a row: its terms add up along j before they are squared).  The norm of n rows' errors stays
+within 4 / sqrt(n) of its expectation; fp32 adds under a tenth.
+"""
+import numpy as np
+import pytest
+
+from coalesced_packed_attention_gb300 import zl
+from oracle import causal as ref
+from tests._lib import ensure_library
+
+pytestmark = pytest.mark.gpu
+A, F = 2.0 ** -8, 2.0 ** -24
+
+
+def f64(x):
+    return x.double().cpu().numpy()
+
+
+def inputs(tq, tk, hq, hk, d, seed):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(*s, generator=g).bfloat16() for s in ((tq, hq, d), (tk, hk, d), (tk, hk, d), (tq, hq, d))]
+
+
+def bounds(q, k, v, do, seqs, scale):
+    """Reference results and their element-wise bounds; rows of no sequence are NaN."""
+    hq, hk, d = q.shape[1], k.shape[1], q.shape[2]
+    want = dict(zip(("o", "lse"), ref.attend(q, k, v, seqs, scale)))
+    want.update(zip(("dq", "dk", "dv"), ref.attend_grad(q, k, v, do, seqs, scale)))
+    tol = {n: np.zeros_like(x) for n, x in want.items()}
+    var = {n: np.zeros_like(x) for n, x in want.items()}
+    b = A * A / 3
+    for q0, n, k0, m in seqs:
+        for h in range(hq):
+            c = h // (hq // hk)
+            Q, K, V, G = q[q0:q0 + n, h], k[k0:k0 + m, c], v[k0:k0 + m, c], do[q0:q0 + n, h]
+            p, o, lse = ref.attend_head(Q, K, V, scale)
+            vis = ref.visible(n, m)
+            es = d * F * scale * (np.abs(Q) @ np.abs(K).T) * vis
+            es_row = es.max(1, initial=0.0, keepdims=True)
+            ep = es + es_row + 2.0 ** -20
+            t_o = A * np.abs(o) + ((A + ep) * p) @ np.abs(V)
+            tol["o"][q0:q0 + n, h] = t_o
+            with np.errstate(invalid="ignore"):
+                tol["lse"][q0:q0 + n, h] = np.where(np.isfinite(lse), es_row[:, 0] + 2.0 ** -20 * (1 + np.abs(lse)), 0.0)
+            dp, dd = G @ V.T, np.sum(G * o, 1, keepdims=True)
+            t_d = np.sum(np.abs(G) * (t_o + d * F * np.abs(o)), 1, keepdims=True)
+            ds = p * (dp - dd)
+            t_ds = (A + ep) * np.abs(ds) + p * (1 + A) * (t_d + d * F * (np.abs(G) @ np.abs(V).T))
+            tol["dv"][k0:k0 + m, c] += ((A + ep) * p).T @ np.abs(G)
+            tol["dk"][k0:k0 + m, c] += scale * t_ds.T @ np.abs(Q)
+            tol["dq"][q0:q0 + n, h] = scale * t_ds @ np.abs(K)
+            var["o"][q0:q0 + n, h] = b * (o ** 2 + p ** 2 @ V ** 2)
+            var_d = np.sum(G ** 2 * var["o"][q0:q0 + n, h], 1, keepdims=True)
+            var["dv"][k0:k0 + m, c] += b * (p ** 2).T @ G ** 2
+            var["dk"][k0:k0 + m, c] += scale ** 2 * (b * ds ** 2 + p ** 2 * var_d).T @ Q ** 2
+            var["dq"][q0:q0 + n, h] = b * scale ** 2 * ds ** 2 @ K ** 2 + var_d * (scale * p @ K) ** 2
+    for name in ("dq", "dk", "dv"):  # fp32 sums over up to some thousand rows, and the rounding
+        with np.errstate(invalid="ignore"):
+            tol[name] = tol[name] * (1 + 2.0 ** -10) + A * np.abs(np.nan_to_num(want[name])) + 1e-30
+            var[name] += b * np.nan_to_num(want[name]) ** 2
+    return want, tol, var
+
+
+class Case:
+    def __init__(self, seqs, hq, hk, d, seed=0, tq=None, tk=None, scale=None, poison=False, ins=None):
+        import torch
+        ensure_library()
+        self.seqs, self.scale = seqs, scale or d ** -0.5
+        tq = tq if tq is not None else max([s[0] + s[1] for s in seqs] + [0])
+        tk = tk if tk is not None else max([s[2] + s[3] for s in seqs] + [0])
+        self.ins = ins or inputs(tq, tk, hq, hk, d, seed)
+        self.in_q, self.in_k = np.zeros(tq, bool), np.zeros(tk, bool)
+        for q0, n, k0, m in seqs:
+            self.in_q[q0:q0 + n], self.in_k[k0:k0 + m] = True, True
+        if poison:  # tokens of no sequence hold NaN in every input
+            for x, used in zip(self.ins, (self.in_q, self.in_k, self.in_k, self.in_q)):
+                x[torch.from_numpy(~used)] = float("nan")
+        self.dev = [x.cuda() for x in self.ins]
+        self.plan = zl.zl_plan_causal(seqs, hq, hk, d, tq, tk)
+        self.bufs = zl.allocate_causal(self.plan, "cuda", backward=True)
+        for n, b in self.bufs.items():
+            b.fill_(255 if n == "workspace" else float("nan"))  # 255: NaN in every workspace word
+
+    def forward(self, stream=None):
+        b, (q, k, v, _) = self.bufs, self.dev
+        zl.zl_causal_attn_fwd(self.plan, q, k, v, b["o"], b["lse"], b["workspace"], self.scale, stream)
+        return self
+
+    def backward(self, stream=None):
+        b, (q, k, v, do) = self.bufs, self.dev
+        zl.zl_causal_attn_bwd(self.plan, q, k, v, b["o"], do, b["lse"], b["dq"], b["dk"], b["dv"], b["workspace"],
+                              self.scale, stream)
+        return self
+
+    def check(self, names=("o", "lse", "dq", "dk", "dv")):
+        import torch
+        torch.cuda.synchronize()
+        assert zl.zl_causal_get_device_status(self.plan) == 0
+        want, tol, var = bounds(*(f64(x) for x in self.ins), self.seqs, self.scale)
+        for n in names:
+            got, used = f64(self.bufs[n]), self.in_k if n in ("dk", "dv") else self.in_q
+            assert np.isnan(got[~used]).all(), f"{n}: a row of no sequence was written"
+            got, w, t = got[used], want[n][used], tol[n][used]
+            fin = np.isfinite(w)
+            assert np.array_equal(got[~fin], w[~fin]), n  # LSE = -inf
+            assert np.isfinite(got[fin]).all(), n
+            over = np.abs(got[fin] - w[fin]) - t[fin]
+            assert over.size == 0 or over.max() <= 0, f"{n}: {over.max():.3e} over its bound"
+            if n != "lse" and over.size:
+                rms = np.sqrt(var[n][used].sum())
+                most = 1.1 + 4 / np.sqrt(got.shape[0] * got.shape[1])
+                off = np.linalg.norm(got[fin] - w[fin])
+                assert off <= most * rms + 1e-30, f"{n}: {off / rms:.2f} times the expected error"
+        return self
+
+
+def packed(*lens):
+    return zl.causal_seqs(lens)
+
+
+@pytest.mark.parametrize("seqs,hq,hk,d", [
+    (packed(1), 1, 1, 64), (packed(1, 2, 0, 3), 4, 2, 64), (packed(128), 2, 2, 128), (packed(129, 127), 4, 4, 64),
+    (packed(300, 1, 64), 8, 1, 128), (packed(257), 6, 2, 64), (packed(200, 131), 5, 1, 128), (packed(140), 7, 1, 64),
+    (packed(77, 400), 12, 1, 64), (packed(9, 33), 128, 1, 64), (packed(40), 100, 2, 64), (packed(513, 256), 16, 2, 128),
+    ([(0, 5, 0, 300), (5, 64, 300, 64), (69, 1, 364, 129)], 8, 2, 128),          # chunks and a token behind cached keys
+    ([(0, 9, 0, 3), (9, 200, 3, 150), (209, 4, 153, 0)], 6, 2, 64),              # queries that see no key
+    ([(40, 70, 10, 70), (0, 30, 100, 30), (115, 0, 90, 5), (116, 3, 140, 260)], 4, 2, 64),  # gaps, any order, no queries
+])
+def test_parity(seqs, hq, hk, d):
+    Case(seqs, hq, hk, d, seed=hq + d, tq=max(s[0] + s[1] for s in seqs) + 3, tk=max(s[2] + s[3] for s in seqs) + 2,
+         poison=True).forward().backward().check()
+
+
+@pytest.mark.parametrize("lens", [(1,), (127, 128), (1, 130, 255, 31), (700,)])
+@pytest.mark.parametrize("hq,hk,d", [(4, 4, 64), (3, 1, 128), (8, 2, 128), (14, 2, 64)])
+def test_lengths_by_heads(lens, hq, hk, d):
+    Case(packed(*lens), hq, hk, d, seed=sum(lens)).forward().backward().check()
+
+
+@pytest.mark.parametrize("hq,hk,d,seqs", [
+    (8, 2, 128, [(0, 1, 0, 9001)]), (4, 4, 64, [(0, 1, 0, 5000), (1, 3, 5000, 4097), (4, 1, 9097, 1)]),
+    (3, 1, 64, [(0, 20, 0, 3001)]), (16, 1, 128, [(0, 2, 0, 2600), (2, 7, 2600, 3)])])
+def test_split_key_ranges(hq, hk, d, seqs):
+    c = Case(seqs, hq, hk, d, seed=5)
+    assert c.plan.fwd_workspace_bytes > 0 and any(t[5] >= 0 for t in c.plan.tiles(0))
+    c.forward().check(("o", "lse"))
+    c.backward().check()
+
+
+def test_peaked_scores_and_other_scales():
+    import torch
+    ins = inputs(333, 333, 6, 2, 128, 11)
+    ins[0] *= 6  # scores up to some 60: sharp rows, maxima that keep growing
+    Case(packed(300, 33), 6, 2, 128, ins=[x.clone() for x in ins]).forward().backward().check()
+    Case(packed(300, 33), 6, 2, 128, ins=ins, scale=1e-3).forward().backward().check()
+    huge = inputs(200, 200, 2, 1, 64, 12)
+    huge[1][150:] *= 1000  # growth past the lazy rescale's threshold many times over
+    Case(packed(200), 2, 1, 64, ins=huge).forward().check(("o", "lse"))
+    assert torch.isfinite(huge[1].float()).all()
+
+
+def test_non_finite_keys_do_not_reach_rows_that_do_not_see_them():
+    import torch
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        ins = inputs(300, 300, 4, 2, 64, 13)
+        clean = Case(packed(300), 4, 2, 64, ins=[x.clone() for x in ins]).forward()
+        ins[1][200:] = bad
+        dirty = Case(packed(300), 4, 2, 64, ins=ins).forward()
+        torch.cuda.synchronize()
+        assert torch.equal(clean.bufs["o"][:200], dirty.bufs["o"][:200])
+        assert torch.equal(clean.bufs["lse"][:200], dirty.bufs["lse"][:200])
+
+
+def test_views_of_a_fused_projection_give_the_same_bits():
+    import torch
+    seqs, hq, hk, d = packed(260, 33, 1), 6, 2, 128
+    c = Case(seqs, hq, hk, d, seed=3).forward().backward()
+    fused = torch.cat([x for x in c.dev[:3]], 1).contiguous()
+    grads = torch.full_like(fused, float("nan"))
+    v = Case(seqs, hq, hk, d, seed=3)
+    cut = lambda x: [x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]]  # noqa: E731
+    v.dev[:3] = cut(fused)
+    v.bufs["dq"], v.bufs["dk"], v.bufs["dv"] = cut(grads)
+    v.forward().backward()
+    torch.cuda.synchronize()
+    for n in ("o", "lse", "dk", "dv"):
+        assert torch.equal(c.bufs[n], v.bufs[n].contiguous()), n
+    v.check()
+
+
+def test_key_gradients_and_outputs_repeat_bit_for_bit():
+    import torch
+    c = Case(packed(1500, 700, 1), 8, 2, 64, seed=8).forward().backward()
+    first = {n: b.clone() for n, b in c.bufs.items()}
+    for _ in range(3):
+        c.forward().backward()
+        torch.cuda.synchronize()
+        for n in ("o", "lse", "dk", "dv"):
+            assert torch.equal(first[n], c.bufs[n]), n
+
+
+def test_one_plan_on_two_streams_and_in_captured_graphs():
+    """The plan holds no state of a launch: two calls at once, and graphs replayed in any order."""
+    import torch
+    seqs, hq, hk, d = [(0, 1, 0, 9000), (1, 40, 9000, 40)], 8, 2, 128
+    cases = [Case(seqs, hq, hk, d, seed=s) for s in (1, 2)]
+    cases[1].plan = cases[0].plan
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s in zip(cases, streams):
+            c.forward(s).backward(s)
+    torch.cuda.synchronize()
+    for c in cases:
+        c.check()
+    graphs = []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.forward().backward()
+        graphs.append(g)
+    for c in cases:
+        for n in ("o", "lse", "dq", "dk", "dv"):
+            c.bufs[n].fill_(float("nan"))
+    for g in (graphs[1], graphs[0], graphs[1]):
+        g.replay()
+    torch.cuda.synchronize()
+    for c in cases:
+        c.check()
+
+
+def test_keys_beyond_32_bit_offsets():
+    """A cache of 2.2 million rows (2^31 elements and more): the last rows' keys and values are found."""
+    import torch
+    ensure_library()
+    rows, hk, hq, d = 2_200_000, 8, 16, 128
+    seqs = [(0, 3, rows - 1400, 1399), (3, 1, 5, 200), (4, 1, rows - 1, 1)]
+    q, _, _, _ = inputs(5, 1, hq, 1, d, 4)
+    cache = torch.zeros(2, rows, hk, d, dtype=torch.bfloat16, device="cuda")
+    small = inputs(1, 1600, 1, hk, d, 6)[1:3]
+    for i in range(2):
+        cache[i, rows - 1400:] = small[i][:1400].cuda()
+        cache[i, 5:205] = small[i][1400:].cuda()
+    plan = zl.zl_plan_causal(seqs, hq, hk, d, 5, rows)
+    b = zl.allocate_causal(plan)
+    zl.zl_causal_attn_fwd(plan, q.cuda(), cache[0], cache[1], b["o"], b["lse"], b["workspace"], d ** -0.5)
+    near = [(0, 3, 0, 1399), (3, 1, 1400, 200), (4, 1, 1399, 1)]
+    c = Case(near, hq, hk, d, ins=[q, small[0], small[1], q.clone()], tq=5, tk=1600)
+    c.bufs["o"].copy_(b["o"])
+    c.bufs["lse"].copy_(b["lse"])
+    c.check(("o", "lse"))
+
+
+def test_shared_keys_have_a_forward_and_no_backward():
+    seqs = [(0, 3, 0, 200), (3, 2, 0, 100)]
+    c = Case(seqs, 4, 2, 64, seed=2).forward().check(("o", "lse"))
+    with pytest.raises(zl.ZlError) as e:
+        c.backward()
+    assert e.value.status == zl.ZL_ERR_INVALID_ARG
+
+
+def test_no_keys_no_queries_no_sequences():
+    import torch
+    c = Case([(0, 4, 0, 0)], 4, 2, 64, tk=0).forward().backward()
+    torch.cuda.synchronize()
+    assert (c.bufs["o"] == 0).all() and (c.bufs["lse"] == -float("inf")).all() and (c.bufs["dq"] == 0).all()
+    c = Case([(0, 0, 0, 130)], 4, 2, 64, tq=0).forward().backward()
+    torch.cuda.synchronize()
+    assert (c.bufs["dk"] == 0).all() and (c.bufs["dv"] == 0).all()
+    c = Case([], 4, 2, 64, tq=3, tk=3).forward().backward()
+    torch.cuda.synchronize()
+    assert all(torch.isnan(c.bufs[n].float()).all() for n in ("o", "lse", "dq", "dk", "dv"))
+
+
+def test_gradient_against_differences():
+    """<dO, O> moves by the gradient times the step, on fp32 sums of the forward's own outputs: the step is large (a
+    bf16 input moves by whole steps) and the difference of two forwards carries their rounding, so the bound
+    is on the directional derivative along the gradient itself."""
+    import torch
+    c = Case(packed(90, 40), 4, 2, 64, seed=21).forward().backward()
+    torch.cuda.synchronize()
+    want = dict(zip(("dq", "dk", "dv"), ref.attend_grad(*(f64(x) for x in c.ins), c.seqs, c.scale)))
+    for i, n in enumerate(("dq", "dk", "dv")):
+        g = f64(c.bufs[n])
+        unit = g / np.linalg.norm(g)
+        step = 1e-4
+        moved = []
+        for sign in (1, -1):
+            x = [f64(y) for y in c.ins]
+            x[i] = x[i] + sign * step * unit
+            moved.append(np.sum(x[3] * ref.attend(x[0], x[1], x[2], c.seqs, c.scale)[0]))
+        slope = (moved[0] - moved[1]) / (2 * step)
+        assert abs(slope - np.sum(want[n] * unit)) <= 1e-5 * abs(slope)
+        # the kernel's gradient against the differences: <g, g_exact> / |g| within its normwise error
+        assert abs(slope - np.linalg.norm(g)) <= 1.2 * A * np.linalg.norm(g)
+
+
+def test_withheld_load_reports_timeout_and_context_survives():
+    import torch
+    ensure_library()
+    seqs, hq, hk, d = packed(200, 30), 4, 2, 128
+    good = Case(seqs, hq, hk, d, seed=6).forward()
+    bad = zl.zl_plan_causal(seqs, hq, hk, d, 230, 230, zl.ZL_PLAN_TEST_WITHHOLD_LOAD)
+    b, (q, k, v, do) = zl.allocate_causal(bad, backward=True), good.dev
+    zl.zl_causal_attn_fwd(bad, q, k, v, b["o"], b["lse"], b["workspace"], good.scale)
+    torch.cuda.synchronize()
+    assert zl.zl_causal_get_device_status(bad) == zl.ZL_ERR_TIMEOUT
+    assert zl.zl_causal_get_device_status(bad) == 0
+    zl.zl_causal_attn_bwd(bad, q, k, v, good.bufs["o"], do, good.bufs["lse"], b["dq"], b["dk"], b["dv"], b["workspace"], good.scale)
+    torch.cuda.synchronize()
+    assert zl.zl_causal_get_device_status(bad) == zl.ZL_ERR_TIMEOUT
+    good.backward().check()
+
+
+def test_launch_refusals():
+    import torch
+    c = Case(packed(30), 4, 2, 64)
+    q, k, v, do = c.dev
+    b = c.bufs
+    fwd = dict(q=q, k=k, v=v, o=b["o"], lse=b["lse"], workspace=b["workspace"], scale=0.125)
+    for bad in (dict(q=q.float()), dict(q=q[:29]), dict(k=k[:, :1]), dict(v=v.transpose(1, 2)), dict(o=None), dict(lse=b["lse"].half()),
+                dict(o=b["o"].view(30, 2, 128)), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
+                dict(scale=float("inf")), dict(scale=1e-42), dict(q=q.cpu())):
+        with pytest.raises((TypeError, ValueError, zl.ZlError)):
+            zl.zl_causal_attn_fwd(c.plan, **{**fwd, **bad})
+    odd = torch.zeros(30 * 4 * 64 + 8, dtype=torch.bfloat16, device="cuda")[1:30 * 4 * 64 + 1].view(30, 4, 64)
+    with pytest.raises(zl.ZlError) as e:
+        zl.zl_causal_attn_fwd(c.plan, **{**fwd, "q": odd})
+    assert e.value.status == zl.ZL_ERR_ALIGN
+    c.forward()
+    bwd = dict(q=q, k=k, v=v, o=b["o"], d_o=do, lse=b["lse"], dq=b["dq"], dk=b["dk"], dv=b["dv"], workspace=b["workspace"],
+               scale=0.125)
+    for bad in (dict(d_o=do[:, :2]), dict(dq=None), dict(dk=b["dk"].float()), dict(workspace=b["workspace"][:64]), dict(scale=0.0)):
+        with pytest.raises((TypeError, ValueError, zl.ZlError)):
+            zl.zl_causal_attn_bwd(c.plan, **{**bwd, **bad})
+    small = zl.zl_plan_causal([(0, 1, 0, 9000)], 8, 2, 128, 1, 9000)
+    with pytest.raises((TypeError, ValueError, zl.ZlError)):  # a split plan needs its workspace
+        x = torch.zeros(9000, 2, 128, dtype=torch.bfloat16, device="cuda")
+        o = torch.zeros(1, 8, 128, dtype=torch.bfloat16, device="cuda")
+        zl.zl_causal_attn_fwd(small, o, x, x, o.clone(), torch.zeros(1, 8, device="cuda"), None, 0.1)
+
+
+def test_projection_to_output_and_back():
+    """Norm, rotation, attention and their gradients in one run, from a projection's output to its gradient,
+    against the composition in 64 bits.  Normwise bound: each of the chain's stored tensors (q, k rotated; P; O; dS;
+    dq, dk before the norm's gradient; the result) is rounded to bf16, at most 0.58 a root mean square each; six of
+    them in a row, independent, stay under 1.5 a; the scores move by scale |q||k| a / 8 ~ a with q and k's
+    rounding, once more for P and once for dS: 3 a in all."""
+    import torch
+    ensure_library()
+    lens, hq, hk, d = (150, 1, 64), 8, 2, 128
+    t = sum(lens)
+    g = torch.Generator().manual_seed(0)
+    qkv = (2 * torch.randn(t, hq + 2 * hk, d, generator=g)).bfloat16()
+    do = torch.randn(t, hq, d, generator=g).bfloat16()
+    w = 1 + 0.2 * torch.randn(2, d, generator=g)
+    pos = torch.cat([torch.arange(n) for n in lens]).int()[:, None]
+    radians, amp = zl.rotary_frequencies(d)
+    seqs, scale = zl.causal_seqs(lens), d ** -0.5
+    plan = zl.zl_plan_causal(seqs, hq, hk, d, t, t)
+    bufs = zl.allocate_qkv_attention(plan, "cuda", backward=True)
+    table = zl.rotary_table(radians, amplitude=amp)
+    dev, wd = qkv.cuda(), w.cuda()
+    dqkv = torch.full_like(dev, float("nan"))
+    zl.qkv_attention_forward(plan, dev, pos.cuda(), table, scale, bufs, wd[0], wd[1])
+    zl.qkv_attention_backward(plan, dev, do.cuda(), dqkv, pos.cuda(), table, scale, bufs, wd[0], wd[1])
+    torch.cuda.synchronize()
+    assert zl.zl_causal_get_device_status(plan) == 0
+    x, wn, ang = f64(qkv), f64(w), ref.angles(pos.numpy(), radians, [d // 2])
+    parts = [x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]]
+    turned = [ref.rotate(ref.rms_norm(parts[i], wn[i], 1e-6), ang, True) for i in range(2)]
+    o, lse = ref.attend(*turned, parts[2], seqs, scale)
+    grads = ref.attend_grad(*turned, parts[2], f64(do), seqs, scale)
+    want = [o, None, None, grads[2]]
+    back = [ref.rms_norm_grad(parts[i], wn[i], 1e-6, ref.rotate(grads[i], -ang, True)) for i in range(2)]
+    got = f64(dqkv)
+
+    def close(a, b):
+        assert np.linalg.norm(a - b) <= 3 * A * np.linalg.norm(b), np.linalg.norm(a - b) / np.linalg.norm(b)
+
+    close(f64(bufs["o"]), want[0])
+    close(got[:, :hq], back[0][0])
+    close(got[:, hq:hq + hk], back[1][0])
+    close(got[:, hq + hk:], grads[2])
+    close(f64(bufs["dq_weight"]), back[0][1])
+    close(f64(bufs["dk_weight"]), back[1][1])
+    # the same queries and keys through the engine's bidirectional attention: the rotated tensors are its layout
+    # (equal head counts), so the operators stand in front of it as well
+    full = zl.zl_plan_worklist([zl.zl_work_item(0, t, 0, t, 0, hk, 0, t, 0, -1, -1)], hk, d, t)
+    k = bufs["k"]
+    fb = zl.forward(full, k, k, dev[:, hq + hk:].contiguous(), scale)
+    torch.cuda.synchronize()
+    kk, vv = f64(k), parts[2]
+    for h in range(hk):
+        s = scale * kk[:, h] @ kk[:, h].T
+        p = np.exp(s - s.max(1, keepdims=True))
+        close(f64(fb["o"])[:t * hk * d].reshape(t, hk, d)[:, h], p / p.sum(1, keepdims=True) @ vv[:, h])
