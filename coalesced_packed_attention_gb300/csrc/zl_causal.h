@@ -5,11 +5,37 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <vector>
 
 #include "../../include/zl.h"
 
 namespace zl {
+
+// A small number kept per device by host code that runs at every launch (a device's SM count, a kernel's
+// resident blocks): set once, read without a lock; two threads that set it at once set the same value.
+class PerDeviceInt {
+ public:
+  template <typename F>
+  cudaError_t get(int* value, F&& query) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool kept = dev >= 0 && dev < kDevices;
+    int v = kept ? v_[dev].load(std::memory_order_relaxed) : 0;
+    if (v == 0) {
+      e = query(dev, &v);
+      if (e != cudaSuccess) return e;
+      if (kept) v_[dev].store(v, std::memory_order_relaxed);
+    }
+    *value = v;
+    return cudaSuccess;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<int> v_[kDevices] = {};
+};
 
 // Query rows are packed by key head: the `group` query heads that share a key head are neighbours, so a
 // block of up to 128 rows is (tokens x group) with row r = token r / group, head r % group.  A block holds

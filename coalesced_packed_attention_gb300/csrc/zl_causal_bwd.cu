@@ -682,10 +682,10 @@ __global__ void __launch_bounds__(256) zl_causal_dq_kernel(const CausalSeq* __re
 
 // Blocks of a grid-stride kernel of 256 threads: as many as can be resident at once, or fewer.
 template <typename K>
-int resident_grid(K kernel, int64_t blocks, int num_sms) {
+int resident_grid(PerDeviceInt& resident, K kernel, int64_t blocks, int num_sms) {
   int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 256, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
-  const int64_t cap = (int64_t)num_sms * per_sm;
+  resident.get(&per_sm, [&](int, int* v) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kernel, 256, 0); });
+  const int64_t cap = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
   return (int)(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
 }
 
@@ -696,7 +696,8 @@ cudaError_t launch_causal_bwd_pre(int head_dim, const __nv_bfloat16* o, const __
   auto k = head_dim == 128 ? zl_causal_pre_kernel<128> : zl_causal_pre_kernel<64>;
   const int64_t by_rows = (rows + 8 * 4 * (256 / head_dim) - 1) / (8 * 4 * (256 / head_dim));
   const int64_t by_acc = (acc_floats / 4 + 255) / 256;
-  k<<<resident_grid(k, by_rows > by_acc ? by_rows : by_acc, num_sms), 256, 0, stream>>>(o, d_o, row_d, rows, acc,
+  static PerDeviceInt resident[2];
+  k<<<resident_grid(resident[head_dim == 128], k, by_rows > by_acc ? by_rows : by_acc, num_sms), 256, 0, stream>>>(o, d_o, row_d, rows, acc,
                                                                                        acc_floats / 4);
   return cudaGetLastError();
 }
@@ -728,7 +729,8 @@ cudaError_t launch_causal_dq(int head_dim, const CausalSeq* seqs, int32_t n_seqs
   const int64_t slabs = acc_blocks * (head_dim / 64);
   if (slabs == 0) return cudaSuccess;
   auto k = head_dim == 128 ? zl_causal_dq_kernel<128> : zl_causal_dq_kernel<64>;
-  k<<<resident_grid(k, slabs, num_sms), 256, 0, stream>>>(seqs, n_seqs, n_q_heads, n_kv_heads, slabs, acc, dq,
+  static PerDeviceInt resident[2];
+  k<<<resident_grid(resident[head_dim == 128], k, slabs, num_sms), 256, 0, stream>>>(seqs, n_seqs, n_q_heads, n_kv_heads, slabs, acc, dq,
                                                           dq_stride, scale);
   return cudaGetLastError();
 }

@@ -43,7 +43,7 @@ struct RopeTensor {
   __nv_bfloat16* out;
   const float* w;
   int64_t x_stride, g_stride, out_stride;  // elements per token
-  int32_t heads, steps;                    // steps of 32 / (d / 8) heads
+  int32_t heads, batches;                  // batches of rope_unroll steps of 32 / (d / 8) heads
 };
 
 struct RopeParams {
@@ -53,7 +53,7 @@ struct RopeParams {
   float* partial;  // weight gradients per block, [blocks][2 d]
   int64_t n_tokens;
   int32_t rot, n_axes, axis1, axis2;  // first pair of the second and the third axis
-  int32_t chunk;                      // steps of one token that one warp takes
+  int32_t chunk;                      // batches of one token that one warp takes
   float eps, amplitude;
 };
 
@@ -93,162 +93,200 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// A warp's unit is a batch of kUnroll steps of one tensor of one token; the loads of the next batch (of the next
+// token after the last) are issued before the current one is computed, so 16-byte loads are in flight through
+// the sines, the sums and the stores alike.
+template <bool kBwd, bool kNorm>
+constexpr int rope_unroll() {
+  return kBwd && kNorm ? 2 : 4;
+}
+
 template <int D, bool kHalf, bool kNorm, bool kBwd>
-__global__ void __launch_bounds__(kRopeThreads) zl_qk_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a step
-  constexpr int kUnroll = kBwd && kNorm ? 2 : 4;      // steps whose loads are in flight together
+  constexpr int kUnroll = rope_unroll<kBwd, kNorm>();
   constexpr bool kDw = kBwd && kNorm;
+  constexpr bool kHasX = !kBwd || kNorm;
+  __shared__ float red[kDw ? kRopeThreads / 32 * kRows : 1][2 * D];  // weights, then (kDw) the weights' gradients
   const int lane = threadIdx.x & 31, sub = lane / kLanes, gl = lane % kLanes, e0 = gl * 8;
-  const int nwarps = gridDim.x * (kRopeThreads / 32);
+  const int64_t nwarps = (int64_t)gridDim.x * (kRopeThreads / 32);
   const bool turns = e0 < p.rot;  // half: rot is a multiple of 16, so all eight values or none
   const int hop = p.rot / 16;
-  const int plane = kHalf && turns ? (gl < hop ? lane + hop : lane - hop) : lane;
+  const bool lower = gl < hop;
+  const int plane = kHalf && turns ? (lower ? lane + hop : lane - hop) : lane;
   const int pe0 = kHalf ? (plane % kLanes) * 8 : e0;  // first channel of the partner values
-  const int s_begin = blockIdx.y * p.chunk;
-  float acc[2][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = 0.f;
+  // the pairs whose sines this lane forms, and the lane that forms the first of those that it uses
+  const int pairs = p.rot / 2, my_pair = 2 * lane;
+  const int src = (kHalf ? (lower ? e0 : e0 - pairs) : e0 / 2) / 2;
+  const uint64_t f0 = my_pair < pairs ? __ldg(p.freq + my_pair) : 0, f1 = my_pair + 1 < pairs ? __ldg(p.freq + my_pair + 1) : 0;
+  auto axis_of = [&](int pair) { return pair < p.axis1 ? 0 : pair < p.axis2 ? 1 : 2; };
+  const int ax0 = my_pair < pairs ? axis_of(my_pair) : 0, ax1 = my_pair + 1 < pairs ? axis_of(my_pair + 1) : 0;
 
-  for (int64_t tok = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); tok < p.n_tokens; tok += nwarps) {
+  if constexpr (kNorm) {
+    if (threadIdx.x < 2 * D) {
+      const float* w = threadIdx.x < D ? p.t[0].w : p.t[1].w;
+      red[0][threadIdx.x] = w ? __ldg(w + threadIdx.x % D) : 1.f;
+    }
+    __syncthreads();
+  }
+  const int nb0 = p.t[0].batches;
+  const int b_begin = blockIdx.y * p.chunk, b_end = min(b_begin + p.chunk, nb0 + p.t[1].batches);
+  float acc0[8], acc1[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc0[i] = acc1[i] = 0.f;
+
+  struct Batch {
+    uint4 x[kUnroll], g[kUnroll];
+  };
+  auto fetch = [&](int64_t tok, int bi, Batch& v) {
+    const RopeTensor& T = p.t[bi >= nb0];
+    const int h0 = (bi >= nb0 ? bi - nb0 : bi) * (kUnroll * kRows) + sub;
+    const __nv_bfloat16* xp = T.x + tok * T.x_stride + (int64_t)h0 * D + e0;
+    const __nv_bfloat16* gp = T.g + tok * T.g_stride + (int64_t)h0 * D + e0;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const bool in = h0 + u * kRows < T.heads;
+      if constexpr (kHasX) v.x[u] = in ? load16(xp + u * kRows * D) : make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (kBwd) v.g[u] = in ? load16(gp + u * kRows * D) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+
+  int64_t tok = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  Batch cur;
+  if (tok < p.n_tokens) fetch(tok, b_begin, cur);
+  for (; tok < p.n_tokens; tok += nwarps) {
     // out[i] = value[i] c[i] + partner[i] s[i], the sign of the sine included
     float c[8], s[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
     if (p.rot > 0) {
       const int32_t* pt = p.positions + tok * p.n_axes;
-      const int32_t t0 = __ldg(pt), t1 = p.n_axes > 1 ? __ldg(pt + 1) : 0, t2 = p.n_axes > 2 ? __ldg(pt + 2) : 0;
-      auto turn = [&](int pair, float& cs, float& sn) {
-        const int32_t t = pair < p.axis1 ? t0 : pair < p.axis2 ? t1 : t2;
-        const uint64_t phase = (uint64_t)(int64_t)t * __ldg(p.freq + pair);
+      float cs[2], sn[2];
+      auto turn = [&](uint64_t f, int axis, float& co, float& si) {
+        const uint64_t phase = (uint64_t)(int64_t)__ldg(pt + axis) * f;
         // top 32 bits as a signed fraction of a turn; 2 pi r = pi (2 r)
-        sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn, &cs);
-        cs *= p.amplitude;
-        sn *= p.amplitude;
+        sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &si, &co);
+        co *= p.amplitude;
+        si *= p.amplitude;
       };
+      turn(f0, ax0, cs[0], sn[0]);
+      turn(f1, ax1, cs[1], sn[1]);
+      // 2 pairs a lane, so the pairs from 2 src on sit in lanes src, src + 1, ...
       if constexpr (kHalf) {
-        if (turns) {
-          const bool lower = gl < hop;
-          const int pair0 = lower ? e0 : e0 - p.rot / 2;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            turn(pair0 + i, c[i], s[i]);
-            s[i] = lower ? -s[i] : s[i];
+        for (int i = 0; i < 8; ++i) {
+          const float co = __shfl_sync(0xffffffffu, cs[i & 1], src + i / 2), si = __shfl_sync(0xffffffffu, sn[i & 1], src + i / 2);
+          if (turns) {
+            c[i] = co;
+            s[i] = lower != kBwd ? -si : si;  // backward turns back
           }
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
+          const float co = __shfl_sync(0xffffffffu, cs[(i / 2) & 1], src + i / 4);
+          const float si = __shfl_sync(0xffffffffu, sn[(i / 2) & 1], src + i / 4);
           if (e0 + i < p.rot) {
-            turn((e0 + i) >> 1, c[i], s[i + 1]);
-            c[i + 1] = c[i];
-            s[i] = -s[i + 1];
+            c[i] = c[i + 1] = co;
+            s[i] = kBwd ? si : -si;
+            s[i + 1] = -s[i];
           }
         }
       }
     }
-    if constexpr (kBwd) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = -s[i];  // the transpose turns back
-    }
-    int s0 = s_begin, s_left = p.chunk;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    float a[8], b[8];  // forward: weights folded into cosine and sine; backward: a = weights
+    for (int bi = b_begin; bi < b_end; ++bi) {
+      Batch nxt;
+      if (bi + 1 < b_end) fetch(tok, bi + 1, nxt);
+      else if (tok + nwarps < p.n_tokens) fetch(tok + nwarps, b_begin, nxt);
+      const int t = bi >= nb0;
       const RopeTensor& T = p.t[t];
-      const int n = max(0, min(T.steps - s0, s_left));  // steps of this tensor in the chunk
-      const int first = s0;
-      s0 = max(0, s0 - T.steps);
-      if (n <= 0) continue;
-      s_left -= n;
-      float a[8], b[8];  // forward: weights folded into cosine and sine; backward: a = weights
-#pragma unroll
-      for (int i = 0; i < 8; ++i) { a[i] = c[i]; b[i] = s[i]; }
-      if constexpr (kNorm) {
-        if (kBwd) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] = T.w ? __ldg(T.w + e0 + i) : 1.f;
-        } else if (T.w) {
+      if (bi == b_begin || bi == nb0) {
+        if constexpr (kNorm) {
+          const float* w = red[0] + t * D;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            a[i] = c[i] * __ldg(T.w + e0 + i);
-            b[i] = s[i] * __ldg(T.w + (kHalf ? pe0 + i : e0 + (i ^ 1)));
+            if constexpr (kBwd) {
+              a[i] = w[e0 + i];
+            } else {
+              a[i] = c[i] * w[e0 + i];
+              b[i] = s[i] * w[kHalf ? pe0 + i : e0 + (i ^ 1)];
+            }
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) { a[i] = c[i]; b[i] = s[i]; }
         }
       }
-      const __nv_bfloat16* xp = T.x + tok * T.x_stride + e0;
-      const __nv_bfloat16* gp = T.g + tok * T.g_stride + e0;
-      __nv_bfloat16* op = T.out + tok * T.out_stride + e0;
-      for (int st = first; st < first + n; st += kUnroll) {
-        uint4 vx[kUnroll], vg[kUnroll];
+      const int h0 = (t ? bi - nb0 : bi) * (kUnroll * kRows) + sub;
+      __nv_bfloat16* op = T.out + tok * T.out_stride + (int64_t)h0 * D + e0;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int h = (st + u) * kRows + sub;
-          vx[u] = vg[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (st + u < first + n && h < T.heads) {
-            if constexpr (!kBwd || kNorm) vx[u] = load16(xp + (int64_t)h * D);
-            if constexpr (kBwd) vg[u] = load16(gp + (int64_t)h * D);
+      for (int u = 0; u < kUnroll; ++u) {
+        const bool ok = h0 + u * kRows < T.heads;
+        float o[8];
+        if constexpr (!kBwd) {
+          float x[8], q[8];
+          unpack8(cur.x[u], x);
+          partners<kHalf>(cur.x[u], x, plane, q);
+          float r = 1.f;
+          if constexpr (kNorm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, p.eps));
           }
-        }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int h = (st + u) * kRows + sub;
-          const bool ok = st + u < first + n && h < T.heads;
-          float o[8];
-          if constexpr (!kBwd) {
-            float x[8], q[8];
-            unpack8(vx[u], x);
-            partners<kHalf>(vx[u], x, plane, q);
-            float r = 1.f;
-            if constexpr (kNorm) {
-              float ss = 0.f;
+          for (int i = 0; i < 8; ++i) {
+            o[i] = fmaf(x[i], a[i], q[i] * b[i]);
+            if constexpr (kNorm) o[i] *= r;
+          }
+        } else {
+          float g[8], q[8], dy[8];
+          unpack8(cur.g[u], g);
+          partners<kHalf>(cur.g[u], g, plane, q);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-              r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, p.eps));
-            }
+          for (int i = 0; i < 8; ++i) dy[i] = fmaf(g[i], c[i], q[i] * s[i]);
+          if constexpr (kNorm) {
+            float x[8];
+            unpack8(cur.x[u], x);
+            float ss = 0.f, dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dot = fmaf(dy[i] * a[i], x[i], dot);
+            const float r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, p.eps));
+            const float m = row_sum<kLanes>(dot) * (r * (1.f / D));  // mean(dn n)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              o[i] = fmaf(x[i], a[i], q[i] * b[i]);
-              if constexpr (kNorm) o[i] *= r;
+              const float nrm = x[i] * r;
+              o[i] = r * fmaf(-m, nrm, dy[i] * a[i]);
+              x[i] = ok ? nrm : 0.f;  // a lane without a head adds nothing, whatever eps makes of its zeros
             }
-          } else {
-            float g[8], q[8], dy[8];
-            unpack8(vg[u], g);
-            partners<kHalf>(vg[u], g, plane, q);
+            if (t == 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dy[i] = fmaf(g[i], c[i], q[i] * s[i]);
-            if constexpr (kNorm) {
-              float x[8];
-              unpack8(vx[u], x);
-              float ss = 0.f, dot = 0.f;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) dot = fmaf(dy[i] * a[i], x[i], dot);
-              const float r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, p.eps));
-              const float m = row_sum<kLanes>(dot) * (r * (1.f / D));  // mean(dn n)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float nrm = x[i] * r;
-                if (ok) acc[t][i] = fmaf(dy[i], nrm, acc[t][i]);
-                o[i] = r * fmaf(-m, nrm, dy[i] * a[i]);
-              }
+              for (int i = 0; i < 8; ++i) acc0[i] = fmaf(dy[i], x[i], acc0[i]);
             } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] = dy[i];
+              for (int i = 0; i < 8; ++i) acc1[i] = fmaf(dy[i], x[i], acc1[i]);
             }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = dy[i];
           }
-          if (ok) *reinterpret_cast<uint4*>(op + (int64_t)h * D) = pack8(o);
         }
+        if (ok) *reinterpret_cast<uint4*>(op + u * kRows * D) = pack8(o);
       }
+      cur = nxt;
     }
   }
   if constexpr (kDw) {
     if (p.partial) {
-      __shared__ float red[kRopeThreads / 32 * kRows][2 * D];
+      __syncthreads();  // the weights in red[0] have been read
       float* row = red[(threadIdx.x >> 5) * kRows + sub];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        row[e0 + i] = acc[0][i];
-        row[D + e0 + i] = acc[1][i];
+        row[e0 + i] = acc0[i];
+        row[D + e0 + i] = acc1[i];
       }
       __syncthreads();
       if (threadIdx.x < 2 * D) {
@@ -323,12 +361,13 @@ RopeKernel pick(bool half, bool norm) {
 // Blocks that the weight gradients' workspace has rows for.
 constexpr int kMaxDwBlocks = 2048;
 
-cudaError_t launch_rope(const zl_qk_rope_desc& d, bool bwd, RopeParams& p, float* dwq, float* dwk,
+cudaError_t launch_rope(const zl_qk_rope_desc& d, bool bwd, int sms, RopeParams& p, float* dwq, float* dwk,
                         cudaStream_t stream) {
-  const int D = d.head_dim, rows = 256 / D;
+  const int D = d.head_dim;
+  const int per_batch = (bwd && d.norm ? rope_unroll<true, true>() : rope_unroll<false, true>()) * (256 / D);  // heads
   for (int t = 0; t < 2; ++t) {
     p.t[t].heads = t == 0 ? d.n_q_heads : d.n_kv_heads;
-    p.t[t].steps = (p.t[t].heads + rows - 1) / rows;
+    p.t[t].batches = (p.t[t].heads + per_batch - 1) / per_batch;
   }
   p.n_tokens = d.n_tokens;
   p.rot = d.rot_dim;
@@ -339,23 +378,24 @@ cudaError_t launch_rope(const zl_qk_rope_desc& d, bool bwd, RopeParams& p, float
   p.amplitude = d.amplitude;
   RopeKernel k = D == 128 ? (bwd ? pick<128, true>(d.half_layout, d.norm) : pick<128, false>(d.half_layout, d.norm))
                           : (bwd ? pick<64, true>(d.half_layout, d.norm) : pick<64, false>(d.half_layout, d.norm));
-  int dev = 0, sms = 0, per_sm = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, kRopeThreads, 0);
+  static PerDeviceInt resident[16];  // blocks per SM of each variant
+  int per_sm = 0;
+  cudaError_t e = resident[(D == 128) * 8 + bwd * 4 + d.half_layout * 2 + d.norm].get(&per_sm, [&](int, int* v) {
+    const cudaError_t r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, k, kRopeThreads, 0);
+    if (*v < 1) *v = 1;
+    return r;
+  });
   if (e != cudaSuccess) return e;
-  if (per_sm < 1) per_sm = 1;
-  // One wave of blocks, a warp per token; with fewer tokens than warps a token's heads are split
-  // over several warps (each forms the token's sines again), down to kUnroll steps a warp.
+  // One wave of blocks, a warp per token; with fewer tokens than warps a token's heads are split over several
+  // warps (each forms the token's sines again), down to one batch a warp.
   const int64_t warps = (int64_t)sms * per_sm * (kRopeThreads / 32);
-  const int steps = p.t[0].steps + p.t[1].steps;
-  int64_t chunks = d.n_tokens > 0 ? warps / d.n_tokens : 1;
-  const int64_t most = (steps + 3) / 4;
-  if (chunks > most) chunks = most;
+  const int batches = p.t[0].batches + p.t[1].batches;
+  int64_t chunks = warps / d.n_tokens;
+  if (chunks > batches) chunks = batches;
   if (p.partial && chunks > kMaxDwBlocks) chunks = kMaxDwBlocks;
   if (chunks < 1) chunks = 1;
-  p.chunk = (int)((steps + chunks - 1) / chunks);
-  const int ny = (steps + p.chunk - 1) / p.chunk;
+  p.chunk = (int)((batches + chunks - 1) / chunks);
+  const int ny = (batches + p.chunk - 1) / p.chunk;
   int64_t nx = (d.n_tokens + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   const int64_t cap = ((int64_t)sms * per_sm + ny - 1) / ny;
   if (nx > cap) nx = cap;
@@ -368,14 +408,18 @@ cudaError_t launch_rope(const zl_qk_rope_desc& d, bool bwd, RopeParams& p, float
   return cudaGetLastError();
 }
 
-// The kernels are built for sm_103a alone.
-zl_status check_device() {
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return ZL_ERR_CUDA;
-  return major == 10 && minor == 3 ? ZL_OK : ZL_ERR_UNSUPPORTED;
+// SM count of the current device; the kernels are built for sm_103a alone.
+zl_status check_device(int* sms) {
+  static PerDeviceInt count;
+  const cudaError_t e = count.get(sms, [](int dev, int* v) {
+    int major = 0, minor = 0;
+    cudaError_t r = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (r == cudaSuccess) r = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (r == cudaSuccess) r = cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
+    if (major != 10 || minor != 3) *v = -1;
+    return r;
+  });
+  return e != cudaSuccess ? ZL_ERR_CUDA : *sms > 0 ? ZL_OK : ZL_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -422,7 +466,8 @@ extern "C" zl_status zl_qk_rope_fwd(const zl_qk_rope_desc* d, const void* q, int
       (s = check_tensor(k_out, k_out_stride, d->n_kv_heads, D)) != ZL_OK)
     return s;
   if (d->rot_dim > 0 && (!positions || !freq)) return ZL_ERR_INVALID_ARG;
-  if ((s = check_device()) != ZL_OK) return s;
+  int sms = 0;
+  if ((s = check_device(&sms)) != ZL_OK) return s;
   RopeParams p{};
   p.t[0] = {static_cast<const __nv_bfloat16*>(q), nullptr, static_cast<__nv_bfloat16*>(q_out), q_weight, q_stride, 0,
             q_out_stride, 0, 0};
@@ -430,7 +475,7 @@ extern "C" zl_status zl_qk_rope_fwd(const zl_qk_rope_desc* d, const void* q, int
             k_out_stride, 0, 0};
   p.positions = positions;
   p.freq = freq;
-  return launch_rope(*d, false, p, nullptr, nullptr, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
+  return launch_rope(*d, false, sms, p, nullptr, nullptr, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
 
 extern "C" zl_status zl_qk_rope_bwd(const zl_qk_rope_desc* d, const void* q, int64_t q_stride, const void* k,
@@ -465,7 +510,8 @@ extern "C" zl_status zl_qk_rope_bwd(const zl_qk_rope_desc* d, const void* q, int
       (s = check_tensor(dq, dq_stride, d->n_q_heads, D)) != ZL_OK || (s = check_tensor(dk, dk_stride, d->n_kv_heads, D)) != ZL_OK)
     return s;
   if (d->rot_dim > 0 && (!positions || !freq)) return ZL_ERR_INVALID_ARG;
-  if ((s = check_device()) != ZL_OK) return s;
+  int sms = 0;
+  if ((s = check_device(&sms)) != ZL_OK) return s;
   RopeParams p{};
   p.t[0] = {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(dq_out), static_cast<__nv_bfloat16*>(dq),
             q_weight, q_stride, dq_out_stride, dq_stride, 0, 0};
@@ -474,5 +520,5 @@ extern "C" zl_status zl_qk_rope_bwd(const zl_qk_rope_desc* d, const void* q, int
   p.positions = positions;
   p.freq = freq;
   p.partial = dw ? static_cast<float*>(workspace) : nullptr;
-  return launch_rope(*d, true, p, dq_weight, dk_weight, st) == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
+  return launch_rope(*d, true, sms, p, dq_weight, dk_weight, st) == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }

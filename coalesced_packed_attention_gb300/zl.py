@@ -413,33 +413,71 @@ def exported_symbols() -> List[str]:
 
 
 # ---------------------------------------------------------------- causal sequences
-def _heads(t, what, shape=None, dtype=None):
-    """(pointer, token stride) of a bf16 [tokens, heads, d] CUDA tensor whose heads are
+_torch_module = None
+
+
+def _torch():
+    """torch, imported by the first call that needs it (the launches below run every layer, and an import
+    statement costs them half a microsecond each)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _heads(t, what, shape, dev):
+    """(pointer, token stride) of a bf16 [tokens, heads, d] tensor on CUDA device `dev` whose heads are
     contiguous; the token stride is free, so views of a fused projection pass."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-        raise TypeError(f"{what}: expected a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{what}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{what}: expected shape {shape or '[tokens, heads, d]'}, got {tuple(t.shape)}")
-    n, h, d = t.shape
-    if n == 0 or h == 0:
-        return None, h * d
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+        raise TypeError(f"{what}: expected a CUDA tensor of {torch.bfloat16}, got {getattr(t, 'dtype', type(t))}")
+    if t.get_device() != dev:
+        raise (ValueError if t.is_cuda else TypeError)(f"{what}: expected a tensor on cuda:{dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    n, h, d = shape
+    s0, s1, s2 = t.stride()
+    if n <= 1 or h == 0:
+        s0 = h * d  # a lone token has no next one
+        if n == 0 or h == 0:
+            return None, s0
+    if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous, got strides {t.stride()}")
-    stride = t.stride(0) if n > 1 else h * d  # a lone token has no next one
-    if stride < h * d:
-        raise ValueError(f"{what}: token stride {stride} below heads * d = {h * d}")
-    return t.data_ptr(), stride
+    if s0 < h * d:
+        raise ValueError(f"{what}: token stride {s0} below heads * d = {h * d}")
+    return t.data_ptr(), s0
 
 
-def _on_current_device(*tensors):
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.device.index != dev:
-            raise ValueError(f"tensor on cuda:{t.device.index}, current device is cuda:{dev}")
+def _dense(t, what, dtype, shape, dev):
+    """Pointer of a contiguous tensor of exactly this type and shape on CUDA device `dev`."""
+    if not isinstance(t, _torch().Tensor) or t.dtype is not dtype:
+        raise TypeError(f"{what}: expected a CUDA tensor of {dtype}, got {getattr(t, 'dtype', type(t))}")
+    if t.get_device() != dev:
+        raise (ValueError if t.is_cuda else TypeError)(f"{what}: expected a tensor on cuda:{dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    return t.data_ptr()
+
+
+def _scratch(t, what, nbytes, dev):
+    """Pointer of a uint8 workspace of at least nbytes bytes on CUDA device `dev` (None where none is needed)."""
+    torch = _torch()
+    if t is None and nbytes == 0:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or t.get_device() != dev:
+        raise TypeError(f"{what}: expected a torch.uint8 tensor on cuda:{dev}")
+    if not t.is_contiguous() or t.numel() < nbytes:
+        raise ValueError(f"{what}: needs {nbytes} contiguous bytes, has {t.numel()}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -481,6 +519,7 @@ class RotaryTable:
     half: bool
     axis_pairs: List[int]
     amplitude: float
+    last: tuple = (None, None)  # the last call's descriptor, by its key
 
 
 def rotary_table(inv_freq: Sequence[float], layout: str = "half", axis_pairs: Optional[Sequence[int]] = None,
@@ -510,50 +549,66 @@ def zl_qk_rope_workspace_bytes(n_tokens: int, n_q_heads: int, n_kv_heads: int, h
     return b.value
 
 
-def _rope_args(q, k, positions, table, norm, eps, q_weight, k_weight, others):
-    """Descriptor, and the pointers of positions, frequencies and weights."""
-    import torch
+_PLAIN = RotaryTable(None, 0, False, [], 1.0)  # no rotation
+
+
+def _rope_args(q, k, positions, table, norm, eps, q_weight, k_weight):
+    """(descriptor, device, query shape, key shape, pointers of positions, frequencies and weights)."""
+    torch = _torch()
     lead = q if q is not None else k
-    if lead is None:
-        raise ValueError("q and k: at least one is needed")
-    if lead.dim() != 3:
+    if not isinstance(lead, torch.Tensor):
+        raise TypeError("q and k: at least one tensor is needed")
+    if lead.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError(f"expected [tokens, heads, d], got {tuple(lead.shape)}")
-    n, _, d = lead.shape
-    hq, hk = (t.shape[1] if t is not None and t.dim() == 3 else 0 for t in (q, k))
-    _on_current_device(q, k, positions, q_weight, k_weight, table.freq if table is not None else None, *others)
-    if table is not None and table.rot_dim > 0:
+    if not lead.is_cuda:
+        raise TypeError(f"expected CUDA tensors, got one on {lead.device}")
+    dev = torch._C._cuda_getDevice()
+    n, hq, d = lead.shape
+    hk = k.shape[1] if k is not None else 0
+    if q is None:
+        hq = 0
+    if table is None:
+        table = _PLAIN
+    pos = freq = None
+    if table.rot_dim > 0:
         axes = len(table.axis_pairs)
-        if positions is None:
-            raise ValueError("positions: a rotation needs them")
-        pos = _ptr(positions, torch.int32, "positions")
-        if tuple(positions.shape) not in ((n, axes),) + (((n,),) if axes == 1 else ()):
-            raise ValueError(f"positions: expected shape {(n, axes)}, got {tuple(positions.shape)}")
-        freq = _ptr(table.freq, torch.int64, "table", table.rot_dim // 2)
-        desc = zl_qk_rope_desc(n, hq, hk, d, int(norm), eps, table.rot_dim, int(table.half), axes,
-                               (ctypes.c_int32 * 3)(*table.axis_pairs), table.amplitude)
-    else:
-        pos = freq = None
-        desc = zl_qk_rope_desc(n, hq, hk, d, int(norm), eps, 0, 0, 0, (ctypes.c_int32 * 3)(), 1.0)
-    return desc, n, hq, hk, d, pos, freq, _ptr(q_weight, torch.float32, "q_weight", d), _ptr(k_weight, torch.float32, "k_weight", d)
+        pos = _dense(positions, "positions", torch.int32,
+                     (n,) if axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1 else (n, axes), dev)
+        freq = _dense(table.freq, "table", torch.int64, (table.rot_dim // 2,), dev)
+    key = (n, hq, hk, d, norm, eps)
+    last = table.last
+    if last[0] != key:
+        pairs = (table.axis_pairs + [0, 0, 0])[:3]
+        last = (key, zl_qk_rope_desc(n, hq, hk, d, int(norm), eps, table.rot_dim, int(table.half), len(table.axis_pairs),
+                                     (ctypes.c_int32 * 3)(*pairs), table.amplitude))
+        table.last = last
+    qw = _dense(q_weight, "q_weight", torch.float32, (d,), dev) if q_weight is not None else None
+    kw = _dense(k_weight, "k_weight", torch.float32, (d,), dev) if k_weight is not None else None
+    return last[1], dev, (n, hq, d), (n, hk, d), pos, freq, qw, kw
 
 
-def _maybe_heads(t, what, n, h, d):
-    if t is None and h == 0:
+def _maybe_heads(t, what, shape, dev):
+    if t is None and shape[1] == 0:
         return None, 0
-    return _heads(t, what, (n, h, d))
+    return _heads(t, what, shape, dev)
 
 
 def zl_qk_rope_fwd(q, k, q_out, k_out, positions, table: Optional[RotaryTable], norm: bool = False, q_weight=None,
                    k_weight=None, eps: float = 1e-6, stream=None):
     """Every head of q [tokens, Hq, d] and k [tokens, Hkv, d] (either may be None) normalised
     (norm=True) and rotated at its token's positions (int32 [tokens, axes]; table None: no
-    rotation) into q_out, k_out, which may be q and k themselves."""
-    desc, n, hq, hk, d, pos, freq, qw, kw = _rope_args(q, k, positions, table, norm, eps, q_weight, k_weight,
-                                                       (q_out, k_out))
-    _check(load_library().zl_qk_rope_fwd(
-        ctypes.byref(desc), *_maybe_heads(q, "q", n, hq, d), *_maybe_heads(k, "k", n, hk, d), qw, kw, pos, freq,
-        *_maybe_heads(q_out, "q_out", n, hq, d), *_maybe_heads(k_out, "k_out", n, hk, d), _stream(stream)),
-        "zl_qk_rope_fwd")
+    rotation) into q_out, k_out, which may be q and k themselves.  Tensors live on the current device."""
+    desc, dev, sq, sk, pos, freq, qw, kw = _rope_args(q, k, positions, table, norm, eps, q_weight, k_weight)
+    pq, nq = _maybe_heads(q, "q", sq, dev)
+    pk, nk = _maybe_heads(k, "k", sk, dev)
+    oq, mq = _maybe_heads(q_out, "q_out", sq, dev)
+    ok, mk = _maybe_heads(k_out, "k_out", sk, dev)
+    st = load_library().zl_qk_rope_fwd(desc, pq, nq, pk, nk, qw, kw, pos, freq, oq, mq, ok, mk, _raw_stream(stream, dev))
+    if st:
+        _check(st, "zl_qk_rope_fwd")
+
+
+_dw_bytes: Dict[int, int] = {}  # workspace of the weights' gradients by head dim
 
 
 def zl_qk_rope_bwd(q, k, dq_out, dk_out, dq, dk, positions, table: Optional[RotaryTable], norm: bool = False,
@@ -562,21 +617,26 @@ def zl_qk_rope_bwd(q, k, dq_out, dk_out, dq, dk, positions, table: Optional[Rota
     """Gradient of zl_qk_rope_fwd: dq, dk from dq_out, dk_out.  With norm=True q and k are the
     forward's inputs (else None will do) and dq_weight, dk_weight, where given, receive the
     weights' gradients (workspace: zl_qk_rope_workspace_bytes)."""
-    import torch
-    desc, n, hq, hk, d, pos, freq, qw, kw = _rope_args(dq_out, dk_out, positions, table, norm, eps, q_weight, k_weight,
-                                                       (q, k, dq, dk, dq_weight, dk_weight, workspace))
-    if norm:
-        xq, xk = _maybe_heads(q, "q", n, hq, d), _maybe_heads(k, "k", n, hk, d)
-    else:
-        xq = xk = (None, 0)
-    need = None
+    torch = _torch()
+    desc, dev, sq, sk, pos, freq, qw, kw = _rope_args(dq_out, dk_out, positions, table, norm, eps, q_weight, k_weight)
+    pq, nq = _maybe_heads(q, "q", sq, dev) if norm else (None, 0)
+    pk, nk = _maybe_heads(k, "k", sk, dev) if norm else (None, 0)
+    gq, lq = _maybe_heads(dq_out, "dq_out", sq, dev)
+    gk, lk = _maybe_heads(dk_out, "dk_out", sk, dev)
+    oq, mq = _maybe_heads(dq, "dq", sq, dev)
+    ok, mk = _maybe_heads(dk, "dk", sk, dev)
+    dqw = dkw = ws = None
     if dq_weight is not None or dk_weight is not None:
-        need = zl_qk_rope_workspace_bytes(n, hq, hk, d)
-    _check(load_library().zl_qk_rope_bwd(
-        ctypes.byref(desc), *xq, *xk, qw, kw, pos, freq, *_maybe_heads(dq_out, "dq_out", n, hq, d),
-        *_maybe_heads(dk_out, "dk_out", n, hk, d), *_maybe_heads(dq, "dq", n, hq, d), *_maybe_heads(dk, "dk", n, hk, d),
-        _ptr(dq_weight, torch.float32, "dq_weight", d), _ptr(dk_weight, torch.float32, "dk_weight", d),
-        _ptr(workspace, torch.uint8, "workspace", need), _stream(stream)), "zl_qk_rope_bwd")
+        d = sq[2]
+        if d not in _dw_bytes:
+            _dw_bytes[d] = zl_qk_rope_workspace_bytes(1, 1, 1, d)
+        dqw = _dense(dq_weight, "dq_weight", torch.float32, (d,), dev) if dq_weight is not None else None
+        dkw = _dense(dk_weight, "dk_weight", torch.float32, (d,), dev) if dk_weight is not None else None
+        ws = _scratch(workspace, "workspace", _dw_bytes[d], dev)
+    st = load_library().zl_qk_rope_bwd(desc, pq, nq, pk, nk, qw, kw, pos, freq, gq, lq, gk, lk, oq, mq, ok, mk, dqw, dkw,
+                                       ws, _raw_stream(stream, dev))
+    if st:
+        _check(st, "zl_qk_rope_bwd")
 
 
 class CausalPlan:
@@ -588,6 +648,8 @@ class CausalPlan:
         self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
         self.q_tokens, self.kv_tokens = q_tokens, kv_tokens
         self.device = device  # CUDA device index the plan was built on (None: host-only plan)
+        self.q_shape, self.kv_shape = (q_tokens, n_q_heads, head_dim), (kv_tokens, n_kv_heads, head_dim)
+        self.lse_shape = (q_tokens, n_q_heads)
         f, b = ctypes.c_int64(), ctypes.c_int64()
         _check(load_library().zl_causal_plan_workspace(self.handle, ctypes.byref(f), ctypes.byref(b)),
                "zl_causal_plan_workspace")
@@ -657,39 +719,43 @@ def allocate_causal(plan: CausalPlan, device="cuda", backward: bool = False) -> 
     return out
 
 
-def _causal_shapes(plan: CausalPlan):
-    return ((plan.q_tokens, plan.n_q_heads, plan.head_dim), (plan.kv_tokens, plan.n_kv_heads, plan.head_dim))
-
-
-def _whole(t, what, shape, dtype):
-    """Pointer of a contiguous CUDA tensor of exactly this shape (None where it is empty)."""
-    p = _ptr(t, dtype, what)
-    if p is None or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {None if t is None else tuple(t.shape)}")
-    return p if t.numel() else None
+def _plan_dev(plan: CausalPlan) -> int:
+    return -2 if plan.device is None else plan.device  # no tensor is on a host-only plan's device
 
 
 def zl_causal_attn_fwd(plan: CausalPlan, q, k, v, o, lse, workspace, scale: float, stream=None):
-    import torch
-    _on_plan_device(plan, q, k, v, o, lse, workspace)
-    sq, sk = _causal_shapes(plan)
+    """Causal attention of every sequence of the plan: q [q_tokens, Hq, d], k, v [kv_tokens, Hkv, d] (views of a
+    fused projection will do) into o (contiguous) and lse [q_tokens, Hq]; workspace: plan.fwd_workspace_bytes."""
+    torch = _torch()
+    dev = _plan_dev(plan)
+    pq, nq = _heads(q, "q", plan.q_shape, dev)
+    pk, nk = _heads(k, "k", plan.kv_shape, dev)
+    pv, nv = _heads(v, "v", plan.kv_shape, dev)
     st = load_library().zl_causal_attn_fwd(
-        plan.handle, *_heads(q, "q", sq), *_heads(k, "k", sk), *_heads(v, "v", sk), _whole(o, "o", sq, torch.bfloat16),
-        _whole(lse, "lse", sq[:2], torch.float32),
-        _ptr(workspace, torch.uint8, "workspace", plan.fwd_workspace_bytes), ctypes.c_float(scale), _stream(stream))
-    _check(st, "zl_causal_attn_fwd")
+        plan.handle, pq, nq, pk, nk, pv, nv, _dense(o, "o", torch.bfloat16, plan.q_shape, dev),
+        _dense(lse, "lse", torch.float32, plan.lse_shape, dev),
+        _scratch(workspace, "workspace", plan.fwd_workspace_bytes, dev), scale, _raw_stream(stream, dev))
+    if st:
+        _check(st, "zl_causal_attn_fwd")
 
 
 def zl_causal_attn_bwd(plan: CausalPlan, q, k, v, o, d_o, lse, dq, dk, dv, workspace, scale: float, stream=None):
-    import torch
-    _on_plan_device(plan, q, k, v, o, d_o, lse, dq, dk, dv, workspace)
-    sq, sk = _causal_shapes(plan)
+    """Gradients dq, dk, dv (bf16, token strides free) of zl_causal_attn_fwd from d_o (contiguous) and the o and lse
+    that it left; workspace: plan.bwd_workspace_bytes."""
+    torch = _torch()
+    dev = _plan_dev(plan)
+    pq, nq = _heads(q, "q", plan.q_shape, dev)
+    pk, nk = _heads(k, "k", plan.kv_shape, dev)
+    pv, nv = _heads(v, "v", plan.kv_shape, dev)
+    gq, mq = _heads(dq, "dq", plan.q_shape, dev)
+    gk, mk = _heads(dk, "dk", plan.kv_shape, dev)
+    gv, mv = _heads(dv, "dv", plan.kv_shape, dev)
     st = load_library().zl_causal_attn_bwd(
-        plan.handle, *_heads(q, "q", sq), *_heads(k, "k", sk), *_heads(v, "v", sk), _whole(o, "o", sq, torch.bfloat16),
-        _whole(d_o, "d_o", sq, torch.bfloat16), _whole(lse, "lse", sq[:2], torch.float32), *_heads(dq, "dq", sq),
-        *_heads(dk, "dk", sk), *_heads(dv, "dv", sk),
-        _ptr(workspace, torch.uint8, "workspace", plan.bwd_workspace_bytes), ctypes.c_float(scale), _stream(stream))
-    _check(st, "zl_causal_attn_bwd")
+        plan.handle, pq, nq, pk, nk, pv, nv, _dense(o, "o", torch.bfloat16, plan.q_shape, dev),
+        _dense(d_o, "d_o", torch.bfloat16, plan.q_shape, dev), _dense(lse, "lse", torch.float32, plan.lse_shape, dev), gq, mq,
+        gk, mk, gv, mv, _scratch(workspace, "workspace", plan.bwd_workspace_bytes, dev), scale, _raw_stream(stream, dev))
+    if st:
+        _check(st, "zl_causal_attn_bwd")
 
 
 def zl_causal_get_device_status(plan: CausalPlan, stream=None) -> int:
@@ -712,7 +778,7 @@ def _qkv_views(plan: CausalPlan, qkv, what="qkv"):
 def allocate_qkv_attention(plan: CausalPlan, device="cuda", backward: bool = False) -> Dict[str, "object"]:
     """allocate_causal plus the normalised, rotated queries and keys, and the weights' gradients."""
     import torch
-    sq, sk = _causal_shapes(plan)
+    sq, sk = plan.q_shape, plan.kv_shape
     out = allocate_causal(plan, device, backward)
     out["q"], out["k"] = (torch.empty(s, dtype=torch.bfloat16, device=device) for s in (sq, sk))
     if backward:
