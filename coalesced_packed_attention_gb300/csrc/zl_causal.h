@@ -49,15 +49,21 @@ struct CausalSeq {
   int64_t acc_block;  // first 128-row block of the sequence in the dQ accumulator: [kv head][query block]
 };
 
+// Tiles carry what the kernels need of their sequence, so that a tile is one load away, not two in a row.
 // One forward tile: up to two query blocks of one (sequence, key head) over a range of key blocks.
-struct CausalTile {
-  int32_t seq, head, block;  // first query block (block, block + 1)
-  int32_t kv_lo, kv_hi;      // key blocks [kv_lo, kv_hi) of 128, as far as the rows see them
-  int32_t part;              // -1: final output; else the tile's slot of partial results
+struct alignas(16) CausalTile {
+  int32_t q_row, q_len, kv_row, kv_len;  // the sequence: first rows and lengths
+  int32_t head, block;                   // key head; first query block (block, block + 1)
+  int32_t kv_lo, kv_hi;                  // key blocks [kv_lo, kv_hi) of 128, as far as the rows see them
+  int32_t part;                          // -1: final output; else the tile's slot of partial results
+  int32_t seq, pad[2];
 };
 // One backward tile: 128 keys of one (sequence, key head).
-struct CausalBwdTile {
-  int32_t seq, head, block, pad;
+struct alignas(16) CausalBwdTile {
+  int32_t q_row, q_len, kv_row, kv_len;
+  int32_t head, block;
+  int32_t acc_block;  // the head's first block in the dQ accumulator
+  int32_t seq;
 };
 // Rows whose key range was split: the combine of `parts` slots from `slot` on.
 struct CausalMerge {
@@ -65,7 +71,6 @@ struct CausalMerge {
 };
 
 struct CausalFwdParams {
-  const CausalSeq* seqs;
   const CausalTile* tiles;
   const int32_t* tile_ptr;  // tiles of thread block b: [tile_ptr[b], tile_ptr[b + 1])
   int32_t* status;
@@ -90,7 +95,6 @@ struct CausalMergeParams {
 };
 
 struct CausalBwdParams {
-  const CausalSeq* seqs;
   const CausalBwdTile* tiles;
   const int32_t* tile_ptr;
   int32_t* status;

@@ -103,7 +103,6 @@ extern "C" zl_status zl_causal_attn_fwd(const zl_causal_plan* p, const void* q, 
            !kv_map(&tv, v, p->kv_tokens, v_stride, p->n_kv_heads, p->head_dim))
     return ZL_ERR_CUDA;
   CausalFwdParams fp;
-  fp.seqs = p->d_seqs;
   fp.tiles = p->d_fwd_tiles;
   fp.tile_ptr = p->d_fwd_ptr;
   fp.status = p->d_status;
@@ -165,7 +164,6 @@ extern "C" zl_status zl_causal_attn_bwd(const zl_causal_plan* p, const void* q, 
              !row_map(&tdo, d_o, p->q_tokens, (int64_t)p->n_q_heads * d, p->n_kv_heads, p->group, d))
       return ZL_ERR_CUDA;
     CausalBwdParams bp;
-    bp.seqs = p->d_seqs;
     bp.tiles = p->d_bwd_tiles;
     bp.tile_ptr = p->d_bwd_ptr;
     bp.status = p->d_status;

@@ -119,9 +119,17 @@ __device__ __forceinline__ void tma_rows(void* dst, const void* map, uint64_t* b
       : "memory");
 }
 
-// The query blocks that a key tile walks: [first, end).
+// The query blocks that a key tile walks, [first, first + n), downwards from one that differs from tile to tile and
+// round: tiles of one head that run side by side are then on neighbouring blocks, never the same one (they would
+// contend on its dQ rows), and what they read and add to together is a few MB.  (Upwards from each tile's diagonal,
+// eight heads to a key head, neighbours are 8 blocks apart, and 8192 tokens of four heads are touched every 20 us,
+// past what L2 holds: xx us a step of 26 487 tokens against xx.)
 struct BwdSpan {
-  int first, n, nqb;
+  int first, n, nqb, start;
+  __device__ __forceinline__ int block(int step) const {
+    const int b = start - step;
+    return first + (b < 0 ? b + n : b);
+  }
 };
 __device__ __forceinline__ BwdSpan walk_of(int block, int q_len, int kv_len, int tb) {
   BwdSpan s;
@@ -129,6 +137,7 @@ __device__ __forceinline__ BwdSpan walk_of(int block, int q_len, int kv_len, int
   const int t0 = max(0, block * 128 - (kv_len - q_len));  // first token that sees the tile's first key
   s.first = min(s.nqb, t0 / tb);
   s.n = s.nqb - s.first;
+  s.start = s.n > 0 ? s.n - 1 - block % s.n : 0;
   return s;
 }
 
@@ -228,12 +237,11 @@ __global__ void __launch_bounds__(512, 1)
         bool ok = true;
         for (int t = t_begin; t < t_end && ok; ++t) {
           const CausalBwdTile tl = p.tiles[t];
-          const CausalSeq sq = p.seqs[tl.seq];
-          const BwdSpan sp = walk_of(tl.block, sq.q_len, sq.kv_len, tb);
+          const BwdSpan sp = walk_of(tl.block, tl.q_len, tl.kv_len, tb);
           if (sp.n == 0) continue;
           if (!cbwait(kv_empty, (kt & 1) ^ 1, abort_flag, p.wait_limit, p.status)) break;
           ++kt;
-          const int kvrow = (int)(sq.kv_offset + (int64_t)tl.block * 128);
+          const int kvrow = tl.kv_row + tl.block * 128;
           mbar_arrive_expect_tx(kv_full, 2 * L::kTile);
           if (p.withhold_load && kt == 1) {
             // test hook: the announced bytes never arrive; a bounded wait runs out
@@ -244,7 +252,7 @@ __global__ void __launch_bounds__(512, 1)
             }
           }
           for (int is = 0; is < sp.n; ++is) {
-            const int tok = (int)(sq.q_offset + (int64_t)(sp.first + is) * tb);
+            const int tok = tl.q_row + sp.block(is) * tb;
             const uint32_t st = qit & 1, ph = (qit >> 1) & 1;
             if (!cbwait(q_empty + st, ph ^ 1, abort_flag, p.wait_limit, p.status)) { ok = false; break; }
             mbar_arrive_expect_tx(q_full + st, row_bytes);
@@ -290,22 +298,21 @@ __global__ void __launch_bounds__(512, 1)
       bool ok = true;
       for (int t = t_begin; t < t_end && ok; ++t) {
         const CausalBwdTile tl = p.tiles[t];
-        const CausalSeq sq = p.seqs[tl.seq];
-        const BwdSpan sp = walk_of(tl.block, sq.q_len, sq.kv_len, tb);
+        const BwdSpan sp = walk_of(tl.block, tl.q_len, tl.kv_len, tb);
         if (sp.n == 0) continue;
         if (!wait_w(kv_full, kt & 1)) break;
         ++kt;
-        const int kvrows = sq.kv_len - tl.block * 128;
+        const int kvrows = tl.kv_len - tl.block * 128;
         if (kvrows < 128) {
           zero_tile_rows<D>(aK, kvrows, lane);
           zero_tile_rows<D>(aV, kvrows, lane);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        // rows of the walk's last block that belong to the sequence
-        const int last_rows = (sq.q_len - (sp.nqb - 1) * tb) * p.group;
+        // rows of the sequence's last query block that belong to it
+        const int last_rows = (tl.q_len - (sp.nqb - 1) * tb) * p.group;
         auto fix_rows = [&](int is, uint32_t tile) {
-          if (is == sp.n - 1 && last_rows < box_rows) {
+          if (last_rows < box_rows && sp.block(is) == sp.nqb - 1) {
             zero_tile_rows<D>(tile, last_rows, lane);
             fence_proxy_async_smem();
             __syncwarp();
@@ -384,9 +391,8 @@ __global__ void __launch_bounds__(512, 1)
     bool ok = true;
     for (int t = t_begin; t < t_end && ok; ++t) {
       const CausalBwdTile tl = p.tiles[t];
-      const CausalSeq sq = p.seqs[tl.seq];
-      const BwdSpan sp = walk_of(tl.block, sq.q_len, sq.kv_len, tb);
-      float* acc_hd = p.acc + (sq.acc_block + (int64_t)tl.head * sp.nqb) * (128 * D);
+      const BwdSpan sp = walk_of(tl.block, tl.q_len, tl.kv_len, tb);
+      float* acc_hd = p.acc + (int64_t)tl.acc_block * (128 * D);
       for (int is = 0; is < sp.n; ++is) {
         if (!__all_sync(0xffffffffu, cbwait(dq_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
         tc_fence_after();
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(512, 1)
         mbar_arrive(dq_empty);  // the next block's dP^T may overwrite R1
         // chunk c (columns 32c..32c+31) of a block is 16 KB contiguous in the accumulator, [8 column
         // groups][128 rows][4]; two buffers, so one chunk is staged while the previous one is read
-        float* blk = acc_hd + (int64_t)(sp.first + is) * (128 * D);
+        float* blk = acc_hd + (int64_t)sp.block(is) * (128 * D);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           const uint32_t b = sit & 1, use = sit >> 1;
@@ -443,11 +449,10 @@ __global__ void __launch_bounds__(512, 1)
     uint32_t nblocks = 0, ntiles = 0;
     for (int t = t_begin; t < t_end; ++t) {
       const CausalBwdTile tl = p.tiles[t];
-      const CausalSeq sq = p.seqs[tl.seq];
-      const BwdSpan sp = walk_of(tl.block, sq.q_len, sq.kv_len, tb);
+      const BwdSpan sp = walk_of(tl.block, tl.q_len, tl.kv_len, tb);
       const int key = tl.block * 128 + t_key;
-      const bool key_ok = key < sq.kv_len;
-      const int64_t ld_base = sq.q_offset * p.n_q_heads + (int64_t)tl.head * p.group + rh;
+      const bool key_ok = key < tl.kv_len;
+      const int64_t ld_base = (int64_t)tl.q_row * p.n_q_heads + (int64_t)tl.head * p.group + rh;
       bool ok = true;
       float lse_n = -kInfC, d_n = 0.f;
       // rows past the sequence and rows that see no key (LSE = -inf) get exp2(-inf) = 0 everywhere
@@ -455,7 +460,7 @@ __global__ void __launch_bounds__(512, 1)
         const int tok = blk * tb + rt;
         lse_n = -kInfC;
         d_n = 0.f;
-        if (rt < tb && tok < sq.q_len) {
+        if (rt < tb && tok < tl.q_len) {
           const int64_t i = ld_base + (int64_t)tok * p.n_q_heads;
           const float l = __ldg(p.lse + i);
           if (l != -kInfC) {
@@ -464,7 +469,7 @@ __global__ void __launch_bounds__(512, 1)
           }
         }
       };
-      if (wg == 0 && sp.n > 0) fetch(sp.first);
+      if (wg == 0 && sp.n > 0) fetch(sp.block(0));
       for (int is = 0; is < sp.n; ++is) {
         if (wg == 0) {
           sLD[256 * (nblocks & 1) + t_key] = lse_n;
@@ -472,12 +477,12 @@ __global__ void __launch_bounds__(512, 1)
         }
         mbar_arrive(ld_full);  // bounded stand-in for a barrier of both warpgroups
         if (!__all_sync(0xffffffffu, cbwait(ld_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
-        if (wg == 0 && is + 1 < sp.n) fetch(sp.first + is + 1);
+        if (wg == 0 && is + 1 < sp.n) fetch(sp.block(is + 1));
 
         const float* sLSE = sLD + 256 * (nblocks & 1);
         const float* sD = sLSE + 128;
         // first column (query row of the block) that sees this key; 128: none
-        const int first = key_ok ? max(0, (key - (sq.kv_len - sq.q_len) - (sp.first + is) * tb) * p.group) : 128;
+        const int first = key_ok ? max(0, (key - (tl.kv_len - tl.q_len) - sp.block(is) * tb) * p.group) : 128;
         if (!__all_sync(0xffffffffu, cbwait(s_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
         tc_fence_after();
         float pr[64];
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(512, 1)
           for (int e = 0; e < 32; ++e) uv[e] = uk[e] = 0u;
         }
         if (key_ok) {
-          const int64_t row = sq.kv_offset + key, col = (int64_t)tl.head * D + dc0 + 32 * c;
+          const int64_t row = (int64_t)tl.kv_row + key, col = (int64_t)tl.head * D + dc0 + 32 * c;
           uint4* dv4 = reinterpret_cast<uint4*>(p.dv + row * p.dv_stride + col);
           uint4* dk4 = reinterpret_cast<uint4*>(p.dk + row * p.dk_stride + col);
           auto f = [](uint32_t x) { return __uint_as_float(x); };

@@ -73,6 +73,12 @@ __device__ __forceinline__ bool cwait(uint64_t* bar, uint32_t parity, volatile i
   }
 }
 
+// Brings the next tile's record into L1 while this one is computed.
+__device__ __forceinline__ void touch(const CausalTile* t) {
+  uint32_t x;
+  asm volatile("ld.global.ca.u32 %0, [%1];" : "=r"(x) : "l"(t));
+}
+
 // What a tile's two sub-tiles cover.
 struct FwdSpan {
   int tok[2];   // first token of the sub-tile within its sequence
@@ -80,13 +86,13 @@ struct FwdSpan {
   int n[2];     // key blocks that some row of it sees, from the tile's first block on
   int nmax;
 };
-__device__ __forceinline__ FwdSpan span_of(const CausalTile& t, int q_len, int kv_len, int tb) {
+__device__ __forceinline__ FwdSpan span_of(const CausalTile& t, int tb) {
   FwdSpan s;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     s.tok[w] = (t.block + w) * tb;
-    s.toks[w] = max(0, min(tb, q_len - s.tok[w]));
-    const int seen = max(0, kv_len - q_len + s.tok[w] + s.toks[w]);  // keys the last of its tokens sees
+    s.toks[w] = max(0, min(tb, t.q_len - s.tok[w]));
+    const int seen = max(0, t.kv_len - t.q_len + s.tok[w] + s.toks[w]);  // keys the last of its tokens sees
     s.n[w] = s.toks[w] > 0 ? max(0, min((seen + 127) >> 7, t.kv_hi) - t.kv_lo) : 0;
   }
   s.nmax = max(s.n[0], s.n[1]);
@@ -99,6 +105,20 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, uint64_t
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
       : "memory");
+}
+
+// 32 bytes of one thread: in one store where the tensor's base allows it (a row's thread then fills whole 32-byte
+// sectors; two 16-byte stores each send half of one).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    uint4* q = static_cast<uint4*>(p);
+    q[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    q[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 template <int D>
@@ -170,8 +190,7 @@ __global__ void __launch_bounds__(320, 1)
       bool ok = true;
       for (int t = t_begin; t < t_end && ok; ++t) {
         const CausalTile tl = p.tiles[t];
-        const CausalSeq sq = p.seqs[tl.seq];
-        const FwdSpan sp = span_of(tl, sq.q_len, sq.kv_len, tb);
+        const FwdSpan sp = span_of(tl, tb);
         if (sp.nmax == 0) continue;
         if (!cwait(q_empty, (q_it & 1) ^ 1, abort_flag, lim, p.status)) break;
         ++q_it;
@@ -180,10 +199,10 @@ __global__ void __launch_bounds__(320, 1)
           mbar_arrive_expect_tx(q_full + w, q_bytes);
           for (int c = 0; c < D / 64; ++c)
             tma_load_4d(sQ + w * L::kTile + c * L::kBox, &tm_q, q_full + w, 64 * c, 0, tl.head,
-                        (int)(sq.q_offset + sp.tok[w]));
+                        tl.q_row + sp.tok[w]);
           ++q_loads[w];
         }
-        const int kv0 = (int)(sq.kv_offset + (int64_t)tl.kv_lo * 128);
+        const int kv0 = tl.kv_row + tl.kv_lo * 128;
         for (int j = 0; j < sp.nmax; ++j) {
           const uint32_t s = kv_it % S, ph = (kv_it / S) & 1;
           if (!cwait(k_empty + s, ph ^ 1, abort_flag, lim, p.status)) { ok = false; break; }
@@ -254,8 +273,7 @@ __global__ void __launch_bounds__(320, 1)
     };
     for (int t = t_begin; t < t_end && ok; ++t) {
       const CausalTile tl = p.tiles[t];
-      const CausalSeq sq = p.seqs[tl.seq];
-      const FwdSpan sp = span_of(tl, sq.q_len, sq.kv_len, tb);
+      const FwdSpan sp = span_of(tl, tb);
       if (sp.nmax == 0) continue;
       uint32_t ps = 0, pph = 0;
       for (int j = 0; j <= sp.nmax; ++j) {
@@ -265,7 +283,7 @@ __global__ void __launch_bounds__(320, 1)
         if (j > 0) {
           if (!wait_w(v_full + ps, pph)) { ok = false; break; }
           // value rows past the sequence's keys are other tokens: their weights are zero, but 0 x NaN is not
-          const int vrows = sq.kv_len - (tl.kv_lo + j - 1) * 128;
+          const int vrows = tl.kv_len - (tl.kv_lo + j - 1) * 128;
           if (vrows < 128) {
             zero_tile_rows<D>(aV + ps * L::kTile, vrows, lane);
             fence_proxy_async_smem();
@@ -308,15 +326,15 @@ __global__ void __launch_bounds__(320, 1)
     uint32_t sc = 0, tiles_done = 0;
     for (int t = t_begin; t < t_end; ++t) {
       const CausalTile tl = p.tiles[t];
-      const CausalSeq sq = p.seqs[tl.seq];
-      const FwdSpan sp = span_of(tl, sq.q_len, sq.kv_len, tb);
+      if (t + 1 < t_end && lane == 0) touch(p.tiles + t + 1);
+      const FwdSpan sp = span_of(tl, tb);
       const int toks = w ? sp.toks[1] : sp.toks[0], n = w ? sp.n[1] : sp.n[0];
       if (toks == 0) continue;
       const int tok = (w ? sp.tok[1] : sp.tok[0]) + rt;
       const bool row_ok = rt < toks;
       // keys this row sees, from the tile's first block on; rows that are not stored need no mask
       const int seen =
-          row_ok ? max(0, sq.kv_len - sq.q_len + tok + 1) - tl.kv_lo * 128 : 0x7fffffff;
+          row_ok ? max(0, tl.kv_len - tl.q_len + tok + 1) - tl.kv_lo * 128 : 0x7fffffff;
 
       float m_used = kNegInf, l = 0.f;
       bool ok = true;
@@ -398,8 +416,9 @@ __global__ void __launch_bounds__(320, 1)
       // sum stays NaN.
       const float inv_l = l == 0.f ? 0.f : __frcp_rn(l);
       const float lse_v = l == 0.f ? kNegInf : (m_used + lg2(l)) * kLn2;
-      const int64_t row = (sq.q_offset + tok) * p.n_q_heads + (int64_t)tl.head * p.group + rh;
+      const int64_t row = ((int64_t)tl.q_row + tok) * p.n_q_heads + (int64_t)tl.head * p.group + rh;
       const int64_t prow = (int64_t)tl.part * 256 + 128 * w + r;
+      const bool wide = ((tl.part < 0 ? reinterpret_cast<uintptr_t>(p.o) : reinterpret_cast<uintptr_t>(p.part_o)) & 31) == 0;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t u[32];
@@ -418,22 +437,24 @@ __global__ void __launch_bounds__(320, 1)
         }
         if (row_ok) {
           if (tl.part < 0) {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + 32 * c);
+            __nv_bfloat16* dst = p.o + row * D + 32 * c;
 #pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4) {
-              uint4 q4;
-              q4.x = pack_bf16(__uint_as_float(u[8 * v4 + 0]) * inv_l, __uint_as_float(u[8 * v4 + 1]) * inv_l);
-              q4.y = pack_bf16(__uint_as_float(u[8 * v4 + 2]) * inv_l, __uint_as_float(u[8 * v4 + 3]) * inv_l);
-              q4.z = pack_bf16(__uint_as_float(u[8 * v4 + 4]) * inv_l, __uint_as_float(u[8 * v4 + 5]) * inv_l);
-              q4.w = pack_bf16(__uint_as_float(u[8 * v4 + 6]) * inv_l, __uint_as_float(u[8 * v4 + 7]) * inv_l);
-              dst[v4] = q4;
+            for (int i = 0; i < 2; ++i) {
+              uint32_t v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[e] = pack_bf16(__uint_as_float(u[16 * i + 2 * e]) * inv_l, __uint_as_float(u[16 * i + 2 * e + 1]) * inv_l);
+              store32(dst + 16 * i, v, wide);
             }
           } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
+            float* dst = p.part_o + prow * D + 32 * c;
 #pragma unroll
-            for (int v4 = 0; v4 < 8; ++v4)
-              dst[v4] = make_float4(__uint_as_float(u[4 * v4 + 0]) * inv_l, __uint_as_float(u[4 * v4 + 1]) * inv_l,
-                                    __uint_as_float(u[4 * v4 + 2]) * inv_l, __uint_as_float(u[4 * v4 + 3]) * inv_l);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(u[8 * i + e]) * inv_l);
+              store32(dst + 8 * i, v, wide);
+            }
           }
         }
       }

@@ -19,9 +19,12 @@ namespace {
 constexpr double kStep1 = 1.0, kStep2 = 1.2, kTileFixed = 1.5, kPartFixed = 1.0;
 // Backward: a query block of a key tile is the unit; a tile's start and end (K, V load, dK, dV output).
 constexpr double kBwdTileFixed = 2.0;
-// Key and value bytes above which tiles of one head are kept together in time, so that what they share stays
-// in L2 (129 MB); below it the longest tiles of all heads go first, which balances better.
+// Longest tiles first balances best, but it spreads the blocks over every (sequence, head), and the tiles of one share
+// what they read: keys and values forward; queries, dO and the dQ accumulator backward.  Where that does not stay in
+// L2 (129 MB) and there are more (sequence, head) pairs than a handful of blocks each can share, the
+// pairs are taken one after the other, longest tile first within each.
 constexpr double kL2Bytes = 60e6;
+constexpr int64_t kFewPairs = 16;
 
 size_t align_up256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -134,18 +137,21 @@ void build_forward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool r
       }
     }
   }
+  auto tile = [&](const Unsplit& u, int32_t lo, int32_t hi, int32_t part) {
+    const CausalSeq& s = p->seqs[u.seq];
+    return CausalTile{(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, u.head, u.block, lo, hi, part, u.seq, {0, 0}};
+  };
   std::vector<double> cost;
   costs(chunk, &cost);
   for (const Unsplit& u : all) {
     const int k = parts_of(u, chunk);
     if (k == 1) {
-      p->fwd_tiles.push_back({u.seq, u.head, u.block, 0, u.n, -1});
+      p->fwd_tiles.push_back(tile(u, 0, u.n, -1));
       continue;
     }
     p->merges.push_back({u.seq, u.head, u.block, p->slots, k, {0, 0, 0}});
     for (int c = 0; c < k; ++c)
-      p->fwd_tiles.push_back({u.seq, u.head, u.block, (int32_t)((int64_t)u.n * c / k), (int32_t)((int64_t)u.n * (c + 1) / k),
-                              p->slots++});
+      p->fwd_tiles.push_back(tile(u, (int32_t)((int64_t)u.n * c / k), (int32_t)((int64_t)u.n * (c + 1) / k), p->slots++));
   }
   schedule(&p->fwd_tiles, cost, resident, p->num_sms, &p->fwd_ptr);
 }
@@ -160,7 +166,8 @@ void build_backward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool 
     for (int32_t h = 0; h < p->n_kv_heads; ++h)
       for (int b = 0; b < nkb; ++b) {
         const int64_t t0 = std::max<int64_t>(0, (int64_t)b * 128 - ((int64_t)s.kv_len - s.q_len));
-        p->bwd_tiles.push_back({i, h, b, 0});
+        p->bwd_tiles.push_back({(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, h, b,
+                                (int32_t)(s.acc_block + (int64_t)h * nqb), i});
         cost.push_back(kBwdTileFixed + (nqb - std::min<int64_t>(nqb, t0 / tb)));
       }
   }
@@ -241,16 +248,18 @@ zl_status build(const zl_causal_seq* seqs, int32_t n_seqs, uint32_t flags, zl_ca
     kv_tiles += ((int64_t)s.kv_len + 127) / 128 * p->n_kv_heads;
     kv_sum += s.kv_len;
   }
-  if (p->q_tokens > kMostRows || p->kv_tokens > kMostRows || q_tiles > (1 << 28) || kv_tiles > (1 << 28))
+  if (p->q_tokens > kMostRows || p->kv_tokens > kMostRows || q_tiles > (1 << 28) || kv_tiles > (1 << 28) ||
+      p->acc_blocks > INT32_MAX)
     return ZL_ERR_UNSUPPORTED;
   if (overlap(q_rows)) return ZL_ERR_INVALID_ARG;  // two sequences would write the same output rows
   p->shared_keys = overlap(kv_rows);
   std::vector<int32_t> by_len(n_seqs);
   for (int32_t i = 0; i < n_seqs; ++i) by_len[i] = i;
   std::stable_sort(by_len.begin(), by_len.end(), [&](int32_t a, int32_t b) { return seqs[a].kv_len > seqs[b].kv_len; });
-  const bool resident = 4.0 * kv_sum * p->n_kv_heads * p->head_dim <= kL2Bytes;
-  build_forward(p, by_len, resident);
-  build_backward(p, by_len, resident);
+  const bool few = (int64_t)n_seqs * p->n_kv_heads <= kFewPairs;
+  build_forward(p, by_len, few || 4.0 * kv_sum * p->n_kv_heads * p->head_dim <= kL2Bytes);
+  // of one row: q and dO in bf16, its accumulator in fp32
+  build_backward(p, by_len, few || p->acc_blocks * 128 * 8.0 * p->head_dim <= kL2Bytes);
   const int64_t D = p->head_dim;
   p->fwd_bytes = (int64_t)p->slots * 256 * (D + 1) * 4;
   p->bwd_bytes = (int64_t)align_up256((size_t)(p->q_tokens * p->n_q_heads * 4)) + p->acc_blocks * 128 * D * 4;
