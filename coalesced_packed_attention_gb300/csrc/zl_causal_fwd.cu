@@ -24,8 +24,8 @@
 //
 // Rounding: S, the running maximum and sum, O and LSE are fp32.  P is rounded to bf16 because it is an operand of
 // the PV product (relative 2^-9 a weight, independent from key to key); its sum is taken before the rounding.
-// Roles (320 threads, one CTA per SM): warps 0-3 and 4-7 the two softmax warpgroups (thread = TMEM lane = row),
-// warp 8 TMA, warp 9 MMA.  TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+d), O1 [384,384+d).
+// Roles (384 threads, one CTA per SM): warps 0-3 and 4-7 the two softmax warpgroups (thread = TMEM lane = row),
+// warp 8 TMA, warp 9 MMA, 10 and 11 idle.  TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+d), O1 [384,384+d).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -45,7 +45,8 @@ struct CausalFwdLayout {
   static constexpr int kQ = 0;               // Q0, Q1
   static constexpr int kK = kQ + 2 * kTile;
   static constexpr int kV = kK + kStages * kTile;
-  static constexpr int kBar = kV + kStages * kTile;
+  static constexpr int kOut = kV + kStages * kTile;  // 4 KB for each softmax warp: 32 rows x 64 channels of O
+  static constexpr int kBar = kOut + 8 * 4096;
   static constexpr int kNumBars = 2 + 1 + 4 * kStages + 2 + 2 + 2 + 1;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 32;
@@ -107,22 +108,15 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, uint64_t
       : "memory");
 }
 
-// 32 bytes of one thread: in one store where the tensor's base allows it (a row's thread then fills whole 32-byte
-// sectors; two 16-byte stores each send half of one).
-__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-  } else {
-    uint4* q = static_cast<uint4*>(p);
-    q[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    q[1] = make_uint4(v[4], v[5], v[6], v[7]);
-  }
-}
+// Launched with 168 registers a thread (three warps to a sub-partition); the softmax warpgroups, which hold a
+// row's 128 scores, take 216 and leave 72 to the warps that issue: per sub-partition 2 x 216 + 72 = 3 x 168, the launch
+// allocation.
+constexpr int kFwdThreads = 384;
+constexpr uint32_t kFwdLaunchRegs = 168, kFwdSoftmaxRegs = 216, kFwdIssueRegs = 72;
+static_assert(2 * kFwdSoftmaxRegs + kFwdIssueRegs == 3 * kFwdLaunchRegs, "register split must equal the launch allocation");
 
 template <int D>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(kFwdThreads, 1)
     zl_causal_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const CausalFwdParams p) {
   using L = CausalFwdLayout<D>;
@@ -182,7 +176,9 @@ __global__ void __launch_bounds__(320, 1)
   const int tb = tokens_per_block(p.group);
   const int t_begin = p.tile_ptr[blockIdx.x], t_end = p.tile_ptr[blockIdx.x + 1];
 
-  if (warp == 8) {
+  if (warp >= 8) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFwdIssueRegs));
+   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       const uint32_t q_bytes = (uint32_t)(D / 64) * (uint32_t)(tb * p.group) * 128u;
@@ -237,7 +233,7 @@ __global__ void __launch_bounds__(320, 1)
         }
       }
     }
-  } else if (warp == 9) {
+   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop (control flow, waits and descriptors are warp-uniform); one elected lane
     // executes each product and commit.
@@ -314,8 +310,10 @@ __global__ void __launch_bounds__(320, 1)
     }
     mma_commit_w(drain);
     wait_w(drain, 0);
+   }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFwdSoftmaxRegs));
     const int w = warp >> 2;          // sub-tile of this warpgroup
     const int r = threadIdx.x & 127;  // row of the sub-tile == TMEM lane
     const int rt = r / p.group, rh = r - rt * p.group;  // its token and head
@@ -418,43 +416,67 @@ __global__ void __launch_bounds__(320, 1)
       const float lse_v = l == 0.f ? kNegInf : (m_used + lg2(l)) * kLn2;
       const int64_t row = ((int64_t)tl.q_row + tok) * p.n_q_heads + (int64_t)tl.head * p.group + rh;
       const int64_t prow = (int64_t)tl.part * 256 + 128 * w + r;
-      const bool wide = ((tl.part < 0 ? reinterpret_cast<uintptr_t>(p.o) : reinterpret_cast<uintptr_t>(p.part_o)) & 31) == 0;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t u[32];
+      auto load_o = [&](int c, uint32_t (&u)[32]) {  // 32 channels of O / l
         if (n > 0) {
           tmem_ld32(tO + 32 * c, u);
           tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) u[e] = 0u;
         }
         // a row without a key beside rows with some: its weights were all zero, and 0 x Inf or NaN of a value
         // that it does not see must not show
-        if (l == 0.f) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) u[e] = 0u;
-        }
-        if (row_ok) {
-          if (tl.part < 0) {
-            __nv_bfloat16* dst = p.o + row * D + 32 * c;
+        for (int e = 0; e < 32; ++e) u[e] = n > 0 && l != 0.f ? __float_as_uint(__uint_as_float(u[e]) * inv_l) : 0u;
+      };
+      if (tl.part < 0) {
+        // 64 channels of the warp's 32 rows through shared memory (16-byte pieces, swizzled by row), so that a store
+        // writes four rows' whole 128 bytes: a store per row and thread kept the load/store unit busy for 2900 cycles
+        // a tile
+        // (the lane is read again here: addresses formed from the one above would be kept in registers through
+        // the loop over key blocks, which has none to spare)
+        int ln;
+        asm volatile("mov.u32 %0, %%laneid;" : "=r"(ln));
+        const uint32_t buf = smem_u32(smem + L::kOut) + warp * 4096;
+        const int rel = row_ok ? rt * p.n_q_heads + rh : -1;
+        __nv_bfloat16* base = p.o + (((int64_t)tl.q_row + tok - rt) * p.n_q_heads + (int64_t)tl.head * p.group) * D + (ln & 7) * 8;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t v[8];
+        for (int half = 0; half < D / 64; ++half) {
+          if (half > 0) __syncwarp();  // the first half has been read
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                v[e] = pack_bf16(__uint_as_float(u[16 * i + 2 * e]) * inv_l, __uint_as_float(u[16 * i + 2 * e + 1]) * inv_l);
-              store32(dst + 16 * i, v, wide);
-            }
-          } else {
-            float* dst = p.part_o + prow * D + 32 * c;
+          for (int c = 0; c < 2; ++c) {
+            uint32_t u[32];
+            load_o(2 * half + c, u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t v[8];
+              uint32_t v[4];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(u[8 * i + e]) * inv_l);
-              store32(dst + 8 * i, v, wide);
+              for (int e = 0; e < 4; ++e) v[e] = pack_bf16(__uint_as_float(u[8 * i + 2 * e]), __uint_as_float(u[8 * i + 2 * e + 1]));
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + ln * 128 + (((4 * c + i) ^ (ln & 7)) << 4)),
+                           "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                           : "memory");
             }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int lr = 4 * i + (ln >> 3);  // lane's row of the warp
+            const int to = __shfl_sync(0xffffffffu, rel, lr);
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(buf + lr * 128 + (((ln & 7) ^ (lr & 7)) << 4))
+                         : "memory");
+            if (to >= 0) *reinterpret_cast<uint4*>(base + (int64_t)to * D + 64 * half) = v;
+          }
+        }
+        __syncwarp();  // the next tile's rows overwrite the buffer
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t u[32];
+          load_o(c, u);
+          if (row_ok) {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
           }
         }
       }
@@ -521,10 +543,17 @@ cudaError_t launch_causal_fwd_impl(const CUtensorMap& tq, const CUtensorMap& tk,
   using L = CausalFwdLayout<D>;
   const int smem = L::kAlloc > 120 * 1024 ? L::kAlloc : 120 * 1024;  // one CTA per SM (TMEM 512 columns)
   static PerDeviceOnce configured;
-  cudaError_t e = configured.run(
-      [&] { return cudaFuncSetAttribute(zl_causal_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  cudaError_t e = configured.run([&] {
+    cudaError_t r = cudaFuncSetAttribute(zl_causal_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (r != cudaSuccess) return r;
+    // a kernel built with another register count would leave an increase waiting for registers forever
+    cudaFuncAttributes fa;
+    r = cudaFuncGetAttributes(&fa, zl_causal_fwd_kernel<D>);
+    if (r != cudaSuccess) return r;
+    return fa.numRegs == (int)kFwdLaunchRegs ? cudaSuccess : cudaErrorInvalidKernelImage;
+  });
   if (e != cudaSuccess) return e;
-  zl_causal_fwd_kernel<D><<<grid, 320, smem, stream>>>(tq, tk, tv, p);
+  zl_causal_fwd_kernel<D><<<grid, kFwdThreads, smem, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
 
