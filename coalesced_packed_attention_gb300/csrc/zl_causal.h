@@ -58,16 +58,23 @@ struct alignas(16) CausalTile {
   int32_t part;                          // -1: final output; else the tile's slot of partial results
   int32_t seq, pad[2];
 };
-// One backward tile: 128 keys of one (sequence, key head).
+// One backward tile: 128 keys of one (sequence, key head) over query blocks [first, first + n), all that see one of
+// the keys or a part of them.
 struct alignas(16) CausalBwdTile {
   int32_t q_row, q_len, kv_row, kv_len;
   int32_t head, block;
   int32_t acc_block;  // the head's first block in the dQ accumulator
-  int32_t seq;
+  int32_t first, n;
+  int32_t part;       // -1: final output; else the tile's slot of partial dK, dV
+  int32_t seq, pad;
 };
 // Rows whose key range was split: the combine of `parts` slots from `slot` on.
 struct CausalMerge {
   int32_t seq, head, block, slot, parts, pad[3];
+};
+// Key tiles whose query range was split: the sum of `parts` slots of dK, dV from `slot` on.
+struct CausalBwdMerge {
+  int32_t kv_row, kv_len, head, block, slot, parts, pad[2];
 };
 
 struct CausalFwdParams {
@@ -104,10 +111,26 @@ struct CausalBwdParams {
   const float* lse;
   const float* row_d;  // D, [q tokens][q heads]
   float* acc;          // fp32 dQ accumulator, [block][d / 4][128][4]
+  float* part;         // [slot][dV, dK][128][d], fp32, dK not yet scaled
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
   int64_t dk_stride, dv_stride;
   float scale, scale_log2;
+};
+
+// The last launch of the backward: dQ from its accumulator, and the sums of split key tiles.
+struct CausalFinishParams {
+  const CausalSeq* seqs;
+  const CausalBwdMerge* merges;
+  int32_t n_seqs, n_merges, n_q_heads, n_kv_heads;
+  int64_t acc_blocks;
+  const float* acc;
+  const float* part;
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  int64_t dq_stride, dk_stride, dv_stride;
+  float scale;
 };
 
 cudaError_t launch_causal_fwd(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -118,9 +141,7 @@ cudaError_t launch_causal_bwd_pre(int head_dim, const __nv_bfloat16* o, const __
                                   int64_t rows, float* acc, int64_t acc_floats, int num_sms, cudaStream_t stream);
 cudaError_t launch_causal_bwd(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& tdo, const CausalBwdParams& p, int grid, cudaStream_t stream);
-cudaError_t launch_causal_dq(int head_dim, const CausalSeq* seqs, int32_t n_seqs, int32_t n_q_heads,
-                             int32_t n_kv_heads, int64_t acc_blocks, const float* acc, __nv_bfloat16* dq,
-                             int64_t dq_stride, float scale, int num_sms, cudaStream_t stream);
+cudaError_t launch_causal_finish(int head_dim, const CausalFinishParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace zl
 
@@ -137,7 +158,8 @@ struct zl_causal_plan {
   std::vector<zl::CausalBwdTile> bwd_tiles;
   std::vector<int32_t> bwd_ptr;
   std::vector<zl::CausalMerge> merges;
-  int32_t slots = 0;
+  std::vector<zl::CausalBwdMerge> bwd_merges;
+  int32_t slots = 0, bwd_slots = 0;
   int64_t acc_blocks = 0;
   int64_t fwd_bytes = 0, bwd_bytes = 0;
 
@@ -148,5 +170,6 @@ struct zl_causal_plan {
   zl::CausalBwdTile* d_bwd_tiles = nullptr;
   int32_t* d_bwd_ptr = nullptr;
   zl::CausalMerge* d_merges = nullptr;
+  zl::CausalBwdMerge* d_bwd_merges = nullptr;
   int32_t* d_status = nullptr;
 };

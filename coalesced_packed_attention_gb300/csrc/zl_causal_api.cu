@@ -152,6 +152,7 @@ extern "C" zl_status zl_causal_attn_bwd(const zl_causal_plan* p, const void* q, 
   float* row_d = static_cast<float*>(workspace);
   const int64_t rows = p->q_tokens * p->n_q_heads;
   float* acc = row_d + (rows * 4 + 255) / 256 * 64;
+  float* part = acc + p->acc_blocks * 128 * d;
   if (rows > 0 && launch_causal_bwd_pre(d, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), row_d,
                                         rows, acc, p->acc_blocks * 128 * d, p->num_sms, st) != cudaSuccess)
     return ZL_ERR_CUDA;
@@ -175,6 +176,7 @@ extern "C" zl_status zl_causal_attn_bwd(const zl_causal_plan* p, const void* q, 
     bp.lse = lse;
     bp.row_d = row_d;
     bp.acc = acc;
+    bp.part = part;
     bp.dk = static_cast<__nv_bfloat16*>(dk);
     bp.dv = static_cast<__nv_bfloat16*>(dv);
     bp.dk_stride = dk_stride;
@@ -183,10 +185,24 @@ extern "C" zl_status zl_causal_attn_bwd(const zl_causal_plan* p, const void* q, 
     bp.scale_log2 = scale * 1.44269504088896340736f;
     if (launch_causal_bwd(d, tq, tk, tv, tdo, bp, (int)p->bwd_ptr.size() - 1, st) != cudaSuccess) return ZL_ERR_CUDA;
   }
-  return launch_causal_dq(d, p->d_seqs, (int32_t)p->seqs.size(), p->n_q_heads, p->n_kv_heads, p->acc_blocks, acc,
-                          static_cast<__nv_bfloat16*>(dq), dq_stride, scale, p->num_sms, st) == cudaSuccess
-             ? ZL_OK
-             : ZL_ERR_CUDA;
+  CausalFinishParams fp;
+  fp.seqs = p->d_seqs;
+  fp.merges = p->d_bwd_merges;
+  fp.n_seqs = (int32_t)p->seqs.size();
+  fp.n_merges = (int32_t)p->bwd_merges.size();
+  fp.n_q_heads = p->n_q_heads;
+  fp.n_kv_heads = p->n_kv_heads;
+  fp.acc_blocks = p->acc_blocks;
+  fp.acc = acc;
+  fp.part = part;
+  fp.dq = static_cast<__nv_bfloat16*>(dq);
+  fp.dk = static_cast<__nv_bfloat16*>(dk);
+  fp.dv = static_cast<__nv_bfloat16*>(dv);
+  fp.dq_stride = dq_stride;
+  fp.dk_stride = dk_stride;
+  fp.dv_stride = dv_stride;
+  fp.scale = scale;
+  return launch_causal_finish(d, fp, p->num_sms, st) == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
 
 extern "C" zl_status zl_causal_get_device_status(const zl_causal_plan* p, void* stream, int32_t* device_status) {

@@ -7,8 +7,9 @@
 //
 // Query rows are packed as in the forward (row r = token r / group, head r % group), so the group's sum is the
 // product's own sum over rows: a tile is 128 keys of one key head and keeps K, V in shared memory and dK, dV in
-// TMEM while it walks the query blocks from the first that sees one of its keys to the sequence's last.  Every
-// dK, dV element is formed by one CTA in a fixed order.  Per block:
+// TMEM while it walks the query blocks from the first that sees one of its keys to the sequence's last.  Where the
+// tiles of a small problem do not fill the SMs evenly the planner splits such a walk; the parts' dK, dV go to the
+// workspace in fp32 and the last kernel adds them.  Every dK, dV element is summed in a fixed order.  Per block:
 //   S^T  = K Q_i^T      (SMEM x SMEM -> TMEM R0)   lanes = keys, columns = query rows
 //   dP^T = V dO_i^T     (SMEM x SMEM -> TMEM R1)
 //   softmax warpgroups (thread = key; each takes 64 columns): P^T (bf16) to TMEM over S^T, dS^T (bf16) to
@@ -30,6 +31,9 @@
 // Roles and budget: warps 0-7 softmax (two warpgroups), 8-11 dQ drain, 12 TMA, 13 MMA, 14-15 idle; launched with
 // 128 registers a thread, traded with setmaxnreg to 136 / 152 / 88, per sub-partition 2 x 136 + 152 + 88 = 4 x 128,
 // exactly the launch allocation.  TMEM (512 columns): R0 [0,128), R1 [128,256), dV [256,256+d), dK [384,384+d).
+// (d = 64 has room for dQ columns of its own and a second stage of dS^T and dO, so that dP^T of the next block need
+// not wait for the drain; built and measured, it was slower: 133.5 against 129.9 us for the step of 4109 tokens, 24/8
+// heads.  There the softmax warpgroups, not the products, fill a block's period.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -47,14 +51,18 @@ struct CausalBwdLayout {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kK = 0;
   static constexpr int kV = kK + kTile;
-  static constexpr int kQ = kV + kTile;             // 2 stages
-  static constexpr int kDO = kQ + 2 * kTile;        // 1 stage (free once dV has read it)
-  static constexpr int kDS = kDO + kTile;           // [128 keys][128 rows] bf16, two 128-byte-swizzled boxes
-  static constexpr int kStageBytes = 128 * 32 * 4;  // one 32-column chunk of a block's dQ, fp32
-  static constexpr int kStage = kDS + 2 * kBox;     // 2 staging buffers of the dQ drain
+  // d = 128 fills the shared memory with two stages of Q and one of dO; at d = 64 there is room to load further ahead
+  // (with two and one the products waited for Q and dO 500 of a block's 3500 cycles)
+  static constexpr int kQStages = D == 64 ? 4 : 2;
+  static constexpr int kDOStages = D == 64 ? 3 : 1;
+  static constexpr int kQ = kV + kTile;
+  static constexpr int kDO = kQ + kQStages * kTile;    // a stage is free once dV has read it
+  static constexpr int kDS = kDO + kDOStages * kTile;  // [128 keys][128 rows] bf16, two 128-byte-swizzled boxes
+  static constexpr int kStageBytes = 128 * 32 * 4;    // one 32-column chunk of a block's dQ, fp32
+  static constexpr int kStage = kDS + 2 * kBox;  // 2 staging buffers of the dQ drain
   static constexpr int kLD = kStage + 2 * kStageBytes;  // [2 block parities] -LSE*log2(e) and -D of a block's rows
   static constexpr int kBar = kLD + 2 * 2 * 128 * 4;
-  static constexpr int kNumBars = 21;
+  static constexpr int kNumBars = 17 + 2 * kQStages + 2 * kDOStages;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 32;
 };
@@ -131,13 +139,12 @@ struct BwdSpan {
     return first + (b < 0 ? b + n : b);
   }
 };
-__device__ __forceinline__ BwdSpan walk_of(int block, int q_len, int kv_len, int tb) {
+__device__ __forceinline__ BwdSpan walk_of(const CausalBwdTile& t, int tb) {
   BwdSpan s;
-  s.nqb = (q_len + tb - 1) / tb;
-  const int t0 = max(0, block * 128 - (kv_len - q_len));  // first token that sees the tile's first key
-  s.first = min(s.nqb, t0 / tb);
-  s.n = s.nqb - s.first;
-  s.start = s.n > 0 ? s.n - 1 - block % s.n : 0;
+  s.nqb = (t.q_len + tb - 1) / tb;
+  s.first = t.first;
+  s.n = t.n;
+  s.start = s.n > 0 ? s.n - 1 - t.block % s.n : 0;
   return s;
 }
 
@@ -151,21 +158,26 @@ __global__ void __launch_bounds__(512, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t* kv_full = bar + 0;
   uint64_t* kv_empty = bar + 1;
-  uint64_t* q_full = bar + 2;   // [2]
-  uint64_t* q_empty = bar + 4;  // [2]
-  uint64_t* do_full = bar + 6;
-  uint64_t* do_empty = bar + 7;     // dV (the last reader of dO) complete
-  uint64_t* s_full = bar + 8;       // S^T of the block in TMEM R0
-  uint64_t* ds_ready = bar + 9;     // dS^T in shared memory, dP^T read out of R1 (256 arrivals)
-  uint64_t* dq_full = bar + 10;
-  uint64_t* dq_empty = bar + 11;
-  uint64_t* kv_done = bar + 12;
-  uint64_t* drain = bar + 13;
-  uint64_t* ld_full = bar + 14;     // LSE / D of a query block staged in shared memory
-  uint64_t* p_ready = bar + 15;     // P^T in TMEM R0 (256 arrivals): the dV product may start
-  uint64_t* dp_full = bar + 16;     // dP^T of the block in TMEM R1
-  uint64_t* stage_full = bar + 17;  // [2] a dQ chunk written to staging buffer b (128 arrivals)
-  uint64_t* stage_free = bar + 19;  // [2] the reduce-add of buffer b has read it
+  uint64_t* s_full = bar + 2;       // S^T of the block in TMEM R0
+  uint64_t* ds_ready = bar + 3;     // dS^T in shared memory, dP^T read out of R1 (256 arrivals)
+  uint64_t* dq_full = bar + 4;
+  uint64_t* dq_empty = bar + 5;
+  uint64_t* kv_done = bar + 6;
+  uint64_t* drain = bar + 7;
+  uint64_t* ld_full = bar + 8;      // LSE / D of a query block staged in shared memory
+  uint64_t* p_ready = bar + 9;      // P^T in TMEM R0 (256 arrivals): the dV product may start
+  uint64_t* dp_full = bar + 10;     // dP^T of the block in TMEM R1
+  uint64_t* stage_full = bar + 11;  // [2] a dQ chunk written to staging buffer b (128 arrivals)
+  uint64_t* stage_free = bar + 13;  // [2] the reduce-add of buffer b has read it
+  uint64_t* q_full = bar + 15;      // [kQStages]
+  uint64_t* q_empty = q_full + L::kQStages;
+  uint64_t* do_full = q_empty + L::kQStages;  // [kDOStages]
+  uint64_t* do_empty = do_full + L::kDOStages;  // dV (the last reader of dO) complete
+  // stage and phase of the it-th query block's Q and dO
+  auto q_stage = [](uint32_t it) { return it % L::kQStages; };
+  auto q_phase = [](uint32_t it) { return (it / L::kQStages) & 1; };
+  auto do_stage = [](uint32_t it) { return it % L::kDOStages; };
+  auto do_phase = [](uint32_t it) { return (it / L::kDOStages) & 1; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);
   float* sLD = reinterpret_cast<float*>(smem + L::kLD);  // block parity b: LSE at 256 b, D at 256 b + 128
@@ -177,8 +189,8 @@ __global__ void __launch_bounds__(512, 1)
   }
   const int tb = tokens_per_block(p.group), box_rows = tb * p.group;
   // rows past the box are never loaded: zero once what lies there
-  for (int b = 0; b < 3 * (D / 64); ++b) {
-    uint8_t* box = smem + L::kQ + b * L::kBox;  // Q stage 0, Q stage 1, dO
+  for (int b = 0; b < (L::kQStages + L::kDOStages) * (D / 64); ++b) {
+    uint8_t* box = smem + L::kQ + b * L::kBox;  // the stages of Q and dO lie one behind the other
     for (int i = box_rows * 8 + threadIdx.x; i < 128 * 8; i += 512)
       reinterpret_cast<uint4*>(box)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
@@ -187,13 +199,17 @@ __global__ void __launch_bounds__(512, 1)
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 1);
-      mbar_init(q_empty + i, 1);
       mbar_init(stage_full + i, 128);
       mbar_init(stage_free + i, 1);
     }
-    mbar_init(do_full, 1);
-    mbar_init(do_empty, 1);
+    for (int i = 0; i < L::kQStages; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
+    }
+    for (int i = 0; i < L::kDOStages; ++i) {
+      mbar_init(do_full + i, 1);
+      mbar_init(do_empty + i, 1);
+    }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     mbar_init(p_ready, 256);
@@ -237,7 +253,7 @@ __global__ void __launch_bounds__(512, 1)
         bool ok = true;
         for (int t = t_begin; t < t_end && ok; ++t) {
           const CausalBwdTile tl = p.tiles[t];
-          const BwdSpan sp = walk_of(tl.block, tl.q_len, tl.kv_len, tb);
+          const BwdSpan sp = walk_of(tl, tb);
           if (sp.n == 0) continue;
           if (!cbwait(kv_empty, (kt & 1) ^ 1, abort_flag, p.wait_limit, p.status)) break;
           ++kt;
@@ -253,15 +269,17 @@ __global__ void __launch_bounds__(512, 1)
           }
           for (int is = 0; is < sp.n; ++is) {
             const int tok = tl.q_row + sp.block(is) * tb;
-            const uint32_t st = qit & 1, ph = (qit >> 1) & 1;
-            if (!cbwait(q_empty + st, ph ^ 1, abort_flag, p.wait_limit, p.status)) { ok = false; break; }
+            const uint32_t st = q_stage(qit);
+            if (!cbwait(q_empty + st, q_phase(qit) ^ 1, abort_flag, p.wait_limit, p.status)) { ok = false; break; }
             mbar_arrive_expect_tx(q_full + st, row_bytes);
             for (int c = 0; c < D / 64; ++c)
               tma_rows(sQ + st * L::kTile + c * L::kBox, &tm_q, q_full + st, 64 * c, tl.head, tok);
             ++qit;
-            if (!cbwait(do_empty, (dit & 1) ^ 1, abort_flag, p.wait_limit, p.status)) { ok = false; break; }
-            mbar_arrive_expect_tx(do_full, row_bytes);
-            for (int c = 0; c < D / 64; ++c) tma_rows(sDO + c * L::kBox, &tm_do, do_full, 64 * c, tl.head, tok);
+            const uint32_t ds = do_stage(dit);
+            if (!cbwait(do_empty + ds, do_phase(dit) ^ 1, abort_flag, p.wait_limit, p.status)) { ok = false; break; }
+            mbar_arrive_expect_tx(do_full + ds, row_bytes);
+            for (int c = 0; c < D / 64; ++c)
+              tma_rows(sDO + ds * L::kTile + c * L::kBox, &tm_do, do_full + ds, 64 * c, tl.head, tok);
             ++dit;
           }
         }
@@ -273,9 +291,10 @@ __global__ void __launch_bounds__(512, 1)
             }
           };
           if (kt) settle(kv_full, (kt - 1) & 1);
-          if (dit) settle(do_full, (dit - 1) & 1);
-          for (uint32_t b = 1; b <= 2; ++b)
-            if (qit >= b) settle(q_full + ((qit - b) & 1), ((qit - b) >> 1) & 1);
+          for (uint32_t b = 1; b <= (uint32_t)L::kDOStages; ++b)
+            if (dit >= b) settle(do_full + do_stage(dit - b), do_phase(dit - b));
+          for (uint32_t b = 1; b <= (uint32_t)L::kQStages; ++b)
+            if (qit >= b) settle(q_full + q_stage(qit - b), q_phase(qit - b));
         }
       }
     } else if (warp == 13) {
@@ -298,7 +317,7 @@ __global__ void __launch_bounds__(512, 1)
       bool ok = true;
       for (int t = t_begin; t < t_end && ok; ++t) {
         const CausalBwdTile tl = p.tiles[t];
-        const BwdSpan sp = walk_of(tl.block, tl.q_len, tl.kv_len, tb);
+        const BwdSpan sp = walk_of(tl, tb);
         if (sp.n == 0) continue;
         if (!wait_w(kv_full, kt & 1)) break;
         ++kt;
@@ -328,32 +347,32 @@ __global__ void __launch_bounds__(512, 1)
           }
           mma_commit_w(s_full);
         };
-        if (!wait_w(q_full + (qit & 1), (qit >> 1) & 1)) break;
-        fix_rows(0, aQ + (qit & 1) * L::kTile);
+        if (!wait_w(q_full + q_stage(qit), q_phase(qit))) break;
+        fix_rows(0, aQ + q_stage(qit) * L::kTile);
         tc_fence_after();
-        issue_s(qit & 1);
+        issue_s(q_stage(qit));
         for (int is = 0; is < sp.n; ++is) {
-          const uint32_t st = qit & 1;
-          if (!wait_w(do_full, qit & 1)) { ok = false; break; }
-          fix_rows(is, aDO);
+          const uint32_t st = q_stage(qit), ds = do_stage(qit);
+          if (!wait_w(do_full + ds, do_phase(qit))) { ok = false; break; }
+          fix_rows(is, aDO + ds * L::kTile);
           if (nblocks > 0 && !wait_w(dq_empty, (nblocks - 1) & 1)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {  // dP^T = V dO^T
             const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
-            mma_ss_w(tR1, dsc(kV, off), dsc(kDO, off), kIdSq, kk > 0);
+            mma_ss_w(tR1, dsc(kV, off), dsc(kDO, ds * L::kTile + off), kIdSq, kk > 0);
           }
           mma_commit_w(dp_full);
           if (!wait_w(p_ready, nblocks & 1)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // dV += P^T dO
-            mma_ts_w(tdV, tR0 + p_col(kk), dsc(mDO, kk * 2048), kIdKV, (is > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_w(do_empty);
+            mma_ts_w(tdV, tR0 + p_col(kk), dsc(mDO, ds * L::kTile + kk * 2048), kIdKV, (is > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_w(do_empty + ds);
           if (is + 1 < sp.n) {
             // S^T of the next block as soon as dV has read P^T out of R0 (products run in issue order)
-            const uint32_t st2 = (qit + 1) & 1, ph2 = ((qit + 1) >> 1) & 1;
-            if (!wait_w(q_full + st2, ph2)) { ok = false; break; }
+            const uint32_t st2 = q_stage(qit + 1);
+            if (!wait_w(q_full + st2, q_phase(qit + 1))) { ok = false; break; }
             fix_rows(is + 1, aQ + st2 * L::kTile);
             tc_fence_after();
             issue_s(st2);
@@ -367,7 +386,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {  // dK += dS^T Q
             const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
-            mma_ss_w(tdK, dsc(kDS, off), dsc(mQ, st * L::kTile + kk * 2048), kIdKV, (is > 0 || kk > 0) ? 1u : 0u);
+            mma_ss_w(tdK, dsc(kDS, off), dsc(mQ, st * L::kTile + kk * 2048), kIdKV,
+                     (is > 0 || kk > 0) ? 1u : 0u);
           }
           mma_commit_w(q_empty + st);
           ++qit;
@@ -391,7 +411,7 @@ __global__ void __launch_bounds__(512, 1)
     bool ok = true;
     for (int t = t_begin; t < t_end && ok; ++t) {
       const CausalBwdTile tl = p.tiles[t];
-      const BwdSpan sp = walk_of(tl.block, tl.q_len, tl.kv_len, tb);
+      const BwdSpan sp = walk_of(tl, tb);
       float* acc_hd = p.acc + (int64_t)tl.acc_block * (128 * D);
       for (int is = 0; is < sp.n; ++is) {
         if (!__all_sync(0xffffffffu, cbwait(dq_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
@@ -449,36 +469,34 @@ __global__ void __launch_bounds__(512, 1)
     uint32_t nblocks = 0, ntiles = 0;
     for (int t = t_begin; t < t_end; ++t) {
       const CausalBwdTile tl = p.tiles[t];
-      const BwdSpan sp = walk_of(tl.block, tl.q_len, tl.kv_len, tb);
+      const BwdSpan sp = walk_of(tl, tb);
       const int key = tl.block * 128 + t_key;
       const bool key_ok = key < tl.kv_len;
       const int64_t ld_base = (int64_t)tl.q_row * p.n_q_heads + (int64_t)tl.head * p.group + rh;
-      bool ok = true;
-      float lse_n = -kInfC, d_n = 0.f;
-      // rows past the sequence and rows that see no key (LSE = -inf) get exp2(-inf) = 0 everywhere
+      // LSE and D of the next block's row, on their way while this block is computed: nothing may look at them before
+      // they are staged
+      float lse_v = -kInfC, d_v = 0.f;
       auto fetch = [&](int blk) {
         const int tok = blk * tb + rt;
-        lse_n = -kInfC;
-        d_n = 0.f;
+        lse_v = -kInfC;
         if (rt < tb && tok < tl.q_len) {
           const int64_t i = ld_base + (int64_t)tok * p.n_q_heads;
-          const float l = __ldg(p.lse + i);
-          if (l != -kInfC) {
-            lse_n = -l * kLog2eC;
-            d_n = -__ldg(p.row_d + i);
-          }
+          lse_v = __ldg(p.lse + i);
+          d_v = __ldg(p.row_d + i);
         }
       };
+      bool ok = true;
       if (wg == 0 && sp.n > 0) fetch(sp.block(0));
       for (int is = 0; is < sp.n; ++is) {
         if (wg == 0) {
-          sLD[256 * (nblocks & 1) + t_key] = lse_n;
-          sLD[256 * (nblocks & 1) + 128 + t_key] = d_n;
+          // rows past the sequence and rows that see no key (LSE = -inf) get exp2(-inf) = 0 everywhere
+          const bool none = lse_v == -kInfC;
+          sLD[256 * (nblocks & 1) + t_key] = none ? -kInfC : -lse_v * kLog2eC;
+          sLD[256 * (nblocks & 1) + 128 + t_key] = none ? 0.f : -d_v;
         }
         mbar_arrive(ld_full);  // bounded stand-in for a barrier of both warpgroups
         if (!__all_sync(0xffffffffu, cbwait(ld_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
         if (wg == 0 && is + 1 < sp.n) fetch(sp.block(is + 1));
-
         const float* sLSE = sLD + 256 * (nblocks & 1);
         const float* sD = sLSE + 128;
         // first column (query row of the block) that sees this key; 128: none
@@ -519,7 +537,7 @@ __global__ void __launch_bounds__(512, 1)
         tc_fence_before();
         mbar_arrive(p_ready);
 
-        // dP^T of this block is issued after the previous block's dQ product, which read the dS^T buffer:
+        // dP^T of this block is issued after the previous block's dQ and dK products, which read the dS^T buffer:
         // once dP^T is complete the buffer may be rewritten
         if (!__all_sync(0xffffffffu, cbwait(dp_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
         tc_fence_after();
@@ -566,7 +584,16 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) uv[e] = uk[e] = 0u;
         }
-        if (key_ok) {
+        if (tl.part >= 0) {  // a part of the tile's queries: summed, scaled and rounded by the last launch
+          float4* pv = reinterpret_cast<float4*>(p.part + ((int64_t)tl.part * 256 + t_key) * D + dc0 + 32 * c);
+          float4* pk = pv + 128 * D / 4;
+          auto f = [](uint32_t x) { return __uint_as_float(x); };
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            pv[i] = make_float4(f(uv[4 * i]), f(uv[4 * i + 1]), f(uv[4 * i + 2]), f(uv[4 * i + 3]));
+            pk[i] = make_float4(f(uk[4 * i]), f(uk[4 * i + 1]), f(uk[4 * i + 2]), f(uk[4 * i + 3]));
+          }
+        } else if (key_ok) {
           const int64_t row = (int64_t)tl.kv_row + key, col = (int64_t)tl.head * D + dc0 + 32 * c;
           uint4* dv4 = reinterpret_cast<uint4*>(p.dv + row * p.dv_stride + col);
           uint4* dk4 = reinterpret_cast<uint4*>(p.dk + row * p.dk_stride + col);
@@ -636,29 +663,27 @@ __global__ void __launch_bounds__(256) zl_causal_pre_kernel(const __nv_bfloat16*
 }
 
 // dQ: one block per 128-row accumulator block and 64-channel half, read in storage order, turned over in shared
-// memory, scaled, rounded to bf16 and written to the rows of its tokens.
+// memory, scaled, rounded to bf16 and written to the rows of its tokens.  After those, one block per split key tile
+// and tensor: its parts are added in order, scaled (dK), rounded and written.
 template <int D>
-__global__ void __launch_bounds__(256) zl_causal_dq_kernel(const CausalSeq* __restrict__ seqs, int32_t n_seqs,
-                                                           int32_t n_q_heads, int32_t n_kv_heads, int64_t n_slabs,
-                                                           const float* __restrict__ acc,
-                                                           __nv_bfloat16* __restrict__ dq, int64_t dq_stride,
-                                                           float scale) {
+__global__ void __launch_bounds__(256) zl_causal_finish_kernel(const CausalFinishParams p) {
   constexpr int kHalves = D / 64;
   __shared__ float4 tile[128][17];
-  const int group = n_q_heads / n_kv_heads, tb = tokens_per_block(group);
+  const int group = p.n_q_heads / p.n_kv_heads, tb = tokens_per_block(group);
+  const int64_t n_slabs = p.acc_blocks * kHalves;
   for (int64_t sl = blockIdx.x; sl < n_slabs; sl += gridDim.x) {
     const int64_t blk = sl / kHalves;
     const int half = (int)(sl % kHalves);
-    int lo = 0, hi = n_seqs - 1;  // last sequence whose first block is <= blk (empty ones share their start)
+    int lo = 0, hi = p.n_seqs - 1;  // last sequence whose first block is <= blk (empty ones share their start)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (seqs[mid].acc_block <= blk) lo = mid; else hi = mid - 1;
+      if (p.seqs[mid].acc_block <= blk) lo = mid; else hi = mid - 1;
     }
-    const CausalSeq sq = seqs[lo];
+    const CausalSeq sq = p.seqs[lo];
     const int nqb = (sq.q_len + tb - 1) / tb;
     const int64_t in_seq = blk - sq.acc_block;
     const int head = (int)(in_seq / nqb), qb = (int)(in_seq % nqb);
-    const float4* src = reinterpret_cast<const float4*>(acc) + sl * (128 * 16);
+    const float4* src = reinterpret_cast<const float4*>(p.acc) + sl * (128 * 16);
     float4 x[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) x[u] = __ldg(src + u * 256 + threadIdx.x);
@@ -675,13 +700,37 @@ __global__ void __launch_bounds__(256) zl_causal_dq_kernel(const CausalSeq* __re
       const int rt = r / group, tok = qb * tb + rt;
       if (rt < tb && tok < sq.q_len) {
         const float4 v = tile[r][2 * c], w = tile[r][2 * c + 1];
-        *reinterpret_cast<uint4*>(dq + (sq.q_offset + tok) * dq_stride +
+        *reinterpret_cast<uint4*>(p.dq + (sq.q_offset + tok) * p.dq_stride +
                                   ((int64_t)head * group + (r - rt * group)) * D + half * 64 + 8 * c) =
-            make_uint4(pack_bf16(v.x * scale, v.y * scale), pack_bf16(v.z * scale, v.w * scale),
-                       pack_bf16(w.x * scale, w.y * scale), pack_bf16(w.z * scale, w.w * scale));
+            make_uint4(pack_bf16(v.x * p.scale, v.y * p.scale), pack_bf16(v.z * p.scale, v.w * p.scale),
+                       pack_bf16(w.x * p.scale, w.y * p.scale), pack_bf16(w.z * p.scale, w.w * p.scale));
       }
     }
     __syncthreads();
+  }
+  // the first item behind the slabs that is this block's
+  int64_t it = blockIdx.x;
+  if (it < n_slabs) it += (n_slabs - it + gridDim.x - 1) / gridDim.x * gridDim.x;
+  for (it -= n_slabs; it < 2 * (int64_t)p.n_merges; it += gridDim.x) {
+    const CausalBwdMerge m = p.merges[it >> 1];
+    const int of_k = (int)(it & 1);
+    const float4* src = reinterpret_cast<const float4*>(p.part) + ((int64_t)m.slot * 2 + of_k) * (128 * D / 4);
+    const float scale = of_k ? p.scale : 1.f;
+    __nv_bfloat16* out = of_k ? p.dk : p.dv;
+    const int64_t stride = of_k ? p.dk_stride : p.dv_stride;
+    for (int k = threadIdx.x; k < 128 * D / 8; k += 256) {
+      const int r = k / (D / 8), c = k % (D / 8), key = m.block * 128 + r;
+      if (key >= m.kv_len) break;  // rows ascend with k
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
+      for (int q = 0; q < m.parts; ++q) {
+        const float4 a = __ldg(src + (int64_t)q * (2 * 128 * D / 4) + 2 * k), b = __ldg(src + (int64_t)q * (2 * 128 * D / 4) + 2 * k + 1);
+        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+        w.x += b.x; w.y += b.y; w.z += b.z; w.w += b.w;
+      }
+      *reinterpret_cast<uint4*>(out + ((int64_t)m.kv_row + key) * stride + (int64_t)m.head * D + 8 * c) =
+          make_uint4(pack_bf16(v.x * scale, v.y * scale), pack_bf16(v.z * scale, v.w * scale),
+                     pack_bf16(w.x * scale, w.y * scale), pack_bf16(w.z * scale, w.w * scale));
+    }
   }
 }
 
@@ -728,15 +777,12 @@ cudaError_t launch_causal_bwd(int head_dim, const CUtensorMap& tq, const CUtenso
   return cudaGetLastError();
 }
 
-cudaError_t launch_causal_dq(int head_dim, const CausalSeq* seqs, int32_t n_seqs, int32_t n_q_heads,
-                             int32_t n_kv_heads, int64_t acc_blocks, const float* acc, __nv_bfloat16* dq,
-                             int64_t dq_stride, float scale, int num_sms, cudaStream_t stream) {
-  const int64_t slabs = acc_blocks * (head_dim / 64);
-  if (slabs == 0) return cudaSuccess;
-  auto k = head_dim == 128 ? zl_causal_dq_kernel<128> : zl_causal_dq_kernel<64>;
+cudaError_t launch_causal_finish(int head_dim, const CausalFinishParams& p, int num_sms, cudaStream_t stream) {
+  const int64_t items = p.acc_blocks * (head_dim / 64) + 2 * (int64_t)p.n_merges;
+  if (items == 0) return cudaSuccess;
+  auto k = head_dim == 128 ? zl_causal_finish_kernel<128> : zl_causal_finish_kernel<64>;
   static PerDeviceInt resident[2];
-  k<<<resident_grid(resident[head_dim == 128], k, slabs, num_sms), 256, 0, stream>>>(seqs, n_seqs, n_q_heads, n_kv_heads, slabs, acc, dq,
-                                                          dq_stride, scale);
+  k<<<resident_grid(resident[head_dim == 128], k, items, num_sms), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

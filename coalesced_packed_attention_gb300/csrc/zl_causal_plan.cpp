@@ -15,10 +15,11 @@ using namespace zl;
 namespace {
 
 // Costs of the forward schedule in units of one 128-key step of a lone sub-tile (about 1.3 us): a step of two
-// sub-tiles, a tile's start and end (Q load, first scores, epilogue), and a part's fp32 output with its share of the merge.
-constexpr double kStep1 = 1.0, kStep2 = 1.2, kTileFixed = 1.5, kPartFixed = 1.0;
-// Backward: a query block of a key tile is the unit; a tile's start and end (K, V load, dK, dV output).
-constexpr double kBwdTileFixed = 2.0;
+// sub-tiles, a tile's start and end (Q load, first scores, epilogue), a part's fp32 output, and the merge's launch.
+constexpr double kStep1 = 1.0, kStep2 = 1.2, kTileFixed = 1.5, kPartFixed = 1.0, kMergeFixed = 3.0;
+// Backward: a query block of a key tile is the unit (about 2 us); a tile's start and end (K, V load, first products, dK,
+// dV output), a part's fp32 output and its share of the sum, which the last launch does on its way.
+constexpr double kBwdTileFixed = 2.0, kBwdPartFixed = 1.0, kBwdMergeFixed = 1.0;
 // Longest tiles first balances best, but it spreads the blocks over every (sequence, head), and the tiles of one share
 // what they read: keys and values forward; queries, dO and the dQ accumulator backward.  Where that does not stay in
 // L2 (129 MB) and there are more (sequence, head) pairs than a handful of blocks each can share, the
@@ -79,97 +80,115 @@ int blocks_seen(const CausalSeq& s, int block, int tb) {
   return (int)((seen + 127) / 128);
 }
 
-struct Unsplit {
+// Pieces of a range of n units when pieces of about `chunk` are wanted (0: none).
+int pieces(int n, int chunk) { return chunk > 0 && n > chunk ? (n + chunk - 1) / chunk : 1; }
+int piece_at(int n, int k, int c) { return (int)((int64_t)n * c / k); }
+
+// The piece size that gives the shortest schedule: no split, or pieces of about an even share of the work and
+// fractions of it, at the price of `merge`.  cost_of(i, n, part) is the cost of n units of item i.
+template <typename Item, typename Cost>
+int choose_chunk(const std::vector<Item>& items, int sms, double merge, const Cost& cost_of) {
+  auto makespan_of = [&](int chunk) {
+    std::vector<double> cost;
+    for (const Item& u : items) {
+      const int k = pieces(u.n, chunk);
+      for (int c = 0; c < k; ++c) cost.push_back(cost_of(u, piece_at(u.n, k, c + 1) - piece_at(u.n, k, c), k > 1));
+    }
+    std::vector<int32_t> order(cost.size());
+    for (size_t i = 0; i < order.size(); ++i) order[i] = (int32_t)i;
+    std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return cost[a] > cost[b]; });
+    return list_schedule(cost, order, std::min<int>((int)cost.size(), sms), nullptr);
+  };
+  double total = 0.0, longest = 0.0;
+  for (const Item& u : items) {
+    const double c = cost_of(u, u.n, false);
+    total += c;
+    longest = std::max(longest, c);
+  }
+  // many tiles to a block balance by themselves
+  if (items.empty() || items.size() > 32u * sms) return 0;
+  const double share = total / sms;
+  double best = makespan_of(0);
+  if (best < 1.04 * share) return 0;
+  int chunk = 0;
+  for (double f : {1.0, 0.7, 0.5, 0.35, 0.25, 0.15}) {
+    const int c = std::max(2, (int)(share * f));
+    const double m = makespan_of(c) + merge;
+    if (m < 0.97 * best) {
+      best = m;
+      chunk = c;
+    }
+  }
+  return chunk;
+}
+
+struct FwdItem {
   int32_t seq, head, block, n;
   bool two;
 };
 
-double fwd_cost(int n, bool two, bool part) {
-  return kTileFixed + n * (two ? kStep2 : kStep1) + (part ? kPartFixed : 0.0);
-}
-
 void build_forward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool resident) {
   const int tb = tokens_per_block(p->group);
-  std::vector<Unsplit> all;
-  double total = 0.0, longest = 0.0;
+  std::vector<FwdItem> all;
   for (int32_t i : by_len) {
     const CausalSeq& s = p->seqs[i];
     const int nqb = (int)(((int64_t)s.q_len + tb - 1) / tb);
     for (int32_t h = 0; h < p->n_kv_heads; ++h)
-      for (int b = (nqb - 1) / 2 * 2; nqb > 0 && b >= 0; b -= 2) {
-        Unsplit u{i, h, b, std::max(blocks_seen(s, b, tb), blocks_seen(s, b + 1, tb)), b + 1 < nqb};
-        all.push_back(u);
-        const double c = fwd_cost(u.n, u.two, false);
-        total += c;
-        longest = std::max(longest, c);
-      }
+      for (int b = (nqb - 1) / 2 * 2; nqb > 0 && b >= 0; b -= 2)
+        all.push_back({i, h, b, std::max(blocks_seen(s, b, tb), blocks_seen(s, b + 1, tb)), b + 1 < nqb});
   }
-  // Split where a lone tile outlasts an even share of the work.  Candidates: parts of about an even share, and
-  // halves and thirds of that; the schedule with the shortest makespan wins (no split included).
-  auto parts_of = [](const Unsplit& u, int chunk) { return chunk > 0 && u.n > chunk ? (u.n + chunk - 1) / chunk : 1; };
-  auto costs = [&](int chunk, std::vector<double>* cost) {
-    cost->clear();
-    for (const Unsplit& u : all) {
-      const int k = parts_of(u, chunk);
-      for (int c = 0; c < k; ++c)
-        cost->push_back(fwd_cost((int)((int64_t)u.n * (c + 1) / k - (int64_t)u.n * c / k), u.two, k > 1));
-    }
+  auto cost_of = [](const FwdItem& u, int n, bool part) {
+    return kTileFixed + n * (u.two ? kStep2 : kStep1) + (part ? kPartFixed : 0.0);
   };
-  auto makespan_of = [&](int chunk) {
-    std::vector<double> cost;
-    costs(chunk, &cost);
-    std::vector<int32_t> order(cost.size());
-    for (size_t i = 0; i < order.size(); ++i) order[i] = (int32_t)i;
-    std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return cost[a] > cost[b]; });
-    return list_schedule(cost, order, std::min<int>((int)cost.size(), p->num_sms), nullptr);
-  };
-  int chunk = 0;
-  const double share = total / p->num_sms;
-  if (longest > 1.05 * share) {
-    double best = makespan_of(0);
-    // the merge is a launch of its own, about three steps long
-    for (double f : {1.0, 0.7, 0.5, 0.33, 0.25}) {
-      const int c = std::max(2, (int)(share * f));
-      const double m = makespan_of(c) + 3.0;
-      if (m < 0.97 * best) {
-        best = m;
-        chunk = c;
-      }
-    }
-  }
-  auto tile = [&](const Unsplit& u, int32_t lo, int32_t hi, int32_t part) {
-    const CausalSeq& s = p->seqs[u.seq];
-    return CausalTile{(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, u.head, u.block, lo, hi, part, u.seq, {0, 0}};
-  };
+  const int chunk = choose_chunk(all, p->num_sms, kMergeFixed, cost_of);
   std::vector<double> cost;
-  costs(chunk, &cost);
-  for (const Unsplit& u : all) {
-    const int k = parts_of(u, chunk);
-    if (k == 1) {
-      p->fwd_tiles.push_back(tile(u, 0, u.n, -1));
-      continue;
+  for (const FwdItem& u : all) {
+    const int k = pieces(u.n, chunk);
+    const CausalSeq& s = p->seqs[u.seq];
+    if (k > 1) p->merges.push_back({u.seq, u.head, u.block, p->slots, k, {0, 0, 0}});
+    for (int c = 0; c < k; ++c) {
+      const int lo = piece_at(u.n, k, c), hi = piece_at(u.n, k, c + 1);
+      p->fwd_tiles.push_back({(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, u.head, u.block, lo, hi,
+                              k > 1 ? p->slots++ : -1, u.seq, {0, 0}});
+      cost.push_back(cost_of(u, hi - lo, k > 1));
     }
-    p->merges.push_back({u.seq, u.head, u.block, p->slots, k, {0, 0, 0}});
-    for (int c = 0; c < k; ++c)
-      p->fwd_tiles.push_back(tile(u, (int32_t)((int64_t)u.n * c / k), (int32_t)((int64_t)u.n * (c + 1) / k), p->slots++));
   }
   schedule(&p->fwd_tiles, cost, resident, p->num_sms, &p->fwd_ptr);
 }
 
+struct BwdItem {
+  int32_t seq, head, block, first, n, nqb;
+};
+
 void build_backward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool resident) {
   const int tb = tokens_per_block(p->group);
-  std::vector<double> cost;
+  std::vector<BwdItem> all;
   for (int32_t i : by_len) {
     const CausalSeq& s = p->seqs[i];
     const int nqb = (int)(((int64_t)s.q_len + tb - 1) / tb);
     const int nkb = (int)(((int64_t)s.kv_len + 127) / 128);
     for (int32_t h = 0; h < p->n_kv_heads; ++h)
       for (int b = 0; b < nkb; ++b) {
+        // the first token that sees the tile's first key
         const int64_t t0 = std::max<int64_t>(0, (int64_t)b * 128 - ((int64_t)s.kv_len - s.q_len));
-        p->bwd_tiles.push_back({(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, h, b,
-                                (int32_t)(s.acc_block + (int64_t)h * nqb), i});
-        cost.push_back(kBwdTileFixed + (nqb - std::min<int64_t>(nqb, t0 / tb)));
+        const int first = (int)std::min<int64_t>(nqb, t0 / tb);
+        all.push_back({i, h, b, first, nqb - first, nqb});
       }
+  }
+  auto cost_of = [](const BwdItem&, int n, bool part) { return kBwdTileFixed + n + (part ? kBwdPartFixed : 0.0); };
+  const int chunk = choose_chunk(all, p->num_sms, kBwdMergeFixed, cost_of);
+  std::vector<double> cost;
+  for (const BwdItem& u : all) {
+    const int k = pieces(u.n, chunk);
+    const CausalSeq& s = p->seqs[u.seq];
+    if (k > 1) p->bwd_merges.push_back({(int32_t)s.kv_offset, s.kv_len, u.head, u.block, p->bwd_slots, k, {0, 0}});
+    for (int c = 0; c < k; ++c) {
+      const int lo = piece_at(u.n, k, c), hi = piece_at(u.n, k, c + 1);
+      p->bwd_tiles.push_back({(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, u.head, u.block,
+                              (int32_t)(s.acc_block + (int64_t)u.head * u.nqb), u.first + lo, hi - lo,
+                              k > 1 ? p->bwd_slots++ : -1, u.seq, 0});
+      cost.push_back(cost_of(u, hi - lo, k > 1));
+    }
   }
   schedule(&p->bwd_tiles, cost, resident, p->num_sms, &p->bwd_ptr);
 }
@@ -193,6 +212,7 @@ zl_status upload_causal(zl_causal_plan* p) {
   const size_t o_bt = take(sizeof(CausalBwdTile) * p->bwd_tiles.size());
   const size_t o_bp = take(sizeof(int32_t) * p->bwd_ptr.size());
   const size_t o_m = take(sizeof(CausalMerge) * p->merges.size());
+  const size_t o_bm = take(sizeof(CausalBwdMerge) * p->bwd_merges.size());
   std::vector<char> blob(at, 0);
   put(&blob, o_seqs, p->seqs);
   put(&blob, o_ft, p->fwd_tiles);
@@ -200,6 +220,7 @@ zl_status upload_causal(zl_causal_plan* p) {
   put(&blob, o_bt, p->bwd_tiles);
   put(&blob, o_bp, p->bwd_ptr);
   put(&blob, o_m, p->merges);
+  put(&blob, o_bm, p->bwd_merges);
   if (cudaMalloc(&p->dev_blob, at) != cudaSuccess) {
     p->dev_blob = nullptr;
     cudaGetLastError();
@@ -218,6 +239,7 @@ zl_status upload_causal(zl_causal_plan* p) {
   p->d_bwd_tiles = reinterpret_cast<CausalBwdTile*>(base + o_bt);
   p->d_bwd_ptr = reinterpret_cast<int32_t*>(base + o_bp);
   p->d_merges = reinterpret_cast<CausalMerge*>(base + o_m);
+  p->d_bwd_merges = reinterpret_cast<CausalBwdMerge*>(base + o_bm);
   return ZL_OK;
 }
 
@@ -262,7 +284,8 @@ zl_status build(const zl_causal_seq* seqs, int32_t n_seqs, uint32_t flags, zl_ca
   build_backward(p, by_len, few || p->acc_blocks * 128 * 8.0 * p->head_dim <= kL2Bytes);
   const int64_t D = p->head_dim;
   p->fwd_bytes = (int64_t)p->slots * 256 * (D + 1) * 4;
-  p->bwd_bytes = (int64_t)align_up256((size_t)(p->q_tokens * p->n_q_heads * 4)) + p->acc_blocks * 128 * D * 4;
+  p->bwd_bytes = (int64_t)align_up256((size_t)(p->q_tokens * p->n_q_heads * 4)) + p->acc_blocks * 128 * D * 4 +
+                 (int64_t)p->bwd_slots * 2 * 128 * D * 4;
   return p->host_only ? ZL_OK : upload_causal(p);
 }
 
@@ -350,7 +373,7 @@ extern "C" zl_status zl_causal_plan_tiles(const zl_causal_plan* p, int32_t which
         std::memcpy(o, v, sizeof(v));
       } else {
         const CausalBwdTile& t = p->bwd_tiles[i];
-        const int32_t v[7] = {t.seq, t.head, t.block, 0, 0, -1, (int32_t)b};
+        const int32_t v[7] = {t.seq, t.head, t.block, t.first, t.first + t.n, t.part, (int32_t)b};
         std::memcpy(o, v, sizeof(v));
       }
     }

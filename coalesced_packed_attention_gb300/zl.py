@@ -656,8 +656,8 @@ class CausalPlan:
         self.fwd_workspace_bytes, self.bwd_workspace_bytes = f.value, b.value
 
     def tiles(self, which: int = 0):
-        """Schedule as (sequence, key head, block, first key block, end key block, part, thread
-        block) tuples; which = 0 forward, 1 backward."""
+        """Schedule as (sequence, key head, block, first, end, part, thread block) tuples; which = 0
+        forward (over key blocks), 1 backward (over query blocks)."""
         n = ctypes.c_int64()
         L = load_library()
         _check(L.zl_causal_plan_tiles(self.handle, which, None, 0, ctypes.byref(n)), "zl_causal_plan_tiles")

@@ -460,7 +460,7 @@ typedef struct zl_causal_plan zl_causal_plan;
 
 /* Plan of the causal attention over n_seqs sequences (host memory, not retained), on the
  * current device: tiles, their static schedule over the SMs, and where few rows face
- * many keys the split of the key range.  n_q_heads must be a multiple of n_kv_heads, query head
+ * many keys, or key tiles too few to fill the SMs, the split of their range.  n_q_heads must be a multiple of n_kv_heads, query head
  * h reads key head h / (n_q_heads / n_kv_heads); at most 128 query heads share a key head.
  * The query tensors have q_tokens rows, the key tensors kv_tokens (below 2^31 - 512).
  * Sequences may come in any order and leave gaps; their query rows must be disjoint.
@@ -481,9 +481,9 @@ ZL_API void zl_causal_plan_destroy(zl_causal_plan* plan);
  * one buffer of the larger size serves both in turn.  Any pointer may be NULL. */
 ZL_API zl_status zl_causal_plan_workspace(const zl_causal_plan* plan, int64_t* fwd_bytes, int64_t* bwd_bytes);
 /* The schedule: which = 0 forward, 1 backward.  *n = tiles; up to cap tiles as 7 int32
- * {sequence, key head, block, first key block, end key block, part, thread block}: forward
- * tiles are two blocks of 128 / group tokens from `block` on, over 128-key blocks, part >= 0 where
- * the key range is split; backward tiles are 128 keys. */
+ * {sequence, key head, block, first, end, part, thread block}.  Forward: two blocks of
+ * 128 / group tokens from `block` on, over 128-key blocks [first, end); backward: 128-key block `block`
+ * over the query blocks [first, end).  part >= 0 where that range is one of several. */
 ZL_API zl_status zl_causal_plan_tiles(const zl_causal_plan* plan, int32_t which, int32_t* out, int64_t cap, int64_t* n);
 
 /* Causal attention: O = softmax(scale q k^T) V over the visible keys and LSE, the natural

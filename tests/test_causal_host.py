@@ -158,8 +158,24 @@ def _check_schedule(seqs, hq, hk, d):
                     assert lo == at
                     at = hi
                 assert at >= -(-seen // 128)
-    bwd = plan.tiles(1)
-    assert sorted(t[:3] for t in bwd) == [(i, h, b) for i, s in enumerate(seqs) for h in range(hk) for b in range(-(-s[3] // 128))]
+    walks, slots = {}, []
+    for s, h, b, lo, hi, part, _ in plan.tiles(1):
+        walks.setdefault((s, h, b), []).append((lo, hi, part))
+        slots += [part] if part >= 0 else []
+    assert sorted(walks) == [(i, h, b) for i, s in enumerate(seqs) for h in range(hk) for b in range(-(-s[3] // 128))]
+    for (i, _, b), w in walks.items():  # from the first query block that sees one of the keys to the last, once
+        _, n, _, m = seqs[i]
+        nqb = -(-n // tb)
+        at = min(nqb, max(0, b * 128 - (m - n)) // tb)
+        assert all((part >= 0) == (len(w) > 1) for _, _, part in w)
+        for lo, hi, _ in sorted(w):
+            assert lo == at
+            at = hi
+        assert at == nqb
+    assert sorted(slots) == list(range(len(slots)))
+    rows = plan.q_tokens * hq * 4
+    assert plan.bwd_workspace_bytes == -(-rows // 256) * 256 + sum(-(-s[1] // tb) for s in seqs) * hk * 128 * d * 4 \
+        + len(slots) * 2 * 128 * d * 4
     assert plan.fwd_workspace_bytes == len(parts) * 256 * (d + 1) * 4
     assert len(parts) == 0 or sorted(parts) == list(range(len(parts)))
     return plan
@@ -182,6 +198,8 @@ def test_long_key_ranges_of_few_rows_are_split_and_many_rows_are_not():
     assert one.fwd_workspace_bytes > 0 and len({t[6] for t in one.tiles(0)}) > 140
     assert _check_schedule(zl.causal_seqs([16384]), 32, 4, 128).fwd_workspace_bytes == 0
     assert _check_schedule(zl.causal_seqs([100, 64]), 4, 2, 64).fwd_workspace_bytes == 0
+    assert any(t[5] >= 0 for t in _check_schedule(zl.causal_seqs([2048, 100]), 24, 8, 64).tiles(1))
+    assert all(t[5] < 0 for t in _check_schedule(zl.causal_seqs([4096] * 12), 24, 8, 64).tiles(1))
 
 
 def test_schedule_is_balanced():
