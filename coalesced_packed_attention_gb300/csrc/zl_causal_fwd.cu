@@ -22,10 +22,13 @@
 // tile, the parts write fp32 O (normalised by their own sum) and LSE to the workspace, and the merge kernel
 // below weighs them by exp(LSE_c - LSE).
 //
+// Tiles follow one another without a pause: the last PV of a tile is issued between the first scores of the next, a
+// third warpgroup takes O out of TMEM (the next tile's first PV waits for that alone), scales and stores it.
 // Rounding: S, the running maximum and sum, O and LSE are fp32.  P is rounded to bf16 because it is an operand of
 // the PV product (relative 2^-9 a weight, independent from key to key); its sum is taken before the rounding.
-// Roles (384 threads, one CTA per SM): warps 0-3 and 4-7 the two softmax warpgroups (thread = TMEM lane = row),
-// warp 8 TMA, warp 9 MMA, 10 and 11 idle.  TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+d), O1 [384,384+d).
+// Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 the two softmax warpgroups (thread = TMEM lane = row),
+// 8-11 output, 12 TMA, 13 MMA, 14 and 15 idle.  TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+d),
+// O1 [384,384+d).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -45,12 +48,13 @@ struct CausalFwdLayout {
   static constexpr int kQ = 0;               // Q0, Q1
   static constexpr int kK = kQ + 2 * kTile;
   static constexpr int kV = kK + kStages * kTile;
-  static constexpr int kOut = kV + kStages * kTile;  // 4 KB for each softmax warp: 32 rows x 64 channels of O
-  static constexpr int kBar = kOut + 8 * 4096;
-  static constexpr int kNumBars = 2 + 1 + 4 * kStages + 2 + 2 + 2 + 1;
+  static constexpr int kOutWarp = 32 * D * 2;  // 32 rows of O for each output warp
+  static constexpr int kOut = kV + kStages * kTile;
+  static constexpr int kStat = kOut + 4 * kOutWarp;  // [sub-tile][row] {1 / l, LSE}
+  static constexpr int kBar = kStat + 2 * 128 * 8;
+  static constexpr int kNumBars = 15 + 2 + 4 * kStages;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kBytes = kMisc + 32;
-  static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024 B
+  static constexpr int kBytes = kMisc + 16;
 };
 
 constexpr float kGrow = 8.0f;  // O is rescaled only when the row maximum grows by more than 2^8
@@ -108,12 +112,13 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, uint64_t
       : "memory");
 }
 
-// Launched with 168 registers a thread (three warps to a sub-partition); the softmax warpgroups, which hold a
-// row's 128 scores, take 216 and leave 72 to the warps that issue: per sub-partition 2 x 216 + 72 = 3 x 168, the launch
-// allocation.
-constexpr int kFwdThreads = 384;
-constexpr uint32_t kFwdLaunchRegs = 168, kFwdSoftmaxRegs = 216, kFwdIssueRegs = 72;
-static_assert(2 * kFwdSoftmaxRegs + kFwdIssueRegs == 3 * kFwdLaunchRegs, "register split must equal the launch allocation");
+// Launched with 128 registers a thread (four warps to a sub-partition); the softmax warpgroups, which hold a row's
+// 128 scores, take 176, the output warpgroup keeps 88 and the warps that issue 72: per sub-partition 2 x 176 + 88 +
+// 72 = 4 x 128, the launch allocation.
+constexpr int kFwdThreads = 512;
+constexpr uint32_t kFwdLaunchRegs = 128, kFwdSoftmaxRegs = 176, kFwdOutRegs = 88, kFwdIssueRegs = 72;
+static_assert(2 * kFwdSoftmaxRegs + kFwdOutRegs + kFwdIssueRegs == 4 * kFwdLaunchRegs,
+              "register split must equal the launch allocation");
 
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -121,34 +126,44 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                          const __grid_constant__ CUtensorMap tm_v, const CausalFwdParams p) {
   using L = CausalFwdLayout<D>;
   constexpr int S = L::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem + L::kQ;
   uint8_t* sK = smem + L::kK;
   uint8_t* sV = smem + L::kV;
+  float2* sStat = reinterpret_cast<float2*>(smem + L::kStat);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* q_full = bar;  // [2] one per sub-tile
-  uint64_t* q_empty = bar + 2;
-  uint64_t* k_full = bar + 3;  // [S]
+  uint64_t* q_full = bar;           // [2] one per sub-tile, as all pairs below
+  uint64_t* q_empty = bar + 2;      // the sub-tile's last scores are done with Q
+  uint64_t* s_full = bar + 4;
+  uint64_t* p_full = bar + 6;
+  uint64_t* o_full = bar + 8;       // last PV of a tile done
+  uint64_t* o_free = bar + 10;      // O has been read out of TMEM
+  uint64_t* stat_full = bar + 12;
+  uint64_t* stat_empty = bar + 14;
+  uint64_t* drain = bar + 16;
+  uint64_t* k_full = bar + 17;      // [S]
   uint64_t* k_empty = k_full + S;
   uint64_t* v_full = k_empty + S;
   uint64_t* v_empty = v_full + S;
-  uint64_t* s_full = v_empty + S;  // [2] per sub-tile
-  uint64_t* p_full = s_full + 2;   // [2]
-  uint64_t* o_bar = p_full + 2;    // [2] last PV of a tile done
-  uint64_t* drain = o_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need a 1024-byte aligned base
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, ZL_ERR_UNSUPPORTED);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 128);
-      mbar_init(o_bar + i, 1);
+      mbar_init(o_full + i, 1);
+      mbar_init(o_free + i, 128);
+      mbar_init(stat_full + i, 128);
+      mbar_init(stat_empty + i, 128);
     }
-    mbar_init(q_empty, 1);
     for (int s = 0; s < S; ++s) {
       mbar_init(k_full + s, 1);
       mbar_init(k_empty + s, 1);
@@ -159,12 +174,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == 12 && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (warp == 9) {
+  if (warp == 13) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -176,147 +191,246 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int tb = tokens_per_block(p.group);
   const int t_begin = p.tile_ptr[blockIdx.x], t_end = p.tile_ptr[blockIdx.x + 1];
 
-  if (warp >= 8) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFwdIssueRegs));
-   if (warp == 8) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint32_t q_bytes = (uint32_t)(D / 64) * (uint32_t)(tb * p.group) * 128u;
-      uint32_t kv_it = 0, q_it = 0, q_loads[2] = {0, 0}, k_loads = 0, v_loads = 0;
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFwdIssueRegs));
+    if (warp == 12) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        const uint32_t q_bytes = (uint32_t)(D / 64) * (uint32_t)(tb * p.group) * 128u;
+        uint32_t k_it = 0, v_it = 0, q_it[2] = {0, 0};
+        bool ok = true;
+        for (int t = t_begin; t < t_end && ok; ++t) {
+          const CausalTile tl = p.tiles[t];
+          const FwdSpan sp = span_of(tl, tb);
+          const int kv0 = tl.kv_row + tl.kv_lo * 128;
+          for (int j = 0; j < sp.nmax && ok; ++j) {
+            const uint32_t s = k_it % S, ph = (k_it / S) & 1;
+            if (!cwait(k_empty + s, ph ^ 1, abort_flag, lim, p.status)) { ok = false; break; }
+            mbar_arrive_expect_tx(k_full + s, L::kTile);
+            if (p.withhold_load && k_it == 0) {
+              // test hook: the announced bytes never arrive; a bounded wait runs out
+            } else {
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(sK + s * L::kTile + c * L::kBox, &tm_k, k_full + s, 64 * c, tl.head, kv0 + j * 128);
+            }
+            ++k_it;
+            // the queries behind the first keys: their place is free once the previous tile's last scores are done
+            for (int w = 0; w < 2 && j == 0; ++w) {
+              if (sp.n[w] == 0) continue;
+              if (!cwait(q_empty + w, (q_it[w] & 1) ^ 1, abort_flag, lim, p.status)) { ok = false; break; }
+              mbar_arrive_expect_tx(q_full + w, q_bytes);
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(sQ + w * L::kTile + c * L::kBox, &tm_q, q_full + w, 64 * c, 0, tl.head, tl.q_row + sp.tok[w]);
+              ++q_it[w];
+            }
+            if (!ok) break;
+            if (!cwait(v_empty + s, ph ^ 1, abort_flag, lim, p.status)) { ok = false; break; }
+            mbar_arrive_expect_tx(v_full + s, L::kTile);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(sV + s * L::kTile + c * L::kBox, &tm_v, v_full + s, 64 * c, tl.head, kv0 + j * 128);
+            ++v_it;
+          }
+        }
+        if (*abort_flag) {
+          // the copies in flight land before the block's shared memory goes back (a bounded wait each)
+          auto settle = [](uint64_t* b, uint32_t parity) {
+            const long long t0 = clock64();
+            while (!mbar_try_wait(smem_u32(b), parity) && clock64() - t0 < 2000000) {
+            }
+          };
+          for (int w = 0; w < 2; ++w)
+            if (q_it[w]) settle(q_full + w, (q_it[w] - 1) & 1);
+          for (uint32_t b = 1; b <= (uint32_t)S; ++b) {
+            if (k_it >= b) settle(k_full + (k_it - b) % S, ((k_it - b) / S) & 1);
+            if (v_it >= b) settle(v_full + (v_it - b) % S, ((v_it - b) / S) & 1);
+          }
+        }
+      }
+    } else if (warp == 13) {
+      // ------------------------------------------------------------ MMA issuer
+      // The whole warp runs the loop (control flow, waits and descriptors are warp-uniform); one elected lane
+      // executes each product and commit.  A block's PV is issued behind the next block's waits, between that
+      // block's scores; "next" may be the next tile's first.
+      constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
+      const uint32_t aV = smem_u32(sV);
+      // low words of the operand descriptors (all share the high word)
+      const uint32_t dQ0 = sdesc_lo(smem_u32(sQ), 16), dK0 = sdesc_lo(smem_u32(sK), 16), dV0 = sdesc_lo(aV, L::kBox);
+      auto dsc = [](uint32_t lo, uint32_t bytes) { return sdesc_join(lo + (bytes >> 4)); };
+      uint32_t kv_it = 0, q_it[2] = {0, 0}, p_it[2] = {0, 0}, o_it[2] = {0, 0};
       bool ok = true;
+      auto wait_w = [&](uint64_t* b, uint32_t parity) {
+        return __all_sync(0xffffffffu, cwait(b, parity, abort_flag, lim, p.status));
+      };
+      // the block whose PV is still to be issued
+      bool pend = false, pend_w[2] = {false, false}, first = false, last[2] = {false, false};
+      int vrows = 128;
+      auto issue_v = [&]() -> bool {  // its values have landed
+        const uint32_t ps = (kv_it - 1) % S;
+        if (!wait_w(v_full + ps, ((kv_it - 1) / S) & 1)) return false;
+        // value rows past the sequence's keys are other tokens: their weights are zero, but 0 x NaN is not
+        if (vrows < 128) {
+          zero_tile_rows<D>(aV + ps * L::kTile, vrows, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        return true;
+      };
+      auto issue_pv = [&](int w) -> bool {
+        const uint32_t ps = (kv_it - 1) % S;
+        if (!wait_w(p_full + w, p_it[w] & 1)) return false;
+        ++p_it[w];
+        if (first) {  // O of the previous tile has left TMEM
+          if (!wait_w(o_free + w, (o_it[w] & 1) ^ 1)) return false;
+          ++o_it[w];
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_w(tmem + 256 + 128 * w, tmem + 128 * w + kk * 8, dsc(dV0, ps * L::kTile + kk * 2048), kIdPV,
+                   (first && kk == 0) ? 0u : 1u);
+        if (last[w]) mma_commit_w(o_full + w);
+        return true;
+      };
       for (int t = t_begin; t < t_end && ok; ++t) {
         const CausalTile tl = p.tiles[t];
         const FwdSpan sp = span_of(tl, tb);
-        if (sp.nmax == 0) continue;
-        if (!cwait(q_empty, (q_it & 1) ^ 1, abort_flag, lim, p.status)) break;
-        ++q_it;
-        for (int w = 0; w < 2; ++w) {
-          if (sp.n[w] == 0) continue;
-          mbar_arrive_expect_tx(q_full + w, q_bytes);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sQ + w * L::kTile + c * L::kBox, &tm_q, q_full + w, 64 * c, 0, tl.head,
-                        tl.q_row + sp.tok[w]);
-          ++q_loads[w];
-        }
-        const int kv0 = tl.kv_row + tl.kv_lo * 128;
         for (int j = 0; j < sp.nmax; ++j) {
           const uint32_t s = kv_it % S, ph = (kv_it / S) & 1;
-          if (!cwait(k_empty + s, ph ^ 1, abort_flag, lim, p.status)) { ok = false; break; }
-          mbar_arrive_expect_tx(k_full + s, L::kTile);
-          if (p.withhold_load && kv_it == 0) {
-            // test hook: the announced bytes never arrive; a bounded wait runs out
-          } else {
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(sK + s * L::kTile + c * L::kBox, &tm_k, k_full + s, 64 * c, tl.head, kv0 + j * 128);
+          if (!wait_w(k_full + s, ph) || (pend && !issue_v())) { ok = false; break; }
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (pend && pend_w[w] && !issue_pv(w)) { ok = false; break; }
+            if (j < sp.n[w]) {
+              if (j == 0) {
+                if (!wait_w(q_full + w, q_it[w] & 1)) { ok = false; break; }
+                ++q_it[w];
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
+                mma_ss_w(tmem + 128 * w, dsc(dQ0, w * L::kTile + off), dsc(dK0, s * L::kTile + off), kIdS, kk > 0 ? 1u : 0u);
+              }
+              mma_commit_w(s_full + w);
+              if (j == sp.n[w] - 1) mma_commit_w(q_empty + w);
+            }
           }
-          ++k_loads;
-          if (!cwait(v_empty + s, ph ^ 1, abort_flag, lim, p.status)) { ok = false; break; }
-          mbar_arrive_expect_tx(v_full + s, L::kTile);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sV + s * L::kTile + c * L::kBox, &tm_v, v_full + s, 64 * c, tl.head, kv0 + j * 128);
-          ++v_loads;
+          if (!ok) break;
+          if (pend) mma_commit_w(v_empty + (kv_it - 1) % S);
+          mma_commit_w(k_empty + s);
+          pend = true;
+          first = j == 0;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            pend_w[w] = j < sp.n[w];
+            last[w] = j == sp.n[w] - 1;
+          }
+          vrows = tl.kv_len - (tl.kv_lo + j) * 128;
           ++kv_it;
         }
       }
-      if (*abort_flag) {
-        // the copies in flight land before the block's shared memory goes back (a bounded wait each)
-        auto settle = [](uint64_t* b, uint32_t parity) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(smem_u32(b), parity) && clock64() - t0 < 2000000) {
-          }
-        };
+      if (ok && pend && issue_v()) {
         for (int w = 0; w < 2; ++w)
-          if (q_loads[w]) settle(q_full + w, (q_loads[w] - 1) & 1);
-        for (uint32_t b = 1; b <= (uint32_t)S; ++b) {
-          if (k_loads >= b) settle(k_full + (k_loads - b) % S, ((k_loads - b) / S) & 1);
-          if (v_loads >= b) settle(v_full + (v_loads - b) % S, ((v_loads - b) / S) & 1);
-        }
+          if (pend_w[w] && !issue_pv(w)) break;
       }
+      mma_commit_w(drain);
+      wait_w(drain, 0);
     }
-   } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop (control flow, waits and descriptors are warp-uniform); one elected lane
-    // executes each product and commit.
-    constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
-    constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
-    const uint32_t aV = smem_u32(sV);
-    const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024), dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
-    const uint64_t dV0 = sdesc_sw128(aV, L::kBox, 1024);
-    uint32_t kv_it = 0, qcount[2] = {0, 0}, pcount[2] = {0, 0};
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ output warpgroup (thread = row of a sub-tile)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFwdOutRegs));
+    const int r = threadIdx.x & 127, rt = r / p.group, rh = r - rt * p.group;  // its token and head
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t buf = smem_u32(smem + L::kOut) + (warp & 3) * L::kOutWarp;
+    constexpr int kPieces = D / 8, kPerStep = 32 / kPieces;  // 16-byte pieces of a row, rows of a store
+    // piece c of row x lies at c ^ (x mod 8) (within 128 bytes), free of bank conflicts for a row's writer and for a
+    // store's readers
+    auto at = [&](int x, int c) { return buf + x * (D * 2) + (c >> 3) * 128 + (((c & 7) ^ (x & 7)) << 4); };
+    uint32_t it[2] = {0, 0};
     bool ok = true;
-    auto wait_w = [&](uint64_t* b, uint32_t parity) {
-      return __all_sync(0xffffffffu, cwait(b, parity, abort_flag, lim, p.status));
-    };
-    auto issue_s = [&](int w, uint32_t stage) {
-      const uint64_t dq = sdesc_add(dQ0, w * L::kTile), dk = sdesc_add(dK0, stage * L::kTile);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t koff = (kk >> 2) * L::kBox + (kk & 3) * 32;
-        mma_ss_w(tmem + 128 * w, sdesc_add(dq, koff), sdesc_add(dk, koff), kIdS, kk > 0 ? 1u : 0u);
-      }
-      mma_commit_w(s_full + w);
-    };
-    auto issue_pv = [&](int w, uint32_t stage, bool first) -> bool {
-      if (!wait_w(p_full + w, pcount[w] & 1)) return false;
-      ++pcount[w];
-      tc_fence_after();
-      const uint64_t dv = sdesc_add(dV0, stage * L::kTile);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ts_w(tmem + 256 + 128 * w, tmem + 128 * w + kk * 8, sdesc_add(dv, kk * 2048), kIdPV,
-                 (first && kk == 0) ? 0u : 1u);
-      return true;
-    };
     for (int t = t_begin; t < t_end && ok; ++t) {
       const CausalTile tl = p.tiles[t];
       const FwdSpan sp = span_of(tl, tb);
-      if (sp.nmax == 0) continue;
-      uint32_t ps = 0, pph = 0;
-      for (int j = 0; j <= sp.nmax; ++j) {
-        const uint32_t s = kv_it % S, ph = (kv_it / S) & 1;
-        const bool more = j < sp.nmax;
-        if (more && !wait_w(k_full + s, ph)) { ok = false; break; }
-        if (j > 0) {
-          if (!wait_w(v_full + ps, pph)) { ok = false; break; }
-          // value rows past the sequence's keys are other tokens: their weights are zero, but 0 x NaN is not
-          const int vrows = tl.kv_len - (tl.kv_lo + j - 1) * 128;
-          if (vrows < 128) {
-            zero_tile_rows<D>(aV + ps * L::kTile, vrows, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (j == 0 && sp.n[w] > 0) {
-            if (!wait_w(q_full + w, qcount[w] & 1)) { ok = false; break; }
-            ++qcount[w];
-          }
+      for (int w = 0; w < 2; ++w) {
+        if (sp.toks[w] == 0) continue;
+        const bool row_ok = rt < sp.toks[w];
+        float2 st = make_float2(0.f, kNegInf);  // no key: O = 0, LSE = -inf
+        if (sp.n[w] > 0) {
+          if (!__all_sync(0xffffffffu, cwait(stat_full + w, it[w] & 1, abort_flag, lim, p.status) &&
+                                           cwait(o_full + w, it[w] & 1, abort_flag, lim, p.status))) { ok = false; break; }
+          ++it[w];
+          st = sStat[128 * w + r];
+          mbar_arrive(stat_empty + w);
           tc_fence_after();
-          if (j > 0 && j <= sp.n[w]) {
-            if (!issue_pv(w, ps, j == 1)) { ok = false; break; }
-            if (j == sp.n[w]) mma_commit_w(o_bar + w);
-          }
-          if (j < sp.n[w]) issue_s(w, s);
         }
-        if (!ok) break;
-        if (j > 0) mma_commit_w(v_empty + ps);
-        if (more) mma_commit_w(k_empty + s);
-        if (j == sp.nmax - 1) mma_commit_w(q_empty);
-        ps = s;
-        pph = ph;
-        if (more) ++kv_it;
+        const int64_t row = ((int64_t)tl.q_row + sp.tok[w] + rt) * p.n_q_heads + (int64_t)tl.head * p.group + rh;
+        const int64_t prow = (int64_t)tl.part * 256 + 128 * w + r;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t u[32];
+          if (sp.n[w] > 0) {
+            tmem_ld32(tmem + lane_base + 256 + 128 * w + 32 * c, u);
+            tmem_ld_wait();
+          }
+          // a row without a key beside rows with some: its weights were all zero, and 0 x Inf or NaN of a value that
+          // it does not see must not show
+          if (st.x == 0.f) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) u[e] = 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(u[8 * i + e]) * st.x;
+            if (tl.part < 0) {
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(lane, 4 * c + i)), "r"(pack_bf16(f[0], f[1])),
+                           "r"(pack_bf16(f[2], f[3])), "r"(pack_bf16(f[4], f[5])), "r"(pack_bf16(f[6], f[7]))
+                           : "memory");
+            } else if (row_ok) {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c + 8 * i);
+              dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+              dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+          }
+        }
+        if (sp.n[w] > 0) {
+          tc_fence_before();
+          mbar_arrive(o_free + w);  // the next tile's first PV may overwrite O
+        }
+        if (row_ok) {
+          if (tl.part < 0) p.lse[row] = st.y;
+          else p.part_lse[prow] = st.y;
+        }
+        if (tl.part < 0) {
+          // a store writes whole rows (two at d = 128): a piece of 32 rows a store kept the load/store unit busy for
+          // 2900 cycles a tile
+          __syncwarp();
+          const int rel = row_ok ? rt * p.n_q_heads + rh : -1;
+          __nv_bfloat16* base = p.o + (row - (rt * p.n_q_heads + rh)) * D + (lane % kPieces) * 8;
+#pragma unroll 4
+          for (int i = 0; i < 32 / kPerStep; ++i) {
+            const int x = i * kPerStep + lane / kPieces;
+            const int to = __shfl_sync(0xffffffffu, rel, x);
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(at(x, lane % kPieces))
+                         : "memory");
+            if (to >= 0) *reinterpret_cast<uint4*>(base + (int64_t)to * D) = v;
+          }
+          __syncwarp();  // the buffer is written again
+        }
       }
     }
-    mma_commit_w(drain);
-    wait_w(drain, 0);
-   }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFwdSoftmaxRegs));
     const int w = warp >> 2;          // sub-tile of this warpgroup
     const int r = threadIdx.x & 127;  // row of the sub-tile == TMEM lane
-    const int rt = r / p.group, rh = r - rt * p.group;  // its token and head
+    const int rt = r / p.group;       // its token
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + 128 * w;
     const uint32_t tO = tmem + lane_base + 256 + 128 * w;
@@ -327,12 +441,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (t + 1 < t_end && lane == 0) touch(p.tiles + t + 1);
       const FwdSpan sp = span_of(tl, tb);
       const int toks = w ? sp.toks[1] : sp.toks[0], n = w ? sp.n[1] : sp.n[0];
-      if (toks == 0) continue;
-      const int tok = (w ? sp.tok[1] : sp.tok[0]) + rt;
-      const bool row_ok = rt < toks;
+      if (n == 0) continue;
       // keys this row sees, from the tile's first block on; rows that are not stored need no mask
-      const int seen =
-          row_ok ? max(0, tl.kv_len - tl.q_len + tok + 1) - tl.kv_lo * 128 : 0x7fffffff;
+      const int seen = rt < toks ? max(0, tl.kv_len - tl.q_len + (w ? sp.tok[1] : sp.tok[0]) + rt + 1) - tl.kv_lo * 128 : 0x7fffffff;
 
       float m_used = kNegInf, l = 0.f;
       bool ok = true;
@@ -405,92 +516,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         mbar_arrive(p_full + w);
       }
       if (!ok) break;
-      if (n > 0) {
-        if (!__all_sync(0xffffffffu, cwait(o_bar + w, tiles_done & 1, abort_flag, lim, p.status))) break;
-        ++tiles_done;
-        tc_fence_after();
-      }
-      // ---- epilogue: O / l and LSE.  l > 0 wherever the row saw a key (its largest weight is >= 2^-8); a NaN
-      // sum stays NaN.
-      const float inv_l = l == 0.f ? 0.f : __frcp_rn(l);
-      const float lse_v = l == 0.f ? kNegInf : (m_used + lg2(l)) * kLn2;
-      const int64_t row = ((int64_t)tl.q_row + tok) * p.n_q_heads + (int64_t)tl.head * p.group + rh;
-      const int64_t prow = (int64_t)tl.part * 256 + 128 * w + r;
-      auto load_o = [&](int c, uint32_t (&u)[32]) {  // 32 channels of O / l
-        if (n > 0) {
-          tmem_ld32(tO + 32 * c, u);
-          tmem_ld_wait();
-        }
-        // a row without a key beside rows with some: its weights were all zero, and 0 x Inf or NaN of a value
-        // that it does not see must not show
-#pragma unroll
-        for (int e = 0; e < 32; ++e) u[e] = n > 0 && l != 0.f ? __float_as_uint(__uint_as_float(u[e]) * inv_l) : 0u;
-      };
-      if (tl.part < 0) {
-        // 64 channels of the warp's 32 rows through shared memory (16-byte pieces, swizzled by row), so that a store
-        // writes four rows' whole 128 bytes: a store per row and thread kept the load/store unit busy for 2900 cycles
-        // a tile
-        // (the lane is read again here: addresses formed from the one above would be kept in registers through
-        // the loop over key blocks, which has none to spare)
-        int ln;
-        asm volatile("mov.u32 %0, %%laneid;" : "=r"(ln));
-        const uint32_t buf = smem_u32(smem + L::kOut) + warp * 4096;
-        const int rel = row_ok ? rt * p.n_q_heads + rh : -1;
-        __nv_bfloat16* base = p.o + (((int64_t)tl.q_row + tok - rt) * p.n_q_heads + (int64_t)tl.head * p.group) * D + (ln & 7) * 8;
-#pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-          if (half > 0) __syncwarp();  // the first half has been read
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t u[32];
-            load_o(2 * half + c, u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = pack_bf16(__uint_as_float(u[8 * i + 2 * e]), __uint_as_float(u[8 * i + 2 * e + 1]));
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + ln * 128 + (((4 * c + i) ^ (ln & 7)) << 4)),
-                           "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                           : "memory");
-            }
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int lr = 4 * i + (ln >> 3);  // lane's row of the warp
-            const int to = __shfl_sync(0xffffffffu, rel, lr);
-            uint4 v;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(buf + lr * 128 + (((ln & 7) ^ (lr & 7)) << 4))
-                         : "memory");
-            if (to >= 0) *reinterpret_cast<uint4*>(base + (int64_t)to * D + 64 * half) = v;
-          }
-        }
-        __syncwarp();  // the next tile's rows overwrite the buffer
-      } else {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t u[32];
-          load_o(c, u);
-          if (row_ok) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + 32 * c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
-          }
-        }
-      }
-      if (row_ok) {
-        if (tl.part < 0) p.lse[row] = lse_v;
-        else p.part_lse[prow] = lse_v;
-      }
-      tc_fence_before();
+      // ---- 1 / l and LSE for the output warpgroup.  l > 0 wherever the row saw a key (its largest weight is >=
+      // 2^-8); a NaN sum stays NaN.
+      if (!__all_sync(0xffffffffu, cwait(stat_empty + w, (tiles_done & 1) ^ 1, abort_flag, lim, p.status))) break;
+      ++tiles_done;
+      sStat[128 * w + r] = make_float2(l == 0.f ? 0.f : __frcp_rn(l), l == 0.f ? kNegInf : (m_used + lg2(l)) * kLn2);
+      mbar_arrive(stat_full + w);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 13) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -541,7 +578,7 @@ template <int D>
 cudaError_t launch_causal_fwd_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                    const CausalFwdParams& p, int grid, cudaStream_t stream) {
   using L = CausalFwdLayout<D>;
-  const int smem = L::kAlloc > 120 * 1024 ? L::kAlloc : 120 * 1024;  // one CTA per SM (TMEM 512 columns)
+  const int smem = L::kBytes > 120 * 1024 ? L::kBytes : 120 * 1024;  // one CTA per SM (TMEM 512 columns)
   static PerDeviceOnce configured;
   cudaError_t e = configured.run([&] {
     cudaError_t r = cudaFuncSetAttribute(zl_causal_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
