@@ -94,7 +94,7 @@ struct CausalFwdParams {
 struct CausalMergeParams {
   const CausalSeq* seqs;
   const CausalMerge* groups;
-  int32_t n_groups, n_q_heads, group;
+  int32_t n_groups, rows, n_q_heads, group;  // rows: the most that a split tile has, of its 256
   const float* part_o;
   const float* part_lse;
   __nv_bfloat16* o;
@@ -135,7 +135,7 @@ struct CausalFinishParams {
 
 cudaError_t launch_causal_fwd(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CausalFwdParams& p, int grid, cudaStream_t stream);
-cudaError_t launch_causal_merge(int head_dim, const CausalMergeParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_causal_merge(int head_dim, const CausalMergeParams& p, cudaStream_t stream);
 // D = rowsum(dO * O) over every row of the query tensor, and zeroing of the dQ accumulator.
 cudaError_t launch_causal_bwd_pre(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* row_d,
                                   int64_t rows, float* acc, int64_t acc_floats, int num_sms, cudaStream_t stream);
@@ -160,6 +160,7 @@ struct zl_causal_plan {
   std::vector<zl::CausalMerge> merges;
   std::vector<zl::CausalBwdMerge> bwd_merges;
   int32_t slots = 0, bwd_slots = 0;
+  int32_t merge_rows = 0;  // rows of a split forward tile that may hold a query (the largest)
   int64_t acc_blocks = 0;
   int64_t fwd_bytes = 0, bwd_bytes = 0;
 

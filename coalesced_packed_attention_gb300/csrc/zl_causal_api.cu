@@ -121,13 +121,14 @@ extern "C" zl_status zl_causal_attn_fwd(const zl_causal_plan* p, const void* q, 
   mp.seqs = p->d_seqs;
   mp.groups = p->d_merges;
   mp.n_groups = (int32_t)p->merges.size();
+  mp.rows = p->merge_rows;
   mp.n_q_heads = p->n_q_heads;
   mp.group = p->group;
   mp.part_o = fp.part_o;
   mp.part_lse = fp.part_lse;
   mp.o = fp.o;
   mp.lse = lse;
-  return launch_causal_merge(p->head_dim, mp, p->num_sms, st) == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
+  return launch_causal_merge(p->head_dim, mp, st) == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
 
 extern "C" zl_status zl_causal_attn_bwd(const zl_causal_plan* p, const void* q, int64_t q_stride, const void* k,

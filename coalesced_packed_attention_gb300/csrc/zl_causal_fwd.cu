@@ -533,18 +533,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 }
 
-// Combine of a tile's parts: LSE = M + ln sum_c exp(LSE_c - M), O = sum_c exp(LSE_c - LSE) O_c.  One block per
-// split tile, one warp per row, d / 32 channels per lane; parts are added in key order.
+// Combine of a tile's parts: LSE = M + ln sum_c exp(LSE_c - M), O = sum_c exp(LSE_c - LSE) O_c.  One warp per row,
+// kMergeRows rows of a split tile a block, d / 32 channels per lane; parts are added in key order.  (A block per tile,
+// its warps going through 256 rows, took 100 us where prompts are split.)
+constexpr int kMergeRows = 4;
 template <int D>
-__global__ void __launch_bounds__(128) zl_causal_merge_kernel(const CausalMergeParams p) {
+__global__ void __launch_bounds__(32 * kMergeRows) zl_causal_merge_kernel(const CausalMergeParams p) {
   constexpr int E = D / 32;
   const CausalMerge G = p.groups[blockIdx.x];
   const CausalSeq sq = p.seqs[G.seq];
   const int lane = threadIdx.x & 31, tb = tokens_per_block(p.group);
-  for (int r = threadIdx.x >> 5; r < 256; r += 4) {
+  {
+    const int r = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
     const int rr = r & 127, rt = rr / p.group;
     const int tok = (G.block + (r >> 7)) * tb + rt;
-    if (rt >= tb || tok >= sq.q_len) continue;  // warp-uniform
+    if (rt >= tb || tok >= sq.q_len) return;  // warp-uniform
     const float* pl = p.part_lse + (int64_t)G.slot * 256 + r;
     float m = kNegInf;
     for (int c = lane; c < G.parts; c += 32) m = fmaxf(m, pl[(int64_t)c * 256]);
@@ -602,10 +605,11 @@ cudaError_t launch_causal_fwd(int head_dim, const CUtensorMap& tq, const CUtenso
                          : launch_causal_fwd_impl<64>(tq, tk, tv, p, grid, stream);
 }
 
-cudaError_t launch_causal_merge(int head_dim, const CausalMergeParams& p, int, cudaStream_t stream) {
+cudaError_t launch_causal_merge(int head_dim, const CausalMergeParams& p, cudaStream_t stream) {
   if (p.n_groups == 0) return cudaSuccess;
-  if (head_dim == 128) zl_causal_merge_kernel<128><<<p.n_groups, 128, 0, stream>>>(p);
-  else zl_causal_merge_kernel<64><<<p.n_groups, 128, 0, stream>>>(p);
+  const dim3 grid(p.n_groups, (p.rows + kMergeRows - 1) / kMergeRows);
+  if (head_dim == 128) zl_causal_merge_kernel<128><<<grid, 32 * kMergeRows, 0, stream>>>(p);
+  else zl_causal_merge_kernel<64><<<grid, 32 * kMergeRows, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -145,7 +145,11 @@ void build_forward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool r
   for (const FwdItem& u : all) {
     const int k = pieces(u.n, chunk);
     const CausalSeq& s = p->seqs[u.seq];
-    if (k > 1) p->merges.push_back({u.seq, u.head, u.block, p->slots, k, {0, 0, 0}});
+    if (k > 1) {
+      p->merges.push_back({u.seq, u.head, u.block, p->slots, k, {0, 0, 0}});
+      const int toks = std::min(tb, s.q_len - (u.block + u.two) * tb);  // of the tile's last query block
+      p->merge_rows = std::max(p->merge_rows, (u.two ? kCausalRows : 0) + toks * p->group);
+    }
     for (int c = 0; c < k; ++c) {
       const int lo = piece_at(u.n, k, c), hi = piece_at(u.n, k, c + 1);
       p->fwd_tiles.push_back({(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, u.head, u.block, lo, hi,
