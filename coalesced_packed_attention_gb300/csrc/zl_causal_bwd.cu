@@ -708,29 +708,29 @@ __global__ void __launch_bounds__(256) zl_causal_finish_kernel(const CausalFinis
     }
     __syncthreads();
   }
-  // the first item behind the slabs that is this block's
+  // the first item behind the slabs that is this block's: a split key tile's dV or dK, kRows of its 128 rows, a
+  // 16-byte piece of the result per thread
+  constexpr int kPieces = D / 8, kRows = 256 / kPieces, kItems = 128 / kRows;
   int64_t it = blockIdx.x;
   if (it < n_slabs) it += (n_slabs - it + gridDim.x - 1) / gridDim.x * gridDim.x;
-  for (it -= n_slabs; it < 2 * (int64_t)p.n_merges; it += gridDim.x) {
-    const CausalBwdMerge m = p.merges[it >> 1];
-    const int of_k = (int)(it & 1);
-    const float4* src = reinterpret_cast<const float4*>(p.part) + ((int64_t)m.slot * 2 + of_k) * (128 * D / 4);
-    const float scale = of_k ? p.scale : 1.f;
-    __nv_bfloat16* out = of_k ? p.dk : p.dv;
-    const int64_t stride = of_k ? p.dk_stride : p.dv_stride;
-    for (int k = threadIdx.x; k < 128 * D / 8; k += 256) {
-      const int r = k / (D / 8), c = k % (D / 8), key = m.block * 128 + r;
-      if (key >= m.kv_len) break;  // rows ascend with k
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
-      for (int q = 0; q < m.parts; ++q) {
-        const float4 a = __ldg(src + (int64_t)q * (2 * 128 * D / 4) + 2 * k), b = __ldg(src + (int64_t)q * (2 * 128 * D / 4) + 2 * k + 1);
-        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
-        w.x += b.x; w.y += b.y; w.z += b.z; w.w += b.w;
-      }
-      *reinterpret_cast<uint4*>(out + ((int64_t)m.kv_row + key) * stride + (int64_t)m.head * D + 8 * c) =
-          make_uint4(pack_bf16(v.x * scale, v.y * scale), pack_bf16(v.z * scale, v.w * scale),
-                     pack_bf16(w.x * scale, w.y * scale), pack_bf16(w.z * scale, w.w * scale));
+  for (it -= n_slabs; it < 2 * kItems * (int64_t)p.n_merges; it += gridDim.x) {
+    const CausalBwdMerge m = p.merges[it / (2 * kItems)];
+    const int of_k = (int)(it / kItems & 1), r = (int)(it % kItems) * kRows + threadIdx.x / kPieces, c = threadIdx.x % kPieces;
+    const int key = m.block * 128 + r;
+    if (key >= m.kv_len) continue;
+    const float4* src = reinterpret_cast<const float4*>(p.part) + ((int64_t)m.slot * 2 + of_k) * (128 * D / 4) + r * (D / 4) + 2 * c;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
+#pragma unroll 4
+    for (int q = 0; q < m.parts; ++q) {
+      const float4 a = __ldg(src + (int64_t)q * (2 * 128 * D / 4)), b = __ldg(src + (int64_t)q * (2 * 128 * D / 4) + 1);
+      v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+      w.x += b.x; w.y += b.y; w.z += b.z; w.w += b.w;
     }
+    const float scale = of_k ? p.scale : 1.f;
+    *reinterpret_cast<uint4*>((of_k ? p.dk : p.dv) + ((int64_t)m.kv_row + key) * (of_k ? p.dk_stride : p.dv_stride) +
+                              (int64_t)m.head * D + 8 * c) =
+        make_uint4(pack_bf16(v.x * scale, v.y * scale), pack_bf16(v.z * scale, v.w * scale),
+                   pack_bf16(w.x * scale, w.y * scale), pack_bf16(w.z * scale, w.w * scale));
   }
 }
 
@@ -778,7 +778,7 @@ cudaError_t launch_causal_bwd(int head_dim, const CUtensorMap& tq, const CUtenso
 }
 
 cudaError_t launch_causal_finish(int head_dim, const CausalFinishParams& p, int num_sms, cudaStream_t stream) {
-  const int64_t items = p.acc_blocks * (head_dim / 64) + 2 * (int64_t)p.n_merges;
+  const int64_t items = p.acc_blocks * (head_dim / 64) + 2 * (head_dim / 16) * (int64_t)p.n_merges;
   if (items == 0) return cudaSuccess;
   auto k = head_dim == 128 ? zl_causal_finish_kernel<128> : zl_causal_finish_kernel<64>;
   static PerDeviceInt resident[2];
