@@ -134,13 +134,13 @@ struct CausalFinishParams {
 };
 
 cudaError_t launch_causal_fwd(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const CausalFwdParams& p, int grid, cudaStream_t stream);
+                              const CausalFwdParams& p, int grid, bool early, cudaStream_t stream);
 cudaError_t launch_causal_merge(int head_dim, const CausalMergeParams& p, cudaStream_t stream);
 // D = rowsum(dO * O) over every row of the query tensor, and zeroing of the dQ accumulator.
 cudaError_t launch_causal_bwd_pre(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* row_d,
                                   int64_t rows, float* acc, int64_t acc_floats, int num_sms, cudaStream_t stream);
 cudaError_t launch_causal_bwd(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const CUtensorMap& tdo, const CausalBwdParams& p, int grid, cudaStream_t stream);
+                              const CUtensorMap& tdo, const CausalBwdParams& p, int grid, bool early, cudaStream_t stream);
 cudaError_t launch_causal_finish(int head_dim, const CausalFinishParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace zl
@@ -160,6 +160,7 @@ struct zl_causal_plan {
   std::vector<zl::CausalMerge> merges;
   std::vector<zl::CausalBwdMerge> bwd_merges;
   int32_t slots = 0, bwd_slots = 0;
+  bool fwd_short = false, bwd_short = false;  // the schedule is under some 100 us: worth setting up early
   int32_t merge_rows = 0;  // rows of a split forward tile that may hold a query (the largest)
   int64_t acc_blocks = 0;
   int64_t fwd_bytes = 0, bwd_bytes = 0;

@@ -115,7 +115,7 @@ extern "C" zl_status zl_causal_attn_fwd(const zl_causal_plan* p, const void* q, 
   fp.part_o = static_cast<float*>(workspace);
   fp.part_lse = fp.part_o + (int64_t)p->slots * 256 * p->head_dim;
   fp.scale_log2 = scale * 1.44269504088896340736f;
-  if (launch_causal_fwd(p->head_dim, tq, tk, tv, fp, (int)p->fwd_ptr.size() - 1, st) != cudaSuccess) return ZL_ERR_CUDA;
+  if (launch_causal_fwd(p->head_dim, tq, tk, tv, fp, (int)p->fwd_ptr.size() - 1, p->fwd_short, st) != cudaSuccess) return ZL_ERR_CUDA;
   if (p->merges.empty()) return ZL_OK;
   CausalMergeParams mp;
   mp.seqs = p->d_seqs;
@@ -184,7 +184,7 @@ extern "C" zl_status zl_causal_attn_bwd(const zl_causal_plan* p, const void* q, 
     bp.dv_stride = dv_stride;
     bp.scale = scale;
     bp.scale_log2 = scale * 1.44269504088896340736f;
-    if (launch_causal_bwd(d, tq, tk, tv, tdo, bp, (int)p->bwd_ptr.size() - 1, st) != cudaSuccess) return ZL_ERR_CUDA;
+    if (launch_causal_bwd(d, tq, tk, tv, tdo, bp, (int)p->bwd_ptr.size() - 1, p->bwd_short, st) != cudaSuccess) return ZL_ERR_CUDA;
   }
   CausalFinishParams fp;
   fp.seqs = p->d_seqs;

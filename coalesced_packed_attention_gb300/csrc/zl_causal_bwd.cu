@@ -39,6 +39,7 @@
 
 #include "zl_causal.h"
 #include "zl_internal.h"
+#include "zl_overlap.cuh"
 #include "zl_ptx.cuh"
 
 namespace zl {
@@ -183,7 +184,9 @@ __global__ void __launch_bounds__(512, 1)
   float* sLD = reinterpret_cast<float*>(smem + L::kLD);  // block parity b: LSE at 256 b, D at 256 b + 128
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  let_next_start();
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need a 1024-byte aligned base
+    wait_for_previous();
     if (threadIdx.x == 0) atomicCAS(p.status, 0, ZL_ERR_UNSUPPORTED);
     return;
   }
@@ -236,6 +239,7 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_previous();
   uint8_t* sK = smem + L::kK;
   uint8_t* sV = smem + L::kV;
   uint8_t* sQ = smem + L::kQ;
@@ -631,6 +635,8 @@ __global__ void __launch_bounds__(256) zl_causal_pre_kernel(const __nv_bfloat16*
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = 4;
   const int lane = threadIdx.x & 31, sub = lane / kLanes, piece = lane % kLanes;
   const int64_t nthreads = (int64_t)gridDim.x * blockDim.x;
+  let_next_start();
+  wait_for_previous();
   float4* z4 = reinterpret_cast<float4*>(acc);
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < acc4; i += nthreads)
     z4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -671,6 +677,8 @@ __global__ void __launch_bounds__(256) zl_causal_finish_kernel(const CausalFinis
   __shared__ float4 tile[128][17];
   const int group = p.n_q_heads / p.n_kv_heads, tb = tokens_per_block(group);
   const int64_t n_slabs = p.acc_blocks * kHalves;
+  let_next_start();
+  wait_for_previous();
   for (int64_t sl = blockIdx.x; sl < n_slabs; sl += gridDim.x) {
     const int64_t blk = sl / kHalves;
     const int half = (int)(sl % kHalves);
@@ -751,13 +759,12 @@ cudaError_t launch_causal_bwd_pre(int head_dim, const __nv_bfloat16* o, const __
   const int64_t by_rows = (rows + 8 * 4 * (256 / head_dim) - 1) / (8 * 4 * (256 / head_dim));
   const int64_t by_acc = (acc_floats / 4 + 255) / 256;
   static PerDeviceInt resident[2];
-  k<<<resident_grid(resident[head_dim == 128], k, by_rows > by_acc ? by_rows : by_acc, num_sms), 256, 0, stream>>>(o, d_o, row_d, rows, acc,
-                                                                                       acc_floats / 4);
-  return cudaGetLastError();
+  return launch_overlapped(k, resident_grid(resident[head_dim == 128], k, by_rows > by_acc ? by_rows : by_acc, num_sms), 256, 0,
+                           stream, o, d_o, row_d, rows, acc, acc_floats / 4);
 }
 
 cudaError_t launch_causal_bwd(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const CUtensorMap& tdo, const CausalBwdParams& p, int grid, cudaStream_t stream) {
+                              const CUtensorMap& tdo, const CausalBwdParams& p, int grid, bool early, cudaStream_t stream) {
   const int smem = head_dim == 128 ? CausalBwdLayout<128>::kBytes : CausalBwdLayout<64>::kBytes;
   const int smem_launch = smem > 120 * 1024 ? smem : 120 * 1024;  // one CTA per SM (TMEM 512 columns)
   auto k = head_dim == 128 ? zl_causal_bwd_kernel<128> : zl_causal_bwd_kernel<64>;
@@ -773,8 +780,7 @@ cudaError_t launch_causal_bwd(int head_dim, const CUtensorMap& tq, const CUtenso
     return fa.numRegs == (int)kLaunchRegs ? cudaSuccess : cudaErrorInvalidKernelImage;
   });
   if (e != cudaSuccess) return e;
-  k<<<grid, 512, smem_launch, stream>>>(tq, tk, tv, tdo, p);
-  return cudaGetLastError();
+  return launch_overlapped_if(early, k, grid, 512, smem_launch, stream, tq, tk, tv, tdo, p);
 }
 
 cudaError_t launch_causal_finish(int head_dim, const CausalFinishParams& p, int num_sms, cudaStream_t stream) {
@@ -782,8 +788,7 @@ cudaError_t launch_causal_finish(int head_dim, const CausalFinishParams& p, int 
   if (items == 0) return cudaSuccess;
   auto k = head_dim == 128 ? zl_causal_finish_kernel<128> : zl_causal_finish_kernel<64>;
   static PerDeviceInt resident[2];
-  k<<<resident_grid(resident[head_dim == 128], k, items, num_sms), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(k, resident_grid(resident[head_dim == 128], k, items, num_sms), 256, 0, stream, p);
 }
 
 }  // namespace zl

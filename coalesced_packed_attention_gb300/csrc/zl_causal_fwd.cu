@@ -34,6 +34,7 @@
 
 #include "zl_causal.h"
 #include "zl_internal.h"
+#include "zl_overlap.cuh"
 #include "zl_ptx.cuh"
 
 namespace zl {
@@ -149,7 +150,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  let_next_start();
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need a 1024-byte aligned base
+    wait_for_previous();
     if (threadIdx.x == 0) atomicCAS(p.status, 0, ZL_ERR_UNSUPPORTED);
     return;
   }
@@ -187,6 +190,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_previous();
   const long long lim = p.wait_limit;
   const int tb = tokens_per_block(p.group);
   const int t_begin = p.tile_ptr[blockIdx.x], t_end = p.tile_ptr[blockIdx.x + 1];
@@ -540,6 +544,8 @@ constexpr int kMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeRows) zl_causal_merge_kernel(const CausalMergeParams p) {
   constexpr int E = D / 32;
+  let_next_start();
+  wait_for_previous();
   const CausalMerge G = p.groups[blockIdx.x];
   const CausalSeq sq = p.seqs[G.seq];
   const int lane = threadIdx.x & 31, tb = tokens_per_block(p.group);
@@ -579,7 +585,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) zl_causal_merge_kernel(const 
 
 template <int D>
 cudaError_t launch_causal_fwd_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                   const CausalFwdParams& p, int grid, cudaStream_t stream) {
+                                   const CausalFwdParams& p, int grid, bool early, cudaStream_t stream) {
   using L = CausalFwdLayout<D>;
   const int smem = L::kBytes > 120 * 1024 ? L::kBytes : 120 * 1024;  // one CTA per SM (TMEM 512 columns)
   static PerDeviceOnce configured;
@@ -593,24 +599,22 @@ cudaError_t launch_causal_fwd_impl(const CUtensorMap& tq, const CUtensorMap& tk,
     return fa.numRegs == (int)kFwdLaunchRegs ? cudaSuccess : cudaErrorInvalidKernelImage;
   });
   if (e != cudaSuccess) return e;
-  zl_causal_fwd_kernel<D><<<grid, kFwdThreads, smem, stream>>>(tq, tk, tv, p);
-  return cudaGetLastError();
+  return launch_overlapped_if(early, zl_causal_fwd_kernel<D>, grid, kFwdThreads, smem, stream, tq, tk, tv, p);
 }
 
 }  // namespace
 
 cudaError_t launch_causal_fwd(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const CausalFwdParams& p, int grid, cudaStream_t stream) {
-  return head_dim == 128 ? launch_causal_fwd_impl<128>(tq, tk, tv, p, grid, stream)
-                         : launch_causal_fwd_impl<64>(tq, tk, tv, p, grid, stream);
+                              const CausalFwdParams& p, int grid, bool early, cudaStream_t stream) {
+  return head_dim == 128 ? launch_causal_fwd_impl<128>(tq, tk, tv, p, grid, early, stream)
+                         : launch_causal_fwd_impl<64>(tq, tk, tv, p, grid, early, stream);
 }
 
 cudaError_t launch_causal_merge(int head_dim, const CausalMergeParams& p, cudaStream_t stream) {
   if (p.n_groups == 0) return cudaSuccess;
   const dim3 grid(p.n_groups, (p.rows + kMergeRows - 1) / kMergeRows);
-  if (head_dim == 128) zl_causal_merge_kernel<128><<<grid, 32 * kMergeRows, 0, stream>>>(p);
-  else zl_causal_merge_kernel<64><<<grid, 32 * kMergeRows, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(head_dim == 128 ? zl_causal_merge_kernel<128> : zl_causal_merge_kernel<64>, grid,
+                           32 * kMergeRows, 0, stream, p);
 }
 
 }  // namespace zl

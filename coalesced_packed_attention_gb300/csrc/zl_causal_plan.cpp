@@ -20,6 +20,8 @@ constexpr double kStep1 = 1.0, kStep2 = 1.2, kTileFixed = 1.5, kPartFixed = 1.0,
 // Backward: a query block of a key tile is the unit (about 2 us); a tile's start and end (K, V load, first products, dK,
 // dV output), a part's fp32 output and its share of the sum, which the last launch does on its way.
 constexpr double kBwdTileFixed = 2.0, kBwdPartFixed = 1.0, kBwdMergeFixed = 1.0;
+// Schedules under some 100 us, in those units (see launch_overlapped_if).
+constexpr double kShortFwd = 80.0, kShortBwd = 50.0;
 // Longest tiles first balances best, but it spreads the blocks over every (sequence, head), and the tiles of one share
 // what they read: keys and values forward; queries, dO and the dQ accumulator backward.  Where that does not stay in
 // L2 (129 MB) and there are more (sequence, head) pairs than a handful of blocks each can share, the
@@ -157,7 +159,7 @@ void build_forward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool r
       cost.push_back(cost_of(u, hi - lo, k > 1));
     }
   }
-  schedule(&p->fwd_tiles, cost, resident, p->num_sms, &p->fwd_ptr);
+  p->fwd_short = schedule(&p->fwd_tiles, cost, resident, p->num_sms, &p->fwd_ptr) < kShortFwd;
 }
 
 struct BwdItem {
@@ -194,7 +196,7 @@ void build_backward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool 
       cost.push_back(cost_of(u, hi - lo, k > 1));
     }
   }
-  schedule(&p->bwd_tiles, cost, resident, p->num_sms, &p->bwd_ptr);
+  p->bwd_short = schedule(&p->bwd_tiles, cost, resident, p->num_sms, &p->bwd_ptr) < kShortBwd;
 }
 
 template <typename T>

@@ -29,6 +29,7 @@
 
 #include "zl_causal.h"
 #include "zl_internal.h"
+#include "zl_overlap.cuh"
 #include "zl_ptx.cuh"
 
 namespace zl {
@@ -50,7 +51,8 @@ struct RopeParams {
   RopeTensor t[2];  // queries, keys
   const int32_t* positions;
   const uint64_t* freq;
-  float* partial;  // weight gradients per block, [blocks][2 d]
+  float* partial;  // weight gradients per block, [blocks][2 d]; null: not wanted, or of the only block and so final:
+  float *dwq, *dwk;
   int64_t n_tokens;
   int32_t rot, n_axes, axis1, axis2;  // first pair of the second and the third axis
   int32_t chunk;                      // batches of one token that one warp takes
@@ -115,6 +117,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
   const bool lower = gl < hop;
   const int plane = kHalf && turns ? (lower ? lane + hop : lane - hop) : lane;
   const int pe0 = kHalf ? (plane % kLanes) * 8 : e0;  // first channel of the partner values
+  let_next_start();
+  wait_for_previous();
   // the pairs whose sines this lane forms, and the lane that forms the first of those that it uses
   const int pairs = p.rot / 2, my_pair = 2 * lane;
   const int src = (kHalf ? (lower ? e0 : e0 - pairs) : e0 / 2) / 2;
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
     }
   }
   if constexpr (kDw) {
-    if (p.partial) {
+    if (p.partial || p.dwq || p.dwk) {
       __syncthreads();  // the weights in red[0] have been read
       float* row = red[(threadIdx.x >> 5) * kRows + sub];
 #pragma unroll
@@ -292,7 +296,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
       if (threadIdx.x < 2 * D) {
         float v = 0.f;
         for (int r = 0; r < kRopeThreads / 32 * kRows; ++r) v += red[r][threadIdx.x];
-        p.partial[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (2 * D) + threadIdx.x] = v;
+        if (p.partial) p.partial[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (2 * D) + threadIdx.x] = v;
+        else if (threadIdx.x < D) { if (p.dwq) p.dwq[threadIdx.x] = v; }
+        else if (p.dwk) p.dwk[threadIdx.x - D] = v;
       }
     }
   }
@@ -304,6 +310,8 @@ __global__ void __launch_bounds__(1024) zl_qk_rope_dw_kernel(const float* __rest
   __shared__ float red[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + x;
+  let_next_start();
+  wait_for_previous();
   float v = 0.f;
 #pragma unroll 4
   for (int r = y; r < rows; r += 32) v += __ldg(partial + (int64_t)r * (2 * d) + col);
@@ -391,6 +399,13 @@ cudaError_t launch_rope(const zl_qk_rope_desc& d, bool bwd, int sms, RopeParams&
   const int64_t warps = (int64_t)sms * per_sm * (kRopeThreads / 32);
   const int batches = p.t[0].batches + p.t[1].batches;
   int64_t chunks = warps / d.n_tokens;
+  // weight gradients of a block's worth of tokens: one block and no second launch (3 us against 2 + 2)
+  if (p.partial && d.n_tokens <= kRopeThreads / 32) {
+    chunks = 1;
+    p.partial = nullptr;
+    p.dwq = dwq;
+    p.dwk = dwk;
+  }
   if (chunks > batches) chunks = batches;
   if (p.partial && chunks > kMaxDwBlocks) chunks = kMaxDwBlocks;
   if (chunks < 1) chunks = 1;
@@ -401,11 +416,9 @@ cudaError_t launch_rope(const zl_qk_rope_desc& d, bool bwd, int sms, RopeParams&
   if (nx > cap) nx = cap;
   if (p.partial && nx * ny > kMaxDwBlocks) nx = kMaxDwBlocks / ny;
   if (nx < 1) nx = 1;
-  k<<<dim3((unsigned)nx, (unsigned)ny), kRopeThreads, 0, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_overlapped(k, dim3((unsigned)nx, (unsigned)ny), kRopeThreads, 0, stream, p);
   if (e != cudaSuccess || !p.partial) return e;
-  zl_qk_rope_dw_kernel<<<2 * D / 32, 1024, 0, stream>>>(p.partial, (int32_t)(nx * ny), D, dwq, dwk);
-  return cudaGetLastError();
+  return launch_overlapped(zl_qk_rope_dw_kernel, 2 * D / 32, 1024, 0, stream, p.partial, (int32_t)(nx * ny), D, dwq, dwk);
 }
 
 // SM count of the current device; the kernels are built for sm_103a alone.

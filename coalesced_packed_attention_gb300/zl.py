@@ -429,7 +429,7 @@ def _torch():
 def _heads(t, what, shape, dev):
     """(pointer, token stride) of a bf16 [tokens, heads, d] tensor on CUDA device `dev` whose heads are
     contiguous; the token stride is free, so views of a fused projection pass."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
         raise TypeError(f"{what}: expected a CUDA tensor of {torch.bfloat16}, got {getattr(t, 'dtype', type(t))}")
     if t.get_device() != dev:
@@ -519,6 +519,8 @@ class RotaryTable:
     half: bool
     axis_pairs: List[int]
     amplitude: float
+    device: int = -1            # CUDA device of freq
+    ptr: Optional[int] = None   # and its address there
     last: tuple = (None, None)  # the last call's descriptor, by its key
 
 
@@ -538,7 +540,7 @@ def rotary_table(inv_freq: Sequence[float], layout: str = "half", axis_pairs: Op
     out = (ctypes.c_uint64 * max(1, n))()
     _check(load_library().zl_rope_frequencies((ctypes.c_double * max(1, n))(*radians), n, out), "zl_rope_frequencies")
     freq = torch.tensor([ctypes.c_int64(x).value for x in out[:n]], dtype=torch.int64).to(device)
-    return RotaryTable(freq, 2 * n, layout == "half", pairs, float(amplitude))
+    return RotaryTable(freq, 2 * n, layout == "half", pairs, float(amplitude), freq.get_device(), freq.data_ptr())
 
 
 def zl_qk_rope_workspace_bytes(n_tokens: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -574,7 +576,9 @@ def _rope_args(q, k, positions, table, norm, eps, q_weight, k_weight):
         axes = len(table.axis_pairs)
         pos = _dense(positions, "positions", torch.int32,
                      (n,) if axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1 else (n, axes), dev)
-        freq = _dense(table.freq, "table", torch.int64, (table.rot_dim // 2,), dev)
+        freq = table.ptr
+        if table.device != dev:
+            raise ValueError(f"table on device {table.device}, current device is cuda:{dev}")
     key = (n, hq, hk, d, norm, eps)
     last = table.last
     if last[0] != key:
