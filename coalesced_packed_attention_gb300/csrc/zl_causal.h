@@ -111,7 +111,7 @@ struct CausalBwdParams {
   const float* lse;
   const float* row_d;  // D, [q tokens][q heads]
   float* acc;          // fp32 dQ accumulator, [block][d / 4][128][4]
-  float* part;         // [slot][dV, dK][128][d], fp32, dK not yet scaled
+  float* part;         // [slot][dV, dK][d / 4][128][4], fp32, dK not yet scaled
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
   int64_t dk_stride, dv_stride;

@@ -577,40 +577,55 @@ __global__ void __launch_bounds__(512, 1)
         ++ntiles;
         tc_fence_after();
       }
+      // Final values leave as bf16 through this warp's own 4 KB of the dS^T buffer (free: kv_done), so that a store
+      // writes whole rows' pieces; a part's fp32 values go to the workspace as [column group][128 keys][4], 512 bytes a
+      // store.  (A thread's own row, 16 bytes a store, kept the load/store unit busy for 2 to 4 us a tile.)
+      constexpr int kPieces = kHalfD / 8, kPerStep = 32 / kPieces;
+      const uint32_t buf = smem_u32(sDS) + wg * L::kBox + (warp & 3) * 4096;
+      // the lane, read again: addresses formed from the one above would be held through the loop over blocks
+      int ln;
+      asm volatile("mov.u32 %0, %%laneid;" : "=r"(ln));
+#pragma unroll 1
+      for (int m = 0; m < 2; ++m) {  // dV, dK
+        const float scale = m ? p.scale : 1.f;
 #pragma unroll
-      for (int c = 0; c < kHalfD / 32; ++c) {
-        uint32_t uv[32], uk[32];
-        if (sp.n > 0) {
-          tmem_ld32(tmem + lane_base + 256 + dc0 + 32 * c, uv);
-          tmem_ld32(tmem + lane_base + 384 + dc0 + 32 * c, uk);
-          tmem_ld_wait();
-        } else {  // no query: the keys' gradients are empty sums
+        for (int c = 0; c < kHalfD / 32; ++c) {
+          uint32_t u[32];
+          if (sp.n > 0) {
+            tmem_ld32(tmem + lane_base + 256 + 128 * m + dc0 + 32 * c, u);
+            tmem_ld_wait();
+          } else {  // no query: the keys' gradients are empty sums
 #pragma unroll
-          for (int e = 0; e < 32; ++e) uv[e] = uk[e] = 0u;
+            for (int e = 0; e < 32; ++e) u[e] = 0u;
+          }
+          if (tl.part >= 0) {  // summed, scaled and rounded by the last launch
+            uint4* dst = reinterpret_cast<uint4*>(p.part) + ((int64_t)tl.part * 2 + m) * (32 * D) + (dc0 / 4 + 8 * c) * 128 + t_key;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i * 128] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+          } else {
+            auto f = [&](int e) { return __uint_as_float(u[e]) * scale; };
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sts_v4(buf + ln * 128 + (((4 * c + i) ^ (ln & 7)) << 4), pack_bf16(f(8 * i), f(8 * i + 1)),
+                     pack_bf16(f(8 * i + 2), f(8 * i + 3)), pack_bf16(f(8 * i + 4), f(8 * i + 5)),
+                     pack_bf16(f(8 * i + 6), f(8 * i + 7)));
+          }
         }
-        if (tl.part >= 0) {  // a part of the tile's queries: summed, scaled and rounded by the last launch
-          float4* pv = reinterpret_cast<float4*>(p.part + ((int64_t)tl.part * 256 + t_key) * D + dc0 + 32 * c);
-          float4* pk = pv + 128 * D / 4;
-          auto f = [](uint32_t x) { return __uint_as_float(x); };
+        if (tl.part < 0) {
+          __syncwarp();
+          __nv_bfloat16* base = (m ? p.dk : p.dv) + (int64_t)tl.head * D + dc0 + (ln % kPieces) * 8;
+          const int64_t stride = m ? p.dk_stride : p.dv_stride;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            pv[i] = make_float4(f(uv[4 * i]), f(uv[4 * i + 1]), f(uv[4 * i + 2]), f(uv[4 * i + 3]));
-            pk[i] = make_float4(f(uk[4 * i]), f(uk[4 * i + 1]), f(uk[4 * i + 2]), f(uk[4 * i + 3]));
+          for (int i = 0; i < 32 / kPerStep; ++i) {
+            const int x = i * kPerStep + ln / kPieces, k = tl.block * 128 + (warp & 3) * 32 + x;
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(buf + x * 128 + (((ln % kPieces) ^ (x & 7)) << 4))
+                         : "memory");
+            if (k < tl.kv_len) *reinterpret_cast<uint4*>(base + ((int64_t)tl.kv_row + k) * stride) = v;
           }
-        } else if (key_ok) {
-          const int64_t row = (int64_t)tl.kv_row + key, col = (int64_t)tl.head * D + dc0 + 32 * c;
-          uint4* dv4 = reinterpret_cast<uint4*>(p.dv + row * p.dv_stride + col);
-          uint4* dk4 = reinterpret_cast<uint4*>(p.dk + row * p.dk_stride + col);
-          auto f = [](uint32_t x) { return __uint_as_float(x); };
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dv4[i] = make_uint4(pack_bf16(f(uv[8 * i]), f(uv[8 * i + 1])), pack_bf16(f(uv[8 * i + 2]), f(uv[8 * i + 3])),
-                                pack_bf16(f(uv[8 * i + 4]), f(uv[8 * i + 5])), pack_bf16(f(uv[8 * i + 6]), f(uv[8 * i + 7])));
-            dk4[i] = make_uint4(pack_bf16(f(uk[8 * i]) * p.scale, f(uk[8 * i + 1]) * p.scale),
-                                pack_bf16(f(uk[8 * i + 2]) * p.scale, f(uk[8 * i + 3]) * p.scale),
-                                pack_bf16(f(uk[8 * i + 4]) * p.scale, f(uk[8 * i + 5]) * p.scale),
-                                pack_bf16(f(uk[8 * i + 6]) * p.scale, f(uk[8 * i + 7]) * p.scale));
-          }
+          __syncwarp();
         }
       }
       tc_fence_before();
@@ -716,29 +731,36 @@ __global__ void __launch_bounds__(256) zl_causal_finish_kernel(const CausalFinis
     }
     __syncthreads();
   }
-  // the first item behind the slabs that is this block's: a split key tile's dV or dK, kRows of its 128 rows, a
-  // 16-byte piece of the result per thread
-  constexpr int kPieces = D / 8, kRows = 256 / kPieces, kItems = 128 / kRows;
+  // the first item behind the slabs that is this block's: 32 channels of a split key tile's dV or dK, a thread for
+  // half of them of one key
+  constexpr int kItems = D / 32;
   int64_t it = blockIdx.x;
   if (it < n_slabs) it += (n_slabs - it + gridDim.x - 1) / gridDim.x * gridDim.x;
   for (it -= n_slabs; it < 2 * kItems * (int64_t)p.n_merges; it += gridDim.x) {
     const CausalBwdMerge m = p.merges[it / (2 * kItems)];
-    const int of_k = (int)(it / kItems & 1), r = (int)(it % kItems) * kRows + threadIdx.x / kPieces, c = threadIdx.x % kPieces;
+    const int of_k = (int)(it / kItems & 1), r = threadIdx.x & 127, g = (int)(it % kItems) * 8 + (threadIdx.x >> 7) * 4;
     const int key = m.block * 128 + r;
     if (key >= m.kv_len) continue;
-    const float4* src = reinterpret_cast<const float4*>(p.part) + ((int64_t)m.slot * 2 + of_k) * (128 * D / 4) + r * (D / 4) + 2 * c;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
-#pragma unroll 4
+    const float4* src = reinterpret_cast<const float4*>(p.part) + ((int64_t)m.slot * 2 + of_k) * (32 * D) + g * 128 + r;
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
     for (int q = 0; q < m.parts; ++q) {
-      const float4 a = __ldg(src + (int64_t)q * (2 * 128 * D / 4)), b = __ldg(src + (int64_t)q * (2 * 128 * D / 4) + 1);
-      v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
-      w.x += b.x; w.y += b.y; w.z += b.z; w.w += b.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 a = __ldg(src + (int64_t)q * (2 * 32 * D) + i * 128);
+        v[i].x += a.x; v[i].y += a.y; v[i].z += a.z; v[i].w += a.w;
+      }
     }
     const float scale = of_k ? p.scale : 1.f;
-    *reinterpret_cast<uint4*>((of_k ? p.dk : p.dv) + ((int64_t)m.kv_row + key) * (of_k ? p.dk_stride : p.dv_stride) +
-                              (int64_t)m.head * D + 8 * c) =
-        make_uint4(pack_bf16(v.x * scale, v.y * scale), pack_bf16(v.z * scale, v.w * scale),
-                   pack_bf16(w.x * scale, w.y * scale), pack_bf16(w.z * scale, w.w * scale));
+    uint4* out = reinterpret_cast<uint4*>((of_k ? p.dk : p.dv) + ((int64_t)m.kv_row + key) * (of_k ? p.dk_stride : p.dv_stride) +
+                                          (int64_t)m.head * D + 4 * g);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      out[i] = make_uint4(pack_bf16(v[2 * i].x * scale, v[2 * i].y * scale), pack_bf16(v[2 * i].z * scale, v[2 * i].w * scale),
+                          pack_bf16(v[2 * i + 1].x * scale, v[2 * i + 1].y * scale),
+                          pack_bf16(v[2 * i + 1].z * scale, v[2 * i + 1].w * scale));
   }
 }
 
@@ -784,7 +806,7 @@ cudaError_t launch_causal_bwd(int head_dim, const CUtensorMap& tq, const CUtenso
 }
 
 cudaError_t launch_causal_finish(int head_dim, const CausalFinishParams& p, int num_sms, cudaStream_t stream) {
-  const int64_t items = p.acc_blocks * (head_dim / 64) + 2 * (head_dim / 16) * (int64_t)p.n_merges;
+  const int64_t items = p.acc_blocks * (head_dim / 64) + 2 * (head_dim / 32) * (int64_t)p.n_merges;
   if (items == 0) return cudaSuccess;
   auto k = head_dim == 128 ? zl_causal_finish_kernel<128> : zl_causal_finish_kernel<64>;
   static PerDeviceInt resident[2];
