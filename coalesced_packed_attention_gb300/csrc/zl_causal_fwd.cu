@@ -177,6 +177,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  // the plan's tables are written once, before any launch: they need not wait for the kernel before this one
+  const int t_begin = p.tile_ptr[blockIdx.x], t_end = p.tile_ptr[blockIdx.x + 1];
+  touch(p.tiles + t_begin);
   if (warp == 12 && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
@@ -193,7 +196,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   wait_for_previous();
   const long long lim = p.wait_limit;
   const int tb = tokens_per_block(p.group);
-  const int t_begin = p.tile_ptr[blockIdx.x], t_end = p.tile_ptr[blockIdx.x + 1];
 
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFwdIssueRegs));

@@ -1,5 +1,6 @@
 // Launches that may be set up while the kernel before them in the stream still runs (programmatic dependent
-// launch).  A kernel launched this way may start early, and touches no global memory before wait_for_previous(), which
+// launch).  A kernel launched this way may start early, and touches no global memory but a plan's own tables before
+// wait_for_previous(), which
 // returns once every earlier kernel of the stream has finished and its writes are visible; each of its threads passes
 // that wait before it ends, so the order is handed on to the kernel after it.  What is saved is the launch latency and
 // the set-up of barriers and tensor memory: 2 us of a kernel behind another.  Kernels, copies and events of other
