@@ -69,8 +69,8 @@ struct alignas(16) CausalBwdTile {
   int32_t seq, pad;
 };
 // Rows whose key range was split: the combine of `parts` slots from `slot` on.
-struct CausalMerge {
-  int32_t seq, head, block, slot, parts, pad[3];
+struct alignas(16) CausalMerge {
+  int32_t q_row, q_len, head, block, slot, parts, pad[2];
 };
 // Key tiles whose query range was split: the sum of `parts` slots of dK, dV from `slot` on.
 struct CausalBwdMerge {
@@ -86,13 +86,12 @@ struct CausalFwdParams {
   int32_t n_q_heads, group;
   __nv_bfloat16* o;
   float* lse;
-  float* part_o;    // [slot][256][d]
+  float* part_o;    // [slot][sub-tile][d / 4][128][4]
   float* part_lse;  // [slot][256]
   float scale_log2;
 };
 
 struct CausalMergeParams {
-  const CausalSeq* seqs;
   const CausalMerge* groups;
   int32_t n_groups, rows, n_q_heads, group;  // rows: the most that a split tile has, of its 256
   const float* part_o;
@@ -150,7 +149,8 @@ struct zl_causal_plan {
   int64_t q_tokens = 0, kv_tokens = 0;
   int device = -1, num_sms = 0;
   bool host_only = false, test_withhold = false;
-  bool shared_keys = false;  // two sequences read the same key rows: no backward
+  bool shared_keys = false;   // two sequences read the same key rows: no backward
+  bool forward_only = false;  // ZL_PLAN_FORWARD_ONLY
 
   std::vector<zl::CausalSeq> seqs;
   std::vector<zl::CausalTile> fwd_tiles;

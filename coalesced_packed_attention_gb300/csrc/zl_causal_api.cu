@@ -118,7 +118,6 @@ extern "C" zl_status zl_causal_attn_fwd(const zl_causal_plan* p, const void* q, 
   if (launch_causal_fwd(p->head_dim, tq, tk, tv, fp, (int)p->fwd_ptr.size() - 1, p->fwd_short, st) != cudaSuccess) return ZL_ERR_CUDA;
   if (p->merges.empty()) return ZL_OK;
   CausalMergeParams mp;
-  mp.seqs = p->d_seqs;
   mp.groups = p->d_merges;
   mp.n_groups = (int32_t)p->merges.size();
   mp.rows = p->merge_rows;
@@ -137,7 +136,7 @@ extern "C" zl_status zl_causal_attn_bwd(const zl_causal_plan* p, const void* q, 
                                         int64_t dk_stride, void* dv, int64_t dv_stride, void* workspace, float scale,
                                         void* stream) {
   NvtxRange range("zl_causal_attn_bwd");
-  if (!ready(p) || p->shared_keys) return ZL_ERR_INVALID_ARG;
+  if (!ready(p) || p->shared_keys || p->forward_only) return ZL_ERR_INVALID_ARG;
   zl_status s = check_inputs(p, q, q_stride, k, k_stride, v, v_stride, scale);
   if (s != ZL_OK) return s;
   const int32_t d = p->head_dim;

@@ -395,10 +395,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(lane, 4 * c + i)), "r"(pack_bf16(f[0], f[1])),
                            "r"(pack_bf16(f[2], f[3])), "r"(pack_bf16(f[4], f[5])), "r"(pack_bf16(f[6], f[7]))
                            : "memory");
-            } else if (row_ok) {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c + 8 * i);
+            } else if (row_ok) {  // [column group][128 rows][4]: a store writes 512 bytes in a row
+              float4* dst = reinterpret_cast<float4*>(p.part_o) + ((int64_t)tl.part * 2 + w) * (32 * D) + (8 * c + 2 * i) * 128 + r;
               dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-              dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+              dst[128] = make_float4(f[4], f[5], f[6], f[7]);
             }
           }
         }
@@ -539,50 +539,77 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 }
 
-// Combine of a tile's parts: LSE = M + ln sum_c exp(LSE_c - M), O = sum_c exp(LSE_c - LSE) O_c.  One warp per row,
-// kMergeRows rows of a split tile a block, d / 32 channels per lane; parts are added in key order.  (A block per tile,
-// its warps going through 256 rows, took 100 us where prompts are split.)
-constexpr int kMergeRows = 4;
-template <int D>
-__global__ void __launch_bounds__(32 * kMergeRows) zl_causal_merge_kernel(const CausalMergeParams p) {
-  constexpr int E = D / 32;
+// Combine of a tile's parts: LSE = M + ln sum_c exp(LSE_c - M), O = sum_c exp(LSE_c - LSE) O_c.  A block takes 32
+// channels of a sub-tile of one split tile, a thread for each row: the parts' rows lie side by side, so that a
+// load reads 512 bytes in a row.  The next part's values are on their way while one is added.  Where no split tile has
+// over 32 rows (single tokens: many parts, few rows) the four warps take every fourth part of the same rows and the
+// sums are joined in shared memory.  Every order is fixed.
+template <int D, bool kFew>
+__global__ void __launch_bounds__(128) zl_causal_merge_kernel(const CausalMergeParams p) {
+  constexpr int kWays = kFew ? 4 : 1;
   let_next_start();
   wait_for_previous();
   const CausalMerge G = p.groups[blockIdx.x];
-  const CausalSeq sq = p.seqs[G.seq];
-  const int lane = threadIdx.x & 31, tb = tokens_per_block(p.group);
-  {
-    const int r = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
-    const int rr = r & 127, rt = rr / p.group;
-    const int tok = (G.block + (r >> 7)) * tb + rt;
-    if (rt >= tb || tok >= sq.q_len) return;  // warp-uniform
-    const float* pl = p.part_lse + (int64_t)G.slot * 256 + r;
-    float m = kNegInf;
-    for (int c = lane; c < G.parts; c += 32) m = fmaxf(m, pl[(int64_t)c * 256]);
+  const int r = kFew ? threadIdx.x & 31 : threadIdx.x, way = kFew ? threadIdx.x >> 5 : 0, w = blockIdx.z, c0 = blockIdx.y * 32;
+  const int tb = tokens_per_block(p.group), rt = r / p.group, tok = (G.block + w) * tb + rt;
+  const bool there = rt < tb && tok < G.q_len;
+  float acc[32];
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-    const float base = m == kNegInf ? 0.f : m;
-    float tot = 0.f;
-    for (int c = lane; c < G.parts; c += 32) tot += expf(pl[(int64_t)c * 256] - base);
+  for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+  float base = 0.f, tot = 0.f;
+  if (there) {
+    const float* pl = p.part_lse + (int64_t)G.slot * 256 + 128 * w + r;
+    const float4* po = reinterpret_cast<const float4*>(p.part_o) + ((int64_t)G.slot * 2 + w) * (32 * D) + (c0 / 4) * 128 + r;
+    float4 x[8];
+    if (way < G.parts) {
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, s);
-    const float inv = tot == 0.f ? 0.f : 1.f / tot;
-    float acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    const float* po = p.part_o + ((int64_t)G.slot * 256 + r) * D + lane * E;
-#pragma unroll 4
-    for (int c = 0; c < G.parts; ++c) {
-      const float wc = expf(pl[(int64_t)c * 256] - base) * inv;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(wc, po[(int64_t)c * 256 * D + e], acc[e]);
+      for (int i = 0; i < 8; ++i) x[i] = __ldg(po + (int64_t)way * (2 * 32 * D) + i * 128);
     }
-    const int64_t row = (sq.q_offset + tok) * p.n_q_heads + (int64_t)G.head * p.group + (rr - rt * p.group);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * E);
+    float m = kNegInf;
+#pragma unroll 8
+    for (int c = 0; c < G.parts; ++c) m = fmaxf(m, __ldg(pl + (int64_t)c * 256));
+    base = m == kNegInf ? 0.f : m;
+#pragma unroll 8
+    for (int c = 0; c < G.parts; ++c) tot += expf(__ldg(pl + (int64_t)c * 256) - base);
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;
+    for (int c = way; c < G.parts; c += kWays) {
+      const float wc = expf(__ldg(pl + (int64_t)c * 256) - base) * inv;
+      float4 y[8];
+      if (c + kWays < G.parts) {
 #pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e], acc[e + 1]);
-    if (lane == 0) p.lse[row] = tot == 0.f ? kNegInf : base + logf(tot);
+        for (int i = 0; i < 8; ++i) y[i] = __ldg(po + (int64_t)(c + kWays) * (2 * 32 * D) + i * 128);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[4 * i] = fmaf(wc, x[i].x, acc[4 * i]);
+        acc[4 * i + 1] = fmaf(wc, x[i].y, acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(wc, x[i].z, acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(wc, x[i].w, acc[4 * i + 3]);
+        x[i] = y[i];
+      }
+    }
   }
+  if constexpr (kFew) {
+    __shared__ float sums[kWays - 1][32][33];
+    if (way > 0) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) sums[way - 1][e][r] = acc[e];
+    }
+    __syncthreads();
+    if (way > 0) return;
+#pragma unroll
+    for (int v = 0; v < kWays - 1; ++v)
+#pragma unroll
+      for (int e = 0; e < 32; ++e) acc[e] += sums[v][e][r];
+  }
+  if (!there) return;
+  const int64_t row = ((int64_t)G.q_row + tok) * p.n_q_heads + (int64_t)G.head * p.group + (r - rt * p.group);
+  uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + c0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    dst[i] = make_uint4(pack_bf16(acc[8 * i], acc[8 * i + 1]), pack_bf16(acc[8 * i + 2], acc[8 * i + 3]),
+                        pack_bf16(acc[8 * i + 4], acc[8 * i + 5]), pack_bf16(acc[8 * i + 6], acc[8 * i + 7]));
+  if (blockIdx.y == 0) p.lse[row] = tot == 0.f ? kNegInf : base + logf(tot);
 }
 
 template <int D>
@@ -614,9 +641,11 @@ cudaError_t launch_causal_fwd(int head_dim, const CUtensorMap& tq, const CUtenso
 
 cudaError_t launch_causal_merge(int head_dim, const CausalMergeParams& p, cudaStream_t stream) {
   if (p.n_groups == 0) return cudaSuccess;
-  const dim3 grid(p.n_groups, (p.rows + kMergeRows - 1) / kMergeRows);
-  return launch_overlapped(head_dim == 128 ? zl_causal_merge_kernel<128> : zl_causal_merge_kernel<64>, grid,
-                           32 * kMergeRows, 0, stream, p);
+  const dim3 grid(p.n_groups, head_dim / 32, p.rows > kCausalRows ? 2 : 1);
+  const bool few = p.rows <= 32;
+  auto k = head_dim == 128 ? (few ? zl_causal_merge_kernel<128, true> : zl_causal_merge_kernel<128, false>)
+                           : (few ? zl_causal_merge_kernel<64, true> : zl_causal_merge_kernel<64, false>);
+  return launch_overlapped(k, grid, 128, 0, stream, p);
 }
 
 }  // namespace zl

@@ -5,7 +5,7 @@
 #include <algorithm>
 #include <cstring>
 #include <new>
-#include <queue>
+#include <utility>
 
 #include "zl_causal.h"
 #include "zl_internal.h"
@@ -14,14 +14,18 @@ using namespace zl;
 
 namespace {
 
-// Costs of the forward schedule in units of one 128-key step of a lone sub-tile (about 1.3 us): a step of two
-// sub-tiles, a tile's start and end (Q load, first scores, epilogue), a part's fp32 output, and the merge's launch.
-constexpr double kStep1 = 1.0, kStep2 = 1.2, kTileFixed = 1.5, kPartFixed = 1.0, kMergeFixed = 3.0;
-// Backward: a query block of a key tile is the unit (about 2 us); a tile's start and end (K, V load, first products, dK,
-// dV output), a part's fp32 output and its share of the sum, which the last launch does on its way.
-constexpr double kBwdTileFixed = 2.0, kBwdPartFixed = 1.0, kBwdMergeFixed = 1.0;
-// Schedules under some 100 us, in those units (see launch_overlapped_if).
-constexpr double kShortFwd = 80.0, kShortBwd = 50.0;
+// What a schedule is weighed by, in microseconds as measured on one GB300 (kernels of a few tiles a thread block):
+// a step (forward: 128 keys of one or of two sub-tiles; backward: a query block of a key tile), a tile's start and
+// end, a part's fp32 output, and for the sum of the parts a launch (forward; the backward's last launch is there
+// anyway) and their bytes, written and read again at some 2.4 TB/s in all.
+struct Rates {
+  double step1, step2, fixed, part, merge, part_bytes;
+};
+Rates fwd_rates(int d) { return d == 128 ? Rates{1.4, 1.5, 2.0, 0.7, 3.5, 256.0 * 128 * 4} : Rates{1.15, 1.35, 1.8, 0.5, 3.5, 256.0 * 64 * 4}; }
+Rates bwd_rates(int d) { return d == 128 ? Rates{2.15, 2.15, 4.5, 1.0, 0.5, 256.0 * 128 * 4} : Rates{1.75, 1.75, 4.0, 0.7, 0.5, 256.0 * 64 * 4}; }
+constexpr double kPartBytesPerUs = 2.4e6;  // of the parts, written and then read
+// A launch shorter than this is set up early (see launch_overlapped_if).
+constexpr double kShortUs = 100.0;
 // Longest tiles first balances best, but it spreads the blocks over every (sequence, head), and the tiles of one share
 // what they read: keys and values forward; queries, dO and the dQ accumulator backward.  Where that does not stay in
 // L2 (129 MB) and there are more (sequence, head) pairs than a handful of blocks each can share, the
@@ -31,46 +35,183 @@ constexpr int64_t kFewPairs = 16;
 
 size_t align_up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-struct Load {
-  double load;
-  int32_t bin;
-  bool operator>(const Load& o) const { return load > o.load || (load == o.load && bin > o.bin); }
+// Pieces of the items (query blocks forward, key tiles backward) in the order and on the thread blocks that run
+// them: units [lo, hi) of an item's n.
+struct Piece {
+  int32_t item, lo, hi, bin;
+  bool cut;  // one of several of its item
 };
 
-// Greedy list schedule: each tile in turn to the block that is free first.  Returns the makespan; bin_of may be null.
-double list_schedule(const std::vector<double>& cost, const std::vector<int32_t>& order, int bins,
-                     std::vector<int32_t>* bin_of) {
-  std::priority_queue<Load, std::vector<Load>, std::greater<Load>> free_at;
-  for (int b = 0; b < bins; ++b) free_at.push({0.0, b});
-  double makespan = 0.0;
-  for (int32_t i : order) {
-    Load l = free_at.top();
-    free_at.pop();
-    if (bin_of) (*bin_of)[i] = l.bin;
-    l.load += cost[i];
-    makespan = std::max(makespan, l.load);
-    free_at.push(l);
+// Thread blocks by load, the least loaded (then the lowest) first: a binary heap of which only the top ever grows.
+struct LeastLoaded {
+  std::vector<std::pair<double, int32_t>> heap;
+  explicit LeastLoaded(int n) {
+    for (int b = 0; b < n; ++b) heap.push_back({0.0, b});
   }
+  // Adds to the top block's load; returns the block and its load.
+  std::pair<double, int32_t> add(double cost) {
+    std::pair<double, int32_t> top = heap[0];
+    top.first += cost;
+    size_t i = 0;
+    for (;;) {
+      size_t c = 2 * i + 1;
+      if (c >= heap.size()) break;
+      if (c + 1 < heap.size() && heap[c + 1] < heap[c]) ++c;
+      if (!(heap[c] < top)) break;
+      heap[i] = heap[c];
+      i = c;
+    }
+    heap[i] = top;
+    return top;
+  }
+};
+
+// Costs of a schedule in microseconds: a piece of n units of item i takes fixed + n * step(i), and `part` more if its
+// item is cut; rows(i) of the 256 rows of a part are there.
+template <typename Item, typename Step, typename Rows>
+struct Costs {
+  const std::vector<Item>& items;
+  Rates r;
+  Step step;
+  Rows rows;
+  double of(int32_t i, int n, bool cut) const { return r.fixed + n * step(items[i]) + (cut ? r.part : 0.0); }
+  // what the parts cost beside the schedule
+  double merge(const std::vector<Piece>& pieces) const {
+    double bytes = 0.0;
+    for (const Piece& p : pieces)
+      if (p.cut) bytes += r.part_bytes * rows(items[p.item]) / 256.0;
+    return bytes > 0.0 ? r.merge + bytes / kPartBytesPerUs : 0.0;
+  }
+};
+
+// The given pieces, each in turn to the thread block that is free first (longest first, or in the order given).
+// Returns the makespan; sets the pieces' blocks and orders them as scheduled.
+template <typename C>
+double list_schedule(const C& c, bool longest_first, int sms, std::vector<Piece>* pieces) {
+  const size_t n = pieces->size();
+  std::vector<std::pair<double, int32_t>> order(n);  // {-cost, index}: longest first, ties in the order given
+  for (size_t i = 0; i < n; ++i)
+    order[i] = {-c.of((*pieces)[i].item, (*pieces)[i].hi - (*pieces)[i].lo, (*pieces)[i].cut), (int32_t)i};
+  if (longest_first && !std::is_sorted(order.begin(), order.end())) std::sort(order.begin(), order.end());
+  LeastLoaded blocks(std::max(1, std::min<int>(sms, (int)n)));
+  double makespan = 0.0;
+  std::vector<Piece> out(n);
+  for (size_t i = 0; i < n; ++i) {
+    const std::pair<double, int32_t> load = blocks.add(-order[i].first);
+    out[i] = (*pieces)[order[i].second];
+    out[i].bin = load.second;
+    makespan = std::max(makespan, load.first);
+  }
+  pieces->swap(out);
   return makespan;
 }
 
-// Lays the tiles out block by block in schedule order; ptr gets bins + 1 entries, bins = min(tiles, sms).
-template <typename T>
-double schedule(std::vector<T>* tiles, std::vector<double> cost, bool longest_first, int sms, std::vector<int32_t>* ptr) {
-  const int n = (int)tiles->size(), bins = std::min(n, sms);
+// Every item in equal pieces of at most `chunk` units (0: whole).
+template <typename C>
+std::vector<Piece> equal_pieces(const C& c, int chunk) {
+  std::vector<Piece> out;
+  for (int32_t i = 0; i < (int32_t)c.items.size(); ++i) {
+    const int n = c.items[i].n, k = chunk > 0 && n > chunk ? (n + chunk - 1) / chunk : 1;
+    for (int j = 0; j < k; ++j) out.push_back({i, (int)((int64_t)n * j / k), (int)((int64_t)n * (j + 1) / k), 0, k > 1});
+  }
+  return out;
+}
+
+// Thread blocks filled one after the other up to a load of `top`, items cut where one is full: an even share of the
+// work each for at most one cut a block.  Pieces have at least kLeastPiece units.  False when the bins do not
+// suffice.
+constexpr int kLeastPiece = 2;
+template <typename C>
+bool cut_schedule(const C& c, double top, int bins, std::vector<Piece>* out) {
+  out->clear();
+  int bin = 0;
+  double room = top;
+  for (int32_t i = 0; i < (int32_t)c.items.size(); ++i) {
+    const int n = c.items[i].n;
+    const double step = c.step(c.items[i]);
+    for (int lo = 0;;) {
+      const int rest = n - lo;
+      if (c.of(i, rest, lo > 0) <= room) {  // the rest of the item, or all of it
+        out->push_back({i, lo, n, bin, lo > 0});
+        room -= c.of(i, rest, lo > 0);
+        break;
+      }
+      int fit = (int)std::max(0.0, (room - c.r.fixed - c.r.part) / step);
+      if (rest - fit < kLeastPiece) fit = rest - kLeastPiece;
+      if (fit >= kLeastPiece) {
+        out->push_back({i, lo, lo + fit, bin, true});
+        lo += fit;
+      } else if (room == top) {
+        return false;  // not even an empty block takes a piece
+      }
+      room = top;
+      if (++bin == bins) return false;
+    }
+  }
+  return true;
+}
+
+// The pieces and their thread blocks: whole items where they balance; where too few of them do not fill the SMs
+// evenly, the best of equal pieces and of cutting at an even load, if it wins more than its parts cost.  `apart`: cuts
+// at an even load may be made (they spread the pieces of neighbouring items over time, and with it what those share).
+template <typename C>
+std::vector<Piece> make_schedule(const C& c, bool longest_first, bool apart, int sms, double* makespan) {
+  std::vector<Piece> best = equal_pieces(c, 0);
+  *makespan = list_schedule(c, longest_first, sms, &best);
+  double total = 0.0, units = 0.0;
+  for (size_t i = 0; i < c.items.size(); ++i) {
+    total += c.of((int32_t)i, c.items[i].n, false);
+    units += c.items[i].n;
+  }
+  // many items to a thread block balance by themselves
+  if (c.items.empty() || c.items.size() > 32u * sms || *makespan < 1.05 * total / sms) return best;
+  double price = 0.95 * *makespan;  // the model is good to some 5 %
+  auto take = [&](std::vector<Piece>* trial, double span) {
+    const double with_merge = span + c.merge(*trial);
+    if (with_merge >= price) return;
+    price = with_merge;
+    *makespan = span;
+    best.swap(*trial);
+  };
+  std::vector<Piece> trial;
+  int last = 0;
+  for (double f : {1.5, 1.25, 1.0, 0.8, 0.6, 0.45, 0.3, 0.2}) {
+    const int chunk = std::max(kLeastPiece, (int)(units / sms * f));
+    if (chunk == last) continue;
+    last = chunk;
+    trial = equal_pieces(c, chunk);
+    const double span = list_schedule(c, longest_first, sms, &trial);
+    take(&trial, span);
+  }
+  if (!apart) return best;
+  double lo = total / sms, hi = 2.0 * lo + c.r.fixed + c.r.part;
+  std::vector<Piece> found;
+  for (int k = 0; k < 10 && hi - lo > 0.02 * lo; ++k) {
+    const double mid = k == 0 ? hi : 0.5 * (lo + hi);
+    if (cut_schedule(c, mid, sms, &trial)) {
+      found.swap(trial);
+      hi = mid;
+    } else if (k == 0) {
+      break;
+    } else {
+      lo = mid;
+    }
+  }
+  if (!found.empty()) take(&found, hi);
+  return best;
+}
+
+// The pieces by thread block, in the order of the schedule; ptr gets one entry more than there are blocks.
+std::vector<Piece> by_block(const std::vector<Piece>& pieces, std::vector<int32_t>* ptr) {
+  int32_t bins = 0;
+  for (const Piece& p : pieces) bins = std::max(bins, p.bin + 1);
   ptr->assign(bins + 1, 0);
-  if (n == 0) return 0.0;
-  std::vector<int32_t> order(n), bin_of(n);
-  for (int i = 0; i < n; ++i) order[i] = i;
-  if (longest_first) std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return cost[a] > cost[b]; });
-  const double makespan = list_schedule(cost, order, bins, &bin_of);
-  for (int i = 0; i < n; ++i) ++(*ptr)[bin_of[i] + 1];
+  for (const Piece& p : pieces) ++(*ptr)[p.bin + 1];
   for (int b = 0; b < bins; ++b) (*ptr)[b + 1] += (*ptr)[b];
   std::vector<int32_t> at(ptr->begin(), ptr->end() - 1);
-  std::vector<T> out(n);
-  for (int32_t i : order) out[at[bin_of[i]]++] = (*tiles)[i];
-  tiles->swap(out);
-  return makespan;
+  std::vector<Piece> out(pieces.size());
+  for (const Piece& p : pieces) out[at[p.bin]++] = p;
+  return out;
 }
 
 // Key blocks that the query block sees (its last token's keys), and whether it has tokens at all.
@@ -82,46 +223,23 @@ int blocks_seen(const CausalSeq& s, int block, int tb) {
   return (int)((seen + 127) / 128);
 }
 
-// Pieces of a range of n units when pieces of about `chunk` are wanted (0: none).
-int pieces(int n, int chunk) { return chunk > 0 && n > chunk ? (n + chunk - 1) / chunk : 1; }
-int piece_at(int n, int k, int c) { return (int)((int64_t)n * c / k); }
-
-// The piece size that gives the shortest schedule: no split, or pieces of about an even share of the work and
-// fractions of it, at the price of `merge`.  cost_of(i, n, part) is the cost of n units of item i.
-template <typename Item, typename Cost>
-int choose_chunk(const std::vector<Item>& items, int sms, double merge, const Cost& cost_of) {
-  auto makespan_of = [&](int chunk) {
-    std::vector<double> cost;
-    for (const Item& u : items) {
-      const int k = pieces(u.n, chunk);
-      for (int c = 0; c < k; ++c) cost.push_back(cost_of(u, piece_at(u.n, k, c + 1) - piece_at(u.n, k, c), k > 1));
-    }
-    std::vector<int32_t> order(cost.size());
-    for (size_t i = 0; i < order.size(); ++i) order[i] = (int32_t)i;
-    std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return cost[a] > cost[b]; });
-    return list_schedule(cost, order, std::min<int>((int)cost.size(), sms), nullptr);
-  };
-  double total = 0.0, longest = 0.0;
-  for (const Item& u : items) {
-    const double c = cost_of(u, u.n, false);
-    total += c;
-    longest = std::max(longest, c);
+// Gives the parts of a cut item, marked by their first unit in `part`, the item's slots in that order; `item_of` is
+// where a tile holds its item's number, cleared here.
+template <typename T, typename F>
+void number_parts(std::vector<T>* tiles, const std::vector<int32_t>& first_slot, const F& item_of) {
+  std::vector<int32_t> cut;
+  for (int32_t i = 0; i < (int32_t)tiles->size(); ++i)
+    if ((*tiles)[i].part >= 0) cut.push_back(i);
+  std::sort(cut.begin(), cut.end(), [&](int32_t a, int32_t b) {
+    T &x = (*tiles)[a], &y = (*tiles)[b];
+    return item_of(x) != item_of(y) ? item_of(x) < item_of(y) : x.part < y.part;
+  });
+  for (size_t k = 0, nth = 0; k < cut.size(); ++k) {
+    T& x = (*tiles)[cut[k]];
+    nth = k > 0 && item_of((*tiles)[cut[k - 1]]) == item_of(x) ? nth + 1 : 0;
+    x.part = first_slot[item_of(x)] + (int32_t)nth;
   }
-  // many tiles to a block balance by themselves
-  if (items.empty() || items.size() > 32u * sms) return 0;
-  const double share = total / sms;
-  double best = makespan_of(0);
-  if (best < 1.04 * share) return 0;
-  int chunk = 0;
-  for (double f : {1.0, 0.7, 0.5, 0.35, 0.25, 0.15}) {
-    const int c = std::max(2, (int)(share * f));
-    const double m = makespan_of(c) + merge;
-    if (m < 0.97 * best) {
-      best = m;
-      chunk = c;
-    }
-  }
-  return chunk;
+  for (T& x : *tiles) item_of(x) = 0;
 }
 
 struct FwdItem {
@@ -139,34 +257,42 @@ void build_forward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool r
       for (int b = (nqb - 1) / 2 * 2; nqb > 0 && b >= 0; b -= 2)
         all.push_back({i, h, b, std::max(blocks_seen(s, b, tb), blocks_seen(s, b + 1, tb)), b + 1 < nqb});
   }
-  auto cost_of = [](const FwdItem& u, int n, bool part) {
-    return kTileFixed + n * (u.two ? kStep2 : kStep1) + (part ? kPartFixed : 0.0);
+  const Rates r = fwd_rates(p->head_dim);
+  auto step = [&](const FwdItem& u) { return u.two ? r.step2 : r.step1; };
+  auto rows = [&](const FwdItem& u) {
+    return (u.two ? kCausalRows : 0) + std::min(tb, p->seqs[u.seq].q_len - (u.block + u.two) * tb) * p->group;
   };
-  const int chunk = choose_chunk(all, p->num_sms, kMergeFixed, cost_of);
-  std::vector<double> cost;
-  for (const FwdItem& u : all) {
-    const int k = pieces(u.n, chunk);
+  const Costs<FwdItem, decltype(step), decltype(rows)> costs{all, r, step, rows};
+  double makespan = 0.0;
+  const std::vector<Piece> pieces = make_schedule(costs, resident, true, p->num_sms, &makespan);
+  p->fwd_short = makespan < kShortUs;
+  // an item's parts take neighbouring slots, in the order of their keys
+  std::vector<int32_t> first_slot(all.size(), -1), parts(all.size(), 0);
+  for (const Piece& x : pieces)
+    if (x.cut) ++parts[x.item];
+  for (size_t i = 0; i < all.size(); ++i) {
+    if (parts[i] == 0) continue;
+    const FwdItem& u = all[i];
+    first_slot[i] = p->slots;
     const CausalSeq& s = p->seqs[u.seq];
-    if (k > 1) {
-      p->merges.push_back({u.seq, u.head, u.block, p->slots, k, {0, 0, 0}});
-      const int toks = std::min(tb, s.q_len - (u.block + u.two) * tb);  // of the tile's last query block
-      p->merge_rows = std::max(p->merge_rows, (u.two ? kCausalRows : 0) + toks * p->group);
-    }
-    for (int c = 0; c < k; ++c) {
-      const int lo = piece_at(u.n, k, c), hi = piece_at(u.n, k, c + 1);
-      p->fwd_tiles.push_back({(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, u.head, u.block, lo, hi,
-                              k > 1 ? p->slots++ : -1, u.seq, {0, 0}});
-      cost.push_back(cost_of(u, hi - lo, k > 1));
-    }
+    p->merges.push_back({(int32_t)s.q_offset, s.q_len, u.head, u.block, p->slots, parts[i], {0, 0}});
+    p->slots += parts[i];
+    p->merge_rows = std::max(p->merge_rows, rows(u));
   }
-  p->fwd_short = schedule(&p->fwd_tiles, cost, resident, p->num_sms, &p->fwd_ptr) < kShortFwd;
+  for (const Piece& x : by_block(pieces, &p->fwd_ptr)) {
+    const FwdItem& u = all[x.item];
+    const CausalSeq& s = p->seqs[u.seq];
+    p->fwd_tiles.push_back({(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, u.head, u.block, x.lo, x.hi,
+                            x.cut ? x.lo : -1, u.seq, {x.item, 0}});
+  }
+  number_parts(&p->fwd_tiles, first_slot, [](CausalTile& t) -> int32_t& { return t.pad[0]; });
 }
 
 struct BwdItem {
   int32_t seq, head, block, first, n, nqb;
 };
 
-void build_backward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool resident) {
+void build_backward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool resident, bool in_l2) {
   const int tb = tokens_per_block(p->group);
   std::vector<BwdItem> all;
   for (int32_t i : by_len) {
@@ -181,22 +307,34 @@ void build_backward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool 
         all.push_back({i, h, b, first, nqb - first, nqb});
       }
   }
-  auto cost_of = [](const BwdItem&, int n, bool part) { return kBwdTileFixed + n + (part ? kBwdPartFixed : 0.0); };
-  const int chunk = choose_chunk(all, p->num_sms, kBwdMergeFixed, cost_of);
-  std::vector<double> cost;
-  for (const BwdItem& u : all) {
-    const int k = pieces(u.n, chunk);
+  const Rates r = bwd_rates(p->head_dim);
+  auto step = [&](const BwdItem&) { return r.step1; };
+  auto rows = [](const BwdItem&) { return 256; };  // dK and dV of 128 keys
+  const Costs<BwdItem, decltype(step), decltype(rows)> costs{all, r, step, rows};
+  double makespan = 0.0;
+  // neighbouring key tiles share the accumulator's blocks: cutting at an even load, 5 % better balanced, took 2450 us
+  // against 2262 for a step whose accumulator and queries (325 MB) do not stay in L2
+  const std::vector<Piece> pieces = make_schedule(costs, resident, in_l2, p->num_sms, &makespan);
+  p->bwd_short = makespan < kShortUs;
+  std::vector<int32_t> first_slot(all.size(), -1), parts(all.size(), 0);
+  for (const Piece& x : pieces)
+    if (x.cut) ++parts[x.item];
+  for (size_t i = 0; i < all.size(); ++i) {
+    if (parts[i] == 0) continue;
+    const BwdItem& u = all[i];
     const CausalSeq& s = p->seqs[u.seq];
-    if (k > 1) p->bwd_merges.push_back({(int32_t)s.kv_offset, s.kv_len, u.head, u.block, p->bwd_slots, k, {0, 0}});
-    for (int c = 0; c < k; ++c) {
-      const int lo = piece_at(u.n, k, c), hi = piece_at(u.n, k, c + 1);
-      p->bwd_tiles.push_back({(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, u.head, u.block,
-                              (int32_t)(s.acc_block + (int64_t)u.head * u.nqb), u.first + lo, hi - lo,
-                              k > 1 ? p->bwd_slots++ : -1, u.seq, 0});
-      cost.push_back(cost_of(u, hi - lo, k > 1));
-    }
+    first_slot[i] = p->bwd_slots;
+    p->bwd_merges.push_back({(int32_t)s.kv_offset, s.kv_len, u.head, u.block, p->bwd_slots, parts[i], {0, 0}});
+    p->bwd_slots += parts[i];
   }
-  p->bwd_short = schedule(&p->bwd_tiles, cost, resident, p->num_sms, &p->bwd_ptr) < kShortBwd;
+  for (const Piece& x : by_block(pieces, &p->bwd_ptr)) {
+    const BwdItem& u = all[x.item];
+    const CausalSeq& s = p->seqs[u.seq];
+    p->bwd_tiles.push_back({(int32_t)s.q_offset, s.q_len, (int32_t)s.kv_offset, s.kv_len, u.head, u.block,
+                            (int32_t)(s.acc_block + (int64_t)u.head * u.nqb), u.first + x.lo, x.hi - x.lo,
+                            x.cut ? x.lo : -1, u.seq, x.item});
+  }
+  number_parts(&p->bwd_tiles, first_slot, [](CausalBwdTile& t) -> int32_t& { return t.pad; });
 }
 
 template <typename T>
@@ -287,10 +425,12 @@ zl_status build(const zl_causal_seq* seqs, int32_t n_seqs, uint32_t flags, zl_ca
   const bool few = (int64_t)n_seqs * p->n_kv_heads <= kFewPairs;
   build_forward(p, by_len, few || 4.0 * kv_sum * p->n_kv_heads * p->head_dim <= kL2Bytes);
   // of one row: q and dO in bf16, its accumulator in fp32
-  build_backward(p, by_len, few || p->acc_blocks * 128 * 8.0 * p->head_dim <= kL2Bytes);
+  const double shared = p->acc_blocks * 128 * 8.0 * p->head_dim;
+  if (!p->forward_only) build_backward(p, by_len, few || shared <= kL2Bytes, shared <= 85e6);
   const int64_t D = p->head_dim;
   p->fwd_bytes = (int64_t)p->slots * 256 * (D + 1) * 4;
-  p->bwd_bytes = (int64_t)align_up256((size_t)(p->q_tokens * p->n_q_heads * 4)) + p->acc_blocks * 128 * D * 4 +
+  if (!p->forward_only)
+    p->bwd_bytes = (int64_t)align_up256((size_t)(p->q_tokens * p->n_q_heads * 4)) + p->acc_blocks * 128 * D * 4 +
                  (int64_t)p->bwd_slots * 2 * 128 * D * 4;
   return p->host_only ? ZL_OK : upload_causal(p);
 }
@@ -304,7 +444,7 @@ extern "C" zl_status zl_plan_causal(const zl_causal_seq* seqs, int32_t n_seqs, i
   if (!out) return ZL_ERR_INVALID_ARG;
   *out = nullptr;
   if (n_seqs < 0 || (n_seqs > 0 && !seqs) || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads || q_tokens < 0 ||
-      kv_tokens < 0 || (flags & ~(ZL_PLAN_HOST_ONLY | ZL_PLAN_TEST_WITHHOLD_LOAD)))
+      kv_tokens < 0 || (flags & ~(ZL_PLAN_HOST_ONLY | ZL_PLAN_TEST_WITHHOLD_LOAD | ZL_PLAN_FORWARD_ONLY)))
     return ZL_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) || n_q_heads / n_kv_heads > kCausalRows || n_q_heads > 65536)
     return ZL_ERR_UNSUPPORTED;
@@ -318,6 +458,7 @@ extern "C" zl_status zl_plan_causal(const zl_causal_seq* seqs, int32_t n_seqs, i
   p->kv_tokens = kv_tokens;
   p->host_only = flags & ZL_PLAN_HOST_ONLY;
   p->test_withhold = flags & ZL_PLAN_TEST_WITHHOLD_LOAD;
+  p->forward_only = flags & ZL_PLAN_FORWARD_ONLY;
   p->num_sms = 152;
   zl_status s = ZL_OK;
   if (!p->host_only) {

@@ -458,6 +458,10 @@ typedef struct {
 
 typedef struct zl_causal_plan zl_causal_plan;
 
+/* Flag for zl_plan_causal: no backward.  Its tables are one entry per 128 keys and head, so a
+ * plan made anew for every step of serving is built several times faster without. */
+#define ZL_PLAN_FORWARD_ONLY 32u
+
 /* Plan of the causal attention over n_seqs sequences (host memory, not retained), on the
  * current device: tiles, their static schedule over the SMs, and where few rows face
  * many keys, or key tiles too few to fill the SMs, the split of their range.  n_q_heads must be a multiple of n_kv_heads, query head
@@ -465,7 +469,7 @@ typedef struct zl_causal_plan zl_causal_plan;
  * The query tensors have q_tokens rows, the key tensors kv_tokens (below 2^31 - 512).
  * Sequences may come in any order and leave gaps; their query rows must be disjoint.
  * They may share key rows (a common prefix): the plan then has no backward.
- * flags: ZL_PLAN_HOST_ONLY, ZL_PLAN_TEST_WITHHOLD_LOAD.
+ * flags: ZL_PLAN_HOST_ONLY, ZL_PLAN_TEST_WITHHOLD_LOAD, ZL_PLAN_FORWARD_ONLY.
  * The plan is read-only once built: launches from one plan may run at the same time on
  * several streams (each with its own outputs and workspace).  Building allocates and
  * copies, so it is not for a stream under capture; launches are.
@@ -508,7 +512,7 @@ ZL_API zl_status zl_causal_attn_fwd(const zl_causal_plan* plan, const void* q, i
  *   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO, keys' gradients summed over their group.
  * dQ is summed in fp32 over 128-key tiles in an order that may vary between runs (its last fp32
  * bits may, before the rounding); dK and dV are formed in one order.
- * ZL_ERR_INVALID_ARG also for a plan whose sequences share key rows. */
+ * ZL_ERR_INVALID_ARG also for a plan whose sequences share key rows, or made forward-only. */
 ZL_API zl_status zl_causal_attn_bwd(const zl_causal_plan* plan, const void* q, int64_t q_stride, const void* k,
                                     int64_t k_stride, const void* v, int64_t v_stride, const void* o, const void* d_o,
                                     const float* lse, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,

@@ -271,6 +271,12 @@ def test_shared_keys_have_a_forward_and_no_backward():
     with pytest.raises(zl.ZlError) as e:
         c.backward()
     assert e.value.status == zl.ZL_ERR_INVALID_ARG
+    c = Case([(0, 3, 0, 200), (3, 2, 200, 100)], 4, 2, 64, seed=3)
+    c.plan = zl.zl_plan_causal(c.seqs, 4, 2, 64, 5, 300, zl.ZL_PLAN_FORWARD_ONLY)
+    c.forward().check(("o", "lse"))
+    with pytest.raises(zl.ZlError) as e:
+        c.backward()
+    assert e.value.status == zl.ZL_ERR_INVALID_ARG
 
 
 def test_no_keys_no_queries_no_sequences():
