@@ -62,19 +62,22 @@ struct RopeParams {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// 16 bytes of bf16 as eight floats
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  f[0] = bf_lo(v.x); f[1] = bf_hi(v.x); f[2] = bf_lo(v.y); f[3] = bf_hi(v.y);
-  f[4] = bf_lo(v.z); f[5] = bf_hi(v.z); f[6] = bf_lo(v.w); f[7] = bf_hi(v.w);
+// 16 bytes of bf16 as four pairs of floats, which the two-wide fp32 operations take: they halve the instructions of
+// the arithmetic (56 % of the issue slots went on it, one value at a time)
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
+  f[0] = make_float2(bf_lo(v.x), bf_hi(v.x));
+  f[1] = make_float2(bf_lo(v.y), bf_hi(v.y));
+  f[2] = make_float2(bf_lo(v.z), bf_hi(v.z));
+  f[3] = make_float2(bf_lo(v.w), bf_hi(v.w));
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  return make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y), pack_bf16(f[3].x, f[3].y));
 }
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
 
 // the partner values of a lane's eight: of the partner lane (half) or the neighbour (interleaved)
 template <bool kHalf>
-__device__ __forceinline__ void partners(const uint4& v, const float (&f)[8], int plane, float (&p)[8]) {
+__device__ __forceinline__ void partners(const uint4& v, int plane, float2 (&p)[4]) {
   if constexpr (kHalf) {
     uint4 o;
     o.x = __shfl_sync(0xffffffffu, v.x, plane);
@@ -83,8 +86,10 @@ __device__ __forceinline__ void partners(const uint4& v, const float (&f)[8], in
     o.w = __shfl_sync(0xffffffffu, v.w, plane);
     unpack8(o, p);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = f[i ^ 1];
+    p[0] = make_float2(bf_hi(v.x), bf_lo(v.x));
+    p[1] = make_float2(bf_hi(v.y), bf_lo(v.y));
+    p[2] = make_float2(bf_hi(v.z), bf_lo(v.z));
+    p[3] = make_float2(bf_hi(v.w), bf_lo(v.w));
   }
 }
 
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
   constexpr int kUnroll = rope_unroll<kBwd, kNorm>();
   constexpr bool kDw = kBwd && kNorm;
   constexpr bool kHasX = !kBwd || kNorm;
-  __shared__ float red[kDw ? kRopeThreads / 32 * kRows : 1][2 * D];  // weights, then (kDw) the weights' gradients
+  __shared__ __align__(16) float red[kDw ? kRopeThreads / 32 * kRows : 1][2 * D];  // weights, then (kDw) the weights' gradients
   const int lane = threadIdx.x & 31, sub = lane / kLanes, gl = lane % kLanes, e0 = gl * 8;
   const int64_t nwarps = (int64_t)gridDim.x * (kRopeThreads / 32);
   const bool turns = e0 < p.rot;  // half: rot is a multiple of 16, so all eight values or none
@@ -135,9 +140,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
   }
   const int nb0 = p.t[0].batches;
   const int b_begin = blockIdx.y * p.chunk, b_end = min(b_begin + p.chunk, nb0 + p.t[1].batches);
-  float acc0[8], acc1[8];
+  float2 acc0[4], acc1[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc0[i] = acc1[i] = 0.f;
+  for (int i = 0; i < 4; ++i) acc0[i] = acc1[i] = make_float2(0.f, 0.f);
 
   struct Batch {
     uint4 x[kUnroll], g[kUnroll];
@@ -198,7 +203,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
         }
       }
     }
-    float a[8], b[8];  // forward: weights folded into cosine and sine; backward: a = weights
+    float2 a[4], b[4];  // forward: cosine and sine, the weights folded in; backward: the weights, and in cs2, sn2 both
+    float2 cs2[4], sn2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cs2[i] = make_float2(c[2 * i], c[2 * i + 1]);
+      sn2[i] = make_float2(s[2 * i], s[2 * i + 1]);
+    }
     for (int bi = b_begin; bi < b_end; ++bi) {
       Batch nxt;
       if (bi + 1 < b_end) fetch(tok, bi + 1, nxt);
@@ -209,17 +220,19 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
         if constexpr (kNorm) {
           const float* w = red[0] + t * D;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
+            const float2 own = make_float2(w[e0 + 2 * i], w[e0 + 2 * i + 1]);
             if constexpr (kBwd) {
-              a[i] = w[e0 + i];
+              a[i] = own;
             } else {
-              a[i] = c[i] * w[e0 + i];
-              b[i] = s[i] * w[kHalf ? pe0 + i : e0 + (i ^ 1)];
+              const float2 other = kHalf ? make_float2(w[pe0 + 2 * i], w[pe0 + 2 * i + 1]) : make_float2(own.y, own.x);
+              a[i] = mul2(cs2[i], own);
+              b[i] = mul2(sn2[i], other);
             }
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) { a[i] = c[i]; b[i] = s[i]; }
+          for (int i = 0; i < 4; ++i) { a[i] = cs2[i]; b[i] = sn2[i]; }
         }
       }
       const int h0 = (t ? bi - nb0 : bi) * (kUnroll * kRows) + sub;
@@ -227,55 +240,58 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const bool ok = h0 + u * kRows < T.heads;
-        float o[8];
+        float2 o[4];
         if constexpr (!kBwd) {
-          float x[8], q[8];
+          float2 x[4], q[4];
           unpack8(cur.x[u], x);
-          partners<kHalf>(cur.x[u], x, plane, q);
-          float r = 1.f;
+          partners<kHalf>(cur.x[u], plane, q);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = fma2(x[i], a[i], mul2(q[i], b[i]));
           if constexpr (kNorm) {
-            float ss = 0.f;
+            float2 ss = mul2(x[0], x[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, p.eps));
-          }
+            for (int i = 1; i < 4; ++i) ss = fma2(x[i], x[i], ss);
+            const float r = rsqrtf(fmaf(row_sum<kLanes>(ss.x + ss.y), 1.f / D, p.eps));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            o[i] = fmaf(x[i], a[i], q[i] * b[i]);
-            if constexpr (kNorm) o[i] *= r;
+            for (int i = 0; i < 4; ++i) o[i] = mul2(o[i], make_float2(r, r));
           }
         } else {
-          float g[8], q[8], dy[8];
+          float2 g[4], q[4], dy[4];
           unpack8(cur.g[u], g);
-          partners<kHalf>(cur.g[u], g, plane, q);
+          partners<kHalf>(cur.g[u], plane, q);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dy[i] = fmaf(g[i], c[i], q[i] * s[i]);
+          for (int i = 0; i < 4; ++i) dy[i] = fma2(g[i], cs2[i], mul2(q[i], sn2[i]));
           if constexpr (kNorm) {
-            float x[8];
+            float2 x[4], dn[4];
             unpack8(cur.x[u], x);
-            float ss = 0.f, dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int i = 0; i < 4; ++i) dn[i] = mul2(dy[i], a[i]);
+            float2 ss = mul2(x[0], x[0]), dot = mul2(dn[0], x[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dot = fmaf(dy[i] * a[i], x[i], dot);
-            const float r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, p.eps));
-            const float m = row_sum<kLanes>(dot) * (r * (1.f / D));  // mean(dn n)
+            for (int i = 1; i < 4; ++i) {
+              ss = fma2(x[i], x[i], ss);
+              dot = fma2(dn[i], x[i], dot);
+            }
+            // a lane without a head adds nothing, whatever eps makes of its zeros
+            float r = rsqrtf(fmaf(row_sum<kLanes>(ss.x + ss.y), 1.f / D, p.eps));
+            r = ok ? r : 0.f;
+            const float m = row_sum<kLanes>(dot.x + dot.y) * (r * (1.f / D));  // mean(dn n)
+            const float2 r2 = make_float2(r, r), nm2 = make_float2(-m, -m);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float nrm = x[i] * r;
-              o[i] = r * fmaf(-m, nrm, dy[i] * a[i]);
-              x[i] = ok ? nrm : 0.f;  // a lane without a head adds nothing, whatever eps makes of its zeros
+            for (int i = 0; i < 4; ++i) {
+              x[i] = mul2(x[i], r2);
+              o[i] = mul2(r2, fma2(nm2, x[i], dn[i]));
             }
             if (t == 0) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) acc0[i] = fmaf(dy[i], x[i], acc0[i]);
+              for (int i = 0; i < 4; ++i) acc0[i] = fma2(dy[i], x[i], acc0[i]);
             } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) acc1[i] = fmaf(dy[i], x[i], acc1[i]);
+              for (int i = 0; i < 4; ++i) acc1[i] = fma2(dy[i], x[i], acc1[i]);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = dy[i];
+            for (int i = 0; i < 4; ++i) o[i] = dy[i];
           }
         }
         if (ok) *reinterpret_cast<uint4*>(op + u * kRows * D) = pack8(o);
@@ -288,9 +304,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
       __syncthreads();  // the weights in red[0] have been read
       float* row = red[(threadIdx.x >> 5) * kRows + sub];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        row[e0 + i] = acc0[i];
-        row[D + e0 + i] = acc1[i];
+      for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<float2*>(row + e0 + 2 * i) = acc0[i];
+        *reinterpret_cast<float2*>(row + D + e0 + 2 * i) = acc1[i];
       }
       __syncthreads();
       if (threadIdx.x < 2 * D) {
