@@ -32,6 +32,9 @@ constexpr double kShortUs = 100.0;
 // pairs are taken one after the other, longest tile first within each.
 constexpr double kL2Bytes = 60e6;
 constexpr int64_t kFewPairs = 16;
+// Up to this much of queries, dO and accumulator the backward's walks may be cut at an even load: 79 MB, 132 us
+// against 139 in equal pieces; 92 MB, 160 against 156 whole; 325 MB, 2450 against 2262.
+constexpr double kCutBytes = 85e6;
 
 size_t align_up256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -312,8 +315,6 @@ void build_backward(zl_causal_plan* p, const std::vector<int32_t>& by_len, bool 
   auto rows = [](const BwdItem&) { return 256; };  // dK and dV of 128 keys
   const Costs<BwdItem, decltype(step), decltype(rows)> costs{all, r, step, rows};
   double makespan = 0.0;
-  // neighbouring key tiles share the accumulator's blocks: cutting at an even load, 5 % better balanced, took 2450 us
-  // against 2262 for a step whose accumulator and queries (325 MB) do not stay in L2
   const std::vector<Piece> pieces = make_schedule(costs, resident, in_l2, p->num_sms, &makespan);
   p->bwd_short = makespan < kShortUs;
   std::vector<int32_t> first_slot(all.size(), -1), parts(all.size(), 0);
@@ -426,7 +427,7 @@ zl_status build(const zl_causal_seq* seqs, int32_t n_seqs, uint32_t flags, zl_ca
   build_forward(p, by_len, few || 4.0 * kv_sum * p->n_kv_heads * p->head_dim <= kL2Bytes);
   // of one row: q and dO in bf16, its accumulator in fp32
   const double shared = p->acc_blocks * 128 * 8.0 * p->head_dim;
-  if (!p->forward_only) build_backward(p, by_len, few || shared <= kL2Bytes, shared <= 85e6);
+  if (!p->forward_only) build_backward(p, by_len, few || shared <= kL2Bytes, shared <= kCutBytes);
   const int64_t D = p->head_dim;
   p->fwd_bytes = (int64_t)p->slots * 256 * (D + 1) * 4;
   if (!p->forward_only)

@@ -496,6 +496,7 @@ ZL_API zl_status zl_causal_plan_tiles(const zl_causal_plan* plan, int32_t which,
  *   o: bf16 [q_tokens, n_q_heads, d] contiguous; lse: fp32 [q_tokens, n_q_heads].
  *   workspace: as zl_causal_plan_workspace (NULL where it says 0).
  *   scale: positive, normal.
+ * Outputs may not overlap inputs or each other.
  * Rows of o and lse that belong to no sequence are left as they were.  Tokens outside the
  * sequences may hold anything, NaN included.  Within a sequence a value row that is not finite
  * makes the rows that see it not finite, and may do so to earlier rows that share its 128-key block

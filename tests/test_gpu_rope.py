@@ -86,7 +86,8 @@ def run(n, hq, hk, d, rot, half, axis_pairs, norm, weights=True, seed=0, far=100
 @pytest.mark.parametrize("n,hq,hk,d,rot,axis_pairs", [
     (1, 1, 1, 64, 64, [32]), (3, 4, 2, 64, 64, [32]), (7, 5, 1, 128, 128, [64]), (33, 24, 8, 64, 32, [16]),
     (5, 3, 3, 128, 96, [16, 24, 8]), (2, 7, 0, 128, 16, [8]), (2, 0, 5, 64, 48, [4, 20]), (301, 9, 2, 128, 128, [0, 64, 0]),
-    (4, 6, 2, 64, 0, [0]), (5000, 4, 2, 64, 64, [32])])
+    (4, 6, 2, 64, 0, [0]), (5000, 4, 2, 64, 64, [32]),
+    (64, 16, 2, 128, 128, [64]), (128, 8, 8, 64, 64, [32]), (129, 4, 4, 128, 64, [32]), (9, 200, 40, 64, 32, [16])])
 def test_parity(n, hq, hk, d, rot, axis_pairs, half, norm):
     run(n, hq, hk, d, rot, half, axis_pairs, norm, seed=n + rot)
 
