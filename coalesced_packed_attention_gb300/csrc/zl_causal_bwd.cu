@@ -494,8 +494,8 @@ __global__ void __launch_bounds__(512, 1)
         lse_v = -kInfC;
         if (rt < tb && tok < tl.q_len) {
           const int64_t i = ld_base + (int64_t)tok * p.n_q_heads;
-          lse_v = __ldg(p.lse + i);
-          d_v = __ldg(p.row_d + i);
+          lse_v = p.lse[i];
+          d_v = p.row_d[i];
         }
       };
       bool ok = true;
@@ -652,10 +652,8 @@ __global__ void __launch_bounds__(512, 1)
 // D = rowsum(dO * O): d / 8 lanes per row of the [tokens, heads, d] tensors, four rows' loads in flight; each
 // block first zeroes its share of the dQ accumulator.  HBM-bound: 4 d bytes read and 4 + 4 d written a row.
 template <int D>
-__global__ void __launch_bounds__(256) zl_causal_pre_kernel(const __nv_bfloat16* __restrict__ o,
-                                                            const __nv_bfloat16* __restrict__ d_o,
-                                                            float* __restrict__ row_d, int64_t rows,
-                                                            float* __restrict__ acc, int64_t acc4) {
+__global__ void __launch_bounds__(256) zl_causal_pre_kernel(const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* row_d,
+                                                            int64_t rows, float* acc, int64_t acc4) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = 4;
   const int lane = threadIdx.x & 31, sub = lane / kLanes, piece = lane % kLanes;
   const int64_t nthreads = (int64_t)gridDim.x * blockDim.x;
@@ -673,8 +671,8 @@ __global__ void __launch_bounds__(256) zl_causal_pre_kernel(const __nv_bfloat16*
       const int64_t row = base + u * kRows + sub;
       a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
       if (row < rows) {
-        a[u] = __ldg(reinterpret_cast<const uint4*>(o + row * D) + piece);
-        b[u] = __ldg(reinterpret_cast<const uint4*>(d_o + row * D) + piece);
+        a[u] = reinterpret_cast<const uint4*>(o + row * D)[piece];
+        b[u] = reinterpret_cast<const uint4*>(d_o + row * D)[piece];
       }
     }
     auto dot2 = [](uint32_t x, uint32_t y, float s) {
@@ -718,7 +716,7 @@ __global__ void __launch_bounds__(256) zl_causal_finish_kernel(const CausalFinis
     const float4* src = reinterpret_cast<const float4*>(p.acc) + sl * (128 * 16);
     float4 x[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) x[u] = __ldg(src + u * 256 + threadIdx.x);
+    for (int u = 0; u < 8; ++u) x[u] = src[u * 256 + threadIdx.x];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int k = u * 256 + threadIdx.x;  // piece (column group k / 128, row k % 128)
@@ -758,7 +756,7 @@ __global__ void __launch_bounds__(256) zl_causal_finish_kernel(const CausalFinis
     for (int q = 0; q < m.parts; ++q) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 a = __ldg(src + (int64_t)q * (2 * 32 * D) + i * 128);
+        const float4 a = src[(int64_t)q * (2 * 32 * D) + i * 128];
         v[i].x += a.x; v[i].y += a.y; v[i].z += a.z; v[i].w += a.w;
       }
     }

@@ -572,21 +572,21 @@ __global__ void __launch_bounds__(128) zl_causal_merge_kernel(const CausalMergeP
     float4 x[8];
     if (way < G.parts) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __ldg(po + (int64_t)way * (2 * 32 * D) + i * 128);
+      for (int i = 0; i < 8; ++i) x[i] = po[(int64_t)way * (2 * 32 * D) + i * 128];
     }
     float m = kNegInf;
 #pragma unroll 8
-    for (int c = 0; c < G.parts; ++c) m = fmaxf(m, __ldg(pl + (int64_t)c * 256));
+    for (int c = 0; c < G.parts; ++c) m = fmaxf(m, pl[(int64_t)c * 256]);
     base = m == kNegInf ? 0.f : m;
 #pragma unroll 8
-    for (int c = 0; c < G.parts; ++c) tot += expf(__ldg(pl + (int64_t)c * 256) - base);
+    for (int c = 0; c < G.parts; ++c) tot += expf(pl[(int64_t)c * 256] - base);
     const float inv = tot == 0.f ? 0.f : 1.f / tot;
     for (int c = way; c < G.parts; c += kWays) {
-      const float wc = expf(__ldg(pl + (int64_t)c * 256) - base) * inv;
+      const float wc = expf(pl[(int64_t)c * 256] - base) * inv;
       float4 y[8];
       if (c + kWays < G.parts) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __ldg(po + (int64_t)(c + kWays) * (2 * 32 * D) + i * 128);
+        for (int i = 0; i < 8; ++i) y[i] = po[(int64_t)(c + kWays) * (2 * 32 * D) + i * 128];
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {

@@ -1,10 +1,11 @@
 // Launches that may be set up while the kernel before them in the stream still runs (programmatic dependent
 // launch).  A kernel launched this way may start early, and touches no global memory but a plan's own tables before
-// wait_for_previous(), which
-// returns once every earlier kernel of the stream has finished and its writes are visible; each of its threads passes
-// that wait before it ends, so the order is handed on to the kernel after it.  What is saved is the launch latency and
-// the set-up of barriers and tensor memory: 2 us of a kernel behind another.  Kernels, copies and events of other
-// origin before or after keep the stream's plain order.
+// wait_for_previous(), which returns once every earlier kernel of the stream has finished and its writes are visible;
+// each of its threads passes that wait before it ends, so the order is handed on to the kernel after it.  What is saved
+// is the launch latency and the set-up of barriers and tensor memory: 2 us of a kernel behind another.
+// Such a kernel lives while its inputs are still being written, so it reads them with plain loads: the read-only path
+// (__ldg, const __restrict__) wants memory that does not change for as long as the kernel lives.
+// Kernels, copies and events of other origin before or after keep the stream's plain order.
 #pragma once
 #include <cuda_runtime.h>
 

@@ -128,14 +128,14 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
   // the pairs whose sines this lane forms, and the lane that forms the first of those that it uses
   const int pairs = p.rot / 2, my_pair = 2 * lane;
   const int src = (kHalf ? (lower ? e0 : e0 - pairs) : e0 / 2) / 2;
-  const uint64_t f0 = my_pair < pairs ? __ldg(p.freq + my_pair) : 0, f1 = my_pair + 1 < pairs ? __ldg(p.freq + my_pair + 1) : 0;
+  const uint64_t f0 = my_pair < pairs ? p.freq[my_pair] : 0, f1 = my_pair + 1 < pairs ? p.freq[my_pair + 1] : 0;
   auto axis_of = [&](int pair) { return pair < p.axis1 ? 0 : pair < p.axis2 ? 1 : 2; };
   const int ax0 = my_pair < pairs ? axis_of(my_pair) : 0, ax1 = my_pair + 1 < pairs ? axis_of(my_pair + 1) : 0;
 
   if constexpr (kNorm) {
     if (threadIdx.x < 2 * D) {
       const float* w = threadIdx.x < D ? p.t[0].w : p.t[1].w;
-      red[0][threadIdx.x] = w ? __ldg(w + threadIdx.x % D) : 1.f;
+      red[0][threadIdx.x] = w ? w[threadIdx.x % D] : 1.f;
     }
     __syncthreads();
   }
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
       const int32_t* pt = p.positions + tok * p.n_axes;
       float cs[2], sn[2];
       auto turn = [&](uint64_t f, int axis, float& co, float& si) {
-        const uint64_t phase = (uint64_t)(int64_t)__ldg(pt + axis) * f;
+        const uint64_t phase = (uint64_t)(int64_t)pt[axis] * f;
         // top 32 bits as a signed fraction of a turn; 2 pi r = pi (2 r)
         sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &si, &co);
         co *= p.amplitude;
@@ -322,8 +322,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
 }
 
 // Sum of the blocks' weight gradients: 32 columns a block, 32 slices of the rows, in order.
-__global__ void __launch_bounds__(1024) zl_qk_rope_dw_kernel(const float* __restrict__ partial, int32_t rows, int32_t d,
-                                                             float* __restrict__ dwq, float* __restrict__ dwk) {
+__global__ void __launch_bounds__(1024) zl_qk_rope_dw_kernel(const float* partial, int32_t rows, int32_t d, float* dwq, float* dwk) {
   __shared__ float red[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + x;
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(1024) zl_qk_rope_dw_kernel(const float* __rest
   wait_for_previous();
   float v = 0.f;
 #pragma unroll 4
-  for (int r = y; r < rows; r += 32) v += __ldg(partial + (int64_t)r * (2 * d) + col);
+  for (int r = y; r < rows; r += 32) v += partial[(int64_t)r * (2 * d) + col];
   red[y][x] = v;
   __syncthreads();
   if (y == 0) {
@@ -364,6 +363,11 @@ zl_status check_desc(const zl_qk_rope_desc* d) {
     if (pairs * 2 != d->rot_dim) return ZL_ERR_INVALID_ARG;
   }
   return ZL_OK;
+}
+
+// An output may lie where its input does, row for row; at another stride it would overwrite rows not yet read.
+bool same_rows(const void* in, int64_t in_stride, const void* out, int64_t out_stride, int64_t n) {
+  return in != out || in_stride == out_stride || n <= 1;
 }
 
 // One of the two tensors' pointers: heads 0 wants none, any other count wants them aligned, with a
@@ -495,6 +499,9 @@ extern "C" zl_status zl_qk_rope_fwd(const zl_qk_rope_desc* d, const void* q, int
       (s = check_tensor(q_out, q_out_stride, d->n_q_heads, D)) != ZL_OK ||
       (s = check_tensor(k_out, k_out_stride, d->n_kv_heads, D)) != ZL_OK)
     return s;
+  if ((d->n_q_heads > 0 && !same_rows(q, q_stride, q_out, q_out_stride, d->n_tokens)) ||
+      (d->n_kv_heads > 0 && !same_rows(k, k_stride, k_out, k_out_stride, d->n_tokens)))
+    return ZL_ERR_INVALID_ARG;
   if (d->rot_dim > 0 && (!positions || !freq)) return ZL_ERR_INVALID_ARG;
   int sms = 0;
   if ((s = check_device(&sms)) != ZL_OK) return s;
@@ -539,6 +546,9 @@ extern "C" zl_status zl_qk_rope_bwd(const zl_qk_rope_desc* d, const void* q, int
       (s = check_tensor(dk_out, dk_out_stride, d->n_kv_heads, D)) != ZL_OK ||
       (s = check_tensor(dq, dq_stride, d->n_q_heads, D)) != ZL_OK || (s = check_tensor(dk, dk_stride, d->n_kv_heads, D)) != ZL_OK)
     return s;
+  if ((d->n_q_heads > 0 && !same_rows(dq_out, dq_out_stride, dq, dq_stride, d->n_tokens)) ||
+      (d->n_kv_heads > 0 && !same_rows(dk_out, dk_out_stride, dk, dk_stride, d->n_tokens)))
+    return ZL_ERR_INVALID_ARG;
   if (d->rot_dim > 0 && (!positions || !freq)) return ZL_ERR_INVALID_ARG;
   int sms = 0;
   if ((s = check_device(&sms)) != ZL_OK) return s;

@@ -9,8 +9,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
-from typing import Dict, List, Optional, Sequence
+from dataclasses import dataclass, field
+from typing import Dict, List, Optional, Sequence, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libzl.so")
@@ -512,17 +512,24 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[st
     raise ValueError(f"scaling: expected None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
 
 
-@dataclass
+@dataclass(frozen=True)
 class RotaryTable:
-    """Frequencies of a rotation on one device, and how the pairs are laid out."""
+    """Frequencies of a rotation on one device, and how the pairs are laid out.  Not to be changed once made (a call
+    reuses the descriptor of the last call of the same sizes); dataclasses.replace makes another."""
     freq: "object"  # int64 tensor holding the 64-bit fractions of a turn per position
     rot_dim: int
     half: bool
-    axis_pairs: List[int]
+    axis_pairs: Tuple[int, ...]
     amplitude: float
-    device: int = -1            # CUDA device of freq
-    ptr: Optional[int] = None   # and its address there
-    last: tuple = (None, None)  # the last call's descriptor, by its key
+    device: int = field(init=False, default=-1, repr=False)           # CUDA device of freq
+    ptr: Optional[int] = field(init=False, default=None, repr=False)  # and its address there
+    last: list = field(init=False, default_factory=lambda: [(None, None)], repr=False, compare=False)
+
+    def __post_init__(self):
+        object.__setattr__(self, "axis_pairs", tuple(self.axis_pairs))
+        if self.freq is not None:
+            object.__setattr__(self, "device", self.freq.get_device())
+            object.__setattr__(self, "ptr", self.freq.data_ptr())
 
 
 def rotary_table(inv_freq: Sequence[float], layout: str = "half", axis_pairs: Optional[Sequence[int]] = None,
@@ -541,7 +548,7 @@ def rotary_table(inv_freq: Sequence[float], layout: str = "half", axis_pairs: Op
     out = (ctypes.c_uint64 * max(1, n))()
     _check(load_library().zl_rope_frequencies((ctypes.c_double * max(1, n))(*radians), n, out), "zl_rope_frequencies")
     freq = torch.tensor([ctypes.c_int64(x).value for x in out[:n]], dtype=torch.int64).to(device)
-    return RotaryTable(freq, 2 * n, layout == "half", pairs, float(amplitude), freq.get_device(), freq.data_ptr())
+    return RotaryTable(freq, 2 * n, layout == "half", tuple(pairs), float(amplitude))
 
 
 def zl_qk_rope_workspace_bytes(n_tokens: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -552,7 +559,7 @@ def zl_qk_rope_workspace_bytes(n_tokens: int, n_q_heads: int, n_kv_heads: int, h
     return b.value
 
 
-_PLAIN = RotaryTable(None, 0, False, [], 1.0)  # no rotation
+_PLAIN = RotaryTable(None, 0, False, (), 1.0)  # no rotation
 
 
 def _rope_args(q, k, positions, table, norm, eps, q_weight, k_weight):
@@ -581,12 +588,12 @@ def _rope_args(q, k, positions, table, norm, eps, q_weight, k_weight):
         if table.device != dev:
             raise ValueError(f"table on device {table.device}, current device is cuda:{dev}")
     key = (n, hq, hk, d, norm, eps)
-    last = table.last
+    last = table.last[0]
     if last[0] != key:
-        pairs = (table.axis_pairs + [0, 0, 0])[:3]
+        pairs = (table.axis_pairs + (0, 0, 0))[:3]
         last = (key, zl_qk_rope_desc(n, hq, hk, d, int(norm), eps, table.rot_dim, int(table.half), len(table.axis_pairs),
                                      (ctypes.c_int32 * 3)(*pairs), table.amplitude))
-        table.last = last
+        table.last[0] = last
     qw = _dense(q_weight, "q_weight", torch.float32, (d,), dev) if q_weight is not None else None
     kw = _dense(k_weight, "k_weight", torch.float32, (d,), dev) if k_weight is not None else None
     return last[1], dev, (n, hq, d), (n, hk, d), pos, freq, qw, kw

@@ -426,7 +426,7 @@ ZL_API zl_status zl_qk_rope_workspace(const zl_qk_rope_desc* desc, int64_t* byte
  *   value.  freq: uint64 [rot_dim / 2] from zl_rope_frequencies, in device memory.
  * One pass; fp32 arithmetic, rounded once.  Uses no state: calls on different streams
  * are independent.  ZL_ERR_INVALID_ARG for a bad descriptor, a missing pointer, a stride
- * below heads * d, or weights without norm; ZL_ERR_ALIGN for a base that is not 16-byte
+ * below heads * d, an output on its input at another stride, or weights without norm; ZL_ERR_ALIGN for a base that is not 16-byte
  * aligned or a stride that is not a multiple of 8. */
 ZL_API zl_status zl_qk_rope_fwd(const zl_qk_rope_desc* desc, const void* q, int64_t q_stride, const void* k,
                                 int64_t k_stride, const float* q_weight, const float* k_weight,
@@ -511,6 +511,8 @@ ZL_API zl_status zl_causal_attn_fwd(const zl_causal_plan* plan, const void* q, i
  * sequence (zero where no query sees a key), other rows left as they were.
  * With P = exp(scale q k^T - LSE), D = rowsum(dO * O), dS = P (dO V^T - D):
  *   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO, keys' gradients summed over their group.
+ * As in the forward, tokens outside the sequences may hold anything; within a sequence a row that is not finite may
+ * make the gradients of every row that shares its blocks of 128 keys or query rows not finite.
  * dQ is summed in fp32 over 128-key tiles in an order that may vary between runs (its last fp32
  * bits may, before the rounding); dK and dV are formed in one order.
  * ZL_ERR_INVALID_ARG also for a plan whose sequences share key rows, or made forward-only. */

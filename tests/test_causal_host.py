@@ -323,9 +323,21 @@ def test_bad_rope_pointers_are_refused_before_any_launch(lib):
         assert back(i, None) == inv
     for i in (0, 2, 8, 10, 12, 14, 18):
         assert back(i, 24) == al
+    for i in (9, 11):  # an output on its input at another stride (backward 13, 15: on its gradient)
+        assert fwd(**{f"_{i}": 512}) == inv and back(i + 4, 512) == inv
     # no tokens: nothing to do, whatever the pointers
     d = _desc(n_tokens=0)
     assert lib.zl_qk_rope_fwd(ctypes.byref(d), None, 0, None, 0, None, None, None, None, None, 0, None, 0, None) == zl.ZL_OK
+
+
+def test_a_rotary_table_is_not_changed_but_replaced():
+    import dataclasses
+    table = zl.rotary_table([1.0, 0.5], "interleaved", device="cpu")
+    with pytest.raises(dataclasses.FrozenInstanceError):
+        table.amplitude = 2.0
+    table.last[0] = ("key", "descriptor")
+    other = dataclasses.replace(table, amplitude=2.0, freq=table.freq.clone())
+    assert other.last == [(None, None)] and other.ptr == other.freq.data_ptr() != table.ptr and other.axis_pairs == (2,)
 
 
 def test_host_tensors_are_refused():

@@ -177,6 +177,61 @@ def test_weight_gradients_repeat_bit_for_bit_and_replay():
         assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
 
 
+def test_launches_in_a_row_see_the_latest_writes():
+    """Kernels that are set up while the one before them runs: the same buffers, inputs that change from call to call,
+    nothing awaited in between, equal the same calls each awaited."""
+    import torch
+    ensure_library()
+    n, hq, hk, d = 200, 8, 2, 128
+    table = zl.rotary_table(zl.rotary_frequencies(d)[0])
+    sets = [[x.cuda() for x in inputs(n, hq, hk, d, 1, s)] for s in (3, 4, 5)]
+    state = [x.clone() for x in sets[0]]
+    out, dx = (torch.empty(n, hq + hk, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dw = torch.empty(2, d, device="cuda")
+    ws = torch.empty(zl.zl_qk_rope_workspace_bytes(n, hq, hk, d), dtype=torch.uint8, device="cuda")
+
+    def calls(wait):
+        got = []
+        for i in range(24):
+            for dst, src in zip(state, sets[i % 3]):
+                dst.copy_(src)
+            qkv, pos, w, _ = state
+            for _ in range(2):
+                zl.zl_qk_rope_fwd(qkv[:, :hq], qkv[:, hq:hq + hk], out[:, :hq], out[:, hq:], pos, table, True, w[0], w[1], EPS)
+                wait()
+                zl.zl_qk_rope_bwd(qkv[:, :hq], qkv[:, hq:hq + hk], out[:, :hq], out[:, hq:], dx[:, :hq], dx[:, hq:], pos,
+                                  table, True, w[0], w[1], dw[0], dw[1], ws, EPS)
+                wait()
+                # in place: the result is the next call's input
+                zl.zl_qk_rope_fwd(dx[:, :hq], dx[:, hq:], qkv[:, :hq], qkv[:, hq:hq + hk], pos, table)
+                wait()
+            got += [out.clone(), dx.clone(), dw.clone()]
+        torch.cuda.synchronize()
+        return got
+
+    for x, y in zip(calls(lambda: None), calls(torch.cuda.synchronize)):
+        assert torch.equal(x, y)
+
+
+def test_calls_on_two_streams_at_once():
+    import torch
+    ensure_library()
+    table = zl.rotary_table(zl.rotary_frequencies(64)[0])
+    work = []
+    for s, n in ((1, 5000), (2, 3333)):
+        qkv, pos, w, _ = (x.cuda() for x in inputs(n, 6, 3, 64, 1, s))
+        work.append((qkv, pos, w, torch.empty_like(qkv), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for qkv, pos, w, out, st in work:
+            zl.zl_qk_rope_fwd(qkv[:, :6], qkv[:, 6:9], out[:, :6], out[:, 6:9], pos, table, True, w[0], w[1], EPS, stream=st)
+    torch.cuda.synchronize()
+    for qkv, pos, w, out, _ in work:
+        want = torch.empty_like(qkv)
+        zl.zl_qk_rope_fwd(qkv[:, :6], qkv[:, 6:9], want[:, :6], want[:, 6:9], pos, table, True, w[0], w[1], EPS)
+        assert torch.equal(out[:, :9], want[:, :9])
+
+
 def test_python_refusals():
     import torch
     ensure_library()
