@@ -17,7 +17,7 @@
 //   only blocks on the diagonal carry it
 //   dV  += P^T dO_i     (TMEM x SMEM)
 //   dQ_i = dS K         (SMEM x SMEM -> TMEM R1)
-//   dK  += dS^T Q_i     (SMEM x SMEM)
+//   dK  += dS^T Q_i     (SMEM x SMEM; d = 64: TMEM x SMEM)
 //   the dQ warpgroup reads dQ_i, stages it 16 KB at a time and hands each chunk to the bulk-copy engine as one
 //   reduce-add into the fp32 accumulator, which a last kernel scales, rounds and writes out.
 // The key tiles of one head reach a query block in an order that may differ from run to run, so dQ may differ
@@ -36,7 +36,8 @@
 // block keep them busy for most of its 3500.
 // Roles and budget: warps 0-7 softmax (two warpgroups), 8-11 dQ drain, 12 TMA, 13 MMA, 14-15 idle; launched with
 // 128 registers a thread, traded with setmaxnreg to 136 / 152 / 88, per sub-partition 2 x 136 + 152 + 88 = 4 x 128,
-// exactly the launch allocation.  TMEM (512 columns): R0 [0,128), R1 [128,256), dV [256,256+d), dK [384,384+d).
+// exactly the launch allocation.  TMEM (512 columns): R0 [0,128), R1 [128,256), dV [256,256+d), dK [384,384+d), and at
+// d = 64 dS^T [448,512).
 // (d = 64 has room for dQ columns of its own and a second stage of dS^T and dO, so that dP^T of the next block need
 // not wait for the drain; built and measured, it was slower: 133.5 against 129.9 us for the step of 4109 tokens, 24/8
 // heads.  There the softmax warpgroups, not the products, fill a block's period.)
@@ -72,6 +73,11 @@ struct CausalBwdLayout {
   static constexpr int kNumBars = 17 + 2 * kQStages + 2 * kDOStages;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 32;
+  // d = 64 leaves TMEM columns for a second copy of dS^T, which dK then takes as its operand: 32 KB less a block through
+  // the shared memory (training step's gradient of 4109 tokens, 24/8 heads: 78.6 against 81.3 us).  K and V kept
+  // there too, as operands of S^T and dP^T, made it 84: products with N = 128 are slower from TMEM.
+  static constexpr bool kDSinTmem = D == 64;
+  static constexpr uint32_t kDSCol = 448;
 };
 
 constexpr float kLog2eC = 1.44269504088896340736f;
@@ -399,8 +405,9 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {  // dK += dS^T Q
             const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
-            mma_ss_w(tdK, dsc(kDS, off), dsc(mQ, st * L::kTile + kk * 2048), kIdKV,
-                     (is > 0 || kk > 0) ? 1u : 0u);
+            const uint32_t more = (is > 0 || kk > 0) ? 1u : 0u, q = st * L::kTile + kk * 2048;
+            if constexpr (L::kDSinTmem) mma_ts_w(tdK, tmem + L::kDSCol + kk * 8, dsc(mQ, q), kIdKV, more);
+            else mma_ss_w(tdK, dsc(kDS, off), dsc(mQ, q), kIdKV, more);
           }
           mma_commit_w(q_empty + st);
           ++qit;
@@ -567,6 +574,7 @@ __global__ void __launch_bounds__(512, 1)
                                    make_float2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]));
             pk[e] = pack_bf16(ds.x, ds.y);
           }
+          if constexpr (L::kDSinTmem) tmem_st16(tmem + lane_base + L::kDSCol + 32 * wg + 16 * c, pk);
           // dS^T row t_key -> box wg of shared memory, 128-byte swizzle
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -575,6 +583,7 @@ __global__ void __launch_bounds__(512, 1)
           }
         }
         fence_proxy_async_smem();
+        if constexpr (L::kDSinTmem) tmem_st_wait();
         tc_fence_before();  // the dP^T loads are complete: dQ may overwrite R1
         mbar_arrive(ds_ready);
         ++nblocks;
