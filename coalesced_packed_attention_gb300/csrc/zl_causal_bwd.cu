@@ -114,10 +114,6 @@ __device__ __forceinline__ void bulk_read_all_but_1() {
 }
 __device__ __forceinline__ void bulk_all_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// TMEM column of the packed bf16 P^T in R0 for K-step kk (16 rows): rows 0-63 are packed by warpgroup 0 into
-// columns [0,32), rows 64-127 by warpgroup 1 into [64,96), each over S^T columns it has already read.
-__device__ __forceinline__ uint32_t p_col(int kk) { return (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8); }
-
 constexpr uint32_t kLaunchRegs = 128;
 constexpr uint32_t kSoftmaxRegs = 136, kDrainRegs = 152, kMiscRegs = 88;
 static_assert(2 * kSoftmaxRegs + kDrainRegs + kMiscRegs == 4 * kLaunchRegs,
@@ -333,7 +329,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t kDS = sdesc_lo(aDS, 16);
       const uint32_t mK = sdesc_lo(aK, L::kBox), mQ = sdesc_lo(aQ, L::kBox), mDO = sdesc_lo(aDO, L::kBox);
       const uint32_t mDS = sdesc_lo(aDS, L::kBox);
-      auto dsc = [](uint32_t lo, uint32_t bytes) { return sdesc_join(lo + (bytes >> 4)); };
+      constexpr int kNextBox = L::kBox / 16 - 4 * 2;  // K steps 0-3 lie in the first box, 4-7 in the second
       uint32_t kt = 0, qit = 0, nblocks = 0;
       bool ok = true;
       for (int t = t_begin; t < t_end && ok; ++t) {
@@ -361,11 +357,8 @@ __global__ void __launch_bounds__(512, 1)
         tc_fence_after();
         auto issue_s = [&](uint32_t st) {  // S^T = K Q^T of the query block in stage st
           const uint32_t dq = kQ + ((st * L::kTile) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
-            mma_ss_w(tR0, dsc(kK, off), dsc(dq, off), kIdSq, kk > 0);
-          }
+          if constexpr (D == 128) mma_ss8_w<2, kNextBox, 2, kNextBox>(tR0, kK, dq, kIdSq, 0u);
+          else mma_ss4_w<2, 0, 2, 0>(tR0, kK, dq, kIdSq, 0u);
           mma_commit_w(s_full);
         };
         if (!wait_w(q_full + q_stage(qit), q_phase(qit))) break;
@@ -378,17 +371,15 @@ __global__ void __launch_bounds__(512, 1)
           fix_rows(is, aDO + ds * L::kTile);
           if (nblocks > 0 && !wait_w(dq_empty, (nblocks - 1) & 1)) { ok = false; break; }
           tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {  // dP^T = V dO^T
-            const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
-            mma_ss_w(tR1, dsc(kV, off), dsc(kDO, ds * L::kTile + off), kIdSq, kk > 0);
-          }
+          const uint32_t ddo = kDO + ((ds * L::kTile) >> 4);  // dP^T = V dO^T
+          if constexpr (D == 128) mma_ss8_w<2, kNextBox, 2, kNextBox>(tR1, kV, ddo, kIdSq, 0u);
+          else mma_ss4_w<2, 0, 2, 0>(tR1, kV, ddo, kIdSq, 0u);
           mma_commit_w(dp_full);
           if (!wait_w(p_ready, nblocks & 1)) { ok = false; break; }
           tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // dV += P^T dO
-            mma_ts_w(tdV, tR0 + p_col(kk), dsc(mDO, ds * L::kTile + kk * 2048), kIdKV, (is > 0 || kk > 0) ? 1u : 0u);
+          // dV += P^T dO; P^T of rows 0-63 is packed by warpgroup 0 into R0's columns [0, 32), of rows 64-127 by
+          // warpgroup 1 into [64, 96), each over S^T columns it has already read
+          mma_ts8_w<8, 32, 128, 0>(tdV, tR0, mDO + ((ds * L::kTile) >> 4), kIdKV, is > 0 ? 1u : 0u);
           mma_commit_w(do_empty + ds);
           if (is + 1 < sp.n) {
             // S^T of the next block as soon as dV has read P^T out of R0 (products run in issue order)
@@ -400,17 +391,12 @@ __global__ void __launch_bounds__(512, 1)
           }
           if (!wait_w(ds_ready, nblocks & 1)) { ok = false; break; }
           tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // dQ = dS K (both operands MN-major), first: the drain starts on it
-            mma_ss_w(tR1, dsc(mDS, kk * 2048), dsc(mK, kk * 2048), kIdDQ, kk > 0);
+          // dQ = dS K (both operands MN-major), first: the drain starts on it
+          mma_ss8_w<128, 0, 128, 0>(tR1, mDS, mK, kIdDQ, 0u);
           mma_commit_w(dq_full);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {  // dK += dS^T Q
-            const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
-            const uint32_t more = (is > 0 || kk > 0) ? 1u : 0u, q = st * L::kTile + kk * 2048;
-            if constexpr (L::kDSinTmem) mma_ts_w(tdK, tmem + L::kDSCol + kk * 8, dsc(mQ, q), kIdKV, more);
-            else mma_ss_w(tdK, dsc(kDS, off), dsc(mQ, q), kIdKV, more);
-          }
+          const uint32_t dq = mQ + ((st * L::kTile) >> 4), more = is > 0 ? 1u : 0u;  // dK += dS^T Q
+          if constexpr (L::kDSinTmem) mma_ts8_w<8, 0, 128, 0>(tdK, tmem + L::kDSCol, dq, kIdKV, more);
+          else mma_ss8_w<2, kNextBox, 128, 0>(tdK, kDS, dq, kIdKV, more);
           mma_commit_w(q_empty + st);
           ++qit;
           ++nblocks;

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const uint32_t aV = smem_u32(sV);
       // low words of the operand descriptors (all share the high word)
       const uint32_t dQ0 = sdesc_lo(smem_u32(sQ), 16), dK0 = sdesc_lo(smem_u32(sK), 16), dV0 = sdesc_lo(aV, L::kBox);
-      auto dsc = [](uint32_t lo, uint32_t bytes) { return sdesc_join(lo + (bytes >> 4)); };
+      constexpr int kNextBox = L::kBox / 16 - 4 * 2;  // K steps 0-3 lie in the first box, 4-7 in the second
       uint32_t kv_it = 0, q_it[2] = {0, 0}, p_it[2] = {0, 0}, o_it[2] = {0, 0};
       bool ok = true;
       auto wait_w = [&](uint64_t* b, uint32_t parity) {
@@ -301,10 +301,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           ++o_it[w];
         }
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts_w(tmem + 256 + 128 * w, tmem + 128 * w + kk * 8, dsc(dV0, ps * L::kTile + kk * 2048), kIdPV,
-                   (first && kk == 0) ? 0u : 1u);
+        mma_ts8_w<8, 0, 128, 0>(tmem + 256 + 128 * w, tmem + 128 * w, dV0 + ((ps * L::kTile) >> 4), kIdPV, first ? 0u : 1u);
         if (last[w]) mma_commit_w(o_full + w);
         return true;
       };
@@ -323,11 +320,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 ++q_it[w];
               }
               tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
-                mma_ss_w(tmem + 128 * w, dsc(dQ0, w * L::kTile + off), dsc(dK0, s * L::kTile + off), kIdS, kk > 0 ? 1u : 0u);
-              }
+              const uint32_t dq = dQ0 + ((w * L::kTile) >> 4), dk = dK0 + ((s * L::kTile) >> 4);
+              if constexpr (D == 128) mma_ss8_w<2, kNextBox, 2, kNextBox>(tmem + 128 * w, dq, dk, kIdS, 0u);
+              else mma_ss4_w<2, 0, 2, 0>(tmem + 128 * w, dq, dk, kIdS, 0u);
               mma_commit_w(s_full + w);
               if (j == sp.n[w] - 1) mma_commit_w(q_empty + w);
             }
