@@ -62,9 +62,10 @@ struct CausalBwdLayout {
   static constexpr int kK = 0;
   static constexpr int kV = kK + kTile;
   // d = 128 fills the shared memory with two stages of Q and one of dO; at d = 64 there is room to load further ahead
-  // (with two and one the products waited for Q and dO 500 of a block's 3500 cycles)
+  // (with two and one the products waited for Q and dO 500 of a block's 3500 cycles; with three or four of dO
+  // nothing waits less, and 12 288 tokens, 16/2 heads, took 460 and 465 us against 451)
   static constexpr int kQStages = D == 64 ? 4 : 2;
-  static constexpr int kDOStages = D == 64 ? 3 : 1;
+  static constexpr int kDOStages = D == 64 ? 2 : 1;
   static constexpr int kQ = kV + kTile;
   static constexpr int kDO = kQ + kQStages * kTile;    // a stage is free once dV has read it
   static constexpr int kDS = kDO + kDOStages * kTile;  // [128 keys][128 rows] bf16, two 128-byte-swizzled boxes
@@ -357,47 +358,56 @@ __global__ void __launch_bounds__(512, 1)
         tc_fence_after();
         auto issue_s = [&](uint32_t st) {  // S^T = K Q^T of the query block in stage st
           const uint32_t dq = kQ + ((st * L::kTile) >> 4);
-          if constexpr (D == 128) mma_ss8_w<2, kNextBox, 2, kNextBox>(tR0, kK, dq, kIdSq, 0u);
-          else mma_ss4_w<2, 0, 2, 0>(tR0, kK, dq, kIdSq, 0u);
-          mma_commit_w(s_full);
+          if constexpr (D == 128) mma_ss8_w<2, kNextBox, 2, kNextBox>(tR0, kK, dq, kIdSq, 0u, s_full);
+          else mma_ss4_w<2, 0, 2, 0>(tR0, kK, dq, kIdSq, 0u, s_full);
         };
-        if (!wait_w(q_full + q_stage(qit), q_phase(qit))) break;
-        fix_rows(0, aQ + q_stage(qit) * L::kTile);
+        // Q, dO of the walk's block `is`, the it-th of all, have landed
+        auto q_here = [&](int is, uint32_t it) -> bool {
+          if (!wait_w(q_full + q_stage(it), q_phase(it))) return false;
+          fix_rows(is, aQ + q_stage(it) * L::kTile);
+          return true;
+        };
+        auto do_here = [&](int is, uint32_t it) -> bool {
+          if (!wait_w(do_full + do_stage(it), do_phase(it))) return false;
+          fix_rows(is, aDO + do_stage(it) * L::kTile);
+          return true;
+        };
+        // d = 64, whose loads run ahead, waits for them before it waits for the softmax, so that a product follows that at
+        // once (12 288 tokens, 16/2 heads: 432 against 440 us; at d = 128 it would be 800 against 762)
+        constexpr bool kAhead = L::kDOStages > 1;
+        if (!q_here(0, qit)) break;
         tc_fence_after();
         issue_s(q_stage(qit));
+        if (kAhead && !do_here(0, qit)) break;
         for (int is = 0; is < sp.n; ++is) {
           const uint32_t st = q_stage(qit), ds = do_stage(qit);
-          if (!wait_w(do_full + ds, do_phase(qit))) { ok = false; break; }
-          fix_rows(is, aDO + ds * L::kTile);
+          const bool next = is + 1 < sp.n;
+          if (!kAhead && !do_here(is, qit)) { ok = false; break; }
           if (nblocks > 0 && !wait_w(dq_empty, (nblocks - 1) & 1)) { ok = false; break; }
           tc_fence_after();
           const uint32_t ddo = kDO + ((ds * L::kTile) >> 4);  // dP^T = V dO^T
-          if constexpr (D == 128) mma_ss8_w<2, kNextBox, 2, kNextBox>(tR1, kV, ddo, kIdSq, 0u);
-          else mma_ss4_w<2, 0, 2, 0>(tR1, kV, ddo, kIdSq, 0u);
-          mma_commit_w(dp_full);
+          if constexpr (D == 128) mma_ss8_w<2, kNextBox, 2, kNextBox>(tR1, kV, ddo, kIdSq, 0u, dp_full);
+          else mma_ss4_w<2, 0, 2, 0>(tR1, kV, ddo, kIdSq, 0u, dp_full);
+          if (kAhead && next && !q_here(is + 1, qit + 1)) { ok = false; break; }
           if (!wait_w(p_ready, nblocks & 1)) { ok = false; break; }
           tc_fence_after();
           // dV += P^T dO; P^T of rows 0-63 is packed by warpgroup 0 into R0's columns [0, 32), of rows 64-127 by
           // warpgroup 1 into [64, 96), each over S^T columns it has already read
-          mma_ts8_w<8, 32, 128, 0>(tdV, tR0, mDO + ((ds * L::kTile) >> 4), kIdKV, is > 0 ? 1u : 0u);
-          mma_commit_w(do_empty + ds);
-          if (is + 1 < sp.n) {
+          mma_ts8_w<8, 32, 128, 0>(tdV, tR0, mDO + ((ds * L::kTile) >> 4), kIdKV, is > 0 ? 1u : 0u, do_empty + ds);
+          if (next) {
             // S^T of the next block as soon as dV has read P^T out of R0 (products run in issue order)
-            const uint32_t st2 = q_stage(qit + 1);
-            if (!wait_w(q_full + st2, q_phase(qit + 1))) { ok = false; break; }
-            fix_rows(is + 1, aQ + st2 * L::kTile);
+            if (!kAhead && !q_here(is + 1, qit + 1)) { ok = false; break; }
             tc_fence_after();
-            issue_s(st2);
+            issue_s(q_stage(qit + 1));
           }
+          if (kAhead && next && !do_here(is + 1, qit + 1)) { ok = false; break; }
           if (!wait_w(ds_ready, nblocks & 1)) { ok = false; break; }
           tc_fence_after();
           // dQ = dS K (both operands MN-major), first: the drain starts on it
-          mma_ss8_w<128, 0, 128, 0>(tR1, mDS, mK, kIdDQ, 0u);
-          mma_commit_w(dq_full);
+          mma_ss8_w<128, 0, 128, 0>(tR1, mDS, mK, kIdDQ, 0u, dq_full);
           const uint32_t dq = mQ + ((st * L::kTile) >> 4), more = is > 0 ? 1u : 0u;  // dK += dS^T Q
-          if constexpr (L::kDSinTmem) mma_ts8_w<8, 0, 128, 0>(tdK, tmem + L::kDSCol, dq, kIdKV, more);
-          else mma_ss8_w<2, kNextBox, 128, 0>(tdK, kDS, dq, kIdKV, more);
-          mma_commit_w(q_empty + st);
+          if constexpr (L::kDSinTmem) mma_ts8_w<8, 0, 128, 0>(tdK, tmem + L::kDSCol, dq, kIdKV, more, q_empty + st);
+          else mma_ss8_w<2, kNextBox, 128, 0>(tdK, kDS, dq, kIdKV, more, q_empty + st);
           ++qit;
           ++nblocks;
         }

@@ -257,6 +257,32 @@ __device__ __forceinline__ void mma_ts8_w(uint32_t d_tmem, uint32_t a, uint32_t 
       "r"(a), "r"(b_lo), "r"(kSdescHi1024), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kA4), "n"(kB), "n"(kB4)
       : "memory");
 }
+// The same, and a commit to `bar`.
+template <int kA, int kA4, int kB, int kB4>
+__device__ __forceinline__ void mma_ts8_w(uint32_t d_tmem, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "add.u32 x, %1, 0 * %6;\n\tadd.u32 y, %2, 0 * %8;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, p;\n\t"
+      "add.u32 x, %1, 1 * %6;\n\tadd.u32 y, %2, 1 * %8;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+      "add.u32 x, %1, 2 * %6;\n\tadd.u32 y, %2, 2 * %8;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+      "add.u32 x, %1, 3 * %6;\n\tadd.u32 y, %2, 3 * %8;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+      "add.u32 x, %1, 4 * %6 + %7;\n\tadd.u32 y, %2, 4 * %8 + %9;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+      "add.u32 x, %1, 5 * %6 + %7;\n\tadd.u32 y, %2, 5 * %8 + %9;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+      "add.u32 x, %1, 6 * %6 + %7;\n\tadd.u32 y, %2, 6 * %8 + %9;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+      "add.u32 x, %1, 7 * %6 + %7;\n\tadd.u32 y, %2, 7 * %8 + %9;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%10];\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b_lo), "r"(kSdescHi1024), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kA4), "n"(kB), "n"(kB4), "r"(smem_u32(bar))
+      : "memory");
+}
 template <int kA, int kA4, int kB, int kB4>
 __device__ __forceinline__ void mma_ss8_w(uint32_t d_tmem, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -282,6 +308,32 @@ __device__ __forceinline__ void mma_ss8_w(uint32_t d_tmem, uint32_t a, uint32_t 
       "r"(a), "r"(b_lo), "r"(kSdescHi1024), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kA4), "n"(kB), "n"(kB4)
       : "memory");
 }
+// The same, and a commit to `bar`.
+template <int kA, int kA4, int kB, int kB4>
+__device__ __forceinline__ void mma_ss8_w(uint32_t d_tmem, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "add.u32 x, %1, 0 * %6;\n\tadd.u32 y, %2, 0 * %8;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t"
+      "add.u32 x, %1, 1 * %6;\n\tadd.u32 y, %2, 1 * %8;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "add.u32 x, %1, 2 * %6;\n\tadd.u32 y, %2, 2 * %8;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "add.u32 x, %1, 3 * %6;\n\tadd.u32 y, %2, 3 * %8;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "add.u32 x, %1, 4 * %6 + %7;\n\tadd.u32 y, %2, 4 * %8 + %9;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "add.u32 x, %1, 5 * %6 + %7;\n\tadd.u32 y, %2, 5 * %8 + %9;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "add.u32 x, %1, 6 * %6 + %7;\n\tadd.u32 y, %2, 6 * %8 + %9;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "add.u32 x, %1, 7 * %6 + %7;\n\tadd.u32 y, %2, 7 * %8 + %9;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%10];\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b_lo), "r"(kSdescHi1024), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kA4), "n"(kB), "n"(kB4), "r"(smem_u32(bar))
+      : "memory");
+}
 template <int kA, int kA4, int kB, int kB4>
 __device__ __forceinline__ void mma_ss4_w(uint32_t d_tmem, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -297,6 +349,24 @@ __device__ __forceinline__ void mma_ss4_w(uint32_t d_tmem, uint32_t a, uint32_t 
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
       "}" ::"r"(d_tmem),
       "r"(a), "r"(b_lo), "r"(kSdescHi1024), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kA4), "n"(kB), "n"(kB4)
+      : "memory");
+}
+// The same, and a commit to `bar`.
+template <int kA, int kA4, int kB, int kB4>
+__device__ __forceinline__ void mma_ss4_w(uint32_t d_tmem, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "add.u32 x, %1, 0 * %6;\n\tadd.u32 y, %2, 0 * %8;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t"
+      "add.u32 x, %1, 1 * %6;\n\tadd.u32 y, %2, 1 * %8;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "add.u32 x, %1, 2 * %6;\n\tadd.u32 y, %2, 2 * %8;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "add.u32 x, %1, 3 * %6;\n\tadd.u32 y, %2, 3 * %8;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%10];\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b_lo), "r"(kSdescHi1024), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kA4), "n"(kB), "n"(kB4), "r"(smem_u32(bar))
       : "memory");
 }
 
