@@ -33,9 +33,9 @@
 // What bounds it at d = 128: shared memory.  A block moves 288 KB of operands, 64 KB of Q and dO, 32 KB of dS and 128 KB of
 // staged dQ through it, 4096 cycles at 128 bytes a cycle, and a block was measured to take 4275 (2560 of them
 // products); 26 487 tokens, 16/2 heads: 1500 us, 1.28 PFLOP/s.  At d = 64 no one stage (timing-only builds of 12 288
-// tokens, 16/2 heads, 474 us: 471 without the loads of Q and dO, 462 with next to no dQ drain, 497 without exponentials, 443
+// tokens, 16/2 heads, when they took 474 us, 432 since: 471 without the loads of Q and dO, 462 with next to no dQ drain, 497 without exponentials, 443
 // without the reads of LSE and D): products with N = 64 take 62 cycles where 32 would do, and the warps'
-// loads and stores of shared memory wait behind their operands; a block takes 3000.
+// loads and stores of shared memory wait behind their operands.
 // Roles and budget: warps 0-7 softmax (two warpgroups), 8-11 dQ drain, 12 TMA, 13 MMA, 14-15 idle; launched with
 // 128 registers a thread, traded with setmaxnreg to 136 / 152 / 88, per sub-partition 2 x 136 + 152 + 88 = 4 x 128,
 // exactly the launch allocation.  TMEM (512 columns): R0 [0,128), R1 [128,256), dV [256,256+d), dK [384,384+d), and at

@@ -31,11 +31,11 @@
 // What bounds it: the chain of one sub-tile, S (512 cycles at d = 128), softmax (1300), PV (512) and the hand-overs between
 // them, 2970 cycles a step of two sub-tiles with 2048 of products; a softmax step is 64 pairs at 13 cycles (two
 // exponentials, scale, sum and rounding share the issue ports: 10.6 cycles a pair with two warps, measured apart) and the
-// row maximum.  One prompt of 16 384 tokens, 32/4 heads: 1.46 ms, 1.50 PFLOP/s, at the board's power limit.
+// row maximum.  One prompt of 16 384 tokens, 32/4 heads: 1.43 ms, 1.54 PFLOP/s, at the board's power limit.
 // Scores computed ahead of PV, which d = 64 has the TMEM columns for, were slower (8192 tokens, 20/4 heads: 225 us against
 // 195): both warpgroups then form exponentials at the same time instead of in turn.  So do the weights handed to PV in two
 // parts (packed batch 261 us against 249).
-// Single tokens over long caches are HBM-bound: 64 sequences, 1.5 GB of keys and values, 237 us, 6.5 TB/s.
+// Single tokens over long caches are HBM-bound: 64 sequences, 1.5 GB of keys and values, 237 to 240 us, 6.5 TB/s.
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 the two softmax warpgroups (thread = TMEM lane = row),
 // 8-11 output, 12 TMA, 13 MMA, 14 and 15 idle.  TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+d),
 // O1 [384,384+d).
