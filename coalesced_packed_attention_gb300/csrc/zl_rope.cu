@@ -44,6 +44,7 @@ struct RopeTensor {
   const __nv_bfloat16* g;  // backward: gradient of the forward's result
   __nv_bfloat16* out;
   const float* w;
+  const uint8_t* rows;                     // backward: 0 where a token has no gradient; null: every token has one
   int64_t x_stride, g_stride, out_stride;  // elements per token
   int32_t heads, batches;                  // batches of rope_unroll steps of 32 / (d / 8) heads
 };
@@ -153,10 +154,17 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
     const int h0 = (bi >= nb0 ? bi - nb0 : bi) * (kUnroll * kRows) + sub;
     const __nv_bfloat16* xp = T.x + tok * T.x_stride + (int64_t)h0 * D + e0;
     const __nv_bfloat16* gp = T.g + tok * T.g_stride + (int64_t)h0 * D + e0;
+    int heads = T.heads;
+    if constexpr (kBwd) {
+      if (T.rows != nullptr && T.rows[tok] == 0) heads = 0;
+    }
+    // What is not loaded has x = 1, g = 0: its norm is finite whatever eps is, so it adds 0 to the weights' gradients, and
+    // a token without a gradient gets 0
+    constexpr uint32_t kOnes = 0x3f803f80u;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const bool in = h0 + u * kRows < T.heads;
-      if constexpr (kHasX) v.x[u] = in ? load16(xp + u * kRows * D) : make_uint4(0u, 0u, 0u, 0u);
+      const bool in = h0 + u * kRows < heads;
+      if constexpr (kHasX) v.x[u] = in ? load16(xp + u * kRows * D) : make_uint4(kOnes, kOnes, kOnes, kOnes);
       if constexpr (kBwd) v.g[u] = in ? load16(gp + u * kRows * D) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
@@ -273,9 +281,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
               ss = fma2(x[i], x[i], ss);
               dot = fma2(dn[i], x[i], dot);
             }
-            // a lane without a head adds nothing, whatever eps makes of its zeros
-            float r = rsqrtf(fmaf(row_sum<kLanes>(ss.x + ss.y), 1.f / D, p.eps));
-            r = ok ? r : 0.f;
+            const float r = rsqrtf(fmaf(row_sum<kLanes>(ss.x + ss.y), 1.f / D, p.eps));
             const float m = row_sum<kLanes>(dot.x + dot.y) * (r * (1.f / D));  // mean(dn n)
             const float2 r2 = make_float2(r, r), nm2 = make_float2(-m, -m);
 #pragma unroll
@@ -506,9 +512,9 @@ extern "C" zl_status zl_qk_rope_fwd(const zl_qk_rope_desc* d, const void* q, int
   int sms = 0;
   if ((s = check_device(&sms)) != ZL_OK) return s;
   RopeParams p{};
-  p.t[0] = {static_cast<const __nv_bfloat16*>(q), nullptr, static_cast<__nv_bfloat16*>(q_out), q_weight, q_stride, 0,
+  p.t[0] = {static_cast<const __nv_bfloat16*>(q), nullptr, static_cast<__nv_bfloat16*>(q_out), q_weight, nullptr, q_stride, 0,
             q_out_stride, 0, 0};
-  p.t[1] = {static_cast<const __nv_bfloat16*>(k), nullptr, static_cast<__nv_bfloat16*>(k_out), k_weight, k_stride, 0,
+  p.t[1] = {static_cast<const __nv_bfloat16*>(k), nullptr, static_cast<__nv_bfloat16*>(k_out), k_weight, nullptr, k_stride, 0,
             k_out_stride, 0, 0};
   p.positions = positions;
   p.freq = freq;
@@ -554,9 +560,9 @@ extern "C" zl_status zl_qk_rope_bwd(const zl_qk_rope_desc* d, const void* q, int
   if ((s = check_device(&sms)) != ZL_OK) return s;
   RopeParams p{};
   p.t[0] = {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(dq_out), static_cast<__nv_bfloat16*>(dq),
-            q_weight, q_stride, dq_out_stride, dq_stride, 0, 0};
+            q_weight, d->q_rows, q_stride, dq_out_stride, dq_stride, 0, 0};
   p.t[1] = {static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(dk_out), static_cast<__nv_bfloat16*>(dk),
-            k_weight, k_stride, dk_out_stride, dk_stride, 0, 0};
+            k_weight, d->k_rows, k_stride, dk_out_stride, dk_stride, 0, 0};
   p.positions = positions;
   p.freq = freq;
   p.partial = dw ? static_cast<float*>(workspace) : nullptr;

@@ -42,7 +42,8 @@ class zl_qk_rope_desc(ctypes.Structure):
     _fields_ = [("n_tokens", ctypes.c_int64), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("rot_dim", ctypes.c_int32), ("half_layout", ctypes.c_int32), ("n_axes", ctypes.c_int32),
-                ("axis_pairs", ctypes.c_int32 * 3), ("amplitude", ctypes.c_float)]
+                ("axis_pairs", ctypes.c_int32 * 3), ("amplitude", ctypes.c_float),
+                ("q_rows", ctypes.c_void_p), ("k_rows", ctypes.c_void_p)]
 
 
 class zl_causal_seq(ctypes.Structure):
@@ -625,12 +626,18 @@ _dw_bytes: Dict[int, int] = {}  # workspace of the weights' gradients by head di
 
 def zl_qk_rope_bwd(q, k, dq_out, dk_out, dq, dk, positions, table: Optional[RotaryTable], norm: bool = False,
                    q_weight=None, k_weight=None, dq_weight=None, dk_weight=None, workspace=None, eps: float = 1e-6,
-                   stream=None):
+                   stream=None, q_rows=None, k_rows=None):
     """Gradient of zl_qk_rope_fwd: dq, dk from dq_out, dk_out.  With norm=True q and k are the
     forward's inputs (else None will do) and dq_weight, dk_weight, where given, receive the
-    weights' gradients (workspace: zl_qk_rope_workspace_bytes)."""
+    weights' gradients (workspace: zl_qk_rope_workspace_bytes).  q_rows, k_rows (uint8 [tokens]): a token whose
+    byte is 0 has gradient zero and adds nothing to the weights', whatever its rows hold."""
     torch = _torch()
     desc, dev, sq, sk, pos, freq, qw, kw = _rope_args(dq_out, dk_out, positions, table, norm, eps, q_weight, k_weight)
+    if q_rows is not None or k_rows is not None:
+        desc = zl_qk_rope_desc.from_buffer_copy(desc)  # the kept descriptor is of sizes alone
+        for name, rows in (("q_rows", q_rows), ("k_rows", k_rows)):
+            if rows is not None:
+                setattr(desc, name, _dense(rows, name, torch.uint8, (sq[0],), dev))
     pq, nq = _maybe_heads(q, "q", sq, dev) if norm else (None, 0)
     pk, nk = _maybe_heads(k, "k", sk, dev) if norm else (None, 0)
     gq, lq = _maybe_heads(dq_out, "dq_out", sq, dev)
@@ -666,6 +673,9 @@ class CausalPlan:
         _check(load_library().zl_causal_plan_workspace(self.handle, ctypes.byref(f), ctypes.byref(b)),
                "zl_causal_plan_workspace")
         self.fwd_workspace_bytes, self.bwd_workspace_bytes = f.value, b.value
+        # uint8 [tokens], 1 where a row belongs to a sequence's queries (keys); None where every row does
+        self.q_rows = self.kv_rows = None
+        self.kv_gaps = None  # int64, the rows whose kv_rows is 0
 
     def tiles(self, which: int = 0):
         """Schedule as (sequence, key head, block, first, end, part, thread block) tuples; which = 0
@@ -699,6 +709,14 @@ def causal_seqs(lengths: Sequence[int]):
     return out
 
 
+def _row_mask(ranges, tokens: int):
+    """uint8 [tokens], 1 in the rows [offset, offset + len) of any range."""
+    rows = bytearray(tokens)
+    for at, n in ranges:
+        rows[at:at + n] = b"\x01" * n
+    return _torch().frombuffer(rows, dtype=_torch().uint8)
+
+
 def zl_plan_causal(seqs: Sequence, n_q_heads: int, n_kv_heads: int, head_dim: int, q_tokens: int, kv_tokens: int,
                    flags: int = 0) -> CausalPlan:
     """Plan over seqs = [(q_offset, q_len, kv_offset, kv_len), ...] on the current device."""
@@ -713,7 +731,15 @@ def zl_plan_causal(seqs: Sequence, n_q_heads: int, n_kv_heads: int, head_dim: in
     device = _plan_device(flags)
     _check(L.zl_plan_causal(arr, len(seqs), n_q_heads, n_kv_heads, head_dim, q_tokens, kv_tokens, flags,
                             ctypes.byref(h)), "zl_plan_causal")
-    return CausalPlan(h.value, n_q_heads, n_kv_heads, head_dim, q_tokens, kv_tokens, device)
+    plan = CausalPlan(h.value, n_q_heads, n_kv_heads, head_dim, q_tokens, kv_tokens, device)
+    if device is not None and q_tokens == kv_tokens and not flags & ZL_PLAN_FORWARD_ONLY:
+        # what qkv_attention_backward needs of a plan that leaves rows out (ranges that overlap have no backward)
+        if sum(s[1] for s in seqs) < q_tokens:
+            plan.q_rows = _row_mask([(s[0], s[1]) for s in seqs], q_tokens).to(f"cuda:{device}")
+        if sum(s[3] for s in seqs) < kv_tokens:
+            plan.kv_rows = _row_mask([(s[2], s[3]) for s in seqs], kv_tokens).to(f"cuda:{device}")
+            plan.kv_gaps = (plan.kv_rows == 0).nonzero()[:, 0]
+    return plan
 
 
 def allocate_causal(plan: CausalPlan, device="cuda", backward: bool = False) -> Dict[str, "object"]:
@@ -812,18 +838,34 @@ def qkv_attention_forward(plan: CausalPlan, qkv, positions, table: Optional[Rota
     return bufs
 
 
+def _zero_rows(t, rows, stream):
+    """t[rows] = 0 on a stream given as the launches take it."""
+    torch = _torch()
+    if stream is None:
+        t.index_fill_(0, rows, 0.0)
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw_stream(stream, t.get_device()), t.device)
+    with torch.cuda.stream(stream):
+        t.index_fill_(0, rows, 0.0)
+
+
 def qkv_attention_backward(plan: CausalPlan, qkv, d_o, dqkv, positions, table: Optional[RotaryTable], scale: float,
                            bufs: dict, q_weight=None, k_weight=None, eps: float = 1e-6, stream=None) -> dict:
     """Gradient of qkv_attention_forward into dqkv (as qkv) and, with weights, bufs["dq_weight"] and
-    bufs["dk_weight"]."""
+    bufs["dk_weight"].  Rows of no sequence get zeros and add nothing to the weights', whatever qkv and d_o hold
+    there."""
     q, k, v = _qkv_views(plan, qkv)
     dq, dk, dv = _qkv_views(plan, dqkv, "dqkv")
     norm = q_weight is not None or k_weight is not None
     zl_causal_attn_bwd(plan, bufs["q"], bufs["k"], v, bufs["o"], d_o, bufs["lse"], bufs["dq"], bufs["dk"], dv,
                        bufs["workspace"], scale, stream)
+    if plan.kv_gaps is not None:
+        _zero_rows(dv, plan.kv_gaps, stream)
     zl_qk_rope_bwd(q, k, bufs["dq"], bufs["dk"], dq, dk, positions, table, norm, q_weight, k_weight,
                    bufs["dq_weight"] if q_weight is not None else None,
-                   bufs["dk_weight"] if k_weight is not None else None, bufs["rope_workspace"], eps, stream)
+                   bufs["dk_weight"] if k_weight is not None else None, bufs["rope_workspace"], eps, stream,
+                   plan.q_rows, plan.kv_rows)
     return bufs
 
 

@@ -406,6 +406,8 @@ typedef struct {
   int32_t n_axes;        /* position axes, 1 .. 3 (rot_dim > 0) */
   int32_t axis_pairs[3]; /* pairs turned by each axis, in order; they add up to rot_dim / 2 */
   float amplitude;       /* factor on the rotated channels (long-context scaling); 1 */
+  const uint8_t* q_rows; /* gradient only, device memory [n_tokens] or NULL (all rows): a token whose */
+  const uint8_t* k_rows; /* byte is 0 belongs to no sequence, see zl_qk_rope_bwd */
 } zl_qk_rope_desc;
 
 /* Radians per position -> the 64-bit fixed-point fraction of a turn per position that
@@ -438,6 +440,8 @@ ZL_API zl_status zl_qk_rope_fwd(const zl_qk_rope_desc* desc, const void* q, int6
  * otherwise).  dq_weight, dk_weight (fp32 [d], written; NULL: not wanted) need the
  * weight, and workspace of zl_qk_rope_workspace bytes.  dq may be dq_out, dk may be dk_out
  * (same stride).  The weights' sums over tokens and heads are taken in a fixed order.
+ * desc->q_rows, k_rows: where a token's byte is 0 its rows of dq (dk) are zero and it adds nothing to
+ * dq_weight (dk_weight), whatever dq_out and q (dk_out and k) hold there, NaN included.
  * Errors as zl_qk_rope_fwd. */
 ZL_API zl_status zl_qk_rope_bwd(const zl_qk_rope_desc* desc, const void* q, int64_t q_stride, const void* k,
                                 int64_t k_stride, const float* q_weight, const float* k_weight,

@@ -355,3 +355,8 @@ def test_forward_only_plans_have_no_backward():
     both, fwd = (zl.zl_plan_causal(seqs, 8, 2, 128, 4, 5900, zl.ZL_PLAN_HOST_ONLY | f) for f in (0, zl.ZL_PLAN_FORWARD_ONLY))
     assert fwd.tiles(0) == both.tiles(0) and fwd.fwd_workspace_bytes == both.fwd_workspace_bytes
     assert fwd.tiles(1) == [] and fwd.bwd_workspace_bytes == 0 and len(both.tiles(1)) > 0
+
+
+def test_row_masks_of_ranges():
+    assert zl._row_mask([(2, 3), (0, 0), (7, 1), (4, 2)], 9).tolist() == [0, 0, 1, 1, 1, 1, 0, 1, 0]
+    assert zl._row_mask([], 2).tolist() == [0, 0]

@@ -450,3 +450,78 @@ def test_projection_to_output_and_back():
         s = scale * kk[:, h] @ kk[:, h].T
         p = np.exp(s - s.max(1, keepdims=True))
         close(f64(fb["o"])[:t * hk * d].reshape(t, hk, d)[:, h], p / p.sum(1, keepdims=True) @ vv[:, h])
+
+
+def projection_reference(qkv, do, pos, w, radians, seqs, scale, hq, hk, eps=1e-6):
+    """In 64 bits: o, the gradient of qkv and the weights' gradients of norm (where w has a weight), rotation and attention
+    over seqs; rows of no sequence have gradient zero."""
+    d = qkv.shape[2]
+    x, g, ang = f64(qkv), np.nan_to_num(f64(do)), ref.angles(pos.numpy(), radians, [d // 2])
+    parts = [np.nan_to_num(y) for y in (x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:])]
+    normed = [parts[i] if w[i] is None else ref.rms_norm(parts[i], f64(w[i]), eps) for i in range(2)]
+    turned = [ref.rotate(y, ang, True) for y in normed]
+    o, _ = ref.attend(*turned, parts[2], seqs, scale)
+    grads = [np.nan_to_num(y) for y in ref.attend_grad(*turned, parts[2], g, seqs, scale)]
+    dqkv, dw = np.zeros_like(x), [None, None]
+    for i, cols in enumerate((slice(0, hq), slice(hq, hq + hk))):
+        dy = ref.rotate(grads[i], -ang, True)
+        if w[i] is None:
+            dqkv[:, cols] = dy
+        else:
+            dqkv[:, cols], dw[i] = ref.rms_norm_grad(parts[i], f64(w[i]), eps, dy)
+    dqkv[:, hq + hk:] = grads[2]
+    return o, dqkv, dw
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("seqs,t", [
+    ([(0, 90, 0, 90), (90, 41, 90, 41)], 160),                 # rows behind the last sequence
+    ([(3, 70, 3, 70), (100, 1, 100, 1), (128, 130, 128, 130)], 300),  # sequences padded to a common stride
+    ([(20, 50, 0, 80), (150, 30, 120, 20)], 200),              # rows that are keys alone, queries alone, neither
+])
+def test_projection_of_padded_batches(seqs, t, norm):
+    """Rows of no sequence hold NaN everywhere, outputs and scratch included: the gradient there is zero, and the weights'
+    gradients are those of the sequences' rows.  Bound as in test_projection_to_output_and_back, 3 a normwise."""
+    import torch
+    ensure_library()
+    hq, hk, d = 8, 2, 64
+    g = torch.Generator().manual_seed(t)
+    qkv = ((2 if norm else 1) * torch.randn(t, hq + 2 * hk, d, generator=g)).bfloat16()  # scores of size 1 either way
+    do = torch.randn(t, hq, d, generator=g).bfloat16()
+    w = 1 + 0.2 * torch.randn(2, d, generator=g)
+    pos = torch.randint(0, 500, (t, 1), generator=g).int()
+    in_q, in_k = np.zeros(t, bool), np.zeros(t, bool)
+    for q0, n, k0, m in seqs:
+        in_q[q0:q0 + n], in_k[k0:k0 + m] = True, True
+    qkv[:, :hq][torch.from_numpy(~in_q)] = float("nan")
+    qkv[:, hq:][torch.from_numpy(~in_k)] = float("nan")
+    do[torch.from_numpy(~in_q)] = float("nan")
+    radians, _ = zl.rotary_frequencies(d)
+    plan = zl.zl_plan_causal(seqs, hq, hk, d, t, t)
+    bufs = zl.allocate_qkv_attention(plan, "cuda", backward=True)
+    for n, b in bufs.items():
+        b.fill_(255 if n.endswith("workspace") else float("nan"))
+    dev, wd = qkv.cuda(), [w[0].cuda(), w[1].cuda()] if norm else [None, None]
+    dqkv = torch.full_like(dev, float("nan"))
+    args = (pos.cuda(), zl.rotary_table(radians))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        zl.qkv_attention_forward(plan, dev, *args, d ** -0.5, bufs, *wd, stream=stream)
+        zl.qkv_attention_backward(plan, dev, do.cuda(), dqkv, *args, d ** -0.5, bufs, *wd, stream=stream)
+        torch.cuda.synchronize()
+        assert zl.zl_causal_get_device_status(plan) == 0
+        o, want, dw = projection_reference(qkv, do, pos, [w[0], w[1]] if norm else [None, None], radians, seqs, d ** -0.5, hq, hk)
+        got = f64(dqkv)
+
+        def close(a, b):
+            assert np.linalg.norm(a - b) <= 3 * A * np.linalg.norm(b), np.linalg.norm(a - b) / np.linalg.norm(b)
+
+        close(f64(bufs["o"])[in_q], o[in_q])
+        assert (got[:, :hq][~in_q] == 0).all() and (got[:, hq:][~in_k] == 0).all()
+        for cols in (slice(0, hq), slice(hq, hq + hk), slice(hq + hk, None)):
+            close(got[:, cols], want[:, cols])
+        if norm:
+            close(f64(bufs["dq_weight"]), dw[0])
+            close(f64(bufs["dk_weight"]), dw[1])
+        dqkv.fill_(float("nan"))

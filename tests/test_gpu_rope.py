@@ -256,3 +256,47 @@ def test_python_refusals():
     with pytest.raises(ValueError):  # a workspace too small
         zl.zl_qk_rope_bwd(x, x, x.clone(), x.clone(), x.clone(), x.clone(), pos, table, True, w, w, dw, dw,
                           torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("n,hq,hk,d,norm,eps", [
+    (5, 3, 2, 64, True, EPS), (5, 3, 2, 64, True, 0.0), (700, 5, 1, 128, True, EPS), (700, 5, 1, 128, False, EPS),
+    (5000, 4, 2, 64, True, 0.0)])
+def test_tokens_without_a_gradient(n, hq, hk, d, norm, eps, half):
+    """Tokens marked as of no sequence: zero gradients, nothing in the weights', whatever their rows hold.  Equal, bit for
+    bit, to the call on rows of ones with zero gradients there, whose terms are exact zeros."""
+    import torch
+    ensure_library()
+    qkv, pos, w, go = inputs(n, hq, hk, d, 1, n)
+    g = torch.Generator().manual_seed(n + 1)
+    live = [(torch.rand(n, generator=g) < 0.7).to(torch.uint8) for _ in range(2)]
+    live[0][0], live[1][-1] = 0, 0
+    table = zl.rotary_table(zl.rotary_frequencies(d)[0], "half" if half else "interleaved")
+    heads = (slice(0, hq), slice(hq, hq + hk))
+    dirty, clean = (qkv.clone(), go.clone()), (qkv.clone(), go.clone())
+    for s, rows in zip(heads, live):
+        for x in dirty:
+            x[:, s][rows == 0] = float("nan")
+        clean[0][:, s][rows == 0] = 1.0
+        clean[1][:, s][rows == 0] = 0.0
+    wd, posd = w.cuda(), pos.cuda()
+    ws = torch.empty(zl.zl_qk_rope_workspace_bytes(n, hq, hk, d), dtype=torch.uint8, device="cuda")
+
+    def back(x, grad, rows):
+        x, grad = x.cuda(), grad.cuda()
+        out, dw = torch.full_like(grad, float("nan")), torch.full((2, d), float("nan"), device="cuda")
+        weights = (wd[0], wd[1], dw[0], dw[1]) if norm else (None,) * 4
+        zl.zl_qk_rope_bwd(x[:, heads[0]], x[:, heads[1]], grad[:, heads[0]], grad[:, heads[1]], out[:, heads[0]], out[:, heads[1]],
+                          posd, table, norm, *weights, ws, eps, q_rows=rows[0], k_rows=rows[1])
+        return out, dw
+
+    got, got_w = back(*dirty, [r.cuda() for r in live])
+    want, want_w = back(*clean, (None, None))
+    assert torch.equal(got, want) and (not norm or torch.equal(got_w, want_w))
+    for s, rows in zip(heads, live):
+        assert (got[:, s][rows.cuda() == 0] == 0).all()
+    one, _ = back(dirty[0], clean[1], (live[0].cuda(), None))  # queries alone
+    assert torch.equal(one[:, heads[0]], want[:, heads[0]])
+    for bad in (live[0], live[0].cuda()[:-1], live[0].cuda().int()):
+        with pytest.raises((TypeError, ValueError)):
+            back(*dirty, (bad, None))
