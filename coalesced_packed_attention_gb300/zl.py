@@ -827,13 +827,22 @@ def allocate_qkv_attention(plan: CausalPlan, device="cuda", backward: bool = Fal
     return out
 
 
+def _sides(q_weight, k_weight):
+    """(queries, keys, norm) of each launch of the rotation: both tensors in one, or, where one of them alone has a
+    weight and with it a norm, one after the other."""
+    if (q_weight is None) == (k_weight is None):
+        return ((True, True, q_weight is not None),)
+    return (True, False, q_weight is not None), (False, True, k_weight is not None)
+
+
 def qkv_attention_forward(plan: CausalPlan, qkv, positions, table: Optional[RotaryTable], scale: float, bufs: dict,
                           q_weight=None, k_weight=None, eps: float = 1e-6, stream=None) -> dict:
     """Causal self-attention from a projection's output qkv [tokens, Hq + 2 Hkv, d]: queries and keys
     normalised where weights are given, rotated, attended; the values are read where they lie."""
     q, k, v = _qkv_views(plan, qkv)
-    norm = q_weight is not None or k_weight is not None
-    zl_qk_rope_fwd(q, k, bufs["q"], bufs["k"], positions, table, norm, q_weight, k_weight, eps, stream)
+    for of_q, of_k, norm in _sides(q_weight, k_weight):
+        zl_qk_rope_fwd(q if of_q else None, k if of_k else None, bufs["q"] if of_q else None, bufs["k"] if of_k else None,
+                       positions, table, norm, q_weight if of_q else None, k_weight if of_k else None, eps, stream)
     zl_causal_attn_fwd(plan, bufs["q"], bufs["k"], v, bufs["o"], bufs["lse"], bufs["workspace"], scale, stream)
     return bufs
 
@@ -857,15 +866,16 @@ def qkv_attention_backward(plan: CausalPlan, qkv, d_o, dqkv, positions, table: O
     there."""
     q, k, v = _qkv_views(plan, qkv)
     dq, dk, dv = _qkv_views(plan, dqkv, "dqkv")
-    norm = q_weight is not None or k_weight is not None
     zl_causal_attn_bwd(plan, bufs["q"], bufs["k"], v, bufs["o"], d_o, bufs["lse"], bufs["dq"], bufs["dk"], dv,
                        bufs["workspace"], scale, stream)
     if plan.kv_gaps is not None:
         _zero_rows(dv, plan.kv_gaps, stream)
-    zl_qk_rope_bwd(q, k, bufs["dq"], bufs["dk"], dq, dk, positions, table, norm, q_weight, k_weight,
-                   bufs["dq_weight"] if q_weight is not None else None,
-                   bufs["dk_weight"] if k_weight is not None else None, bufs["rope_workspace"], eps, stream,
-                   plan.q_rows, plan.kv_rows)
+    for of_q, of_k, norm in _sides(q_weight, k_weight):
+        zl_qk_rope_bwd(q if of_q else None, k if of_k else None, bufs["dq"] if of_q else None, bufs["dk"] if of_k else None,
+                       dq if of_q else None, dk if of_k else None, positions, table, norm, q_weight if of_q else None,
+                       k_weight if of_k else None, bufs["dq_weight"] if of_q and norm else None,
+                       bufs["dk_weight"] if of_k and norm else None, bufs["rope_workspace"], eps, stream,
+                       plan.q_rows if of_q else None, plan.kv_rows if of_k else None)
     return bufs
 
 

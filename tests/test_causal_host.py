@@ -360,3 +360,9 @@ def test_forward_only_plans_have_no_backward():
 def test_row_masks_of_ranges():
     assert zl._row_mask([(2, 3), (0, 0), (7, 1), (4, 2)], 9).tolist() == [0, 0, 1, 1, 1, 1, 0, 1, 0]
     assert zl._row_mask([], 2).tolist() == [0, 0]
+
+
+def test_norm_is_of_the_sides_that_have_a_weight():
+    assert zl._sides(None, None) == ((True, True, False),) and zl._sides(1, 2) == ((True, True, True),)
+    assert zl._sides(1, None) == ((True, False, True), (False, True, False))
+    assert zl._sides(None, 1) == ((True, False, False), (False, True, True))

@@ -525,3 +525,42 @@ def test_projection_of_padded_batches(seqs, t, norm):
             close(f64(bufs["dq_weight"]), dw[0])
             close(f64(bufs["dk_weight"]), dw[1])
         dqkv.fill_(float("nan"))
+
+
+@pytest.mark.parametrize("side", [0, 1])
+def test_projection_with_one_weight_norms_that_side_alone(side):
+    """A weight for the queries alone (or the keys alone): the other tensor is rotated as it is.  Its heads are far from
+    unit size, so that a norm there would show; bound as in test_projection_to_output_and_back."""
+    import torch
+    ensure_library()
+    seqs, t, hq, hk, d = [(0, 90, 0, 90), (95, 40, 95, 40)], 140, 6, 2, 128
+    g = torch.Generator().manual_seed(side)
+    qkv = torch.randn(t, hq + 2 * hk, d, generator=g)
+    qkv[:, hq:hq + hk] *= 0.5 if side == 0 else 1.0
+    qkv[:, :hq] *= 0.5 if side == 1 else 1.0
+    qkv, do = qkv.bfloat16(), torch.randn(t, hq, d, generator=g).bfloat16()
+    w = [None, None]
+    w[side] = 1 + 0.2 * torch.randn(d, generator=g)
+    pos = torch.randint(0, 500, (t, 1), generator=g).int()
+    radians, _ = zl.rotary_frequencies(d)
+    plan = zl.zl_plan_causal(seqs, hq, hk, d, t, t)
+    bufs = zl.allocate_qkv_attention(plan, "cuda", backward=True)
+    for b in (bufs["dq_weight"], bufs["dk_weight"]):
+        b.fill_(7.0)
+    dev, wd = qkv.cuda(), [None if x is None else x.cuda() for x in w]
+    dqkv = torch.full_like(dev, float("nan"))
+    args = (pos.cuda(), zl.rotary_table(radians), d ** -0.5, bufs, *wd)
+    zl.qkv_attention_forward(plan, dev, *args)
+    zl.qkv_attention_backward(plan, dev, do.cuda(), dqkv, *args)
+    torch.cuda.synchronize()
+    o, want, dw = projection_reference(qkv, do, pos, w, radians, seqs, d ** -0.5, hq, hk)
+    used = np.r_[0:90, 95:135]
+
+    def close(a, b):
+        assert np.linalg.norm(a - b) <= 3 * A * np.linalg.norm(b), np.linalg.norm(a - b) / np.linalg.norm(b)
+
+    close(f64(bufs["o"])[used], o[used])
+    for cols in (slice(0, hq), slice(hq, hq + hk), slice(hq + hk, None)):
+        close(f64(dqkv)[:, cols], want[:, cols])
+    close(f64(bufs[("dq_weight", "dk_weight")[side]]), dw[side])
+    assert (bufs[("dk_weight", "dq_weight")[side]] == 7.0).all()  # not wanted: left as it was
