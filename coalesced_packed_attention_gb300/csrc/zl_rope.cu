@@ -95,6 +95,16 @@ __device__ __forceinline__ void partners(const uint4& v, int plane, float2 (&p)[
   }
 }
 
+// The words of `yes` whose pairs turn (the half layout: all of a lane's or none), of `no` the others: channels past the
+// rotated ones have no partner and pass through as they are, where a product with a sine of 0 would make NaN of an
+// Inf, their own or their neighbour's.
+template <bool kHalf>
+__device__ __forceinline__ uint4 where_turning(int e0, int rot, const uint4& yes, const uint4& no) {
+  constexpr int kStep = kHalf ? 0 : 2;
+  return make_uint4(e0 < rot ? yes.x : no.x, e0 + kStep < rot ? yes.y : no.y, e0 + 2 * kStep < rot ? yes.z : no.z,
+                    e0 + 3 * kStep < rot ? yes.w : no.w);
+}
+
 template <int kLanes>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -110,7 +120,10 @@ constexpr int rope_unroll() {
   return kBwd && kNorm ? 2 : 4;
 }
 
-template <int D, bool kHalf, bool kNorm, bool kBwd>
+// kPlain: every channel is rotated (rot = d) and every token has a gradient.  The selects that let the other channels
+// through and the look at a token's byte cost 2 to 4 % of a launch (49 144 tokens, 20/20 heads: gradient 257 against
+// 250 us), so they are compiled for the calls that have such channels or bytes alone.
+template <int D, bool kHalf, bool kNorm, bool kBwd, bool kPlain>
 __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a step
   constexpr int kUnroll = rope_unroll<kBwd, kNorm>();
@@ -155,16 +168,17 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
     const __nv_bfloat16* xp = T.x + tok * T.x_stride + (int64_t)h0 * D + e0;
     const __nv_bfloat16* gp = T.g + tok * T.g_stride + (int64_t)h0 * D + e0;
     int heads = T.heads;
-    if constexpr (kBwd) {
+    if constexpr (kBwd && !kPlain) {
       if (T.rows != nullptr && T.rows[tok] == 0) heads = 0;
     }
-    // What is not loaded has x = 1, g = 0: its norm is finite whatever eps is, so it adds 0 to the weights' gradients, and
-    // a token without a gradient gets 0
-    constexpr uint32_t kOnes = 0x3f803f80u;
+    // What is not loaded has g = 0 and x = 1, whose norm is finite whatever eps is: it adds 0 to the weights' gradients,
+    // and a token without a gradient gets 0.  (Plain calls take x = 0, which needs no register, and r = 0 below: gradient
+    // of 49 144 tokens, 20/20 heads, 250 against 254 us.)
+    constexpr uint32_t kFill = kPlain ? 0u : 0x3f803f80u;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const bool in = h0 + u * kRows < heads;
-      if constexpr (kHasX) v.x[u] = in ? load16(xp + u * kRows * D) : make_uint4(kOnes, kOnes, kOnes, kOnes);
+      if constexpr (kHasX) v.x[u] = in ? load16(xp + u * kRows * D) : make_uint4(kFill, kFill, kFill, kFill);
       if constexpr (kBwd) v.g[u] = in ? load16(gp + u * kRows * D) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
@@ -250,10 +264,18 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
       for (int u = 0; u < kUnroll; ++u) {
         const bool ok = h0 + u * kRows < T.heads;
         float2 o[4];
+        auto partner_values = [&](const uint4& v, float2 (&q)[4]) {
+          partners<kHalf>(v, plane, q);
+          if constexpr (kNorm && !kPlain) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (e0 + (kHalf ? 0 : 2 * i) >= p.rot) q[i] = make_float2(0.f, 0.f);
+          }
+        };
         if constexpr (!kBwd) {
           float2 x[4], q[4];
           unpack8(cur.x[u], x);
-          partners<kHalf>(cur.x[u], plane, q);
+          partner_values(cur.x[u], q);
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[i] = fma2(x[i], a[i], mul2(q[i], b[i]));
           if constexpr (kNorm) {
@@ -267,7 +289,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
         } else {
           float2 g[4], q[4], dy[4];
           unpack8(cur.g[u], g);
-          partners<kHalf>(cur.g[u], plane, q);
+          partner_values(cur.g[u], q);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dy[i] = fma2(g[i], cs2[i], mul2(q[i], sn2[i]));
           if constexpr (kNorm) {
@@ -281,7 +303,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
               ss = fma2(x[i], x[i], ss);
               dot = fma2(dn[i], x[i], dot);
             }
-            const float r = rsqrtf(fmaf(row_sum<kLanes>(ss.x + ss.y), 1.f / D, p.eps));
+            float r = rsqrtf(fmaf(row_sum<kLanes>(ss.x + ss.y), 1.f / D, p.eps));
+            if constexpr (kPlain) r = ok ? r : 0.f;  // a lane without a head adds nothing, whatever eps makes of its zeros
             const float m = row_sum<kLanes>(dot.x + dot.y) * (r * (1.f / D));  // mean(dn n)
             const float2 r2 = make_float2(r, r), nm2 = make_float2(-m, -m);
 #pragma unroll
@@ -301,7 +324,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) zl_qk_rope_kernel(const RopeP
             for (int i = 0; i < 4; ++i) o[i] = dy[i];
           }
         }
-        if (ok) *reinterpret_cast<uint4*>(op + u * kRows * D) = pack8(o);
+        if (ok) {
+          if constexpr (kNorm || kPlain) *reinterpret_cast<uint4*>(op + u * kRows * D) = pack8(o);
+          else *reinterpret_cast<uint4*>(op + u * kRows * D) = where_turning<kHalf>(e0, p.rot, pack8(o), kBwd ? cur.g[u] : cur.x[u]);
+        }
       }
       cur = nxt;
     }
@@ -387,10 +413,15 @@ zl_status check_tensor(const void* p, int64_t stride, int32_t heads, int32_t d) 
 
 using RopeKernel = void (*)(const RopeParams);
 
-template <int D, bool kBwd>
+template <int D, bool kBwd, bool kPlain>
 RopeKernel pick(bool half, bool norm) {
-  if (half) return norm ? zl_qk_rope_kernel<D, true, true, kBwd> : zl_qk_rope_kernel<D, true, false, kBwd>;
-  return norm ? zl_qk_rope_kernel<D, false, true, kBwd> : zl_qk_rope_kernel<D, false, false, kBwd>;
+  if (half) return norm ? zl_qk_rope_kernel<D, true, true, kBwd, kPlain> : zl_qk_rope_kernel<D, true, false, kBwd, kPlain>;
+  return norm ? zl_qk_rope_kernel<D, false, true, kBwd, kPlain> : zl_qk_rope_kernel<D, false, false, kBwd, kPlain>;
+}
+template <int D>
+RopeKernel pick(bool half, bool norm, bool bwd, bool plain) {
+  if (bwd) return plain ? pick<D, true, true>(half, norm) : pick<D, true, false>(half, norm);
+  return plain ? pick<D, false, true>(half, norm) : pick<D, false, false>(half, norm);
 }
 
 // Blocks that the weight gradients' workspace has rows for.
@@ -411,11 +442,11 @@ cudaError_t launch_rope(const zl_qk_rope_desc& d, bool bwd, int sms, RopeParams&
   p.axis2 = p.n_axes > 2 ? d.axis_pairs[0] + d.axis_pairs[1] : INT32_MAX;
   p.eps = d.eps;
   p.amplitude = d.amplitude;
-  RopeKernel k = D == 128 ? (bwd ? pick<128, true>(d.half_layout, d.norm) : pick<128, false>(d.half_layout, d.norm))
-                          : (bwd ? pick<64, true>(d.half_layout, d.norm) : pick<64, false>(d.half_layout, d.norm));
-  static PerDeviceInt resident[16];  // blocks per SM of each variant
+  const bool plain = d.rot_dim == D && !p.t[0].rows && !p.t[1].rows;
+  const RopeKernel k = D == 128 ? pick<128>(d.half_layout, d.norm, bwd, plain) : pick<64>(d.half_layout, d.norm, bwd, plain);
+  static PerDeviceInt resident[32];  // blocks per SM of each variant
   int per_sm = 0;
-  cudaError_t e = resident[(D == 128) * 8 + bwd * 4 + d.half_layout * 2 + d.norm].get(&per_sm, [&](int, int* v) {
+  cudaError_t e = resident[(D == 128) * 16 + plain * 8 + bwd * 4 + d.half_layout * 2 + d.norm].get(&per_sm, [&](int, int* v) {
     const cudaError_t r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, k, kRopeThreads, 0);
     if (*v < 1) *v = 1;
     return r;

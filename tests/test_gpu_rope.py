@@ -300,3 +300,38 @@ def test_tokens_without_a_gradient(n, hq, hk, d, norm, eps, half):
     for bad in (live[0], live[0].cuda()[:-1], live[0].cuda().int()):
         with pytest.raises((TypeError, ValueError)):
             back(*dirty, (bad, None))
+
+
+@pytest.mark.parametrize("half,rots", [(True, (0, 16, 32, 48)), (False, (0, 2, 6, 32, 62))])
+@pytest.mark.parametrize("d", [64, 128])
+def test_channels_past_the_rotated_ones_pass_through(half, rots, d):
+    """Inf, NaN and -0 there stay what they are, bit for bit, and reach no other channel; forward and gradient."""
+    import torch
+    ensure_library()
+    n, h = 37, 5
+    x = inputs(n, h, 1, d, 1, 2)[0][:, :h]
+    pos = torch.arange(n).int()[:, None].cuda()
+    bits = lambda t: t.cpu().view(torch.int16)  # noqa: E731
+    for rot in rots:
+        table = zl.rotary_table(zl.rotary_frequencies(rot)[0], "half" if half else "interleaved", amplitude=1.5) if rot else None
+        dirty = x.clone()
+        for i, bad in enumerate((float("inf"), float("-inf"), float("nan"), -0.0)):
+            dirty[i::5, i::3, rot + 1 + 3 * i::11] = bad
+        outs = {}
+        for name, y in (("clean", x), ("dirty", dirty)):
+            y = y.cuda()
+            outs[name] = [torch.empty_like(y), torch.empty_like(y)]
+            zl.zl_qk_rope_fwd(y, None, outs[name][0], None, pos, table)
+            zl.zl_qk_rope_bwd(None, None, y, None, outs[name][1], None, pos, table)
+        for c, o in zip(outs["clean"], outs["dirty"]):
+            assert torch.equal(bits(o)[..., rot:], dirty.view(torch.int16)[..., rot:])
+            assert torch.equal(bits(o)[..., :rot], bits(c)[..., :rot])
+        # norm: an Inf makes 1 / rms zero, and NaN of itself alone
+        lone = x.clone()
+        lone[:, :, rot + 1] = float("inf")
+        o = torch.empty_like(lone.cuda())
+        zl.zl_qk_rope_fwd(lone.cuda(), None, o, None, pos, table, True, None, None, EPS)
+        o = o.cpu()
+        assert torch.isnan(o[:, :, rot + 1]).all()
+        o[:, :, rot + 1] = 0.0
+        assert (o == 0).all()
