@@ -518,7 +518,8 @@ __global__ void __launch_bounds__(512, 1)
         const float* sLSE = sLD + 256 * (nblocks & 1);
         const float* sD = sLSE + 128;
         // first column (query row of the block) that sees this key; 128: none
-        const int first = key_ok ? max(0, (key - (tl.kv_len - tl.q_len) - sp.block(is) * tb) * p.group) : 128;
+        // (clamped before the product: over 2^31 / group keys behind the block it would not fit)
+        const int first = key_ok ? max(0, key - (tl.kv_len - tl.q_len) - sp.block(is) * tb) * p.group : 128;
         if (!__all_sync(0xffffffffu, cbwait(s_full, nblocks & 1, abort_flag, p.wait_limit, p.status))) { ok = false; break; }
         tc_fence_after();
         float pr[64];

@@ -564,3 +564,39 @@ def test_projection_with_one_weight_norms_that_side_alone(side):
         close(f64(dqkv)[:, cols], want[:, cols])
     close(f64(bufs[("dq_weight", "dk_weight")[side]]), dw[side])
     assert (bufs[("dk_weight", "dq_weight")[side]] == 7.0).all()  # not wanted: left as it was
+
+
+def test_gradient_far_behind_the_query():
+    """128 query heads of one token over more than 2^24 keys: the distance times the group passes 2^31.  The keys are zero, so
+    every weight is 1 / m and dV is the same row for every key; a few values at both ends make dK.  Bounds as at the
+    head of this file."""
+    import torch
+    ensure_library()
+    m, hq, d, ends = 2 ** 24 + 200, 128, 64, 300
+    scale = d ** -0.5
+    q, _, v, do = inputs(1, 2 * ends, hq, 1, d, 31)
+    big = torch.zeros(2, m, 1, d, dtype=torch.bfloat16, device="cuda")
+    big[1, :ends], big[1, -ends:] = v[:ends].cuda(), v[ends:].cuda()
+    plan = zl.zl_plan_causal([(0, 1, 0, m)], hq, 1, d, 1, m)
+    b = zl.allocate_causal(plan, backward=True)
+    for n in ("dk", "dv"):
+        b[n].fill_(float("nan"))
+    zl.zl_causal_attn_fwd(plan, q.cuda(), big[0], big[1], b["o"], b["lse"], b["workspace"], scale)
+    zl.zl_causal_attn_bwd(plan, q.cuda(), big[0], big[1], b["o"], do.cuda(), b["lse"], b["dq"], b["dk"], b["dv"], b["workspace"], scale)
+    torch.cuda.synchronize()
+    assert zl.zl_causal_get_device_status(plan) == 0
+    Q, V, G = f64(q)[0], f64(v)[:, 0], f64(do)[0]
+    p, ep = 1 / m, 2.0 ** -20 * (2 + np.log(m))
+    assert np.abs(f64(b["lse"])[0] - np.log(m)).max() <= 2.0 ** -20 * (1 + np.log(m))
+    o, t_o = p * V.sum(0), A * p * np.abs(V.sum(0)) + (A + ep) * p * np.abs(V).sum(0)
+    dv = p * G.sum(0)
+    got = f64(b["dv"][0, 0])
+    assert (np.abs(got - dv) <= (A + ep) * p * np.abs(G).sum(0) * (1 + 2.0 ** -10) + A * np.abs(dv)).all()
+    assert torch.equal(b["dv"], b["dv"][:1].expand_as(b["dv"]))
+    dd, t_d = G @ o, np.abs(G) @ (t_o + d * F * np.abs(o))
+    ds = p * (G @ V.T - dd[:, None])  # [heads, keys of both ends]
+    t_ds = (A + ep) * np.abs(ds) + p * (1 + A) * (t_d[:, None] + d * F * np.abs(G) @ np.abs(V).T)
+    dk, t_dk = scale * ds.T @ Q, scale * t_ds.T @ np.abs(Q)
+    got = np.concatenate([f64(b["dk"][:ends, 0]), f64(b["dk"][-ends:, 0])])
+    assert (np.abs(got - dk) <= t_dk * (1 + 2.0 ** -10) + A * np.abs(dk) + 1e-30).all()
+    assert (b["dq"] == 0).all()
