@@ -415,8 +415,10 @@ __global__ void __launch_bounds__(512, 1)
         mma_commit_w(kv_done);
         mma_commit_w(kv_empty);
       }
+      // every product has ended before the block's memory goes back, after a wait that gave up too (that wait returns at
+      // once; a bounded one of its own then)
       mma_commit_w(drain);
-      wait_w(drain, 0);
+      if (!wait_w(drain, 0)) mbar_wait(drain, 0);
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ dQ drain warpgroup (thread = query row)

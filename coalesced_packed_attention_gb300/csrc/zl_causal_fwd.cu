@@ -350,8 +350,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int w = 0; w < 2; ++w)
           if (pend_w[w] && !issue_pv(w)) break;
       }
+      // every product has ended before the block's memory goes back, after a wait that gave up too (that wait returns at
+      // once; a bounded one of its own then)
       mma_commit_w(drain);
-      wait_w(drain, 0);
+      if (!wait_w(drain, 0)) mbar_wait(drain, 0);
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ output warpgroup (thread = row of a sub-tile)

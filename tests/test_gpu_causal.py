@@ -600,3 +600,20 @@ def test_gradient_far_behind_the_query():
     got = np.concatenate([f64(b["dk"][:ends, 0]), f64(b["dk"][-ends:, 0])])
     assert (np.abs(got - dk) <= t_dk * (1 + 2.0 ** -10) + A * np.abs(dk) + 1e-30).all()
     assert (b["dq"] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_launches_behind_one_that_gave_up_are_right(d):
+    """Blocks that gave up a wait have handed back their products, copies and tensor memory: the launches behind them in
+    the stream, on the same SMs, are right."""
+    seqs, hq, hk = packed(400, 130, 70), 8, 2
+    good = Case(seqs, hq, hk, d, seed=6)
+    bad = zl.zl_plan_causal(seqs, hq, hk, d, 600, 600, zl.ZL_PLAN_TEST_WITHHOLD_LOAD)
+    b, (q, k, v, do) = zl.allocate_causal(bad, backward=True), good.dev
+    for _ in range(3):
+        zl.zl_causal_attn_fwd(bad, q, k, v, b["o"], b["lse"], b["workspace"], good.scale)
+        good.forward()
+        zl.zl_causal_attn_bwd(bad, q, k, v, good.bufs["o"], do, good.bufs["lse"], b["dq"], b["dk"], b["dv"], b["workspace"], good.scale)
+        good.backward()
+        assert zl.zl_causal_get_device_status(bad) == zl.ZL_ERR_TIMEOUT
+    good.check()
