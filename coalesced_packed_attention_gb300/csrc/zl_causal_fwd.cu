@@ -376,7 +376,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const bool row_ok = rt < sp.toks[w];
         float2 st = make_float2(0.f, kNegInf);  // no key: O = 0, LSE = -inf
         if (sp.n[w] > 0) {
-          if (!__all_sync(0xffffffffu, cwait(stat_full + w, it[w] & 1, abort_flag, lim, p.status) &&
+          // this wait alone lasts a whole tile, up to 2^24 steps of 3200 cycles: 64 times the limit (a role that is stuck
+          // gives up at its own limit, and that ends this wait as well)
+          if (!__all_sync(0xffffffffu, cwait(stat_full + w, it[w] & 1, abort_flag, lim << 6, p.status) &&
                                            cwait(o_full + w, it[w] & 1, abort_flag, lim, p.status))) { ok = false; break; }
           ++it[w];
           st = sStat[128 * w + r];

@@ -617,3 +617,23 @@ def test_launches_behind_one_that_gave_up_are_right(d):
         good.backward()
         assert zl.zl_causal_get_device_status(bad) == zl.ZL_ERR_TIMEOUT
     good.check()
+
+
+def test_tiles_that_take_longer_than_a_wait_may():
+    """152 tiles of 256 rows over 2^26 keys each: no range is split, and a tile takes longer (0.7 s) than a wait between two
+    steps may.  Keys and values are zero, so O = 0 and LSE = ln of the keys seen."""
+    import torch
+    ensure_library()
+    n, m, d = 152 * 256, 2 ** 26, 64
+    plan = zl.zl_plan_causal([(0, n, 0, m)], 1, 1, d, n, m, zl.ZL_PLAN_FORWARD_ONLY)
+    tiles = plan.tiles(0)
+    assert all(t[5] < 0 for t in tiles) and len({t[6] for t in tiles}) == len(tiles) == 152
+    zeros = torch.zeros(m, 1, d, dtype=torch.bfloat16, device="cuda")
+    b = zl.allocate_causal(plan)
+    b["o"].fill_(float("nan"))
+    b["lse"].fill_(float("nan"))
+    zl.zl_causal_attn_fwd(plan, zeros[:n], zeros, zeros, b["o"], b["lse"], b["workspace"], 0.125)
+    torch.cuda.synchronize()
+    assert zl.zl_causal_get_device_status(plan) == 0
+    want = np.log(m - n + 1 + np.arange(n))
+    assert (b["o"] == 0).all() and np.abs(f64(b["lse"])[:, 0] - want).max() <= 2.0 ** -20 * (1 + want.max())
