@@ -142,6 +142,17 @@ cudaError_t launch_causal_bwd(int head_dim, const CUtensorMap& tq, const CUtenso
                               const CUtensorMap& tdo, const CausalBwdParams& p, int grid, bool early, cudaStream_t stream);
 cudaError_t launch_causal_finish(int head_dim, const CausalFinishParams& p, int num_sms, cudaStream_t stream);
 
+// A plan's tables in device memory.  They belong to the plan and to every graph that captured a launch from it, so that a
+// graph may be replayed after its plan is gone.
+struct CausalTables {
+  void* ptr = nullptr;
+  int device = -1;
+  std::atomic<int32_t> owners{1};
+  CausalTables* next = nullptr;  // in the list of those without owners
+};
+// Where the stream is being captured, makes its graph an owner of the plan's tables.
+zl_status hold_tables(const zl_causal_plan* p, cudaStream_t stream);
+
 }  // namespace zl
 
 struct zl_causal_plan {
@@ -165,7 +176,7 @@ struct zl_causal_plan {
   int64_t acc_blocks = 0;
   int64_t fwd_bytes = 0, bwd_bytes = 0;
 
-  void* dev_blob = nullptr;
+  zl::CausalTables* tables = nullptr;
   zl::CausalSeq* d_seqs = nullptr;
   zl::CausalTile* d_fwd_tiles = nullptr;
   int32_t* d_fwd_ptr = nullptr;

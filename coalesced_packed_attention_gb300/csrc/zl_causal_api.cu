@@ -56,7 +56,7 @@ bool row_map(CUtensorMap* m, const void* base, int64_t tokens, int64_t stride, i
 
 // A plan that can be launched, with the device it was built on current.
 bool ready(const zl_causal_plan* p) {
-  if (!p || p->host_only || !p->dev_blob) return false;
+  if (!p || p->host_only || !p->tables) return false;
   int dev = -1;
   return cudaGetDevice(&dev) == cudaSuccess && dev == p->device;
 }
@@ -115,6 +115,7 @@ extern "C" zl_status zl_causal_attn_fwd(const zl_causal_plan* p, const void* q, 
   fp.part_o = static_cast<float*>(workspace);
   fp.part_lse = fp.part_o + (int64_t)p->slots * 256 * p->head_dim;
   fp.scale_log2 = scale * 1.44269504088896340736f;
+  if ((s = hold_tables(p, st)) != ZL_OK) return s;
   if (launch_causal_fwd(p->head_dim, tq, tk, tv, fp, (int)p->fwd_ptr.size() - 1, p->fwd_short, st) != cudaSuccess) return ZL_ERR_CUDA;
   if (p->merges.empty()) return ZL_OK;
   CausalMergeParams mp;
@@ -153,6 +154,7 @@ extern "C" zl_status zl_causal_attn_bwd(const zl_causal_plan* p, const void* q, 
   const int64_t rows = p->q_tokens * p->n_q_heads;
   float* acc = row_d + (rows * 4 + 255) / 256 * 64;
   float* part = acc + p->acc_blocks * 128 * d;
+  if ((s = hold_tables(p, st)) != ZL_OK) return s;
   if (rows > 0 && launch_causal_bwd_pre(d, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), row_d,
                                         rows, acc, p->acc_blocks * 128 * d, p->num_sms, st) != cudaSuccess)
     return ZL_ERR_CUDA;

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <mutex>
 #include <new>
 #include <utility>
 
@@ -343,6 +344,43 @@ void put(std::vector<char>* blob, size_t at, const std::vector<T>& v) {
   if (!v.empty()) std::memcpy(blob->data() + at, v.data(), v.size() * sizeof(T));
 }
 
+// Tables that no plan and no graph owns any more.  The last owner may be a graph, whose end is told on a thread that must
+// not call CUDA, so they are freed by the next plan that is made or destroyed.
+std::mutex dead_lock;
+CausalTables* dead = nullptr;
+
+void disown(void* tables) {
+  CausalTables* t = static_cast<CausalTables*>(tables);
+  if (t->owners.fetch_sub(1, std::memory_order_acq_rel) != 1) return;
+  std::lock_guard<std::mutex> lock(dead_lock);
+  t->next = dead;
+  dead = t;
+}
+
+void free_dead() {
+  CausalTables* list;
+  {
+    std::lock_guard<std::mutex> lock(dead_lock);
+    list = dead;
+    dead = nullptr;
+  }
+  if (!list) return;
+  // a plan may go while this thread captures a stream, which a plain cudaFree would spoil
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+  int dev = -1;
+  const bool known = cudaGetDevice(&dev) == cudaSuccess;
+  while (list) {
+    CausalTables* t = list;
+    list = t->next;
+    if (known && t->device != dev) cudaSetDevice(t->device);
+    if (t->ptr) cudaFree(t->ptr);
+    if (known && t->device != dev) cudaSetDevice(dev);
+    delete t;
+  }
+  if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
+}
+
 zl_status upload_causal(zl_causal_plan* p) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -366,17 +404,19 @@ zl_status upload_causal(zl_causal_plan* p) {
   put(&blob, o_bp, p->bwd_ptr);
   put(&blob, o_m, p->merges);
   put(&blob, o_bm, p->bwd_merges);
-  if (cudaMalloc(&p->dev_blob, at) != cudaSuccess) {
-    p->dev_blob = nullptr;
+  p->tables = new CausalTables;
+  p->tables->device = p->device;
+  if (cudaMalloc(&p->tables->ptr, at) != cudaSuccess) {
+    p->tables->ptr = nullptr;
     cudaGetLastError();
     return ZL_ERR_NO_MEMORY;
   }
   // the copy from pageable memory may still be on its way when the call returns; launches on other streams
   // do not wait for it, so it is awaited here
-  if (cudaMemcpy(p->dev_blob, blob.data(), at, cudaMemcpyHostToDevice) != cudaSuccess ||
+  if (cudaMemcpy(p->tables->ptr, blob.data(), at, cudaMemcpyHostToDevice) != cudaSuccess ||
       cudaStreamSynchronize(nullptr) != cudaSuccess)
     return ZL_ERR_CUDA;
-  char* base = static_cast<char*>(p->dev_blob);
+  char* base = static_cast<char*>(p->tables->ptr);
   p->d_status = reinterpret_cast<int32_t*>(base + o_status);
   p->d_seqs = reinterpret_cast<CausalSeq*>(base + o_seqs);
   p->d_fwd_tiles = reinterpret_cast<CausalTile*>(base + o_ft);
@@ -438,6 +478,24 @@ zl_status build(const zl_causal_seq* seqs, int32_t n_seqs, uint32_t flags, zl_ca
 
 }  // namespace
 
+zl_status zl::hold_tables(const zl_causal_plan* p, cudaStream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  cudaGraph_t graph = nullptr;
+  if (cudaStreamGetCaptureInfo(stream, &status, nullptr, &graph) != cudaSuccess) return ZL_ERR_CUDA;
+  if (status != cudaStreamCaptureStatusActive) return ZL_OK;
+  cudaUserObject_t object;
+  p->tables->owners.fetch_add(1, std::memory_order_relaxed);
+  if (cudaUserObjectCreate(&object, p->tables, disown, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
+    disown(p->tables);
+    return ZL_ERR_CUDA;
+  }
+  if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) != cudaSuccess) {
+    cudaUserObjectRelease(object, 1);
+    return ZL_ERR_CUDA;
+  }
+  return ZL_OK;
+}
+
 extern "C" zl_status zl_plan_causal(const zl_causal_seq* seqs, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
                                     int32_t head_dim, int64_t q_tokens, int64_t kv_tokens, uint32_t flags,
                                     zl_causal_plan** out) {
@@ -461,6 +519,7 @@ extern "C" zl_status zl_plan_causal(const zl_causal_seq* seqs, int32_t n_seqs, i
   p->test_withhold = flags & ZL_PLAN_TEST_WITHHOLD_LOAD;
   p->forward_only = flags & ZL_PLAN_FORWARD_ONLY;
   p->num_sms = 152;
+  free_dead();
   zl_status s = ZL_OK;
   if (!p->host_only) {
     int major = 0, minor = 0;
@@ -491,13 +550,8 @@ extern "C" zl_status zl_plan_causal(const zl_causal_seq* seqs, int32_t n_seqs, i
 
 extern "C" void zl_causal_plan_destroy(zl_causal_plan* p) {
   if (!p) return;
-  if (p->dev_blob) {
-    int dev = -1;
-    const bool other = cudaGetDevice(&dev) == cudaSuccess && dev != p->device;
-    if (other) cudaSetDevice(p->device);
-    cudaFree(p->dev_blob);
-    if (other) cudaSetDevice(dev);
-  }
+  if (p->tables) disown(p->tables);
+  free_dead();
   delete p;
 }
 

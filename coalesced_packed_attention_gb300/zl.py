@@ -673,7 +673,8 @@ class CausalPlan:
         _check(load_library().zl_causal_plan_workspace(self.handle, ctypes.byref(f), ctypes.byref(b)),
                "zl_causal_plan_workspace")
         self.fwd_workspace_bytes, self.bwd_workspace_bytes = f.value, b.value
-        # uint8 [tokens], 1 where a row belongs to a sequence's queries (keys); None where every row does
+        # uint8 [tokens], 1 where a row belongs to a sequence's queries (keys); None where every row does.  Tensors as any
+        # other: a graph that captured qkv_attention_backward needs the plan object kept for them.
         self.q_rows = self.kv_rows = None
         self.kv_gaps = None  # int64, the rows whose kv_rows is 0
 

@@ -483,7 +483,9 @@ typedef struct zl_causal_plan zl_causal_plan;
 ZL_API zl_status zl_plan_causal(const zl_causal_seq* seqs, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
                                 int32_t head_dim, int64_t q_tokens, int64_t kv_tokens, uint32_t flags,
                                 zl_causal_plan** out);
-/* Free a plan; NULL is ignored.  No launch that uses it may still be running. */
+/* Free a plan; NULL is ignored.  No launch that uses it may still be running.  A graph that captured launches from
+ * the plan holds the plan's device tables and may be replayed afterwards; they are freed when the graph and its
+ * executables are gone and the next causal plan is made or destroyed. */
 ZL_API void zl_causal_plan_destroy(zl_causal_plan* plan);
 /* Device scratch that the forward (0 where no key range is split) and the backward need;
  * one buffer of the larger size serves both in turn.  Any pointer may be NULL. */

@@ -637,3 +637,64 @@ def test_tiles_that_take_longer_than_a_wait_may():
     assert zl.zl_causal_get_device_status(plan) == 0
     want = np.log(m - n + 1 + np.arange(n))
     assert (b["o"] == 0).all() and np.abs(f64(b["lse"])[:, 0] - want).max() <= 2.0 ** -20 * (1 + want.max())
+
+
+def test_a_graph_outlives_its_plan():
+    """A captured forward and gradient is replayed after its plan is gone and others have taken its place in memory; the
+    plan goes once before the capture's end, once after."""
+    import gc
+    import torch
+    seqs, hq, hk, d = [(0, 1, 0, 9000), (1, 40, 9000, 40)], 8, 2, 128
+    for early in (False, True):
+        c = Case(seqs, hq, hk, d, seed=12)
+        c.forward().backward()  # whatever a kernel sets up at its first launch
+        never_launched = zl.zl_plan_causal(seqs, hq, hk, d, 41, 9040)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.forward()
+            never_launched.destroy()  # frees its memory at once, which must not spoil the capture
+            c.backward()
+            if early:
+                c.plan.destroy()
+        if not early:
+            c.plan.destroy()
+        for n in ("o", "lse", "dq", "dk", "dv"):
+            c.bufs[n].fill_(float("nan"))
+        others = [zl.zl_plan_causal(packed(*range(k, k + 40)), hq, hk, d, 4000, 4000) for k in range(1, 20)]
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        c.plan = zl.zl_plan_causal(seqs, hq, hk, d, 41, 9040)
+        c.check()
+        del g, others
+        gc.collect()
+
+
+def test_tables_of_graphs_and_plans_that_are_gone_are_freed():
+    import gc
+    import torch
+    seqs, d = [(0, 1, 0, 2 ** 22)], 64  # 32 768 key tiles, tables of 1.6 MB
+    k = torch.zeros(2 ** 22, 1, d, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(1, 1, d, dtype=torch.bfloat16, device="cuda")
+
+    def once():
+        plan = zl.zl_plan_causal(seqs, 1, 1, d, 1, 2 ** 22)
+        b = zl.allocate_causal(plan)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            zl.zl_causal_attn_fwd(plan, q, k, k, b["o"], b["lse"], b["workspace"], 0.125)
+        del plan
+        g.replay()
+        torch.cuda.synchronize()
+
+    free = []
+    for i in range(120):
+        once()
+        gc.collect()
+        if i in (40, 119):
+            torch.cuda.synchronize()
+            torch.cuda.empty_cache()
+            zl.zl_plan_causal([], 1, 1, d, 0, 0)
+            free.append(torch.cuda.mem_get_info()[0])
+    assert free[0] - free[1] < 32 * 2 ** 20  # 79 plans of 2 MB and more came and went
