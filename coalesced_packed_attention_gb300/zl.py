@@ -528,7 +528,16 @@ class RotaryTable:
 
     def __post_init__(self):
         object.__setattr__(self, "axis_pairs", tuple(self.axis_pairs))
-        if self.freq is not None:
+        if self.freq is None:
+            if self.rot_dim != 0:
+                raise ValueError(f"freq: needed where rot_dim is {self.rot_dim}")
+        else:
+            # kernels read rot_dim / 2 numbers from here
+            torch = _torch()
+            if not isinstance(self.freq, torch.Tensor) or self.freq.dtype is not torch.int64:
+                raise TypeError(f"freq: expected a tensor of {torch.int64}, got {getattr(self.freq, 'dtype', type(self.freq))}")
+            if self.freq.dim() != 1 or not self.freq.is_contiguous() or 2 * self.freq.numel() != self.rot_dim:
+                raise ValueError(f"freq: expected {self.rot_dim} / 2 contiguous numbers, got shape {tuple(self.freq.shape)}")
             object.__setattr__(self, "device", self.freq.get_device())
             object.__setattr__(self, "ptr", self.freq.data_ptr())
 

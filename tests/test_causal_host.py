@@ -366,3 +366,16 @@ def test_norm_is_of_the_sides_that_have_a_weight():
     assert zl._sides(None, None) == ((True, True, False),) and zl._sides(1, 2) == ((True, True, True),)
     assert zl._sides(1, None) == ((True, False, True), (False, True, False))
     assert zl._sides(None, 1) == ((True, False, False), (False, True, True))
+
+
+def test_a_rotary_table_holds_a_number_for_every_pair():
+    """The kernels read rot_dim / 2 of them: a table whose tensor is shorter, or of another type or layout, is refused."""
+    import dataclasses
+    import torch
+    table = zl.rotary_table([1.0, 0.5, 0.25, 0.125], "interleaved", device="cpu")
+    for bad in (dict(rot_dim=16), dict(rot_dim=16, axis_pairs=(8,)), dict(rot_dim=4, axis_pairs=(2,)), dict(freq=table.freq[:2]),
+                dict(freq=torch.arange(8)[::2]), dict(freq=table.freq.view(2, 2)), dict(freq=table.freq.int()),
+                dict(freq=table.freq.double()), dict(freq=[1, 2, 3, 4]), dict(freq=None)):
+        with pytest.raises((TypeError, ValueError)):
+            dataclasses.replace(table, **bad)
+    assert dataclasses.replace(table, axis_pairs=(2, 2)).axis_pairs == (2, 2)
