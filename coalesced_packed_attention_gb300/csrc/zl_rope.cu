@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(1024) zl_qk_rope_dw_kernel(const float* partia
   }
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
 
 zl_status check_desc(const zl_qk_rope_desc* d) {
   if (!d) return ZL_ERR_INVALID_ARG;
@@ -409,6 +410,12 @@ zl_status check_tensor(const void* p, int64_t stride, int32_t heads, int32_t d) 
   if (!p || stride < (int64_t)heads * d) return ZL_ERR_INVALID_ARG;
   if (!aligned16(p) || stride % 8) return ZL_ERR_ALIGN;
   return ZL_OK;
+}
+
+// What is read number by number: weights, positions, frequencies.
+bool numbers_aligned(const float* qw, const float* kw, const int32_t* positions, const uint64_t* freq) {
+  return aligned(qw, sizeof(float)) && aligned(kw, sizeof(float)) && aligned(positions, sizeof(int32_t)) &&
+         aligned(freq, sizeof(uint64_t));
 }
 
 using RopeKernel = void (*)(const RopeParams);
@@ -540,6 +547,7 @@ extern "C" zl_status zl_qk_rope_fwd(const zl_qk_rope_desc* d, const void* q, int
       (d->n_kv_heads > 0 && !same_rows(k, k_stride, k_out, k_out_stride, d->n_tokens)))
     return ZL_ERR_INVALID_ARG;
   if (d->rot_dim > 0 && (!positions || !freq)) return ZL_ERR_INVALID_ARG;
+  if (!numbers_aligned(q_weight, k_weight, positions, freq)) return ZL_ERR_ALIGN;
   int sms = 0;
   if ((s = check_device(&sms)) != ZL_OK) return s;
   RopeParams p{};
@@ -587,6 +595,8 @@ extern "C" zl_status zl_qk_rope_bwd(const zl_qk_rope_desc* d, const void* q, int
       (d->n_kv_heads > 0 && !same_rows(dk_out, dk_out_stride, dk, dk_stride, d->n_tokens)))
     return ZL_ERR_INVALID_ARG;
   if (d->rot_dim > 0 && (!positions || !freq)) return ZL_ERR_INVALID_ARG;
+  if (!numbers_aligned(q_weight, k_weight, positions, freq) || !numbers_aligned(dq_weight, dk_weight, nullptr, nullptr))
+    return ZL_ERR_ALIGN;
   int sms = 0;
   if ((s = check_device(&sms)) != ZL_OK) return s;
   RopeParams p{};

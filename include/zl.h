@@ -429,7 +429,7 @@ ZL_API zl_status zl_qk_rope_workspace(const zl_qk_rope_desc* desc, int64_t* byte
  * One pass; fp32 arithmetic, rounded once.  Uses no state: calls on different streams
  * are independent.  ZL_ERR_INVALID_ARG for a bad descriptor, a missing pointer, a stride
  * below heads * d, an output on its input at another stride, or weights without norm; ZL_ERR_ALIGN for a base that is not 16-byte
- * aligned or a stride that is not a multiple of 8. */
+ * aligned, a stride that is not a multiple of 8, or weights, positions or frequencies off their type's alignment. */
 ZL_API zl_status zl_qk_rope_fwd(const zl_qk_rope_desc* desc, const void* q, int64_t q_stride, const void* k,
                                 int64_t k_stride, const float* q_weight, const float* k_weight,
                                 const int32_t* positions, const uint64_t* freq, void* q_out, int64_t q_out_stride,

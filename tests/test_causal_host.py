@@ -379,3 +379,15 @@ def test_a_rotary_table_holds_a_number_for_every_pair():
         with pytest.raises((TypeError, ValueError)):
             dataclasses.replace(table, **bad)
     assert dataclasses.replace(table, axis_pairs=(2, 2)).axis_pairs == (2, 2)
+
+
+def test_rope_numbers_off_their_alignment_are_refused(lib):
+    """Weights, positions and frequencies are read number by number: a pointer off their type's alignment would fault."""
+    d = ctypes.byref(_desc())
+    fwd = [16, 256, 16, 128, 16, 16, 16, 16, 16, 256, 16, 128, None]
+    bwd = [16, 256, 16, 128, 16, 16, 16, 16, 16, 256, 16, 128, 16, 256, 16, 128, 16, 16, 16, None]
+    for i, off in ((4, 18), (5, 17), (6, 18), (7, 20)):  # weights, positions, frequencies
+        for fn, args in ((lib.zl_qk_rope_fwd, fwd), (lib.zl_qk_rope_bwd, bwd)):
+            assert fn(d, *args[:i], off, *args[i + 1:]) == zl.ZL_ERR_ALIGN
+    for i in (16, 17):  # weights' gradients
+        assert lib.zl_qk_rope_bwd(d, *bwd[:i], 18, *bwd[i + 1:]) == zl.ZL_ERR_ALIGN
