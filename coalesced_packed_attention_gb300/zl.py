@@ -489,9 +489,12 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[st
       "linear"  every frequency divided by the factor (positions pressed together);
       "ntk"     the base raised so that the slowest pair is divided by the factor, the
                 fastest kept;
-      "yarn"    pairs that turn more than `fast` times in original_len positions kept, those
-                under `slow` turns divided by the factor, a ramp over the turns between;
-                amplitude 0.1 ln(factor) + 1."""
+      "yarn"    the first pairs kept, the last divided by the factor, a ramp over the pair's index
+                between: from the pair that turns `fast` times in original_len positions, rounded
+                down, to the one that turns `slow` times, rounded up; amplitude 0.1 ln(factor) + 1.
+                (As released checkpoints were trained.  A ramp over the number of turns, as the method is
+                also written, gives other frequencies between, up to 3 times at factor 16;
+                rotary_table takes those, or any.)"""
     import math
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError(f"rot_dim: expected an even number from 2 on, got {rot_dim}")
@@ -505,9 +508,16 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[st
     if scaling == "linear":
         return [f / factor for f in freqs], 1.0
     if scaling == "yarn":
+        if not (base > 1 and slow > 0):
+            raise ValueError("yarn: expected base > 1 and slow > 0")
+
+        def pair_of(turns):  # original_len base^(-2i / rot_dim) / (2 pi) = turns
+            return rot_dim * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(base))
+
+        first, last = max(0, math.floor(pair_of(fast))), min(rot_dim - 1, math.ceil(pair_of(slow)))
         out = []
-        for f in freqs:
-            keep = min(1.0, max(0.0, (original_len * f / (2 * math.pi) - slow) / (fast - slow)))
+        for i, f in enumerate(freqs):
+            keep = 1.0 - min(1.0, max(0.0, (i - first) / max(last - first, 1e-3)))
             out.append(f * keep + f / factor * (1 - keep))
         return out, 0.1 * math.log(factor) + 1.0
     raise ValueError(f"scaling: expected None, 'linear', 'ntk' or 'yarn', got {scaling!r}")

@@ -391,3 +391,25 @@ def test_rope_numbers_off_their_alignment_are_refused(lib):
             assert fn(d, *args[:i], off, *args[i + 1:]) == zl.ZL_ERR_ALIGN
     for i in (16, 17):  # weights' gradients
         assert lib.zl_qk_rope_bwd(d, *bwd[:i], 18, *bwd[i + 1:]) == zl.ZL_ERR_ALIGN
+
+
+def test_yarn_ramps_over_the_pairs():
+    """As released checkpoints do.  128 channels, base 10 000, 4096 positions: 128 ln(4096 / (2 pi 32)) / (2 ln 10 000) = 20.9,
+    with 1 for 32 turns 45.03: pairs to 20 kept, from 46 on divided, 1 / 26 a pair between."""
+    plain, _ = zl.rotary_frequencies(128)
+    yarn, amp = zl.rotary_frequencies(128, scaling="yarn", factor=16.0, original_len=4096)
+    assert abs(amp - 1.2772588722239782) < 1e-15
+    kept = [(y / f - 1 / 16) / (15 / 16) for f, y in zip(plain, yarn)]
+    assert all(abs(k - 1) < 1e-12 for k in kept[:21]) and all(abs(k) < 1e-12 for k in kept[46:])
+    assert all(abs(kept[20 + i] - (1 - i / 26)) < 1e-12 for i in range(27))
+    # 64 channels, base 500 000, 8192 positions, factor 8: pairs 9.04 -> 9 to 17.50 -> 18
+    plain, _ = zl.rotary_frequencies(64, base=500000.0)
+    yarn, _ = zl.rotary_frequencies(64, base=500000.0, scaling="yarn", factor=8.0, original_len=8192)
+    kept = [(y / f - 1 / 8) / (7 / 8) for f, y in zip(plain, yarn)]
+    assert abs(kept[9] - 1) < 1e-12 and abs(kept[10] - 8 / 9) < 1e-12 and abs(kept[17] - 1 / 9) < 1e-12 and abs(kept[18]) < 1e-12
+    # a context so short that the first pair already turns too seldom: divided from pair 0 (or 1) on, nothing negative
+    yarn, _ = zl.rotary_frequencies(16, scaling="yarn", factor=2.0, original_len=4)
+    assert all(abs(y * 2 / f - 1) < 1e-12 for f, y in list(zip(zl.rotary_frequencies(16)[0], yarn))[1:])
+    for bad in (dict(base=1.0), dict(slow=0.0)):
+        with pytest.raises(ValueError):
+            zl.rotary_frequencies(16, scaling="yarn", **bad)
