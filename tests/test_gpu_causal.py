@@ -698,3 +698,79 @@ def test_tables_of_graphs_and_plans_that_are_gone_are_freed():
             zl.zl_plan_causal([], 1, 1, d, 0, 0)
             free.append(torch.cuda.mem_get_info()[0])
     assert free[0] - free[1] < 32 * 2 ** 20  # 79 plans of 2 MB and more came and went
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Queries, outputs and gradients behind 2^31 elements, in views of a fused projection: the same rows at offset 0 give
+    the same bits (dQ within its bound), and the rows in front stay as they were; the rotation of all of them as well."""
+    import torch
+    lens, hq, hk, d, rows = (300, 1, 77), 16, 2, 128, 1_060_000
+    c = Case(packed(*lens), hq, hk, d, seed=41).forward().backward()
+    t, at = sum(lens), rows - sum(lens)
+    assert at * hq * d > 2 ** 31
+    fused = torch.full((rows, hq + 2 * hk, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    grads = torch.full_like(fused, float("nan"))
+    o, do = (torch.full((rows, hq, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cut = lambda x: [x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]]  # noqa: E731
+    for dst, src in zip([*cut(fused), do], c.dev):
+        dst[at:] = src
+    plan = zl.zl_plan_causal([(q0 + at, n, k0 + at, m) for q0, n, k0, m in c.seqs], hq, hk, d, rows, rows)
+    lse = torch.full((rows, hq), float("nan"), device="cuda")
+    ws = torch.empty(max(plan.fwd_workspace_bytes, plan.bwd_workspace_bytes), dtype=torch.uint8, device="cuda")
+    zl.zl_causal_attn_fwd(plan, *cut(fused), o, lse, ws, c.scale)
+    zl.zl_causal_attn_bwd(plan, *cut(fused), o, do, lse, *cut(grads), ws, c.scale)
+    torch.cuda.synchronize()
+    assert zl.zl_causal_get_device_status(plan) == 0
+    far = dict(zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *cut(grads))))
+    for n, x in far.items():
+        assert n == "dq" or torch.equal(x[at:], c.bufs[n]), n
+        assert all(torch.isnan(y).all() for y in x[:at].split(100_000)), n
+        c.bufs[n].copy_(x[at:])
+    c.check()
+    table = zl.rotary_table(zl.rotary_frequencies(d)[0])
+    pos = torch.arange(rows, device="cuda").int()[:, None]
+    w = 1 + 0.2 * torch.randn(2, d, device="cuda")
+    q, k, _ = cut(fused)
+    gq, gk, _ = cut(grads)
+    zl.zl_qk_rope_fwd(q, k, gq, gk, pos, table, True, w[0], w[1])
+    near = torch.empty_like(fused[at:])
+    zl.zl_qk_rope_fwd(q[at:], k[at:], *cut(near)[:2], pos[at:], table, True, w[0], w[1])
+    assert torch.equal(grads[at:, :hq + hk], near[:, :hq + hk])
+    zl.zl_qk_rope_bwd(q, k, gq, gk, gq, gk, pos, table, True, w[0], w[1])
+    zl.zl_qk_rope_bwd(q[at:], k[at:], *cut(near)[:2], *cut(near)[:2], pos[at:], table, True, w[0], w[1])
+    assert torch.equal(grads[at:, :hq + hk], near[:, :hq + hk])
+
+
+@pytest.mark.parametrize("lens,hq,hk,d", [
+    ((5000, 3000, 4100, 2900), 16, 8, 128), ((2600, 5000, 3000, 4100, 2600, 4999, 5001, 3000), 8, 8, 64)])
+def test_large_batches(lens, hq, hk, d):
+    """Batches that are launched plainly (100 us and more), whose tiles are taken sequence by sequence and many to a thread
+    block, against the reference: all rows of some key heads."""
+    import torch
+    ensure_library()
+    t, group, seqs, scale = sum(lens), hq // hk, packed(*lens), d ** -0.5
+    ins = inputs(t, t, hq, hk, d, t)
+    dev = [x.cuda() for x in ins]
+    plan = zl.zl_plan_causal(seqs, hq, hk, d, t, t)
+    for which in (0, 1):
+        tiles = plan.tiles(which)
+        per = [[x[4] - x[3] for x in tiles if x[6] == b] for b in range(152)]
+        assert min(len(p) for p in per) >= 3 and all(x[5] < 0 for x in tiles)
+        assert any(p != sorted(p, reverse=True) for p in per)  # not longest first over all
+    b = zl.allocate_causal(plan, backward=True)
+    zl.zl_causal_attn_fwd(plan, *dev[:3], b["o"], b["lse"], b["workspace"], scale)
+    zl.zl_causal_attn_bwd(plan, *dev[:3], b["o"], dev[3], b["lse"], b["dq"], b["dk"], b["dv"], b["workspace"], scale)
+    torch.cuda.synchronize()
+    assert zl.zl_causal_get_device_status(plan) == 0
+    for s, c in ((0, 0), (1, hk - 1), (len(lens) - 1, hk // 2)):
+        q0, n, _, _ = seqs[s]
+        hs, ks = slice(c * group, (c + 1) * group), slice(c, c + 1)
+        part = [f64(x[q0:q0 + n, h]) for x, h in zip(ins, (hs, ks, ks, hs))]
+        want, tol, var = bounds(*part, [(0, n, 0, n)], scale)
+        for name in ("o", "lse", "dq", "dk", "dv"):
+            got = f64(b[name][q0:q0 + n, ks if name in ("dk", "dv") else hs])
+            over = np.abs(got - want[name]) - tol[name]
+            assert over.max() <= 0, f"{name}: {over.max():.3e} over its bound"
+            if name != "lse":
+                off, rms = np.linalg.norm(got - want[name]), np.sqrt(var[name].sum())
+                assert off <= (1.1 + 4 / np.sqrt(got.shape[0] * got.shape[1])) * rms, f"{name}: {off / rms:.2f} times the expected error"
