@@ -32,8 +32,8 @@
 //
 // What bounds it at d = 128: shared memory.  A block moves 288 KB of operands, 64 KB of Q and dO, 32 KB of dS and 128 KB of
 // staged dQ through it, 4096 cycles at 128 bytes a cycle, and a block was measured to take 4275 (2560 of them
-// products); 26 487 tokens, 16/2 heads: 1500 us, 1.28 PFLOP/s.  At d = 64 no one stage (timing-only builds of 12 288
-// tokens, 16/2 heads, when they took 474 us, 432 since: 471 without the loads of Q and dO, 462 with next to no dQ drain, 497 without exponentials, 443
+// products); 26 487 tokens, 16/2 heads: 1470 to 1500 us, 1.28 PFLOP/s.  At d = 64 no one stage (timing-only builds of 8192 +
+// 4096 tokens, 16/2 heads, when they took 474 us, 432 since: 471 without the loads of Q and dO, 462 with next to no dQ drain, 497 without exponentials, 443
 // without the reads of LSE and D): products with N = 64 take 62 cycles where 32 would do, and the warps'
 // loads and stores of shared memory wait behind their operands.
 // Roles and budget: warps 0-7 softmax (two warpgroups), 8-11 dQ drain, 12 TMA, 13 MMA, 14-15 idle; launched with
@@ -63,7 +63,7 @@ struct CausalBwdLayout {
   static constexpr int kV = kK + kTile;
   // d = 128 fills the shared memory with two stages of Q and one of dO; at d = 64 there is room to load further ahead
   // (with two and one the products waited for Q and dO 500 of a block's 3500 cycles; with three or four of dO
-  // nothing waits less, and 12 288 tokens, 16/2 heads, took 460 and 465 us against 451)
+  // nothing waits less, and 8192 + 4096 tokens, 16/2 heads, took 460 and 465 us against 451)
   static constexpr int kQStages = D == 64 ? 4 : 2;
   static constexpr int kDOStages = D == 64 ? 2 : 1;
   static constexpr int kQ = kV + kTile;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(512, 1)
           return true;
         };
         // d = 64, whose loads run ahead, waits for them before it waits for the softmax, so that a product follows that at
-        // once (12 288 tokens, 16/2 heads: 432 against 440 us; at d = 128 it would be 800 against 762)
+        // once (8192 + 4096 tokens, 16/2 heads: 432 against 440 us; at d = 128 it would be 800 against 762)
         constexpr bool kAhead = L::kDOStages > 1;
         if (!q_here(0, qit)) break;
         tc_fence_after();

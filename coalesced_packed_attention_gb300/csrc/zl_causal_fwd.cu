@@ -31,7 +31,7 @@
 // What bounds it: the chain of one sub-tile, S (512 cycles at d = 128), softmax (1300), PV (512) and the hand-overs between
 // them, 2970 cycles a step of two sub-tiles with 2048 of products; a softmax step is 64 pairs at 13 cycles (two
 // exponentials, scale, sum and rounding share the issue ports: 10.6 cycles a pair with two warps, measured apart) and the
-// row maximum.  One prompt of 16 384 tokens, 32/4 heads: 1.43 ms, 1.54 PFLOP/s, at the board's power limit.
+// row maximum.  One prompt of 16 384 tokens, 32/4 heads: 1.43 to 1.46 ms, 1.5 PFLOP/s, at the board's power limit.
 // Scores computed ahead of PV, which d = 64 has the TMEM columns for, were slower (8192 tokens, 20/4 heads: 225 us against
 // 195): both warpgroups then form exponentials at the same time instead of in turn.  So do the weights handed to PV in two
 // parts (packed batch 261 us against 249).
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         return __all_sync(0xffffffffu, cwait(b, parity, abort_flag, lim, p.status));
       };
       // Q of the next tile is waited for ahead of the weights of this tile's last block at d = 64, behind them at d = 128
-      // (12 288 tokens, 16/2 heads, ahead against behind: 176 and 181 us at d = 64, 239 and 228 at d = 128)
+      // (8192 + 4096 tokens, 16/2 heads, ahead against behind: 176 and 181 us at d = 64, 239 and 228 at d = 128)
       constexpr bool kQAhead = D == 64;
       // the block whose PV is still to be issued
       bool pend = false, pend_w[2] = {false, false}, first = false, last[2] = {false, false};

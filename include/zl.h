@@ -426,7 +426,8 @@ ZL_API zl_status zl_qk_rope_workspace(const zl_qk_rope_desc* desc, int64_t* byte
  *   other overlap).  A tensor with 0 heads may be NULL.
  *   q_weight, k_weight: fp32 [d] or NULL.  positions: int32 [n_tokens, n_axes], any
  *   value.  freq: uint64 [rot_dim / 2] from zl_rope_frequencies, in device memory.
- * One pass; fp32 arithmetic, rounded once.  Uses no state: calls on different streams
+ * One pass; fp32 arithmetic, rounded once (the squares' sum too: a row with values past some 10^18 has a norm of
+ * infinity).  Channels past the rotated ones without norm are copied bit for bit.  Uses no state: calls on different streams
  * are independent.  ZL_ERR_INVALID_ARG for a bad descriptor, a missing pointer, a stride
  * below heads * d, an output on its input at another stride, or weights without norm; ZL_ERR_ALIGN for a base that is not 16-byte
  * aligned, a stride that is not a multiple of 8, or weights, positions or frequencies off their type's alignment. */
@@ -487,7 +488,9 @@ ZL_API zl_status zl_plan_causal(const zl_causal_seq* seqs, int32_t n_seqs, int32
  * the plan holds the plan's device tables and may be replayed afterwards; they are freed when the graph and its
  * executables are gone and the next causal plan is made or destroyed. */
 ZL_API void zl_causal_plan_destroy(zl_causal_plan* plan);
-/* Device scratch that the forward (0 where no key range is split) and the backward need;
+/* Device scratch that the forward (0 where no key range is split) and the backward need
+ * (for each sequence and key head whole blocks of 128 rows x d fp32: much more than dQ itself
+ * where sequences times heads a key head are far under 128 rows);
  * one buffer of the larger size serves both in turn.  Any pointer may be NULL. */
 ZL_API zl_status zl_causal_plan_workspace(const zl_causal_plan* plan, int64_t* fwd_bytes, int64_t* bwd_bytes);
 /* The schedule: which = 0 forward, 1 backward.  *n = tiles; up to cap tiles as 7 int32
