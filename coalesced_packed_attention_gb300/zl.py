@@ -870,12 +870,9 @@ def qkv_attention_forward(plan: CausalPlan, qkv, positions, table: Optional[Rota
 def _zero_rows(t, rows, stream):
     """t[rows] = 0 on a stream given as the launches take it."""
     torch = _torch()
-    if stream is None:
-        t.index_fill_(0, rows, 0.0)
-        return
-    if not isinstance(stream, torch.cuda.Stream):
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_raw_stream(stream, t.get_device()), t.device)
-    with torch.cuda.stream(stream):
+    with torch.no_grad(), torch.cuda.stream(stream):  # None: the current one
         t.index_fill_(0, rows, 0.0)
 
 

@@ -524,6 +524,10 @@ def test_projection_of_padded_batches(seqs, t, norm):
         if norm:
             close(f64(bufs["dq_weight"]), dw[0])
             close(f64(bufs["dk_weight"]), dw[1])
+        leaf = torch.full_like(dev, float("nan")).requires_grad_()  # a buffer that autograd knows is written like any other
+        zl.qkv_attention_backward(plan, dev, do.cuda(), leaf, *args, d ** -0.5, bufs, *wd, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(leaf.detach()[:, hq + hk:], dqkv[:, hq + hk:])
         dqkv.fill_(float("nan"))
 
 
