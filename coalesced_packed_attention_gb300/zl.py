@@ -508,10 +508,12 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[st
     if scaling == "linear":
         return [f / factor for f in freqs], 1.0
     if scaling == "yarn":
-        if not (base > 1 and slow > 0):
-            raise ValueError("yarn: expected base > 1 and slow > 0")
+        if not (base > 1 and fast > 0):
+            raise ValueError("yarn: expected base > 1 and fast > 0")
 
         def pair_of(turns):  # original_len base^(-2i / rot_dim) / (2 pi) = turns
+            if turns <= 0:  # no pair turns as seldom
+                return rot_dim
             return rot_dim * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(base))
 
         first, last = max(0, math.floor(pair_of(fast))), min(rot_dim - 1, math.ceil(pair_of(slow)))
@@ -544,10 +546,11 @@ class RotaryTable:
         else:
             # kernels read rot_dim / 2 numbers from here
             torch = _torch()
-            if not isinstance(self.freq, torch.Tensor) or self.freq.dtype is not torch.int64:
+            if not isinstance(self.freq, torch.Tensor) or self.freq.dtype not in (torch.int64, torch.uint64):
                 raise TypeError(f"freq: expected a tensor of {torch.int64}, got {getattr(self.freq, 'dtype', type(self.freq))}")
-            if self.freq.dim() != 1 or not self.freq.is_contiguous() or 2 * self.freq.numel() != self.rot_dim:
-                raise ValueError(f"freq: expected {self.rot_dim} / 2 contiguous numbers, got shape {tuple(self.freq.shape)}")
+            if not self.freq.is_contiguous() or 2 * self.freq.numel() < self.rot_dim:
+                raise ValueError(f"freq: needs {self.rot_dim} / 2 contiguous numbers, got shape {tuple(self.freq.shape)}, "
+                                 f"strides {self.freq.stride()}")
             object.__setattr__(self, "device", self.freq.get_device())
             object.__setattr__(self, "ptr", self.freq.data_ptr())
 

@@ -373,12 +373,13 @@ def test_a_rotary_table_holds_a_number_for_every_pair():
     import dataclasses
     import torch
     table = zl.rotary_table([1.0, 0.5, 0.25, 0.125], "interleaved", device="cpu")
-    for bad in (dict(rot_dim=16), dict(rot_dim=16, axis_pairs=(8,)), dict(rot_dim=4, axis_pairs=(2,)), dict(freq=table.freq[:2]),
-                dict(freq=torch.arange(8)[::2]), dict(freq=table.freq.view(2, 2)), dict(freq=table.freq.int()),
-                dict(freq=table.freq.double()), dict(freq=[1, 2, 3, 4]), dict(freq=None)):
+    for bad in (dict(rot_dim=16), dict(rot_dim=16, axis_pairs=(8,)), dict(freq=table.freq[:3]),
+                dict(freq=torch.arange(8)[::2]), dict(freq=table.freq.int()), dict(freq=table.freq.double()),
+                dict(freq=[1, 2, 3, 4]), dict(freq=None)):
         with pytest.raises((TypeError, ValueError)):
             dataclasses.replace(table, **bad)
     assert dataclasses.replace(table, axis_pairs=(2, 2)).axis_pairs == (2, 2)
+    assert dataclasses.replace(table, rot_dim=4, axis_pairs=(2,)).rot_dim == 4  # its first pairs alone
 
 
 def test_rope_numbers_off_their_alignment_are_refused(lib):
@@ -410,6 +411,10 @@ def test_yarn_ramps_over_the_pairs():
     # a context so short that the first pair already turns too seldom: divided from pair 0 (or 1) on, nothing negative
     yarn, _ = zl.rotary_frequencies(16, scaling="yarn", factor=2.0, original_len=4)
     assert all(abs(y * 2 / f - 1) < 1e-12 for f, y in list(zip(zl.rotary_frequencies(16)[0], yarn))[1:])
-    for bad in (dict(base=1.0), dict(slow=0.0)):
+    # no pair turns 0 times: the ramp ends past the last pair, at 127 (the channels less one)
+    open_end, _ = zl.rotary_frequencies(128, scaling="yarn", factor=16.0, original_len=4096, slow=0.0)
+    plain, _ = zl.rotary_frequencies(128)
+    assert abs((open_end[63] / plain[63] - 1 / 16) / (15 / 16) - (1 - 43 / 107)) < 1e-12
+    for bad in (dict(base=1.0), dict(slow=-2.0, fast=-1.0)):
         with pytest.raises(ValueError):
             zl.rotary_frequencies(16, scaling="yarn", **bad)
