@@ -37,6 +37,20 @@ class PerDeviceInt {
   std::atomic<int> v_[kDevices] = {};
 };
 
+// SM count of the current device; the kernels are built for sm_103a alone.
+inline zl_status check_device(int* sms) {
+  static PerDeviceInt count;
+  const cudaError_t e = count.get(sms, [](int dev, int* v) {
+    int major = 0, minor = 0;
+    cudaError_t r = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (r == cudaSuccess) r = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (r == cudaSuccess) r = cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
+    if (major != 10 || minor != 3) *v = -1;
+    return r;
+  });
+  return e != cudaSuccess ? ZL_ERR_CUDA : *sms > 0 ? ZL_OK : ZL_ERR_UNSUPPORTED;
+}
+
 // Query rows are packed by key head: the `group` query heads that share a key head are neighbours, so a
 // block of up to 128 rows is (tokens x group) with row r = token r / group, head r % group.  A block holds
 // tokens_per_block(group) whole tokens; its rows past tokens x group are never stored.

@@ -1,0 +1,754 @@
+// Attention of new tokens over the 4-bit cache.
+//
+// With the group's query heads of all new tokens as rows r of one key head:
+//   S[key, r] = scale K Q^T,  P = exp(S - max),  O^T[channel, r] = V^T P,  LSE = max + log sum P,
+// one pass over the keys with the running maximum and sum of a softmax.  Bound by the cache's bytes, 1.125 d a
+// slot and key head: at the copy rate an SM has 6 cycles (d = 128) for a slot, in which it has to turn 256 codes into fp16
+// and to multiply them.  So codes become operands in registers, where the matrix instructions take them:
+//  - K is the A operand (16 keys x 16 channels) of m16n8k16, rows the 8 columns: a warp's products serve 8 rows at no
+//    waste for small groups.  The sum over channels has any order, so lane t of a quad takes the quarter t of the
+//    channels, 16 bytes of a row, and two scales serve it.
+//  - S^T's accumulator becomes P's operand by one 8 x 8 transposition (movmatrix) each 8 keys.
+//  - V is the A operand V^T (16 channels x 16 keys).  Its pairs run over keys: two keys' bytes become bytes of pairs with
+//    four logic instructions for 16 codes, before they are turned into fp16.  Lane g takes the g-th eighth of the channels, so one
+//    scale a key serves it.
+//  - code * scale is exact in fp16; Q is scaled by a power of two a row so that fp16 holds its bf16 digits.
+// Every warp streams runs of 32 slots of its own through shared memory (bulk copies, a ring of stages, no other warp in
+// between); 4 warps of a block share a (sequence, key head, row tile) and join at its end.
+// The slots of all items lie in a row that is dealt out evenly over the blocks, whatever the lengths: a block writes what
+// it holds alone; items cut between blocks leave parts (O, max, sum) that a second launch joins in order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "zl_internal.h"
+#include "zl_kv4.cuh"
+#include "zl_overlap.cuh"
+#include "zl_ptx.cuh"
+
+namespace zl {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnit = 32;          // slots of a unit: two tiles
+constexpr int kMaxBlocks = 640;    // blocks of a launch at most: what the workspace has room for
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.f;    // the maximum may lag by 2^8 before the sums are rescaled
+
+// An item cut between blocks: its first block describes it for the join.
+struct Cut {
+  int32_t parts;   // 0: no item begins here that another block ends
+  int32_t which;   // part of the first block (the following blocks' parts are their first)
+  int32_t token0;  // row of the item's sequence in q and o
+  int32_t head0;   // first query head
+  int32_t row0, rows;
+  int32_t pad[2];
+};
+
+struct AttnParams {
+  Kv4 c;
+  const __nv_bfloat16* q;
+  int64_t q_stride, n_tokens;
+  const int32_t* starts;
+  __nv_bfloat16* o;
+  float* lse;
+  float* part_o;   // [2 blocks][rows][d]
+  float2* part_ml; // [2 blocks][rows]: maximum (base 2) and sum
+  Cut* cuts;       // [blocks]
+  float* scores;   // [sequence][key head][slot][score_rows], base 2
+  const float* w_in;
+  float* w_out;
+  float decay;
+  float scale_log2;
+  int32_t group, q_heads, max_new, score_rows;
+};
+
+// ---------------------------------------------------------------- pieces of a product
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t o;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(x));
+  return o;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t o;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(hi), "f"(lo));
+  return o;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// ---------------------------------------------------------------- the schedule
+// A block's run of units, item by item; the producers of the warps and their consumers each walk it by themselves.
+template <int NT>
+struct Walk {
+  int64_t left;        // units of the block's run from this segment on
+  int32_t seq, item;   // item: key head x row tiles
+  int32_t n, m, first; // the sequence's new tokens, slots and first token
+  int32_t row_tiles, chunks, items;
+  int32_t a, e;        // this segment: units [a, e) of the item's `chunks`
+
+  __device__ void load(const AttnParams& p) {
+    n = kv4_new(p.c, p.starts, p.n_tokens, p.max_new, seq, &first);
+    m = kv4_len(p.c, seq);
+    row_tiles = (n * p.group + 8 * NT - 1) / (8 * NT);
+    chunks = m > 0 ? (m + kUnit - 1) / kUnit : 1;
+    items = p.c.heads * row_tiles;
+  }
+  __device__ int64_t units() const { return (int64_t)items * chunks; }
+  __device__ void cut() { e = (int)(left < chunks - a ? a + left : chunks); }
+  __device__ bool done() const { return left <= 0; }
+  __device__ void next(const AttnParams& p) {
+    left -= e - a;
+    if (left <= 0) return;
+    a = 0;
+    if (++item == items) {
+      item = 0;
+      do {
+        if (++seq >= p.c.n_seqs) {
+          left = 0;
+          return;
+        }
+        load(p);
+      } while (items == 0);
+    }
+    cut();
+  }
+};
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStageBytes = 2 * 18 * D;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kPitch = D + 4;  // floats of a row in the join's buffer
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kJoin = kWarps * kRows * kPitch * 4;
+  static constexpr int kSmem = kRing + kJoin + kWarps * kRows * 8;
+  static constexpr int kBlocks = NT == 1 ? 4 : NT == 2 ? 3 : 2;  // an SM's, by registers and shared memory
+};
+
+template <int D, int NT, bool kScores>
+__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_kernel(const AttnParams p) {
+  using S = Shape<D, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[kWarps * S::kStages];
+  __shared__ int64_t warp_sums[kWarps];
+  __shared__ int64_t s_before;
+  __shared__ int s_seq;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  float* join = reinterpret_cast<float*>(smem + S::kRing);
+  float2* join_ml = reinterpret_cast<float2*>(smem + S::kRing + S::kJoin);
+  if (threadIdx.x < kWarps * S::kStages) mbar_init(&bars[threadIdx.x], 1);
+  if (threadIdx.x == 0) {
+    s_seq = -1;
+    fence_mbar_init();
+  }
+  let_next_start();
+  wait_for_previous();
+
+  // this block's run
+  Walk<NT> cons;
+  {
+    const int n = p.c.n_seqs, per = (n + kThreads - 1) / kThreads;
+    const int b0 = min(n, (int)threadIdx.x * per), b1 = min(n, b0 + per);
+    int64_t mine = 0, total;
+    for (int b = b0; b < b1; ++b) {
+      cons.seq = b;
+      cons.load(p);
+      mine += cons.units();
+    }
+    int64_t before = kv4_scan<kThreads>(mine, &total, warp_sums);
+    const int64_t each = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kWarps);
+    const int64_t at = each * blockIdx.x, end = min(total, at + each);
+    if (at < end && at >= before && at < before + mine) {
+      int b = b0;
+      for (;; ++b) {
+        cons.seq = b;
+        cons.load(p);
+        if (at < before + cons.units()) break;
+        before += cons.units();
+      }
+      s_seq = b;
+      s_before = before;
+    }
+    __syncthreads();
+    if (s_seq < 0) {  // nothing for this block (uniform: the run is empty)
+      if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;
+      return;
+    }
+    cons.seq = s_seq;
+    cons.load(p);
+    cons.left = end - at;
+    const int64_t off = at - s_before;
+    cons.item = (int)(off / cons.chunks);
+    cons.a = (int)(off - (int64_t)cons.item * cons.chunks);
+    cons.cut();
+    if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;  // an item cut at the run's end sets it below
+  }
+  const int64_t share = cons.left;  // of every block before the last one
+
+  Walk<NT> prod = cons;
+  int prod_x = prod.a + warp;  // next unit of this warp to load
+  auto settle = [&](Walk<NT>& w, int& x) {  // to the next unit of this warp, in this segment or a later one
+    while (!w.done() && x >= w.e) {
+      w.next(p);
+      x = w.a + warp;
+    }
+  };
+  settle(prod, prod_x);
+  uint8_t* ring = smem + warp * S::kStages * S::kStageBytes;
+  uint64_t* bar = bars + warp * S::kStages;
+  uint32_t there = 0;   // two bits a stage: which tiles of it were copied
+  uint32_t phases = 0;  // parity of each stage's next wait
+  int fill = 0, drain = 0, in_flight = 0;
+  auto produce = [&]() {
+    if (prod.done()) return;
+    const int head = prod.item / prod.row_tiles, slot = prod_x * kUnit;
+    uint8_t* dst = ring + fill * S::kStageBytes;
+    uint8_t* src0 = slot < prod.m ? kv4_tile<D>(p.c, prod.seq, head, slot) : nullptr;
+    uint8_t* src1 = slot + kKv4Slots < prod.m ? kv4_tile<D>(p.c, prod.seq, head, slot + kKv4Slots) : nullptr;
+    if (lane == 0) {
+      const uint32_t b = smem_u32(&bar[fill]);
+      if ((slot < prod.m && !src0) || (slot + kKv4Slots < prod.m && !src1)) kv4_report(p.c, ZL_KV4_BAD_PAGE);
+      mbar_arrive_expect_tx(&bar[fill], (src0 ? 18 * D : 0) + (src1 ? 18 * D : 0));
+      if (src0 && src1 == src0 + 18 * D) {
+        bulk_load(smem_u32(dst), src0, 36 * D, b);
+      } else {
+        if (src0) bulk_load(smem_u32(dst), src0, 18 * D, b);
+        if (src1) bulk_load(smem_u32(dst) + 18 * D, src1, 18 * D, b);
+      }
+    }
+    there = (there & ~(3u << (2 * fill))) | ((src0 ? 1u : 0u) | (src1 ? 2u : 0u)) << (2 * fill);
+    fill = fill + 1 == S::kStages ? 0 : fill + 1;
+    ++in_flight;
+    prod_x += kWarps;
+    settle(prod, prod_x);
+  };
+#pragma unroll
+  for (int i = 0; i < S::kStages; ++i) produce();
+
+  // rows of a lane's keys in a tile: the pairs of odd lanes are swapped, so that a load of four keys' values meets both
+  // halves of the banks
+  const int key0 = (g & ~1) | ((g & 1) ^ ((g >> 1) & 1));  // row g of a product; row g + 8 is key0 + 8
+  const int ka = 2 * t + (t & 1), kb = 2 * t + 1 - (t & 1);
+  bool first_segment = true, alive = true;
+  for (; !cons.done(); cons.next(p)) {
+    const int head = cons.item / cons.row_tiles, row0 = (cons.item - head * cons.row_tiles) * S::kRows;
+    const int rows = cons.n * p.group;
+    // queries: lane (g, t) holds quarter t of the channels of row g of every 8
+    uint32_t qf[NT][D / 16][2];
+    float f[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = row0 + 8 * j + g;
+      uint4 raw[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int tok = r / p.group;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(cons.first + tok) * p.q_stride +
+                                                          (int64_t)(head * p.group + r - tok * p.group) * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) raw[i] = src[i];
+      }
+      uint32_t top = 0;  // the largest magnitude's bits
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          top = max(top, w[x] & 0x7FFF0000u);
+          top = max(top, (w[x] << 16) & 0x7FFF0000u);
+        }
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ex = max(1, min(253, (int)(top >> 23)));  // 2^(ex - 127): the row's size
+      const float down = __uint_as_float((uint32_t)(254 - ex) << 23), up = __uint_as_float((uint32_t)ex << 23);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x)  // four channels are a step's
+          qf[j][2 * i + x / 2][x & 1] = pack_half(__uint_as_float(w[x] << 16) * down, __uint_as_float(w[x] & 0xFFFF0000u) * down);
+      }
+      const float mine = up * p.scale_log2;
+      f[j][0] = __shfl_sync(0xffffffffu, mine, 8 * t);
+      f[j][1] = __shfl_sync(0xffffffffu, mine, 8 * t + 4);
+    }
+    float acc[D / 16][NT][4], ref[NT][2], sum[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      ref[j][0] = ref[j][1] = -INFINITY;
+      sum[j][0] = sum[j][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
+    }
+    const int full = cons.m - cons.n + row0 / p.group;  // slots up to here are seen by every row
+
+    for (int x = cons.a + warp; x < cons.e; x += kWarps) {
+      if (!alive) continue;
+      const uint32_t stage = smem_u32(ring + drain * S::kStageBytes);
+      alive = __all_sync(0xffffffffu, mbar_wait(&bar[drain], (phases >> drain) & 1));
+      if (!alive) {
+        if (lane == 0) kv4_report(p.c, ZL_KV4_TIMEOUT);
+        continue;
+      }
+      const uint32_t have = (there >> (2 * drain)) & 3;
+      phases ^= 1u << drain;
+      drain = drain + 1 == S::kStages ? 0 : drain + 1;
+      --in_flight;
+      const int slot0 = x * kUnit;
+      const bool plain = have == 3 && slot0 + kUnit - 1 <= full;
+      float s[2][NT][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t tile = stage + i * 18 * D;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.f;
+        uint32_t ca[D / 32], cb[D / 32], sa[2], sb[2];
+        if constexpr (D == 128) {
+          const uint4 a = lds128(tile + key0 * 64 + t * 16), b = lds128(tile + (key0 + 8) * 64 + t * 16);
+          ca[0] = a.x; ca[1] = a.y; ca[2] = a.z; ca[3] = a.w;
+          cb[0] = b.x; cb[1] = b.y; cb[2] = b.z; cb[3] = b.w;
+          const uint32_t at = tile + 16 * D + key0 * 8 + 2 * t;
+          sa[0] = lds8(at); sa[1] = lds8(at + 1); sb[0] = lds8(at + 64); sb[1] = lds8(at + 65);
+        } else {
+          const uint2 a = lds64(tile + key0 * 32 + t * 8), b = lds64(tile + (key0 + 8) * 32 + t * 8);
+          ca[0] = a.x; ca[1] = a.y;
+          cb[0] = b.x; cb[1] = b.y;
+          sa[0] = sa[1] = lds8(tile + 16 * D + key0 * 4 + t);
+          sb[0] = sb[1] = lds8(tile + 16 * D + (key0 + 8) * 4 + t);
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {  // a word: 8 channels, two steps
+          uint32_t a[4], b[4];
+          kv4_decode(ca[w], a);
+          kv4_decode(cb[w], b);
+          const uint32_t s2a = kv4_scale2(sa[w / 2], sa[w / 2]), s2b = kv4_scale2(sb[w / 2], sb[w / 2]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            a[y] = kv4_mul(a[y], s2a);
+            b[y] = kv4_mul(b[y], s2b);
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              mma16(s[i][j], a[2 * y], b[2 * y], a[2 * y + 1], b[2 * y + 1], qf[j][2 * w + y][0], qf[j][2 * w + y][1]);
+        }
+      }
+      // base-2 scores; slots that a row does not see, or that are not there, are -inf
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s[i][j][y] *= f[j][y & 1];
+      if (!plain) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int last = cons.m - cons.n + (row0 + 8 * j + 2 * t + y) / p.group - slot0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const bool ok = (have >> i) & 1;
+              if (!ok || i * 16 + key0 > last) s[i][j][y] = -INFINITY;
+              if (!ok || i * 16 + key0 + 8 > last) s[i][j][y + 2] = -INFINITY;
+            }
+          }
+      }
+      if constexpr (kScores) {
+        const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift;
+        float* dst = p.scores + (((int64_t)cons.seq * p.c.heads + head) * slots + slot0) * p.score_rows + row0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int key = i * 16 + key0 + 8 * y;
+            if (slot0 + key >= cons.m) continue;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              if (row0 + 8 * j + 2 * t < rows)
+                *reinterpret_cast<float2*>(dst + (int64_t)key * p.score_rows + 8 * j + 2 * t) = make_float2(s[i][j][2 * y], s[i][j][2 * y + 1]);
+          }
+      }
+      float top[NT][2];
+      bool grow = false;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          top[j][y] = fmaxf(fmaxf(s[0][j][y], s[0][j][y + 2]), fmaxf(s[1][j][y], s[1][j][y + 2]));
+          grow |= top[j][y] > ref[j][y] + kRescale;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float m = top[j][y];
+#pragma unroll
+            for (int x2 = 4; x2 < 32; x2 <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x2));
+            m = fmaxf(m, ref[j][y]);
+            const float down = m == -INFINITY ? 1.f : ex2(ref[j][y] - m);
+            ref[j][y] = m;
+            sum[j][y] *= down;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              acc[i][j][y] *= down;
+              acc[i][j][y + 2] *= down;
+            }
+          }
+      }
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float r0 = ref[j][0] == -INFINITY ? 0.f : ref[j][0], r1 = ref[j][1] == -INFINITY ? 0.f : ref[j][1];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float p0 = ex2(s[i][j][0] - r0), p1 = ex2(s[i][j][1] - r1), p2 = ex2(s[i][j][2] - r0), p3 = ex2(s[i][j][3] - r1);
+          sum[j][0] += p0 + p2;
+          sum[j][1] += p1 + p3;
+          pb[i][j][0] = transpose8(pack_half(p0, p1));
+          pb[i][j][1] = transpose8(pack_half(p2, p3));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t tile = stage + i * 18 * D;
+        const int keys[4] = {ka, kb, ka + 8, kb + 8};
+        uint32_t v[4][D / 64], sc[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          if constexpr (D == 128) {
+            const uint2 w = lds64(tile + 8 * D + keys[y] * 64 + g * 8);
+            v[y][0] = w.x;
+            v[y][1] = w.y;
+            sc[y] = lds8(tile + 17 * D + keys[y] * 8 + g);
+          } else {
+            v[y][0] = lds32(tile + 8 * D + keys[y] * 32 + g * 4);
+            sc[y] = lds8(tile + 17 * D + keys[y] * 4 + (g >> 1));
+          }
+        }
+        if (!plain) {
+          // what lies in slots past the end may be no number: 0 times it is not 0
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if (!((have >> i) & 1) || slot0 + i * 16 + keys[y] >= cons.m) sc[y] = 0;
+        }
+        const uint32_t s01 = kv4_scale2(sc[0], sc[1]), s23 = kv4_scale2(sc[2], sc[3]);
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) {
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          kv4_decode((v[0][w] & 0x0F0F0F0Fu) | ((v[1][w] << 4) & 0xF0F0F0F0u), a0);
+          kv4_decode(((v[0][w] >> 4) & 0x0F0F0F0Fu) | (v[1][w] & 0xF0F0F0F0u), a1);
+          kv4_decode((v[2][w] & 0x0F0F0F0Fu) | ((v[3][w] << 4) & 0xF0F0F0F0u), a2);
+          kv4_decode(((v[2][w] >> 4) & 0x0F0F0F0Fu) | (v[3][w] & 0xF0F0F0F0u), a3);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            a0[y] = kv4_mul(a0[y], s01);
+            a1[y] = kv4_mul(a1[y], s01);
+            a2[y] = kv4_mul(a2[y], s23);
+            a3[y] = kv4_mul(a3[y], s23);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma16(acc[4 * w + y][j], a0[y], a1[y], a2[y], a3[y], pb[i][j][0], pb[i][j][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      produce();
+    }
+
+    // the warps' parts of the segment become one
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int x2 = 4; x2 < 32; x2 <<= 1) sum[j][y] += __shfl_xor_sync(0xffffffffu, sum[j][y], x2);
+        const int row = 8 * j + 2 * t + y;
+        if (g == 0) join_ml[warp * S::kRows + row] = make_float2(ref[j][y], sum[j][y]);
+        float* dst = join + (warp * S::kRows + row) * S::kPitch + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < D / 16; i += 2)
+          *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(acc[i][j][y], acc[i][j][y + 2], acc[i + 1][j][y], acc[i + 1][j][y + 2]);
+      }
+    __syncthreads();
+    const bool whole = cons.a == 0 && cons.e == cons.chunks;
+    const int part = 2 * blockIdx.x + (first_segment ? 0 : 1);
+    constexpr int kLanes = D / 4;  // threads of a row
+    const int c4 = threadIdx.x % kLanes;
+    for (int r = threadIdx.x / kLanes; r < S::kRows && row0 + r < rows; r += kThreads / kLanes) {
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, join_ml[w * S::kRows + r].x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = join_ml[w * S::kRows + r];
+        const float k = m == -INFINITY ? 1.f : ex2(ml.x - m);
+        const float4 x = *reinterpret_cast<const float4*>(join + (w * S::kRows + r) * S::kPitch + 4 * c4);
+        l = fmaf(ml.y, k, l);
+        o = make_float4(fmaf(x.x, k, o.x), fmaf(x.y, k, o.y), fmaf(x.z, k, o.z), fmaf(x.w, k, o.w));
+      }
+      if (whole) {
+        const int tok = (row0 + r) / p.group;
+        const int64_t at = (int64_t)(cons.first + tok) * p.q_heads + head * p.group + (row0 + r - tok * p.group);
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        if (c4 == 0) p.lse[at] = m == -INFINITY && !(l > 0.f) && l == l ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + ((int64_t)part * S::kRows + r) * D + 4 * c4) = o;
+        if (c4 == 0) p.part_ml[(int64_t)part * S::kRows + r] = make_float2(m, l);
+      }
+    }
+    if (threadIdx.x == 0 && cons.a == 0 && cons.e < cons.chunks) {
+      // the run ends inside this item: full shares follow until its end
+      Cut c;
+      c.which = first_segment ? 0 : 1;
+      c.token0 = cons.first;
+      c.head0 = head * p.group;
+      c.row0 = row0;
+      c.rows = rows;
+      c.pad[0] = c.pad[1] = 0;
+      const int64_t rest = cons.chunks - cons.e;
+      c.parts = 1 + (int)((rest + share - 1) / share);
+      p.cuts[blockIdx.x] = c;
+    }
+    first_segment = false;
+    __syncthreads();  // the join's buffer has been read
+  }
+  // copies still under way (after a wait that gave up): none may land in memory that is no longer this block's
+  while (in_flight > 0) {
+    mbar_wait(&bar[drain], (phases >> drain) & 1);
+    phases ^= 1u << drain;
+    drain = drain + 1 == S::kStages ? 0 : drain + 1;
+    --in_flight;
+  }
+}
+
+// ---------------------------------------------------------------- joining cut items
+template <int D>
+__global__ void __launch_bounds__(256) zl_kv4_join_kernel(const AttnParams p, int32_t tile_rows) {
+  let_next_start();
+  wait_for_previous();
+  const Cut c = p.cuts[blockIdx.x];
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (c.parts == 0 || c.row0 + r >= c.rows || r >= tile_rows) return;
+  auto part = [&](int i) { return (int64_t)(i == 0 ? 2 * blockIdx.x + c.which : 2 * (blockIdx.x + i)) * tile_rows + r; };
+  float m = -INFINITY;
+  for (int i = lane; i < c.parts; i += 32) m = fmaxf(m, p.part_ml[part(i)].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  constexpr int kPer = D / 32;
+  float o[kPer] = {}, l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < c.parts; ++i) {
+    const float2 ml = p.part_ml[part(i)];
+    const float k = m == -INFINITY ? 1.f : ex2(ml.x - m);
+    l = fmaf(ml.y, k, l);
+    const float* src = p.part_o + part(i) * D + lane * kPer;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] = fmaf(src[x], k, o[x]);
+  }
+  const int tok = (c.row0 + r) / p.group;
+  const int64_t at = (int64_t)(c.token0 + tok) * p.q_heads + c.head0 + (c.row0 + r - tok * p.group);
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + at * D + lane * kPer);
+#pragma unroll
+  for (int x = 0; x < kPer; x += 2) dst[x / 2] = pack_bf16(o[x] * inv, o[x + 1] * inv);
+  if (lane == 0) p.lse[at] = m == -INFINITY && !(l > 0.f) && l == l ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+}
+
+// ---------------------------------------------------------------- accumulated weights
+// weights_out[slot] = decay weights[slot] + sum over rows of 2^(score - lse): a slot's scores lie side by side.
+constexpr int kWeightSlots = 1024;  // slots a block takes
+__global__ void __launch_bounds__(256) zl_kv4_weights_kernel(const AttnParams p) {
+  let_next_start();
+  wait_for_previous();
+  const int b = blockIdx.z, h = blockIdx.y;
+  extern __shared__ float lse2[];  // base-2 LSE of every row; rows that see nothing take no part
+  const int m = kv4_len(p.c, b);
+  const int s0 = blockIdx.x * kWeightSlots, s1 = min(m, s0 + kWeightSlots);
+  if (s0 >= s1) return;
+  int first = 0;
+  const int n = kv4_new(p.c, p.starts, p.n_tokens, p.max_new, b, &first), rows = n * p.group;
+  for (int r = threadIdx.x; r < rows; r += 256) {
+    const int tok = r / p.group;
+    lse2[r] = p.lse[(int64_t)(first + tok) * p.q_heads + h * p.group + r - tok * p.group] * kLog2e;
+  }
+  __syncthreads();
+  const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift, base = ((int64_t)b * p.c.heads + h) * slots;
+  for (int s = s0 + threadIdx.x; s < s1; s += 256) {
+    const float* x = p.scores + (base + s) * p.score_rows;
+    float w = p.w_in && s < m - n ? p.decay * p.w_in[base + s] : 0.f;
+    for (int r = 0; r < rows; ++r) {
+      const float l = lse2[r];
+      w += l == -INFINITY ? 0.f : ex2(x[r] - l);
+    }
+    p.w_out[base + s] = w;
+  }
+}
+
+// ---------------------------------------------------------------- host
+int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+
+// 8-row columns of a warp's products: as many as the rows of a key head need, up to 32 rows a pass over the cache.
+int row_columns(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+struct Layout {
+  int64_t ml, cuts, scores, total;
+  int32_t score_rows;
+};
+Layout layout(const zl_kv4_cache& c, int32_t group, int32_t max_new, bool weights) {
+  const int64_t rows = (int64_t)group * max_new, tile = 8 * row_columns(rows);
+  Layout l;
+  l.ml = round16((int64_t)2 * kMaxBlocks * tile * c.head_dim * 4);
+  l.cuts = l.ml + round16((int64_t)2 * kMaxBlocks * tile * 8);
+  l.scores = l.cuts + round16((int64_t)kMaxBlocks * sizeof(Cut));
+  l.score_rows = (int32_t)((rows + 1) / 2 * 2);
+  l.total = l.scores;
+  if (weights) l.total += (int64_t)c.n_seqs * c.n_kv_heads * c.max_pages * c.page * l.score_rows * 4;
+  return l;
+}
+
+zl_status check_heads(const zl_kv4_cache* c, int32_t n_q_heads, int32_t max_new) {
+  if (n_q_heads < 1 || n_q_heads % c->n_kv_heads || max_new < 1) return ZL_ERR_INVALID_ARG;
+  const int64_t group = n_q_heads / c->n_kv_heads;
+  if (group > 128 || group * max_new > 8192) return ZL_ERR_UNSUPPORTED;
+  return ZL_OK;
+}
+
+template <int D, int NT, bool kScores>
+cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
+  using S = Shape<D, NT>;
+  const auto kernel = zl_kv4_attn_kernel<D, NT, kScores>;
+  static PerDeviceInt resident;
+  int per_sm = 0;
+  cudaError_t e = resident.get(&per_sm, [&](int, int* v) {
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (r == cudaSuccess) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kernel, kThreads, S::kSmem);
+    if (*v < 1) *v = 1;
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  const int blocks = sms * per_sm < kMaxBlocks ? sms * per_sm : kMaxBlocks;
+  e = launch_overlapped(kernel, blocks, kThreads, S::kSmem, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(zl_kv4_join_kernel<D>, dim3(blocks, NT), 256, 0, stream, p, S::kRows);
+}
+template <int D, bool kScores>
+cudaError_t launch_attn(const AttnParams& p, int columns, int sms, cudaStream_t stream) {
+  return columns == 1   ? launch_attn<D, 1, kScores>(p, sms, stream)
+         : columns == 2 ? launch_attn<D, 2, kScores>(p, sms, stream)
+                        : launch_attn<D, 4, kScores>(p, sms, stream);
+}
+
+}  // namespace
+}  // namespace zl
+
+using namespace zl;
+
+extern "C" zl_status zl_kv4_attn_workspace(const zl_kv4_cache* cache, int32_t n_q_heads, int32_t max_new, int32_t weights,
+                                           int64_t* bytes) {
+  Kv4 c;
+  zl_status s = kv4_check(cache, &c);
+  if (s != ZL_OK) return s;
+  if (!bytes || (weights != 0 && weights != 1)) return ZL_ERR_INVALID_ARG;
+  if ((s = check_heads(cache, n_q_heads, max_new)) != ZL_OK) return s;
+  *bytes = layout(*cache, n_q_heads / cache->n_kv_heads, max_new, weights != 0).total;
+  return ZL_OK;
+}
+
+extern "C" zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, int64_t q_stride, int64_t n_tokens,
+                                     int32_t n_q_heads, const int32_t* starts, int32_t max_new, void* o, float* lse,
+                                     const float* weights, float* weights_out, float decay, void* workspace, float scale,
+                                     void* stream) {
+  NvtxRange range("zl_kv4_attn_fwd");
+  AttnParams p{};
+  zl_status s = kv4_check(cache, &p.c);
+  if (s != ZL_OK) return s;
+  if ((s = check_heads(cache, n_q_heads, max_new)) != ZL_OK) return s;
+  if (n_tokens < 0 || n_tokens > INT32_MAX || !(scale > 0.f) || !std::isnormal(scale) || !std::isfinite(decay)) return ZL_ERR_INVALID_ARG;
+  if ((!starts && n_tokens != cache->n_seqs) || (weights && !weights_out)) return ZL_ERR_INVALID_ARG;
+  if (cache->n_seqs == 0) return ZL_OK;
+  if (n_tokens > 0) {  // without tokens the weights still carry over
+    if ((s = kv4_check_rows(q, q_stride, (int64_t)n_q_heads * cache->head_dim)) != ZL_OK) return s;
+    if (!o || !lse) return ZL_ERR_INVALID_ARG;
+    if (!kv4_aligned(o, 16) || !kv4_aligned(lse, 4)) return ZL_ERR_ALIGN;
+  } else if (!weights_out) {
+    return ZL_OK;
+  }
+  if (!workspace) return ZL_ERR_INVALID_ARG;
+  if (!kv4_aligned(workspace, 16) || !kv4_aligned(starts, 4) || !kv4_aligned(weights, 4) || !kv4_aligned(weights_out, 4)) return ZL_ERR_ALIGN;
+  if (weights_out && (cache->n_seqs > 65535 || cache->n_kv_heads > 65535)) return ZL_ERR_UNSUPPORTED;
+  int sms = 0;
+  if ((s = check_device(&sms)) != ZL_OK) return s;
+  const int32_t group = n_q_heads / cache->n_kv_heads;
+  const Layout l = layout(*cache, group, max_new, weights_out != nullptr);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.n_tokens = n_tokens;
+  p.starts = starts;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + l.ml);
+  p.cuts = reinterpret_cast<Cut*>(ws + l.cuts);
+  p.scores = reinterpret_cast<float*>(ws + l.scores);
+  p.w_in = weights;
+  p.w_out = weights_out;
+  p.decay = decay;
+  p.scale_log2 = scale * kLog2e;
+  p.group = group;
+  p.q_heads = n_q_heads;
+  p.max_new = max_new;
+  p.score_rows = l.score_rows;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int columns = row_columns((int64_t)group * max_new);
+  cudaError_t e = cudaSuccess;
+  if (n_tokens > 0) {
+    if (cache->head_dim == 128) e = weights_out ? launch_attn<128, true>(p, columns, sms, st) : launch_attn<128, false>(p, columns, sms, st);
+    else e = weights_out ? launch_attn<64, true>(p, columns, sms, st) : launch_attn<64, false>(p, columns, sms, st);
+  }
+  if (e == cudaSuccess && weights_out && cache->max_pages > 0) {
+    const int64_t slots = (int64_t)cache->max_pages * cache->page;
+    e = launch_overlapped(zl_kv4_weights_kernel, dim3((unsigned)((slots + kWeightSlots - 1) / kWeightSlots), cache->n_kv_heads, cache->n_seqs),
+                          256, (size_t)group * max_new * 4, st, p);
+  }
+  return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
+}

@@ -486,20 +486,6 @@ cudaError_t launch_rope(const zl_qk_rope_desc& d, bool bwd, int sms, RopeParams&
   return launch_overlapped(zl_qk_rope_dw_kernel, 2 * D / 32, 1024, 0, stream, p.partial, (int32_t)(nx * ny), D, dwq, dwk);
 }
 
-// SM count of the current device; the kernels are built for sm_103a alone.
-zl_status check_device(int* sms) {
-  static PerDeviceInt count;
-  const cudaError_t e = count.get(sms, [](int dev, int* v) {
-    int major = 0, minor = 0;
-    cudaError_t r = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-    if (r == cudaSuccess) r = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    if (r == cudaSuccess) r = cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
-    if (major != 10 || minor != 3) *v = -1;
-    return r;
-  });
-  return e != cudaSuccess ? ZL_ERR_CUDA : *sms > 0 ? ZL_OK : ZL_ERR_UNSUPPORTED;
-}
-
 }  // namespace
 
 }  // namespace zl

@@ -21,6 +21,7 @@ ZL_PLAN_TEST_WITHHOLD_LOAD = 2
 ZL_PLAN_FUSE_LOCAL_KMERGE = 8
 ZL_PLAN_DETERMINISTIC_DQ = 16
 ZL_PLAN_FORWARD_ONLY = 32
+ZL_KV4_BAD_PAGE, ZL_KV4_BAD_LEN, ZL_KV4_BAD_STARTS, ZL_KV4_TIMEOUT = 1, 2, 4, 8
 
 
 class ZlError(RuntimeError):
@@ -49,6 +50,13 @@ class zl_qk_rope_desc(ctypes.Structure):
 class zl_causal_seq(ctypes.Structure):
     _fields_ = [("q_offset", ctypes.c_int64), ("kv_offset", ctypes.c_int64),
                 ("q_len", ctypes.c_int32), ("kv_len", ctypes.c_int32)]
+
+
+class zl_kv4_cache(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("data", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
 
 
 class zl_bucket(ctypes.Structure):
@@ -103,6 +111,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "zl_causal_attn_fwd": (I32, [P, P, I64, P, I64, P, I64, P, P, P, F, P]),
         "zl_causal_attn_bwd": (I32, [P, P, I64, P, I64, P, I64, P, P, P, P, I64, P, I64, P, I64, P, F, P]),
         "zl_causal_get_device_status": (I32, [P, P, pI32]),
+        "zl_kv4_write": (I32, [ctypes.POINTER(zl_kv4_cache), P, I64, P, I64, I64, P, P, P, P]),
+        "zl_kv4_read": (I32, [ctypes.POINTER(zl_kv4_cache), P, I64, P, I64, I64, P, P]),
+        "zl_kv4_attn_workspace": (I32, [ctypes.POINTER(zl_kv4_cache), I32, I32, I32, pI64]),
+        "zl_kv4_attn_fwd": (I32, [ctypes.POINTER(zl_kv4_cache), P, I64, I64, I32, P, I32, P, P, P, P, F, P, F, P]),
+        "zl_kv4_evict_workspace": (I32, [ctypes.POINTER(zl_kv4_cache), pI64]),
+        "zl_kv4_evict": (I32, [ctypes.POINTER(zl_kv4_cache), P, P, I32, I32, P, P, P, P]),
         "zl_catalog_cut": (I32, [ctypes.POINTER(zl_bucket), I32, pI32, ctypes.POINTER(ctypes.c_double)]),
         "zl_pack_fillers": (I32, [pD, pD, I32, I32, pD, pD, ctypes.c_double, ctypes.c_double, pI32, pD, pD, pI32, pD]),
     }
@@ -411,7 +425,8 @@ def exported_symbols() -> List[str]:
             "zl_get_device_status", "zl_status_string", "zl_version", "zl_catalog_cut", "zl_pack_fillers",
             "zl_rope_frequencies", "zl_qk_rope_workspace", "zl_qk_rope_fwd", "zl_qk_rope_bwd", "zl_plan_causal",
             "zl_causal_plan_destroy", "zl_causal_plan_workspace", "zl_causal_plan_tiles", "zl_causal_attn_fwd",
-            "zl_causal_attn_bwd", "zl_causal_get_device_status"]
+            "zl_causal_attn_bwd", "zl_causal_get_device_status", "zl_kv4_write", "zl_kv4_read", "zl_kv4_attn_workspace",
+            "zl_kv4_attn_fwd", "zl_kv4_evict_workspace", "zl_kv4_evict"]
 
 
 # ---------------------------------------------------------------- causal sequences
@@ -897,6 +912,187 @@ def qkv_attention_backward(plan: CausalPlan, qkv, d_o, dqkv, positions, table: O
                        bufs["dk_weight"] if of_k and norm else None, bufs["rope_workspace"], eps, stream,
                        plan.q_rows if of_q else None, plan.kv_rows if of_k else None)
     return bufs
+
+
+# ---------------------------------------------------------------- key-value cache in 4 bits
+@dataclass(frozen=True)
+class Kv4Cache:
+    """A cache's tensors on one CUDA device.  Not to be changed once made (its calls reuse one descriptor), but for the
+    tensors' contents: lens and pages are read by every call.
+      data   uint8 [pages, key heads, page / 16, 18 d]: the rows' codes and scales (zl.h has the layout); zl_kv4_write fills it
+      pages  int32 [sequences, pages of a sequence]: where slot s of a sequence lies, page s / page
+      lens   int32 [sequences]: slots in use
+    status: an int32 tensor of one number in which calls note what they had to leave out; see zl_kv4_get_device_status."""
+    data: "object"
+    pages: "object"
+    lens: "object"
+    status: "object" = None
+    desc: zl_kv4_cache = field(init=False, repr=False, compare=False)
+    device: int = field(init=False, default=-1, repr=False)
+    slots: int = field(init=False, default=0, repr=False)        # that the table has room for
+    token_shape: tuple = field(init=False, default=(), repr=False)  # key heads, d
+    slot_shape: tuple = field(init=False, default=(), repr=False)   # of weights and positions
+    sizes: dict = field(init=False, default_factory=dict, repr=False, compare=False)  # workspaces by sizes
+
+    def __post_init__(self):
+        torch = _torch()
+        if not isinstance(self.data, torch.Tensor) or self.data.dtype is not torch.uint8 or not self.data.is_cuda:
+            raise TypeError(f"data: expected a CUDA tensor of {torch.uint8}, got {getattr(self.data, 'dtype', type(self.data))}")
+        if self.data.dim() != 4 or self.data.shape[3] not in (18 * 64, 18 * 128):
+            raise ValueError(f"data: expected [pages, key heads, page / 16, 18 d], d 64 or 128, got {tuple(self.data.shape)}")
+        if not self.data.is_contiguous():
+            raise ValueError("data: must be contiguous")
+        dev = self.data.get_device()
+        n_pages, heads, tiles, width = self.data.shape
+        if not isinstance(self.pages, torch.Tensor) or self.pages.dim() != 2:
+            raise TypeError("pages: expected a CUDA tensor [sequences, pages of a sequence]")
+        n, most = self.pages.shape
+        if self.status is None:
+            object.__setattr__(self, "status", torch.zeros(1, dtype=torch.int32, device=self.data.device))
+        pages, lens = _dense(self.pages, "pages", torch.int32, (n, most), dev), _dense(self.lens, "lens", torch.int32, (n,), dev)
+        status = _dense(self.status, "status", torch.int32, (1,), dev)
+        desc = zl_kv4_cache(n, heads, width // 18, 16 * tiles, most, n_pages, self.data.data_ptr(), pages, lens, status)
+        _check(load_library().zl_kv4_evict_workspace(ctypes.byref(desc), ctypes.byref(ctypes.c_int64())), "Kv4Cache")
+        for name, x in (("desc", desc), ("device", dev), ("slots", most * 16 * tiles), ("token_shape", (heads, width // 18)),
+                        ("slot_shape", (n, heads, most * 16 * tiles))):
+            object.__setattr__(self, name, x)
+
+
+def allocate_kv4(n_seqs: int, max_pages: int, n_kv_heads: int, head_dim: int, page: int = 64, n_pages: Optional[int] = None,
+                 device="cuda") -> Kv4Cache:
+    """An empty cache; without n_pages, of n_seqs * max_pages pages that belong to the sequences in order (else the
+    caller fills `pages`)."""
+    import torch
+    if page not in (16, 32, 64, 128, 256) or head_dim not in (64, 128):
+        raise ValueError(f"expected a page of 16, 32, 64, 128 or 256 slots and d of 64 or 128, got {page} and {head_dim}")
+    ids = torch.arange(n_seqs * max_pages, dtype=torch.int32, device=device).view(n_seqs, max_pages)
+    if n_pages is not None:
+        ids.fill_(-1)
+    data = torch.zeros(n_seqs * max_pages if n_pages is None else n_pages, n_kv_heads, page // 16, 18 * head_dim,
+                       dtype=torch.uint8, device=device)
+    return Kv4Cache(data, ids, torch.zeros(n_seqs, dtype=torch.int32, device=device))
+
+
+def _kv4_dev(cache: Kv4Cache) -> int:
+    """The cache's device, which has to be the current one (launches go to it)."""
+    dev = cache.device
+    if _torch()._C._cuda_getDevice() != dev:
+        raise ValueError(f"cache on cuda:{dev}, current device is another")
+    return dev
+
+
+def _kv4_starts(cache, starts, dev):
+    return None if starts is None else _dense(starts, "starts", _torch().int32, (cache.slot_shape[0] + 1,), dev)
+
+
+def zl_kv4_write(cache: Kv4Cache, k, v, starts=None, positions=None, slot_positions=None, stream=None):
+    """New tokens' keys and values [tokens, Hkv, d] (views of a fused projection will do) into the last slots of their
+    sequences: sequence b brings tokens starts[b] .. starts[b + 1] - 1 (int32 [sequences + 1]; None: token b) and cache.lens
+    counts them already.  positions (int32 [tokens]) with slot_positions (int32 [sequences, Hkv, cache.slots]): the slots'
+    positions, which zl_kv4_evict goes by."""
+    torch = _torch()
+    dev = _kv4_dev(cache)
+    n = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+    shape = (n, *cache.token_shape)
+    pk, nk = _heads(k, "k", shape, dev)
+    pv, nv = _heads(v, "v", shape, dev)
+    ps = ss = None
+    if positions is not None or slot_positions is not None:
+        ps = _dense(positions, "positions", torch.int32, (n,), dev)
+        ss = _dense(slot_positions, "slot_positions", torch.int32, cache.slot_shape, dev)
+    st = load_library().zl_kv4_write(cache.desc, pk, nk, pv, nv, n, _kv4_starts(cache, starts, dev), ps, ss,
+                                     _raw_stream(stream, dev))
+    if st:
+        _check(st, "zl_kv4_write")
+
+
+def zl_kv4_read(cache: Kv4Cache, k_out, v_out, row_starts, stream=None):
+    """All that the cache holds as bf16 rows: slot s of sequence b becomes row row_starts[b] + s (int64 [sequences]) of
+    k_out, v_out [rows, Hkv, d]; zl_causal_attn_fwd takes them as keys and values."""
+    torch = _torch()
+    dev = _kv4_dev(cache)
+    n = k_out.shape[0] if isinstance(k_out, torch.Tensor) and k_out.dim() == 3 else 0
+    shape = (n, *cache.token_shape)
+    pk, nk = _heads(k_out, "k_out", shape, dev)
+    pv, nv = _heads(v_out, "v_out", shape, dev)
+    st = load_library().zl_kv4_read(cache.desc, pk, nk, pv, nv, n,
+                                    _dense(row_starts, "row_starts", torch.int64, (cache.slot_shape[0],), dev),
+                                    _raw_stream(stream, dev))
+    if st:
+        _check(st, "zl_kv4_read")
+
+
+def zl_kv4_attn_workspace_bytes(cache: Kv4Cache, n_q_heads: int, max_new: int = 1, weights: bool = False) -> int:
+    """Scratch bytes of zl_kv4_attn_fwd."""
+    key = (n_q_heads, max_new, bool(weights))
+    if key not in cache.sizes:
+        b = ctypes.c_int64()
+        _check(load_library().zl_kv4_attn_workspace(cache.desc, n_q_heads, max_new, int(key[2]), ctypes.byref(b)),
+               "zl_kv4_attn_workspace")
+        cache.sizes[key] = b.value
+    return cache.sizes[key]
+
+
+def zl_kv4_attn_fwd(cache: Kv4Cache, q, o, lse, workspace, scale: float, starts=None, max_new: int = 1, weights=None,
+                    weights_out=None, decay: float = 1.0, stream=None):
+    """Attention of the newest tokens q [tokens, Hq, d] over the cache, which holds their keys and values already, into o
+    (contiguous) and lse [tokens, Hq].  starts as in zl_kv4_write; no sequence brings more than max_new tokens.
+    weights_out (fp32 [sequences, Hkv, cache.slots]) becomes decay * weights plus what each slot received of the softmax,
+    summed over the new tokens and the heads of its group; weights may be the same tensor, or None for zeros.
+    workspace: zl_kv4_attn_workspace_bytes(cache, Hq, max_new, weights_out is not None)."""
+    torch = _torch()
+    dev = _kv4_dev(cache)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q: expected a CUDA tensor [tokens, Hq, d]")
+    n, hq = q.shape[0], q.shape[1]
+    shape = (n, hq, cache.token_shape[1])
+    pq, nq = _heads(q, "q", shape, dev)
+    if weights is not None and weights_out is None:
+        raise ValueError("weights without weights_out")
+    w = _dense(weights, "weights", torch.float32, cache.slot_shape, dev) if weights is not None else None
+    wo = _dense(weights_out, "weights_out", torch.float32, cache.slot_shape, dev) if weights_out is not None else None
+    st = load_library().zl_kv4_attn_fwd(
+        cache.desc, pq, nq, n, hq, _kv4_starts(cache, starts, dev), max_new, _dense(o, "o", torch.bfloat16, shape, dev),
+        _dense(lse, "lse", torch.float32, shape[:2], dev), w, wo, decay,
+        _scratch(workspace, "workspace", zl_kv4_attn_workspace_bytes(cache, hq, max_new, wo is not None), dev), scale,
+        _raw_stream(stream, dev))
+    if st:
+        _check(st, "zl_kv4_attn_fwd")
+
+
+def zl_kv4_evict_workspace_bytes(cache: Kv4Cache) -> int:
+    """Scratch bytes of zl_kv4_evict."""
+    if "evict" not in cache.sizes:
+        b = ctypes.c_int64()
+        _check(load_library().zl_kv4_evict_workspace(cache.desc, ctypes.byref(b)), "zl_kv4_evict_workspace")
+        cache.sizes["evict"] = b.value
+    return cache.sizes["evict"]
+
+
+def zl_kv4_evict(cache: Kv4Cache, weights, positions, keep: int, recent: int, workspace, weights_out=None, positions_out=None,
+                 stream=None):
+    """Every head of a sequence longer than `keep` keeps `keep` slots: those among the last `recent` positions first, then
+    the largest weights (ties: the lower slot); survivors from behind move into the slots given up.  weights (fp32),
+    positions (int32): [sequences, Hkv, cache.slots]; their new contents go to weights_out, positions_out (None: in
+    place).  The new lengths are cache.lens.clamp(max=keep), which the caller sets."""
+    torch = _torch()
+    dev = _kv4_dev(cache)
+    w = _dense(weights, "weights", torch.float32, cache.slot_shape, dev)
+    ps = _dense(positions, "positions", torch.int32, cache.slot_shape, dev)
+    wo = w if weights_out is None else _dense(weights_out, "weights_out", torch.float32, cache.slot_shape, dev)
+    po = ps if positions_out is None else _dense(positions_out, "positions_out", torch.int32, cache.slot_shape, dev)
+    st = load_library().zl_kv4_evict(cache.desc, w, ps, keep, recent, wo, po,
+                                     _scratch(workspace, "workspace", zl_kv4_evict_workspace_bytes(cache), dev),
+                                     _raw_stream(stream, dev))
+    if st:
+        _check(st, "zl_kv4_evict")
+
+
+def zl_kv4_get_device_status(cache: Kv4Cache) -> int:
+    """ZL_KV4_* bits of what calls on this cache had to leave out since the last query; waits for the device."""
+    s = int(cache.status.item())
+    cache.status.zero_()
+    return s
 
 
 # ---------------------------------------------------------------- host placement slice

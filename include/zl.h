@@ -534,6 +534,93 @@ ZL_API zl_status zl_causal_attn_bwd(const zl_causal_plan* plan, const void* q, i
  * gave up), synchronising the stream. */
 ZL_API zl_status zl_causal_get_device_status(const zl_causal_plan* plan, void* stream, int32_t* device_status);
 
+/* ----------------------------------------------------------------------------------
+ * Key-value cache in 4 bits (library mechanics; no passage): what an autoregressive model that serves on this
+ * library keeps of its keys and values in 1.125 bytes a channel pair instead of 4.  Writing rows into it, reading them
+ * back, attention of new tokens over it, and eviction by accumulated attention weight.  Lengths and page tables
+ * live in device memory, so one captured graph serves every step.
+ *
+ * The cache is pages of `page` slots.  A page holds, for each key head, page / 16 tiles of 16 slots; a tile is 18 d
+ * bytes: the keys' codes [16][d / 2], the values' codes [16][d / 2], the keys' scales [16][d / 16], the values'
+ * scales [16][d / 16].  A code is 4 bits, sign, two of exponent, one of mantissa (0 .5 1 1.5 2 3 4 6), channel 2j in the
+ * low half of byte j.  A scale serves 16 channels: 8 bits, five of exponent (bias 15) and three of
+ * mantissa, at most 2^13.  Channel = code * scale, exact in bf16 and in fp16.
+ *
+ * Slot s of sequence b is slot s % page of page pages[b][s / page].  Sequences may share pages that no call writes.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t n_seqs;       /* >= 0 */
+  int32_t n_kv_heads;   /* 1 .. 1024 */
+  int32_t head_dim;     /* 64 or 128 */
+  int32_t page;         /* slots a page: 16, 32, 64, 128 or 256 */
+  int32_t max_pages;    /* pages a sequence may have: the width of `pages`; max_pages * page < 2^30 */
+  int64_t n_pages;      /* pages of `data` */
+  void* data;           /* [n_pages][n_kv_heads][page / 16][18 d], 16-byte aligned */
+  const int32_t* pages; /* device [n_seqs][max_pages]; entries past a sequence's slots are not read */
+  const int32_t* lens;  /* device [n_seqs]: slots in use, the new tokens of the call among them */
+  int32_t* status;      /* device, or NULL: bits below are set where a call met what it had to leave out */
+} zl_kv4_cache;
+
+/* What device memory told a call and the call left out; nothing is read or written out of range for it. */
+#define ZL_KV4_BAD_PAGE 1   /* a page outside 0 .. n_pages - 1: its slots are not there */
+#define ZL_KV4_BAD_LEN 2    /* a length outside 0 .. max_pages * page: taken as the nearer of the two */
+#define ZL_KV4_BAD_STARTS 4 /* a sequence's rows outside the tensors, or more than max_new: it takes no part */
+#define ZL_KV4_TIMEOUT 8    /* a bounded device wait gave up */
+
+/* New tokens' keys and values into the cache.  k, v: bf16 [n_tokens, n_kv_heads, d] with token strides (as the causal
+ * operators).  Sequence b brings tokens [starts[b], starts[b + 1]) (device, n_seqs + 1 numbers, ascending; NULL:
+ * n_tokens is n_seqs and sequence b brings token b) for its last slots, [lens[b] - n, lens[b]); tokens for slots
+ * below 0 and tokens of no sequence are left out.  Each block of 16 channels takes the scale nearest to its
+ * largest magnitude / 6 and each channel the nearest code, ties to even; NaN is held as 0, infinities as the largest
+ * magnitude, 6 * 2^13.  positions (device int32 [n_tokens]) and slot_positions (int32 [n_seqs, n_kv_heads, max_pages * page]),
+ * both or neither: the slot's position becomes the token's, for eviction.
+ * Pages that it writes belong to one sequence alone. */
+ZL_API zl_status zl_kv4_write(const zl_kv4_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              int64_t n_tokens, const int32_t* starts, const int32_t* positions, int32_t* slot_positions,
+                              void* stream);
+
+/* What the cache holds, as bf16 rows: slot s of sequence b becomes row row_starts[b] + s (device int64 [n_seqs]) of k_out,
+ * v_out [n_rows, n_kv_heads, d] with token strides, s < lens[b].  Rows of no sequence are left as they were; sequences' rows must be disjoint.
+ * Slots of a bad page read as 0.  The rows serve zl_causal_attn_fwd (kv_offset = row_starts[b]). */
+ZL_API zl_status zl_kv4_read(const zl_kv4_cache* cache, void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
+                             int64_t n_rows, const int64_t* row_starts, void* stream);
+
+/* Device scratch of zl_kv4_attn_fwd for these sizes; with weights != 0 it holds every score of the new tokens:
+ * 4 * max_new * group bytes for each slot that the table has room for. */
+ZL_API zl_status zl_kv4_attn_workspace(const zl_kv4_cache* cache, int32_t n_q_heads, int32_t max_new, int32_t weights,
+                                       int64_t* bytes);
+
+/* Attention of the newest tokens over the cache, which holds their own keys and values already: with n tokens
+ * [starts[b], starts[b + 1]) (as zl_kv4_write; at most max_new of a sequence) query i sees slots j <= lens[b] - n + i.
+ *   q: bf16 [n_tokens, n_q_heads, d] with a token stride; n_q_heads a multiple of n_kv_heads, query head h reads key
+ *   head h / (n_q_heads / n_kv_heads).  o: bf16 [n_tokens, n_q_heads, d] contiguous; lse: fp32 [n_tokens, n_q_heads]; 0 and
+ *   -inf for a query that sees no slot.  Rows of no sequence are left as they were.
+ *   weights, weights_out: fp32 [n_seqs, n_kv_heads, max_pages * page] or NULL.  weights_out[slot] = decay * weights[slot] + the sum of the
+ *   slot's softmax weights over the new tokens and the group's heads, for slots below lens[b]; weights counts as 0 where it is
+ *   NULL and in the new tokens' slots.  The two may be the same buffer.  decay: finite.
+ *   scale: positive, normal.  workspace: zl_kv4_attn_workspace bytes (no call may share it with one that may run at the same time).
+ * P is rounded to fp16 (its row's running maximum is 1 to 256); sums are fp32.  Results repeat bit for bit.
+ * For prompts (more than some 64 rows, tokens x group, a key head) zl_kv4_read and zl_causal_attn_fwd are faster. */
+ZL_API zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, int64_t q_stride, int64_t n_tokens,
+                                 int32_t n_q_heads, const int32_t* starts, int32_t max_new, void* o, float* lse,
+                                 const float* weights, float* weights_out, float decay, void* workspace, float scale,
+                                 void* stream);
+
+/* Device scratch of zl_kv4_evict. */
+ZL_API zl_status zl_kv4_evict_workspace(const zl_kv4_cache* cache, int64_t* bytes);
+
+/* Every head of a sequence longer than `keep` slots gives up all but `keep` of them.  In order of claim: the slots whose
+ * position is above newest - recent (newest: the largest position in the head's slots), then the others; among each the
+ * larger weight, then the lower slot (NaN ranks below all numbers).  Survivors in slots >= keep move, in order, into
+ * the slots below keep that were given up, in order; other slots stay where they are.  The new lengths are
+ * min(lens[b], keep): the caller sets them.
+ *   weights fp32, positions int32 [n_seqs, n_kv_heads, max_pages * page]: by slot, not changed; weights_out,
+ *   positions_out: the same for the kept slots, in their new places (rest left as it was); either may be its input
+ *   (then only moved slots are written).  keep >= 1, recent >= 0.  workspace: zl_kv4_evict_workspace bytes.
+ * Calling it again with the same inputs and lens leaves the same cache.  Pages that it writes belong to one sequence alone. */
+ZL_API zl_status zl_kv4_evict(const zl_kv4_cache* cache, const float* weights, const int32_t* positions, int32_t keep,
+                              int32_t recent, float* weights_out, int32_t* positions_out, void* workspace, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
