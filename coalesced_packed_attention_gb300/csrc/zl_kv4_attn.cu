@@ -97,6 +97,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
@@ -108,11 +113,23 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
+  return x;
+}
+// log of a sum l of 2^(score - m); -inf for an empty one, NaN stays.
+__device__ __forceinline__ float natural_lse(float m, float l) { return l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l); }
+
 // ---------------------------------------------------------------- the schedule
+// The items' costs in a row, dealt out evenly: an item costs its units and kItemCost more (its queries, its join), which
+// stand before the first unit.  A cut inside them belongs to the first unit.
+constexpr int kItemCost = 4;
+
 // A block's run of units, item by item; the producers of the warps and their consumers each walk it by themselves.
 template <int NT>
 struct Walk {
-  int64_t left;        // units of the block's run from this segment on
+  int64_t left;        // cost of the block's run from this segment on
   int32_t seq, item;   // item: key head x row tiles
   int32_t n, m, first; // the sequence's new tokens, slots and first token
   int32_t row_tiles, chunks, items;
@@ -125,13 +142,18 @@ struct Walk {
     chunks = m > 0 ? (m + kUnit - 1) / kUnit : 1;
     items = p.c.heads * row_tiles;
   }
-  __device__ int64_t units() const { return (int64_t)items * chunks; }
-  __device__ void cut() { e = (int)(left < chunks - a ? a + left : chunks); }
-  __device__ bool done() const { return left <= 0; }
+  __device__ int64_t cost() const { return (int64_t)items * (chunks + kItemCost); }
+  // at cost `off` of the item: the segment from there on, without units where `left` ends before the first one
+  __device__ void enter(int off) {
+    const int end = (int)(left < chunks + kItemCost - off ? off + left : chunks + kItemCost);
+    a = off > kItemCost ? off - kItemCost : 0;
+    e = end > kItemCost ? end - kItemCost : 0;
+    left -= end - off;
+  }
+  __device__ bool done() const { return a >= e; }  // a segment without units is the last
   __device__ void next(const AttnParams& p) {
-    left -= e - a;
+    a = e = 0;
     if (left <= 0) return;
-    a = 0;
     if (++item == items) {
       item = 0;
       do {
@@ -142,7 +164,7 @@ struct Walk {
         load(p);
       } while (items == 0);
     }
-    cut();
+    enter(0);
   }
 };
 
@@ -179,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
 
   // this block's run
   Walk<NT> cons;
+  int64_t each;  // cost of a block's run
   {
     const int n = p.c.n_seqs, per = (n + kThreads - 1) / kThreads;
     const int b0 = min(n, (int)threadIdx.x * per), b1 = min(n, b0 + per);
@@ -186,18 +209,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
     for (int b = b0; b < b1; ++b) {
       cons.seq = b;
       cons.load(p);
-      mine += cons.units();
+      mine += cons.cost();
     }
     int64_t before = kv4_scan<kThreads>(mine, &total, warp_sums);
-    const int64_t each = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kWarps);
+    each = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(kWarps + kItemCost));
     const int64_t at = each * blockIdx.x, end = min(total, at + each);
     if (at < end && at >= before && at < before + mine) {
       int b = b0;
       for (;; ++b) {
         cons.seq = b;
         cons.load(p);
-        if (at < before + cons.units()) break;
-        before += cons.units();
+        if (at < before + cons.cost()) break;
+        before += cons.cost();
       }
       s_seq = b;
       s_before = before;
@@ -210,23 +233,27 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
     cons.seq = s_seq;
     cons.load(p);
     cons.left = end - at;
-    const int64_t off = at - s_before;
-    cons.item = (int)(off / cons.chunks);
-    cons.a = (int)(off - (int64_t)cons.item * cons.chunks);
-    cons.cut();
+    const int64_t off = at - s_before, of_item = cons.chunks + kItemCost;
+    cons.item = (int)(off / of_item);
+    cons.enter((int)(off - cons.item * of_item));
     if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;  // an item cut at the run's end sets it below
   }
-  const int64_t share = cons.left;  // of every block before the last one
 
   Walk<NT> prod = cons;
   int prod_x = prod.a + warp;  // next unit of this warp to load
-  auto settle = [&](Walk<NT>& w, int& x) {  // to the next unit of this warp, in this segment or a later one
-    while (!w.done() && x >= w.e) {
-      w.next(p);
-      x = w.a + warp;
+  int page0 = -1, page1 = -1;  // the pages of its two tiles, loaded ahead of their use
+  auto settle = [&]() {        // to the next unit of this warp, in this segment or a later one
+    while (!prod.done() && prod_x >= prod.e) {
+      prod.next(p);
+      prod_x = prod.a + warp;
     }
+    if (prod.done()) return;
+    const int slot = prod_x * kUnit;
+    const int32_t* table = p.c.pages + (int64_t)prod.seq * p.c.max_pages;
+    page0 = slot < prod.m ? table[slot >> p.c.page_shift] : -1;
+    page1 = slot + kKv4Slots >= prod.m ? -1 : p.c.page_shift > 4 ? page0 : table[(slot >> 4) + 1];
   };
-  settle(prod, prod_x);
+  settle();
   uint8_t* ring = smem + warp * S::kStages * S::kStageBytes;
   uint64_t* bar = bars + warp * S::kStages;
   uint32_t there = 0;   // two bits a stage: which tiles of it were copied
@@ -234,26 +261,27 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
   int fill = 0, drain = 0, in_flight = 0;
   auto produce = [&]() {
     if (prod.done()) return;
-    const int head = prod.item / prod.row_tiles, slot = prod_x * kUnit;
-    uint8_t* dst = ring + fill * S::kStageBytes;
-    uint8_t* src0 = slot < prod.m ? kv4_tile<D>(p.c, prod.seq, head, slot) : nullptr;
-    uint8_t* src1 = slot + kKv4Slots < prod.m ? kv4_tile<D>(p.c, prod.seq, head, slot + kKv4Slots) : nullptr;
+    const int head = NT == 1 && prod.row_tiles == 1 ? prod.item : prod.item / prod.row_tiles, slot = prod_x * kUnit;
+    const bool ok0 = (uint32_t)page0 < (uint32_t)p.c.n_pages, ok1 = (uint32_t)page1 < (uint32_t)p.c.n_pages;
     if (lane == 0) {
-      const uint32_t b = smem_u32(&bar[fill]);
-      if ((slot < prod.m && !src0) || (slot + kKv4Slots < prod.m && !src1)) kv4_report(p.c, ZL_KV4_BAD_PAGE);
-      mbar_arrive_expect_tx(&bar[fill], (src0 ? 18 * D : 0) + (src1 ? 18 * D : 0));
-      if (src0 && src1 == src0 + 18 * D) {
-        bulk_load(smem_u32(dst), src0, 36 * D, b);
+      const uint32_t dst = smem_u32(ring + fill * S::kStageBytes), b = smem_u32(&bar[fill]);
+      // tiles of the cache number less than 2^32
+      const uint32_t shift = p.c.page_shift - 4, within = (slot >> 4) & ((1 << shift) - 1);
+      const uint8_t* src0 = p.c.data + (uint64_t)((((uint32_t)page0 * p.c.heads + head) << shift) + within) * (18 * D);
+      mbar_arrive_expect_tx(&bar[fill], (ok0 ? 18 * D : 0) + (ok1 ? 18 * D : 0));
+      if (ok0 && ok1 && shift > 0) {  // the two are neighbours
+        bulk_load(dst, src0, 36 * D, b);
       } else {
-        if (src0) bulk_load(smem_u32(dst), src0, 18 * D, b);
-        if (src1) bulk_load(smem_u32(dst) + 18 * D, src1, 18 * D, b);
+        if (ok0) bulk_load(dst, src0, 18 * D, b);
+        if (ok1) bulk_load(dst + 18 * D, shift > 0 ? src0 + 18 * D : p.c.data + (uint64_t)((uint32_t)page1 * p.c.heads + head) * (18 * D), 18 * D, b);
+        if ((!ok0 && slot < prod.m) || (!ok1 && slot + kKv4Slots < prod.m)) kv4_report(p.c, ZL_KV4_BAD_PAGE);
       }
     }
-    there = (there & ~(3u << (2 * fill))) | ((src0 ? 1u : 0u) | (src1 ? 2u : 0u)) << (2 * fill);
+    there = (there & ~(3u << (2 * fill))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * fill);
     fill = fill + 1 == S::kStages ? 0 : fill + 1;
     ++in_flight;
     prod_x += kWarps;
-    settle(prod, prod_x);
+    settle();
   };
 #pragma unroll
   for (int i = 0; i < S::kStages; ++i) produce();
@@ -303,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         for (int x = 0; x < 4; ++x)  // four channels are a step's
           qf[j][2 * i + x / 2][x & 1] = pack_half(__uint_as_float(w[x] << 16) * down, __uint_as_float(w[x] & 0xFFFF0000u) * down);
       }
-      const float mine = up * p.scale_log2;
+      const float mine = fmaxf(up * p.scale_log2, 0x1p-126f);  // not 0, which -inf is multiplied by
       f[j][0] = __shfl_sync(0xffffffffu, mine, 8 * t);
       f[j][1] = __shfl_sync(0xffffffffu, mine, 8 * t + 4);
     }
@@ -343,20 +371,22 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
           ca[0] = a.x; ca[1] = a.y; ca[2] = a.z; ca[3] = a.w;
           cb[0] = b.x; cb[1] = b.y; cb[2] = b.z; cb[3] = b.w;
           const uint32_t at = tile + 16 * D + key0 * 8 + 2 * t;
-          sa[0] = lds8(at); sa[1] = lds8(at + 1); sb[0] = lds8(at + 64); sb[1] = lds8(at + 65);
+          const uint32_t pa = lds16(at), pb = lds16(at + 64);
+          sa[0] = __byte_perm(pa, 0, 0x4040) << 7; sa[1] = __byte_perm(pa, 0, 0x4141) << 7;
+          sb[0] = __byte_perm(pb, 0, 0x4040) << 7; sb[1] = __byte_perm(pb, 0, 0x4141) << 7;
         } else {
           const uint2 a = lds64(tile + key0 * 32 + t * 8), b = lds64(tile + (key0 + 8) * 32 + t * 8);
           ca[0] = a.x; ca[1] = a.y;
           cb[0] = b.x; cb[1] = b.y;
-          sa[0] = sa[1] = lds8(tile + 16 * D + key0 * 4 + t);
-          sb[0] = sb[1] = lds8(tile + 16 * D + (key0 + 8) * 4 + t);
+          sa[0] = sa[1] = __byte_perm(lds8(tile + 16 * D + key0 * 4 + t), 0, 0x4040) << 7;
+          sb[0] = sb[1] = __byte_perm(lds8(tile + 16 * D + (key0 + 8) * 4 + t), 0, 0x4040) << 7;
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {  // a word: 8 channels, two steps
           uint32_t a[4], b[4];
           kv4_decode(ca[w], a);
           kv4_decode(cb[w], b);
-          const uint32_t s2a = kv4_scale2(sa[w / 2], sa[w / 2]), s2b = kv4_scale2(sb[w / 2], sb[w / 2]);
+          const uint32_t s2a = sa[w / 2], s2b = sb[w / 2];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             a[y] = kv4_mul(a[y], s2a);
@@ -369,13 +399,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
               mma16(s[i][j], a[2 * y], b[2 * y], a[2 * y + 1], b[2 * y + 1], qf[j][2 * w + y][0], qf[j][2 * w + y][1]);
         }
       }
-      // base-2 scores; slots that a row does not see, or that are not there, are -inf
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) s[i][j][y] *= f[j][y & 1];
+      // slots that a row does not see, or that are not there, are -inf; the products' sums become base-2 scores by f
       if (!plain) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -402,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
 #pragma unroll
             for (int j = 0; j < NT; ++j)
               if (row0 + 8 * j + 2 * t < rows)
-                *reinterpret_cast<float2*>(dst + (int64_t)key * p.score_rows + 8 * j + 2 * t) = make_float2(s[i][j][2 * y], s[i][j][2 * y + 1]);
+                *reinterpret_cast<float2*>(dst + (int64_t)key * p.score_rows + 8 * j + 2 * t) = make_float2(s[i][j][2 * y] * f[j][0], s[i][j][2 * y + 1] * f[j][1]);
           }
       }
       float top[NT][2];
@@ -411,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          top[j][y] = fmaxf(fmaxf(s[0][j][y], s[0][j][y + 2]), fmaxf(s[1][j][y], s[1][j][y + 2]));
+          top[j][y] = max3(fmaxf(s[0][j][y], s[0][j][y + 2]), s[1][j][y], s[1][j][y + 2]) * f[j][y];
           grow |= top[j][y] > ref[j][y] + kRescale;
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -439,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         const float r0 = ref[j][0] == -INFINITY ? 0.f : ref[j][0], r1 = ref[j][1] == -INFINITY ? 0.f : ref[j][1];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float p0 = ex2(s[i][j][0] - r0), p1 = ex2(s[i][j][1] - r1), p2 = ex2(s[i][j][2] - r0), p3 = ex2(s[i][j][3] - r1);
+          const float p0 = ex2(fmaf(s[i][j][0], f[j][0], -r0)), p1 = ex2(fmaf(s[i][j][1], f[j][1], -r1));
+          const float p2 = ex2(fmaf(s[i][j][2], f[j][0], -r0)), p3 = ex2(fmaf(s[i][j][3], f[j][1], -r1));
           sum[j][0] += p0 + p2;
           sum[j][1] += p1 + p3;
           pb[i][j][0] = transpose8(pack_half(p0, p1));
@@ -469,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
           for (int y = 0; y < 4; ++y)
             if (!((have >> i) & 1) || slot0 + i * 16 + keys[y] >= cons.m) sc[y] = 0;
         }
-        const uint32_t s01 = kv4_scale2(sc[0], sc[1]), s23 = kv4_scale2(sc[2], sc[3]);
+        const uint32_t s01 = __byte_perm(sc[0], sc[1], 0x1410) << 7, s23 = __byte_perm(sc[2], sc[3], 0x1410) << 7;
 #pragma unroll
         for (int w = 0; w < D / 64; ++w) {
           uint32_t a0[4], a1[4], a2[4], a3[4];
@@ -529,14 +554,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         const int64_t at = (int64_t)(cons.first + tok) * p.q_heads + head * p.group + (row0 + r - tok * p.group);
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
         *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (c4 == 0) p.lse[at] = m == -INFINITY && !(l > 0.f) && l == l ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+        if (c4 == 0) p.lse[at] = natural_lse(m, l);
       } else {
         *reinterpret_cast<float4*>(p.part_o + ((int64_t)part * S::kRows + r) * D + 4 * c4) = o;
         if (c4 == 0) p.part_ml[(int64_t)part * S::kRows + r] = make_float2(m, l);
       }
     }
     if (threadIdx.x == 0 && cons.a == 0 && cons.e < cons.chunks) {
-      // the run ends inside this item: full shares follow until its end
       Cut c;
       c.which = first_segment ? 0 : 1;
       c.token0 = cons.first;
@@ -544,8 +568,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
       c.row0 = row0;
       c.rows = rows;
       c.pad[0] = c.pad[1] = 0;
-      const int64_t rest = cons.chunks - cons.e;
-      c.parts = 1 + (int)((rest + share - 1) / share);
+      const int64_t rest = cons.chunks - cons.e;  // full runs follow until the item's end
+      c.parts = 1 + (int)((rest + each - 1) / each);
       p.cuts[blockIdx.x] = c;
     }
     first_segment = false;
@@ -561,28 +585,51 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
 }
 
 // ---------------------------------------------------------------- joining cut items
+// A block takes 8 rows of a cut item; four warps a row share its parts.  (One warp a row took 39 us for the 76 parts of a
+// sequence of 131 071 slots and 8 key heads.)
+constexpr int kJoinWays = 4;
 template <int D>
-__global__ void __launch_bounds__(256) zl_kv4_join_kernel(const AttnParams p, int32_t tile_rows) {
+__global__ void __launch_bounds__(256 * kJoinWays) zl_kv4_join_kernel(const AttnParams p, int32_t tile_rows) {
+  __shared__ float s_o[kJoinWays][8][D];
+  __shared__ float2 s_ml[kJoinWays][8];
   let_next_start();
   wait_for_previous();
   const Cut c = p.cuts[blockIdx.x];
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (c.parts == 0 || c.row0 + r >= c.rows || r >= tile_rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = warp & 7, way = warp >> 3;
+  const int r = blockIdx.y * 8 + row;
+  if (c.parts == 0 || c.row0 + (int)blockIdx.y * 8 >= c.rows) return;
+  const bool there = c.row0 + r < c.rows;
   auto part = [&](int i) { return (int64_t)(i == 0 ? 2 * blockIdx.x + c.which : 2 * (blockIdx.x + i)) * tile_rows + r; };
-  float m = -INFINITY;
-  for (int i = lane; i < c.parts; i += 32) m = fmaxf(m, p.part_ml[part(i)].x);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   constexpr int kPer = D / 32;
-  float o[kPer] = {}, l = 0.f;
+  float m = -INFINITY, l = 0.f, o[kPer] = {};
+  if (there) {
+    for (int i = lane; i < c.parts; i += 32) m = fmaxf(m, p.part_ml[part(i)].x);
+    m = warp_max(m);
 #pragma unroll 4
-  for (int i = 0; i < c.parts; ++i) {
-    const float2 ml = p.part_ml[part(i)];
-    const float k = m == -INFINITY ? 1.f : ex2(ml.x - m);
-    l = fmaf(ml.y, k, l);
-    const float* src = p.part_o + part(i) * D + lane * kPer;
+    for (int i = way; i < c.parts; i += kJoinWays) {
+      const float2 ml = p.part_ml[part(i)];
+      const float k = m == -INFINITY ? 1.f : ex2(ml.x - m);
+      l = fmaf(ml.y, k, l);
+      const float* src = p.part_o + part(i) * D + lane * kPer;
+      if constexpr (kPer == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        o[0] = fmaf(v.x, k, o[0]); o[1] = fmaf(v.y, k, o[1]); o[2] = fmaf(v.z, k, o[2]); o[3] = fmaf(v.w, k, o[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        o[0] = fmaf(v.x, k, o[0]); o[1] = fmaf(v.y, k, o[1]);
+      }
+    }
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] = fmaf(src[x], k, o[x]);
+    for (int x = 0; x < kPer; ++x) s_o[way][row][lane * kPer + x] = o[x];
+    if (lane == 0) s_ml[way][row] = make_float2(m, l);
+  }
+  __syncthreads();
+  if (!there || way != 0) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWays; ++w) {
+    l += s_ml[w][row].y;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] += s_o[w][row][lane * kPer + x];
   }
   const int tok = (c.row0 + r) / p.group;
   const int64_t at = (int64_t)(c.token0 + tok) * p.q_heads + c.head0 + (c.row0 + r - tok * p.group);
@@ -590,7 +637,7 @@ __global__ void __launch_bounds__(256) zl_kv4_join_kernel(const AttnParams p, in
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + at * D + lane * kPer);
 #pragma unroll
   for (int x = 0; x < kPer; x += 2) dst[x / 2] = pack_bf16(o[x] * inv, o[x + 1] * inv);
-  if (lane == 0) p.lse[at] = m == -INFINITY && !(l > 0.f) && l == l ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+  if (lane == 0) p.lse[at] = natural_lse(m, l);
 }
 
 // ---------------------------------------------------------------- accumulated weights
@@ -668,7 +715,7 @@ cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
   const int blocks = sms * per_sm < kMaxBlocks ? sms * per_sm : kMaxBlocks;
   e = launch_overlapped(kernel, blocks, kThreads, S::kSmem, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(zl_kv4_join_kernel<D>, dim3(blocks, NT), 256, 0, stream, p, S::kRows);
+  return launch_overlapped(zl_kv4_join_kernel<D>, dim3(blocks, NT), 256 * kJoinWays, 0, stream, p, S::kRows);
 }
 template <int D, bool kScores>
 cudaError_t launch_attn(const AttnParams& p, int columns, int sms, cudaStream_t stream) {
