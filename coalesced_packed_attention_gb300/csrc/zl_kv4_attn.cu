@@ -36,12 +36,15 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;          // slots of a unit: two tiles
 constexpr int kMaxBlocks = 640;    // blocks of a launch at most: what the workspace has room for
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t kTwice = 0x00800080u;  // a scale's bits times this: the scale in both halves, by the multiplier, which has time
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+constexpr float kLow = -1e30f;     // the running maximum of rows that have seen nothing
 constexpr float kRescale = 8.f;    // the maximum may lag by 2^8 before the sums are rescaled
 
 // An item cut between blocks: its first block describes it for the join.
-struct Cut {
-  int32_t parts;   // 0: no item begins here that another block ends
-  int32_t which;   // part of the first block (the following blocks' parts are their first)
+struct alignas(16) Cut {
+  int32_t parts;   // 0: the item was not cut, or none that begins in this block
+  int32_t which;   // part of its first block, 2 block + (0 the block's first segment, 1 another); the following blocks' parts are their first
   int32_t token0;  // row of the item's sequence in q and o
   int32_t head0;   // first query head
   int32_t row0, rows;
@@ -57,8 +60,9 @@ struct AttnParams {
   float* lse;
   float* part_o;   // [2 blocks][rows][d]
   float2* part_ml; // [2 blocks][rows]: maximum (base 2) and sum
-  Cut* cuts;       // [blocks]
-  float* scores;   // [sequence][key head][slot][score_rows], base 2
+  Cut* cuts;       // by item where there are no more items than blocks, else by the block in which the item begins
+  int32_t max_tiles, by_item;  // row tiles of max_new tokens; how cuts is laid out
+  float* scores;   // [sequence][key head][score_rows][slot], base 2
   const float* w_in;
   float* w_out;
   float decay;
@@ -68,13 +72,19 @@ struct AttnParams {
 
 // ---------------------------------------------------------------- pieces of a product
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The first product of a sum.
+__device__ __forceinline__ void mma16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t o;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(x));
   return o;
 }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
@@ -82,57 +92,28 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(hi), "f"(lo));
   return o;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int i = 16; i > 0; i >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
-  return x;
-}
 // log of a sum l of 2^(score - m); -inf for an empty one, NaN stays.
-__device__ __forceinline__ float natural_lse(float m, float l) { return l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l); }
+__device__ __forceinline__ float natural_lse(float m, float l) { return l == 0.f ? -INFINITY : m * kLn2 + logf(l); }
 
 // ---------------------------------------------------------------- the schedule
 // The items' costs in a row, dealt out evenly: an item costs its units and kItemCost more (its queries, its join), which
-// stand before the first unit.  A cut inside them belongs to the first unit.
-constexpr int kItemCost = 4;
+// stand before the first unit.  A cut inside them belongs to the first unit.  (64 single tokens over 15 to 16 384 slots
+// each: 98 us at 4, 87 at 8 and 12, 90 at 20.)
+constexpr int kItemCost = 8;
 
 // A block's run of units, item by item; the producers of the warps and their consumers each walk it by themselves.
 template <int NT>
 struct Walk {
   int64_t left;        // cost of the block's run from this segment on
-  int32_t seq, item;   // item: key head x row tiles
-  int32_t n, m, first; // the sequence's new tokens, slots and first token
-  int32_t row_tiles, chunks, items;
+  int32_t seq, head, tile;  // an item: a key head's row tile
+  int32_t n, m, first;      // the sequence's new tokens, slots and first token
+  int32_t row_tiles, chunks;
   int32_t a, e;        // this segment: units [a, e) of the item's `chunks`
 
   __device__ void load(const AttnParams& p) {
@@ -140,9 +121,8 @@ struct Walk {
     m = kv4_len(p.c, seq);
     row_tiles = (n * p.group + 8 * NT - 1) / (8 * NT);
     chunks = m > 0 ? (m + kUnit - 1) / kUnit : 1;
-    items = p.c.heads * row_tiles;
   }
-  __device__ int64_t cost() const { return (int64_t)items * (chunks + kItemCost); }
+  __device__ int64_t cost(const AttnParams& p) const { return (int64_t)p.c.heads * row_tiles * (chunks + kItemCost); }
   // at cost `off` of the item: the segment from there on, without units where `left` ends before the first one
   __device__ void enter(int off) {
     const int end = (int)(left < chunks + kItemCost - off ? off + left : chunks + kItemCost);
@@ -154,15 +134,18 @@ struct Walk {
   __device__ void next(const AttnParams& p) {
     a = e = 0;
     if (left <= 0) return;
-    if (++item == items) {
-      item = 0;
-      do {
-        if (++seq >= p.c.n_seqs) {
-          left = 0;
-          return;
-        }
-        load(p);
-      } while (items == 0);
+    if (++tile == row_tiles) {
+      tile = 0;
+      if (++head == p.c.heads) {
+        head = 0;
+        do {
+          if (++seq >= p.c.n_seqs) {
+            left = 0;
+            return;
+          }
+          load(p);
+        } while (row_tiles == 0);
+      }
     }
     enter(0);
   }
@@ -209,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
     for (int b = b0; b < b1; ++b) {
       cons.seq = b;
       cons.load(p);
-      mine += cons.cost();
+      mine += cons.cost(p);
     }
     int64_t before = kv4_scan<kThreads>(mine, &total, warp_sums);
     each = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(kWarps + kItemCost));
@@ -219,69 +202,84 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
       for (;; ++b) {
         cons.seq = b;
         cons.load(p);
-        if (at < before + cons.cost()) break;
-        before += cons.cost();
+        if (at < before + cons.cost(p)) break;
+        before += cons.cost(p);
       }
       s_seq = b;
       s_before = before;
     }
     __syncthreads();
     if (s_seq < 0) {  // nothing for this block (uniform: the run is empty)
-      if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;
+      if (threadIdx.x == 0 && !p.by_item) p.cuts[blockIdx.x].parts = 0;
       return;
     }
     cons.seq = s_seq;
     cons.load(p);
     cons.left = end - at;
     const int64_t off = at - s_before, of_item = cons.chunks + kItemCost;
-    cons.item = (int)(off / of_item);
-    cons.enter((int)(off - cons.item * of_item));
-    if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;  // an item cut at the run's end sets it below
+    const int item = (int)(off / of_item);
+    cons.head = item / cons.row_tiles;
+    cons.tile = item - cons.head * cons.row_tiles;
+    cons.enter((int)(off - item * of_item));
+    if (threadIdx.x == 0 && !p.by_item) p.cuts[blockIdx.x].parts = 0;  // an item cut at the run's end sets it below
   }
 
+  // Loading: a warp looks up the places of its next 32 units at once, one a lane, and issues them one by one.
   Walk<NT> prod = cons;
-  int prod_x = prod.a + warp;  // next unit of this warp to load
-  int page0 = -1, page1 = -1;  // the pages of its two tiles, loaded ahead of their use
-  auto settle = [&]() {        // to the next unit of this warp, in this segment or a later one
-    while (!prod.done() && prod_x >= prod.e) {
+  int prod_x = prod.a + warp;         // the next unit to look up
+  uint32_t tile0 = kNone, tile1 = kNone;  // the two tiles of a lane's unit
+  int batch = 0, batch_end = 0;       // units looked up and not yet issued: lanes [batch, batch_end)
+  bool any_bad = false;               // a page of this run is none of the cache's
+  auto look_up = [&]() {
+    batch = batch_end = 0;
+    while (prod_x >= prod.e) {  // to the next segment that has a unit for this warp
       prod.next(p);
+      if (prod.done()) return;
       prod_x = prod.a + warp;
     }
-    if (prod.done()) return;
-    const int slot = prod_x * kUnit;
+    const int x = prod_x + kWarps * lane, slot = x * kUnit, shift = p.c.page_shift - 4;
     const int32_t* table = p.c.pages + (int64_t)prod.seq * p.c.max_pages;
-    page0 = slot < prod.m ? table[slot >> p.c.page_shift] : -1;
-    page1 = slot + kKv4Slots >= prod.m ? -1 : p.c.page_shift > 4 ? page0 : table[(slot >> 4) + 1];
+    bool bad = false;
+    auto place = [&](int at) {  // tiles of the cache number less than 2^32
+      if (x >= prod.e || at >= prod.m) return kNone;
+      const uint32_t page = table[at >> p.c.page_shift];
+      if (page >= (uint32_t)p.c.n_pages) {
+        bad = true;
+        return kNone;
+      }
+      return ((page * p.c.heads + prod.head) << shift) + ((at >> 4) & ((1 << shift) - 1));
+    };
+    tile0 = place(slot);
+    tile1 = place(slot + kKv4Slots);
+    if (bad) kv4_report(p.c, ZL_KV4_BAD_PAGE);
+    any_bad |= __any_sync(0xffffffffu, bad);
+    batch_end = min(32, (prod.e - prod_x + kWarps - 1) / kWarps);
+    prod_x += 32 * kWarps;
   };
-  settle();
   uint8_t* ring = smem + warp * S::kStages * S::kStageBytes;
   uint64_t* bar = bars + warp * S::kStages;
-  uint32_t there = 0;   // two bits a stage: which tiles of it were copied
   uint32_t phases = 0;  // parity of each stage's next wait
   int fill = 0, drain = 0, in_flight = 0;
   auto produce = [&]() {
-    if (prod.done()) return;
-    const int head = NT == 1 && prod.row_tiles == 1 ? prod.item : prod.item / prod.row_tiles, slot = prod_x * kUnit;
-    const bool ok0 = (uint32_t)page0 < (uint32_t)p.c.n_pages, ok1 = (uint32_t)page1 < (uint32_t)p.c.n_pages;
+    if (batch == batch_end) {
+      look_up();
+      if (batch == batch_end) return;
+    }
+    const uint32_t t0 = __shfl_sync(0xffffffffu, tile0, batch), t1 = __shfl_sync(0xffffffffu, tile1, batch);
+    ++batch;
     if (lane == 0) {
       const uint32_t dst = smem_u32(ring + fill * S::kStageBytes), b = smem_u32(&bar[fill]);
-      // tiles of the cache number less than 2^32
-      const uint32_t shift = p.c.page_shift - 4, within = (slot >> 4) & ((1 << shift) - 1);
-      const uint8_t* src0 = p.c.data + (uint64_t)((((uint32_t)page0 * p.c.heads + head) << shift) + within) * (18 * D);
-      mbar_arrive_expect_tx(&bar[fill], (ok0 ? 18 * D : 0) + (ok1 ? 18 * D : 0));
-      if (ok0 && ok1 && shift > 0) {  // the two are neighbours
-        bulk_load(dst, src0, 36 * D, b);
+      if (t0 != kNone && t1 == t0 + 1) {
+        mbar_arrive_expect_tx(&bar[fill], 36 * D);
+        bulk_load(dst, p.c.data + (uint64_t)t0 * (18 * D), 36 * D, b);
       } else {
-        if (ok0) bulk_load(dst, src0, 18 * D, b);
-        if (ok1) bulk_load(dst + 18 * D, shift > 0 ? src0 + 18 * D : p.c.data + (uint64_t)((uint32_t)page1 * p.c.heads + head) * (18 * D), 18 * D, b);
-        if ((!ok0 && slot < prod.m) || (!ok1 && slot + kKv4Slots < prod.m)) kv4_report(p.c, ZL_KV4_BAD_PAGE);
+        mbar_arrive_expect_tx(&bar[fill], (t0 != kNone ? 18 * D : 0) + (t1 != kNone ? 18 * D : 0));
+        if (t0 != kNone) bulk_load(dst, p.c.data + (uint64_t)t0 * (18 * D), 18 * D, b);
+        if (t1 != kNone) bulk_load(dst + 18 * D, p.c.data + (uint64_t)t1 * (18 * D), 18 * D, b);
       }
     }
-    there = (there & ~(3u << (2 * fill))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * fill);
-    fill = fill + 1 == S::kStages ? 0 : fill + 1;
+    fill = (fill + 1) % S::kStages;
     ++in_flight;
-    prod_x += kWarps;
-    settle();
   };
 #pragma unroll
   for (int i = 0; i < S::kStages; ++i) produce();
@@ -290,13 +288,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
   // halves of the banks
   const int key0 = (g & ~1) | ((g & 1) ^ ((g >> 1) & 1));  // row g of a product; row g + 8 is key0 + 8
   const int ka = 2 * t + (t & 1), kb = 2 * t + 1 - (t & 1);
+  // where a lane reads in a tile: codes and scales of its keys' K (8 keys on: half of them further), and of its V
+  const int k_at = key0 * (D / 2) + t * (D / 8), ks_at = 16 * D + key0 * (D / 16) + t * (D / 64);
+  const int va_at = 8 * D + ka * (D / 2) + g * (D / 16), vb_at = 8 * D + kb * (D / 2) + g * (D / 16);
+  const int vsa_at = 17 * D + ka * (D / 16) + g * D / 128, vsb_at = 17 * D + kb * (D / 16) + g * D / 128;
   bool first_segment = true, alive = true;
   for (; !cons.done(); cons.next(p)) {
-    const int head = cons.item / cons.row_tiles, row0 = (cons.item - head * cons.row_tiles) * S::kRows;
+    const int head = cons.head, row0 = cons.tile * S::kRows;
     const int rows = cons.n * p.group;
     // queries: lane (g, t) holds quarter t of the channels of row g of every 8
     uint32_t qf[NT][D / 16][2];
-    float f[NT][2];
+    float2 f[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int r = row0 + 8 * j + g;
@@ -332,14 +334,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
           qf[j][2 * i + x / 2][x & 1] = pack_half(__uint_as_float(w[x] << 16) * down, __uint_as_float(w[x] & 0xFFFF0000u) * down);
       }
       const float mine = fmaxf(up * p.scale_log2, 0x1p-126f);  // not 0, which -inf is multiplied by
-      f[j][0] = __shfl_sync(0xffffffffu, mine, 8 * t);
-      f[j][1] = __shfl_sync(0xffffffffu, mine, 8 * t + 4);
+      f[j] = make_float2(__shfl_sync(0xffffffffu, mine, 8 * t), __shfl_sync(0xffffffffu, mine, 8 * t + 4));
     }
-    float acc[D / 16][NT][4], ref[NT][2], sum[NT][2];
+    float acc[D / 16][NT][4];
+    float2 ref[NT], sum[NT];  // of a lane's two rows of every 8
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      ref[j][0] = ref[j][1] = -INFINITY;
-      sum[j][0] = sum[j][1] = 0.f;
+      ref[j] = make_float2(kLow, kLow);
+      sum[j] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
     }
@@ -347,39 +349,41 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
 
     for (int x = cons.a + warp; x < cons.e; x += kWarps) {
       if (!alive) continue;
-      const uint32_t stage = smem_u32(ring + drain * S::kStageBytes);
+      const uint8_t* stage = ring + drain * S::kStageBytes;
       alive = __all_sync(0xffffffffu, mbar_wait(&bar[drain], (phases >> drain) & 1));
       if (!alive) {
         if (lane == 0) kv4_report(p.c, ZL_KV4_TIMEOUT);
         continue;
       }
-      const uint32_t have = (there >> (2 * drain)) & 3;
       phases ^= 1u << drain;
-      drain = drain + 1 == S::kStages ? 0 : drain + 1;
+      drain = (drain + 1) % S::kStages;
       --in_flight;
       const int slot0 = x * kUnit;
-      const bool plain = have == 3 && slot0 + kUnit - 1 <= full;
+      const bool plain = slot0 + kUnit - 1 <= full && !any_bad;
+      bool have[2] = {true, true};
+      if (!plain)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int at = slot0 + i * kKv4Slots;
+          have[i] = at < cons.m && (uint32_t)p.c.pages[(int64_t)cons.seq * p.c.max_pages + (at >> p.c.page_shift)] < (uint32_t)p.c.n_pages;
+        }
       float s[2][NT][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t tile = stage + i * 18 * D;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.f;
+        const uint8_t* tile = stage + i * 18 * D;
         uint32_t ca[D / 32], cb[D / 32], sa[2], sb[2];
         if constexpr (D == 128) {
-          const uint4 a = lds128(tile + key0 * 64 + t * 16), b = lds128(tile + (key0 + 8) * 64 + t * 16);
+          const uint4 a = *reinterpret_cast<const uint4*>(tile + k_at), b = *reinterpret_cast<const uint4*>(tile + k_at + 512);
           ca[0] = a.x; ca[1] = a.y; ca[2] = a.z; ca[3] = a.w;
           cb[0] = b.x; cb[1] = b.y; cb[2] = b.z; cb[3] = b.w;
-          const uint32_t at = tile + 16 * D + key0 * 8 + 2 * t;
-          const uint32_t pa = lds16(at), pb = lds16(at + 64);
-          sa[0] = __byte_perm(pa, 0, 0x4040) << 7; sa[1] = __byte_perm(pa, 0, 0x4141) << 7;
-          sb[0] = __byte_perm(pb, 0, 0x4040) << 7; sb[1] = __byte_perm(pb, 0, 0x4141) << 7;
+          const uint8_t* at = tile + ks_at;
+          sa[0] = at[0] * kTwice; sa[1] = at[1] * kTwice; sb[0] = at[64] * kTwice; sb[1] = at[65] * kTwice;
         } else {
-          const uint2 a = lds64(tile + key0 * 32 + t * 8), b = lds64(tile + (key0 + 8) * 32 + t * 8);
+          const uint2 a = *reinterpret_cast<const uint2*>(tile + k_at), b = *reinterpret_cast<const uint2*>(tile + k_at + 256);
           ca[0] = a.x; ca[1] = a.y;
           cb[0] = b.x; cb[1] = b.y;
-          sa[0] = sa[1] = __byte_perm(lds8(tile + 16 * D + key0 * 4 + t), 0, 0x4040) << 7;
-          sb[0] = sb[1] = __byte_perm(lds8(tile + 16 * D + (key0 + 8) * 4 + t), 0, 0x4040) << 7;
+          sa[0] = sa[1] = tile[ks_at] * kTwice;
+          sb[0] = sb[1] = tile[ks_at + 32] * kTwice;
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {  // a word: 8 channels, two steps
@@ -396,7 +400,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
           for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-              mma16(s[i][j], a[2 * y], b[2 * y], a[2 * y + 1], b[2 * y + 1], qf[j][2 * w + y][0], qf[j][2 * w + y][1]);
+            {
+              if (w == 0 && y == 0) mma16_first(s[i][j], a[0], b[0], a[1], b[1], qf[j][0][0], qf[j][0][1]);
+              else mma16(s[i][j], a[2 * y], b[2 * y], a[2 * y + 1], b[2 * y + 1], qf[j][2 * w + y][0], qf[j][2 * w + y][1]);
+            }
         }
       }
       // slots that a row does not see, or that are not there, are -inf; the products' sums become base-2 scores by f
@@ -408,15 +415,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
             const int last = cons.m - cons.n + (row0 + 8 * j + 2 * t + y) / p.group - slot0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const bool ok = (have >> i) & 1;
-              if (!ok || i * 16 + key0 > last) s[i][j][y] = -INFINITY;
-              if (!ok || i * 16 + key0 + 8 > last) s[i][j][y + 2] = -INFINITY;
+              if (!have[i] || i * 16 + key0 > last) s[i][j][y] = -INFINITY;
+              if (!have[i] || i * 16 + key0 + 8 > last) s[i][j][y + 2] = -INFINITY;
             }
           }
       }
       if constexpr (kScores) {
         const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift;
-        float* dst = p.scores + (((int64_t)cons.seq * p.c.heads + head) * slots + slot0) * p.score_rows + row0;
+        float* dst = p.scores + (((int64_t)cons.seq * p.c.heads + head) * p.score_rows + row0) * slots + slot0;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -424,75 +430,81 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
             const int key = i * 16 + key0 + 8 * y;
             if (slot0 + key >= cons.m) continue;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-              if (row0 + 8 * j + 2 * t < rows)
-                *reinterpret_cast<float2*>(dst + (int64_t)key * p.score_rows + 8 * j + 2 * t) = make_float2(s[i][j][2 * y] * f[j][0], s[i][j][2 * y + 1] * f[j][1]);
-          }
-      }
-      float top[NT][2];
-      bool grow = false;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          top[j][y] = max3(fmaxf(s[0][j][y], s[0][j][y + 2]), s[1][j][y], s[1][j][y + 2]) * f[j][y];
-          grow |= top[j][y] > ref[j][y] + kRescale;
-        }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float m = top[j][y];
-#pragma unroll
-            for (int x2 = 4; x2 < 32; x2 <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x2));
-            m = fmaxf(m, ref[j][y]);
-            const float down = m == -INFINITY ? 1.f : ex2(ref[j][y] - m);
-            ref[j][y] = m;
-            sum[j][y] *= down;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              acc[i][j][y] *= down;
-              acc[i][j][y + 2] *= down;
+            for (int j = 0; j < NT; ++j) {
+              const float2 x2 = mul2(make_float2(s[i][j][2 * y], s[i][j][2 * y + 1]), f[j]);
+              const int r = 8 * j + 2 * t;
+              if (row0 + r < rows) dst[r * slots + key] = x2.x;
+              if (row0 + r + 1 < rows) dst[(r + 1) * slots + key] = x2.y;
             }
           }
+      }
+      float2 top[NT];
+      bool grow = false;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        top[j] = mul2(make_float2(max3(fmaxf(s[0][j][0], s[0][j][2]), s[1][j][0], s[1][j][2]),
+                                  max3(fmaxf(s[0][j][1], s[0][j][3]), s[1][j][1], s[1][j][3])),
+                      f[j]);
+        const float2 most = add2(ref[j], make_float2(kRescale, kRescale));
+        grow |= top[j].x > most.x || top[j].y > most.y;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float2 m = top[j];
+#pragma unroll
+          for (int x2 = 4; x2 < 32; x2 <<= 1) {
+            m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, x2));
+            m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, x2));
+          }
+          m = make_float2(fmaxf(m.x, ref[j].x), fmaxf(m.y, ref[j].y));
+          const float2 down = make_float2(ex2(ref[j].x - m.x), ex2(ref[j].y - m.y));
+          ref[j] = m;
+          sum[j] = mul2(sum[j], down);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            acc[i][j][0] *= down.x;
+            acc[i][j][1] *= down.y;
+            acc[i][j][2] *= down.x;
+            acc[i][j][3] *= down.y;
+          }
+        }
       }
       uint32_t pb[2][NT][2];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const float r0 = ref[j][0] == -INFINITY ? 0.f : ref[j][0], r1 = ref[j][1] == -INFINITY ? 0.f : ref[j][1];
+        const float2 low = make_float2(-ref[j].x, -ref[j].y);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float p0 = ex2(fmaf(s[i][j][0], f[j][0], -r0)), p1 = ex2(fmaf(s[i][j][1], f[j][1], -r1));
-          const float p2 = ex2(fmaf(s[i][j][2], f[j][0], -r0)), p3 = ex2(fmaf(s[i][j][3], f[j][1], -r1));
-          sum[j][0] += p0 + p2;
-          sum[j][1] += p1 + p3;
-          pb[i][j][0] = transpose8(pack_half(p0, p1));
-          pb[i][j][1] = transpose8(pack_half(p2, p3));
+          const float2 e0 = fma2(make_float2(s[i][j][0], s[i][j][1]), f[j], low), e1 = fma2(make_float2(s[i][j][2], s[i][j][3]), f[j], low);
+          const float2 p0 = make_float2(ex2(e0.x), ex2(e0.y)), p1 = make_float2(ex2(e1.x), ex2(e1.y));
+          sum[j] = add2(sum[j], add2(p0, p1));
+          pb[i][j][0] = transpose8(pack_half(p0.x, p0.y));
+          pb[i][j][1] = transpose8(pack_half(p1.x, p1.y));
         }
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t tile = stage + i * 18 * D;
+        const uint8_t* tile = stage + i * 18 * D;
         const int keys[4] = {ka, kb, ka + 8, kb + 8};
         uint32_t v[4][D / 64], sc[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           if constexpr (D == 128) {
-            const uint2 w = lds64(tile + 8 * D + keys[y] * 64 + g * 8);
+            const uint2 w = *reinterpret_cast<const uint2*>(tile + (y & 1 ? vb_at : va_at) + (y / 2) * 512);
             v[y][0] = w.x;
             v[y][1] = w.y;
-            sc[y] = lds8(tile + 17 * D + keys[y] * 8 + g);
+            sc[y] = tile[(y & 1 ? vsb_at : vsa_at) + (y / 2) * 64];
           } else {
-            v[y][0] = lds32(tile + 8 * D + keys[y] * 32 + g * 4);
-            sc[y] = lds8(tile + 17 * D + keys[y] * 4 + (g >> 1));
+            v[y][0] = *reinterpret_cast<const uint32_t*>(tile + (y & 1 ? vb_at : va_at) + (y / 2) * 256);
+            sc[y] = tile[(y & 1 ? vsb_at : vsa_at) + (y / 2) * 32];
           }
         }
         if (!plain) {
           // what lies in slots past the end may be no number: 0 times it is not 0
 #pragma unroll
           for (int y = 0; y < 4; ++y)
-            if (!((have >> i) & 1) || slot0 + i * 16 + keys[y] >= cons.m) sc[y] = 0;
+            if (!have[i] || slot0 + i * 16 + keys[y] >= cons.m) sc[y] = 0;
         }
         const uint32_t s01 = __byte_perm(sc[0], sc[1], 0x1410) << 7, s23 = __byte_perm(sc[2], sc[3], 0x1410) << 7;
 #pragma unroll
@@ -522,10 +534,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
+        float all = y ? sum[j].y : sum[j].x;
 #pragma unroll
-        for (int x2 = 4; x2 < 32; x2 <<= 1) sum[j][y] += __shfl_xor_sync(0xffffffffu, sum[j][y], x2);
+        for (int x2 = 4; x2 < 32; x2 <<= 1) all += __shfl_xor_sync(0xffffffffu, all, x2);
         const int row = 8 * j + 2 * t + y;
-        if (g == 0) join_ml[warp * S::kRows + row] = make_float2(ref[j][y], sum[j][y]);
+        if (g == 0) join_ml[warp * S::kRows + row] = make_float2(y ? ref[j].y : ref[j].x, all);
         float* dst = join + (warp * S::kRows + row) * S::kPitch + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2)
@@ -537,14 +550,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
     constexpr int kLanes = D / 4;  // threads of a row
     const int c4 = threadIdx.x % kLanes;
     for (int r = threadIdx.x / kLanes; r < S::kRows && row0 + r < rows; r += kThreads / kLanes) {
-      float m = -INFINITY, l = 0.f;
+      float m = kLow, l = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, join_ml[w * S::kRows + r].x);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 ml = join_ml[w * S::kRows + r];
-        const float k = m == -INFINITY ? 1.f : ex2(ml.x - m);
+        const float k = ex2(ml.x - m);
         const float4 x = *reinterpret_cast<const float4*>(join + (w * S::kRows + r) * S::kPitch + 4 * c4);
         l = fmaf(ml.y, k, l);
         o = make_float4(fmaf(x.x, k, o.x), fmaf(x.y, k, o.y), fmaf(x.z, k, o.z), fmaf(x.w, k, o.w));
@@ -560,17 +573,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         if (c4 == 0) p.part_ml[(int64_t)part * S::kRows + r] = make_float2(m, l);
       }
     }
-    if (threadIdx.x == 0 && cons.a == 0 && cons.e < cons.chunks) {
-      Cut c;
-      c.which = first_segment ? 0 : 1;
-      c.token0 = cons.first;
-      c.head0 = head * p.group;
-      c.row0 = row0;
-      c.rows = rows;
-      c.pad[0] = c.pad[1] = 0;
-      const int64_t rest = cons.chunks - cons.e;  // full runs follow until the item's end
-      c.parts = 1 + (int)((rest + each - 1) / each);
-      p.cuts[blockIdx.x] = c;
+    if (threadIdx.x == 0 && cons.a == 0 && (p.by_item || !whole)) {
+      const int rest = cons.chunks - cons.e;  // full runs follow until the item's end
+      Cut c = {whole ? 0 : 1 + (int)((rest + each - 1) / each), part, cons.first, head * p.group, row0, rows, {0, 0}};
+      p.cuts[p.by_item ? ((int64_t)cons.seq * p.c.heads + head) * p.max_tiles + cons.tile : blockIdx.x] = c;
     }
     first_segment = false;
     __syncthreads();  // the join's buffer has been read
@@ -579,57 +585,75 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
   while (in_flight > 0) {
     mbar_wait(&bar[drain], (phases >> drain) & 1);
     phases ^= 1u << drain;
-    drain = drain + 1 == S::kStages ? 0 : drain + 1;
+    drain = (drain + 1) % S::kStages;
     --in_flight;
   }
 }
 
 // ---------------------------------------------------------------- joining cut items
-// A block takes 8 rows of a cut item; four warps a row share its parts.  (One warp a row took 39 us for the 76 parts of a
-// sequence of 131 071 slots and 8 key heads.)
-constexpr int kJoinWays = 4;
-template <int D>
-__global__ void __launch_bounds__(256 * kJoinWays) zl_kv4_join_kernel(const AttnParams p, int32_t tile_rows) {
-  __shared__ float s_o[kJoinWays][8][D];
-  __shared__ float2 s_ml[kJoinWays][8];
+// kSplit: a block a row, its 8 warps share the parts (few items, each cut many times: 76 parts of a sequence of 131 071 slots
+// took one warp a row 39 us); else a block 8 rows, a warp a row.
+template <int D, int kRows, bool kSplit>
+__global__ void __launch_bounds__(256) zl_kv4_join_kernel(const AttnParams p) {
+  constexpr int kPer = D / 32;
+  __shared__ float s_o[8][kSplit ? D : 1];
+  __shared__ float2 s_ml[8];
   let_next_start();
   wait_for_previous();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = kSplit ? blockIdx.y : blockIdx.y * 8 + warp;
   const Cut c = p.cuts[blockIdx.x];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = warp & 7, way = warp >> 3;
-  const int r = blockIdx.y * 8 + row;
-  if (c.parts == 0 || c.row0 + (int)blockIdx.y * 8 >= c.rows) return;
-  const bool there = c.row0 + r < c.rows;
-  auto part = [&](int i) { return (int64_t)(i == 0 ? 2 * blockIdx.x + c.which : 2 * (blockIdx.x + i)) * tile_rows + r; };
-  constexpr int kPer = D / 32;
-  float m = -INFINITY, l = 0.f, o[kPer] = {};
-  if (there) {
-    for (int i = lane; i < c.parts; i += 32) m = fmaxf(m, p.part_ml[part(i)].x);
-    m = warp_max(m);
-#pragma unroll 4
-    for (int i = way; i < c.parts; i += kJoinWays) {
-      const float2 ml = p.part_ml[part(i)];
-      const float k = m == -INFINITY ? 1.f : ex2(ml.x - m);
-      l = fmaf(ml.y, k, l);
-      const float* src = p.part_o + part(i) * D + lane * kPer;
+  if (p.by_item) {  // items without rows were not described
+    const int b = blockIdx.x / (p.c.heads * p.max_tiles);
+    int first;
+    const int n = kv4_new(p.c, p.starts, p.n_tokens, p.max_new, b, &first);
+    if ((int)(blockIdx.x % p.max_tiles) * kRows + r >= n * p.group) return;
+  }
+  if (c.parts == 0 || c.row0 + r >= c.rows) return;
+  const int first_block = c.which >> 1;
+  float m = kLow, l = 0.f, o[kPer] = {};
+  auto add = [&](float m2, float l2, const float (&o2)[kPer]) {
+    const float top = fmaxf(m, m2), k1 = ex2(m - top), k2 = ex2(m2 - top);
+    m = top;
+    l = l * k1 + l2 * k2;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] = o[x] * k1 + o2[x] * k2;
+  };
+  // parts in batches, whose loads are under way together
+  constexpr int kBatch = 8, kStep = kSplit ? 8 : 1;
+  for (int i0 = kSplit ? warp : 0; i0 < c.parts; i0 += kBatch * kStep) {
+    float2 ml[kBatch];
+    float o2[kBatch][kPer];
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int i = min(i0 + y * kStep, c.parts - 1);
+      const int64_t at = (int64_t)(i == 0 ? c.which : 2 * (first_block + i)) * kRows + r;
+      ml[y] = p.part_ml[at];
+      const float* src = p.part_o + at * D + lane * kPer;
       if constexpr (kPer == 4) {
         const float4 v = *reinterpret_cast<const float4*>(src);
-        o[0] = fmaf(v.x, k, o[0]); o[1] = fmaf(v.y, k, o[1]); o[2] = fmaf(v.z, k, o[2]); o[3] = fmaf(v.w, k, o[3]);
+        o2[y][0] = v.x; o2[y][1] = v.y; o2[y][2] = v.z; o2[y][3] = v.w;
       } else {
         const float2 v = *reinterpret_cast<const float2*>(src);
-        o[0] = fmaf(v.x, k, o[0]); o[1] = fmaf(v.y, k, o[1]);
+        o2[y][0] = v.x; o2[y][1] = v.y;
       }
     }
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) s_o[way][row][lane * kPer + x] = o[x];
-    if (lane == 0) s_ml[way][row] = make_float2(m, l);
+    for (int y = 0; y < kBatch; ++y)
+      if (i0 + y * kStep < c.parts) add(ml[y].x, ml[y].y, o2[y]);
   }
-  __syncthreads();
-  if (!there || way != 0) return;
+  if constexpr (kSplit) {
 #pragma unroll
-  for (int w = 1; w < kJoinWays; ++w) {
-    l += s_ml[w][row].y;
+    for (int x = 0; x < kPer; ++x) s_o[warp][lane * kPer + x] = o[x];
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp != 0) return;
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] += s_o[w][row][lane * kPer + x];
+    for (int w = 1; w < 8; ++w) {
+      float o2[kPer];
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) o2[x] = s_o[w][lane * kPer + x];
+      add(s_ml[w].x, s_ml[w].y, o2);
+    }
   }
   const int tok = (c.row0 + r) / p.group;
   const int64_t at = (int64_t)(c.token0 + tok) * p.q_heads + c.head0 + (c.row0 + r - tok * p.group);
@@ -641,33 +665,49 @@ __global__ void __launch_bounds__(256 * kJoinWays) zl_kv4_join_kernel(const Attn
 }
 
 // ---------------------------------------------------------------- accumulated weights
-// weights_out[slot] = decay weights[slot] + sum over rows of 2^(score - lse): a slot's scores lie side by side.
-constexpr int kWeightSlots = 1024;  // slots a block takes
-__global__ void __launch_bounds__(256) zl_kv4_weights_kernel(const AttnParams p) {
+// weights_out[slot] = decay weights[slot] + sum over rows of 2^(score - lse).  A row's scores lie side by side: four slots a
+// thread, eight rows' loads under way at a time.
+constexpr int kWeightThreads = 128;
+constexpr int kWeightSlots = 4 * kWeightThreads;  // slots a block takes
+__global__ void __launch_bounds__(kWeightThreads) zl_kv4_weights_kernel(const AttnParams p) {
   let_next_start();
   wait_for_previous();
   const int b = blockIdx.z, h = blockIdx.y;
-  extern __shared__ float lse2[];  // base-2 LSE of every row; rows that see nothing take no part
+  extern __shared__ float lse2[];  // base-2 LSE of every row; of rows that see nothing +inf: 2^(-inf) each
   const int m = kv4_len(p.c, b);
-  const int s0 = blockIdx.x * kWeightSlots, s1 = min(m, s0 + kWeightSlots);
-  if (s0 >= s1) return;
+  const int s = blockIdx.x * kWeightSlots + 4 * threadIdx.x;
+  if (blockIdx.x * kWeightSlots >= m) return;
   int first = 0;
   const int n = kv4_new(p.c, p.starts, p.n_tokens, p.max_new, b, &first), rows = n * p.group;
-  for (int r = threadIdx.x; r < rows; r += 256) {
+  for (int r = threadIdx.x; r < rows; r += kWeightThreads) {
     const int tok = r / p.group;
-    lse2[r] = p.lse[(int64_t)(first + tok) * p.q_heads + h * p.group + r - tok * p.group] * kLog2e;
+    const float l = p.lse[(int64_t)(first + tok) * p.q_heads + h * p.group + r - tok * p.group];
+    lse2[r] = l == -INFINITY ? INFINITY : l * kLog2e;
   }
   __syncthreads();
-  const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift, base = ((int64_t)b * p.c.heads + h) * slots;
-  for (int s = s0 + threadIdx.x; s < s1; s += 256) {
-    const float* x = p.scores + (base + s) * p.score_rows;
-    float w = p.w_in && s < m - n ? p.decay * p.w_in[base + s] : 0.f;
-    for (int r = 0; r < rows; ++r) {
-      const float l = lse2[r];
-      w += l == -INFINITY ? 0.f : ex2(x[r] - l);
+  if (s >= m) return;
+  const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift, at = ((int64_t)b * p.c.heads + h) * slots + s;
+  const float* x = p.scores + ((int64_t)b * p.c.heads + h) * p.score_rows * slots + s;
+  float w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = p.w_in && s + i < m - n ? p.decay * p.w_in[at + i] : 0.f;
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) v[y] = *reinterpret_cast<const float4*>(x + min(r0 + y, rows - 1) * slots);
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      if (r0 + y >= rows) break;
+      const float l = lse2[r0 + y];
+      w[0] += ex2(v[y].x - l);
+      w[1] += ex2(v[y].y - l);
+      w[2] += ex2(v[y].z - l);
+      w[3] += ex2(v[y].w - l);
     }
-    p.w_out[base + s] = w;
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (s + i < m) p.w_out[at + i] = w[i];
 }
 
 // ---------------------------------------------------------------- host
@@ -686,7 +726,7 @@ Layout layout(const zl_kv4_cache& c, int32_t group, int32_t max_new, bool weight
   l.ml = round16((int64_t)2 * kMaxBlocks * tile * c.head_dim * 4);
   l.cuts = l.ml + round16((int64_t)2 * kMaxBlocks * tile * 8);
   l.scores = l.cuts + round16((int64_t)kMaxBlocks * sizeof(Cut));
-  l.score_rows = (int32_t)((rows + 1) / 2 * 2);
+  l.score_rows = (int32_t)rows;
   l.total = l.scores;
   if (weights) l.total += (int64_t)c.n_seqs * c.n_kv_heads * c.max_pages * c.page * l.score_rows * 4;
   return l;
@@ -700,7 +740,7 @@ zl_status check_heads(const zl_kv4_cache* c, int32_t n_q_heads, int32_t max_new)
 }
 
 template <int D, int NT, bool kScores>
-cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_attn(AttnParams& p, int sms, cudaStream_t stream) {
   using S = Shape<D, NT>;
   const auto kernel = zl_kv4_attn_kernel<D, NT, kScores>;
   static PerDeviceInt resident;
@@ -713,12 +753,17 @@ cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
   });
   if (e != cudaSuccess) return e;
   const int blocks = sms * per_sm < kMaxBlocks ? sms * per_sm : kMaxBlocks;
+  p.max_tiles = (p.max_new * p.group + S::kRows - 1) / S::kRows;
+  const int64_t items = (int64_t)p.c.n_seqs * p.c.heads * p.max_tiles;
+  p.by_item = items <= blocks;
   e = launch_overlapped(kernel, blocks, kThreads, S::kSmem, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(zl_kv4_join_kernel<D>, dim3(blocks, NT), 256 * kJoinWays, 0, stream, p, S::kRows);
+  const unsigned cuts = p.by_item ? (unsigned)items : (unsigned)blocks;
+  if (items * 8 <= blocks) return launch_overlapped(zl_kv4_join_kernel<D, S::kRows, true>, dim3(cuts, S::kRows), 256, 0, stream, p);
+  return launch_overlapped(zl_kv4_join_kernel<D, S::kRows, false>, dim3(cuts, NT), 256, 0, stream, p);
 }
 template <int D, bool kScores>
-cudaError_t launch_attn(const AttnParams& p, int columns, int sms, cudaStream_t stream) {
+cudaError_t launch_attn(AttnParams& p, int columns, int sms, cudaStream_t stream) {
   return columns == 1   ? launch_attn<D, 1, kScores>(p, sms, stream)
          : columns == 2 ? launch_attn<D, 2, kScores>(p, sms, stream)
                         : launch_attn<D, 4, kScores>(p, sms, stream);
@@ -795,7 +840,7 @@ extern "C" zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, i
   if (e == cudaSuccess && weights_out && cache->max_pages > 0) {
     const int64_t slots = (int64_t)cache->max_pages * cache->page;
     e = launch_overlapped(zl_kv4_weights_kernel, dim3((unsigned)((slots + kWeightSlots - 1) / kWeightSlots), cache->n_kv_heads, cache->n_seqs),
-                          256, (size_t)group * max_new * 4, st, p);
+                          kWeightThreads, (size_t)group * max_new * 4, st, p);
   }
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
