@@ -2,23 +2,26 @@
 //
 // Every (sequence, key head) keeps `keep` of its n slots: those with a position above newest - recent first, then
 // the largest weights, ties to the lower slot.  Finding the border is a radix selection over the weights' bits, eight at a
-// time, by one block; survivors behind slot keep and the slots given up before it are then counted in slot order and
-// listed, and a second launch moves the rows, 1.125 d bytes each, over all SMs.  Nothing is sorted and unmoved rows are not
-// touched: a step's eviction moves one row a head.
-// Bound by latency at serving sizes (a few passes over 4 n bytes by one block) and by the weights' and positions' bytes past them.
+// time; survivors behind slot keep and the slots given up before it are then numbered in slot order, and the i-th survivor
+// moves into the i-th slot given up.  Nothing is sorted and unmoved rows are not touched: a step's eviction moves one row a head.
+// Numbering needs one prefix sum: with k(s) slots kept before slot s, a slot given up has number s - k(s), a survivor k(s) - k(keep).
+// A cluster of up to 8 blocks takes a head, each a run of its slots, which it loads once and holds in shared memory; they
+// exchange histograms and counts through each other's shared memory, and one launch does all.
+// Bound by latency at serving sizes (seven exchanges and three trips to memory), by the weights' and positions' bytes past them.
 #include <cuda_runtime.h>
 
 #include "zl_internal.h"
 #include "zl_kv4.cuh"
 #include "zl_overlap.cuh"
+#include "zl_ptx.cuh"
 
 namespace zl {
 namespace {
 
-constexpr int kPickThreads = 1024;
-constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kMoveThreads = 256;
-constexpr int kMoves = 64;  // rows a block of the second launch moves
+constexpr int kEvictThreads = 512;  // at least the bins of the first histogram
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kHeldSlots = 24576;  // that a block's shared memory has room for (8 bytes each)
+constexpr int kCluster = 8;
 
 struct EvictParams {
   Kv4 c;
@@ -26,8 +29,7 @@ struct EvictParams {
   const int32_t* positions;
   float* weights_out;
   int32_t* positions_out;
-  int32_t* counts;  // [sequence][key head]: moves
-  int32_t* moves;   // [sequence][key head][2][capacity]: slots given up, survivors
+  int32_t* moves;  // [sequence][key head][2][capacity]: slots given up, survivors
   int32_t keep, recent, capacity;
 };
 
@@ -38,202 +40,319 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Sum of a number over the block; every thread gets it.
-__device__ __forceinline__ int block_sum(int x, int* warp_sums) {
-  x = __reduce_add_sync(0xffffffffu, x);
-  if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = x;
-  __syncthreads();
-  int all = 0;
-#pragma unroll
-  for (int i = 0; i < kPickWarps; ++i) all += warp_sums[i];
-  __syncthreads();
-  return all;
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the cluster; what each wrote before it, to shared or global memory, the others see after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// An int of the same variable in another block of the cluster.
+__device__ __forceinline__ int peer(const int* mine, uint32_t rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
 }
 
-__global__ void __launch_bounds__(kPickThreads) zl_kv4_pick_kernel(const EvictParams p) {
-  __shared__ int hist[kPickWarps][256];
-  __shared__ int warp_sums[kPickWarps];
+// Exclusive prefix of a number per warp over the block's warps (lane 0's counts); warp_sums is free again after the next sync.
+__device__ __forceinline__ int before_warp(int x, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) warp_sums[warp] = x;
+  __syncthreads();
+  const int x_of = lane < kEvictWarps ? warp_sums[lane] : 0;
+  int run = x_of;
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, run, i);
+    if (lane >= i) run += y;
+  }
+  *total = __shfl_sync(0xffffffffu, run, 31);
+  return __shfl_sync(0xffffffffu, run, warp) - __shfl_sync(0xffffffffu, x_of, warp);
+}
+
+// kHeld: the block's run of slots is kept in shared memory; else (runs past kHeldSlots) it is read again in each pass.
+template <int D, bool kHeld>
+__global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const EvictParams p) {
+  extern __shared__ int held[];  // [2][run]: ranks, positions
+  __shared__ int hist[2][512];   // of two rounds in turn; the first round's: others, then the recent ones
+  __shared__ int local[4][512];  // of a quarter of the warps
+  __shared__ int sum[512];
+  __shared__ int warp_sums[kEvictWarps];
+  __shared__ int pub[4];  // read by the cluster: newest position, kept below `keep`, kept
   __shared__ int s_digit, s_above;
+  const uint32_t cr = cluster_rank(), cn = cluster_size();
+  const int item = blockIdx.x / cn, b = item / p.c.heads, h = item - b * p.c.heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next_start();
   wait_for_previous();
-  const int b = blockIdx.x / p.c.heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t base = (int64_t)blockIdx.x * ((int64_t)p.c.max_pages << p.c.page_shift);
+  const int64_t base = (int64_t)item * ((int64_t)p.c.max_pages << p.c.page_shift);
   const float* w = p.weights + base;
   const int32_t* pos = p.positions + base;
   float* w_out = p.weights_out + base;
   int32_t* pos_out = p.positions_out + base;
   const bool copy_w = p.weights_out != p.weights, copy_pos = p.positions_out != p.positions;
   const int n = kv4_len(p.c, b), keep = p.keep;
+  // this block's run of slots
+  const int run = ((n + (int)cn - 1) / (int)cn + 31) / 32 * 32;
+  const int lo = min(n, (int)cr * run), count = min(n, lo + run) - lo;
   if (n <= keep) {
-    for (int s = threadIdx.x; s < n; s += kPickThreads) {
-      if (copy_w) w_out[s] = w[s];
-      if (copy_pos) pos_out[s] = pos[s];
+    for (int i = tid; i < count; i += kEvictThreads) {
+      if (copy_w) w_out[lo + i] = w[lo + i];
+      if (copy_pos) pos_out[lo + i] = pos[lo + i];
     }
-    if (threadIdx.x == 0) p.counts[blockIdx.x] = 0;
     return;
   }
-  // the newest position, and how many slots lie within `recent` of it
+  uint32_t* held_rank = reinterpret_cast<uint32_t*>(held);
+  int* held_pos = held + run;
+  auto rank_at = [&](int i) { return kHeld ? held_rank[i] : rank_of(w[lo + i]); };
+  auto pos_at = [&](int i) { return kHeld ? held_pos[i] : pos[lo + i]; };
   int newest = INT32_MIN;
-  for (int s = threadIdx.x; s < n; s += kPickThreads) newest = max(newest, pos[s]);
+#pragma unroll 4
+  for (int i = tid; i < count; i += kEvictThreads) {
+    const int at = pos[lo + i];
+    if constexpr (kHeld) {
+      held_rank[i] = rank_of(w[lo + i]);
+      held_pos[i] = at;
+    }
+    newest = max(newest, at);
+  }
   newest = __reduce_max_sync(0xffffffffu, newest);
   if (lane == 0) warp_sums[warp] = newest;
+  for (int i = tid; i < 4 * 512; i += kEvictThreads) (&local[0][0])[i] = 0;
   __syncthreads();
-  newest = __reduce_max_sync(0xffffffffu, warp_sums[lane]);
-  __syncthreads();
+  newest = __reduce_max_sync(0xffffffffu, warp_sums[lane % kEvictWarps]);
+  if (cn > 1) {
+    if (tid == 0) pub[0] = newest;
+    cluster_sync();
+    newest = __reduce_max_sync(0xffffffffu, peer(&pub[0], lane < cn ? lane : 0));
+  }
   const int64_t border = (int64_t)newest - p.recent;
-  int mine = 0;
-  for (int s = threadIdx.x; s < n; s += kPickThreads) mine += pos[s] > border;
-  const int safe = block_sum(mine, warp_sums);
-  // the slots among which the weights decide: the recent ones where they alone are too many, else the others
-  const bool among_recent = safe > keep;
-  int need = among_recent ? keep : keep - safe;
+
   // radix selection: after each round the border's leading digits, and how many of those that share them still count
+  bool among_recent = false;  // the slots among which the weights decide: the recent ones where they alone are too many
+  int need = 0, ties = 0;     // at the end: how many slots of the border's rank stay; how many lie in this block's run
+  int ties_before = 0, ties_all = 0;
   uint32_t prefix = 0, mask = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = lane; i < 256; i += 32) hist[warp][i] = 0;
-    __syncwarp();
-    for (int s = threadIdx.x; s < n; s += kPickThreads) {
-      if ((pos[s] > border) != among_recent) continue;
-      const uint32_t r = rank_of(w[s]);
-      if ((r & mask) == prefix) atomicAdd(&hist[warp][(r >> shift) & 255], 1);
+  for (int round = 0; round < 4; ++round) {
+    const int shift = 24 - 8 * round, bins = round == 0 ? 512 : 256;
+    int* mine = local[warp & 3];
+#pragma unroll 4
+    for (int i = tid; i < count; i += kEvictThreads) {
+      const bool recent = pos_at(i) > border;
+      const uint32_t r = rank_at(i);
+      if (round == 0) atomicAdd(&mine[(r >> 24) + (recent ? 256 : 0)], 1);
+      else if (recent == among_recent && (r & mask) == prefix) atomicAdd(&mine[(r >> shift) & 255], 1);
     }
     __syncthreads();
-    if (threadIdx.x < 256) {
-      int sum = 0;
+    int* mine_all = hist[round & 1];
+    if (tid < bins) {
+      mine_all[tid] = local[0][tid] + local[1][tid] + local[2][tid] + local[3][tid];
 #pragma unroll
-      for (int i = 0; i < kPickWarps; ++i) sum += hist[i][threadIdx.x];
-      hist[0][threadIdx.x] = sum;
+      for (int i = 0; i < 4; ++i) local[i][tid] = 0;
+    }
+    if (cn > 1) cluster_sync();
+    else __syncthreads();
+    if (tid < bins) {
+      int all = 0;
+      if (cn > 1) for (uint32_t i = 0; i < cn; ++i) all += peer(&mine_all[tid], i);
+      else all = mine_all[tid];
+      sum[tid] = all;
     }
     __syncthreads();
+    if (round == 0) {
+      int safe = 0;
+#pragma unroll
+      for (int i = 0; i < 256; i += 32) safe += sum[256 + i + lane];
+      safe = __reduce_add_sync(0xffffffffu, safe);
+      among_recent = safe > keep;
+      need = among_recent ? keep : keep - safe;
+    }
     if (warp == 0) {
       // counts of digits from the top: the digit at which they reach `need`
+      const int* bin = sum + (round == 0 && among_recent ? 256 : 0);
       int above = 0;
       for (int d0 = 224; d0 >= 0; d0 -= 32) {
-        const int x = hist[0][d0 + 31 - lane];  // lane 0 has the largest digit
-        int run = x;
+        const int x = bin[d0 + 31 - lane];  // lane 0 has the largest digit
+        int up = x;
 #pragma unroll
         for (int i = 1; i < 32; i <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, run, i);
-          if (lane >= i) run += y;
+          const int y = __shfl_up_sync(0xffffffffu, up, i);
+          if (lane >= i) up += y;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, above + run >= need);
-        if (hit) {
-          const int first = __ffs(hit) - 1;
-          const int up = __shfl_sync(0xffffffffu, above + run - x, first);
+        const unsigned hit = __ballot_sync(0xffffffffu, above + up >= need);
+        if (hit || d0 == 0) {
+          const int first = hit ? __ffs(hit) - 1 : 31;
+          const int upto = __shfl_sync(0xffffffffu, above + up - x, first);
           if (lane == 0) {
             s_digit = d0 + 31 - first;
-            s_above = up;
+            s_above = upto;
           }
           break;
         }
-        above += __shfl_sync(0xffffffffu, run, 31);
+        above += __shfl_sync(0xffffffffu, up, 31);
       }
     }
     __syncthreads();
     need -= s_above;
     prefix |= (uint32_t)s_digit << shift;
     mask |= 255u << shift;
-    __syncthreads();
+    if (round == 3) {  // the last digit's count is that of the border's rank itself
+      ties_all = sum[s_digit];
+      const int of = lane < cn ? (cn > 1 ? peer(&mine_all[s_digit], lane) : mine_all[s_digit]) : 0;
+      ties_before = __reduce_add_sync(0xffffffffu, lane < cr ? of : 0);
+      ties = __shfl_sync(0xffffffffu, of, cr);
+    }
   }
-  // `need` of the slots at the border stay, the lowest ones.  Warps take contiguous runs of slots.
-  const int run = ((n + kPickWarps - 1) / kPickWarps + 31) / 32 * 32;
-  const int s0 = min(n, warp * run), s1 = min(n, s0 + run);
-  // 0: given up, 1: stays, 2: at the border
-  auto state = [&](int s) {
-    const bool recent = pos[s] > border;
+  // `need` of the slots at the border stay, the lowest ones.  Warps take contiguous parts of the run.
+  const int part = ((count + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
+  const int i0 = min(count, warp * part), i1 = min(count, i0 + part);
+  auto state = [&](int i) {  // 0: given up, 1: stays, 2: at the border
+    if (i >= i1) return 0;
+    const bool recent = pos_at(i) > border;
     if (recent != among_recent) return recent ? 1 : 0;
-    const uint32_t r = rank_of(w[s]);
+    const uint32_t r = rank_at(i);
     return r > prefix ? 1 : r == prefix ? 2 : 0;
   };
-  int ties = 0;
-  for (int s = s0; s < s1; s += 32) ties += __popc(__ballot_sync(0xffffffffu, s + lane < s1 && state(s + lane) == 2));
-  if (lane == 0) warp_sums[warp] = ties;
-  __syncthreads();
-  int ties_before = 0;
-  for (int i = 0; i < warp; ++i) ties_before += warp_sums[i];
-  __syncthreads();
-  auto stays = [&](int s, int& tie) {  // of a warp's 32 slots from s on; tie: ties before them
-    const int st = s + lane < s1 ? state(s + lane) : 0;
+  int tie0 = ties_before;  // ties before this warp's part
+  if (ties > 0 && need < ties_all) {
+    int mine = 0, all;
+    for (int i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, state(i + lane) == 2));
+    __syncthreads();
+    tie0 += before_warp(mine, warp_sums, &all);
+  }
+  auto stays = [&](int i, int& tie) {  // of a warp's 32 slots from i on; tie: ties before them
+    const int st = state(i + lane);
     const unsigned at_border = __ballot_sync(0xffffffffu, st == 2);
-    const bool kept = st == 1 || (st == 2 && tie + __popc(at_border & ((1u << lane) - 1)) < need);
+    const bool kept = st == 1 || (st == 2 && (need == ties_all || tie + __popc(at_border & ((1u << lane) - 1)) < need));
     tie += __popc(at_border);
     return kept;
   };
-  int holes = 0, movers = 0, tie = ties_before;
-  for (int s = s0; s < s1; s += 32) {
-    const bool kept = stays(s, tie), in = s + lane < s1;
-    holes += __popc(__ballot_sync(0xffffffffu, in && !kept && s + lane < keep));
-    movers += __popc(__ballot_sync(0xffffffffu, kept && s + lane >= keep));
-  }
-  if (lane == 0) {
-    hist[0][warp] = holes;
-    hist[1][warp] = movers;
+  int kept_front = 0, kept = 0, tie = tie0;
+  for (int i = i0; i < i1; i += 32) {
+    const unsigned k = __ballot_sync(0xffffffffu, stays(i, tie));
+    kept += __popc(k);
+    const int front = keep - (lo + i);  // of these 32 slots that many lie below `keep`
+    if (front > 0) kept_front += __popc(front >= 32 ? k : k & ((1u << front) - 1));
   }
   __syncthreads();
-  int hole_at = 0, mover_at = 0, total = 0;
-  for (int i = 0; i < kPickWarps; ++i) {
-    if (i < warp) {
-      hole_at += hist[0][i];
-      mover_at += hist[1][i];
+  int front_all, kept_all;
+  before_warp(kept_front, warp_sums, &front_all);
+  __syncthreads();
+  int k = before_warp(kept, warp_sums, &kept_all);  // slots kept before this warp's part
+  if (cn > 1) {
+    if (tid == 0) {
+      pub[1] = front_all;
+      pub[2] = kept_all;
     }
-    total += hist[0][i];
+    cluster_sync();
+    const int f = lane < cn ? peer(&pub[1], lane) : 0, a = lane < cr ? peer(&pub[2], lane) : 0;
+    front_all = __reduce_add_sync(0xffffffffu, f);
+    k += __reduce_add_sync(0xffffffffu, a);
   }
-  int32_t* list = p.moves + (int64_t)blockIdx.x * 2 * p.capacity;
-  tie = ties_before;
-  for (int s = s0; s < s1; s += 32) {
-    const bool kept = stays(s, tie), in = s + lane < s1;
-    const int slot = s + lane;
-    const bool hole = in && !kept && slot < keep, mover = kept && slot >= keep;
-    const unsigned h = __ballot_sync(0xffffffffu, hole), m = __ballot_sync(0xffffffffu, mover);
-    // within the lists whatever happens to the inputs meanwhile
-    const int hole_i = hole_at + __popc(h & ((1u << lane) - 1)), mover_i = mover_at + __popc(m & ((1u << lane) - 1));
-    if (hole && hole_i < p.capacity) list[hole_i] = slot;
-    if (mover && mover_i < p.capacity) list[p.capacity + mover_i] = slot;
-    hole_at += __popc(h);
-    mover_at += __popc(m);
-    if (kept && slot < keep) {
-      if (copy_w) w_out[slot] = w[slot];
-      if (copy_pos) pos_out[slot] = pos[slot];
+  int32_t* holes = p.moves + (int64_t)item * 2 * p.capacity;
+  int32_t* movers = holes + p.capacity;
+  tie = tie0;
+  for (int i = i0; i < i1; i += 32) {
+    const bool kept_here = stays(i, tie);
+    const unsigned all = __ballot_sync(0xffffffffu, kept_here);
+    const int slot = lo + i + lane, before = k + __popc(all & ((1u << lane) - 1));
+    k += __popc(all);
+    if (i + lane < i1) {
+      // within the lists whatever happens to the inputs meanwhile
+      if (!kept_here && slot < keep && slot - before < p.capacity) holes[slot - before] = slot;
+      if (kept_here && slot >= keep && before - front_all < p.capacity) movers[before - front_all] = slot;
+      if (kept_here && slot < keep) {
+        if (copy_w) w_out[slot] = w[slot];
+        if (copy_pos) pos_out[slot] = pos[slot];
+      }
     }
   }
-  if (threadIdx.x == 0) p.counts[blockIdx.x] = min(total, p.capacity);
+  if (cn > 1) cluster_sync();
+  else __syncthreads();
+
+  // 16 lanes a move: codes of keys and values in 16-byte pieces, scales, weight and position; four moves under way
+  constexpr int kAtOnce = 4, kGroups = kEvictThreads / 16;
+  const int moves = min(keep - front_all, p.capacity), l = tid & 15;
+  constexpr int kPieces = D / 32;  // 16-byte pieces of a row's codes
+  for (int i0 = (int)cr * kGroups + tid / 16; i0 < moves; i0 += (int)cn * kGroups * kAtOnce) {
+    int to[kAtOnce], from[kAtOnce];
+    uint4 v[kAtOnce];
+    uint8_t* dst[kAtOnce];
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) {
+      const int i = i0 + y * (int)cn * kGroups;
+      to[y] = from[y] = -1;
+      if (i < moves) {
+        to[y] = holes[i];
+        from[y] = movers[i];
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) {
+      dst[y] = nullptr;
+      if (to[y] < 0) continue;
+      dst[y] = kv4_tile<D>(p.c, b, h, to[y]);
+      const uint8_t* src = kv4_tile<D>(p.c, b, h, from[y]);
+      if (l == 14) v[y].x = __float_as_uint(w[from[y]]);
+      if (l == 15) v[y].x = pos[from[y]];
+      if (!dst[y] || !src) {
+        dst[y] = nullptr;
+        if (l == 0) kv4_report(p.c, ZL_KV4_BAD_PAGE);
+        continue;
+      }
+      const int r0 = to[y] & 15, r1 = from[y] & 15;
+      if (l < 2 * kPieces) {
+        const int at = (l / kPieces) * 8 * D + (l % kPieces) * 16;
+        v[y] = *reinterpret_cast<const uint4*>(src + at + r1 * (D / 2));
+        dst[y] += at + r0 * (D / 2);
+      } else if (l >= 8 && l < 8 + 2 * (D / 64)) {
+        const int at = 16 * D + ((l - 8) / (D / 64)) * D + ((l - 8) % (D / 64)) * 4;
+        v[y].x = *reinterpret_cast<const uint32_t*>(src + at + r1 * (D / 16));
+        dst[y] += at + r0 * (D / 16);
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) {
+      if (to[y] < 0) continue;
+      if (l == 14) w_out[to[y]] = __uint_as_float(v[y].x);
+      if (l == 15) pos_out[to[y]] = v[y].x;
+      if (!dst[y]) continue;
+      if (l < 2 * kPieces) *reinterpret_cast<uint4*>(dst[y]) = v[y];
+      else if (l >= 8 && l < 8 + 2 * (D / 64)) *reinterpret_cast<uint32_t*>(dst[y]) = v[y].x;
+    }
+  }
 }
 
-// 16 lanes a move: codes of keys and values in 16-byte pieces, scales, weight and position.
-template <int D>
-__global__ void __launch_bounds__(kMoveThreads) zl_kv4_move_kernel(const EvictParams p) {
-  let_next_start();
-  wait_for_previous();
-  const int item = blockIdx.y + blockIdx.z * 65535;
-  if (item >= p.c.n_seqs * p.c.heads) return;
-  const int b = item / p.c.heads, h = item - b * p.c.heads;
-  const int count = p.counts[item];
-  const int32_t* list = p.moves + (int64_t)item * 2 * p.capacity;
-  const int64_t base = (int64_t)item * ((int64_t)p.c.max_pages << p.c.page_shift);
-  const int end = min(count, ((int)blockIdx.x + 1) * kMoves);
-  for (int i = blockIdx.x * kMoves + threadIdx.x / 16; i < end; i += kMoveThreads / 16) {
-    const int l = threadIdx.x & 15, to = list[i], from = list[p.capacity + i];
-    if (l == 14) p.weights_out[base + to] = p.weights[base + from];
-    if (l == 15) p.positions_out[base + to] = p.positions[base + from];
-    uint8_t* dst = kv4_tile<D>(p.c, b, h, to);
-    const uint8_t* src = kv4_tile<D>(p.c, b, h, from);
-    if (!dst || !src) {
-      if (l == 0) kv4_report(p.c, ZL_KV4_BAD_PAGE);
-      continue;
-    }
-    constexpr int kPieces = D / 32;  // 16-byte pieces of a row's codes
-    const int r0 = to & 15, r1 = from & 15;
-    if (l < 2 * kPieces) {
-      const int at = (l / kPieces) * 8 * D + (l % kPieces) * 16;
-      *reinterpret_cast<uint4*>(dst + at + r0 * (D / 2)) = *reinterpret_cast<const uint4*>(src + at + r1 * (D / 2));
-    } else if (l >= 8 && l < 8 + 2 * (D / 64)) {
-      const int at = 16 * D + ((l - 8) / (D / 64)) * D + ((l - 8) % (D / 64)) * 4;
-      *reinterpret_cast<uint32_t*>(dst + at + r0 * (D / 16)) = *reinterpret_cast<const uint32_t*>(src + at + r1 * (D / 16));
-    }
-  }
+template <int D, bool kHeld>
+cudaError_t launch_evict(const EvictParams& p, int cluster, int64_t items, int64_t run, cudaStream_t stream) {
+  const auto kernel = zl_kv4_evict_kernel<D, kHeld>;
+  static PerDeviceOnce once;
+  cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld ? kHeldSlots * 8 : 0); });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * cluster));
+  cfg.blockDim = dim3(kEvictThreads);
+  cfg.dynamicSmemBytes = kHeld ? (size_t)run * 8 : 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
-
-int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
 
 }  // namespace
 }  // namespace zl
@@ -247,7 +366,7 @@ extern "C" zl_status zl_kv4_evict_workspace(const zl_kv4_cache* cache, int64_t* 
   if (!bytes) return ZL_ERR_INVALID_ARG;
   const int64_t items = (int64_t)cache->n_seqs * cache->n_kv_heads;
   // moves are no more than half the slots: the slots given up in front are below keep, the survivors past it
-  *bytes = round16(items * 4) + items * 2 * ((int64_t)cache->max_pages * cache->page / 2) * 4;
+  *bytes = items * 2 * ((int64_t)cache->max_pages * cache->page / 2) * 4;
   return ZL_OK;
 }
 
@@ -266,22 +385,26 @@ extern "C" zl_status zl_kv4_evict(const zl_kv4_cache* cache, const float* weight
   int sms = 0;
   if ((s = check_device(&sms)) != ZL_OK) return s;
   const int64_t items = (int64_t)cache->n_seqs * cache->n_kv_heads, slots = (int64_t)cache->max_pages * cache->page;
-  if (items > INT32_MAX) return ZL_ERR_UNSUPPORTED;
+  if (items * kCluster > INT32_MAX) return ZL_ERR_UNSUPPORTED;
   p.weights = weights;
   p.positions = positions;
   p.weights_out = weights_out;
   p.positions_out = positions_out;
-  p.counts = static_cast<int32_t*>(workspace);
-  p.moves = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + round16(items * 4));
+  p.moves = static_cast<int32_t*>(workspace);
   p.keep = keep;
   p.recent = recent;
   p.capacity = (int32_t)(slots / 2);
+  // blocks of a head: enough that a thread has four slots at most, as far as the SMs have room for two blocks each; more
+  // where its slots would not fit their shared memory
+  int cluster = 1;
+  while (cluster < kCluster && ((slots > (int64_t)cluster * 4 * kEvictThreads && items * cluster * 2 <= 2 * sms) ||
+                                slots > (int64_t)cluster * (kHeldSlots - 32)))
+    cluster *= 2;
+  const int64_t run = ((slots + cluster - 1) / cluster + 31) / 32 * 32;
+  const bool held = run <= kHeldSlots;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_overlapped(zl_kv4_pick_kernel, (unsigned)items, kPickThreads, 0, st, p);
-  const int64_t most = slots - keep < keep ? slots - keep : keep;  // moves of an item at most
-  if (e == cudaSuccess && most > 0) {
-    const dim3 grid((unsigned)((most + kMoves - 1) / kMoves), (unsigned)(items < 65535 ? items : 65535), (unsigned)((items + 65534) / 65535));
-    e = launch_overlapped(cache->head_dim == 128 ? zl_kv4_move_kernel<128> : zl_kv4_move_kernel<64>, grid, kMoveThreads, 0, st, p);
-  }
+  cudaError_t e;
+  if (cache->head_dim == 128) e = held ? launch_evict<128, true>(p, cluster, items, run, st) : launch_evict<128, false>(p, cluster, items, run, st);
+  else e = held ? launch_evict<64, true>(p, cluster, items, run, st) : launch_evict<64, false>(p, cluster, items, run, st);
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }

@@ -1,11 +1,13 @@
 // Rows of the 4-bit cache: new keys and values in, all of a sequence's out.
 //
 // In: a block of 16 channels has the scale s nearest to max|x| / 6 (five bits of exponent, three of mantissa) and each
-// channel the code nearest to |x| / s, ties to even.  Every step is exact or correctly rounded: the quotients of bf16 numbers
-// by 6 or by a four-bit s are at least 2^-14 (relative) away from the borders that they do not hit, far more than
-// a division's 2^-24, so the codes are those of exact arithmetic.
+// channel the code nearest to |x| / s, ties to even.  The codes are those of exact arithmetic: quotients of bf16 numbers
+// by 6 or by a four-bit s either hit a border between two codes (scales) or miss it by 2^-12 (relative) and more, so
+// a product with the reciprocal, off by 2^-23 at most, rounded to a multiple of 2^-15 of itself, is on the right side, or on
+// the border, where the conversion's own ties to even decide.  (IEEE divisions took two thirds of the time.)
 // Out: code * s has six bits at most, exact in fp16 and bf16.
-// Both move bytes: a thread takes 8 channels (16 bytes of bf16, 4 of codes), two threads share a scale.
+// Both move bytes: a thread takes 8 channels (16 bytes of bf16, 4 of codes), two threads share a scale, and has several
+// loads under way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -18,7 +20,8 @@ namespace zl {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kWriteTokens = 4;  // tokens a block takes at a time
+constexpr int kWriteTokens = 32;  // tokens a block takes at most: a lane each looks up where one goes
+constexpr int kWriteLoads = 4;    // units of 8 channels that a thread has under way
 
 struct WriteParams {
   Kv4 c;
@@ -28,23 +31,43 @@ struct WriteParams {
   const int32_t* positions;
   int32_t* slot_positions;
   int64_t n_tokens;
+  int32_t per_block;  // tokens of a block
 };
+
+// A product off by 2^-23 at most, to the multiple of 2^-15 (of its power of two) that it is meant to be, if there is one.
+__device__ __forceinline__ float snap(float x) { return __uint_as_float((__float_as_uint(x) + 0x80u) & 0xFFFFFF00u); }
 
 // Bits of the scale of a block whose largest magnitude is amax.
 __device__ __forceinline__ uint32_t scale_bits(float amax) {
-  const float q = __fdiv_rn(amax, 6.f);
+  const float q = snap(amax * (1.f / 6.f));
   if (q < 0x1p-14f) return (uint32_t)__float2int_rn(q * 0x1p17f);  // steps of 2^-17; 8 of them are the first normal number
   const uint32_t b = __float_as_uint(q);
   const uint32_t r = ((b + 0x7FFFFu + ((b >> 20) & 1)) >> 20) - ((127 - 15) << 3);  // three bits of mantissa, ties to even
   return r < 224 ? r : 224;                                                         // 2^13
 }
 
-__device__ __forceinline__ float scale_value(uint32_t bits) { return __half2float(__ushort_as_half((unsigned short)(bits << 7))); }
-
-__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+// Eight numbers' codes; x / s by its reciprocal.
+__device__ __forceinline__ uint32_t encode8(const uint32_t (&w)[4], float inv) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = snap(__uint_as_float(w[i] << 16) * inv);
+    y[2 * i + 1] = snap(__uint_as_float(w[i] & 0xFFFF0000u) * inv);
+  }
   uint32_t o;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tmov.b32 %0, {t, 0, 0, 0};\n\t}" : "=r"(o) : "f"(lo), "f"(hi));
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(o)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return o;
+}
+
+// Largest magnitude of a block of 16, as bf16 bits: this thread's 8 numbers and its neighbour's.
+__device__ __forceinline__ uint32_t block_max(const uint32_t (&w)[4]) {
+  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  m = max(m & 0xFFFFu, m >> 16);
+  return max(m, __shfl_xor_sync(0xffffffffu, m, 1));
 }
 
 template <int D>
@@ -52,83 +75,90 @@ __global__ void __launch_bounds__(kRowThreads) zl_kv4_write_kernel(const WritePa
   __shared__ int s_seq[kWriteTokens], s_slot[kWriteTokens];
   let_next_start();
   wait_for_previous();
-  const int64_t t0 = (int64_t)blockIdx.x * kWriteTokens;
-  if (threadIdx.x < kWriteTokens) {
-    const int64_t t = t0 + threadIdx.x;
-    int seq = -1, slot = -1;
-    if (t < p.n_tokens) {
-      int lo = (int)t;
-      if (p.starts) {  // the last sequence that starts at or before the token
-        int hi = p.c.n_seqs;
-        lo = 0;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) / 2;
-          if (p.starts[mid] <= t) lo = mid;
-          else hi = mid;
-        }
+  const int64_t t0 = (int64_t)blockIdx.x * p.per_block;
+  const int tokens = (int)min((int64_t)p.per_block, p.n_tokens - t0);
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int64_t t = t0 + lane;
+    int b = (int)t0;
+    if (p.starts) {  // the last sequence that starts at or before the block's first token, 32 ways at a time
+      int lo = 0, hi = p.c.n_seqs;
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const int before = __popc(__ballot_sync(0xffffffffu, at < hi && p.starts[min(at, hi - 1)] <= t0));
+        lo += max(0, before - 1) * step;
+        hi = min(hi, lo + step);
       }
+      b = lo;
+    }
+    int seq = -1, slot = -1;
+    if (lane < tokens) {
+      if (!p.starts) b = (int)t;
+      else
+        while (b + 1 < p.c.n_seqs && p.starts[b + 1] <= t) ++b;
       int first = 0;
-      const int n = kv4_new(p.c, p.starts, p.n_tokens, INT32_MAX, lo, &first);
+      const int n = kv4_new(p.c, p.starts, p.n_tokens, INT32_MAX, b, &first);
       if (t >= first && t - first < n) {
-        seq = lo;
-        slot = kv4_len(p.c, lo) - n + (int)(t - first);
+        seq = b;
+        slot = kv4_len(p.c, b) - n + (int)(t - first);
       }
     }
-    s_seq[threadIdx.x] = seq;
-    s_slot[threadIdx.x] = slot;
+    s_seq[lane] = seq;
+    s_slot[lane] = slot;
   }
   __syncthreads();
-  const int per_row = p.c.heads * (D / 8);  // threads of a token's keys or values
-  const int units = kWriteTokens * 2 * per_row;
-  // two threads of a scale are neighbours: per_row is even and 256 is
-#pragma unroll 2
-  for (int base = 0; base < units; base += kRowThreads) {
-    const int u = base + threadIdx.x;
-    const int tok = u / (2 * per_row), rest = u - tok * 2 * per_row;
-    const int which = rest >= per_row, e = rest - which * per_row;
-    const int h = e / (D / 8), c8 = e % (D / 8);
-    const int seq = u < units ? s_seq[tok] : -1, slot = u < units ? s_slot[tok] : -1;
-    const bool there = seq >= 0 && slot >= 0;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    uint8_t* tile = nullptr;
-    if (there) {
-      raw = *reinterpret_cast<const uint4*>((which ? p.x[1] : p.x[0]) + (t0 + tok) * (which ? p.stride[1] : p.stride[0]) + h * D + c8 * 8);
-      tile = kv4_tile<D>(p.c, seq, h, slot);
-      if (!tile) kv4_report(p.c, ZL_KV4_BAD_PAGE);
-    }
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float x[8], amax = 0.f;
+  const int per_row = p.c.heads * (D / 8);  // units of a token's keys or values: 8 channels each
+  const int units = tokens * 2 * per_row;
+  // the two threads of a scale are neighbours: per_row and the block's size are even
+  for (int base = 0; base < units; base += kRowThreads * kWriteLoads) {
+    uint32_t w[kWriteLoads][4];
+    uint8_t* dst[kWriteLoads];  // the row's codes in the cache; null: not there
+    int at_scale[kWriteLoads];  // from there to the scale
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-      amax = fmaxf(amax, fabsf(x[i]));  // of a number and NaN the number
-    }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    if (!tile) continue;
-    const uint32_t sb = scale_bits(amax);
-    const float s = scale_value(sb);
-    uint32_t codes = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float y[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float v = x[2 * i + j];
-        y[j] = v == v && sb ? __fdiv_rn(v, s) : 0.f;
+    for (int y = 0; y < kWriteLoads; ++y) {
+      const int u = base + y * kRowThreads + threadIdx.x;
+      const int tok = u / (2 * per_row), rest = u - tok * 2 * per_row;
+      const int which = rest >= per_row, e = rest - which * per_row;
+      const int h = e / (D / 8), c8 = e % (D / 8);
+      uint4 raw = make_uint4(0, 0, 0, 0);
+      dst[y] = nullptr;
+      at_scale[y] = 0;
+      if (u < units && s_slot[tok] >= 0) {
+        const int slot = s_slot[tok], row = slot & 15;
+        raw = *reinterpret_cast<const uint4*>((which ? p.x[1] : p.x[0]) + (t0 + tok) * (which ? p.stride[1] : p.stride[0]) + h * D + c8 * 8);
+        uint8_t* tile = kv4_tile<D>(p.c, s_seq[tok], h, slot);
+        if (!tile) kv4_report(p.c, ZL_KV4_BAD_PAGE);
+        else dst[y] = tile + which * 8 * D + row * (D / 2) + c8 * 4;
+        at_scale[y] = 16 * D - which * 7 * D - row * (D / 2 - D / 16) - c8 * 4 + c8 / 2;
       }
-      codes |= encode2(y[0], y[1]) << (8 * i);
+      w[y][0] = raw.x; w[y][1] = raw.y; w[y][2] = raw.z; w[y][3] = raw.w;
     }
-    const int row = slot & 15;
-    *reinterpret_cast<uint32_t*>(tile + which * 8 * D + row * (D / 2) + c8 * 4) = codes;
-    if (!(c8 & 1)) tile[16 * D + which * D + row * (D / 16) + c8 / 2] = (uint8_t)sb;
+#pragma unroll
+    for (int y = 0; y < kWriteLoads; ++y) {
+      uint32_t m = block_max(w[y]);
+      if (__any_sync(0xffffffffu, m > 0x7F80u)) {  // NaN is held as 0
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if ((w[y][i] & 0x7FFFu) > 0x7F80u) w[y][i] &= 0xFFFF0000u;
+          if ((w[y][i] & 0x7FFF0000u) > 0x7F800000u) w[y][i] &= 0xFFFFu;
+        }
+        m = block_max(w[y]);
+      }
+      const uint32_t sb = scale_bits(__uint_as_float(m << 16));
+      // scale 0: every channel is 0
+      const float s = __half2float(__ushort_as_half((unsigned short)(sb << 7)));
+      const uint32_t codes = sb ? encode8(w[y], __frcp_rn(s)) : 0;
+      if (dst[y]) {
+        *reinterpret_cast<uint32_t*>(dst[y]) = codes;
+        if (!(threadIdx.x & 1)) dst[y][at_scale[y]] = (uint8_t)sb;
+      }
+    }
   }
   if (p.slot_positions) {
-    for (int u = threadIdx.x; u < kWriteTokens * p.c.heads; u += kRowThreads) {
+    const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift;
+    for (int u = threadIdx.x; u < tokens * p.c.heads; u += kRowThreads) {
       const int tok = u / p.c.heads, h = u % p.c.heads;
-      if (s_seq[tok] >= 0 && s_slot[tok] >= 0) {
-        const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift;
-        p.slot_positions[((int64_t)s_seq[tok] * p.c.heads + h) * slots + s_slot[tok]] = p.positions[t0 + tok];
-      }
+      if (s_slot[tok] >= 0) p.slot_positions[((int64_t)s_seq[tok] * p.c.heads + h) * slots + s_slot[tok]] = p.positions[t0 + tok];
     }
   }
 }
@@ -151,7 +181,8 @@ __device__ __forceinline__ uint32_t to_bf16x2(uint32_t half2_bits) {
   return o;
 }
 
-// A block takes a run of the 16-slot tiles of all sequences, every head of a tile.
+// The 16-slot tiles of all sequences' heads in a row (a tile's heads side by side, as their rows are), dealt out evenly
+// over the blocks; a warp takes one at a time, all its loads under way together.
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) zl_kv4_read_kernel(const ReadParams p) {
   __shared__ int64_t warp_sums[kRowThreads / 32];
@@ -159,63 +190,69 @@ __global__ void __launch_bounds__(kRowThreads) zl_kv4_read_kernel(const ReadPara
   __shared__ int s_seq;
   let_next_start();
   wait_for_previous();
-  // tiles of all sequences in a row, dealt out evenly
   const int n = p.c.n_seqs, per = (n + kRowThreads - 1) / kRowThreads;
   const int b0 = min(n, (int)threadIdx.x * per), b1 = min(n, b0 + per);
   int64_t mine = 0, total;
   for (int b = b0; b < b1; ++b) mine += (kv4_len(p.c, b) + kKv4Slots - 1) / kKv4Slots;
   int64_t before = kv4_scan<kRowThreads>(mine, &total, warp_sums);
-  int64_t at = total * blockIdx.x / gridDim.x;
-  const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
-  if (at >= end) return;
-  if (at >= before && at < before + mine) {
+  const int64_t begin = total * p.c.heads * blockIdx.x / gridDim.x, end = total * p.c.heads * (blockIdx.x + 1) / gridDim.x;
+  if (begin >= end) return;
+  const int64_t begin_tile = begin / p.c.heads;
+  if (begin_tile >= before && begin_tile < before + mine) {
     int b = b0;
     for (;; ++b) {
       const int tiles = (kv4_len(p.c, b) + kKv4Slots - 1) / kKv4Slots;
-      if (at < before + tiles) break;
+      if (begin_tile < before + tiles) break;
       before += tiles;
     }
     s_seq = b;
     s_before = before;
   }
   __syncthreads();
-  int seq = s_seq, tile = (int)(at - s_before), len = kv4_len(p.c, seq);
-  const int units = p.c.heads * kKv4Slots * 2 * (D / 8);
-  for (; at < end; ++at, ++tile) {
-    while (tile * kKv4Slots >= len) {  // the next sequence that holds a slot
+  int seq = s_seq, len = kv4_len(p.c, seq);
+  int64_t seq_begin = s_before * p.c.heads;  // first tile and head of the sequence
+  const int lane = threadIdx.x & 31;
+  for (int64_t at = begin + (threadIdx.x >> 5); at < end; at += kRowThreads / 32) {
+    int64_t seq_size = (int64_t)((len + kKv4Slots - 1) / kKv4Slots) * p.c.heads;
+    while (at - seq_begin >= seq_size) {  // a later sequence
       if (++seq >= n) return;
-      tile = 0;
+      seq_begin += seq_size;
       len = kv4_len(p.c, seq);
+      seq_size = (int64_t)((len + kKv4Slots - 1) / kKv4Slots) * p.c.heads;
     }
+    const int off = (int)(at - seq_begin), tile = off / p.c.heads, h = off - tile * p.c.heads;
     const int64_t row0 = p.row_starts[seq];
+    const uint8_t* src = kv4_tile<D>(p.c, seq, h, tile * kKv4Slots);
     if (row0 < 0 || row0 > p.n_rows - len) {
-      if (threadIdx.x == 0) kv4_report(p.c, ZL_KV4_BAD_STARTS);
+      if (lane == 0) kv4_report(p.c, ZL_KV4_BAD_STARTS);
       continue;
     }
+    if (!src && lane == 0) kv4_report(p.c, ZL_KV4_BAD_PAGE);
     const int rows = min(kKv4Slots, len - tile * kKv4Slots);
-    const uint8_t* src0 = kv4_tile<D>(p.c, seq, 0, tile * kKv4Slots);
-    if (!src0 && threadIdx.x == 0) kv4_report(p.c, ZL_KV4_BAD_PAGE);
-    const int64_t head_step = (int64_t)(18 * D) << (p.c.page_shift - 4);
-    // a warp writes 512 contiguous bytes of a row: threads run over channels, heads, slots, then keys and values
-#pragma unroll 4
-    for (int u = threadIdx.x; u < units; u += kRowThreads) {
-      const int c8 = u % (D / 8), hr = u / (D / 8);
-      const int h = hr % p.c.heads, rw = hr / p.c.heads;
-      const int row = rw & 15, which = rw >> 4;
-      if (row >= rows) continue;
-      uint4 o = make_uint4(0, 0, 0, 0);
-      if (src0) {
-        const uint8_t* src = src0 + h * head_step;
-        const uint32_t codes = *reinterpret_cast<const uint32_t*>(src + which * 8 * D + row * (D / 2) + c8 * 4);
-        const uint32_t sb = src[16 * D + which * D + row * (D / 16) + c8 / 2];
-        const uint32_t s2 = kv4_scale2(sb, sb);
-        uint32_t v[4];
-        kv4_decode(codes, v);
-        o = make_uint4(to_bf16x2(kv4_mul(v[0], s2)), to_bf16x2(kv4_mul(v[1], s2)), to_bf16x2(kv4_mul(v[2], s2)),
-                       to_bf16x2(kv4_mul(v[3], s2)));
+    constexpr int kPerRow = D / 8, kRowsAtOnce = 32 / kPerRow, kLoads = kKv4Slots / kRowsAtOnce;
+    const int c8 = lane % kPerRow, r0 = lane / kPerRow;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      uint32_t codes[kLoads], sb[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int row = r0 + i * kRowsAtOnce;
+        codes[i] = sb[i] = 0;
+        if (src) {  // a tile is there as a whole
+          codes[i] = *reinterpret_cast<const uint32_t*>(src + which * 8 * D + row * (D / 2) + c8 * 4);
+          sb[i] = src[16 * D + which * D + row * (D / 16) + c8 / 2];
+        }
       }
-      __nv_bfloat16* dst = which ? p.out[1] : p.out[0];
-      *reinterpret_cast<uint4*>(dst + (row0 + tile * kKv4Slots + row) * (which ? p.stride[1] : p.stride[0]) + h * D + c8 * 8) = o;
+      __nv_bfloat16* dst = (which ? p.out[1] : p.out[0]) + (row0 + tile * kKv4Slots + r0) * (which ? p.stride[1] : p.stride[0]) + h * D + c8 * 8;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        uint32_t v[4];
+        kv4_decode(codes[i], v);
+        const uint32_t s2 = kv4_scale2(sb[i], sb[i]);
+        const uint4 o = make_uint4(to_bf16x2(kv4_mul(v[0], s2)), to_bf16x2(kv4_mul(v[1], s2)), to_bf16x2(kv4_mul(v[2], s2)),
+                                   to_bf16x2(kv4_mul(v[3], s2)));
+        if (r0 + i * kRowsAtOnce < rows) *reinterpret_cast<uint4*>(dst + i * kRowsAtOnce * (which ? p.stride[1] : p.stride[0])) = o;
+      }
     }
   }
 }
@@ -248,7 +285,10 @@ extern "C" zl_status zl_kv4_write(const zl_kv4_cache* cache, const void* k, int6
   p.positions = positions;
   p.slot_positions = slot_positions;
   p.n_tokens = n_tokens;
-  const unsigned blocks = (unsigned)((n_tokens + kWriteTokens - 1) / kWriteTokens);
+  // as few tokens a block as give every SM four blocks
+  const int64_t even = (n_tokens + 4 * sms - 1) / (4 * sms);
+  p.per_block = (int32_t)(even < kWriteTokens ? even : kWriteTokens);
+  const unsigned blocks = (unsigned)((n_tokens + p.per_block - 1) / p.per_block);
   const auto kernel = cache->head_dim == 128 ? zl_kv4_write_kernel<128> : zl_kv4_write_kernel<64>;
   return launch_overlapped(kernel, blocks, kRowThreads, 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
@@ -282,9 +322,9 @@ extern "C" zl_status zl_kv4_read(const zl_kv4_cache* cache, void* k_out, int64_t
     return r;
   });
   if (e != cudaSuccess) return ZL_ERR_CUDA;
-  // no more blocks than the rows asked for have tiles
-  const int64_t tiles = n_rows / kKv4Slots + cache->n_seqs;
-  const int64_t blocks = (int64_t)sms * per_sm < tiles ? (int64_t)sms * per_sm : tiles;
+  // no more warps than the rows asked for have tiles
+  const int64_t most = ((n_rows / kKv4Slots + cache->n_seqs) * cache->n_kv_heads + kRowThreads / 32 - 1) / (kRowThreads / 32);
+  const int64_t blocks = (int64_t)sms * per_sm < most ? (int64_t)sms * per_sm : most;
   e = launch_overlapped(kernel, (unsigned)blocks, kRowThreads, 0, static_cast<cudaStream_t>(stream), p);
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
