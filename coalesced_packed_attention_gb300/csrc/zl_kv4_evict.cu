@@ -177,39 +177,36 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
       need = among_recent ? keep : keep - safe;
     }
     if (warp == 0) {
-      // counts of digits from the top: the digit at which they reach `need`
-      const int* bin = sum + (round == 0 && among_recent ? 256 : 0);
-      int above = 0;
-      for (int d0 = 224; d0 >= 0; d0 -= 32) {
-        const int x = bin[d0 + 31 - lane];  // lane 0 has the largest digit
-        int up = x;
+      // counts of digits from the top, eight a lane: the digit at which they reach `need`
+      const int* bin = sum + (round == 0 && among_recent ? 256 : 0) + 248 - 8 * lane;
+      int x[8], mine_sum = 0;
 #pragma unroll
-        for (int i = 1; i < 32; i <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, up, i);
-          if (lane >= i) up += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, above + up >= need);
-        if (hit || d0 == 0) {
-          const int first = hit ? __ffs(hit) - 1 : 31;
-          const int upto = __shfl_sync(0xffffffffu, above + up - x, first);
-          if (lane == 0) {
-            s_digit = d0 + 31 - first;
-            s_above = upto;
-          }
-          break;
-        }
-        above += __shfl_sync(0xffffffffu, up, 31);
+      for (int i = 0; i < 8; ++i) mine_sum += x[i] = bin[7 - i];
+      int up = mine_sum;
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, up, i);
+        if (lane >= i) up += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, up >= need);
+      if (lane == (hit ? __ffs(hit) - 1 : 31)) {
+        int above = up - mine_sum, i = 0;
+        while (i < 7 && above + x[i] < need) above += x[i++];
+        s_digit = 255 - 8 * lane - i;
+        s_above = above;
       }
     }
     __syncthreads();
     need -= s_above;
     prefix |= (uint32_t)s_digit << shift;
     mask |= 255u << shift;
-    if (round == 3) {  // the last digit's count is that of the border's rank itself
-      ties_all = sum[s_digit];
-      const int of = lane < cn ? (cn > 1 ? peer(&mine_all[s_digit], lane) : mine_all[s_digit]) : 0;
+    ties_all = sum[s_digit + (round == 0 && among_recent ? 256 : 0)];
+    if (round == 3 || ties_all == need) {  // all that share the digits so far stay, or the digits are the border's rank itself
+      const int* at = &mine_all[s_digit + (round == 0 && among_recent ? 256 : 0)];
+      const int of = lane < cn ? (cn > 1 ? peer(at, lane) : *at) : 0;
       ties_before = __reduce_add_sync(0xffffffffu, lane < cr ? of : 0);
       ties = __shfl_sync(0xffffffffu, of, cr);
+      break;
     }
   }
   // `need` of the slots at the border stay, the lowest ones.  Warps take contiguous parts of the run.
@@ -219,7 +216,7 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
     if (i >= i1) return 0;
     const bool recent = pos_at(i) > border;
     if (recent != among_recent) return recent ? 1 : 0;
-    const uint32_t r = rank_at(i);
+    const uint32_t r = rank_at(i) & mask;
     return r > prefix ? 1 : r == prefix ? 2 : 0;
   };
   int tie0 = ties_before;  // ties before this warp's part

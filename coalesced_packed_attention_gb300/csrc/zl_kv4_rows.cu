@@ -73,6 +73,7 @@ __device__ __forceinline__ uint32_t block_max(const uint32_t (&w)[4]) {
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) zl_kv4_write_kernel(const WriteParams p) {
   __shared__ int s_seq[kWriteTokens], s_slot[kWriteTokens];
+  __shared__ uint8_t* s_tile[kWriteTokens];
   let_next_start();
   wait_for_previous();
   const int64_t t0 = (int64_t)blockIdx.x * p.per_block;
@@ -105,52 +106,53 @@ __global__ void __launch_bounds__(kRowThreads) zl_kv4_write_kernel(const WritePa
     }
     s_seq[lane] = seq;
     s_slot[lane] = slot;
+    s_tile[lane] = slot >= 0 ? kv4_tile<D>(p.c, seq, 0, slot) : nullptr;  // of the first head
+    if (slot >= 0 && !s_tile[lane]) kv4_report(p.c, ZL_KV4_BAD_PAGE);
   }
   __syncthreads();
-  const int per_row = p.c.heads * (D / 8);  // units of a token's keys or values: 8 channels each
-  const int units = tokens * 2 * per_row;
-  // the two threads of a scale are neighbours: per_row and the block's size are even
-  for (int base = 0; base < units; base += kRowThreads * kWriteLoads) {
-    uint32_t w[kWriteLoads][4];
-    uint8_t* dst[kWriteLoads];  // the row's codes in the cache; null: not there
-    int at_scale[kWriteLoads];  // from there to the scale
+  // A thread keeps to one column: 8 channels of a head's key or value; where a token has fewer than the block has threads,
+  // several tokens side by side.  The two threads of a scale are neighbours: columns come by the 16.
+  const int per_row = p.c.heads * (D / 8), columns = 2 * per_row;
+  const int wide = min(columns, kRowThreads), side = kRowThreads / wide;
+  const int head_step = (18 * D) << (p.c.page_shift - 4);
+  for (int c0 = 0; c0 < columns; c0 += wide) {
+    const int c = c0 + threadIdx.x % wide, tok0 = threadIdx.x / wide;
+    const bool mine = c < columns && tok0 < side;
+    const int which = c >= per_row, e = c - which * per_row, h = e / (D / 8), c8 = e % (D / 8);
+    const int64_t stride = which ? p.stride[1] : p.stride[0];
+    const __nv_bfloat16* src = (which ? p.x[1] : p.x[0]) + t0 * stride + h * D + c8 * 8;
+    const int codes_at = h * head_step + which * 8 * D + c8 * 4, scale_at = h * head_step + 16 * D + which * D + c8 / 2;
+    for (int i0 = 0; i0 < tokens; i0 += side * kWriteLoads) {
+      uint32_t w[kWriteLoads][4];
 #pragma unroll
-    for (int y = 0; y < kWriteLoads; ++y) {
-      const int u = base + y * kRowThreads + threadIdx.x;
-      const int tok = u / (2 * per_row), rest = u - tok * 2 * per_row;
-      const int which = rest >= per_row, e = rest - which * per_row;
-      const int h = e / (D / 8), c8 = e % (D / 8);
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      dst[y] = nullptr;
-      at_scale[y] = 0;
-      if (u < units && s_slot[tok] >= 0) {
-        const int slot = s_slot[tok], row = slot & 15;
-        raw = *reinterpret_cast<const uint4*>((which ? p.x[1] : p.x[0]) + (t0 + tok) * (which ? p.stride[1] : p.stride[0]) + h * D + c8 * 8);
-        uint8_t* tile = kv4_tile<D>(p.c, s_seq[tok], h, slot);
-        if (!tile) kv4_report(p.c, ZL_KV4_BAD_PAGE);
-        else dst[y] = tile + which * 8 * D + row * (D / 2) + c8 * 4;
-        at_scale[y] = 16 * D - which * 7 * D - row * (D / 2 - D / 16) - c8 * 4 + c8 / 2;
+      for (int y = 0; y < kWriteLoads; ++y) {
+        const int tok = i0 + y * side + tok0;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (mine && tok < tokens && s_tile[tok]) raw = *reinterpret_cast<const uint4*>(src + tok * stride);
+        w[y][0] = raw.x; w[y][1] = raw.y; w[y][2] = raw.z; w[y][3] = raw.w;
       }
-      w[y][0] = raw.x; w[y][1] = raw.y; w[y][2] = raw.z; w[y][3] = raw.w;
-    }
 #pragma unroll
-    for (int y = 0; y < kWriteLoads; ++y) {
-      uint32_t m = block_max(w[y]);
-      if (__any_sync(0xffffffffu, m > 0x7F80u)) {  // NaN is held as 0
+      for (int y = 0; y < kWriteLoads; ++y) {
+        uint32_t m = block_max(w[y]);
+        if (__any_sync(0xffffffffu, m > 0x7F80u)) {  // NaN is held as 0
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if ((w[y][i] & 0x7FFFu) > 0x7F80u) w[y][i] &= 0xFFFF0000u;
-          if ((w[y][i] & 0x7FFF0000u) > 0x7F800000u) w[y][i] &= 0xFFFFu;
+          for (int i = 0; i < 4; ++i) {
+            if ((w[y][i] & 0x7FFFu) > 0x7F80u) w[y][i] &= 0xFFFF0000u;
+            if ((w[y][i] & 0x7FFF0000u) > 0x7F800000u) w[y][i] &= 0xFFFFu;
+          }
+          m = block_max(w[y]);
         }
-        m = block_max(w[y]);
-      }
-      const uint32_t sb = scale_bits(__uint_as_float(m << 16));
-      // scale 0: every channel is 0
-      const float s = __half2float(__ushort_as_half((unsigned short)(sb << 7)));
-      const uint32_t codes = sb ? encode8(w[y], __frcp_rn(s)) : 0;
-      if (dst[y]) {
-        *reinterpret_cast<uint32_t*>(dst[y]) = codes;
-        if (!(threadIdx.x & 1)) dst[y][at_scale[y]] = (uint8_t)sb;
+        const uint32_t sb = scale_bits(__uint_as_float(m << 16));
+        // scale 0: every channel is 0
+        const float s = __half2float(__ushort_as_half((unsigned short)(sb << 7)));
+        const uint32_t codes = sb ? encode8(w[y], __frcp_rn(s)) : 0;
+        const int tok = i0 + y * side + tok0;
+        if (mine && tok < tokens && s_tile[tok]) {
+          uint8_t* tile = s_tile[tok];
+          const int row = s_slot[tok] & 15;
+          *reinterpret_cast<uint32_t*>(tile + codes_at + row * (D / 2)) = codes;
+          if (!(c8 & 1)) tile[scale_at + row * (D / 16)] = (uint8_t)sb;
+        }
       }
     }
   }
