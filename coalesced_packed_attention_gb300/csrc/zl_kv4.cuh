@@ -69,14 +69,18 @@ __device__ __forceinline__ int kv4_new(const Kv4& c, const int32_t* starts, int6
   kv4_report(c, ZL_KV4_BAD_STARTS);
   return 0;
 }
-// Tile of a slot, or null where its page is none of the cache's.
+// Number of a slot's tile in `data` (they are less than 2^32), or kKv4None where its page is none of the cache's.
+constexpr uint32_t kKv4None = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t kv4_place(const Kv4& c, int b, int h, int slot) {
+  const uint32_t page = c.pages[(int64_t)b * c.max_pages + (slot >> c.page_shift)];
+  const int shift = c.page_shift - 4;
+  return page < (uint32_t)c.n_pages ? ((page * c.heads + h) << shift) + ((slot >> 4) & ((1 << shift) - 1)) : kKv4None;
+}
+// The tile itself, or null.
 template <int D>
 __device__ __forceinline__ uint8_t* kv4_tile(const Kv4& c, int b, int h, int slot) {
-  const int page = c.pages[(int64_t)b * c.max_pages + (slot >> c.page_shift)];
-  if (page < 0 || page >= c.n_pages) return nullptr;
-  const int tiles_shift = c.page_shift - 4;
-  const int64_t tile = (((int64_t)page * c.heads + h) << tiles_shift) + ((slot >> 4) & ((1 << tiles_shift) - 1));
-  return c.data + tile * (18 * D);
+  const uint32_t place = kv4_place(c, b, h, slot);
+  return place == kKv4None ? nullptr : c.data + (uint64_t)place * (18 * D);
 }
 
 // Four codes of two channels each -> four pairs of fp16.

@@ -37,7 +37,6 @@ constexpr int kUnit = 32;          // slots of a unit: two tiles
 constexpr int kMaxBlocks = 640;    // blocks of a launch at most: what the workspace has room for
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kTwice = 0x00800080u;  // a scale's bits times this: the scale in both halves, by the multiplier, which has time
-constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr float kLow = -1e30f;     // the running maximum of rows that have seen nothing
 constexpr float kRescale = 8.f;    // the maximum may lag by 2^8 before the sums are rescaled
 
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
   // Loading: a warp looks up the places of its next 32 units at once, one a lane, and issues them one by one.
   Walk<NT> prod = cons;
   int prod_x = prod.a + warp;         // the next unit to look up
-  uint32_t tile0 = kNone, tile1 = kNone;  // the two tiles of a lane's unit
+  uint32_t tile0 = kKv4None, tile1 = kKv4None;  // the two tiles of a lane's unit
   int batch = 0, batch_end = 0;       // units looked up and not yet issued: lanes [batch, batch_end)
   bool any_bad = false;               // a page of this run is none of the cache's
   auto look_up = [&]() {
@@ -237,17 +236,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
       if (prod.done()) return;
       prod_x = prod.a + warp;
     }
-    const int x = prod_x + kWarps * lane, slot = x * kUnit, shift = p.c.page_shift - 4;
-    const int32_t* table = p.c.pages + (int64_t)prod.seq * p.c.max_pages;
+    const int x = prod_x + kWarps * lane, slot = x * kUnit;
     bool bad = false;
-    auto place = [&](int at) {  // tiles of the cache number less than 2^32
-      if (x >= prod.e || at >= prod.m) return kNone;
-      const uint32_t page = table[at >> p.c.page_shift];
-      if (page >= (uint32_t)p.c.n_pages) {
-        bad = true;
-        return kNone;
-      }
-      return ((page * p.c.heads + prod.head) << shift) + ((at >> 4) & ((1 << shift) - 1));
+    auto place = [&](int at) {
+      if (x >= prod.e || at >= prod.m) return kKv4None;
+      const uint32_t tile = kv4_place(p.c, prod.seq, prod.head, at);
+      bad |= tile == kKv4None;
+      return tile;
     };
     tile0 = place(slot);
     tile1 = place(slot + kKv4Slots);
@@ -269,13 +264,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
     ++batch;
     if (lane == 0) {
       const uint32_t dst = smem_u32(ring + fill * S::kStageBytes), b = smem_u32(&bar[fill]);
-      if (t0 != kNone && t1 == t0 + 1) {
+      if (t0 != kKv4None && t1 == t0 + 1) {
         mbar_arrive_expect_tx(&bar[fill], 36 * D);
         bulk_load(dst, p.c.data + (uint64_t)t0 * (18 * D), 36 * D, b);
       } else {
-        mbar_arrive_expect_tx(&bar[fill], (t0 != kNone ? 18 * D : 0) + (t1 != kNone ? 18 * D : 0));
-        if (t0 != kNone) bulk_load(dst, p.c.data + (uint64_t)t0 * (18 * D), 18 * D, b);
-        if (t1 != kNone) bulk_load(dst + 18 * D, p.c.data + (uint64_t)t1 * (18 * D), 18 * D, b);
+        mbar_arrive_expect_tx(&bar[fill], (t0 != kKv4None ? 18 * D : 0) + (t1 != kKv4None ? 18 * D : 0));
+        if (t0 != kKv4None) bulk_load(dst, p.c.data + (uint64_t)t0 * (18 * D), 18 * D, b);
+        if (t1 != kKv4None) bulk_load(dst + 18 * D, p.c.data + (uint64_t)t1 * (18 * D), 18 * D, b);
       }
     }
     fill = (fill + 1) % S::kStages;
@@ -365,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int at = slot0 + i * kKv4Slots;
-          have[i] = at < cons.m && (uint32_t)p.c.pages[(int64_t)cons.seq * p.c.max_pages + (at >> p.c.page_shift)] < (uint32_t)p.c.n_pages;
+          have[i] = at < cons.m && kv4_place(p.c, cons.seq, 0, at) != kKv4None;
         }
       float s[2][NT][4];
 #pragma unroll

@@ -6,7 +6,8 @@
 // moves into the i-th slot given up.  Nothing is sorted and unmoved rows are not touched: a step's eviction moves one row a head.
 // Numbering needs one prefix sum: with k(s) slots kept before slot s, a slot given up has number s - k(s), a survivor k(s) - k(keep).
 // A cluster of up to 8 blocks takes a head, each a run of its slots, which it loads once and holds in shared memory; they
-// exchange histograms and counts through each other's shared memory, and one launch does all.
+// exchange histograms and counts through each other's shared memory.  A head's blocks also make its moves where they are few;
+// many are made by a second launch over all SMs.
 // Bound by latency at serving sizes (seven exchanges and three trips to memory), by the weights' and positions' bytes past them.
 #include <cuda_runtime.h>
 
@@ -22,6 +23,9 @@ constexpr int kEvictThreads = 512;  // at least the bins of the first histogram
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kHeldSlots = 24576;  // that a block's shared memory has room for (8 bytes each)
 constexpr int kCluster = 8;
+constexpr int kMoveThreads = 256;
+constexpr int kMoves = 128;        // moves that a block of the second launch makes
+constexpr int kMovesApart = 256;   // moves a head from which on a second launch makes them
 
 struct EvictParams {
   Kv4 c;
@@ -29,7 +33,8 @@ struct EvictParams {
   const int32_t* positions;
   float* weights_out;
   int32_t* positions_out;
-  int32_t* moves;  // [sequence][key head][2][capacity]: slots given up, survivors
+  int32_t* counts;  // [sequence][key head]: moves, where a launch of their own makes them (else null)
+  int2* moves;      // [sequence][key head][2][capacity]: slots given up, survivors: slot and tile
   int32_t keep, recent, capacity;
 };
 
@@ -79,6 +84,48 @@ __device__ __forceinline__ int before_warp(int x, int* warp_sums, int* total) {
   return __shfl_sync(0xffffffffu, run, warp) - __shfl_sync(0xffffffffu, x_of, warp);
 }
 
+// Moves i, i + step, .. of a head, kAtOnce of them, below `end`: 16 lanes a move, codes of keys and values in 16-byte pieces,
+// scales, weight and position.  A lane's piece is found by a pointer rather than by branches, so that all loads are under way
+// together (a register that two branches load into is waited for between them: 14 us instead of 5 for 1790 rows of each of 4 heads).
+template <int D, int kAtOnce>
+__device__ __forceinline__ void move_rows(const EvictParams& p, int item, int i, int step, int end) {
+  const int l = threadIdx.x & 15;
+  const int64_t base = (int64_t)item * ((int64_t)p.c.max_pages << p.c.page_shift);
+  const int2* holes = p.moves + (int64_t)item * 2 * p.capacity;
+  constexpr int kPieces = D / 32;  // of a row's codes
+  const bool code = l < 2 * kPieces, scale = l >= 8 && l < 8 + 2 * (D / 64), number = l >= 14;
+  // where a lane's piece of row 0 lies in a tile, and of the next row
+  const int at = code ? (l / kPieces) * 8 * D + (l % kPieces) * 16 : 16 * D + ((l - 8) / (D / 64)) * D + ((l - 8) % (D / 64)) * 4;
+  const int pitch = code ? D / 2 : D / 16;
+  const uint8_t* in = reinterpret_cast<const uint8_t*>(l == 14 ? static_cast<const void*>(p.weights + base) : p.positions + base);
+  uint8_t* out = reinterpret_cast<uint8_t*>(l == 14 ? static_cast<void*>(p.weights_out + base) : p.positions_out + base);
+  int2 to[kAtOnce], from[kAtOnce];
+#pragma unroll
+  for (int y = 0; y < kAtOnce; ++y) {
+    const int j = min(i + y * step, end - 1);
+    to[y] = holes[j];
+    from[y] = holes[p.capacity + j];
+  }
+  uint4 v[kAtOnce];
+  uint32_t u[kAtOnce];
+  bool does[kAtOnce];
+#pragma unroll
+  for (int y = 0; y < kAtOnce; ++y) {
+    const bool bad = (uint32_t)to[y].y == kKv4None || (uint32_t)from[y].y == kKv4None;
+    does[y] = i + y * step < end && (number || ((code || scale) && !bad));
+    if (bad && l == 0 && i + y * step < end) kv4_report(p.c, ZL_KV4_BAD_PAGE);
+    const uint8_t* src = number ? in + (int64_t)from[y].x * 4 : p.c.data + (uint64_t)(uint32_t)from[y].y * (18 * D) + at + (from[y].x & 15) * pitch;
+    if (does[y] && code) v[y] = *reinterpret_cast<const uint4*>(src);
+    if (does[y] && !code) u[y] = *reinterpret_cast<const uint32_t*>(src);
+  }
+#pragma unroll
+  for (int y = 0; y < kAtOnce; ++y) {
+    uint8_t* dst = number ? out + (int64_t)to[y].x * 4 : p.c.data + (uint64_t)(uint32_t)to[y].y * (18 * D) + at + (to[y].x & 15) * pitch;
+    if (does[y] && code) *reinterpret_cast<uint4*>(dst) = v[y];
+    if (does[y] && !code) *reinterpret_cast<uint32_t*>(dst) = u[y];
+  }
+}
+
 // kHeld: the block's run of slots is kept in shared memory; else (runs past kHeldSlots) it is read again in each pass.
 template <int D, bool kHeld>
 __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const EvictParams p) {
@@ -109,6 +156,7 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
       if (copy_w) w_out[lo + i] = w[lo + i];
       if (copy_pos) pos_out[lo + i] = pos[lo + i];
     }
+    if (p.counts && cr == 0 && tid == 0) p.counts[item] = 0;
     return;
   }
   uint32_t* held_rank = reinterpret_cast<uint32_t*>(held);
@@ -255,8 +303,8 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
     front_all = __reduce_add_sync(0xffffffffu, f);
     k += __reduce_add_sync(0xffffffffu, a);
   }
-  int32_t* holes = p.moves + (int64_t)item * 2 * p.capacity;
-  int32_t* movers = holes + p.capacity;
+  int2* holes = p.moves + (int64_t)item * 2 * p.capacity;
+  int2* movers = holes + p.capacity;
   tie = tie0;
   for (int i = i0; i < i1; i += 32) {
     const bool kept_here = stays(i, tie);
@@ -265,68 +313,35 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
     k += __popc(all);
     if (i + lane < i1) {
       // within the lists whatever happens to the inputs meanwhile
-      if (!kept_here && slot < keep && slot - before < p.capacity) holes[slot - before] = slot;
-      if (kept_here && slot >= keep && before - front_all < p.capacity) movers[before - front_all] = slot;
+      if (!kept_here && slot < keep && slot - before < p.capacity) holes[slot - before] = make_int2(slot, kv4_place(p.c, b, h, slot));
+      if (kept_here && slot >= keep && before - front_all < p.capacity) movers[before - front_all] = make_int2(slot, kv4_place(p.c, b, h, slot));
       if (kept_here && slot < keep) {
         if (copy_w) w_out[slot] = w[slot];
         if (copy_pos) pos_out[slot] = pos[slot];
       }
     }
   }
+  const int moves = min(keep - front_all, p.capacity);
+  if (p.counts) {
+    if (cn > 1) cluster_sync();  // no block may end while another reads its shared memory
+    if (cr == 0 && tid == 0) p.counts[item] = moves;
+    return;
+  }
   if (cn > 1) cluster_sync();
   else __syncthreads();
+  constexpr int kGroups = kEvictThreads / 16;
+  for (int i = (int)cr * kGroups; i < moves; i += (int)cn * kGroups) move_rows<D, 1>(p, item, i + tid / 16, kGroups, min(moves, i + kGroups));
+}
 
-  // 16 lanes a move: codes of keys and values in 16-byte pieces, scales, weight and position; four moves under way
-  constexpr int kAtOnce = 4, kGroups = kEvictThreads / 16;
-  const int moves = min(keep - front_all, p.capacity), l = tid & 15;
-  constexpr int kPieces = D / 32;  // 16-byte pieces of a row's codes
-  for (int i0 = (int)cr * kGroups + tid / 16; i0 < moves; i0 += (int)cn * kGroups * kAtOnce) {
-    int to[kAtOnce], from[kAtOnce];
-    uint4 v[kAtOnce];
-    uint8_t* dst[kAtOnce];
-#pragma unroll
-    for (int y = 0; y < kAtOnce; ++y) {
-      const int i = i0 + y * (int)cn * kGroups;
-      to[y] = from[y] = -1;
-      if (i < moves) {
-        to[y] = holes[i];
-        from[y] = movers[i];
-      }
-    }
-#pragma unroll
-    for (int y = 0; y < kAtOnce; ++y) {
-      dst[y] = nullptr;
-      if (to[y] < 0) continue;
-      dst[y] = kv4_tile<D>(p.c, b, h, to[y]);
-      const uint8_t* src = kv4_tile<D>(p.c, b, h, from[y]);
-      if (l == 14) v[y].x = __float_as_uint(w[from[y]]);
-      if (l == 15) v[y].x = pos[from[y]];
-      if (!dst[y] || !src) {
-        dst[y] = nullptr;
-        if (l == 0) kv4_report(p.c, ZL_KV4_BAD_PAGE);
-        continue;
-      }
-      const int r0 = to[y] & 15, r1 = from[y] & 15;
-      if (l < 2 * kPieces) {
-        const int at = (l / kPieces) * 8 * D + (l % kPieces) * 16;
-        v[y] = *reinterpret_cast<const uint4*>(src + at + r1 * (D / 2));
-        dst[y] += at + r0 * (D / 2);
-      } else if (l >= 8 && l < 8 + 2 * (D / 64)) {
-        const int at = 16 * D + ((l - 8) / (D / 64)) * D + ((l - 8) % (D / 64)) * 4;
-        v[y].x = *reinterpret_cast<const uint32_t*>(src + at + r1 * (D / 16));
-        dst[y] += at + r0 * (D / 16);
-      }
-    }
-#pragma unroll
-    for (int y = 0; y < kAtOnce; ++y) {
-      if (to[y] < 0) continue;
-      if (l == 14) w_out[to[y]] = __uint_as_float(v[y].x);
-      if (l == 15) pos_out[to[y]] = v[y].x;
-      if (!dst[y]) continue;
-      if (l < 2 * kPieces) *reinterpret_cast<uint4*>(dst[y]) = v[y];
-      else if (l >= 8 && l < 8 + 2 * (D / 64)) *reinterpret_cast<uint32_t*>(dst[y]) = v[y].x;
-    }
-  }
+// kMoves of a head a block.
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) zl_kv4_move_kernel(const EvictParams p) {
+  let_next_start();
+  wait_for_previous();
+  const int item = blockIdx.y + blockIdx.z * 65535;
+  if (item >= p.c.n_seqs * p.c.heads) return;
+  const int first = blockIdx.x * kMoves, moves = p.counts[item];
+  if (first < moves) move_rows<D, kMoves * 16 / kMoveThreads>(p, item, first + threadIdx.x / 16, kMoveThreads / 16, min(moves, first + kMoves));
 }
 
 template <int D, bool kHeld>
@@ -351,6 +366,8 @@ cudaError_t launch_evict(const EvictParams& p, int cluster, int64_t items, int64
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+
 }  // namespace
 }  // namespace zl
 
@@ -363,7 +380,7 @@ extern "C" zl_status zl_kv4_evict_workspace(const zl_kv4_cache* cache, int64_t* 
   if (!bytes) return ZL_ERR_INVALID_ARG;
   const int64_t items = (int64_t)cache->n_seqs * cache->n_kv_heads;
   // moves are no more than half the slots: the slots given up in front are below keep, the survivors past it
-  *bytes = items * 2 * ((int64_t)cache->max_pages * cache->page / 2) * 4;
+  *bytes = round16(items * 4) + items * 2 * ((int64_t)cache->max_pages * cache->page / 2) * 8;
   return ZL_OK;
 }
 
@@ -387,7 +404,10 @@ extern "C" zl_status zl_kv4_evict(const zl_kv4_cache* cache, const float* weight
   p.positions = positions;
   p.weights_out = weights_out;
   p.positions_out = positions_out;
-  p.moves = static_cast<int32_t*>(workspace);
+  p.moves = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + round16(items * 4));
+  const int64_t most = slots - keep < keep ? slots - keep : keep;  // moves of a head at most
+  const bool apart = most > kMovesApart;
+  p.counts = apart ? static_cast<int32_t*>(workspace) : nullptr;
   p.keep = keep;
   p.recent = recent;
   p.capacity = (int32_t)(slots / 2);
@@ -403,5 +423,9 @@ extern "C" zl_status zl_kv4_evict(const zl_kv4_cache* cache, const float* weight
   cudaError_t e;
   if (cache->head_dim == 128) e = held ? launch_evict<128, true>(p, cluster, items, run, st) : launch_evict<128, false>(p, cluster, items, run, st);
   else e = held ? launch_evict<64, true>(p, cluster, items, run, st) : launch_evict<64, false>(p, cluster, items, run, st);
+  if (e == cudaSuccess && apart) {
+    const dim3 grid((unsigned)((most + kMoves - 1) / kMoves), (unsigned)(items < 65535 ? items : 65535), (unsigned)((items + 65534) / 65535));
+    e = launch_overlapped(cache->head_dim == 128 ? zl_kv4_move_kernel<128> : zl_kv4_move_kernel<64>, grid, kMoveThreads, 0, st, p);
+  }
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
