@@ -2,8 +2,8 @@
 //
 // In: a block of 16 channels has the scale s nearest to max|x| / 6 (five bits of exponent, three of mantissa) and each
 // channel the code nearest to |x| / s, ties to even.  The codes are those of exact arithmetic: quotients of bf16 numbers
-// by 6 or by a four-bit s either hit a border between two codes (scales) or miss it by 2^-12 (relative) and more, so
-// a product with the reciprocal, off by 2^-23 at most, rounded to a multiple of 2^-15 of itself, is on the right side, or on
+// by 6 or by a four-bit s either hit a border between two codes (scales) or miss it by 2^-11 and more, so
+// a product with the reciprocal, off by 2^-20 at most, rounded to a multiple of 2^-16, is on the right side, or on
 // the border, where the conversion's own ties to even decide.  (IEEE divisions took two thirds of the time.)
 // Out: code * s has six bits at most, exact in fp16 and bf16.
 // Both move bytes: a thread takes 8 channels (16 bytes of bf16, 4 of codes), two threads share a scale, and has several
@@ -15,6 +15,7 @@
 #include "zl_internal.h"
 #include "zl_kv4.cuh"
 #include "zl_overlap.cuh"
+#include "zl_ptx.cuh"
 
 namespace zl {
 namespace {
@@ -34,46 +35,55 @@ struct WriteParams {
   int32_t per_block;  // tokens of a block
 };
 
-// A product off by 2^-23 at most, to the multiple of 2^-15 (of its power of two) that it is meant to be, if there is one.
-__device__ __forceinline__ float snap(float x) { return __uint_as_float((__float_as_uint(x) + 0x80u) & 0xFFFFFF00u); }
-
 // Bits of the scale of a block whose largest magnitude is amax.
 __device__ __forceinline__ uint32_t scale_bits(float amax) {
-  const float q = snap(amax * (1.f / 6.f));
+  // a sixth, to the multiple of 2^-15 of its power of two that it is meant to be, if there is one
+  const uint32_t b = (__float_as_uint(amax * (1.f / 6.f)) + 0x80u) & 0xFFFFFF00u;
+  const float q = __uint_as_float(b);
   if (q < 0x1p-14f) return (uint32_t)__float2int_rn(q * 0x1p17f);  // steps of 2^-17; 8 of them are the first normal number
-  const uint32_t b = __float_as_uint(q);
   const uint32_t r = ((b + 0x7FFFFu + ((b >> 20) & 1)) >> 20) - ((127 - 15) << 3);  // three bits of mantissa, ties to even
   return r < 224 ? r : 224;                                                         // 2^13
 }
 
-// Eight numbers' codes; x / s by its reciprocal.
+// Eight numbers' codes; inv: 1 / s, to an ulp or two.
 __device__ __forceinline__ uint32_t encode8(const uint32_t (&w)[4], float inv) {
-  float y[8];
+  // at 192 numbers are 2^-16 apart
+  const float2 inv2 = make_float2(inv, inv), up = make_float2(192.f, 192.f), down = make_float2(-192.f, -192.f);
+  float2 y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y[2 * i] = snap(__uint_as_float(w[i] << 16) * inv);
-    y[2 * i + 1] = snap(__uint_as_float(w[i] & 0xFFFF0000u) * inv);
-  }
+  for (int i = 0; i < 4; ++i)
+    y[i] = add2(fma2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), inv2, up), down);
   uint32_t o;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(o)
-      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+      : "f"(y[0].x), "f"(y[0].y), "f"(y[1].x), "f"(y[1].y), "f"(y[2].x), "f"(y[2].y), "f"(y[3].x), "f"(y[3].y));
   return o;
 }
 
-// Largest magnitude of a block of 16, as bf16 bits: this thread's 8 numbers and its neighbour's.
+// Largest magnitudes of a block of 16, as bf16 bits: this thread's 8 numbers and its neighbour's; above 0x7F80 where one is NaN.
+__device__ __forceinline__ uint32_t abs_max(uint32_t a, uint32_t b) {
+  uint32_t o;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+  return o;
+}
 __device__ __forceinline__ uint32_t block_max(const uint32_t (&w)[4]) {
-  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-  m = max(m & 0xFFFFu, m >> 16);
+  uint32_t m = abs_max(abs_max(w[0], w[1]), abs_max(w[2], w[3]));
+  m = abs_max(m, m >> 16) & 0x7FFFu;
   return max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) zl_kv4_write_kernel(const WriteParams p) {
   __shared__ int s_seq[kWriteTokens], s_slot[kWriteTokens];
-  __shared__ uint8_t* s_tile[kWriteTokens];
+  __shared__ uint8_t* s_codes[kWriteTokens];  // the token's row in its tile of the first head: codes and scales, or null
+  __shared__ uint8_t* s_scales[kWriteTokens];
   let_next_start();
   wait_for_previous();
   const int64_t t0 = (int64_t)blockIdx.x * p.per_block;
@@ -106,8 +116,10 @@ __global__ void __launch_bounds__(kRowThreads) zl_kv4_write_kernel(const WritePa
     }
     s_seq[lane] = seq;
     s_slot[lane] = slot;
-    s_tile[lane] = slot >= 0 ? kv4_tile<D>(p.c, seq, 0, slot) : nullptr;  // of the first head
-    if (slot >= 0 && !s_tile[lane]) kv4_report(p.c, ZL_KV4_BAD_PAGE);
+    uint8_t* tile = slot >= 0 ? kv4_tile<D>(p.c, seq, 0, slot) : nullptr;
+    if (slot >= 0 && !tile) kv4_report(p.c, ZL_KV4_BAD_PAGE);
+    s_codes[lane] = tile ? tile + (slot & 15) * (D / 2) : nullptr;
+    s_scales[lane] = tile + 16 * D + (slot & 15) * (D / 16);
   }
   __syncthreads();
   // A thread keeps to one column: 8 channels of a head's key or value; where a token has fewer than the block has threads,
@@ -121,37 +133,39 @@ __global__ void __launch_bounds__(kRowThreads) zl_kv4_write_kernel(const WritePa
     const int which = c >= per_row, e = c - which * per_row, h = e / (D / 8), c8 = e % (D / 8);
     const int64_t stride = which ? p.stride[1] : p.stride[0];
     const __nv_bfloat16* src = (which ? p.x[1] : p.x[0]) + t0 * stride + h * D + c8 * 8;
-    const int codes_at = h * head_step + which * 8 * D + c8 * 4, scale_at = h * head_step + 16 * D + which * D + c8 / 2;
+    const int codes_at = h * head_step + which * 8 * D + c8 * 4, scale_at = h * head_step + which * D + c8 / 2;
     for (int i0 = 0; i0 < tokens; i0 += side * kWriteLoads) {
       uint32_t w[kWriteLoads][4];
+      uint8_t* codes[kWriteLoads];
 #pragma unroll
       for (int y = 0; y < kWriteLoads; ++y) {
         const int tok = i0 + y * side + tok0;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (mine && tok < tokens && s_tile[tok]) raw = *reinterpret_cast<const uint4*>(src + tok * stride);
+        codes[y] = mine && tok < tokens ? s_codes[tok] : nullptr;
+        const uint4 raw = codes[y] ? *reinterpret_cast<const uint4*>(src + tok * stride) : make_uint4(0, 0, 0, 0);
         w[y][0] = raw.x; w[y][1] = raw.y; w[y][2] = raw.z; w[y][3] = raw.w;
       }
+      uint32_t m[kWriteLoads], most = 0;
 #pragma unroll
-      for (int y = 0; y < kWriteLoads; ++y) {
-        uint32_t m = block_max(w[y]);
-        if (__any_sync(0xffffffffu, m > 0x7F80u)) {  // NaN is held as 0
+      for (int y = 0; y < kWriteLoads; ++y) most = max(most, m[y] = block_max(w[y]));
+      if (__any_sync(0xffffffffu, most > 0x7F80u)) {  // NaN is held as 0
+#pragma unroll
+        for (int y = 0; y < kWriteLoads; ++y) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if ((w[y][i] & 0x7FFFu) > 0x7F80u) w[y][i] &= 0xFFFF0000u;
             if ((w[y][i] & 0x7FFF0000u) > 0x7F800000u) w[y][i] &= 0xFFFFu;
           }
-          m = block_max(w[y]);
+          m[y] = block_max(w[y]);
         }
-        const uint32_t sb = scale_bits(__uint_as_float(m << 16));
-        // scale 0: every channel is 0
+      }
+#pragma unroll
+      for (int y = 0; y < kWriteLoads; ++y) {
+        const uint32_t sb = scale_bits(__uint_as_float(m[y] << 16));
         const float s = __half2float(__ushort_as_half((unsigned short)(sb << 7)));
-        const uint32_t codes = sb ? encode8(w[y], __frcp_rn(s)) : 0;
-        const int tok = i0 + y * side + tok0;
-        if (mine && tok < tokens && s_tile[tok]) {
-          uint8_t* tile = s_tile[tok];
-          const int row = s_slot[tok] & 15;
-          *reinterpret_cast<uint32_t*>(tile + codes_at + row * (D / 2)) = codes;
-          if (!(c8 & 1)) tile[scale_at + row * (D / 16)] = (uint8_t)sb;
+        if (codes[y]) {
+          // scale 0: every channel is 0
+          *reinterpret_cast<uint32_t*>(codes[y] + codes_at) = sb ? encode8(w[y], reciprocal(s)) : 0;
+          if (!(c8 & 1)) s_scales[i0 + y * side + tok0][scale_at] = (uint8_t)sb;
         }
       }
     }
