@@ -159,7 +159,7 @@ struct Shape {
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kJoin = kWarps * kRows * kPitch * 4;
   static constexpr int kSmem = kRing + kJoin + kWarps * kRows * 8;
-  static constexpr int kBlocks = NT == 1 ? 4 : NT == 2 ? 3 : 2;  // an SM's, by registers and shared memory
+  static constexpr int kBlocks = NT == 1 || D == 64 ? 4 : 2;  // an SM's, by registers and shared memory
 };
 
 template <int D, int NT, bool kScores>
@@ -417,21 +417,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
       }
       if constexpr (kScores) {
         const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift;
-        float* dst = p.scores + (((int64_t)cons.seq * p.c.heads + head) * p.score_rows + row0) * slots + slot0;
+        float* dst = p.scores + (((int64_t)cons.seq * p.c.heads + head) * p.score_rows + row0 + 2 * t) * slots + slot0 + key0;
+        const int left = cons.m - slot0 - key0, rows_left = rows - row0 - 2 * t;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < NT; ++j, dst += 8 * slots) {
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int key = i * 16 + key0 + 8 * y;
-            if (slot0 + key >= cons.m) continue;
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
+            for (int y = 0; y < 2; ++y) {
               const float2 x2 = mul2(make_float2(s[i][j][2 * y], s[i][j][2 * y + 1]), f[j]);
-              const int r = 8 * j + 2 * t;
-              if (row0 + r < rows) dst[r * slots + key] = x2.x;
-              if (row0 + r + 1 < rows) dst[(r + 1) * slots + key] = x2.y;
+              const bool in = 16 * i + 8 * y < left;
+              if (in && 8 * j < rows_left) dst[16 * i + 8 * y] = x2.x;
+              if (in && 8 * j + 1 < rows_left) dst[slots + 16 * i + 8 * y] = x2.y;
             }
-          }
+        }
       }
       float2 top[NT];
       bool grow = false;
@@ -660,56 +659,67 @@ __global__ void __launch_bounds__(256) zl_kv4_join_kernel(const AttnParams p) {
 }
 
 // ---------------------------------------------------------------- accumulated weights
-// weights_out[slot] = decay weights[slot] + sum over rows of 2^(score - lse).  A row's scores lie side by side: four slots a
-// thread, eight rows' loads under way at a time.
+// weights_out[slot] = decay weights[slot] + sum over rows of 2^(score - lse).  A row's scores lie side by side; a thread takes
+// kPer slots and has kBatch rows' loads under way at a time: four slots where rows are few, one where they are many and slots
+// would not fill the SMs (48 rows over 17 000 slots and 8 heads: 21 us with four).
 constexpr int kWeightThreads = 128;
-constexpr int kWeightSlots = 4 * kWeightThreads;  // slots a block takes
+template <int kPer, int kBatch>
 __global__ void __launch_bounds__(kWeightThreads) zl_kv4_weights_kernel(const AttnParams p) {
   let_next_start();
   wait_for_previous();
-  const int b = blockIdx.z, h = blockIdx.y;
+  const int b = blockIdx.z, h = blockIdx.y, s0 = blockIdx.x * kWeightThreads * kPer, s = s0 + kPer * threadIdx.x;
   extern __shared__ float lse2[];  // base-2 LSE of every row; of rows that see nothing +inf: 2^(-inf) each
   const int m = kv4_len(p.c, b);
-  const int s = blockIdx.x * kWeightSlots + 4 * threadIdx.x;
-  if (blockIdx.x * kWeightSlots >= m) return;
   int first = 0;
   const int n = kv4_new(p.c, p.starts, p.n_tokens, p.max_new, b, &first), rows = n * p.group;
+  if (s0 >= m) return;
+  const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift, at = ((int64_t)b * p.c.heads + h) * slots + s;
+  const float* x = p.scores + ((int64_t)b * p.c.heads + h) * p.score_rows * slots + s;
+  float v[kBatch][kPer], w[kPer];
+  auto load = [&](int r0) {  // slots of the table past the last one are the workspace's, too
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const float* from = x + (int64_t)min(r0 + y, p.score_rows - 1) * slots;
+      if constexpr (kPer == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(from);
+        v[y][0] = f.x; v[y][1] = f.y; v[y][2] = f.z; v[y][3] = f.w;
+      } else {
+        v[y][0] = *from;
+      }
+    }
+  };
+  const bool in = s < m;
+  if (in) load(0);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) w[i] = p.w_in && s + i < m - n ? p.decay * p.w_in[at + i] : 0.f;
   for (int r = threadIdx.x; r < rows; r += kWeightThreads) {
     const int tok = r / p.group;
     const float l = p.lse[(int64_t)(first + tok) * p.q_heads + h * p.group + r - tok * p.group];
     lse2[r] = l == -INFINITY ? INFINITY : l * kLog2e;
   }
   __syncthreads();
-  if (s >= m) return;
-  const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift, at = ((int64_t)b * p.c.heads + h) * slots + s;
-  const float* x = p.scores + ((int64_t)b * p.c.heads + h) * p.score_rows * slots + s;
-  float w[4];
+  if (!in) return;
+  for (int r0 = 0; r0 < rows; r0 += kBatch) {
+    if (r0 > 0) load(r0);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = p.w_in && s + i < m - n ? p.decay * p.w_in[at + i] : 0.f;
-  for (int r0 = 0; r0 < rows; r0 += 8) {
-    float4 v[8];
+    for (int y = 0; y < kBatch; ++y) {
+      const float l = r0 + y < rows ? lse2[r0 + y] : INFINITY;
 #pragma unroll
-    for (int y = 0; y < 8; ++y) v[y] = *reinterpret_cast<const float4*>(x + min(r0 + y, rows - 1) * slots);
-#pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      if (r0 + y >= rows) break;
-      const float l = lse2[r0 + y];
-      w[0] += ex2(v[y].x - l);
-      w[1] += ex2(v[y].y - l);
-      w[2] += ex2(v[y].z - l);
-      w[3] += ex2(v[y].w - l);
+      for (int i = 0; i < kPer; ++i) w[i] += l == INFINITY ? 0.f : ex2(v[y][i] - l);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kPer; ++i)
     if (s + i < m) p.w_out[at + i] = w[i];
 }
 
 // ---------------------------------------------------------------- host
 int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
 
-// 8-row columns of a warp's products: as many as the rows of a key head need, up to 32 rows a pass over the cache.
-int row_columns(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// 8-row columns of a warp's products: one where a key head has no more rows, else two, and as many passes over the cache as the
+// rows need.  (Four in a pass, at two blocks an SM for their registers: 66 us instead of 54 for 32 rows over 16 x 4096 slots,
+// 32/8 heads, d = 128; 31 instead of 33 at d = 64.)
+int row_columns(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 struct Layout {
   int64_t ml, cuts, scores, total;
@@ -759,9 +769,7 @@ cudaError_t launch_attn(AttnParams& p, int sms, cudaStream_t stream) {
 }
 template <int D, bool kScores>
 cudaError_t launch_attn(AttnParams& p, int columns, int sms, cudaStream_t stream) {
-  return columns == 1   ? launch_attn<D, 1, kScores>(p, sms, stream)
-         : columns == 2 ? launch_attn<D, 2, kScores>(p, sms, stream)
-                        : launch_attn<D, 4, kScores>(p, sms, stream);
+  return columns == 1 ? launch_attn<D, 1, kScores>(p, sms, stream) : launch_attn<D, 2, kScores>(p, sms, stream);
 }
 
 }  // namespace
@@ -834,8 +842,11 @@ extern "C" zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, i
   }
   if (e == cudaSuccess && weights_out && cache->max_pages > 0) {
     const int64_t slots = (int64_t)cache->max_pages * cache->page;
-    e = launch_overlapped(zl_kv4_weights_kernel, dim3((unsigned)((slots + kWeightSlots - 1) / kWeightSlots), cache->n_kv_heads, cache->n_seqs),
-                          kWeightThreads, (size_t)group * max_new * 4, st, p);
+    const bool few = l.score_rows <= 8;
+    const int block_slots = kWeightThreads * (few ? 4 : 1);
+    e = launch_overlapped(few ? zl_kv4_weights_kernel<4, 4> : zl_kv4_weights_kernel<1, 16>,
+                          dim3((unsigned)((slots + block_slots - 1) / block_slots), cache->n_kv_heads, cache->n_seqs), kWeightThreads,
+                          (size_t)l.score_rows * 4, st, p);
   }
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
