@@ -23,6 +23,7 @@ constexpr int kEvictThreads = 512;  // at least the bins of the first histogram
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kHeldSlots = 24576;  // that a block's shared memory has room for (8 bytes each)
 constexpr int kCluster = 8;
+constexpr int kFew = 4;            // slots given up that are looked for one by one
 constexpr int kMoveThreads = 256;
 constexpr int kMoves = 128;        // moves that a block of the second launch makes
 constexpr int kMovesApart = 256;   // moves a head from which on a second launch makes them
@@ -40,9 +41,9 @@ struct EvictParams {
 
 // Larger weights have larger numbers; NaN has the smallest, -0 is 0.
 __device__ __forceinline__ uint32_t rank_of(float w) {
-  if (w != w) return 0;
   const uint32_t b = __float_as_uint(w + 0.f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t r = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return w == w ? r : 0;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -66,22 +67,6 @@ __device__ __forceinline__ int peer(const int* mine, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
-}
-
-// Exclusive prefix of a number per warp over the block's warps (lane 0's counts); warp_sums is free again after the next sync.
-__device__ __forceinline__ int before_warp(int x, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) warp_sums[warp] = x;
-  __syncthreads();
-  const int x_of = lane < kEvictWarps ? warp_sums[lane] : 0;
-  int run = x_of;
-#pragma unroll
-  for (int i = 1; i < 32; i <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, run, i);
-    if (lane >= i) run += y;
-  }
-  *total = __shfl_sync(0xffffffffu, run, 31);
-  return __shfl_sync(0xffffffffu, run, warp) - __shfl_sync(0xffffffffu, x_of, warp);
 }
 
 // Moves i, i + step, .. of a head, kAtOnce of them, below `end`: 16 lanes a move, codes of keys and values in 16-byte pieces,
@@ -126,16 +111,40 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int item, int i,
   }
 }
 
+// The same for one move whose slots are known: from slot `from` to slot `to`.
+template <int D>
+__device__ __forceinline__ void move_row(const EvictParams& p, int b, int h, int64_t base, int to, int from) {
+  const int l = threadIdx.x & 15;
+  if (l == 14) p.weights_out[base + to] = p.weights[base + from];
+  if (l == 15) p.positions_out[base + to] = p.positions[base + from];
+  uint8_t* dst = kv4_tile<D>(p.c, b, h, to);
+  const uint8_t* src = kv4_tile<D>(p.c, b, h, from);
+  if (!dst || !src) {
+    if (l == 0) kv4_report(p.c, ZL_KV4_BAD_PAGE);
+    return;
+  }
+  constexpr int kPieces = D / 32;
+  const int r0 = to & 15, r1 = from & 15;
+  if (l < 2 * kPieces) {
+    const int at = (l / kPieces) * 8 * D + (l % kPieces) * 16;
+    *reinterpret_cast<uint4*>(dst + at + r0 * (D / 2)) = *reinterpret_cast<const uint4*>(src + at + r1 * (D / 2));
+  } else if (l >= 8 && l < 8 + 2 * (D / 64)) {
+    const int at = 16 * D + ((l - 8) / (D / 64)) * D + ((l - 8) % (D / 64)) * 4;
+    *reinterpret_cast<uint32_t*>(dst + at + r0 * (D / 16)) = *reinterpret_cast<const uint32_t*>(src + at + r1 * (D / 16));
+  }
+}
+
 // kHeld: the block's run of slots is kept in shared memory; else (runs past kHeldSlots) it is read again in each pass.
 template <int D, bool kHeld>
 __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const EvictParams p) {
-  extern __shared__ int held[];  // [2][run]: ranks, positions
-  __shared__ int hist[2][512];   // of two rounds in turn; the first round's: others, then the recent ones
-  __shared__ int local[4][512];  // of a quarter of the warps
-  __shared__ int sum[512];
-  __shared__ int warp_sums[kEvictWarps];
-  __shared__ int pub[4];  // read by the cluster: newest position, kept below `keep`, kept
-  __shared__ int s_digit, s_above;
+  extern __shared__ int held[];            // [2][run]: weights, positions
+  __shared__ int local[4][512];            // a round's histogram, of a quarter of the warps; the first round's: others, then the recent ones
+  __shared__ int hist[2][512];             // of the block, of two rounds in turn
+  __shared__ int warp_sums[2][kEvictWarps];
+  __shared__ uint64_t warp_least[kEvictWarps];
+  __shared__ uint32_t kept_bits[kHeld ? kHeldSlots / 32 : 1];  // of 32 slots each: which stay
+  __shared__ int pub[4];                   // read by the cluster: newest position, kept below `keep`, kept
+  __shared__ int s_digit, s_above, s_count;
   const uint32_t cr = cluster_rank(), cn = cluster_size();
   const int item = blockIdx.x / cn, b = item / p.c.heads, h = item - b * p.c.heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -159,141 +168,220 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
     if (p.counts && cr == 0 && tid == 0) p.counts[item] = 0;
     return;
   }
-  uint32_t* held_rank = reinterpret_cast<uint32_t*>(held);
+  float* held_w = reinterpret_cast<float*>(held);
   int* held_pos = held + run;
-  auto rank_at = [&](int i) { return kHeld ? held_rank[i] : rank_of(w[lo + i]); };
+  auto w_at = [&](int i) { return kHeld ? held_w[i] : w[lo + i]; };
   auto pos_at = [&](int i) { return kHeld ? held_pos[i] : pos[lo + i]; };
   int newest = INT32_MIN;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = tid; i < count; i += kEvictThreads) {
     const int at = pos[lo + i];
     if constexpr (kHeld) {
-      held_rank[i] = rank_of(w[lo + i]);
+      held_w[i] = w[lo + i];
       held_pos[i] = at;
     }
     newest = max(newest, at);
   }
   newest = __reduce_max_sync(0xffffffffu, newest);
-  if (lane == 0) warp_sums[warp] = newest;
-  for (int i = tid; i < 4 * 512; i += kEvictThreads) (&local[0][0])[i] = 0;
+  if (lane == 0) warp_sums[0][warp] = newest;
+  if (tid == 0) s_digit = s_above = s_count = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) local[i][tid] = 0;
   __syncthreads();
-  newest = __reduce_max_sync(0xffffffffu, warp_sums[lane % kEvictWarps]);
+  newest = __reduce_max_sync(0xffffffffu, warp_sums[0][lane % kEvictWarps]);
   if (cn > 1) {
     if (tid == 0) pub[0] = newest;
     cluster_sync();
     newest = __reduce_max_sync(0xffffffffu, peer(&pub[0], lane < cn ? lane : 0));
   }
-  const int64_t border = (int64_t)newest - p.recent;
+  // position above newest - p.recent: the difference fits 32 bits without a sign
+  auto is_recent = [&](int at) { return (uint32_t)newest - (uint32_t)at < (uint32_t)p.recent; };
+
+  // A step gives up a slot or a few: the least in claim, one after another, and no selection by digits.
+  if (cn == 1 && kHeld && n - keep <= kFew) {
+    int gone[kFew];
+#pragma unroll
+    for (int y = 0; y < kFew; ++y) {
+      gone[y] = INT32_MAX;
+      if (y >= n - keep) continue;
+      // 33 bits of claim, then 31 of the slot: the highest of equals goes first
+      uint64_t least = ~0ull;
+      for (int i = tid; i < n; i += kEvictThreads) {
+        bool out = false;
+#pragma unroll
+        for (int z = 0; z < y; ++z) out |= gone[z] == i;
+        const uint64_t claim = ((uint64_t)(is_recent(held_pos[i]) ? 1 : 0) << 63) | ((uint64_t)rank_of(held_w[i]) << 31) | (uint32_t)(INT32_MAX - i);
+        if (!out && claim < least) least = claim;
+      }
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) {
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, least, i);
+        least = other < least ? other : least;
+      }
+      if (lane == 0) warp_least[warp] = least;
+      __syncthreads();
+      least = warp_least[lane % kEvictWarps];
+#pragma unroll
+      for (int i = kEvictWarps / 2; i > 0; i >>= 1) {
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, least, i);
+        least = other < least ? other : least;
+      }
+      gone[y] = INT32_MAX - (int)(least & INT32_MAX);
+      __syncthreads();  // the warps' least ones have been read
+    }
+    if (copy_w || copy_pos)
+      for (int i = tid; i < keep; i += kEvictThreads) {
+        bool out = false;
+#pragma unroll
+        for (int y = 0; y < kFew; ++y) out |= gone[y] == i;
+        if (out) continue;
+        if (copy_w) w_out[i] = held_w[i];
+        if (copy_pos) pos_out[i] = held_pos[i];
+      }
+    // the i-th survivor in the last slots and the i-th slot given up before them, by counting; 16 lanes a move
+    int to = INT32_MAX, from = INT32_MAX, moves = 0;
+    const int i = tid / 16;
+#pragma unroll
+    for (int y = 0; y < kFew; ++y) {
+      int before = 0;
+#pragma unroll
+      for (int z = 0; z < kFew; ++z) before += gone[z] < gone[y];
+      if (gone[y] < keep) {
+        ++moves;
+        if (before == i) to = gone[y];
+      }
+    }
+    int number = 0;
+    for (int slot = keep; slot < n; ++slot) {
+      bool out = false;
+#pragma unroll
+      for (int y = 0; y < kFew; ++y) out |= gone[y] == slot;
+      if (!out && number++ == i) from = slot;
+    }
+    if (p.counts) {  // for the launch that follows
+      if (tid == 0) p.counts[item] = 0;
+    }
+    if (i < moves && from < n) move_row<D>(p, b, h, base, to, from);
+    return;
+  }
 
   // radix selection: after each round the border's leading digits, and how many of those that share them still count
   bool among_recent = false;  // the slots among which the weights decide: the recent ones where they alone are too many
-  int need = 0, ties = 0;     // at the end: how many slots of the border's rank stay; how many lie in this block's run
-  int ties_before = 0, ties_all = 0;
+  int need = 0;               // how many slots of the border's digits stay ..
+  int ties_all = 0, ties = 0, ties_before = 0;  // .. of how many there are: in all, in this block's run, before it
   uint32_t prefix = 0, mask = 0;
   for (int round = 0; round < 4; ++round) {
-    const int shift = 24 - 8 * round, bins = round == 0 ? 512 : 256;
+    const int shift = 24 - 8 * round;
     int* mine = local[warp & 3];
 #pragma unroll 4
     for (int i = tid; i < count; i += kEvictThreads) {
-      const bool recent = pos_at(i) > border;
-      const uint32_t r = rank_at(i);
-      if (round == 0) atomicAdd(&mine[(r >> 24) + (recent ? 256 : 0)], 1);
-      else if (recent == among_recent && (r & mask) == prefix) atomicAdd(&mine[(r >> shift) & 255], 1);
+      const bool recent = is_recent(pos_at(i));
+      const uint32_t r = rank_of(w_at(i));
+      // the largest digit first: threads below number them so
+      if (round == 0) atomicAdd(&mine[(255 - (r >> 24)) + (recent ? 256 : 0)], 1);
+      else if (recent == among_recent && (r & mask) == prefix) atomicAdd(&mine[255 - ((r >> shift) & 255)], 1);
     }
     __syncthreads();
-    int* mine_all = hist[round & 1];
-    if (tid < bins) {
-      mine_all[tid] = local[0][tid] + local[1][tid] + local[2][tid] + local[3][tid];
+    int* of_block = hist[round & 1];
+    int x = local[0][tid] + local[1][tid] + local[2][tid] + local[3][tid];
+    of_block[tid] = x;
+    if (cn > 1) {
+      cluster_sync();
+      x = 0;
+      for (uint32_t i = 0; i < cn; ++i) x += peer(&of_block[tid], i);
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) local[i][tid] = 0;
+    for (int i = 0; i < 4; ++i) local[i][tid] = 0;
+    // counts of digits from the top, of 256 threads each: where they reach `need`
+    int up = x;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, up, i);
+      if (lane >= i) up += y;
     }
-    if (cn > 1) cluster_sync();
-    else __syncthreads();
-    if (tid < bins) {
-      int all = 0;
-      if (cn > 1) for (uint32_t i = 0; i < cn; ++i) all += peer(&mine_all[tid], i);
-      else all = mine_all[tid];
-      sum[tid] = all;
-    }
+    if (lane == 31) warp_sums[round & 1][warp] = up;
     __syncthreads();
+    const int sums = lane < kEvictWarps ? warp_sums[round & 1][lane] : 0;
     if (round == 0) {
-      int safe = 0;
-#pragma unroll
-      for (int i = 0; i < 256; i += 32) safe += sum[256 + i + lane];
-      safe = __reduce_add_sync(0xffffffffu, safe);
+      const int safe = __reduce_add_sync(0xffffffffu, lane >= 8 ? sums : 0);
       among_recent = safe > keep;
       need = among_recent ? keep : keep - safe;
     }
-    if (warp == 0) {
-      // counts of digits from the top, eight a lane: the digit at which they reach `need`
-      const int* bin = sum + (round == 0 && among_recent ? 256 : 0) + 248 - 8 * lane;
-      int x[8], mine_sum = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mine_sum += x[i] = bin[7 - i];
-      int up = mine_sum;
-#pragma unroll
-      for (int i = 1; i < 32; i <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, up, i);
-        if (lane >= i) up += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, up >= need);
-      if (lane == (hit ? __ffs(hit) - 1 : 31)) {
-        int above = up - mine_sum, i = 0;
-        while (i < 7 && above + x[i] < need) above += x[i++];
-        s_digit = 255 - 8 * lane - i;
-        s_above = above;
-      }
+    const int of = round == 0 && among_recent ? 8 : 0;  // the first warp of the digits that decide
+    const int above = up - x + __reduce_add_sync(0xffffffffu, lane >= of && lane < warp ? sums : 0);
+    if (warp >= of && warp < of + 8 && ((above < need && above + x >= need) || (need == 0 && tid == 32 * of))) {
+      s_digit = tid & 255;
+      s_above = above;
+      s_count = x;
     }
     __syncthreads();
     need -= s_above;
-    prefix |= (uint32_t)s_digit << shift;
+    ties_all = s_count;
+    prefix |= (uint32_t)(255 - s_digit) << shift;
     mask |= 255u << shift;
-    ties_all = sum[s_digit + (round == 0 && among_recent ? 256 : 0)];
     if (round == 3 || ties_all == need) {  // all that share the digits so far stay, or the digits are the border's rank itself
-      const int* at = &mine_all[s_digit + (round == 0 && among_recent ? 256 : 0)];
-      const int of = lane < cn ? (cn > 1 ? peer(at, lane) : *at) : 0;
-      ties_before = __reduce_add_sync(0xffffffffu, lane < cr ? of : 0);
-      ties = __shfl_sync(0xffffffffu, of, cr);
+      const int* at = &of_block[s_digit + 32 * of];
+      const int there = lane < cn ? (cn > 1 ? peer(at, lane) : *at) : 0;
+      ties_before = __reduce_add_sync(0xffffffffu, lane < cr ? there : 0);
+      ties = __shfl_sync(0xffffffffu, there, cr);
       break;
     }
   }
   // `need` of the slots at the border stay, the lowest ones.  Warps take contiguous parts of the run.
   const int part = ((count + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
   const int i0 = min(count, warp * part), i1 = min(count, i0 + part);
-  auto state = [&](int i) {  // 0: given up, 1: stays, 2: at the border
-    if (i >= i1) return 0;
-    const bool recent = pos_at(i) > border;
-    if (recent != among_recent) return recent ? 1 : 0;
-    const uint32_t r = rank_at(i) & mask;
-    return r > prefix ? 1 : r == prefix ? 2 : 0;
+  // of a warp's 32 slots from i on, as bits: those that stay for sure and those at the border
+  auto states = [&](int i, uint32_t* border) {
+    const bool in = i + lane < i1;
+    const int at = in ? i + lane : i0;
+    const bool recent = is_recent(pos_at(at)), decides = recent == among_recent;
+    const uint32_t r = rank_of(w_at(at)) & mask;
+    *border = __ballot_sync(0xffffffffu, in & decides & (r == prefix));
+    return __ballot_sync(0xffffffffu, in & (decides ? r > prefix : recent));
   };
+  const bool all_ties = need == ties_all;
   int tie0 = ties_before;  // ties before this warp's part
-  if (ties > 0 && need < ties_all) {
-    int mine = 0, all;
-    for (int i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, state(i + lane) == 2));
+  if (ties > 0 && !all_ties) {
+    int mine = 0;
+    for (int i = i0; i < i1; i += 32) {
+      uint32_t border;
+      states(i, &border);
+      mine += __popc(border);
+    }
+    __syncthreads();  // the rounds' sums have been read
+    if (lane == 0) warp_sums[0][warp] = mine;
     __syncthreads();
-    tie0 += before_warp(mine, warp_sums, &all);
+    tie0 += __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[0][lane % kEvictWarps] : 0);
   }
-  auto stays = [&](int i, int& tie) {  // of a warp's 32 slots from i on; tie: ties before them
-    const int st = state(i + lane);
-    const unsigned at_border = __ballot_sync(0xffffffffu, st == 2);
-    const bool kept = st == 1 || (st == 2 && (need == ties_all || tie + __popc(at_border & ((1u << lane) - 1)) < need));
-    tie += __popc(at_border);
-    return kept;
+  auto stays = [&](int i, int& tie) {  // those that stay; tie: ties before them
+    uint32_t border;
+    const uint32_t sure = states(i, &border);
+    if (all_ties) return sure | border;
+    const bool in = tie + __popc(border & ((1u << lane) - 1)) < need;
+    tie += __popc(border);
+    return sure | (border & __ballot_sync(0xffffffffu, in));
   };
   int kept_front = 0, kept = 0, tie = tie0;
+#pragma unroll 4
   for (int i = i0; i < i1; i += 32) {
-    const unsigned k = __ballot_sync(0xffffffffu, stays(i, tie));
+    const uint32_t k = stays(i, tie);
+    if constexpr (kHeld)
+      if (lane == 0) kept_bits[i / 32] = k;
     kept += __popc(k);
-    const int front = keep - (lo + i);  // of these 32 slots that many lie below `keep`
-    if (front > 0) kept_front += __popc(front >= 32 ? k : k & ((1u << front) - 1));
+    const int front = min(max(keep - (lo + i), 0), 32);  // of these 32 slots that many lie below `keep`
+    kept_front += __popc(k & (uint32_t)((1ull << front) - 1));
+  }
+  __syncthreads();  // sums have been read
+  if (lane == 0) {
+    warp_sums[0][warp] = kept_front;
+    warp_sums[1][warp] = kept;
   }
   __syncthreads();
-  int front_all, kept_all;
-  before_warp(kept_front, warp_sums, &front_all);
-  __syncthreads();
-  int k = before_warp(kept, warp_sums, &kept_all);  // slots kept before this warp's part
+  const int sum0 = lane < kEvictWarps ? warp_sums[0][lane] : 0, sum1 = lane < kEvictWarps ? warp_sums[1][lane] : 0;
+  int front_all = __reduce_add_sync(0xffffffffu, sum0);               // kept below `keep`
+  int k = __reduce_add_sync(0xffffffffu, lane < warp ? sum1 : 0);     // kept before this warp's part
   if (cn > 1) {
+    const int kept_all = __reduce_add_sync(0xffffffffu, sum1);
     if (tid == 0) {
       pub[1] = front_all;
       pub[2] = kept_all;
@@ -306,19 +394,19 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
   int2* holes = p.moves + (int64_t)item * 2 * p.capacity;
   int2* movers = holes + p.capacity;
   tie = tie0;
+#pragma unroll 4
   for (int i = i0; i < i1; i += 32) {
-    const bool kept_here = stays(i, tie);
-    const unsigned all = __ballot_sync(0xffffffffu, kept_here);
+    const uint32_t all = kHeld ? kept_bits[i / 32] : stays(i, tie);
     const int slot = lo + i + lane, before = k + __popc(all & ((1u << lane) - 1));
+    const bool kept_here = (all >> lane) & 1, front = slot < keep;
     k += __popc(all);
-    if (i + lane < i1) {
-      // within the lists whatever happens to the inputs meanwhile
-      if (!kept_here && slot < keep && slot - before < p.capacity) holes[slot - before] = make_int2(slot, kv4_place(p.c, b, h, slot));
-      if (kept_here && slot >= keep && before - front_all < p.capacity) movers[before - front_all] = make_int2(slot, kv4_place(p.c, b, h, slot));
-      if (kept_here && slot < keep) {
-        if (copy_w) w_out[slot] = w[slot];
-        if (copy_pos) pos_out[slot] = pos[slot];
-      }
+    if (i + lane >= i1) continue;
+    const int at = front ? slot - before : before - front_all;
+    // within the lists whatever happens to the inputs meanwhile
+    if (kept_here != front && at < p.capacity) (front ? holes : movers)[at] = make_int2(slot, kv4_place(p.c, b, h, slot));
+    if (kept_here && front) {
+      if (copy_w) w_out[slot] = w_at(i + lane);
+      if (copy_pos) pos_out[slot] = pos_at(i + lane);
     }
   }
   const int moves = min(keep - front_all, p.capacity);

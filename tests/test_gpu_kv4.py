@@ -125,6 +125,42 @@ def test_write_ties_zeros_tiny_large_and_no_numbers():
             assert np.array_equal(np.where(a == 8, 0, a) if len(a) == d else a, np.where(b == 8, 0, b) if len(b) == d else b), s
 
 
+def test_write_every_quotient():
+    """Every pair of a scale's and a channel's leading digits that bf16 has, at normal and at the smallest scales; every
+    largest magnitude."""
+    import torch
+    rows = []
+    for e in (0, -9, -14, -15, -17):
+        for m in range(8, 16):
+            s = m / 8 * 2.0 ** e
+            if s * 2 ** 17 != np.floor(s * 2 ** 17):
+                continue  # the smallest scales have fewer digits
+            x = np.concatenate([np.arange(128, 256) / 128 * 2.0 ** (e + i) for i in range(-4, 3)])
+            x = x[x <= 6 * s]
+            x = np.concatenate([x, np.zeros(-len(x) % 15)]).reshape(-1, 15)
+            rows.append(np.concatenate([np.full((len(x), 1), 6 * s), x], 1))
+    blocks = np.concatenate(rows)
+    top = np.arange(1, 0x7F80, dtype=np.uint32) << 16  # every bf16 number as a block's largest
+    top = top.view(np.float32).astype(np.float64)
+    more = np.zeros((len(top), 16))
+    more[:, 3], more[:, 7] = -top, top / 2
+    blocks = np.concatenate([blocks, more])
+    blocks = np.concatenate([blocks, np.zeros((-len(blocks) % 4, 16))]).reshape(-1, 64)
+    x = torch.from_numpy(blocks).bfloat16()[:, None].cuda()
+    n = len(blocks)
+    c = zl.allocate_kv4(1, -(-n // 256), 1, 64, page=256)
+    c.lens.fill_(n)
+    zl.zl_kv4_write(c, x, -x, torch.tensor([0, n], dtype=torch.int32).cuda())
+    codes, bits = ref.encode(f64(x)[:, 0])
+    tiles = c.data.cpu().numpy().reshape(-1, 18 * 64)
+    got_bits = np.concatenate([tiles[:, 16 * 64 + i * 64:16 * 64 + (i + 1) * 64].reshape(-1, 4)[:n] for i in range(2)])
+    assert np.array_equal(got_bits, np.concatenate([bits, bits]))
+    k, v = torch.empty_like(x), torch.empty_like(x)
+    zl.zl_kv4_read(c, k, v, torch.zeros(1, dtype=torch.int64).cuda())
+    want = ref.decode(codes, bits)
+    assert np.array_equal(f64(k)[:, 0], want) and np.array_equal(f64(v)[:, 0], -want)
+
+
 def test_write_one_token_each_without_starts_and_odd_lengths():
     import torch
     lens = [1, 16, 17, 0, 48]  # a sequence of no slots has none for its token
@@ -376,9 +412,9 @@ def test_bad_lengths_and_starts_are_left_out():
 
 
 # ---------------------------------------------------------------- eviction
-def check_eviction(lens, heads, d, page, keep, recent, weights, positions, seed, in_place):
+def check_eviction(lens, heads, d, page, keep, recent, weights, positions, seed, in_place, table=0):
     import torch
-    c, data, pages = make_cache(lens, heads, d, page, seed)
+    c, data, pages = make_cache(lens, heads, d, page, seed, extra_pages=max(0, table - max(-(-n // page) for n in lens)))
     w, pos = torch.from_numpy(weights).float().cuda(), torch.from_numpy(positions).int().cuda()
     wo, po = torch.full_like(w, 7.0), torch.full_like(pos, 7)
     if in_place:
@@ -423,6 +459,23 @@ def test_eviction(heads, d, page, lens, keep, recent, kind, in_place):
         w = rng.choice(np.array([0.0, -0.0, np.nan, np.inf, -np.inf, 1e-45, -1e-45, 3.0, -3.0], np.float32), shape)
     pos = np.argsort(rng.random(shape), -1)
     check_eviction(lens, heads, d, page, keep, recent, w.astype(np.float32), pos, 31, in_place)
+
+
+@pytest.mark.parametrize("kind", ["plain", "ties", "odd"])
+@pytest.mark.parametrize("keep,recent", [(64, 0), (64, 5), (64, 64), (64, 100), (2, 1)])
+def test_eviction_of_a_few_slots(kind, keep, recent):
+    """One to six more than are kept, in a table with and without room for many moves."""
+    rng = np.random.default_rng(45)
+    lens = [keep + i for i in (1, 2, 3, 4, 5, 6, 0)]
+    for slots, in_place in ((80, False), (80, True), (640, False)):
+        shape = (len(lens), 2, slots)
+        w = rng.exponential(size=shape)
+        if kind == "ties":
+            w = np.round(w)
+        if kind == "odd":
+            w = rng.choice(np.array([0.0, -0.0, np.nan, np.inf, -np.inf, 3.0, -3.0]), shape)
+        pos = np.argsort(rng.random(shape), -1) - 40
+        check_eviction(lens, 2, 64, 16, keep, recent, w.astype(np.float32), pos, 46, in_place, table=slots // 16)
 
 
 def test_eviction_among_equal_weights_and_extreme_positions():
