@@ -1095,6 +1095,63 @@ def zl_kv4_get_device_status(cache: Kv4Cache) -> int:
     return s
 
 
+def allocate_kv4_attention(cache: Kv4Cache, n_tokens: int, n_q_heads: int, max_new: int = 1, evicts: bool = False) -> Dict[str, "object"]:
+    """Buffers of qkv_attention_cached for n_tokens new tokens, at most max_new of a sequence; evicts: with the slots'
+    accumulated weights and positions, which belong to the cache's sequences and live as long as they do."""
+    import torch
+    heads, d = cache.token_shape
+    device = cache.data.device
+    bf = dict(dtype=torch.bfloat16, device=device)
+    ws = zl_kv4_attn_workspace_bytes(cache, n_q_heads, max_new, evicts)
+    if evicts:
+        ws = max(ws, zl_kv4_evict_workspace_bytes(cache))
+    out = {"q": torch.empty(n_tokens, n_q_heads, d, **bf), "k": torch.empty(n_tokens, heads, d, **bf),
+           "o": torch.empty(n_tokens, n_q_heads, d, **bf),
+           "lse": torch.empty(n_tokens, n_q_heads, dtype=torch.float32, device=device),
+           "workspace": torch.empty(max(16, ws), dtype=torch.uint8, device=device)}
+    if evicts:
+        out["weights"] = torch.zeros(cache.slot_shape, dtype=torch.float32, device=device)
+        out["positions"] = torch.zeros(cache.slot_shape, dtype=torch.int32, device=device)
+    return out
+
+
+def qkv_attention_cached(cache: Kv4Cache, qkv, positions, table: Optional[RotaryTable], scale: float, bufs: dict, q_weight=None,
+                         k_weight=None, eps: float = 1e-6, starts=None, max_new: int = 1, keep: Optional[int] = None,
+                         recent: int = 0, decay: float = 1.0, stream=None) -> dict:
+    """A serving step from a projection's output qkv [tokens, Hq + 2 Hkv, d]: queries and keys normalised where weights are
+    given and rotated, keys and values into the 4-bit cache, attention of the new tokens over it (bufs["o"],
+    bufs["lse"]).  starts, max_new as in zl_kv4_attn_fwd; cache.lens counts the new tokens already.  With keep, sequences
+    live on that many slots: the step's softmax weights are added to bufs["weights"] (decay * the sums so far), every
+    head keeps its `keep` slots, and cache.lens becomes no more than that.  One captured graph serves every step."""
+    torch = _torch()
+    heads, d = cache.token_shape
+    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 3 or qkv.shape[1] <= 2 * heads or qkv.shape[2] != d:
+        raise ValueError(f"qkv: expected [tokens, Hq + {2 * heads}, {d}], got {tuple(getattr(qkv, 'shape', ()))}")
+    if keep is not None:
+        if "weights" not in bufs:
+            raise ValueError("keep: needs buffers that were allocated with evicts=True")
+        if not isinstance(positions, torch.Tensor) or positions.numel() != qkv.shape[0]:
+            raise ValueError("keep: needs one position a token")
+    hq = qkv.shape[1] - 2 * heads
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + heads], qkv[:, hq + heads:]
+    for of_q, of_k, norm in _sides(q_weight, k_weight):
+        zl_qk_rope_fwd(q if of_q else None, k if of_k else None, bufs["q"] if of_q else None, bufs["k"] if of_k else None,
+                       positions, table, norm, q_weight if of_q else None, k_weight if of_k else None, eps, stream)
+    if keep is None:
+        zl_kv4_write(cache, bufs["k"], v, starts, stream=stream)
+        zl_kv4_attn_fwd(cache, bufs["q"], bufs["o"], bufs["lse"], bufs["workspace"], scale, starts, max_new, stream=stream)
+        return bufs
+    w, at = bufs["weights"], bufs["positions"]
+    zl_kv4_write(cache, bufs["k"], v, starts, positions.view(-1), at, stream)
+    zl_kv4_attn_fwd(cache, bufs["q"], bufs["o"], bufs["lse"], bufs["workspace"], scale, starts, max_new, w, w, decay, stream)
+    zl_kv4_evict(cache, w, at, keep, recent, bufs["workspace"], stream=stream)
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw_stream(stream, cache.device), cache.data.device)
+    with torch.cuda.stream(stream):  # None: the current one
+        cache.lens.clamp_(max=keep)
+    return bufs
+
+
 # ---------------------------------------------------------------- host placement slice
 def catalog_cut(buckets):
     """zl_catalog_cut over [(seq_len, count, time, mem), ...] sorted by time: returns

@@ -354,6 +354,22 @@ def test_attention_scores_far_apart_and_queries_of_any_size(size):
     run_attention(c, data, pages, lens, [1, 2], 4, 23, size=size, weights=True)
 
 
+def test_a_table_without_pages():
+    import torch
+    c = zl.Kv4Cache(torch.zeros(0, 2, 1, 18 * 64, dtype=torch.uint8).cuda(), torch.zeros(2, 0, dtype=torch.int32).cuda(),
+                    torch.zeros(2, dtype=torch.int32).cuda())
+    q, o, lse = torch.ones(2, 4, 64).bfloat16().cuda(), torch.full((2, 4, 64), 7.0).bfloat16().cuda(), torch.empty(2, 4).cuda()
+    w = torch.empty(c.slot_shape).cuda()
+    ws = torch.empty(zl.zl_kv4_attn_workspace_bytes(c, 4, 1, True), dtype=torch.uint8).cuda()
+    zl.zl_kv4_attn_fwd(c, q, o, lse, ws, 0.1, weights_out=w)
+    assert (o == 0).all() and (lse == -np.inf).all()
+    k = torch.ones(2, 2, 64).bfloat16().cuda()
+    zl.zl_kv4_write(c, k, k)
+    zl.zl_kv4_read(c, k, k, torch.zeros(2, dtype=torch.int64).cuda())
+    zl.zl_kv4_evict(c, w, w.int(), 3, 1, torch.empty(16, dtype=torch.uint8).cuda())
+    assert zl.zl_kv4_get_device_status(c) == 0 and (k == 1).all()
+
+
 def test_attention_repeats_bit_for_bit():
     import torch
     lens = [5000, 1, 777]
@@ -459,6 +475,17 @@ def test_eviction(heads, d, page, lens, keep, recent, kind, in_place):
         w = rng.choice(np.array([0.0, -0.0, np.nan, np.inf, -np.inf, 1e-45, -1e-45, 3.0, -3.0], np.float32), shape)
     pos = np.argsort(rng.random(shape), -1)
     check_eviction(lens, heads, d, page, keep, recent, w.astype(np.float32), pos, 31, in_place)
+
+
+@pytest.mark.parametrize("slots,keep", [(20011, 5003), (60000, 200), (230000, 129)])
+def test_eviction_of_long_sequences(slots, keep):
+    """Eight blocks a head; past 196 608 slots a run does not fit a block's shared memory."""
+    rng = np.random.default_rng(47)
+    lens = [slots, slots // 7, keep + 2]
+    shape = (3, 1, -(-slots // 256) * 256)
+    w = np.round(rng.exponential(size=shape) * 64).astype(np.float32)
+    pos = np.argsort(rng.random(shape), -1)
+    check_eviction(lens, 1, 64, 256, keep, 50, w, pos, 48, False)
 
 
 @pytest.mark.parametrize("kind", ["plain", "ties", "odd"])
@@ -605,6 +632,71 @@ def test_prompt_through_the_cache_and_the_causal_attention():
         # P is bf16 there: half a step more of every weight
         assert np.abs(f64(bufs["o"]) - want["o"]).max() <= (tol["o"] + 2.0 ** -8 * np.abs(v.float().cpu().numpy()).max() * 2).max()
         assert np.abs(f64(bufs["lse"]) - want["lse"]).max() <= 1e-4
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("on_stream", [False, True])
+def test_projection_to_output_through_the_cache(norm, on_stream):
+    """Three steps from a projection's output, the last on a budget, against the operators one by one in 64 bits."""
+    import torch
+    from oracle import causal
+    heads, hq, d, page, B = 2, 6, 64, 16, 3
+    c = zl.allocate_kv4(B, 5, heads, d, page=page)
+    freqs, amplitude = zl.rotary_frequencies(d)
+    table = zl.rotary_table(freqs, amplitude=amplitude)
+    g = torch.Generator().manual_seed(50)
+    qw, kw = ((1 + 0.1 * torch.randn(d, generator=g)).cuda() if norm else None for _ in range(2))
+    total = np.zeros(B, int)
+    data, pages = c.data.cpu().numpy(), c.pages.cpu().numpy()
+    stream = torch.cuda.Stream() if on_stream else None
+    w = np.zeros(c.slot_shape)
+    for new, keep in (([20, 37, 5], None), ([1, 1, 0], None), ([3, 1, 2], 30)):
+        n = sum(new)
+        s, ds = starts_of(new)
+        qkv = torch.randn(n, hq + 2 * heads, d, generator=g).bfloat16().cuda()
+        total = total + new
+        pos = np.concatenate([np.arange(total[b] - new[b], total[b]) for b in range(B)])
+        bufs = zl.allocate_kv4_attention(c, n, hq, max(new), evicts=keep is not None)
+        if keep is not None:
+            bufs["positions"].copy_(torch.arange(c.slots, dtype=torch.int32))
+            bufs["weights"].copy_(torch.rand(c.slot_shape, generator=g))
+            w = f64(bufs["weights"])
+        c.lens.copy_(torch.from_numpy(total).int())
+        dpos = torch.from_numpy(pos).int().cuda()
+        torch.cuda.synchronize()
+        zl.qkv_attention_cached(c, qkv, dpos, table, d ** -0.5, bufs, qw, kw, starts=ds, max_new=max(new), keep=keep, recent=4,
+                                stream=stream)
+        torch.cuda.synchronize()
+        # rotation within its own rounding; from there on with the rows that it left
+        ang = causal.angles(pos[:, None], freqs, [d // 2])
+        for x, y, weight in ((qkv[:, :hq], bufs["q"], qw), (qkv[:, hq:hq + heads], bufs["k"], kw)):
+            want = f64(x)
+            if norm:
+                want = causal.rms_norm(want, f64(weight), 1e-6)
+            want = causal.rotate(want, ang, True) * amplitude
+            assert np.abs(f64(y) - want).max() <= 2.0 ** -7 * (1 + np.abs(want).max())
+        ref.write(data, pages, total, s, f64(bufs["k"]), f64(qkv[:, hq + heads:]))
+        want, tol = reference(f64(bufs["q"]), data, pages, total, s, d ** -0.5, w if keep is not None else None)
+        within(f64(bufs["o"]), want["o"], tol["o"], "o")
+        within(f64(bufs["lse"]), want["lse"], tol["lse"], "lse")
+        if keep is not None:
+            for b in range(B):
+                for h in range(heads):
+                    order = want["weights"][b, h, :total[b]]
+                    for a, to in ref.evict_moves(order, np.arange(total[b]), keep, 4):
+                        ref.put_row(data, pages, b, h, to, ref.get_row(data, pages, b, h, a))
+            assert np.array_equal(c.lens.cpu().numpy(), np.minimum(total, keep))
+        got = c.data.cpu().numpy()
+        for b in range(B):
+            for h in range(heads):
+                m = total[b] if keep is None else min(total[b], keep)
+                for y, z in zip(ref.sequence(got, pages, b, h, m), ref.sequence(data, pages, b, h, m)):
+                    assert np.array_equal(y, z)
+    assert zl.zl_kv4_get_device_status(c) == 0
+    with pytest.raises(ValueError):
+        zl.qkv_attention_cached(c, qkv[:, :2 * heads], dpos, table, 0.1, bufs)
+    with pytest.raises(ValueError):
+        zl.qkv_attention_cached(c, qkv, dpos, table, 0.1, zl.allocate_kv4_attention(c, n, hq, 3), starts=ds, max_new=3, keep=3)
 
 
 def test_calls_on_other_streams_at_once():
