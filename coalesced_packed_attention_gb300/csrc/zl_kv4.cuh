@@ -30,7 +30,7 @@ inline zl_status kv4_check(const zl_kv4_cache* c, Kv4* out) {
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256) return ZL_ERR_UNSUPPORTED;
   if (c->n_seqs < 0 || c->n_seqs > (1 << 20) || c->n_kv_heads < 1 || c->n_kv_heads > 1024 || c->max_pages < 0 ||
       c->n_pages < 0 || c->n_pages > INT32_MAX || (int64_t)c->max_pages * c->page >= 1 << 30 ||
-      c->n_pages * c->n_kv_heads * (c->page / 16) >= UINT32_MAX)
+      c->n_pages * c->n_kv_heads * (c->page / 16) >= 1 << 28)  // of 1152 bytes and more: 309 GB
     return ZL_ERR_INVALID_ARG;
   if (c->n_seqs > 0 && (!c->lens || (c->max_pages > 0 && !c->pages) || (c->n_pages > 0 && !c->data))) return ZL_ERR_INVALID_ARG;
   if (!kv4_aligned(c->data, 16) || !kv4_aligned(c->pages, 4) || !kv4_aligned(c->lens, 4) || !kv4_aligned(c->status, 4))
@@ -69,7 +69,7 @@ __device__ __forceinline__ int kv4_new(const Kv4& c, const int32_t* starts, int6
   kv4_report(c, ZL_KV4_BAD_STARTS);
   return 0;
 }
-// Number of a slot's tile in `data` (they are less than 2^32), or kKv4None where its page is none of the cache's.
+// Number of a slot's tile in `data` (they are less than 2^28), or kKv4None where its page is none of the cache's.
 constexpr uint32_t kKv4None = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t kv4_place(const Kv4& c, int b, int h, int slot) {
   const uint32_t page = c.pages[(int64_t)b * c.max_pages + (slot >> c.page_shift)];

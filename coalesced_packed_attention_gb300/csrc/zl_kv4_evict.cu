@@ -25,7 +25,7 @@ constexpr int kHeldSlots = 24576;  // that a block's shared memory has room for 
 constexpr int kCluster = 8;
 constexpr int kFew = 4;            // slots given up that are looked for one by one
 constexpr int kMoveThreads = 256;
-constexpr int kMoves = 128;        // moves that a block of the second launch makes
+constexpr int kMoves = 64;         // moves that a block of the second launch makes
 constexpr int kMovesApart = 256;   // moves a head from which on a second launch makes them
 
 struct EvictParams {
@@ -35,7 +35,7 @@ struct EvictParams {
   float* weights_out;
   int32_t* positions_out;
   int32_t* counts;  // [sequence][key head]: moves, where a launch of their own makes them (else null)
-  int2* moves;      // [sequence][key head][2][capacity]: slots given up, survivors: slot and tile
+  uint32_t* moves;  // [sequence][key head][4][capacity]: slots given up, their rows; survivors' slots, their rows (16 tile + row)
   int32_t keep, recent, capacity;
 };
 
@@ -69,45 +69,50 @@ __device__ __forceinline__ int peer(const int* mine, uint32_t rank) {
   return v;
 }
 
-// Moves i, i + step, .. of a head, kAtOnce of them, below `end`: 16 lanes a move, codes of keys and values in 16-byte pieces,
-// scales, weight and position.  A lane's piece is found by a pointer rather than by branches, so that all loads are under way
-// together (a register that two branches load into is waited for between them: 14 us instead of 5 for 1790 rows of each of 4 heads).
-template <int D, int kAtOnce>
-__device__ __forceinline__ void move_rows(const EvictParams& p, int item, int i, int step, int end) {
-  const int l = threadIdx.x & 15;
-  const int64_t base = (int64_t)item * ((int64_t)p.c.max_pages << p.c.page_shift);
-  const int2* holes = p.moves + (int64_t)item * 2 * p.capacity;
-  constexpr int kPieces = D / 32;  // of a row's codes
-  const bool code = l < 2 * kPieces, scale = l >= 8 && l < 8 + 2 * (D / 64), number = l >= 14;
-  // where a lane's piece of row 0 lies in a tile, and of the next row
-  const int at = code ? (l / kPieces) * 8 * D + (l % kPieces) * 16 : 16 * D + ((l - 8) / (D / 64)) * D + ((l - 8) % (D / 64)) * 4;
-  const int pitch = code ? D / 2 : D / 16;
-  const uint8_t* in = reinterpret_cast<const uint8_t*>(l == 14 ? static_cast<const void*>(p.weights + base) : p.positions + base);
-  uint8_t* out = reinterpret_cast<uint8_t*>(l == 14 ? static_cast<void*>(p.weights_out + base) : p.positions_out + base);
-  int2 to[kAtOnce], from[kAtOnce];
-#pragma unroll
-  for (int y = 0; y < kAtOnce; ++y) {
-    const int j = min(i + y * step, end - 1);
-    to[y] = holes[j];
-    from[y] = holes[p.capacity + j];
+// 16 lanes a move: codes of keys and values in 16-byte pieces, scales, weight and position.  A lane's piece of a slot or of a
+// row is found by a pointer rather than by branches, so that all loads are under way together (a register that two branches
+// load into is waited for between them: 14 us instead of 5 for 1790 rows of each of 4 heads).
+template <int D>
+struct Piece {
+  static constexpr int kPieces = D / 32;  // of a row's codes
+  bool code, number, idle;
+  int at, pitch;
+  const uint8_t* in;
+  uint8_t* out;
+  __device__ Piece(const EvictParams& p, int64_t base) {
+    const int l = threadIdx.x & 15;
+    code = l < 2 * kPieces;
+    number = l >= 14;
+    idle = !code && !number && (l < 8 || l >= 8 + 2 * (D / 64));
+    at = code ? (l / kPieces) * 8 * D + (l % kPieces) * 16 : 16 * D + ((l - 8) / (D / 64)) * D + ((l - 8) % (D / 64)) * 4;
+    pitch = number ? 4 : code ? D / 2 : D / 16;
+    in = l == 14 ? reinterpret_cast<const uint8_t*>(p.weights + base) : l == 15 ? reinterpret_cast<const uint8_t*>(p.positions + base) : p.c.data;
+    out = l == 14 ? reinterpret_cast<uint8_t*>(p.weights_out + base) : l == 15 ? reinterpret_cast<uint8_t*>(p.positions_out + base) : p.c.data;
   }
+  // bytes to the piece of slot or row x
+  __device__ int64_t offset(uint32_t x) const { return number ? (int64_t)x * 4 : (int64_t)(x >> 4) * (18 * D) + at + (x & 15) * pitch; }
+};
+// Moves i, i + step, .. of a head, kAtOnce of them, whose numbers of slots or rows (a lane's own kind) are known.
+template <int D, int kAtOnce>
+__device__ __forceinline__ void move_pieces(const EvictParams& p, const Piece<D>& piece, const uint32_t (&to)[kAtOnce], const uint32_t (&from)[kAtOnce],
+                                            int i, int step, int end) {
   uint4 v[kAtOnce];
   uint32_t u[kAtOnce];
   bool does[kAtOnce];
 #pragma unroll
   for (int y = 0; y < kAtOnce; ++y) {
-    const bool bad = (uint32_t)to[y].y == kKv4None || (uint32_t)from[y].y == kKv4None;
-    does[y] = i + y * step < end && (number || ((code || scale) && !bad));
-    if (bad && l == 0 && i + y * step < end) kv4_report(p.c, ZL_KV4_BAD_PAGE);
-    const uint8_t* src = number ? in + (int64_t)from[y].x * 4 : p.c.data + (uint64_t)(uint32_t)from[y].y * (18 * D) + at + (from[y].x & 15) * pitch;
-    if (does[y] && code) v[y] = *reinterpret_cast<const uint4*>(src);
-    if (does[y] && !code) u[y] = *reinterpret_cast<const uint32_t*>(src);
+    const bool in = i + y * step < end, bad = !piece.number && (to[y] == kKv4None || from[y] == kKv4None);
+    does[y] = in && !piece.idle && !bad;
+    if (in && bad && (threadIdx.x & 15) == 0) kv4_report(p.c, ZL_KV4_BAD_PAGE);
+    const uint8_t* src = piece.in + piece.offset(from[y]);
+    if (does[y] && piece.code) v[y] = *reinterpret_cast<const uint4*>(src);
+    if (does[y] && !piece.code) u[y] = *reinterpret_cast<const uint32_t*>(src);
   }
 #pragma unroll
   for (int y = 0; y < kAtOnce; ++y) {
-    uint8_t* dst = number ? out + (int64_t)to[y].x * 4 : p.c.data + (uint64_t)(uint32_t)to[y].y * (18 * D) + at + (to[y].x & 15) * pitch;
-    if (does[y] && code) *reinterpret_cast<uint4*>(dst) = v[y];
-    if (does[y] && !code) *reinterpret_cast<uint32_t*>(dst) = u[y];
+    uint8_t* dst = piece.out + piece.offset(to[y]);
+    if (does[y] && piece.code) *reinterpret_cast<uint4*>(dst) = v[y];
+    if (does[y] && !piece.code) *reinterpret_cast<uint32_t*>(dst) = u[y];
   }
 }
 
@@ -287,8 +292,12 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
     of_block[tid] = x;
     if (cn > 1) {
       cluster_sync();
+      int of_peer[kCluster];
+#pragma unroll
+      for (uint32_t i = 0; i < kCluster; ++i) of_peer[i] = peer(&of_block[tid], min(i, cn - 1));
       x = 0;
-      for (uint32_t i = 0; i < cn; ++i) x += peer(&of_block[tid], i);
+#pragma unroll
+      for (uint32_t i = 0; i < kCluster; ++i) x += i < cn ? of_peer[i] : 0;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) local[i][tid] = 0;
@@ -391,22 +400,36 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
     front_all = __reduce_add_sync(0xffffffffu, f);
     k += __reduce_add_sync(0xffffffffu, a);
   }
-  int2* holes = p.moves + (int64_t)item * 2 * p.capacity;
-  int2* movers = holes + p.capacity;
+  uint32_t* list = p.moves + (int64_t)item * 4 * p.capacity;
   tie = tie0;
-#pragma unroll 4
-  for (int i = i0; i < i1; i += 32) {
-    const uint32_t all = kHeld ? kept_bits[i / 32] : stays(i, tie);
-    const int slot = lo + i + lane, before = k + __popc(all & ((1u << lane) - 1));
-    const bool kept_here = (all >> lane) & 1, front = slot < keep;
-    k += __popc(all);
-    if (i + lane >= i1) continue;
-    const int at = front ? slot - before : before - front_all;
-    // within the lists whatever happens to the inputs meanwhile
-    if (kept_here != front && at < p.capacity) (front ? holes : movers)[at] = make_int2(slot, kv4_place(p.c, b, h, slot));
-    if (kept_here && front) {
-      if (copy_w) w_out[slot] = w_at(i + lane);
-      if (copy_pos) pos_out[slot] = pos_at(i + lane);
+  // four times 32 slots at a time, their pages' loads under way together
+  constexpr int kAtOnce = 4;
+  for (int i = i0; i < i1; i += 32 * kAtOnce) {
+    int at[kAtOnce];
+    uint32_t place[kAtOnce];
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) {
+      at[y] = -1;
+      if (i + 32 * y >= i1) continue;  // the whole warp
+      const uint32_t all = kHeld ? kept_bits[i / 32 + y] : stays(i + 32 * y, tie);
+      const int mine = i + 32 * y + lane, slot = lo + mine, before = k + __popc(all & ((1u << lane) - 1));
+      const bool kept_here = (all >> lane) & 1, front = slot < keep;
+      k += __popc(all);
+      if (mine < i1 && kept_here != front) at[y] = front ? slot - before : 2 * p.capacity + before - front_all;
+      if (mine < i1 && kept_here && front) {
+        if (copy_w) w_out[slot] = w_at(mine);
+        if (copy_pos) pos_out[slot] = pos_at(mine);
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) place[y] = at[y] >= 0 ? kv4_place(p.c, b, h, lo + i + 32 * y + lane) : 0;
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) {
+      // within the lists whatever happens to the inputs meanwhile
+      if (at[y] < 0 || (at[y] < 2 * p.capacity ? at[y] : at[y] - 2 * p.capacity) >= p.capacity) continue;
+      const int slot = lo + i + 32 * y + lane;
+      list[at[y]] = slot;
+      list[at[y] + p.capacity] = place[y] == kKv4None ? kKv4None : place[y] * 16 + (slot & 15);
     }
   }
   const int moves = min(keep - front_all, p.capacity);
@@ -418,18 +441,34 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
   if (cn > 1) cluster_sync();
   else __syncthreads();
   constexpr int kGroups = kEvictThreads / 16;
-  for (int i = (int)cr * kGroups; i < moves; i += (int)cn * kGroups) move_rows<D, 1>(p, item, i + tid / 16, kGroups, min(moves, i + kGroups));
+  const Piece<D> piece(p, base);
+  const uint32_t* mine = list + (piece.number ? 0 : p.capacity);
+  for (int i = (int)cr * kGroups + tid / 16; i < moves; i += (int)cn * kGroups) {
+    const uint32_t to[1] = {mine[i]}, from[1] = {mine[i + 2 * p.capacity]};
+    move_pieces<D, 1>(p, piece, to, from, i, 0, moves);
+  }
 }
 
-// kMoves of a head a block.
+// kMoves of a head a block, four in each group of 16 lanes; the list is loaded before it is known how far it reaches.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) zl_kv4_move_kernel(const EvictParams p) {
   let_next_start();
   wait_for_previous();
   const int item = blockIdx.y + blockIdx.z * 65535;
   if (item >= p.c.n_seqs * p.c.heads) return;
-  const int first = blockIdx.x * kMoves, moves = p.counts[item];
-  if (first < moves) move_rows<D, kMoves * 16 / kMoveThreads>(p, item, first + threadIdx.x / 16, kMoveThreads / 16, min(moves, first + kMoves));
+  constexpr int kGroups = kMoveThreads / 16, kAtOnce = kMoves / kGroups;
+  const Piece<D> piece(p, (int64_t)item * ((int64_t)p.c.max_pages << p.c.page_shift));
+  const uint32_t* mine = p.moves + (int64_t)item * 4 * p.capacity + (piece.number ? 0 : p.capacity);
+  const int i = blockIdx.x * kMoves + threadIdx.x / 16;
+  uint32_t to[kAtOnce], from[kAtOnce];
+#pragma unroll
+  for (int y = 0; y < kAtOnce; ++y) {
+    const int at = min(i + y * kGroups, p.capacity - 1);
+    to[y] = mine[at];
+    from[y] = mine[at + 2 * p.capacity];
+  }
+  const int moves = p.counts[item];
+  if (blockIdx.x * kMoves < moves) move_pieces<D, kAtOnce>(p, piece, to, from, i, kGroups, moves);
 }
 
 template <int D, bool kHeld>
@@ -468,7 +507,7 @@ extern "C" zl_status zl_kv4_evict_workspace(const zl_kv4_cache* cache, int64_t* 
   if (!bytes) return ZL_ERR_INVALID_ARG;
   const int64_t items = (int64_t)cache->n_seqs * cache->n_kv_heads;
   // moves are no more than half the slots: the slots given up in front are below keep, the survivors past it
-  *bytes = round16(items * 4) + items * 2 * ((int64_t)cache->max_pages * cache->page / 2) * 8;
+  *bytes = round16(items * 4) + items * 4 * ((int64_t)cache->max_pages * cache->page / 2) * 4;
   return ZL_OK;
 }
 
@@ -492,7 +531,7 @@ extern "C" zl_status zl_kv4_evict(const zl_kv4_cache* cache, const float* weight
   p.positions = positions;
   p.weights_out = weights_out;
   p.positions_out = positions_out;
-  p.moves = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + round16(items * 4));
+  p.moves = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + round16(items * 4));
   const int64_t most = slots - keep < keep ? slots - keep : keep;  // moves of a head at most
   const bool apart = most > kMovesApart;
   p.counts = apart ? static_cast<int32_t*>(workspace) : nullptr;
