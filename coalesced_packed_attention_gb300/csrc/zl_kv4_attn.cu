@@ -24,9 +24,8 @@
 #include <cmath>
 
 #include "zl_internal.h"
-#include "zl_kv4.cuh"
+#include "zl_kv4_attn.cuh"
 #include "zl_overlap.cuh"
-#include "zl_ptx.cuh"
 
 namespace zl {
 namespace {
@@ -34,40 +33,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;          // slots of a unit: two tiles
+constexpr int kItemCost = 8;       // units: 64 single tokens over 15 to 16 384 slots each took 98 us at 4, 87 at 8 and 12, 90 at 20
 constexpr int kMaxBlocks = 640;    // blocks of a launch at most: what the workspace has room for
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kTwice = 0x00800080u;  // a scale's bits times this: the scale in both halves, by the multiplier, which has time
-constexpr float kLow = -1e30f;     // the running maximum of rows that have seen nothing
-constexpr float kRescale = 8.f;    // the maximum may lag by 2^8 before the sums are rescaled
-
-// An item cut between blocks: its first block describes it for the join.
-struct alignas(16) Cut {
-  int32_t parts;   // 0: the item was not cut, or none that begins in this block
-  int32_t which;   // part of its first block, 2 block + (0 the block's first segment, 1 another); the following blocks' parts are their first
-  int32_t token0;  // row of the item's sequence in q and o
-  int32_t head0;   // first query head
-  int32_t row0, rows;
-  int32_t pad[2];
-};
-
-struct AttnParams {
-  Kv4 c;
-  const __nv_bfloat16* q;
-  int64_t q_stride, n_tokens;
-  const int32_t* starts;
-  __nv_bfloat16* o;
-  float* lse;
-  float* part_o;   // [2 blocks][rows][d]
-  float2* part_ml; // [2 blocks][rows]: maximum (base 2) and sum
-  Cut* cuts;       // by item where there are no more items than blocks, else by the block in which the item begins
-  int32_t max_tiles, by_item;  // row tiles of max_new tokens; how cuts is laid out
-  float* scores;   // [sequence][key head][score_rows][slot], base 2
-  const float* w_in;
-  float* w_out;
-  float decay;
-  float scale_log2;
-  int32_t group, q_heads, max_new, score_rows;
-};
 
 // ---------------------------------------------------------------- pieces of a product
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -97,59 +65,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-// log of a sum l of 2^(score - m); -inf for an empty one, NaN stays.
-__device__ __forceinline__ float natural_lse(float m, float l) { return l == 0.f ? -INFINITY : m * kLn2 + logf(l); }
-
-// ---------------------------------------------------------------- the schedule
-// The items' costs in a row, dealt out evenly: an item costs its units and kItemCost more (its queries, its join), which
-// stand before the first unit.  A cut inside them belongs to the first unit.  (64 single tokens over 15 to 16 384 slots
-// each: 98 us at 4, 87 at 8 and 12, 90 at 20.)
-constexpr int kItemCost = 8;
-
-// A block's run of units, item by item; the producers of the warps and their consumers each walk it by themselves.
-template <int NT>
-struct Walk {
-  int64_t left;        // cost of the block's run from this segment on
-  int32_t seq, head, tile;  // an item: a key head's row tile
-  int32_t n, m, first;      // the sequence's new tokens, slots and first token
-  int32_t row_tiles, chunks;
-  int32_t a, e;        // this segment: units [a, e) of the item's `chunks`
-
-  __device__ void load(const AttnParams& p) {
-    n = kv4_new(p.c, p.starts, p.n_tokens, p.max_new, seq, &first);
-    m = kv4_len(p.c, seq);
-    row_tiles = (n * p.group + 8 * NT - 1) / (8 * NT);
-    chunks = m > 0 ? (m + kUnit - 1) / kUnit : 1;
-  }
-  __device__ int64_t cost(const AttnParams& p) const { return (int64_t)p.c.heads * row_tiles * (chunks + kItemCost); }
-  // at cost `off` of the item: the segment from there on, without units where `left` ends before the first one
-  __device__ void enter(int off) {
-    const int end = (int)(left < chunks + kItemCost - off ? off + left : chunks + kItemCost);
-    a = off > kItemCost ? off - kItemCost : 0;
-    e = end > kItemCost ? end - kItemCost : 0;
-    left -= end - off;
-  }
-  __device__ bool done() const { return a >= e; }  // a segment without units is the last
-  __device__ void next(const AttnParams& p) {
-    a = e = 0;
-    if (left <= 0) return;
-    if (++tile == row_tiles) {
-      tile = 0;
-      if (++head == p.c.heads) {
-        head = 0;
-        do {
-          if (++seq >= p.c.n_seqs) {
-            left = 0;
-            return;
-          }
-          load(p);
-        } while (row_tiles == 0);
-      }
-    }
-    enter(0);
-  }
-};
-
+// ---------------------------------------------------------------- the kernel
 template <int D, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
@@ -174,57 +90,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
   float* join = reinterpret_cast<float*>(smem + S::kRing);
   float2* join_ml = reinterpret_cast<float2*>(smem + S::kRing + S::kJoin);
   if (threadIdx.x < kWarps * S::kStages) mbar_init(&bars[threadIdx.x], 1);
-  if (threadIdx.x == 0) {
-    s_seq = -1;
-    fence_mbar_init();
-  }
+  if (threadIdx.x == 0) fence_mbar_init();
   let_next_start();
   wait_for_previous();
 
-  // this block's run
-  Walk<NT> cons;
-  int64_t each;  // cost of a block's run
-  {
-    const int n = p.c.n_seqs, per = (n + kThreads - 1) / kThreads;
-    const int b0 = min(n, (int)threadIdx.x * per), b1 = min(n, b0 + per);
-    int64_t mine = 0, total;
-    for (int b = b0; b < b1; ++b) {
-      cons.seq = b;
-      cons.load(p);
-      mine += cons.cost(p);
-    }
-    int64_t before = kv4_scan<kThreads>(mine, &total, warp_sums);
-    each = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(kWarps + kItemCost));
-    const int64_t at = each * blockIdx.x, end = min(total, at + each);
-    if (at < end && at >= before && at < before + mine) {
-      int b = b0;
-      for (;; ++b) {
-        cons.seq = b;
-        cons.load(p);
-        if (at < before + cons.cost(p)) break;
-        before += cons.cost(p);
-      }
-      s_seq = b;
-      s_before = before;
-    }
-    __syncthreads();
-    if (s_seq < 0) {  // nothing for this block (uniform: the run is empty)
-      if (threadIdx.x == 0 && !p.by_item) p.cuts[blockIdx.x].parts = 0;
-      return;
-    }
-    cons.seq = s_seq;
-    cons.load(p);
-    cons.left = end - at;
-    const int64_t off = at - s_before, of_item = cons.chunks + kItemCost;
-    const int item = (int)(off / of_item);
-    cons.head = item / cons.row_tiles;
-    cons.tile = item - cons.head * cons.row_tiles;
-    cons.enter((int)(off - item * of_item));
-    if (threadIdx.x == 0 && !p.by_item) p.cuts[blockIdx.x].parts = 0;  // an item cut at the run's end sets it below
-  }
+  using W = Walk<S::kRows, kUnit, kItemCost>;
+  W cons;
+  int64_t each;
+  if (!first_segment_of<kThreads, kWarps + kItemCost>(p, warp_sums, &s_before, &s_seq, cons, &each)) return;
 
   // Loading: a warp looks up the places of its next 32 units at once, one a lane, and issues them one by one.
-  Walk<NT> prod = cons;
+  W prod = cons;
   int prod_x = prod.a + warp;         // the next unit to look up
   uint32_t tile0 = kKv4None, tile1 = kKv4None;  // the two tiles of a lane's unit
   int batch = 0, batch_end = 0;       // units looked up and not yet issued: lanes [batch, batch_end)
@@ -567,11 +443,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         if (c4 == 0) p.part_ml[(int64_t)part * S::kRows + r] = make_float2(m, l);
       }
     }
-    if (threadIdx.x == 0 && cons.a == 0 && (p.by_item || !whole)) {
-      const int rest = cons.chunks - cons.e;  // full runs follow until the item's end
-      Cut c = {whole ? 0 : 1 + (int)((rest + each - 1) / each), part, cons.first, head * p.group, row0, rows, {0, 0}};
-      p.cuts[p.by_item ? ((int64_t)cons.seq * p.c.heads + head) * p.max_tiles + cons.tile : blockIdx.x] = c;
-    }
+    if (threadIdx.x == 0) describe(p, cons, part, row0, rows, each);
     first_segment = false;
     __syncthreads();  // the join's buffer has been read
   }
@@ -721,16 +593,21 @@ int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
 // 32/8 heads, d = 128; 31 instead of 33 at d = 64.)
 int row_columns(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
+// From here on the tensor-core kernel.
+constexpr int64_t kChunkFrom = 17;
+int64_t tile_rows(int64_t rows) { return rows < kChunkFrom ? 8 * row_columns(rows) : kChunkRows; }
+int64_t most_blocks(int64_t rows) { return rows < kChunkFrom ? kMaxBlocks : kChunkMaxBlocks; }
+
 struct Layout {
   int64_t ml, cuts, scores, total;
   int32_t score_rows;
 };
 Layout layout(const zl_kv4_cache& c, int32_t group, int32_t max_new, bool weights) {
-  const int64_t rows = (int64_t)group * max_new, tile = 8 * row_columns(rows);
+  const int64_t rows = (int64_t)group * max_new, tile = tile_rows(rows), blocks = most_blocks(rows);
   Layout l;
-  l.ml = round16((int64_t)2 * kMaxBlocks * tile * c.head_dim * 4);
-  l.cuts = l.ml + round16((int64_t)2 * kMaxBlocks * tile * 8);
-  l.scores = l.cuts + round16((int64_t)kMaxBlocks * sizeof(Cut));
+  l.ml = round16(2 * blocks * tile * c.head_dim * 4);
+  l.cuts = l.ml + round16(2 * blocks * tile * 8);
+  l.scores = l.cuts + round16(blocks * (int64_t)sizeof(Cut));
   l.score_rows = (int32_t)rows;
   l.total = l.scores;
   if (weights) l.total += (int64_t)c.n_seqs * c.n_kv_heads * c.max_pages * c.page * l.score_rows * 4;
@@ -742,6 +619,19 @@ zl_status check_heads(const zl_kv4_cache* c, int32_t n_q_heads, int32_t max_new)
   const int64_t group = n_q_heads / c->n_kv_heads;
   if (group > 128 || group * max_new > 8192) return ZL_ERR_UNSUPPORTED;
   return ZL_OK;
+}
+
+// The join behind either kernel: items may be fewer than its blocks, and described one by one.
+template <int D, int kRows, typename Launch>
+cudaError_t launch_joined(AttnParams& p, int blocks, cudaStream_t stream, Launch&& launch) {
+  p.max_tiles = (p.max_new * p.group + kRows - 1) / kRows;
+  const int64_t items = (int64_t)p.c.n_seqs * p.c.heads * p.max_tiles;
+  p.by_item = items <= blocks;
+  const cudaError_t e = launch();
+  if (e != cudaSuccess) return e;
+  const unsigned cuts = p.by_item ? (unsigned)items : (unsigned)blocks;
+  if (items * 8 <= blocks) return launch_overlapped(zl_kv4_join_kernel<D, kRows, true>, dim3(cuts, kRows), 256, 0, stream, p);
+  return launch_overlapped(zl_kv4_join_kernel<D, kRows, false>, dim3(cuts, kRows / 8), 256, 0, stream, p);
 }
 
 template <int D, int NT, bool kScores>
@@ -758,18 +648,14 @@ cudaError_t launch_attn(AttnParams& p, int sms, cudaStream_t stream) {
   });
   if (e != cudaSuccess) return e;
   const int blocks = sms * per_sm < kMaxBlocks ? sms * per_sm : kMaxBlocks;
-  p.max_tiles = (p.max_new * p.group + S::kRows - 1) / S::kRows;
-  const int64_t items = (int64_t)p.c.n_seqs * p.c.heads * p.max_tiles;
-  p.by_item = items <= blocks;
-  e = launch_overlapped(kernel, blocks, kThreads, S::kSmem, stream, p);
-  if (e != cudaSuccess) return e;
-  const unsigned cuts = p.by_item ? (unsigned)items : (unsigned)blocks;
-  if (items * 8 <= blocks) return launch_overlapped(zl_kv4_join_kernel<D, S::kRows, true>, dim3(cuts, S::kRows), 256, 0, stream, p);
-  return launch_overlapped(zl_kv4_join_kernel<D, S::kRows, false>, dim3(cuts, NT), 256, 0, stream, p);
+  return launch_joined<D, S::kRows>(p, blocks, stream, [&] { return launch_overlapped(kernel, blocks, kThreads, S::kSmem, stream, p); });
 }
 template <int D, bool kScores>
-cudaError_t launch_attn(AttnParams& p, int columns, int sms, cudaStream_t stream) {
-  return columns == 1 ? launch_attn<D, 1, kScores>(p, sms, stream) : launch_attn<D, 2, kScores>(p, sms, stream);
+cudaError_t launch_attn(AttnParams& p, int64_t rows, int sms, cudaStream_t stream) {
+  if (rows < kChunkFrom)
+    return row_columns(rows) == 1 ? launch_attn<D, 1, kScores>(p, sms, stream) : launch_attn<D, 2, kScores>(p, sms, stream);
+  const int blocks = sms < kChunkMaxBlocks ? sms : kChunkMaxBlocks;
+  return launch_joined<D, kChunkRows>(p, blocks, stream, [&] { return launch_kv4_chunk(D, kScores, p, blocks, stream); });
 }
 
 }  // namespace
@@ -834,11 +720,11 @@ extern "C" zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, i
   p.max_new = max_new;
   p.score_rows = l.score_rows;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int columns = row_columns((int64_t)group * max_new);
+  const int64_t rows = (int64_t)group * max_new;
   cudaError_t e = cudaSuccess;
   if (n_tokens > 0) {
-    if (cache->head_dim == 128) e = weights_out ? launch_attn<128, true>(p, columns, sms, st) : launch_attn<128, false>(p, columns, sms, st);
-    else e = weights_out ? launch_attn<64, true>(p, columns, sms, st) : launch_attn<64, false>(p, columns, sms, st);
+    if (cache->head_dim == 128) e = weights_out ? launch_attn<128, true>(p, rows, sms, st) : launch_attn<128, false>(p, rows, sms, st);
+    else e = weights_out ? launch_attn<64, true>(p, rows, sms, st) : launch_attn<64, false>(p, rows, sms, st);
   }
   if (e == cudaSuccess && weights_out && cache->max_pages > 0) {
     const int64_t slots = (int64_t)cache->max_pages * cache->page;
