@@ -21,6 +21,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "zl_internal.h"
@@ -593,21 +594,30 @@ int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
 // 32/8 heads, d = 128; 31 instead of 33 at d = 64.)
 int row_columns(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
-// From here on the tensor-core kernel.
-constexpr int64_t kChunkFrom = 17;
-int64_t tile_rows(int64_t rows) { return rows < kChunkFrom ? 8 * row_columns(rows) : kChunkRows; }
-int64_t most_blocks(int64_t rows) { return rows < kChunkFrom ? kMaxBlocks : kChunkMaxBlocks; }
+// The tensor-core kernel (zl_kv4_chunk.cu) instead: for more than two passes' rows over slots enough to pay for its start.
+// Measured (us; here / there): 32, 48, 64, 128 rows over 16 x 4096 slots of 8 key heads, d = 128: 52 / 56, 71 / 58, 88 / 59, 165 / 67;
+// d = 64: 34 / 46, 44 / 46, 75 / 48.  Few slots: 64 rows over 4 x 1000 of 4 heads 13 / 20, 4 x 4000 20 / 22, 8 x 1000 of 8 heads
+// 22 / 21; 128 rows over 4 x 2000 of 4 heads 21 / 26, 4 x 4000 29 / 28.  So by the product, of the slots that the table has
+// room for, as lengths lie on the device.  Not with weights: its scores leave a row a thread, which costs what it gains
+// (16 x 2000 slots of 4 heads, 64 and 128 rows: 44 / 48, 76 / 71 at d = 128, 36 / 42, 61 / 62 at d = 64).
+constexpr int64_t kChunkFrom = 33;
+constexpr int64_t kChunkWork = int64_t{1} << 22;  // rows x slots x key heads
+bool by_chunks(const zl_kv4_cache& c, int64_t rows, bool weights) {
+  return !weights && rows >= kChunkFrom && rows * c.n_seqs * c.n_kv_heads >= kChunkWork / std::max(1, c.max_pages * c.page);
+}
 
 struct Layout {
   int64_t ml, cuts, scores, total;
   int32_t score_rows;
 };
 Layout layout(const zl_kv4_cache& c, int32_t group, int32_t max_new, bool weights) {
-  const int64_t rows = (int64_t)group * max_new, tile = tile_rows(rows), blocks = most_blocks(rows);
+  const int64_t rows = (int64_t)group * max_new, tile = 8 * row_columns(rows);
+  // room for either kernel's parts, so that a call of fewer rows or without weights fits where this one does
+  const int64_t part_rows = 2 * (rows < kChunkFrom ? kMaxBlocks * tile : std::max<int64_t>(kMaxBlocks * tile, kChunkMaxBlocks * kChunkRows));
   Layout l;
-  l.ml = round16(2 * blocks * tile * c.head_dim * 4);
-  l.cuts = l.ml + round16(2 * blocks * tile * 8);
-  l.scores = l.cuts + round16(blocks * (int64_t)sizeof(Cut));
+  l.ml = part_rows * c.head_dim * 4;
+  l.cuts = l.ml + part_rows * 8;
+  l.scores = l.cuts + round16(kMaxBlocks * (int64_t)sizeof(Cut));
   l.score_rows = (int32_t)rows;
   l.total = l.scores;
   if (weights) l.total += (int64_t)c.n_seqs * c.n_kv_heads * c.max_pages * c.page * l.score_rows * 4;
@@ -651,11 +661,11 @@ cudaError_t launch_attn(AttnParams& p, int sms, cudaStream_t stream) {
   return launch_joined<D, S::kRows>(p, blocks, stream, [&] { return launch_overlapped(kernel, blocks, kThreads, S::kSmem, stream, p); });
 }
 template <int D, bool kScores>
-cudaError_t launch_attn(AttnParams& p, int64_t rows, int sms, cudaStream_t stream) {
-  if (rows < kChunkFrom)
+cudaError_t launch_attn(AttnParams& p, int64_t rows, bool chunks, int sms, cudaStream_t stream) {
+  if (!chunks)
     return row_columns(rows) == 1 ? launch_attn<D, 1, kScores>(p, sms, stream) : launch_attn<D, 2, kScores>(p, sms, stream);
   const int blocks = sms < kChunkMaxBlocks ? sms : kChunkMaxBlocks;
-  return launch_joined<D, kChunkRows>(p, blocks, stream, [&] { return launch_kv4_chunk(D, kScores, p, blocks, stream); });
+  return launch_joined<D, kChunkRows>(p, blocks, stream, [&] { return launch_kv4_chunk(D, p, blocks, stream); });
 }
 
 }  // namespace
@@ -723,8 +733,9 @@ extern "C" zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, i
   const int64_t rows = (int64_t)group * max_new;
   cudaError_t e = cudaSuccess;
   if (n_tokens > 0) {
-    if (cache->head_dim == 128) e = weights_out ? launch_attn<128, true>(p, rows, sms, st) : launch_attn<128, false>(p, rows, sms, st);
-    else e = weights_out ? launch_attn<64, true>(p, rows, sms, st) : launch_attn<64, false>(p, rows, sms, st);
+    const bool chunks = by_chunks(*cache, rows, weights_out != nullptr);
+    if (cache->head_dim == 128) e = weights_out ? launch_attn<128, true>(p, rows, chunks, sms, st) : launch_attn<128, false>(p, rows, chunks, sms, st);
+    else e = weights_out ? launch_attn<64, true>(p, rows, chunks, sms, st) : launch_attn<64, false>(p, rows, chunks, sms, st);
   }
   if (e == cudaSuccess && weights_out && cache->max_pages > 0) {
     const int64_t slots = (int64_t)cache->max_pages * cache->page;

@@ -142,9 +142,9 @@ __device__ __forceinline__ void describe(const AttnParams& p, const W& w, int pa
   p.cuts[p.by_item ? ((int64_t)w.seq * p.c.heads + w.head) * p.max_tiles + w.tile : blockIdx.x] = c;
 }
 
-// Rows of more than 16 a key head: tensor-core kernel (zl_kv4_chunk.cu); its blocks and rows of a tile.
+// Many rows a key head: tensor-core kernel (zl_kv4_chunk.cu); its blocks and rows of a tile.
 constexpr int kChunkRows = 128;
 constexpr int kChunkMaxBlocks = 160;
-cudaError_t launch_kv4_chunk(int head_dim, bool scores, const AttnParams& p, int blocks, cudaStream_t stream);
+cudaError_t launch_kv4_chunk(int head_dim, const AttnParams& p, int blocks, cudaStream_t stream);
 
 }  // namespace zl

@@ -1,14 +1,18 @@
 // Attention of many rows over the 4-bit cache: chunks of prompts, drafted tokens of large groups.
 //
-// With more than 16 rows (tokens x group) a key head, forming fp16 operands from codes for every 16 rows is what a pass
-// over the cache costs (zl_kv4_attn.cu).  Here it is done once for 128 rows: eight warps turn a block of 128 slots into
+// With many rows (tokens x group) a key head, forming fp16 operands from codes for every 16 rows is what a pass over the
+// cache costs (zl_kv4_attn.cu, which also has the rule between the two).  Here it is done once for 128 rows: eight warps turn a block of 128 slots into
 // fp16 tiles in shared memory (exact: code * scale has six bits), and the tensor core takes them as tcgen05 operands,
 //   S = Q K^T (both from shared memory),  O += P V (P from tensor memory, V channel-major),
 // with 128 rows to a tile and S, P and O in tensor memory; one warpgroup does the softmax, a thread a row.
 //
 // Per block of 128 slots the tensor core works 1024 cycles (d = 128), the exponentials of 128 rows take 1024, and shared
-// memory moves 178 KB (codes in and out 18 + 18, tiles in 64, operands out 96): 1400 cycles, which is the bound.  Rows that a
-// tile lacks cost nothing in the softmax (their warps pass by) and the same in the products.
+// memory moves 178 KB (codes in and out 18 + 18, tiles in 64, operands out 96): 1400 cycles.  Measured, a block takes some 3500
+// (128 rows over 16 x 4096 slots of 8 key heads, d = 128: 67 us, 27 blocks an SM; 16-row passes 165; rows read back and causal
+// attention 110): the chain S -> maximum -> exponentials -> P -> P V of the one warpgroup that a tile of 128 rows has, each step
+// some 400 to 1200 cycles with its waits.  The scores kept in 208 registers a thread between maximum and exponentials, with the
+// next block's keys formed ahead of this block's values, took as long (67 us).  Rows that a tile lacks cost nothing in the
+// softmax (their warps pass by) and the same in the products.
 // Order: S of a block is issued ahead of P V of the one before it, so that the softmax always has scores to work on; two
 // buffers each of S, P, K and V, three of codes.
 // Roles (448 threads, one block an SM): warps 0-3 softmax and output (thread = row = TMEM lane), 4-11 operands, 12 products,
@@ -48,7 +52,7 @@ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-template <int D, bool kScores>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnParams p) {
   using L = Layout<D>;
   using W = Walk<kChunkRows, kUnit, kItemCost>;
@@ -294,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnPar
     // ------------------------------------------------------------ softmax, output: thread = row
     const int r = threadIdx.x;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift;
     uint32_t it = 0, segs = 0;
     bool ok = true, first_segment = true;
     for (; !seg.done() && ok; seg.next(p), ++segs) {
@@ -343,26 +346,6 @@ __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnPar
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int e = 0; e < 32; e += 2) top = max3(top, __uint_as_float(u[c][e]), __uint_as_float(u[c][e + 1]));
-            if constexpr (kScores) {
-              if (row < rows) {
-                float* dst = p.scores + (((int64_t)seg.seq * p.c.heads + seg.head) * p.score_rows + row) * slots + slot0 + 64 * half;
-                const int left = seg.m - slot0 - 64 * half;
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                  for (int e = 0; e < 32; e += 4) {
-                    const float4 v = make_float4(__uint_as_float(u[c][e]) * f, __uint_as_float(u[c][e + 1]) * f,
-                                                 __uint_as_float(u[c][e + 2]) * f, __uint_as_float(u[c][e + 3]) * f);
-                    if (32 * c + e + 3 < left) {
-                      *reinterpret_cast<float4*>(dst + 32 * c + e) = v;
-                    } else {
-                      if (32 * c + e < left) dst[32 * c + e] = v.x;
-                      if (32 * c + e + 1 < left) dst[32 * c + e + 1] = v.y;
-                      if (32 * c + e + 2 < left) dst[32 * c + e + 2] = v.z;
-                    }
-                  }
-              }
-            }
           }
           top *= f;
           grow = top > ref + kRescale;
@@ -472,9 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnPar
   if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool kScores>
+template <int D>
 cudaError_t launch(const AttnParams& p, int blocks, cudaStream_t stream) {
-  const auto kernel = zl_kv4_chunk_kernel<D, kScores>;
+  const auto kernel = zl_kv4_chunk_kernel<D>;
   static PerDeviceOnce once;
   const cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem); });
   if (e != cudaSuccess) return e;
@@ -483,9 +466,8 @@ cudaError_t launch(const AttnParams& p, int blocks, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_kv4_chunk(int head_dim, bool scores, const AttnParams& p, int blocks, cudaStream_t stream) {
-  if (head_dim == 128) return scores ? launch<128, true>(p, blocks, stream) : launch<128, false>(p, blocks, stream);
-  return scores ? launch<64, true>(p, blocks, stream) : launch<64, false>(p, blocks, stream);
+cudaError_t launch_kv4_chunk(int head_dim, const AttnParams& p, int blocks, cudaStream_t stream) {
+  return head_dim == 128 ? launch<128>(p, blocks, stream) : launch<64>(p, blocks, stream);
 }
 
 }  // namespace zl

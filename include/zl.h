@@ -600,7 +600,8 @@ ZL_API zl_status zl_kv4_attn_workspace(const zl_kv4_cache* cache, int32_t n_q_he
  *   NULL and in the new tokens' slots.  The two may be the same buffer.  decay: finite.
  *   scale: positive, normal.  workspace: zl_kv4_attn_workspace bytes (no call may share it with one that may run at the same time).
  * P is rounded to fp16 (its row's running maximum is 1 to 256); sums are fp32.  Results repeat bit for bit.
- * For prompts (more than some 64 rows, tokens x group, a key head) zl_kv4_read and zl_causal_attn_fwd are faster. */
+ * workspace bytes for max_new tokens, or with weights, serve fewer tokens and calls without weights of the same cache.
+ * For prompts (more than some 300 rows, tokens x group, a key head) zl_kv4_read and zl_causal_attn_fwd are faster. */
 ZL_API zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, int64_t q_stride, int64_t n_tokens,
                                  int32_t n_q_heads, const int32_t* starts, int32_t max_new, void* o, float* lse,
                                  const float* weights, float* weights_out, float decay, void* workspace, float scale,

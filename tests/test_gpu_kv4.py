@@ -393,6 +393,88 @@ def test_attention_leaves_out_bad_pages_and_says_so():
     assert zl.zl_kv4_get_device_status(c) == 0 and (o[1] == 0).all() and (lse[1] == -np.inf).all()
 
 
+# Many rows: from 33 rows a key head on, and rows x key heads x slots that the table has room for of 2^22 on, another kernel runs.
+def many(lens, heads, d, page, seed, rows):
+    """A cache whose table is wide enough for it (entries past a sequence's slots are not read)."""
+    width = -(-2 ** 22 // (rows * heads * len(lens) * page))
+    return make_cache(lens, heads, d, page, seed, extra_pages=max(0, width - max([-(-n // page) for n in lens] + [1])))
+
+
+@pytest.mark.parametrize("hq,heads,d,new", [
+    (8, 2, 64, [9, 1, 0, 16, 3, 2, 16, 5]), (7, 1, 128, [5, 3, 1, 0, 2, 4, 5, 1]), (3, 3, 128, [33, 1, 40, 7, 0, 2, 39, 31]),
+    (32, 2, 64, [3, 0, 1, 2, 3, 1, 2, 3]), (6, 2, 128, [43, 1, 86, 20, 85, 3, 70, 128]), (128, 1, 64, [1] * 8), (100, 1, 128, [2] * 8)])
+@pytest.mark.parametrize("page", [16, 128])
+def test_attention_of_many_rows(hq, heads, d, new, page):
+    lens = [300, 1, 128, 127, 0, 129, 700, 255]
+    c, data, pages = many(lens, heads, d, page, 40, hq // heads * max(new))
+    run_attention(c, data, pages, lens, new, hq, 41, no_starts=new == [1] * 8)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [17, 64])
+def test_attention_of_many_rows_of_one_long_sequence(d, new):
+    import torch
+    lens = [20011]  # cut between blocks; with 64 tokens in two tiles of rows
+    c, data, pages = many(lens, 2, d, 64, 42, 4 * new)
+    a = run_attention(c, data, pages, lens, [new], 8, 43)
+    b = run_attention(c, data, pages, lens, [new], 8, 43)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])  # bit for bit
+
+
+def test_attention_of_many_rows_of_many_sequences():
+    rng = np.random.default_rng(44)
+    lens, new = [int(x) for x in rng.integers(0, 400, 300)], [int(x) for x in rng.integers(0, 12, 300)]
+    c, data, pages = many(lens, 1, 64, 16, 45, 4 * 11)
+    run_attention(c, data, pages, lens, new, 4, 46)
+
+
+@pytest.mark.parametrize("size", [1e-30, 30.0, 1e4])
+def test_attention_of_many_rows_and_queries_of_any_size(size):
+    lens, new = [50, 333, 4], [20, 7, 10]
+    c, data, pages = many(lens, 2, 128, 16, 47, 40)
+    run_attention(c, data, pages, lens, new, 4, 48, size=size)
+
+
+def test_attention_of_many_rows_leaves_out_bad_pages_and_says_so():
+    import torch
+    lens, new = [300, 64, 140], [12, 9, 3]
+    c, data, pages = many(lens, 2, 64, 16, 49, 48)
+    pages[0, 2], pages[0, 8:16], pages[1, :], pages[2, 1] = -5, 10 ** 6, 10 ** 6, data.shape[0]
+    c.pages.copy_(torch.from_numpy(pages).int())
+    o, lse = run_attention(c, data, pages, lens, new, 8, 50)
+    assert (o[13:22] == 0).all() and (lse[13:22] == -np.inf).all()  # the second sequence, which has no page at all
+
+
+def test_attention_of_many_rows_captured_and_replayed_with_other_lengths():
+    import torch
+    lens, new = [513, 200, 130], [16, 11, 16]
+    c, data, pages = many(lens, 2, 128, 64, 51, 64)
+    starts, ds = starts_of(new)
+    q = torch.randn(43, 8, 128, generator=torch.Generator().manual_seed(52)).bfloat16().cuda()
+    o, lse = torch.empty_like(q), torch.empty(43, 8).cuda()
+    ws = torch.empty(zl.zl_kv4_attn_workspace_bytes(c, 8, 16), dtype=torch.uint8).cuda()
+    zl.zl_kv4_attn_fwd(c, q, o, lse, ws, 0.1, ds, 16)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        zl.zl_kv4_attn_fwd(c, q, o, lse, ws, 0.1, ds, 16)
+    for now in (lens, [257, 129, 16], [16, 0, 128]):
+        c.lens.copy_(torch.tensor(now, dtype=torch.int32))
+        graph.replay()
+        want, tol = reference(f64(q), data, pages, now, starts, 0.1)
+        within(f64(o), want["o"], tol["o"], "o")
+        within(f64(lse), want["lse"], tol["lse"], "lse")
+
+
+def test_workspace_of_more_tokens_or_with_weights_serves_fewer_and_without():
+    lens, new = [300, 64], [12, 9]
+    c, data, pages = many(lens, 2, 64, 16, 53, 48)
+    for more, weights in ((16, False), (12, True), (2000, False)):
+        assert zl.zl_kv4_attn_workspace_bytes(c, 8, more, weights) >= zl.zl_kv4_attn_workspace_bytes(c, 8, 12)
+    for most in (1, 4, 8, 9, 16):
+        assert zl.zl_kv4_attn_workspace_bytes(c, 8, most) <= zl.zl_kv4_attn_workspace_bytes(c, 8, most + 1)
+
+
 def test_bad_lengths_and_starts_are_left_out():
     import torch
     c, data, pages = make_cache([32, 32, 32], 1, 64, 16, 28)
