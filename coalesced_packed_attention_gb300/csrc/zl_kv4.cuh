@@ -30,6 +30,7 @@ inline zl_status kv4_check(const zl_kv4_cache* c, Kv4* out) {
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256) return ZL_ERR_UNSUPPORTED;
   if (c->n_seqs < 0 || c->n_seqs > (1 << 20) || c->n_kv_heads < 1 || c->n_kv_heads > 1024 || c->max_pages < 0 ||
       c->n_pages < 0 || c->n_pages > INT32_MAX || (int64_t)c->max_pages * c->page >= 1 << 30 ||
+      (int64_t)c->max_pages * (c->page / 16) * c->n_kv_heads > INT32_MAX ||  // a sequence's tiles are numbered
       c->n_pages * c->n_kv_heads * (c->page / 16) >= 1 << 28)  // of 1152 bytes and more: 309 GB
     return ZL_ERR_INVALID_ARG;
   if (c->n_seqs > 0 && (!c->lens || (c->max_pages > 0 && !c->pages) || (c->n_pages > 0 && !c->data))) return ZL_ERR_INVALID_ARG;

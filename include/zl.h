@@ -553,7 +553,7 @@ typedef struct {
   int32_t n_kv_heads;   /* 1 .. 1024 */
   int32_t head_dim;     /* 64 or 128 */
   int32_t page;         /* slots a page: 16, 32, 64, 128 or 256 */
-  int32_t max_pages;    /* pages a sequence may have: the width of `pages`; max_pages * page < 2^30 */
+  int32_t max_pages;    /* pages a sequence may have: the width of `pages`; max_pages * page < 2^30, n_kv_heads * max_pages * page < 2^35 */
   int64_t n_pages;      /* pages of `data` */
   void* data;           /* [n_pages][n_kv_heads][page / 16][18 d], 16-byte aligned */
   const int32_t* pages; /* device [n_seqs][max_pages]; entries past a sequence's slots are not read */
@@ -593,7 +593,7 @@ ZL_API zl_status zl_kv4_attn_workspace(const zl_kv4_cache* cache, int32_t n_q_he
 /* Attention of the newest tokens over the cache, which holds their own keys and values already: with n tokens
  * [starts[b], starts[b + 1]) (as zl_kv4_write; at most max_new of a sequence) query i sees slots j <= lens[b] - n + i.
  *   q: bf16 [n_tokens, n_q_heads, d] with a token stride; n_q_heads a multiple of n_kv_heads, query head h reads key
- *   head h / (n_q_heads / n_kv_heads).  o: bf16 [n_tokens, n_q_heads, d] contiguous; lse: fp32 [n_tokens, n_q_heads]; 0 and
+ *   head h / group, group = n_q_heads / n_kv_heads <= 128 and max_new * group <= 8192 (ZL_ERR_UNSUPPORTED past them).  o: bf16 [n_tokens, n_q_heads, d] contiguous; lse: fp32 [n_tokens, n_q_heads]; 0 and
  *   -inf for a query that sees no slot.  Rows of no sequence are left as they were.
  *   weights, weights_out: fp32 [n_seqs, n_kv_heads, max_pages * page] or NULL.  weights_out[slot] = decay * weights[slot] + the sum of the
  *   slot's softmax weights over the new tokens and the group's heads, for slots below lens[b]; weights counts as 0 where it is

@@ -104,7 +104,7 @@ def cache(**change):
 BAD_CACHES = [(dict(head_dim=96), zl.ZL_ERR_UNSUPPORTED), (dict(page=48), zl.ZL_ERR_UNSUPPORTED), (dict(page=0), zl.ZL_ERR_UNSUPPORTED),
               (dict(n_seqs=-1), zl.ZL_ERR_INVALID_ARG), (dict(n_kv_heads=0), zl.ZL_ERR_INVALID_ARG),
               (dict(n_kv_heads=1025), zl.ZL_ERR_INVALID_ARG), (dict(max_pages=-1), zl.ZL_ERR_INVALID_ARG),
-              (dict(max_pages=1 << 27), zl.ZL_ERR_INVALID_ARG), (dict(n_pages=-1), zl.ZL_ERR_INVALID_ARG),
+              (dict(max_pages=1 << 27), zl.ZL_ERR_INVALID_ARG), (dict(max_pages=1 << 25, n_kv_heads=64), zl.ZL_ERR_INVALID_ARG), (dict(n_pages=-1), zl.ZL_ERR_INVALID_ARG),
               (dict(n_pages=1 << 31), zl.ZL_ERR_INVALID_ARG), (dict(data=0), zl.ZL_ERR_INVALID_ARG),
               (dict(pages=0), zl.ZL_ERR_INVALID_ARG), (dict(lens=0), zl.ZL_ERR_INVALID_ARG), (dict(data=0x1008), zl.ZL_ERR_ALIGN),
               (dict(pages=0x2002), zl.ZL_ERR_ALIGN), (dict(lens=0x3001), zl.ZL_ERR_ALIGN), (dict(status=0x4002), zl.ZL_ERR_ALIGN)]
