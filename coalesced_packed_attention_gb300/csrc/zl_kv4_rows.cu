@@ -7,7 +7,8 @@
 // the border, where the conversion's own ties to even decide.  (IEEE divisions took two thirds of the time.)
 // Out: code * s has six bits at most, exact in fp16 and bf16.
 // Both move bytes: a thread takes 8 channels (16 bytes of bf16, 4 of codes), two threads share a scale, and has several
-// loads under way.
+// loads under way.  Measured at 8 heads, d = 128: 14 336 tokens in 21 us (75 MB, 3.6 TB/s: the arithmetic of the codes and one wave of
+// blocks), 4 x 16 384 slots out in 58 us (344 MB, 5.9 TB/s, 0.89 of a copy).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
