@@ -99,6 +99,21 @@ __device__ __forceinline__ uint32_t kv4_mul(uint32_t a, uint32_t b) {
 // A scale's bits are those of an fp16 number from its exponent on: two of them, low and high half.
 __device__ __forceinline__ uint32_t kv4_scale2(uint32_t lo, uint32_t hi) { return (lo << 7) | (hi << 23); }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the cluster; what each wrote before it, to shared or global memory, the others see after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Exclusive prefix sum over a block's threads, and the total; warp_sums: one number a warp in shared memory.
 template <int kThreads>
 __device__ __forceinline__ int64_t kv4_scan(int64_t mine, int64_t* total, int64_t* warp_sums) {

@@ -16,7 +16,8 @@
 // Every warp streams runs of 32 slots of its own through shared memory (bulk copies, a ring of stages, no other warp in
 // between); 4 warps of a block share a (sequence, key head, row tile) and join at its end.
 // The slots of all items lie in a row that is dealt out evenly over the blocks, whatever the lengths: a block writes what
-// it holds alone; items cut between blocks leave parts (O, max, sum) that a second launch joins in order.
+// it holds alone; items cut between blocks leave parts (O, max, sum) that a second launch joins in order.  Short items go to a block
+// or a cluster of blocks each instead, which joins them itself.
 // Measured, 32/8 heads, d = 128: 64 single tokens behind 1 to 16 384 slots 85 us (436 MB, 5.1 TB/s; the loads without arithmetic
 // 69 us), one behind 131 071 slots 35 us and 4 for its join (151 MB).  What is above the loads is arithmetic that they
 // do not hide: some 595 instructions for 32 slots, 256 of them conversions and products at half rate.
@@ -38,6 +39,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;          // slots of a unit: two tiles
 constexpr int kItemCost = 8;       // units: 64 single tokens over 15 to 16 384 slots each took 98 us at 4, 87 at 8 and 12, 90 at 20
+constexpr int kMaxCluster = 8;
 constexpr int kMaxBlocks = 640;    // blocks of a launch at most: what the workspace has room for
 constexpr uint32_t kTwice = 0x00800080u;  // a scale's bits times this: the scale in both halves, by the multiplier, which has time
 
@@ -69,6 +71,26 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// Numbers of the same place in another block of the cluster.
+__device__ __forceinline__ uint32_t peer_address(const void* mine, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float2 peer2(const float2* mine, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer_address(mine, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer4(const float* mine, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer_address(mine, rank))
+               : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- the kernel
 template <int D, int NT>
 struct Shape {
@@ -82,7 +104,9 @@ struct Shape {
   static constexpr int kBlocks = NT == 1 || D == 64 ? 4 : 2;  // an SM's, by registers and shared memory
 };
 
-template <int D, int NT, bool kScores>
+// kCluster: a cluster takes one item, each of its blocks an equal part of the units, and joins it through its blocks' shared memory: no
+// second launch.  Else the items' units are dealt out evenly.  (The rule between them: cluster_of.)
+template <int D, int NT, bool kScores, bool kCluster>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_kernel(const AttnParams p) {
   using S = Shape<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -90,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
   __shared__ int64_t warp_sums[kWarps];
   __shared__ int64_t s_before;
   __shared__ int s_seq;
+  __shared__ float2 block_ml[kCluster ? S::kRows : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   float* join = reinterpret_cast<float*>(smem + S::kRing);
   float2* join_ml = reinterpret_cast<float2*>(smem + S::kRing + S::kJoin);
@@ -100,8 +125,22 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
 
   using W = Walk<S::kRows, kUnit, kItemCost>;
   W cons;
-  int64_t each;
-  if (!first_segment_of<kThreads, kWarps + kItemCost>(p, warp_sums, &s_before, &s_seq, cons, &each)) return;
+  int64_t each = 0;
+  const uint32_t cluster = kCluster ? cluster_size() : 1;
+  if constexpr (kCluster) {
+    const int item = blockIdx.x / cluster, pair = item / p.max_tiles;
+    cons.tile = item - pair * p.max_tiles;
+    cons.seq = pair / p.c.heads;
+    cons.head = pair - cons.seq * p.c.heads;
+    cons.left = 0;
+    cons.load(p);
+    if (cons.tile >= cons.row_tiles) return;  // all of the cluster
+    const int per = (cons.chunks + (int)cluster - 1) / (int)cluster;
+    cons.a = min(cons.chunks, per * (int)cluster_rank());
+    cons.e = min(cons.chunks, cons.a + per);
+  } else if (!first_segment_of<kThreads, kWarps + kItemCost>(p, warp_sums, &s_before, &s_seq, cons, &each)) {
+    return;
+  }
 
   // Loading: a warp looks up the places of its next 32 units at once, one a lane, and issues them one by one.
   W prod = cons;
@@ -168,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
   const int va_at = 8 * D + ka * (D / 2) + g * (D / 16), vb_at = 8 * D + kb * (D / 2) + g * (D / 16);
   const int vsa_at = 17 * D + ka * (D / 16) + g * D / 128, vsb_at = 17 * D + kb * (D / 16) + g * D / 128;
   bool first_segment = true, alive = true;
-  for (; !cons.done(); cons.next(p)) {
+  for (bool more = kCluster || !cons.done(); more; cons.next(p), more = !cons.done()) {  // a cluster's block joins with no units, too
     const int head = cons.head, row0 = cons.tile * S::kRows;
     const int rows = cons.n * p.group;
     // queries: lane (g, t) holds quarter t of the channels of row g of every 8
@@ -419,10 +458,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
           *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(acc[i][j][y], acc[i][j][y + 2], acc[i + 1][j][y], acc[i + 1][j][y + 2]);
       }
     __syncthreads();
-    const bool whole = cons.a == 0 && cons.e == cons.chunks;
+    const bool whole = kCluster || (cons.a == 0 && cons.e == cons.chunks);
     const int part = 2 * blockIdx.x + (first_segment ? 0 : 1);
     constexpr int kLanes = D / 4;  // threads of a row
     const int c4 = threadIdx.x % kLanes;
+    auto store = [&](int r, float m, float l, const float4& o) {
+      const int tok = (row0 + r) / p.group;
+      const int64_t at = (int64_t)(cons.first + tok) * p.q_heads + head * p.group + (row0 + r - tok * p.group);
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      if (c4 == 0) p.lse[at] = natural_lse(m, l);
+    };
     for (int r = threadIdx.x / kLanes; r < S::kRows && row0 + r < rows; r += kThreads / kLanes) {
       float m = kLow, l = 0.f;
 #pragma unroll
@@ -436,18 +482,49 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         l = fmaf(ml.y, k, l);
         o = make_float4(fmaf(x.x, k, o.x), fmaf(x.y, k, o.y), fmaf(x.z, k, o.z), fmaf(x.w, k, o.w));
       }
-      if (whole) {
-        const int tok = (row0 + r) / p.group;
-        const int64_t at = (int64_t)(cons.first + tok) * p.q_heads + head * p.group + (row0 + r - tok * p.group);
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (c4 == 0) p.lse[at] = natural_lse(m, l);
+      if (kCluster && cluster > 1) {  // the first warp's place is this thread's own
+        *reinterpret_cast<float4*>(join + r * S::kPitch + 4 * c4) = o;
+        if (c4 == 0) block_ml[r] = make_float2(m, l);
+      } else if (whole) {
+        store(r, m, l, o);
       } else {
         *reinterpret_cast<float4*>(p.part_o + ((int64_t)part * S::kRows + r) * D + 4 * c4) = o;
         if (c4 == 0) p.part_ml[(int64_t)part * S::kRows + r] = make_float2(m, l);
       }
     }
-    if (threadIdx.x == 0) describe(p, cons, part, row0, rows, each);
+    if constexpr (kCluster) {
+      if (cluster > 1) {
+        __syncwarp();
+        cluster_sync();
+        // the blocks' parts become one, in order; a row's are put together by one block
+        for (int r = cluster_rank() + cluster * (threadIdx.x / kLanes); r < S::kRows && row0 + r < rows; r += cluster * (kThreads / kLanes)) {
+          float2 ml[kMaxCluster];
+          float4 x[kMaxCluster];
+#pragma unroll
+          for (uint32_t i = 0; i < kMaxCluster; ++i) {
+            const uint32_t from = min(i, cluster - 1);
+            ml[i] = peer2(&block_ml[r], from);
+            x[i] = peer4(join + r * S::kPitch + 4 * c4, from);
+          }
+          float m = kLow, l = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (uint32_t i = 0; i < kMaxCluster; ++i) m = fmaxf(m, ml[i].x);
+#pragma unroll
+          for (uint32_t i = 0; i < kMaxCluster; ++i) {
+            if (i >= cluster) break;
+            const float k = ex2(ml[i].x - m);
+            l = fmaf(ml[i].y, k, l);
+            o = make_float4(fmaf(x[i].x, k, o.x), fmaf(x[i].y, k, o.y), fmaf(x[i].z, k, o.z), fmaf(x[i].w, k, o.w));
+          }
+          store(r, m, l, o);
+        }
+        __syncwarp();
+        cluster_sync();  // no block may end while another reads its shared memory
+      }
+    } else if (threadIdx.x == 0) {
+      describe(p, cons, part, row0, rows, each);
+    }
     first_segment = false;
     __syncthreads();  // the join's buffer has been read
   }
@@ -600,12 +677,12 @@ int row_columns(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 // The tensor-core kernel (zl_kv4_chunk.cu) instead: for more than two passes' rows over slots enough to pay for its start.
 // Measured (us; here / there): 32, 48, 64, 128 rows over 16 x 4096 slots of 8 key heads, d = 128: 52 / 56, 71 / 58, 88 / 59, 165 / 67;
-// d = 64: 34 / 46, 44 / 46, 75 / 48.  Few slots: 64 rows over 4 x 1000 of 4 heads 13 / 20, 4 x 4000 20 / 22, 8 x 1000 of 8 heads
-// 22 / 21; 128 rows over 4 x 2000 of 4 heads 21 / 26, 4 x 4000 29 / 28.  So by the product, of the slots that the table has
-// room for, as lengths lie on the device.  Not with weights: its scores leave a row a thread, which costs what it gains
+// d = 64: 34 / 46, 44 / 46, 75 / 48.  Few slots: 64 rows over 4 x 1000 of 4 heads 10 / 20, 4 x 4000 17 / 22, 8 x 1000 of 8 heads
+// 16 / 21, 8 x 2000 31 / 27; 128 rows over 4 x 2000 of 4 heads 17 / 26, 4 x 4000 29 / 28.  So by the product, of the slots that the
+// table has room for, as lengths lie on the device.  Not with weights: its scores leave a row a thread, which costs what it gains
 // (16 x 2000 slots of 4 heads, 64 and 128 rows: 44 / 48, 76 / 71 at d = 128, 36 / 42, 61 / 62 at d = 64).
 constexpr int64_t kChunkFrom = 33;
-constexpr int64_t kChunkWork = int64_t{1} << 22;  // rows x slots x key heads
+constexpr int64_t kChunkWork = int64_t{3} << 21;  // rows x slots x key heads
 bool by_chunks(const zl_kv4_cache& c, int64_t rows, bool weights) {
   return !weights && rows >= kChunkFrom && rows * c.n_seqs * c.n_kv_heads >= kChunkWork / std::max(1, c.max_pages * c.page);
 }
@@ -648,10 +725,47 @@ cudaError_t launch_joined(AttnParams& p, int blocks, cudaStream_t stream, Launch
   return launch_overlapped(zl_kv4_join_kernel<D, kRows, false>, dim3(cuts, kRows / 8), 256, 0, stream, p);
 }
 
+// Blocks of an item's cluster (2^n up to 8, as far as all are resident), or 0: the dealt-out form.  Clusters save its second launch
+// and its search for a block's run, but let a long item wait for its own blocks alone: for slots (that the table has room for) of which a
+// warp gets 8 units at most, or 5 where dealing out would have twice as many blocks.  Measured (us, dealt out / clusters; d = 128, groups of
+// 4, single tokens): 8 items of 300, 2000, 4000, 8000 slots 10.0 / 5.9, 10.0 / 7.1, 10.7 / 8.7, 11.4 / 12.3; 64 items 11.2 / 7.0, 14.5 / 10.0,
+// 15.5 / 13.7, 24.1 / 22.6; 256 items of 300, 1000, 8000 slots 12.9 / 8.3, 16.3 / 13.1, 59.6 / 62.2; one item of 4000, 8000 slots 9.6 / 8.5,
+// 9.4 / 12.0.  Single row tiles go a block each past the resident ones, too: 1024 items of 300, 1000 slots 21.9 / 18.0, 40.7 / 37.1, of 1 to
+// 1024 slots 19.0 / 17.9 (row tiles of a maximum that most sequences may not reach would be blocks without work).
+int cluster_of(int64_t items, int64_t slots, int tiles, int blocks) {
+  int c = kMaxCluster;
+  while (c > 1 && items * c > blocks) c /= 2;
+  const int64_t units = items * 2 * kMaxCluster <= blocks ? 5 : 8;  // of a warp
+  return (items <= blocks || (tiles == 1 && items <= INT32_MAX)) && slots <= c * units * kWarps * kUnit ? c : 0;
+}
+
+template <int D, int NT, bool kScores>
+cudaError_t launch_clusters(const AttnParams& p, int cluster, cudaStream_t stream) {
+  using S = Shape<D, NT>;
+  const auto kernel = zl_kv4_attn_kernel<D, NT, kScores, true>;
+  static PerDeviceOnce once;
+  const cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem); });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.c.n_seqs * p.c.heads * p.max_tiles * cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <int D, int NT, bool kScores>
 cudaError_t launch_attn(AttnParams& p, int sms, cudaStream_t stream) {
   using S = Shape<D, NT>;
-  const auto kernel = zl_kv4_attn_kernel<D, NT, kScores>;
+  const auto kernel = zl_kv4_attn_kernel<D, NT, kScores, false>;
   static PerDeviceInt resident;
   int per_sm = 0;
   cudaError_t e = resident.get(&per_sm, [&](int, int* v) {
@@ -662,6 +776,9 @@ cudaError_t launch_attn(AttnParams& p, int sms, cudaStream_t stream) {
   });
   if (e != cudaSuccess) return e;
   const int blocks = sms * per_sm < kMaxBlocks ? sms * per_sm : kMaxBlocks;
+  p.max_tiles = (p.max_new * p.group + S::kRows - 1) / S::kRows;
+  if (const int cluster = cluster_of((int64_t)p.c.n_seqs * p.c.heads * p.max_tiles, (int64_t)p.c.max_pages << p.c.page_shift, p.max_tiles, blocks))
+    return launch_clusters<D, NT, kScores>(p, cluster, stream);
   return launch_joined<D, S::kRows>(p, blocks, stream, [&] { return launch_overlapped(kernel, blocks, kThreads, S::kSmem, stream, p); });
 }
 template <int D, bool kScores>

@@ -48,20 +48,6 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
   return w == w ? r : 0;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// Every thread of the cluster; what each wrote before it, to shared or global memory, the others see after it.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // An int of the same variable in another block of the cluster.
 __device__ __forceinline__ int peer(const int* mine, uint32_t rank) {
   uint32_t a;

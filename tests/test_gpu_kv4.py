@@ -318,6 +318,28 @@ def test_attention_several_tokens(hq, heads, d, weights):
     run_attention(c, data, pages, lens, new, hq, 11, weights=weights, decay=0.5)
 
 
+# Tables of up to 8192 slots and few items: a cluster of blocks takes an item.  Wider ones (entries past a sequence's slots are not
+# read): units dealt out.
+@pytest.mark.parametrize("hq,heads,d", SHAPES)
+@pytest.mark.parametrize("weights", [False, True])
+def test_attention_dealt_out(hq, heads, d, weights):
+    lens, new = [5, 40, 16, 300, 0, 3, 700, 1500], [3, 3, 0, 2, 0, 1, 1, 1]
+    c, data, pages = make_cache(lens, heads, d, 256, 54, extra_pages=33)
+    assert c.slots > 8192
+    run_attention(c, data, pages, lens, new, hq, 55, weights=weights, decay=0.5)
+
+
+@pytest.mark.parametrize("hq,heads,d,n", [(4, 1, 128, 3), (8, 2, 64, 40), (16, 1, 64, 100), (9, 3, 128, 80), (2, 2, 128, 200), (6, 3, 64, 500)])
+def test_attention_by_clusters_of_every_size(hq, heads, d, n):
+    rng = np.random.default_rng(56)  # 8, 4 and 2 blocks an item, one, one for more items than there are blocks
+    lens, new = [int(x) for x in rng.integers(0, 900, n)], [int(x) for x in rng.integers(0, 3, n)]
+    c, data, pages = make_cache(lens, heads, d, 64, 57)
+    a = run_attention(c, data, pages, lens, new, hq, 58, weights=n % 2 == 1)
+    b = run_attention(c, data, pages, lens, new, hq, 58, weights=n % 2 == 1)
+    import torch
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])  # bit for bit
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_more_queries_than_slots_and_none(d):
     lens, new = [0, 2, 0, 1], [2, 7, 1, 3]
@@ -393,10 +415,10 @@ def test_attention_leaves_out_bad_pages_and_says_so():
     assert zl.zl_kv4_get_device_status(c) == 0 and (o[1] == 0).all() and (lse[1] == -np.inf).all()
 
 
-# Many rows: from 33 rows a key head on, and rows x key heads x slots that the table has room for of 2^22 on, another kernel runs.
+# Many rows: from 33 rows a key head on, and rows x key heads x slots that the table has room for of 3 x 2^21 on, another kernel runs.
 def many(lens, heads, d, page, seed, rows):
     """A cache whose table is wide enough for it (entries past a sequence's slots are not read)."""
-    width = -(-2 ** 22 // (rows * heads * len(lens) * page))
+    width = -(-3 * 2 ** 21 // (rows * heads * len(lens) * page))
     return make_cache(lens, heads, d, page, seed, extra_pages=max(0, width - max([-(-n // page) for n in lens] + [1])))
 
 
