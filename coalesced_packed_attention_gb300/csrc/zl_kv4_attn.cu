@@ -77,6 +77,11 @@ __device__ __forceinline__ uint32_t peer_address(const void* mine, uint32_t rank
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
   return a;
 }
+__device__ __forceinline__ float peer1(const float* mine, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_address(mine, rank)) : "memory");
+  return v;
+}
 __device__ __forceinline__ float2 peer2(const float2* mine, uint32_t rank) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer_address(mine, rank)) : "memory");
@@ -89,6 +94,30 @@ __device__ __forceinline__ float4 peer4(const float* mine, uint32_t rank) {
                : "r"(peer_address(mine, rank))
                : "memory");
   return v;
+}
+
+// weights_out of slots [s0, s1) of an item whose rows are all this block's: scores that it has just written, four slots a thread.
+__device__ __forceinline__ void add_weights(const AttnParams& p, int seq, int head, int m, int n, int rows, int s0, int s1, const float* row_lse) {
+  const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift, pair = (int64_t)seq * p.c.heads + head;
+  const float* x = p.scores + pair * p.score_rows * slots;
+  for (int s = s0 + 4 * threadIdx.x; s < s1; s += 4 * kThreads) {
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = p.w_in && s + i < m - n ? p.decay * p.w_in[pair * slots + s + i] : 0.f;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      const float4 v = *reinterpret_cast<const float4*>(x + r * slots + s);  // slots of the table past the last one are the workspace's, too
+      const float l = row_lse[r];
+      if (l == INFINITY) continue;
+      w[0] += ex2(v.x - l);
+      w[1] += ex2(v.y - l);
+      w[2] += ex2(v.z - l);
+      w[3] += ex2(v.w - l);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (s + i < s1) p.w_out[pair * slots + s + i] = w[i];
+  }
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -115,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
   __shared__ int64_t s_before;
   __shared__ int s_seq;
   __shared__ float2 block_ml[kCluster ? S::kRows : 1];
+  __shared__ float row_lse[kCluster && kScores ? S::kRows : 1];  // of the rows that this block put together, then of all; base 2
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   float* join = reinterpret_cast<float*>(smem + S::kRing);
   float2* join_ml = reinterpret_cast<float2*>(smem + S::kRing + S::kJoin);
@@ -134,7 +164,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
     cons.head = pair - cons.seq * p.c.heads;
     cons.left = 0;
     cons.load(p);
-    if (cons.tile >= cons.row_tiles) return;  // all of the cluster
+    if (cons.tile >= cons.row_tiles) {  // all of the cluster
+      if (kScores && p.own_weights) {
+        const int64_t at = (int64_t)item * ((int64_t)p.c.max_pages << p.c.page_shift);
+        for (int s = cluster_rank() * kThreads + threadIdx.x; s < cons.m; s += cluster * kThreads) p.w_out[at + s] = p.w_in ? p.decay * p.w_in[at + s] : 0.f;
+      }
+      return;
+    }
     const int per = (cons.chunks + (int)cluster - 1) / (int)cluster;
     cons.a = min(cons.chunks, per * (int)cluster_rank());
     cons.e = min(cons.chunks, cons.a + per);
@@ -467,7 +503,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
       const int64_t at = (int64_t)(cons.first + tok) * p.q_heads + head * p.group + (row0 + r - tok * p.group);
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-      if (c4 == 0) p.lse[at] = natural_lse(m, l);
+      if (c4 == 0) {
+        const float lse = natural_lse(m, l);
+        p.lse[at] = lse;
+        if constexpr (kCluster && kScores) row_lse[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;  // rows that see nothing: 2^(-inf) each
+      }
     };
     for (int r = threadIdx.x / kLanes; r < S::kRows && row0 + r < rows; r += kThreads / kLanes) {
       float m = kLow, l = 0.f;
@@ -522,6 +562,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         __syncwarp();
         cluster_sync();  // no block may end while another reads its shared memory
       }
+      if constexpr (kScores)
+        if (p.own_weights) {
+          if (cluster > 1) {
+            const int r = threadIdx.x;
+            float mine = 0.f;
+            if (r < S::kRows) mine = peer1(&row_lse[r], r % cluster);
+            cluster_sync();
+            if (r < S::kRows) row_lse[r] = mine;
+          }
+          __syncthreads();
+          add_weights(p, cons.seq, head, cons.m, cons.n, rows, cons.a * kUnit, min(cons.m, cons.e * kUnit), row_lse);
+        }
     } else if (threadIdx.x == 0) {
       describe(p, cons, part, row0, rows, each);
     }
@@ -777,8 +829,12 @@ cudaError_t launch_attn(AttnParams& p, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int blocks = sms * per_sm < kMaxBlocks ? sms * per_sm : kMaxBlocks;
   p.max_tiles = (p.max_new * p.group + S::kRows - 1) / S::kRows;
-  if (const int cluster = cluster_of((int64_t)p.c.n_seqs * p.c.heads * p.max_tiles, (int64_t)p.c.max_pages << p.c.page_shift, p.max_tiles, blocks))
+  if (const int cluster = cluster_of((int64_t)p.c.n_seqs * p.c.heads * p.max_tiles, (int64_t)p.c.max_pages << p.c.page_shift, p.max_tiles, blocks)) {
+    // all of an item's rows in one cluster: no launch for the weights either (us, with it / without: 8 items of 1000 slots 8.4 / 7.7, 128 of
+    // 1000 13.3 / 12.0, 512 of 300 13.2 / 11.3)
+    p.own_weights = kScores && p.max_tiles == 1;
     return launch_clusters<D, NT, kScores>(p, cluster, stream);
+  }
   return launch_joined<D, S::kRows>(p, blocks, stream, [&] { return launch_overlapped(kernel, blocks, kThreads, S::kSmem, stream, p); });
 }
 template <int D, bool kScores>
@@ -858,7 +914,7 @@ extern "C" zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, i
     if (cache->head_dim == 128) e = weights_out ? launch_attn<128, true>(p, rows, chunks, sms, st) : launch_attn<128, false>(p, rows, chunks, sms, st);
     else e = weights_out ? launch_attn<64, true>(p, rows, chunks, sms, st) : launch_attn<64, false>(p, rows, chunks, sms, st);
   }
-  if (e == cudaSuccess && weights_out && cache->max_pages > 0) {
+  if (e == cudaSuccess && weights_out && cache->max_pages > 0 && !p.own_weights) {
     const int64_t slots = (int64_t)cache->max_pages * cache->page;
     const bool few = l.score_rows <= 8;
     const int block_slots = kWeightThreads * (few ? 4 : 1);

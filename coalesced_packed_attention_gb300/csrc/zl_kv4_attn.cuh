@@ -36,6 +36,7 @@ struct AttnParams {
   float decay;
   float scale_log2;
   int32_t group, q_heads, max_new, score_rows;
+  int32_t own_weights;  // the attention kernel adds them up itself
 };
 
 // log of a sum l of 2^(score - m); -inf for an empty one, NaN stays.
