@@ -340,6 +340,15 @@ def test_attention_by_clusters_of_every_size(hq, heads, d, n):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])  # bit for bit
 
 
+@pytest.mark.parametrize("hq,heads,d,n", [(4, 1, 128, 30), (8, 2, 64, 60), (16, 1, 128, 200), (6, 3, 64, 300)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_weights_by_clusters_of_every_size(hq, heads, d, n, in_place):
+    rng = np.random.default_rng(59)  # sequences without new tokens among them, whose sums decay all the same
+    lens, new = [int(x) for x in rng.integers(0, 500, n)], [int(x) for x in rng.integers(0, 2 if hq > 8 else 3, n)]
+    c, data, pages = make_cache(lens, heads, d, 16, 60)
+    run_attention(c, data, pages, lens, new, hq, 61, weights=True, decay=0.75, in_place=in_place)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_more_queries_than_slots_and_none(d):
     lens, new = [0, 2, 0, 1], [2, 7, 1, 3]
