@@ -839,7 +839,7 @@ cudaError_t launch_attn(AttnParams& p, int sms, cudaStream_t stream) {
 }
 template <int D, bool kScores>
 cudaError_t launch_attn(AttnParams& p, int64_t rows, bool chunks, int sms, cudaStream_t stream) {
-  if (!chunks)
+  if (kScores || !chunks)
     return row_columns(rows) == 1 ? launch_attn<D, 1, kScores>(p, sms, stream) : launch_attn<D, 2, kScores>(p, sms, stream);
   const int blocks = sms < kChunkMaxBlocks ? sms : kChunkMaxBlocks;
   return launch_joined<D, kChunkRows>(p, blocks, stream, [&] { return launch_kv4_chunk(D, p, blocks, stream); });
