@@ -148,8 +148,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   float* join = reinterpret_cast<float*>(smem + S::kRing);
   float2* join_ml = reinterpret_cast<float2*>(smem + S::kRing + S::kJoin);
-  if (threadIdx.x < kWarps * S::kStages) mbar_init(&bars[threadIdx.x], 1);
-  if (threadIdx.x == 0) fence_mbar_init();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps * S::kStages; ++i) mbar_init(&bars[i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();  // every warp loads on barriers of its own, which it may do at once
   let_next_start();
   wait_for_previous();
 
