@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         top[j] = mul2(make_float2(max3(fmaxf(s[0][j][0], s[0][j][2]), s[1][j][0], s[1][j][2]),
                                   max3(fmaxf(s[0][j][1], s[0][j][3]), s[1][j][1], s[1][j][3])),
                       f[j]);
-        const float2 most = add2(ref[j], make_float2(kRescale, kRescale));
+        const float2 most = add2(ref[j], make_float2(lag_of(ref[j].x), lag_of(ref[j].y)));
         grow |= top[j].x > most.x || top[j].y > most.y;
       }
       if (__any_sync(0xffffffffu, grow)) {
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
             m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, x2));
             m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, x2));
           }
-          m = make_float2(fmaxf(m.x, ref[j].x), fmaxf(m.y, ref[j].y));
+          m = make_float2(fmaxf(reference_of(m.x), ref[j].x), fmaxf(reference_of(m.y), ref[j].y));
           const float2 down = make_float2(ex2(ref[j].x - m.x), ex2(ref[j].y - m.y));
           ref[j] = m;
           sum[j] = mul2(sum[j], down);

@@ -6,8 +6,15 @@
 namespace zl {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLow = -1e30f;     // the running maximum of rows that have seen nothing
+constexpr float kLow = -1e30f;     // the reference of rows that have seen nothing
 constexpr float kRescale = 8.f;    // the maximum may lag by 2^8 before the sums are rescaled
+// P = 2^(score - reference) is rounded to fp16, whose smallest number is 2^-24: at a reference of the maximum itself, weights below
+// 2^-25 of it would be lost in O but not in the sum (O too small by up to slots x 2^-25, 3 % at 2^20 slots).  With the reference
+// 2^7 below it P is up to 2^7, with the lag 2^15, of fp16's 2^16, and what is lost lies below 2^-32.  Scores of 2^20 and more keep the room for
+// their own rounding instead.
+constexpr float kBelow = 7.f, kFar = 0x1p20f;
+__device__ __forceinline__ float reference_of(float top) { return fabsf(top) < kFar ? top - kBelow : top; }
+__device__ __forceinline__ float lag_of(float ref) { return fabsf(ref) < kFar ? kBelow + kRescale : kRescale; }
 
 // An item cut between blocks: its first block describes it for the join.
 struct alignas(16) Cut {

@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnPar
               for (int e = 0; e < 32; e += 2) top = max3(top, __uint_as_float(u[c][e]), __uint_as_float(u[c][e + 1]));
           }
           top *= f;
-          grow = top > ref + kRescale;
-          most = fmaxf(ref, top);
+          grow = top > ref + lag_of(ref);
+          most = fmaxf(ref, reference_of(top));
         }
         // O is whole up to the unit before (within the segment; at its end the last one was waited for)
         if (x > seg.a && !(ok = wait(pv_done, (it - 1) & 1))) break;

@@ -599,7 +599,9 @@ ZL_API zl_status zl_kv4_attn_workspace(const zl_kv4_cache* cache, int32_t n_q_he
  *   slot's softmax weights over the new tokens and the group's heads, for slots below lens[b]; weights counts as 0 where it is
  *   NULL and in the new tokens' slots.  The two may be the same buffer.  decay: finite.
  *   scale: positive, normal.  workspace: zl_kv4_attn_workspace bytes (no call may share it with one that may run at the same time).
- * P is rounded to fp16 (its row's running maximum is 1 to 256); sums are fp32.  Results repeat bit for bit.
+ * P is rounded to fp16 (its row's running maximum is 2^7 to 2^15): weights below 2^-32 of a row's largest count as 0 in O, not in
+ * lse or weights_out (below 2^-25 where scores reach 2^20, to base 2, in magnitude; scores have to stay below 2^28).  Sums are fp32.
+ * Results repeat bit for bit.
  * workspace bytes for max_new tokens, or with weights, serve fewer tokens and calls without weights of the same cache.
  * For prompts (more than some 300 rows, tokens x group, a key head) zl_kv4_read and zl_causal_attn_fwd are faster. */
 ZL_API zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, int64_t q_stride, int64_t n_tokens,
