@@ -1095,12 +1095,18 @@ def zl_kv4_get_device_status(cache: Kv4Cache) -> int:
     return s
 
 
-def allocate_kv4_attention(cache: Kv4Cache, n_tokens: int, n_q_heads: int, max_new: int = 1, evicts: bool = False) -> Dict[str, "object"]:
+def allocate_kv4_attention(cache: Kv4Cache, n_tokens: int, n_q_heads: int, max_new: int = 1, evicts: bool = False,
+                           state: Optional[Dict[str, "object"]] = None) -> Dict[str, "object"]:
     """Buffers of qkv_attention_cached for n_tokens new tokens, at most max_new of a sequence; evicts: with the slots'
-    accumulated weights and positions, which belong to the cache's sequences and live as long as they do."""
+    accumulated weights and positions, which belong to the cache's sequences and live as long as they do.  state: buffers
+    that hold them already, for calls of other sizes on the same sequences (a prompt's, which without evicts need no room
+    for its scores)."""
     import torch
     heads, d = cache.token_shape
     device = cache.data.device
+    if state is not None:
+        _dense(state["weights"], "state's weights", torch.float32, cache.slot_shape, cache.device)
+        _dense(state["positions"], "state's positions", torch.int32, cache.slot_shape, cache.device)
     bf = dict(dtype=torch.bfloat16, device=device)
     ws = zl_kv4_attn_workspace_bytes(cache, n_q_heads, max_new, evicts)
     if evicts:
@@ -1109,10 +1115,20 @@ def allocate_kv4_attention(cache: Kv4Cache, n_tokens: int, n_q_heads: int, max_n
            "o": torch.empty(n_tokens, n_q_heads, d, **bf),
            "lse": torch.empty(n_tokens, n_q_heads, dtype=torch.float32, device=device),
            "workspace": torch.empty(max(16, ws), dtype=torch.uint8, device=device)}
-    if evicts:
+    if state is not None:
+        out["weights"], out["positions"] = state["weights"], state["positions"]
+    elif evicts:
         out["weights"] = torch.zeros(cache.slot_shape, dtype=torch.float32, device=device)
         out["positions"] = torch.zeros(cache.slot_shape, dtype=torch.int32, device=device)
     return out
+
+
+def _kv4_zero_new(cache: Kv4Cache, weights, starts):
+    """The new tokens' slots of weights, and those behind them, which are not in use, become 0."""
+    torch = _torch()
+    new = 1 if starts is None else starts[1:] - starts[:-1]
+    slot = torch.arange(cache.slots, dtype=torch.int32, device=weights.device)
+    weights.masked_fill_(slot >= (cache.lens - new)[:, None, None], 0.0)
 
 
 def qkv_attention_cached(cache: Kv4Cache, qkv, positions, table: Optional[RotaryTable], scale: float, bufs: dict, q_weight=None,
@@ -1122,33 +1138,43 @@ def qkv_attention_cached(cache: Kv4Cache, qkv, positions, table: Optional[Rotary
     given and rotated, keys and values into the 4-bit cache, attention of the new tokens over it (bufs["o"],
     bufs["lse"]).  starts, max_new as in zl_kv4_attn_fwd; cache.lens counts the new tokens already.  With keep, sequences
     live on that many slots: the step's softmax weights are added to bufs["weights"] (decay * the sums so far), every
-    head keeps its `keep` slots, and cache.lens becomes no more than that.  One captured graph serves every step."""
+    head keeps its `keep` slots, and cache.lens becomes no more than that.  One captured graph serves every step.
+    Without keep, buffers that hold weights and positions are brought up to date all the same: the new tokens' positions are
+    noted and their slots' weights begin at 0, so that a prompt may enter this way and its steps go on with keep.  (With keep
+    a prompt's rows are attended 16 at a time and every score is kept until the end; keep=cache.slots adds up weights and
+    evicts nothing.)"""
     torch = _torch()
     heads, d = cache.token_shape
     if not isinstance(qkv, torch.Tensor) or qkv.dim() != 3 or qkv.shape[1] <= 2 * heads or qkv.shape[2] != d:
         raise ValueError(f"qkv: expected [tokens, Hq + {2 * heads}, {d}], got {tuple(getattr(qkv, 'shape', ()))}")
-    if keep is not None:
-        if "weights" not in bufs:
-            raise ValueError("keep: needs buffers that were allocated with evicts=True")
-        if not isinstance(positions, torch.Tensor) or positions.numel() != qkv.shape[0]:
-            raise ValueError("keep: needs one position a token")
+    w, at = bufs.get("weights"), bufs.get("positions")
+    if keep is not None and w is None:
+        raise ValueError("keep: needs buffers that were allocated with evicts=True")
+    if w is not None and (not isinstance(positions, torch.Tensor) or positions.numel() != qkv.shape[0]):
+        raise ValueError("buffers with weights: need one position a token")
     hq = qkv.shape[1] - 2 * heads
     q, k, v = qkv[:, :hq], qkv[:, hq:hq + heads], qkv[:, hq + heads:]
     for of_q, of_k, norm in _sides(q_weight, k_weight):
         zl_qk_rope_fwd(q if of_q else None, k if of_k else None, bufs["q"] if of_q else None, bufs["k"] if of_k else None,
                        positions, table, norm, q_weight if of_q else None, k_weight if of_k else None, eps, stream)
-    if keep is None:
+    if w is None:
         zl_kv4_write(cache, bufs["k"], v, starts, stream=stream)
+    else:
+        zl_kv4_write(cache, bufs["k"], v, starts, positions.view(-1), at, stream)
+    if keep is None:
         zl_kv4_attn_fwd(cache, bufs["q"], bufs["o"], bufs["lse"], bufs["workspace"], scale, starts, max_new, stream=stream)
+    else:
+        zl_kv4_attn_fwd(cache, bufs["q"], bufs["o"], bufs["lse"], bufs["workspace"], scale, starts, max_new, w, w, decay, stream)
+        zl_kv4_evict(cache, w, at, keep, recent, bufs["workspace"], stream=stream)
+    if w is None:
         return bufs
-    w, at = bufs["weights"], bufs["positions"]
-    zl_kv4_write(cache, bufs["k"], v, starts, positions.view(-1), at, stream)
-    zl_kv4_attn_fwd(cache, bufs["q"], bufs["o"], bufs["lse"], bufs["workspace"], scale, starts, max_new, w, w, decay, stream)
-    zl_kv4_evict(cache, w, at, keep, recent, bufs["workspace"], stream=stream)
     if stream is not None and not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_raw_stream(stream, cache.device), cache.data.device)
     with torch.cuda.stream(stream):  # None: the current one
-        cache.lens.clamp_(max=keep)
+        if keep is None:
+            _kv4_zero_new(cache, w, starts)
+        else:
+            cache.lens.clamp_(max=keep)
     return bufs
 
 

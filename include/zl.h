@@ -574,6 +574,8 @@ typedef struct {
  * largest magnitude / 6 and each channel the nearest code, ties to even; NaN is held as 0, infinities as the largest
  * magnitude, 6 * 2^13.  positions (device int32 [n_tokens]) and slot_positions (int32 [n_seqs, n_kv_heads, max_pages * page]),
  * both or neither: the slot's position becomes the token's, for eviction.
+ * Accumulated weights are not its own: zl_kv4_attn_fwd with weights begins new tokens' slots at 0, and after an attention
+ * without weights the caller sets theirs.
  * Pages that it writes belong to one sequence alone. */
 ZL_API zl_status zl_kv4_write(const zl_kv4_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                               int64_t n_tokens, const int32_t* starts, const int32_t* positions, int32_t* slot_positions,

@@ -121,3 +121,103 @@ def test_scores_of_any_size(rows, new, table, power, sign):
     q, o, lse = attend_one_hot(c, rows, new, 0.3, 2.0 ** power)
     top = 2.0 ** power * 0.3 * (3.0 if sign > 0 else -1.5)
     assert (o == 1.5).all() and (np.abs(lse / top - 1) < 2.0 ** -20 + 1 / abs(top)).all()
+
+
+# ---------------------------------------------------------------- state that goes on from call to call
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_prompt_without_keep_then_steps_on_a_budget(shared, graph):
+    """Prompts in several calls, steps on a budget behind them, and a row that becomes another sequence's: what eviction goes by
+    comes from the calls alone."""
+    import torch
+    heads, hq, d, keep, recent = 2, 4, 64, 24, 8
+    c = zl.allocate_kv4(2, 4, heads, d, page=16)
+    step = zl.allocate_kv4_attention(c, 12, hq, 6, evicts=True)
+    prompt = zl.allocate_kv4_attention(c, 20, hq, 10, state=step) if shared else step
+    T = {None: 10 if shared else 6, keep: 6}
+    g = torch.Generator().manual_seed(60)
+    table = zl.rotary_table(zl.rotary_frequencies(d)[0])
+    data, pages = c.data.cpu().numpy(), c.pages.cpu().numpy()
+    w, pos = np.zeros(c.slot_shape), np.zeros(c.slot_shape, int)
+    lens, at = np.zeros(2, int), np.zeros(2, int)
+    calls = {}
+
+    def call(k):
+        n = T[k]
+        if k not in calls:
+            inputs = (torch.empty(2 * n, hq + 2 * heads, d, dtype=torch.bfloat16).cuda(), torch.zeros(2 * n, dtype=torch.int32).cuda(), starts_of([n, n])[1])
+            calls[k] = [inputs, None]
+        (qkv, positions, ds), captured = calls[k]
+        qkv.copy_(torch.randn(qkv.shape, generator=g))
+        positions.copy_(torch.from_numpy(np.concatenate([at[b] + np.arange(n) for b in range(2)])))
+
+        def body():
+            c.lens.add_(n)
+            zl.qkv_attention_cached(c, qkv, positions, table, d ** -0.5, prompt if k is None else step, starts=ds, max_new=n, keep=k, recent=recent)
+
+        if not graph:
+            body()
+        else:
+            if captured is None:
+                held = [x.clone() for x in (c.data, c.lens, step["weights"], step["positions"])]
+                side = torch.cuda.Stream()
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    body()
+                torch.cuda.current_stream().wait_stream(side)
+                for x, y in zip((c.data, c.lens, step["weights"], step["positions"]), held):
+                    x.copy_(y)
+                captured = calls[k][1] = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(captured):
+                    body()
+            captured.replay()
+        return qkv, prompt if k is None else step
+
+    for turn in range(12):
+        if turn == 7:  # the second row is another sequence's from here on
+            lens[1] = at[1] = 0
+            c.lens.copy_(torch.from_numpy(lens).int())
+        k = None if turn < 3 or turn == 7 else keep
+        n = T[k]
+        qkv, bufs = call(k)
+        starts = [0, n, 2 * n]
+        lens, at = lens + n, at + n
+        ref.write(data, pages, lens, starts, f64(bufs["k"]), f64(qkv[:, hq + heads:]))
+        want, tol = reference(f64(bufs["q"]), data, pages, lens, starts, d ** -0.5, w)
+        within(f64(bufs["o"]), want["o"], tol["o"], "o")
+        within(f64(bufs["lse"]), want["lse"], tol["lse"], "lse")
+        for b in range(2):
+            pos[b, :, lens[b] - n:lens[b]] = at[b] - n + np.arange(n)
+            w[b, :, lens[b] - n:lens[b]] = 0
+        if k is not None:
+            w = np.where(np.isnan(want["weights"]), w, want["weights"])
+            for b in range(2):
+                for h in range(heads):
+                    for a, to in ref.evict_moves(w[b, h, :lens[b]], pos[b, h, :lens[b]], keep, recent):
+                        ref.put_row(data, pages, b, h, to, ref.get_row(data, pages, b, h, a))
+                        w[b, h, to], pos[b, h, to] = w[b, h, a], pos[b, h, a]
+            lens = np.minimum(lens, keep)
+        got_w, got_pos = f64(step["weights"]), step["positions"].cpu().numpy()
+        for b in range(2):
+            m = lens[b]
+            assert np.array_equal(got_pos[b, :, :m], pos[b, :, :m]), turn
+            off = np.abs(got_w[b, :, :m] - w[b, :, :m])
+            assert off.max() <= (2 * tol["weights"].max() if k is not None else 0), turn
+            w[b, :, :m] = got_w[b, :, :m]
+        assert np.array_equal(c.lens.cpu().numpy(), lens)
+    assert zl.zl_kv4_get_device_status(c) == 0
+
+
+def test_buffers_with_state_want_one_position_a_token_and_the_cache_s_sizes():
+    import torch
+    c = zl.allocate_kv4(2, 2, 2, 64, page=16)
+    c.lens.fill_(1)
+    bufs = zl.allocate_kv4_attention(c, 2, 4, evicts=True)
+    other = zl.allocate_kv4(2, 3, 2, 64, page=16)
+    with pytest.raises(ValueError):
+        zl.allocate_kv4_attention(other, 2, 4, state=bufs)
+    more = zl.allocate_kv4_attention(c, 2, 4, state=bufs)
+    assert more["weights"] is bufs["weights"] and more["positions"] is bufs["positions"]
+    qkv, table = torch.ones(2, 8, 64).bfloat16().cuda(), zl.rotary_table(zl.rotary_frequencies(64)[0])
+    with pytest.raises(ValueError):
+        zl.qkv_attention_cached(c, qkv, torch.zeros(1, dtype=torch.int32).cuda(), table, 0.1, bufs)
