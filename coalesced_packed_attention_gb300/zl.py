@@ -1089,9 +1089,14 @@ def zl_kv4_evict(cache: Kv4Cache, weights, positions, keep: int, recent: int, wo
 
 
 def zl_kv4_get_device_status(cache: Kv4Cache) -> int:
-    """ZL_KV4_* bits of what calls on this cache had to leave out since the last query; waits for the device."""
+    """ZL_KV4_* bits of what calls on this cache had to leave out since the last query.  Waits for all of the device's streams;
+    calls sent by other threads meanwhile may be told of now, in the next query, or not at all."""
+    torch = _torch()
+    torch.cuda.synchronize(cache.device)
     s = int(cache.status.item())
-    cache.status.zero_()
+    if s:
+        cache.status.zero_()
+        torch.cuda.current_stream(cache.device).synchronize()  # calls on other streams come behind it
     return s
 
 

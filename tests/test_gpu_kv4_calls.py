@@ -221,3 +221,22 @@ def test_buffers_with_state_want_one_position_a_token_and_the_cache_s_sizes():
     qkv, table = torch.ones(2, 8, 64).bfloat16().cuda(), zl.rotary_table(zl.rotary_frequencies(64)[0])
     with pytest.raises(ValueError):
         zl.qkv_attention_cached(c, qkv, torch.zeros(1, dtype=torch.int32).cuda(), table, 0.1, bufs)
+
+
+# ---------------------------------------------------------------- status
+def test_the_status_of_a_call_under_way_on_another_stream():
+    import torch
+    c, _, _ = make_cache([40, 40], 2, 64, 16, 72)
+    c.pages[1, 0] = -1
+    q, o, lse = torch.ones(2, 4, 64).bfloat16().cuda(), torch.empty(2, 4, 64).bfloat16().cuda(), torch.empty(2, 4).cuda()
+    ws = torch.empty(zl.zl_kv4_attn_workspace_bytes(c, 4), dtype=torch.uint8).cuda()
+    zl.zl_kv4_attn_fwd(c, q, o, lse, ws, 0.1)
+    assert zl.zl_kv4_get_device_status(c) == zl.ZL_KV4_BAD_PAGE
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)
+        zl.zl_kv4_attn_fwd(c, q, o, lse, ws, 0.1, stream=side)
+        assert zl.zl_kv4_get_device_status(c) == zl.ZL_KV4_BAD_PAGE
+        assert zl.zl_kv4_get_device_status(c) == 0
