@@ -28,6 +28,7 @@ constexpr int kCluster = 8;
 constexpr int kFew = 4;            // slots given up that are looked for one by one
 constexpr int kMoveThreads = 256;
 constexpr int kMoves = 64;         // moves that a block of the second launch makes
+constexpr uint32_t kGone = 0x80000000u;  // of a listed slot: its row is not there
 constexpr int kMovesApart = 256;   // moves a head from which on a second launch makes them
 
 struct EvictParams {
@@ -37,7 +38,7 @@ struct EvictParams {
   float* weights_out;
   int32_t* positions_out;
   int32_t* counts;  // [sequence][key head]: moves, where a launch of their own makes them (else null)
-  uint32_t* moves;  // [sequence][key head][4][capacity]: slots given up, their rows; survivors' slots, their rows (16 tile + row)
+  uint32_t* moves;  // [sequence][key head][4][capacity]: slots given up, their rows; survivors' slots, their rows (16 tile + row); see kGone
   int32_t keep, recent, capacity;
 };
 
@@ -78,7 +79,7 @@ struct Piece {
     out = l == 14 ? reinterpret_cast<uint8_t*>(p.weights_out + base) : l == 15 ? reinterpret_cast<uint8_t*>(p.positions_out + base) : p.c.data;
   }
   // bytes to the piece of slot or row x
-  __device__ int64_t offset(uint32_t x) const { return number ? (int64_t)x * 4 : (int64_t)(x >> 4) * (18 * D) + at + (x & 15) * pitch; }
+  __device__ int64_t offset(uint32_t x) const { return number ? (int64_t)(x & ~kGone) * 4 : (int64_t)(x >> 4) * (18 * D) + at + (x & 15) * pitch; }
 };
 // Moves i, i + step, .. of a head, kAtOnce of them, whose numbers of slots or rows (a lane's own kind) are known.
 template <int D, int kAtOnce>
@@ -89,10 +90,12 @@ __device__ __forceinline__ void move_pieces(const EvictParams& p, const Piece<D>
   bool does[kAtOnce];
 #pragma unroll
   for (int y = 0; y < kAtOnce; ++y) {
-    const bool in = i + y * step < end, bad = !piece.number && (to[y] == kKv4None || from[y] == kKv4None);
-    does[y] = in && !piece.idle && !bad;
+    const bool in = i + y * step < end;
+    // a row that is not there takes its weight and position out of the move, too: the slot given up keeps its own
+    const bool bad = piece.number ? (int32_t)(to[y] | from[y]) < 0 : to[y] == kKv4None || from[y] == kKv4None;
+    does[y] = in && !piece.idle && (piece.number || !bad);
     if (in && bad && (threadIdx.x & 15) == 0) kv4_report(p.c, ZL_KV4_BAD_PAGE);
-    const uint8_t* src = piece.in + piece.offset(from[y]);
+    const uint8_t* src = piece.in + piece.offset(piece.number && bad ? to[y] : from[y]);
     if (does[y] && piece.code) v[y] = *reinterpret_cast<const uint4*>(src);
     if (does[y] && !piece.code) u[y] = *reinterpret_cast<const uint32_t*>(src);
   }
@@ -108,11 +111,12 @@ __device__ __forceinline__ void move_pieces(const EvictParams& p, const Piece<D>
 template <int D>
 __device__ __forceinline__ void move_row(const EvictParams& p, int b, int h, int64_t base, int to, int from) {
   const int l = threadIdx.x & 15;
-  if (l == 14) p.weights_out[base + to] = p.weights[base + from];
-  if (l == 15) p.positions_out[base + to] = p.positions[base + from];
   uint8_t* dst = kv4_tile<D>(p.c, b, h, to);
   const uint8_t* src = kv4_tile<D>(p.c, b, h, from);
-  if (!dst || !src) {
+  const bool bad = !dst || !src;
+  if (l == 14) p.weights_out[base + to] = p.weights[base + (bad ? to : from)];
+  if (l == 15) p.positions_out[base + to] = p.positions[base + (bad ? to : from)];
+  if (bad) {
     if (l == 0) kv4_report(p.c, ZL_KV4_BAD_PAGE);
     return;
   }
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
       // within the lists whatever happens to the inputs meanwhile
       if (at[y] < 0 || (at[y] < 2 * p.capacity ? at[y] : at[y] - 2 * p.capacity) >= p.capacity) continue;
       const int slot = lo + i + 32 * y + lane;
-      list[at[y]] = slot;
+      list[at[y]] = place[y] == kKv4None ? slot | kGone : slot;
       list[at[y] + p.capacity] = place[y] == kKv4None ? kKv4None : place[y] * 16 + (slot & 15);
     }
   }

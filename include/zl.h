@@ -617,7 +617,8 @@ ZL_API zl_status zl_kv4_evict_workspace(const zl_kv4_cache* cache, int64_t* byte
 /* Every head of a sequence longer than `keep` slots gives up all but `keep` of them.  In order of claim: the slots whose
  * position is above newest - recent (newest: the largest position in the head's slots), then the others; among each the
  * larger weight, then the lower slot (NaN ranks below all numbers).  Survivors in slots >= keep move, in order, into
- * the slots below keep that were given up, in order; other slots stay where they are.  The new lengths are
+ * the slots below keep that were given up, in order; other slots stay where they are.  Where either slot of a move lies in a
+ * bad page the slot given up stays as it was, with its weight and position.  The new lengths are
  * min(lens[b], keep): the caller sets them.
  *   weights fp32, positions int32 [n_seqs, n_kv_heads, max_pages * page]: by slot, not changed; weights_out,
  *   positions_out: the same for the kept slots, in their new places (rest left as it was); either may be its input

@@ -240,3 +240,38 @@ def test_the_status_of_a_call_under_way_on_another_stream():
         zl.zl_kv4_attn_fwd(c, q, o, lse, ws, 0.1, stream=side)
         assert zl.zl_kv4_get_device_status(c) == zl.ZL_KV4_BAD_PAGE
         assert zl.zl_kv4_get_device_status(c) == 0
+
+
+# ---------------------------------------------------------------- eviction
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,keep,table", [(64, 61, 0), (64, 40, 0), (700, 300, 0), (64, 62, 640)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_eviction_leaves_out_whole_moves_of_bad_pages(lens, keep, table, d, in_place):
+    import torch
+    c, data, pages = make_cache([lens], 2, d, 16, 73, extra_pages=table // 16)
+    bad = [1, (lens - 1) // 16]
+    pages[0, bad] = -1, 10 ** 6
+    c.pages.copy_(torch.from_numpy(pages).int())
+    rng = np.random.default_rng(74)
+    w, pos = rng.random(c.slot_shape).astype(np.float32), np.argsort(rng.random(c.slot_shape), -1)
+    w[0, :, 16:32] *= 1e-3  # slots given up, in a page that is not there
+    w[0, :, lens - 5:lens] += 1
+    dw, dp = torch.from_numpy(w).cuda(), torch.from_numpy(pos).int().cuda()
+    wo, po = (dw, dp) if in_place else (torch.full_like(dw, 7.0), torch.full_like(dp, 7))
+    zl.zl_kv4_evict(c, dw, dp, keep, 0, torch.empty(zl.zl_kv4_evict_workspace_bytes(c), dtype=torch.uint8).cuda(), wo, po)
+    assert zl.zl_kv4_get_device_status(c) == zl.ZL_KV4_BAD_PAGE
+    want, ww, wp = data.copy(), np.full_like(w, 7.0), np.full_like(pos, 7)
+    if in_place:
+        ww, wp = w.copy(), pos.copy()
+    ww[..., :keep], wp[..., :keep] = w[..., :keep], pos[..., :keep]
+    left_out = 0
+    for h in range(2):
+        for a, to in ref.evict_moves(w[0, h, :lens], pos[0, h, :lens], keep, 0):
+            if a // 16 in bad or to // 16 in bad:
+                left_out += 1
+                continue
+            ref.put_row(want, pages, 0, h, to, ref.get_row(data, pages, 0, h, a))
+            ww[0, h, to], wp[0, h, to] = w[0, h, a], pos[0, h, a]
+    assert left_out > 0
+    assert np.array_equal(c.data.cpu().numpy(), want)
+    assert np.array_equal(wo.cpu().numpy(), ww) and np.array_equal(po.cpu().numpy(), wp)
