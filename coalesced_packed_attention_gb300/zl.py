@@ -1069,6 +1069,11 @@ def zl_kv4_evict_workspace_bytes(cache: Kv4Cache) -> int:
     return cache.sizes["evict"]
 
 
+def _kv4_check_budget(keep, recent):
+    if not 1 <= keep < 1 << 31 or not 0 <= recent < 1 << 31:
+        _check(ZL_ERR_INVALID_ARG, f"keep {keep}, recent {recent}")
+
+
 def zl_kv4_evict(cache: Kv4Cache, weights, positions, keep: int, recent: int, workspace, weights_out=None, positions_out=None,
                  stream=None):
     """Every head of a sequence longer than `keep` keeps `keep` slots: those among the last `recent` positions first, then
@@ -1079,6 +1084,7 @@ def zl_kv4_evict(cache: Kv4Cache, weights, positions, keep: int, recent: int, wo
     dev = _kv4_dev(cache)
     w = _dense(weights, "weights", torch.float32, cache.slot_shape, dev)
     ps = _dense(positions, "positions", torch.int32, cache.slot_shape, dev)
+    _kv4_check_budget(keep, recent)
     wo = w if weights_out is None else _dense(weights_out, "weights_out", torch.float32, cache.slot_shape, dev)
     po = ps if positions_out is None else _dense(positions_out, "positions_out", torch.int32, cache.slot_shape, dev)
     st = load_library().zl_kv4_evict(cache.desc, w, ps, keep, recent, wo, po,
@@ -1136,6 +1142,29 @@ def _kv4_zero_new(cache: Kv4Cache, weights, starts):
     weights.masked_fill_(slot >= (cache.lens - new)[:, None, None], 0.0)
 
 
+def _kv4_check_step(cache: Kv4Cache, n: int, hq: int, scale, bufs, starts, max_new, keep, recent, decay):
+    """Raises what one of a step's calls would refuse, before the first of them changes anything."""
+    torch = _torch()
+    dev, d = _kv4_dev(cache), cache.token_shape[1]
+    nbytes = zl_kv4_attn_workspace_bytes(cache, hq, max_new, keep is not None)
+    if keep is not None:
+        _kv4_check_budget(keep, recent)
+        nbytes = max(nbytes, zl_kv4_evict_workspace_bytes(cache))
+        if cache.slot_shape[0] > 65535:
+            _check(ZL_ERR_UNSUPPORTED, "keep, more than 65535 sequences")
+    at = _dense(bufs["o"], "o", torch.bfloat16, (n, hq, d), dev) | _scratch(bufs["workspace"], "workspace", nbytes, dev)
+    _dense(bufs["lse"], "lse", torch.float32, (n, hq), dev)
+    if "weights" in bufs:
+        _dense(bufs["weights"], "weights", torch.float32, cache.slot_shape, dev)
+        _dense(bufs["positions"], "positions", torch.int32, cache.slot_shape, dev)
+    _kv4_starts(cache, starts, dev)
+    if at % 16:
+        _check(ZL_ERR_ALIGN, "o, workspace")
+    s, f = ctypes.c_float(scale).value, ctypes.c_float(decay).value
+    if not 2.0 ** -126 <= s < float("inf") or f - f != 0.0 or (starts is None and n != cache.slot_shape[0]):
+        _check(ZL_ERR_INVALID_ARG, "scale, decay, tokens without starts")
+
+
 def qkv_attention_cached(cache: Kv4Cache, qkv, positions, table: Optional[RotaryTable], scale: float, bufs: dict, q_weight=None,
                          k_weight=None, eps: float = 1e-6, starts=None, max_new: int = 1, keep: Optional[int] = None,
                          recent: int = 0, decay: float = 1.0, stream=None) -> dict:
@@ -1158,6 +1187,7 @@ def qkv_attention_cached(cache: Kv4Cache, qkv, positions, table: Optional[Rotary
     if w is not None and (not isinstance(positions, torch.Tensor) or positions.numel() != qkv.shape[0]):
         raise ValueError("buffers with weights: need one position a token")
     hq = qkv.shape[1] - 2 * heads
+    _kv4_check_step(cache, qkv.shape[0], hq, scale, bufs, starts, max_new, keep, recent, decay)
     q, k, v = qkv[:, :hq], qkv[:, hq:hq + heads], qkv[:, hq + heads:]
     for of_q, of_k, norm in _sides(q_weight, k_weight):
         zl_qk_rope_fwd(q if of_q else None, k if of_k else None, bufs["q"] if of_q else None, bufs["k"] if of_k else None,

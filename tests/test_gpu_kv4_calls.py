@@ -275,3 +275,32 @@ def test_eviction_leaves_out_whole_moves_of_bad_pages(lens, keep, table, d, in_p
     assert left_out > 0
     assert np.array_equal(c.data.cpu().numpy(), want)
     assert np.array_equal(wo.cpu().numpy(), ww) and np.array_equal(po.cpu().numpy(), wp)
+
+
+# ---------------------------------------------------------------- refusals
+def test_a_refused_step_leaves_everything_as_it_was():
+    import torch
+    heads, hq, d, n = 2, 4, 64, 3
+    c = zl.allocate_kv4(n, 2, heads, d, page=16)
+    c.lens.fill_(5)
+    bufs = zl.allocate_kv4_attention(c, n, hq, evicts=True)
+    bufs["weights"].fill_(3.0)
+    qkv, at = torch.ones(n, hq + 2 * heads, d).bfloat16().cuda(), torch.full((n,), 4, dtype=torch.int32).cuda()
+    table = zl.rotary_table(zl.rotary_frequencies(d)[0])
+    held = (c.data, c.lens, bufs["weights"], bufs["positions"])
+    before = [x.clone() for x in held]
+    ok = dict(cache=c, qkv=qkv, positions=at, table=table, scale=0.1, bufs=bufs, keep=4)
+    for bad in (dict(keep=0), dict(keep=-3), dict(recent=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=1e-40),
+                dict(decay=float("inf")), dict(max_new=0), dict(max_new=5000), dict(max_new=64), dict(bufs={**bufs, "o": bufs["o"][:2]}),
+                dict(bufs={**bufs, "lse": bufs["lse"].half()}), dict(bufs={**bufs, "workspace": bufs["workspace"][:64]}),
+                dict(bufs={**bufs, "weights": bufs["weights"][:1]}), dict(bufs={**bufs, "positions": bufs["positions"].long()}),
+                dict(starts=torch.zeros(3, dtype=torch.int32).cuda()), dict(keep=2 ** 31), dict(keep=2 ** 32 + 4), dict(recent=2 ** 31), dict(keep=None, scale=-1.0),
+                dict(keep=None, max_new=0), dict(keep=None, bufs={**bufs, "o": bufs["o"].float()})):
+        with pytest.raises((zl.ZlError, TypeError, ValueError)):
+            zl.qkv_attention_cached(**{**ok, **bad})
+        assert all(torch.equal(x, y) for x, y in zip(held, before)), bad
+    zl.qkv_attention_cached(**ok)
+    assert (c.lens == 4).all()
+    for bad in (dict(keep=2 ** 32 + 4), dict(keep=0), dict(recent=2 ** 32)):
+        with pytest.raises(zl.ZlError):
+            zl.zl_kv4_evict(**{**dict(cache=c, weights=bufs["weights"], positions=bufs["positions"], keep=3, recent=1, workspace=bufs["workspace"]), **bad})
