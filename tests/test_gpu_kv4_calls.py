@@ -304,3 +304,67 @@ def test_a_refused_step_leaves_everything_as_it_was():
     for bad in (dict(keep=2 ** 32 + 4), dict(keep=0), dict(recent=2 ** 32)):
         with pytest.raises(zl.ZlError):
             zl.zl_kv4_evict(**{**dict(cache=c, weights=bufs["weights"], positions=bufs["positions"], keep=3, recent=1, workspace=bufs["workspace"]), **bad})
+
+
+# ---------------------------------------------------------------- starts, workspaces, streams
+def test_a_write_with_descending_starts_changes_the_rows_of_the_range_that_is_there():
+    import torch
+    c, data, pages = make_cache([32, 32, 32], 1, 64, 16, 28)
+    x = torch.randn(4, 1, 64, generator=torch.Generator().manual_seed(75)).bfloat16().cuda()
+    zl.zl_kv4_write(c, x, -x, torch.tensor([0, 5, 1, 4], dtype=torch.int32).cuda())
+    assert zl.zl_kv4_get_device_status(c) == zl.ZL_KV4_BAD_STARTS
+    want = data.copy()
+    ref.write(want, pages[2:], [32], [0, 3], f64(x[1:]), -f64(x[1:]))
+    got = c.data.cpu().numpy()
+    for s in range(32):
+        for a, b in zip(ref.get_row(got, pages, 2, 0, s), ref.get_row(want, pages, 2, 0, s)):
+            assert np.array_equal(np.where(a == 8, 0, a) if len(a) == 64 else a, np.where(b == 8, 0, b) if len(b) == 64 else b)
+    keep = np.ones(len(data), bool)
+    keep[pages[2]] = False
+    assert np.array_equal(got[keep], data[keep])
+
+
+@pytest.mark.parametrize("lens,rows", [([300, 64], 0), ([300, 64], 48), ([5000, 9000], 0)])
+def test_one_workspace_serves_smaller_calls(lens, rows):
+    import torch
+    new = [12, 9]
+    c, data, pages = many(lens, 2, 64, 16, 53, rows) if rows else make_cache(lens, 2, 64, 16, 53)
+    ws = torch.empty(max(zl.zl_kv4_attn_workspace_bytes(c, 8, 16), zl.zl_kv4_attn_workspace_bytes(c, 8, 12, True)), dtype=torch.uint8).cuda()
+    g = torch.Generator().manual_seed(76)
+    w_in = torch.rand(c.slot_shape, generator=g).cuda()
+    for now, weights in (([12, 9], False), ([2, 1], False), ([12, 9], True), ([1, 1], True), ([5, 0], False), ([9, 9], False), ([1, 2], True)):
+        starts, ds = starts_of(now)
+        q = torch.randn(sum(now), 8, 64, generator=g).bfloat16().cuda()
+        o, lse, w = torch.empty_like(q), torch.empty(sum(now), 8).cuda(), torch.zeros(c.slot_shape).cuda()
+        kw = dict(weights=w_in, weights_out=w) if weights else {}
+        zl.zl_kv4_attn_fwd(c, q, o, lse, ws, 0.125, ds, max(now), **kw)
+        want, tol = reference(f64(q), data, pages, lens, starts, 0.125, f64(w_in) if weights else None)
+        within(f64(o), want["o"], tol["o"], "o")
+        within(f64(lse), want["lse"], tol["lse"], "lse")
+        if weights:
+            within(f64(w), want["weights"], tol["weights"], "weights")
+    assert zl.zl_kv4_get_device_status(c) == 0
+
+
+@pytest.mark.parametrize("rows", [0, 64])
+def test_calls_that_cut_items_on_other_streams_at_once(rows):
+    import torch
+    lens, new = [9000, 10, 3000], ([16, 10, 3] if rows else [1, 1, 1])
+    c, data, pages = many(lens, 2, 128, 64, 77, rows) if rows else make_cache(lens, 2, 128, 64, 77)
+    assert c.slots > 8192
+    starts, ds = starts_of(new)
+    outs, g = [], torch.Generator().manual_seed(78)
+    for _ in range(6):
+        q = torch.randn(sum(new), 8, 128, generator=g).bfloat16().cuda()
+        ws = torch.full((zl.zl_kv4_attn_workspace_bytes(c, 8, max(new)),), 255, dtype=torch.uint8).cuda()
+        outs.append((q, torch.empty_like(q), torch.empty(sum(new), 8).cuda(), ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, o, lse, ws, stream in outs:
+            zl.zl_kv4_attn_fwd(c, q, o, lse, ws, 0.1, ds, max(new), stream=stream)
+    torch.cuda.synchronize()
+    assert zl.zl_kv4_get_device_status(c) == 0
+    for q, o, lse, _, _ in outs:
+        want, tol = reference(f64(q), data, pages, lens, starts, 0.1)
+        within(f64(o), want["o"], tol["o"], "o")
+        within(f64(lse), want["lse"], tol["lse"], "lse")
