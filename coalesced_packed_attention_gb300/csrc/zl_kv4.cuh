@@ -111,6 +111,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 // Every thread of the cluster; what each wrote before it, to shared or global memory, the others see after it.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // .aligned: the warp's lanes come together, also from branches
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnPar
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
+          __syncwarp();  // lanes without a row have gone ahead
           tmem_ld32(tmem + lane_base + 256 + c, o);
           tmem_ld_wait();
           if (row >= rows) continue;

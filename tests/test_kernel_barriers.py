@@ -44,3 +44,14 @@ def test_barriers_are_initialised_before_any_warp_uses_them(text):
     # one thread initialises them all, and fences behind that
     block = text[text.rindex("== 0) {", 0, text.index("mbar_init(")) + len("== 0) "):fence]
     assert block.count("{") == block.count("}") + 1
+
+
+def test_aligned_instructions_come_behind_a_whole_warp():
+    """Barriers of a cluster and loads from tensor memory are .aligned: all lanes of a warp execute them together."""
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu*"))):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for m in re.finditer(r"barrier\.cluster\.arrive[a-z.]*aligned", text):
+            assert "__syncwarp();" in text[text.rindex("{", 0, text.rindex("asm", 0, m.start())):m.start()], path
+        # where lanes leave a loop's body early, they wait for one another ahead of the next load
+        for m in re.finditer(r"(.*)\s*tmem_ld\w+\([^;]*;\s*tmem_ld_wait\(\);\s*if \([^;]*\) continue;", text):
+            assert m.group(1).strip() == "__syncwarp();", path
