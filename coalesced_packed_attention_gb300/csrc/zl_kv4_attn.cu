@@ -860,6 +860,8 @@ extern "C" zl_status zl_kv4_attn_workspace(const zl_kv4_cache* cache, int32_t n_
   if (s != ZL_OK) return s;
   if (!bytes || (weights != 0 && weights != 1)) return ZL_ERR_INVALID_ARG;
   if ((s = check_heads(cache, n_q_heads, max_new)) != ZL_OK) return s;
+  // every factor is within its own limit, their product need not be a number of bytes
+  if (weights && (double)cache->n_seqs * cache->max_pages * cache->page * n_q_heads * max_new > 0x1p60) return ZL_ERR_UNSUPPORTED;
   *bytes = layout(*cache, n_q_heads / cache->n_kv_heads, max_new, weights != 0).total;
   return ZL_OK;
 }

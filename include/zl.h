@@ -588,7 +588,7 @@ ZL_API zl_status zl_kv4_read(const zl_kv4_cache* cache, void* k_out, int64_t k_s
                              int64_t n_rows, const int64_t* row_starts, void* stream);
 
 /* Device scratch of zl_kv4_attn_fwd for these sizes; with weights != 0 it holds every score of the new tokens:
- * 4 * max_new * group bytes for each slot that the table has room for. */
+ * 4 * max_new * group bytes for each slot that the table has room for (ZL_ERR_UNSUPPORTED past 2^62). */
 ZL_API zl_status zl_kv4_attn_workspace(const zl_kv4_cache* cache, int32_t n_q_heads, int32_t max_new, int32_t weights,
                                        int64_t* bytes);
 
