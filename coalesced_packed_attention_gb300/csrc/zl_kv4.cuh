@@ -38,7 +38,8 @@ inline zl_status kv4_check(const zl_kv4_cache* c, Kv4* out) {
     return ZL_ERR_ALIGN;
   int shift = 0;
   while ((1 << shift) < c->page) ++shift;
-  *out = {static_cast<uint8_t*>(c->data), c->pages, c->lens, c->status, c->n_pages, c->n_seqs, c->n_kv_heads, c->max_pages, shift};
+  *out = {static_cast<uint8_t*>(c->data), c->pages,      c->lens,      c->status, c->n_pages,
+          c->n_seqs,                      c->n_kv_heads, c->max_pages, shift};
   return ZL_OK;
 }
 

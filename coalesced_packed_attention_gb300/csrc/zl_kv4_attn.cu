@@ -2,25 +2,25 @@
 //
 // With the group's query heads of all new tokens as rows r of one key head:
 //   S[key, r] = scale K Q^T,  P = exp(S - max),  O^T[channel, r] = V^T P,  LSE = max + log sum P,
-// one pass over the keys with the running maximum and sum of a softmax.  Bound by the cache's bytes, 1.125 d a
-// slot and key head: at the copy rate an SM has 6 cycles (d = 128) for a slot, in which it has to turn 256 codes into fp16
-// and to multiply them.  So codes become operands in registers, where the matrix instructions take them:
+// one pass over the keys with the running maximum and sum of a softmax.  Bound by the cache's bytes, 1.125 d a slot and
+// key head: at the copy rate an SM has 6 cycles (d = 128) for a slot, in which it has to turn 256 codes into fp16 and
+// to multiply them.  So codes become operands in registers, where the matrix instructions take them:
 //  - K is the A operand (16 keys x 16 channels) of m16n8k16, rows the 8 columns: a warp's products serve 8 rows at no
 //    waste for small groups.  The sum over channels has any order, so lane t of a quad takes the quarter t of the
 //    channels, 16 bytes of a row, and two scales serve it.
 //  - S^T's accumulator becomes P's operand by one 8 x 8 transposition (movmatrix) each 8 keys.
-//  - V is the A operand V^T (16 channels x 16 keys).  Its pairs run over keys: two keys' bytes become bytes of pairs with
-//    four logic instructions for 16 codes, before they are turned into fp16.  Lane g takes the g-th eighth of the channels, so one
-//    scale a key serves it.
+//  - V is the A operand V^T (16 channels x 16 keys).  Its pairs run over keys: two keys' bytes become bytes of pairs
+//    with four logic instructions for 16 codes, before they are turned into fp16.  Lane g takes the g-th eighth of the
+//    channels, so one scale a key serves it.
 //  - code * scale is exact in fp16; Q is scaled by a power of two a row so that fp16 holds its bf16 digits.
 // Every warp streams runs of 32 slots of its own through shared memory (bulk copies, a ring of stages, no other warp in
 // between); 4 warps of a block share a (sequence, key head, row tile) and join at its end.
-// The slots of all items lie in a row that is dealt out evenly over the blocks, whatever the lengths: a block writes what
-// it holds alone; items cut between blocks leave parts (O, max, sum) that a second launch joins in order.  Short items go to a block
-// or a cluster of blocks each instead, which joins them itself.
-// Measured, 32/8 heads, d = 128: 64 single tokens behind 1 to 16 384 slots 85 us (436 MB, 5.1 TB/s; the loads without arithmetic
-// 69 us), one behind 131 071 slots 35 us and 4 for its join (151 MB).  What is above the loads is arithmetic that they
-// do not hide: some 595 instructions for 32 slots, 256 of them conversions and products at half rate.
+// The slots of all items lie in a row that is dealt out evenly over the blocks, whatever the lengths: a block writes
+// what it holds alone; items cut between blocks leave parts (O, max, sum) that a second launch joins in order.  Short
+// items go to a block or a cluster of blocks each instead, which joins them itself.
+// Measured, 32/8 heads, d = 128: 64 single tokens behind 1 to 16 384 slots 85 us (436 MB, 5.1 TB/s; the loads without
+// arithmetic 69 us), one behind 131 071 slots 35 us and 4 for its join (151 MB).  What is above the loads is arithmetic
+// that they do not hide: some 595 instructions for 32 slots, 256 of them conversions and products at half rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,19 +38,21 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;          // slots of a unit: two tiles
-constexpr int kItemCost = 8;       // units: 64 single tokens over 15 to 16 384 slots each took 98 us at 4, 87 at 8 and 12, 90 at 20
+constexpr int kItemCost = 8;       // units: 64 single tokens over 15 to 16 384 slots took 98 us at 4, 87 at 8 and 12, 90 at 20
 constexpr int kMaxCluster = 8;
 constexpr int kMaxBlocks = 640;    // blocks of a launch at most: what the workspace has room for
-constexpr uint32_t kTwice = 0x00800080u;  // a scale's bits times this: the scale in both halves, by the multiplier, which has time
+constexpr uint32_t kTwice = 0x00800080u;  // a scale's bits times this: the scale in both halves (the multiplier has time)
 
 // ---------------------------------------------------------------- pieces of a product
-__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // The first product of a sum.
-__device__ __forceinline__ void mma16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -96,8 +98,10 @@ __device__ __forceinline__ float4 peer4(const float* mine, uint32_t rank) {
   return v;
 }
 
-// weights_out of slots [s0, s1) of an item whose rows are all this block's: scores that it has just written, four slots a thread.
-__device__ __forceinline__ void add_weights(const AttnParams& p, int seq, int head, int m, int n, int rows, int s0, int s1, const float* row_lse) {
+// weights_out of slots [s0, s1) of an item whose rows are all this block's: scores that it has just written, four slots
+// a thread.
+__device__ __forceinline__ void add_weights(const AttnParams& p, int seq, int head, int m, int n, int rows, int s0, int s1,
+                                            const float* row_lse) {
   const int64_t slots = (int64_t)p.c.max_pages << p.c.page_shift, pair = (int64_t)seq * p.c.heads + head;
   const float* x = p.scores + pair * p.score_rows * slots;
   for (int s = s0 + 4 * threadIdx.x; s < s1; s += 4 * kThreads) {
@@ -106,7 +110,8 @@ __device__ __forceinline__ void add_weights(const AttnParams& p, int seq, int he
     for (int i = 0; i < 4; ++i) w[i] = p.w_in && s + i < m - n ? p.decay * p.w_in[pair * slots + s + i] : 0.f;
 #pragma unroll 4
     for (int r = 0; r < rows; ++r) {
-      const float4 v = *reinterpret_cast<const float4*>(x + r * slots + s);  // slots of the table past the last one are the workspace's, too
+      // slots of the table past the last one are the workspace's, too
+      const float4 v = *reinterpret_cast<const float4*>(x + r * slots + s);
       const float l = row_lse[r];
       if (l == INFINITY) continue;
       w[0] += ex2(v.x - l);
@@ -133,8 +138,8 @@ struct Shape {
   static constexpr int kBlocks = NT == 1 || D == 64 ? 4 : 2;  // an SM's, by registers and shared memory
 };
 
-// kCluster: a cluster takes one item, each of its blocks an equal part of the units, and joins it through its blocks' shared memory: no
-// second launch.  Else the items' units are dealt out evenly.  (The rule between them: cluster_of.)
+// kCluster: a cluster takes one item, each of its blocks an equal part of the units, and joins it through its blocks'
+// shared memory: no second launch.  Else the items' units are dealt out evenly.  (The rule between them: cluster_of.)
 template <int D, int NT, bool kScores, bool kCluster>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_kernel(const AttnParams p) {
   using S = Shape<D, NT>;
@@ -170,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
     if (cons.tile >= cons.row_tiles) {  // all of the cluster
       if (kScores && p.own_weights) {
         const int64_t at = (int64_t)item * ((int64_t)p.c.max_pages << p.c.page_shift);
-        for (int s = cluster_rank() * kThreads + threadIdx.x; s < cons.m; s += cluster * kThreads) p.w_out[at + s] = p.w_in ? p.decay * p.w_in[at + s] : 0.f;
+        for (int s = cluster_rank() * kThreads + threadIdx.x; s < cons.m; s += cluster * kThreads)
+          p.w_out[at + s] = p.w_in ? p.decay * p.w_in[at + s] : 0.f;
       }
       return;
     }
@@ -246,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
   const int va_at = 8 * D + ka * (D / 2) + g * (D / 16), vb_at = 8 * D + kb * (D / 2) + g * (D / 16);
   const int vsa_at = 17 * D + ka * (D / 16) + g * D / 128, vsb_at = 17 * D + kb * (D / 16) + g * D / 128;
   bool first_segment = true, alive = true;
-  for (bool more = kCluster || !cons.done(); more; cons.next(p), more = !cons.done()) {  // a cluster's block joins with no units, too
+  // (a cluster's block joins with no units, too)
+  for (bool more = kCluster || !cons.done(); more; cons.next(p), more = !cons.done()) {
     const int head = cons.head, row0 = cons.tile * S::kRows;
     const int rows = cons.n * p.group;
     // queries: lane (g, t) holds quarter t of the channels of row g of every 8
@@ -428,7 +435,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         const float2 low = make_float2(-ref[j].x, -ref[j].y);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float2 e0 = fma2(make_float2(s[i][j][0], s[i][j][1]), f[j], low), e1 = fma2(make_float2(s[i][j][2], s[i][j][3]), f[j], low);
+          const float2 e0 = fma2(make_float2(s[i][j][0], s[i][j][1]), f[j], low);
+          const float2 e1 = fma2(make_float2(s[i][j][2], s[i][j][3]), f[j], low);
           const float2 p0 = make_float2(ex2(e0.x), ex2(e0.y)), p1 = make_float2(ex2(e1.x), ex2(e1.y));
           sum[j] = add2(sum[j], add2(p0, p1));
           pb[i][j][0] = transpose8(pack_half(p0.x, p0.y));
@@ -494,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         float* dst = join + (warp * S::kRows + row) * S::kPitch + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2)
-          *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(acc[i][j][y], acc[i][j][y + 2], acc[i + 1][j][y], acc[i + 1][j][y + 2]);
+          *reinterpret_cast<float4*>(dst + 2 * i) =
+              make_float4(acc[i][j][y], acc[i][j][y + 2], acc[i + 1][j][y], acc[i + 1][j][y + 2]);
       }
     __syncthreads();
     const bool whole = kCluster || (cons.a == 0 && cons.e == cons.chunks);
@@ -505,11 +514,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
       const int tok = (row0 + r) / p.group;
       const int64_t at = (int64_t)(cons.first + tok) * p.q_heads + head * p.group + (row0 + r - tok * p.group);
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
       if (c4 == 0) {
         const float lse = natural_lse(m, l);
         p.lse[at] = lse;
-        if constexpr (kCluster && kScores) row_lse[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;  // rows that see nothing: 2^(-inf) each
+        // rows that see nothing: 2^(-inf) each
+        if constexpr (kCluster && kScores) row_lse[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;
       }
     };
     for (int r = threadIdx.x / kLanes; r < S::kRows && row0 + r < rows; r += kThreads / kLanes) {
@@ -540,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kBlocks) zl_kv4_attn_k
         __syncwarp();
         cluster_sync();
         // the blocks' parts become one, in order; a row's are put together by one block
-        for (int r = cluster_rank() + cluster * (threadIdx.x / kLanes); r < S::kRows && row0 + r < rows; r += cluster * (kThreads / kLanes)) {
+        for (int r = cluster_rank() + cluster * (threadIdx.x / kLanes); r < S::kRows && row0 + r < rows;
+             r += cluster * (kThreads / kLanes)) {
           float2 ml[kMaxCluster];
           float4 x[kMaxCluster];
 #pragma unroll
@@ -667,10 +679,10 @@ __global__ void __launch_bounds__(256) zl_kv4_join_kernel(const AttnParams p) {
 }
 
 // ---------------------------------------------------------------- accumulated weights
-// weights_out[slot] = decay weights[slot] + sum over rows of 2^(score - lse).  A row's scores lie side by side; a thread takes
-// kPer slots and has kBatch rows' loads under way at a time: four slots where rows are few, one where they are many and slots
-// would not fill the SMs (48 rows over 17 000 slots and 8 heads, out of L2: 21 us with four, 10 with one; 4 rows over 48 x 2049 slots
-// and 8 heads 7 us).
+// weights_out[slot] = decay weights[slot] + sum over rows of 2^(score - lse).  A row's scores lie side by side; a thread
+// takes kPer slots and has kBatch rows' loads under way at a time: four slots where rows are few, one where they are many
+// and slots would not fill the SMs (48 rows over 17 000 slots and 8 heads, out of L2: 21 us with four, 10 with one; 4
+// rows over 48 x 2049 slots and 8 heads 7 us).
 constexpr int kWeightThreads = 128;
 template <int kPer, int kBatch>
 __global__ void __launch_bounds__(kWeightThreads) zl_kv4_weights_kernel(const AttnParams p) {
@@ -725,17 +737,18 @@ __global__ void __launch_bounds__(kWeightThreads) zl_kv4_weights_kernel(const At
 // ---------------------------------------------------------------- host
 int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
 
-// 8-row columns of a warp's products: one where a key head has no more rows, else two, and as many passes over the cache as the
-// rows need.  (Four in a pass, at two blocks an SM for their registers: 66 us instead of 54 for 32 rows over 16 x 4096 slots,
-// 32/8 heads, d = 128; 31 instead of 33 at d = 64.)
+// 8-row columns of a warp's products: one where a key head has no more rows, else two, and as many passes over the
+// cache as the rows need.  (Four in a pass, at two blocks an SM for their registers: 66 us instead of 54 for 32 rows
+// over 16 x 4096 slots, 32/8 heads, d = 128; 31 instead of 33 at d = 64.)
 int row_columns(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
-// The tensor-core kernel (zl_kv4_chunk.cu) instead: for more than two passes' rows over slots enough to pay for its start.
-// Measured (us; here / there): 32, 48, 64, 128 rows over 16 x 4096 slots of 8 key heads, d = 128: 52 / 56, 71 / 58, 88 / 59, 165 / 67;
-// d = 64: 34 / 46, 44 / 46, 75 / 48.  Few slots: 64 rows over 4 x 1000 of 4 heads 10 / 20, 4 x 4000 17 / 22, 8 x 1000 of 8 heads
-// 16 / 21, 8 x 2000 31 / 27; 128 rows over 4 x 2000 of 4 heads 17 / 26, 4 x 4000 29 / 28.  So by the product, of the slots that the
-// table has room for, as lengths lie on the device.  Not with weights: its scores leave a row a thread, which costs what it gains
-// (16 x 2000 slots of 4 heads, 64 and 128 rows: 44 / 48, 76 / 71 at d = 128, 36 / 42, 61 / 62 at d = 64).
+// The tensor-core kernel (zl_kv4_chunk.cu) instead: for more than two passes' rows over slots enough to pay for its
+// start.  Measured (us; here / there): 32, 48, 64, 128 rows over 16 x 4096 slots of 8 key heads, d = 128: 52 / 56, 71 /
+// 58, 88 / 59, 165 / 67; d = 64: 34 / 46, 44 / 46, 75 / 48.  Few slots: 64 rows over 4 x 1000 of 4 heads 10 / 20, 4 x
+// 4000 17 / 22, 8 x 1000 of 8 heads 16 / 21, 8 x 2000 31 / 27; 128 rows over 4 x 2000 of 4 heads 17 / 26, 4 x 4000 29 /
+// 28.  So by the product, of the slots that the table has room for, as lengths lie on the device.  Not with weights:
+// its scores leave a row a thread, which costs what it gains (16 x 2000 slots of 4 heads, 64 and 128 rows: 44 / 48, 76
+// / 71 at d = 128, 36 / 42, 61 / 62 at d = 64).
 constexpr int64_t kChunkFrom = 33;
 constexpr int64_t kChunkWork = int64_t{3} << 21;  // rows x slots x key heads
 bool by_chunks(const zl_kv4_cache& c, int64_t rows, bool weights) {
@@ -749,7 +762,8 @@ struct Layout {
 Layout layout(const zl_kv4_cache& c, int32_t group, int32_t max_new, bool weights) {
   const int64_t rows = (int64_t)group * max_new, tile = 8 * row_columns(rows);
   // room for either kernel's parts, so that a call of fewer rows or without weights fits where this one does
-  const int64_t part_rows = 2 * (rows < kChunkFrom ? kMaxBlocks * tile : std::max<int64_t>(kMaxBlocks * tile, kChunkMaxBlocks * kChunkRows));
+  const int64_t part_rows =
+      2 * (rows < kChunkFrom ? kMaxBlocks * tile : std::max<int64_t>(kMaxBlocks * tile, kChunkMaxBlocks * kChunkRows));
   Layout l;
   l.ml = part_rows * c.head_dim * 4;
   l.cuts = l.ml + part_rows * 8;
@@ -780,13 +794,15 @@ cudaError_t launch_joined(AttnParams& p, int blocks, cudaStream_t stream, Launch
   return launch_overlapped(zl_kv4_join_kernel<D, kRows, false>, dim3(cuts, kRows / 8), 256, 0, stream, p);
 }
 
-// Blocks of an item's cluster (2^n up to 8, as far as all are resident), or 0: the dealt-out form.  Clusters save its second launch
-// and its search for a block's run, but let a long item wait for its own blocks alone: for slots (that the table has room for) of which a
-// warp gets 8 units at most, or 5 where dealing out would have twice as many blocks.  Measured (us, dealt out / clusters; d = 128, groups of
-// 4, single tokens): 8 items of 300, 2000, 4000, 8000 slots 10.0 / 5.9, 10.0 / 7.1, 10.7 / 8.7, 11.4 / 12.3; 64 items 11.2 / 7.0, 14.5 / 10.0,
-// 15.5 / 13.7, 24.1 / 22.6; 256 items of 300, 1000, 8000 slots 12.9 / 8.3, 16.3 / 13.1, 59.6 / 62.2; one item of 4000, 8000 slots 9.6 / 8.5,
-// 9.4 / 12.0.  Single row tiles go a block each past the resident ones, too: 1024 items of 300, 1000 slots 21.9 / 18.0, 40.7 / 37.1, of 1 to
-// 1024 slots 19.0 / 17.9 (row tiles of a maximum that most sequences may not reach would be blocks without work).
+// Blocks of an item's cluster (2^n up to 8, as far as all are resident), or 0: the dealt-out form.  Clusters save its
+// second launch and its search for a block's run, but let a long item wait for its own blocks alone: for slots (that
+// the table has room for) of which a warp gets 8 units at most, or 5 where dealing out would have twice as many blocks.
+// Measured (us, dealt out / clusters; d = 128, groups of 4, single tokens): 8 items of 300, 2000, 4000, 8000 slots 10.0
+// / 5.9, 10.0 / 7.1, 10.7 / 8.7, 11.4 / 12.3; 64 items 11.2 / 7.0, 14.5 / 10.0, 15.5 / 13.7, 24.1 / 22.6; 256 items of
+// 300, 1000, 8000 slots 12.9 / 8.3, 16.3 / 13.1, 59.6 / 62.2; one item of 4000, 8000 slots 9.6 / 8.5, 9.4 / 12.0.
+// Single row tiles go a block each past the resident ones, too: 1024 items of 300, 1000 slots 21.9 / 18.0, 40.7 / 37.1,
+// of 1 to 1024 slots 19.0 / 17.9 (row tiles of a maximum that most sequences may not reach would be blocks without
+// work).
 int cluster_of(int64_t items, int64_t slots, int tiles, int blocks) {
   int c = kMaxCluster;
   while (c > 1 && items * c > blocks) c /= 2;
@@ -799,7 +815,8 @@ cudaError_t launch_clusters(const AttnParams& p, int cluster, cudaStream_t strea
   using S = Shape<D, NT>;
   const auto kernel = zl_kv4_attn_kernel<D, NT, kScores, true>;
   static PerDeviceOnce once;
-  const cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem); });
+  const cudaError_t e = once.run(
+      [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem); });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.c.n_seqs * p.c.heads * p.max_tiles * cluster);
@@ -832,13 +849,15 @@ cudaError_t launch_attn(AttnParams& p, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int blocks = sms * per_sm < kMaxBlocks ? sms * per_sm : kMaxBlocks;
   p.max_tiles = (p.max_new * p.group + S::kRows - 1) / S::kRows;
-  if (const int cluster = cluster_of((int64_t)p.c.n_seqs * p.c.heads * p.max_tiles, (int64_t)p.c.max_pages << p.c.page_shift, p.max_tiles, blocks)) {
-    // all of an item's rows in one cluster: no launch for the weights either (us, with it / without: 8 items of 1000 slots 8.4 / 7.7, 128 of
-    // 1000 13.3 / 12.0, 512 of 300 13.2 / 11.3)
+  const int64_t items = (int64_t)p.c.n_seqs * p.c.heads * p.max_tiles, slots = (int64_t)p.c.max_pages << p.c.page_shift;
+  if (const int cluster = cluster_of(items, slots, p.max_tiles, blocks)) {
+    // all of an item's rows in one cluster: no launch for the weights either (us, with it / without: 8 items of 1000
+    // slots 8.4 / 7.7, 128 of 1000 13.3 / 12.0, 512 of 300 13.2 / 11.3)
     p.own_weights = kScores && p.max_tiles == 1;
     return launch_clusters<D, NT, kScores>(p, cluster, stream);
   }
-  return launch_joined<D, S::kRows>(p, blocks, stream, [&] { return launch_overlapped(kernel, blocks, kThreads, S::kSmem, stream, p); });
+  return launch_joined<D, S::kRows>(p, blocks, stream,
+                                    [&] { return launch_overlapped(kernel, blocks, kThreads, S::kSmem, stream, p); });
 }
 template <int D, bool kScores>
 cudaError_t launch_attn(AttnParams& p, int64_t rows, bool chunks, int sms, cudaStream_t stream) {
@@ -875,7 +894,8 @@ extern "C" zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, i
   zl_status s = kv4_check(cache, &p.c);
   if (s != ZL_OK) return s;
   if ((s = check_heads(cache, n_q_heads, max_new)) != ZL_OK) return s;
-  if (n_tokens < 0 || n_tokens > INT32_MAX || !(scale > 0.f) || !std::isnormal(scale) || !std::isfinite(decay)) return ZL_ERR_INVALID_ARG;
+  if (n_tokens < 0 || n_tokens > INT32_MAX || !(scale > 0.f) || !std::isnormal(scale) || !std::isfinite(decay))
+    return ZL_ERR_INVALID_ARG;
   if ((!starts && n_tokens != cache->n_seqs) || (weights && !weights_out)) return ZL_ERR_INVALID_ARG;
   if (cache->n_seqs == 0) return ZL_OK;
   if (n_tokens > 0) {  // without tokens the weights still carry over
@@ -886,7 +906,8 @@ extern "C" zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, i
     return ZL_OK;
   }
   if (!workspace) return ZL_ERR_INVALID_ARG;
-  if (!kv4_aligned(workspace, 16) || !kv4_aligned(starts, 4) || !kv4_aligned(weights, 4) || !kv4_aligned(weights_out, 4)) return ZL_ERR_ALIGN;
+  if (!kv4_aligned(workspace, 16) || !kv4_aligned(starts, 4) || !kv4_aligned(weights, 4) || !kv4_aligned(weights_out, 4))
+    return ZL_ERR_ALIGN;
   if (weights_out && (cache->n_seqs > 65535 || cache->n_kv_heads > 65535)) return ZL_ERR_UNSUPPORTED;
   int sms = 0;
   if ((s = check_device(&sms)) != ZL_OK) return s;
@@ -916,15 +937,17 @@ extern "C" zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, i
   cudaError_t e = cudaSuccess;
   if (n_tokens > 0) {
     const bool chunks = by_chunks(*cache, rows, weights_out != nullptr);
-    if (cache->head_dim == 128) e = weights_out ? launch_attn<128, true>(p, rows, chunks, sms, st) : launch_attn<128, false>(p, rows, chunks, sms, st);
-    else e = weights_out ? launch_attn<64, true>(p, rows, chunks, sms, st) : launch_attn<64, false>(p, rows, chunks, sms, st);
+    if (cache->head_dim == 128)
+      e = weights_out ? launch_attn<128, true>(p, rows, chunks, sms, st) : launch_attn<128, false>(p, rows, chunks, sms, st);
+    else
+      e = weights_out ? launch_attn<64, true>(p, rows, chunks, sms, st) : launch_attn<64, false>(p, rows, chunks, sms, st);
   }
   if (e == cudaSuccess && weights_out && cache->max_pages > 0 && !p.own_weights) {
     const int64_t slots = (int64_t)cache->max_pages * cache->page;
     const bool few = l.score_rows <= 8;
     const int block_slots = kWeightThreads * (few ? 4 : 1);
-    e = launch_overlapped(few ? zl_kv4_weights_kernel<4, 4> : zl_kv4_weights_kernel<1, 16>,
-                          dim3((unsigned)((slots + block_slots - 1) / block_slots), cache->n_kv_heads, cache->n_seqs), kWeightThreads,
+    const dim3 grid((unsigned)((slots + block_slots - 1) / block_slots), cache->n_kv_heads, cache->n_seqs);
+    e = launch_overlapped(few ? zl_kv4_weights_kernel<4, 4> : zl_kv4_weights_kernel<1, 16>, grid, kWeightThreads,
                           (size_t)l.score_rows * 4, st, p);
   }
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;

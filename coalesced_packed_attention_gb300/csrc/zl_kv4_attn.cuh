@@ -8,10 +8,10 @@ namespace zl {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLow = -1e30f;     // the reference of rows that have seen nothing
 constexpr float kRescale = 8.f;    // the maximum may lag by 2^8 before the sums are rescaled
-// P = 2^(score - reference) is rounded to fp16, whose smallest number is 2^-24: at a reference of the maximum itself, weights below
-// 2^-25 of it would be lost in O but not in the sum (O too small by up to slots x 2^-25, 3 % at 2^20 slots).  With the reference
-// 2^7 below it P is up to 2^7, with the lag 2^15, of fp16's 2^16, and what is lost lies below 2^-32.  Scores of 2^20 and more keep the room for
-// their own rounding instead.
+// P = 2^(score - reference) is rounded to fp16, whose smallest number is 2^-24: at a reference of the maximum itself,
+// weights below 2^-25 of it would be lost in O but not in the sum (O too small by up to slots x 2^-25, 3 % at 2^20
+// slots).  With the reference 2^7 below it P is up to 2^7, with the lag 2^15, of fp16's 2^16, and what is lost lies
+// below 2^-32.  Scores of 2^20 and more keep the room for their own rounding instead.
 constexpr float kBelow = 7.f, kFar = 0x1p20f;
 __device__ __forceinline__ float reference_of(float top) { return fabsf(top) < kFar ? top - kBelow : top; }
 __device__ __forceinline__ float lag_of(float ref) { return fabsf(ref) < kFar ? kBelow + kRescale : kRescale; }
@@ -19,7 +19,7 @@ __device__ __forceinline__ float lag_of(float ref) { return fabsf(ref) < kFar ? 
 // An item cut between blocks: its first block describes it for the join.
 struct alignas(16) Cut {
   int32_t parts;   // 0: the item was not cut, or none that begins in this block
-  int32_t which;   // part of its first block, 2 block + (0 the block's first segment, 1 another); the following blocks' parts are their first
+  int32_t which;   // part of its first block, 2 block + (0 the block's first segment, 1 another); the next blocks' are their first
   int32_t token0;  // row of the item's sequence in q and o
   int32_t head0;   // first query head
   int32_t row0, rows;
@@ -98,10 +98,11 @@ struct Walk {
 };
 
 
-// The block's run: false where it has none.  Every thread calls it; warp_sums has a number a warp, *seq_before and *seq are
-// shared.  *each: cost of a full run.
+// The block's run: false where it has none.  Every thread calls it; warp_sums has a number a warp, *seq_before and *seq
+// are shared.  *each: cost of a full run.
 template <int kThreads, int kLeast, typename W>
-__device__ bool first_segment_of(const AttnParams& p, int64_t* warp_sums, int64_t* seq_before, int* seq, W& w, int64_t* each_out) {
+__device__ bool first_segment_of(const AttnParams& p, int64_t* warp_sums, int64_t* seq_before, int* seq, W& w,
+                                 int64_t* each_out) {
   if (threadIdx.x == 0) *seq = -1;
   const int n = p.c.n_seqs, per = (n + kThreads - 1) / kThreads;
   const int b0 = min(n, (int)threadIdx.x * per), b1 = min(n, b0 + per);

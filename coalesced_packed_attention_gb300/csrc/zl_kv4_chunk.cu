@@ -1,22 +1,23 @@
 // Attention of many rows over the 4-bit cache: chunks of prompts, drafted tokens of large groups.
 //
-// With many rows (tokens x group) a key head, forming fp16 operands from codes for every 16 rows is what a pass over the
-// cache costs (zl_kv4_attn.cu, which also has the rule between the two).  Here it is done once for 128 rows: eight warps turn a block of 128 slots into
-// fp16 tiles in shared memory (exact: code * scale has six bits), and the tensor core takes them as tcgen05 operands,
+// With many rows (tokens x group) a key head, forming fp16 operands from codes for every 16 rows is what a pass over
+// the cache costs (zl_kv4_attn.cu, which also has the rule between the two).  Here it is done once for 128 rows: eight
+// warps turn a block of 128 slots into fp16 tiles in shared memory (exact: code * scale has six bits), and the tensor
+// core takes them as tcgen05 operands,
 //   S = Q K^T (both from shared memory),  O += P V (P from tensor memory, V channel-major),
 // with 128 rows to a tile and S, P and O in tensor memory; one warpgroup does the softmax, a thread a row.
 //
-// Per block of 128 slots the tensor core works 1024 cycles (d = 128), the exponentials of 128 rows take 1024, and shared
-// memory moves 178 KB (codes in and out 18 + 18, tiles in 64, operands out 96): 1400 cycles.  Measured, a block takes some 3500
-// (128 rows over 16 x 4096 slots of 8 key heads, d = 128: 67 us, 27 blocks an SM; 16-row passes 165; rows read back and causal
-// attention 110): the chain S -> maximum -> exponentials -> P -> P V of the one warpgroup that a tile of 128 rows has, each step
-// some 400 to 1200 cycles with its waits.  The scores kept in 208 registers a thread between maximum and exponentials, with the
-// next block's keys formed ahead of this block's values, took as long (67 us).  Rows that a tile lacks cost nothing in the
-// softmax (their warps pass by) and the same in the products.
-// Order: S of a block is issued ahead of P V of the one before it, so that the softmax always has scores to work on; two
-// buffers each of S, P, K and V, three of codes.
-// Roles (448 threads, one block an SM): warps 0-3 softmax and output (thread = row = TMEM lane), 4-11 operands, 12 products,
-// 13 copies.  TMEM (512 columns): S [0,128) [128,256), O [256,256+d), P [384,448) [448,512).
+// Per block of 128 slots the tensor core works 1024 cycles (d = 128), the exponentials of 128 rows take 1024, and
+// shared memory moves 178 KB (codes in and out 18 + 18, tiles in 64, operands out 96): 1400 cycles.  Measured, a block
+// takes some 3500 (128 rows over 16 x 4096 slots of 8 key heads, d = 128: 67 us, 27 blocks an SM; 16-row passes 165;
+// rows read back and causal attention 110): the chain S -> maximum -> exponentials -> P -> P V of the one warpgroup
+// that a tile of 128 rows has, each step some 400 to 1200 cycles with its waits.  The scores kept in 208 registers a
+// thread between maximum and exponentials, with the next block's keys formed ahead of this block's values, took as long
+// (67 us).  Rows that a tile lacks cost nothing in the softmax (their warps pass by) and the same in the products.
+// Order: S of a block is issued ahead of P V of the one before it, so that the softmax always has scores to work on;
+// two buffers each of S, P, K and V, three of codes.
+// Roles (448 threads, one block an SM): warps 0-3 softmax and output (thread = row = TMEM lane), 4-11 operands, 12
+// products, 13 copies.  TMEM (512 columns): S [0,128) [128,256), O [256,256+d), P [384,448) [448,512).
 // Items, cuts and the join are those of the other kernel, with tiles of 128 rows and units of 128 slots.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -164,7 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnPar
       }
     }
     if (abort_flag)  // the copies in flight land before the block's shared memory goes back (a bounded wait each)
-      for (uint32_t i = 1; i <= kCodeStages && i <= it; ++i) mbar_wait(codes_full + (it - i) % kCodeStages, (it - i) / kCodeStages & 1);
+      for (uint32_t i = 1; i <= kCodeStages && i <= it; ++i)
+        mbar_wait(codes_full + (it - i) % kCodeStages, (it - i) / kCodeStages & 1);
   } else if (warp == 12) {
     // ------------------------------------------------------------ products
     // The whole warp runs the loop; one elected lane executes each product and commit.
@@ -220,8 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnPar
         for (int i = 0; i < kLoads; ++i) raw[i] = make_uint4(0, 0, 0, 0);
         if (row < seg.n * p.group) {
           const int tok = row / p.group;
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(seg.first + tok) * p.q_stride +
-                                                            (int64_t)(seg.head * p.group + row - tok * p.group) * D + half * (D / 2));
+          const int64_t head_at = (int64_t)(seg.head * p.group + row - tok * p.group) * D + half * (D / 2);
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(seg.first + tok) * p.q_stride + head_at);
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) raw[i] = src[i];
         }
@@ -245,7 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnPar
             memcpy(&o[y], &h, 4);
           }
           const int box = D == 128 ? half : 0, chunk = D == 128 ? i : half * kLoads + i;
-          *reinterpret_cast<uint4*>(smem + L::kQ + box * L::kBox + r * 128 + ((chunk ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(smem + L::kQ + box * L::kBox + r * 128 + ((chunk ^ (r & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
         if (half == 0) row_factor[r] = fmaxf(up * p.scale_log2, 0x1p-126f);  // not 0, which -inf is multiplied by
         fence_proxy_async_smem();
@@ -274,7 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnPar
             kv4_decode(w[i], v);
             const uint32_t s = (i < 2) != upper ? sa : sb;
             const int chunk = ((part & 1) * 4 + (i ^ (upper ? 2 : 0))) ^ (key & 7);
-            *reinterpret_cast<uint4*>(dst + (chunk << 4)) = make_uint4(kv4_mul(v[0], s), kv4_mul(v[1], s), kv4_mul(v[2], s), kv4_mul(v[3], s));
+            *reinterpret_cast<uint4*>(dst + (chunk << 4)) =
+                make_uint4(kv4_mul(v[0], s), kv4_mul(v[1], s), kv4_mul(v[2], s), kv4_mul(v[3], s));
           }
         }
         fence_proxy_async_smem();
@@ -432,13 +436,15 @@ __global__ void __launch_bounds__(kThreads, 1) zl_kv4_chunk_kernel(const AttnPar
             for (int e = 0; e < 32; e += 8) {
               uint32_t w[4];
 #pragma unroll
-              for (int y = 0; y < 4; ++y) w[y] = pack_bf16(__uint_as_float(o[e + 2 * y]) * inv, __uint_as_float(o[e + 2 * y + 1]) * inv);
+              for (int y = 0; y < 4; ++y)
+                w[y] = pack_bf16(__uint_as_float(o[e + 2 * y]) * inv, __uint_as_float(o[e + 2 * y + 1]) * inv);
               *reinterpret_cast<uint4*>(p.o + at * D + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(p.part_o + ((int64_t)part * kChunkRows + r) * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              *reinterpret_cast<uint4*>(p.part_o + ((int64_t)part * kChunkRows + r) * D + c + e) =
+                  make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
         if (row < rows) {
@@ -460,7 +466,8 @@ template <int D>
 cudaError_t launch(const AttnParams& p, int blocks, cudaStream_t stream) {
   const auto kernel = zl_kv4_chunk_kernel<D>;
   static PerDeviceOnce once;
-  const cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem); });
+  const cudaError_t e = once.run(
+      [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem); });
   if (e != cudaSuccess) return e;
   return launch_overlapped(kernel, blocks, kThreads, Layout<D>::kSmem, stream, p);
 }

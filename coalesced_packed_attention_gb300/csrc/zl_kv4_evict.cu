@@ -1,16 +1,16 @@
 // Eviction from the 4-bit cache by accumulated attention weight.
 //
-// Every (sequence, key head) keeps `keep` of its n slots: those with a position above newest - recent first, then
-// the largest weights, ties to the lower slot.  Finding the border is a radix selection over the weights' bits, eight at a
-// time; survivors behind slot keep and the slots given up before it are then numbered in slot order, and the i-th survivor
-// moves into the i-th slot given up.  Nothing is sorted and unmoved rows are not touched: a step's eviction moves one row a head.
-// Numbering needs one prefix sum: with k(s) slots kept before slot s, a slot given up has number s - k(s), a survivor k(s) - k(keep).
-// A cluster of up to 8 blocks takes a head, each a run of its slots, which it loads once and holds in shared memory; they
-// exchange histograms and counts through each other's shared memory.  A head's blocks also make its moves where they are few;
-// many are made by a second launch over all SMs.
-// Bound by latency at serving sizes (seven exchanges and three trips to memory), by the weights' and positions' bytes past them.
-// Measured: one of 1025 slots of each of 64 heads 7.5 us; 16 384 slots of 4 heads to 2048 15 us and 4.5 for the moves; 32 x 8 heads
-// of 100 to 8192 slots to 2048, d = 64, 22 us and 20.
+// Every (sequence, key head) keeps `keep` of its n slots: those with a position above newest - recent first, then the
+// largest weights, ties to the lower slot.  Finding the border is a radix selection over the weights' bits, eight at a
+// time; survivors behind slot keep and the slots given up before it are then numbered in slot order, and the i-th
+// survivor moves into the i-th slot given up.  Nothing is sorted and unmoved rows are not touched: a step's eviction
+// moves one row a head.  Numbering needs one prefix sum: with k(s) slots kept before slot s, a slot given up has number
+// s - k(s), a survivor k(s) - k(keep).  A cluster of up to 8 blocks takes a head, each a run of its slots, which it
+// loads once and holds in shared memory; they exchange histograms and counts through each other's shared memory.  A
+// head's blocks also make its moves where they are few; many are made by a second launch over all SMs.
+// Bound by latency at serving sizes (seven exchanges and three trips to memory), by the weights' and positions' bytes
+// past them.  Measured: one of 1025 slots of each of 64 heads 7.5 us; 16 384 slots of 4 heads to 2048 15 us and 4.5 for
+// the moves; 32 x 8 heads of 100 to 8192 slots to 2048, d = 64, 22 us and 20.
 #include <cuda_runtime.h>
 
 #include "zl_internal.h"
@@ -38,7 +38,8 @@ struct EvictParams {
   float* weights_out;
   int32_t* positions_out;
   int32_t* counts;  // [sequence][key head]: moves, where a launch of their own makes them (else null)
-  uint32_t* moves;  // [sequence][key head][4][capacity]: slots given up, their rows; survivors' slots, their rows (16 tile + row); see kGone
+  // [sequence][key head][4][capacity]: slots given up, their rows; survivors' slots, their rows (16 tile + row); see kGone
+  uint32_t* moves;
   int32_t keep, recent, capacity;
 };
 
@@ -58,9 +59,9 @@ __device__ __forceinline__ int peer(const int* mine, uint32_t rank) {
   return v;
 }
 
-// 16 lanes a move: codes of keys and values in 16-byte pieces, scales, weight and position.  A lane's piece of a slot or of a
-// row is found by a pointer rather than by branches, so that all loads are under way together (a register that two branches
-// load into is waited for between them: 14 us instead of 5 for 1790 rows of each of 4 heads).
+// 16 lanes a move: codes of keys and values in 16-byte pieces, scales, weight and position.  A lane's piece of a slot
+// or of a row is found by a pointer rather than by branches, so that all loads are under way together (a register that
+// two branches load into is waited for between them: 14 us instead of 5 for 1790 rows of each of 4 heads).
 template <int D>
 struct Piece {
   static constexpr int kPieces = D / 32;  // of a row's codes
@@ -75,16 +76,22 @@ struct Piece {
     idle = !code && !number && (l < 8 || l >= 8 + 2 * (D / 64));
     at = code ? (l / kPieces) * 8 * D + (l % kPieces) * 16 : 16 * D + ((l - 8) / (D / 64)) * D + ((l - 8) % (D / 64)) * 4;
     pitch = number ? 4 : code ? D / 2 : D / 16;
-    in = l == 14 ? reinterpret_cast<const uint8_t*>(p.weights + base) : l == 15 ? reinterpret_cast<const uint8_t*>(p.positions + base) : p.c.data;
-    out = l == 14 ? reinterpret_cast<uint8_t*>(p.weights_out + base) : l == 15 ? reinterpret_cast<uint8_t*>(p.positions_out + base) : p.c.data;
+    in = l == 14   ? reinterpret_cast<const uint8_t*>(p.weights + base)
+         : l == 15 ? reinterpret_cast<const uint8_t*>(p.positions + base)
+                   : p.c.data;
+    out = l == 14   ? reinterpret_cast<uint8_t*>(p.weights_out + base)
+          : l == 15 ? reinterpret_cast<uint8_t*>(p.positions_out + base)
+                    : p.c.data;
   }
   // bytes to the piece of slot or row x
-  __device__ int64_t offset(uint32_t x) const { return number ? (int64_t)(x & ~kGone) * 4 : (int64_t)(x >> 4) * (18 * D) + at + (x & 15) * pitch; }
+  __device__ int64_t offset(uint32_t x) const {
+    return number ? (int64_t)(x & ~kGone) * 4 : (int64_t)(x >> 4) * (18 * D) + at + (x & 15) * pitch;
+  }
 };
 // Moves i, i + step, .. of a head, kAtOnce of them, whose numbers of slots or rows (a lane's own kind) are known.
 template <int D, int kAtOnce>
-__device__ __forceinline__ void move_pieces(const EvictParams& p, const Piece<D>& piece, const uint32_t (&to)[kAtOnce], const uint32_t (&from)[kAtOnce],
-                                            int i, int step, int end) {
+__device__ __forceinline__ void move_pieces(const EvictParams& p, const Piece<D>& piece, const uint32_t (&to)[kAtOnce],
+                                            const uint32_t (&from)[kAtOnce], int i, int step, int end) {
   uint4 v[kAtOnce];
   uint32_t u[kAtOnce];
   bool does[kAtOnce];
@@ -135,7 +142,7 @@ __device__ __forceinline__ void move_row(const EvictParams& p, int b, int h, int
 template <int D, bool kHeld>
 __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const EvictParams p) {
   extern __shared__ int held[];            // [2][run]: weights, positions
-  __shared__ int local[4][512];            // a round's histogram, of a quarter of the warps; the first round's: others, then the recent ones
+  __shared__ int local[4][512];            // a round's histogram, of a quarter of the warps; the first's: others, then recent ones
   __shared__ int hist[2][512];             // of the block, of two rounds in turn
   __shared__ int warp_sums[2][kEvictWarps];
   __shared__ uint64_t warp_least[kEvictWarps];
@@ -207,7 +214,8 @@ __global__ void __launch_bounds__(kEvictThreads) zl_kv4_evict_kernel(const Evict
         bool out = false;
 #pragma unroll
         for (int z = 0; z < y; ++z) out |= gone[z] == i;
-        const uint64_t claim = ((uint64_t)(is_recent(held_pos[i]) ? 1 : 0) << 63) | ((uint64_t)rank_of(held_w[i]) << 31) | (uint32_t)(INT32_MAX - i);
+        const uint64_t claim = ((uint64_t)(is_recent(held_pos[i]) ? 1 : 0) << 63) | ((uint64_t)rank_of(held_w[i]) << 31) |
+                               (uint32_t)(INT32_MAX - i);
         if (!out && claim < least) least = claim;
       }
 #pragma unroll
@@ -467,7 +475,8 @@ template <int D, bool kHeld>
 cudaError_t launch_evict(const EvictParams& p, int cluster, int64_t items, int64_t run, cudaStream_t stream) {
   const auto kernel = zl_kv4_evict_kernel<D, kHeld>;
   static PerDeviceOnce once;
-  cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld ? kHeldSlots * 8 : 0); });
+  constexpr int kMost = kHeld ? kHeldSlots * 8 : 0;
+  cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost); });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * cluster));
@@ -530,8 +539,8 @@ extern "C" zl_status zl_kv4_evict(const zl_kv4_cache* cache, const float* weight
   p.keep = keep;
   p.recent = recent;
   p.capacity = (int32_t)(slots / 2);
-  // blocks of a head: enough that a thread has four slots at most, as far as the SMs have room for two blocks each; more
-  // where its slots would not fit their shared memory
+  // blocks of a head: enough that a thread has four slots at most, as far as the SMs have room for two blocks each;
+  // more where its slots would not fit their shared memory
   int cluster = 1;
   while (cluster < kCluster && ((slots > (int64_t)cluster * 4 * kEvictThreads && items * cluster * 2 <= 2 * sms) ||
                                 slots > (int64_t)cluster * (kHeldSlots - 32)))
@@ -540,11 +549,15 @@ extern "C" zl_status zl_kv4_evict(const zl_kv4_cache* cache, const float* weight
   const bool held = run <= kHeldSlots;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (cache->head_dim == 128) e = held ? launch_evict<128, true>(p, cluster, items, run, st) : launch_evict<128, false>(p, cluster, items, run, st);
-  else e = held ? launch_evict<64, true>(p, cluster, items, run, st) : launch_evict<64, false>(p, cluster, items, run, st);
+  if (cache->head_dim == 128)
+    e = held ? launch_evict<128, true>(p, cluster, items, run, st) : launch_evict<128, false>(p, cluster, items, run, st);
+  else
+    e = held ? launch_evict<64, true>(p, cluster, items, run, st) : launch_evict<64, false>(p, cluster, items, run, st);
   if (e == cudaSuccess && apart) {
-    const dim3 grid((unsigned)((most + kMoves - 1) / kMoves), (unsigned)(items < 65535 ? items : 65535), (unsigned)((items + 65534) / 65535));
-    e = launch_overlapped(cache->head_dim == 128 ? zl_kv4_move_kernel<128> : zl_kv4_move_kernel<64>, grid, kMoveThreads, 0, st, p);
+    const dim3 grid((unsigned)((most + kMoves - 1) / kMoves), (unsigned)(items < 65535 ? items : 65535),
+                    (unsigned)((items + 65534) / 65535));
+    const auto kernel = cache->head_dim == 128 ? zl_kv4_move_kernel<128> : zl_kv4_move_kernel<64>;
+    e = launch_overlapped(kernel, grid, kMoveThreads, 0, st, p);
   }
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }

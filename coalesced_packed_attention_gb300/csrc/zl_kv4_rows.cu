@@ -1,14 +1,14 @@
 // Rows of the 4-bit cache: new keys and values in, all of a sequence's out.
 //
 // In: a block of 16 channels has the scale s nearest to max|x| / 6 (five bits of exponent, three of mantissa) and each
-// channel the code nearest to |x| / s, ties to even.  The codes are those of exact arithmetic: quotients of bf16 numbers
-// by 6 or by a four-bit s either hit a border between two codes (scales) or miss it by 2^-11 and more, so
-// a product with the reciprocal, off by 2^-20 at most, rounded to a multiple of 2^-16, is on the right side, or on
-// the border, where the conversion's own ties to even decide.  (IEEE divisions took two thirds of the time.)
+// channel the code nearest to |x| / s, ties to even.  The codes are those of exact arithmetic: quotients of bf16
+// numbers by 6 or by a four-bit s either hit a border between two codes (scales) or miss it by 2^-11 and more, so a
+// product with the reciprocal, off by 2^-20 at most, rounded to a multiple of 2^-16, is on the right side, or on the
+// border, where the conversion's own ties to even decide.  (IEEE divisions took two thirds of the time.)
 // Out: code * s has six bits at most, exact in fp16 and bf16.
 // Both move bytes: a thread takes 8 channels (16 bytes of bf16, 4 of codes), two threads share a scale, and has several
-// loads under way.  Measured at 8 heads, d = 128: 14 336 tokens in 21 us (75 MB, 3.6 TB/s: the arithmetic of the codes and one wave of
-// blocks), 4 x 16 384 slots out in 58 us (344 MB, 5.9 TB/s, 0.89 of a copy).
+// loads under way.  Measured at 8 heads, d = 128: 14 336 tokens in 21 us (75 MB, 3.6 TB/s: the arithmetic of the codes
+// and one wave of blocks), 4 x 16 384 slots out in 58 us (344 MB, 5.9 TB/s, 0.89 of a copy).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -63,7 +63,8 @@ __device__ __forceinline__ uint32_t encode8(const uint32_t (&w)[4], float inv) {
   return o;
 }
 
-// Largest magnitudes of a block of 16, as bf16 bits: this thread's 8 numbers and its neighbour's; above 0x7F80 where one is NaN.
+// Largest magnitudes of a block of 16, as bf16 bits: this thread's 8 numbers and its neighbour's; above 0x7F80 where
+// one is NaN.
 __device__ __forceinline__ uint32_t abs_max(uint32_t a, uint32_t b) {
   uint32_t o;
   asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
@@ -123,8 +124,8 @@ __global__ void __launch_bounds__(kRowThreads) zl_kv4_write_kernel(const WritePa
     s_scales[lane] = tile + 16 * D + (slot & 15) * (D / 16);
   }
   __syncthreads();
-  // A thread keeps to one column: 8 channels of a head's key or value; where a token has fewer than the block has threads,
-  // several tokens side by side.  The two threads of a scale are neighbours: columns come by the 16.
+  // A thread keeps to one column: 8 channels of a head's key or value; where a token has fewer than the block has
+  // threads, several tokens side by side.  The two threads of a scale are neighbours: columns come by the 16.
   const int per_row = p.c.heads * (D / 8), columns = 2 * per_row;
   const int wide = min(columns, kRowThreads), side = kRowThreads / wide;
   const int head_step = (18 * D) << (p.c.page_shift - 4);
@@ -260,7 +261,8 @@ __global__ void __launch_bounds__(kRowThreads) zl_kv4_read_kernel(const ReadPara
           sb[i] = src[16 * D + which * D + row * (D / 16) + c8 / 2];
         }
       }
-      __nv_bfloat16* dst = (which ? p.out[1] : p.out[0]) + (row0 + tile * kKv4Slots + r0) * (which ? p.stride[1] : p.stride[0]) + h * D + c8 * 8;
+      const int64_t stride = which ? p.stride[1] : p.stride[0];
+      __nv_bfloat16* dst = (which ? p.out[1] : p.out[0]) + (row0 + tile * kKv4Slots + r0) * stride + h * D + c8 * 8;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         uint32_t v[4];
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kRowThreads) zl_kv4_read_kernel(const ReadPara
         const uint32_t s2 = kv4_scale2(sb[i], sb[i]);
         const uint4 o = make_uint4(to_bf16x2(kv4_mul(v[0], s2)), to_bf16x2(kv4_mul(v[1], s2)), to_bf16x2(kv4_mul(v[2], s2)),
                                    to_bf16x2(kv4_mul(v[3], s2)));
-        if (r0 + i * kRowsAtOnce < rows) *reinterpret_cast<uint4*>(dst + i * kRowsAtOnce * (which ? p.stride[1] : p.stride[0])) = o;
+        if (r0 + i * kRowsAtOnce < rows) *reinterpret_cast<uint4*>(dst + i * kRowsAtOnce * stride) = o;
       }
     }
   }
@@ -307,7 +309,8 @@ extern "C" zl_status zl_kv4_write(const zl_kv4_cache* cache, const void* k, int6
   p.per_block = (int32_t)(even < kWriteTokens ? even : kWriteTokens);
   const unsigned blocks = (unsigned)((n_tokens + p.per_block - 1) / p.per_block);
   const auto kernel = cache->head_dim == 128 ? zl_kv4_write_kernel<128> : zl_kv4_write_kernel<64>;
-  return launch_overlapped(kernel, blocks, kRowThreads, 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
+  const cudaError_t e = launch_overlapped(kernel, blocks, kRowThreads, 0, static_cast<cudaStream_t>(stream), p);
+  return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
 
 extern "C" zl_status zl_kv4_read(const zl_kv4_cache* cache, void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,

@@ -549,12 +549,13 @@ ZL_API zl_status zl_causal_get_device_status(const zl_causal_plan* plan, void* s
  * Slot s of sequence b is slot s % page of page pages[b][s / page].  Sequences may share pages that no call writes.
  * ---------------------------------------------------------------------------------- */
 typedef struct {
-  int32_t n_seqs;       /* >= 0 */
+  int32_t n_seqs;       /* 0 .. 2^20 */
   int32_t n_kv_heads;   /* 1 .. 1024 */
   int32_t head_dim;     /* 64 or 128 */
   int32_t page;         /* slots a page: 16, 32, 64, 128 or 256 */
-  int32_t max_pages;    /* pages a sequence may have: the width of `pages`; max_pages * page < 2^30, n_kv_heads * max_pages * page < 2^35 */
-  int64_t n_pages;      /* pages of `data` */
+  int32_t max_pages;    /* pages a sequence may have: the width of `pages`; max_pages * page < 2^30 and
+                         * n_kv_heads * max_pages * page < 2^35 */
+  int64_t n_pages;      /* pages of `data`; n_pages * n_kv_heads * page < 2^32 */
   void* data;           /* [n_pages][n_kv_heads][page / 16][18 d], 16-byte aligned */
   const int32_t* pages; /* device [n_seqs][max_pages]; entries past a sequence's slots are not read */
   const int32_t* lens;  /* device [n_seqs]: slots in use, the new tokens of the call among them */
@@ -572,18 +573,19 @@ typedef struct {
  * n_tokens is n_seqs and sequence b brings token b) for its last slots, [lens[b] - n, lens[b]); tokens for slots
  * below 0 and tokens of no sequence are left out.  Each block of 16 channels takes the scale nearest to its
  * largest magnitude / 6 and each channel the nearest code, ties to even; NaN is held as 0, infinities as the largest
- * magnitude, 6 * 2^13.  positions (device int32 [n_tokens]) and slot_positions (int32 [n_seqs, n_kv_heads, max_pages * page]),
- * both or neither: the slot's position becomes the token's, for eviction.
- * Accumulated weights are not its own: zl_kv4_attn_fwd with weights begins new tokens' slots at 0, and after an attention
- * without weights the caller sets theirs.
+ * magnitude, 6 * 2^13.  positions (device int32 [n_tokens]) and slot_positions (int32 [n_seqs, n_kv_heads,
+ * max_pages * page]), both or neither: the slot's position becomes the token's, for eviction.
+ * Accumulated weights are not its own: zl_kv4_attn_fwd with weights begins new tokens' slots at 0, and after an
+ * attention without weights the caller sets theirs.
  * Pages that it writes belong to one sequence alone. */
 ZL_API zl_status zl_kv4_write(const zl_kv4_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                               int64_t n_tokens, const int32_t* starts, const int32_t* positions, int32_t* slot_positions,
                               void* stream);
 
-/* What the cache holds, as bf16 rows: slot s of sequence b becomes row row_starts[b] + s (device int64 [n_seqs]) of k_out,
- * v_out [n_rows, n_kv_heads, d] with token strides, s < lens[b].  Rows of no sequence are left as they were; sequences' rows must be disjoint.
- * Slots of a bad page read as 0.  The rows serve zl_causal_attn_fwd (kv_offset = row_starts[b]). */
+/* What the cache holds, as bf16 rows: slot s of sequence b becomes row row_starts[b] + s (device int64 [n_seqs]) of
+ * k_out, v_out [n_rows, n_kv_heads, d] with token strides, s < lens[b].  Rows of no sequence are left as they were;
+ * sequences' rows must be disjoint.  Slots of a bad page read as 0.  The rows serve zl_causal_attn_fwd
+ * (kv_offset = row_starts[b]). */
 ZL_API zl_status zl_kv4_read(const zl_kv4_cache* cache, void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
                              int64_t n_rows, const int64_t* row_starts, void* stream);
 
@@ -595,17 +597,21 @@ ZL_API zl_status zl_kv4_attn_workspace(const zl_kv4_cache* cache, int32_t n_q_he
 /* Attention of the newest tokens over the cache, which holds their own keys and values already: with n tokens
  * [starts[b], starts[b + 1]) (as zl_kv4_write; at most max_new of a sequence) query i sees slots j <= lens[b] - n + i.
  *   q: bf16 [n_tokens, n_q_heads, d] with a token stride; n_q_heads a multiple of n_kv_heads, query head h reads key
- *   head h / group, group = n_q_heads / n_kv_heads <= 128 and max_new * group <= 8192 (ZL_ERR_UNSUPPORTED past them).  o: bf16 [n_tokens, n_q_heads, d] contiguous; lse: fp32 [n_tokens, n_q_heads]; 0 and
- *   -inf for a query that sees no slot.  Rows of no sequence are left as they were.
- *   weights, weights_out: fp32 [n_seqs, n_kv_heads, max_pages * page] or NULL.  weights_out[slot] = decay * weights[slot] + the sum of the
- *   slot's softmax weights over the new tokens and the group's heads, for slots below lens[b]; weights counts as 0 where it is
- *   NULL and in the new tokens' slots.  The two may be the same buffer.  decay: finite.
- *   scale: positive, normal.  workspace: zl_kv4_attn_workspace bytes (no call may share it with one that may run at the same time).
- * P is rounded to fp16 (its row's running maximum is 2^7 to 2^15): weights below 2^-32 of a row's largest count as 0 in O, not in
- * lse or weights_out (below 2^-25 where scores reach 2^20, to base 2, in magnitude; scores have to stay below 2^28).  Sums are fp32.
- * Results repeat bit for bit.
- * workspace bytes for max_new tokens, or with weights, serve fewer tokens and calls without weights of the same cache.
- * For prompts (more than some 300 rows, tokens x group, a key head) zl_kv4_read and zl_causal_attn_fwd are faster. */
+ *   head h / group, group = n_q_heads / n_kv_heads <= 128 and max_new * group <= 8192 (ZL_ERR_UNSUPPORTED past them).
+ *   o: bf16 [n_tokens, n_q_heads, d] contiguous; lse: fp32 [n_tokens, n_q_heads]; 0 and -inf for a query that sees no
+ *   slot.  Rows of no sequence are left as they were.
+ *   weights, weights_out: fp32 [n_seqs, n_kv_heads, max_pages * page] or NULL.  weights_out[slot] = decay *
+ *   weights[slot] + the sum of the slot's softmax weights over the new tokens and the group's heads, for slots below
+ *   lens[b]; weights counts as 0 where it is NULL and in the new tokens' slots.  The two may be the same buffer.  Up to
+ *   65535 sequences (ZL_ERR_UNSUPPORTED).  decay: finite.
+ *   scale: positive, normal.  workspace: zl_kv4_attn_workspace bytes (no call may share it with one that may run at the
+ *   same time); those for max_new tokens, or with weights, serve fewer tokens and calls without weights of the same
+ *   cache.
+ * P is rounded to fp16 (its row's running maximum is 2^7 to 2^15): weights below 2^-32 of a row's largest count as 0 in
+ * O, not in lse or weights_out (below 2^-25 where scores reach 2^20, to base 2, in magnitude; scores have to stay below
+ * 2^28).  Sums are fp32.  Results repeat bit for bit.
+ * With weights rows are attended 16 at a time and their scores kept.  For prompts (more than some 300 rows, tokens x
+ * group, a key head) zl_kv4_read and zl_causal_attn_fwd are faster. */
 ZL_API zl_status zl_kv4_attn_fwd(const zl_kv4_cache* cache, const void* q, int64_t q_stride, int64_t n_tokens,
                                  int32_t n_q_heads, const int32_t* starts, int32_t max_new, void* o, float* lse,
                                  const float* weights, float* weights_out, float decay, void* workspace, float scale,
@@ -617,9 +623,9 @@ ZL_API zl_status zl_kv4_evict_workspace(const zl_kv4_cache* cache, int64_t* byte
 /* Every head of a sequence longer than `keep` slots gives up all but `keep` of them.  In order of claim: the slots whose
  * position is above newest - recent (newest: the largest position in the head's slots), then the others; among each the
  * larger weight, then the lower slot (NaN ranks below all numbers).  Survivors in slots >= keep move, in order, into
- * the slots below keep that were given up, in order; other slots stay where they are.  Where either slot of a move lies in a
- * bad page the slot given up stays as it was, with its weight and position.  The new lengths are
- * min(lens[b], keep): the caller sets them.
+ * the slots below keep that were given up, in order; other slots stay where they are.  Where either slot of a move lies
+ * in a bad page the slot given up stays as it was, with its weight and position.  The new lengths are min(lens[b],
+ * keep): the caller sets them.
  *   weights fp32, positions int32 [n_seqs, n_kv_heads, max_pages * page]: by slot, not changed; weights_out,
  *   positions_out: the same for the kept slots, in their new places (rest left as it was); either may be its input
  *   (then only moved slots are written).  keep >= 1, recent >= 0.  workspace: zl_kv4_evict_workspace bytes.

@@ -15,7 +15,8 @@ def lib():
     return ensure_library()
 
 
-@pytest.mark.parametrize("d,page,lens,weights", [(128, 16, [33, 500, 1, 130], False), (64, 64, [200] * 24, True), (128, 256, [250] * 200, False)])
+@pytest.mark.parametrize("d,page,lens,weights", [
+    (128, 16, [33, 500, 1, 130], False), (64, 64, [200] * 24, True), (128, 256, [250] * 200, False)])
 def test_short_calls_one_after_another(d, page, lens, weights):
     """Clusters of every size, launch behind launch, each with outputs of its own: every one of them the first one's."""
     import torch
@@ -43,7 +44,8 @@ def one_hot_cache(scores, v, d, page, table=0):
     k, x = np.zeros((n, 1, d)), np.repeat(np.asarray(v, float)[:, None, None], d, 2)
     k[:, 0, 0] = scores
     c.lens.fill_(n)
-    zl.zl_kv4_write(c, torch.from_numpy(k).bfloat16().cuda(), torch.from_numpy(x).bfloat16().cuda(), torch.tensor([0, n], dtype=torch.int32).cuda())
+    zl.zl_kv4_write(c, torch.from_numpy(k).bfloat16().cuda(), torch.from_numpy(x).bfloat16().cuda(),
+                    torch.tensor([0, n], dtype=torch.int32).cuda())
     data, pages = c.data.cpu().numpy(), c.pages.cpu().numpy()
     kk, vv = ref.sequence(data, pages, 0, 0, n)
     assert np.array_equal(kk, k[:, 0]) and np.array_equal(vv, x[:, 0])
@@ -103,7 +105,8 @@ def test_scores_that_rise_slowly(rows, new, table, d, step):
     for h in range(rows // new):
         p, want, wl = ref.attend_head(q[:, h], k, vv, scale)
         es = scale * 12 * 2.0 ** -22
-        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * es + 2.0 ** -20 + 2.0 ** -22 * 12 * scale + n * F) * (p @ np.abs(vv)) + 2.0 ** -32 * 6 * n
+        tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -32 * 12 * n + \
+            (2.0 ** -11 + 2 * es + 2.0 ** -20 + 2.0 ** -22 * 12 * scale + n * F) * (p @ np.abs(vv))
         assert (np.abs(o[:, h] - want) <= tol).all()
         assert np.abs(lse[:, h] - wl).max() <= 2 * es + 2.0 ** -20 * (1 + np.abs(wl).max()) + n * F
 
@@ -145,7 +148,8 @@ def test_a_prompt_without_keep_then_steps_on_a_budget(shared, graph):
     def call(k):
         n = T[k]
         if k not in calls:
-            inputs = (torch.empty(2 * n, hq + 2 * heads, d, dtype=torch.bfloat16).cuda(), torch.zeros(2 * n, dtype=torch.int32).cuda(), starts_of([n, n])[1])
+            inputs = (torch.empty(2 * n, hq + 2 * heads, d, dtype=torch.bfloat16).cuda(),
+                      torch.zeros(2 * n, dtype=torch.int32).cuda(), starts_of([n, n])[1])
             calls[k] = [inputs, None]
         (qkv, positions, ds), captured = calls[k]
         qkv.copy_(torch.randn(qkv.shape, generator=g))
@@ -153,7 +157,8 @@ def test_a_prompt_without_keep_then_steps_on_a_budget(shared, graph):
 
         def body():
             c.lens.add_(n)
-            zl.qkv_attention_cached(c, qkv, positions, table, d ** -0.5, prompt if k is None else step, starts=ds, max_new=n, keep=k, recent=recent)
+            zl.qkv_attention_cached(c, qkv, positions, table, d ** -0.5, prompt if k is None else step, starts=ds, max_new=n,
+                                    keep=k, recent=recent)
 
         if not graph:
             body()
@@ -290,12 +295,13 @@ def test_a_refused_step_leaves_everything_as_it_was():
     held = (c.data, c.lens, bufs["weights"], bufs["positions"])
     before = [x.clone() for x in held]
     ok = dict(cache=c, qkv=qkv, positions=at, table=table, scale=0.1, bufs=bufs, keep=4)
-    for bad in (dict(keep=0), dict(keep=-3), dict(recent=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=1e-40),
+    for bad in (dict(keep=0), dict(keep=-3), dict(recent=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
+                dict(scale=1e-40),
                 dict(decay=float("inf")), dict(max_new=0), dict(max_new=5000), dict(max_new=64), dict(bufs={**bufs, "o": bufs["o"][:2]}),
                 dict(bufs={**bufs, "lse": bufs["lse"].half()}), dict(bufs={**bufs, "workspace": bufs["workspace"][:64]}),
                 dict(bufs={**bufs, "weights": bufs["weights"][:1]}), dict(bufs={**bufs, "positions": bufs["positions"].long()}),
-                dict(starts=torch.zeros(3, dtype=torch.int32).cuda()), dict(keep=2 ** 31), dict(keep=2 ** 32 + 4), dict(recent=2 ** 31), dict(keep=None, scale=-1.0),
-                dict(keep=None, max_new=0), dict(keep=None, bufs={**bufs, "o": bufs["o"].float()})):
+                dict(starts=torch.zeros(3, dtype=torch.int32).cuda()), dict(keep=2 ** 31), dict(keep=2 ** 32 + 4),
+                dict(recent=2 ** 31), dict(keep=None, scale=-1.0), dict(keep=None, max_new=0), dict(keep=None, bufs={**bufs, "o": bufs["o"].float()})):
         with pytest.raises((zl.ZlError, TypeError, ValueError)):
             zl.qkv_attention_cached(**{**ok, **bad})
         assert all(torch.equal(x, y) for x, y in zip(held, before)), bad
@@ -303,7 +309,8 @@ def test_a_refused_step_leaves_everything_as_it_was():
     assert (c.lens == 4).all()
     for bad in (dict(keep=2 ** 32 + 4), dict(keep=0), dict(recent=2 ** 32)):
         with pytest.raises(zl.ZlError):
-            zl.zl_kv4_evict(**{**dict(cache=c, weights=bufs["weights"], positions=bufs["positions"], keep=3, recent=1, workspace=bufs["workspace"]), **bad})
+            zl.zl_kv4_evict(**{**dict(cache=c, weights=bufs["weights"], positions=bufs["positions"], keep=3, recent=1,
+                                      workspace=bufs["workspace"]), **bad})
 
 
 # ---------------------------------------------------------------- starts, workspaces, streams
@@ -329,10 +336,12 @@ def test_one_workspace_serves_smaller_calls(lens, rows):
     import torch
     new = [12, 9]
     c, data, pages = many(lens, 2, 64, 16, 53, rows) if rows else make_cache(lens, 2, 64, 16, 53)
-    ws = torch.empty(max(zl.zl_kv4_attn_workspace_bytes(c, 8, 16), zl.zl_kv4_attn_workspace_bytes(c, 8, 12, True)), dtype=torch.uint8).cuda()
+    ws = torch.empty(max(zl.zl_kv4_attn_workspace_bytes(c, 8, 16), zl.zl_kv4_attn_workspace_bytes(c, 8, 12, True)),
+                     dtype=torch.uint8).cuda()
     g = torch.Generator().manual_seed(76)
     w_in = torch.rand(c.slot_shape, generator=g).cuda()
-    for now, weights in (([12, 9], False), ([2, 1], False), ([12, 9], True), ([1, 1], True), ([5, 0], False), ([9, 9], False), ([1, 2], True)):
+    for now, weights in (([12, 9], False), ([2, 1], False), ([12, 9], True), ([1, 1], True), ([5, 0], False), ([9, 9], False),
+                         ([1, 2], True)):
         starts, ds = starts_of(now)
         q = torch.randn(sum(now), 8, 64, generator=g).bfloat16().cuda()
         o, lse, w = torch.empty_like(q), torch.empty(sum(now), 8).cuda(), torch.zeros(c.slot_shape).cuda()
