@@ -288,7 +288,8 @@ extern "C" zl_status zl_kv4_write(const zl_kv4_cache* cache, const void* k, int6
   WriteParams p{};
   zl_status s = kv4_check(cache, &p.c);
   if (s != ZL_OK) return s;
-  if (n_tokens < 0 || n_tokens > INT32_MAX || (!positions) != (!slot_positions)) return ZL_ERR_INVALID_ARG;
+  if (n_tokens < 0 || n_tokens > INT32_MAX) return ZL_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!positions) != (!slot_positions)) return ZL_ERR_INVALID_ARG;  // none of no tokens
   if (!starts && n_tokens != cache->n_seqs) return ZL_ERR_INVALID_ARG;
   if (n_tokens == 0 || cache->n_seqs == 0) return ZL_OK;
   const int64_t row = (int64_t)cache->n_kv_heads * cache->head_dim;

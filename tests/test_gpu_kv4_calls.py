@@ -377,3 +377,34 @@ def test_calls_that_cut_items_on_other_streams_at_once(rows):
         want, tol = reference(f64(q), data, pages, lens, starts, 0.1)
         within(f64(o), want["o"], tol["o"], "o")
         within(f64(lse), want["lse"], tol["lse"], "lse")
+
+
+@pytest.mark.parametrize("keep", [None, 8])
+def test_steps_without_tokens_and_on_streams_of_either_kind(keep):
+    """No sequence brings a token: nothing but a decay of the weights; then a step on a stream given as an object, as a number, or not."""
+    import torch
+    heads, hq, d, n = 2, 4, 64, 3
+    table = zl.rotary_table(zl.rotary_frequencies(d)[0])
+    g = torch.Generator().manual_seed(79)
+    qkv, at = torch.randn(n, hq + 2 * heads, d, generator=g).bfloat16().cuda(), torch.full((n,), 6, dtype=torch.int32).cuda()
+    results = []
+    for stream in (None, torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        c = zl.allocate_kv4(n, 2, heads, d, page=16)
+        bufs = zl.allocate_kv4_attention(c, n, hq, evicts=True)
+        none = zl.allocate_kv4_attention(c, 0, hq, evicts=True, state=bufs)
+        c.lens.fill_(6)
+        bufs["weights"].fill_(2.0)
+        torch.cuda.synchronize()
+        zl.qkv_attention_cached(c, qkv[:0], at[:0], table, 0.1, none, starts=torch.zeros(n + 1, dtype=torch.int32).cuda(), keep=keep,
+                                recent=2, decay=0.5, stream=stream)
+        torch.cuda.synchronize()
+        assert (bufs["weights"][:, :, :6] == (2.0 if keep is None else 1.0)).all() and (c.lens == 6).all()
+        with torch.cuda.stream(None if stream is None else stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)):
+            c.lens.add_(1)
+        zl.qkv_attention_cached(c, qkv, at, table, 0.1, bufs, keep=keep, recent=2, stream=stream)
+        assert zl.zl_kv4_get_device_status(c) == 0
+        assert (bufs["positions"][:, :, 6] == 6).all() and (c.lens == 7).all()
+        assert keep is not None or (bufs["weights"][:, :, 6] == 0).all()
+        results.append([bufs[x].clone() for x in ("o", "lse", "weights", "positions")] + [c.data])
+    for other in results[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(results[0], other))
