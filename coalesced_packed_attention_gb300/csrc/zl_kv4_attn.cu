@@ -18,8 +18,8 @@
 // The slots of all items lie in a row that is dealt out evenly over the blocks, whatever the lengths: a block writes
 // what it holds alone; items cut between blocks leave parts (O, max, sum) that a second launch joins in order.  Short
 // items go to a block or a cluster of blocks each instead, which joins them itself.
-// Measured, 32/8 heads, d = 128: 64 single tokens behind 1 to 16 384 slots 85 us (436 MB, 5.1 TB/s; the loads without
-// arithmetic 69 us), one behind 131 071 slots 35 us and 4 for its join (151 MB).  What is above the loads is arithmetic
+// Measured, 32/8 heads, d = 128: 64 single tokens behind 1 to 16 384 slots 86 us (436 MB, 5.1 TB/s; the loads without
+// arithmetic 69 us), one behind 131 071 slots 34 us and 6 for its join (151 MB).  What is above the loads is arithmetic
 // that they do not hide: some 595 instructions for 32 slots, 256 of them conversions and products at half rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -10,7 +10,7 @@
 // head's blocks also make its moves where they are few; many are made by a second launch over all SMs.
 // Bound by latency at serving sizes (seven exchanges and three trips to memory), by the weights' and positions' bytes
 // past them.  Measured: one of 1025 slots of each of 64 heads 7.5 us; 16 384 slots of 4 heads to 2048 15 us and 4.5 for
-// the moves; 32 x 8 heads of 100 to 8192 slots to 2048, d = 64, 22 us and 20.
+// the moves; 32 x 8 heads of 100 to 8192 slots to 2048, d = 64, 22 us and 21.
 #include <cuda_runtime.h>
 
 #include "zl_internal.h"
