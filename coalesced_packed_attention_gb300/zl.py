@@ -928,6 +928,7 @@ class Kv4Cache:
     lens: "object"
     status: "object" = None
     desc: zl_kv4_cache = field(init=False, repr=False, compare=False)
+    no_rows: zl_kv4_cache = field(init=False, repr=False, compare=False)  # of no pages: calls on it note slots alone
     device: int = field(init=False, default=-1, repr=False)
     slots: int = field(init=False, default=0, repr=False)        # that the table has room for
     token_shape: tuple = field(init=False, default=(), repr=False)  # key heads, d
@@ -953,8 +954,9 @@ class Kv4Cache:
         status = _dense(self.status, "status", torch.int32, (1,), dev)
         desc = zl_kv4_cache(n, heads, width // 18, 16 * tiles, most, n_pages, self.data.data_ptr(), pages, lens, status)
         _check(load_library().zl_kv4_evict_workspace(ctypes.byref(desc), ctypes.byref(ctypes.c_int64())), "Kv4Cache")
-        for name, x in (("desc", desc), ("device", dev), ("slots", most * 16 * tiles), ("token_shape", (heads, width // 18)),
-                        ("slot_shape", (n, heads, most * 16 * tiles))):
+        no_rows = zl_kv4_cache(n, heads, width // 18, 16 * tiles, most, 0, None, pages, lens, None)
+        for name, x in (("desc", desc), ("no_rows", no_rows), ("device", dev), ("slots", most * 16 * tiles),
+                        ("token_shape", (heads, width // 18)), ("slot_shape", (n, heads, most * 16 * tiles))):
             object.__setattr__(self, name, x)
 
 
@@ -1126,43 +1128,14 @@ def allocate_kv4_attention(cache: Kv4Cache, n_tokens: int, n_q_heads: int, max_n
            "o": torch.empty(n_tokens, n_q_heads, d, **bf),
            "lse": torch.empty(n_tokens, n_q_heads, dtype=torch.float32, device=device),
            "workspace": torch.empty(max(16, ws), dtype=torch.uint8, device=device)}
+    if evicts or state is not None:
+        out["zeros"] = torch.zeros(n_tokens, dtype=torch.int32, device=device)
     if state is not None:
         out["weights"], out["positions"] = state["weights"], state["positions"]
     elif evicts:
         out["weights"] = torch.zeros(cache.slot_shape, dtype=torch.float32, device=device)
         out["positions"] = torch.zeros(cache.slot_shape, dtype=torch.int32, device=device)
     return out
-
-
-def _kv4_zero_new(cache: Kv4Cache, weights, starts):
-    """The new tokens' slots of weights, and those behind them, which are not in use, become 0."""
-    torch = _torch()
-    new = 1 if starts is None else starts[1:] - starts[:-1]
-    slot = torch.arange(cache.slots, dtype=torch.int32, device=weights.device)
-    weights.masked_fill_(slot >= (cache.lens - new)[:, None, None], 0.0)
-
-
-def _kv4_check_step(cache: Kv4Cache, n: int, hq: int, scale, bufs, starts, max_new, keep, recent, decay):
-    """Raises what one of a step's calls would refuse, before the first of them changes anything."""
-    torch = _torch()
-    dev, d = _kv4_dev(cache), cache.token_shape[1]
-    nbytes = zl_kv4_attn_workspace_bytes(cache, hq, max_new, keep is not None)
-    if keep is not None:
-        _kv4_check_budget(keep, recent)
-        nbytes = max(nbytes, zl_kv4_evict_workspace_bytes(cache))
-        if cache.slot_shape[0] > 65535:
-            _check(ZL_ERR_UNSUPPORTED, "keep, more than 65535 sequences")
-    at = _dense(bufs["o"], "o", torch.bfloat16, (n, hq, d), dev) | _scratch(bufs["workspace"], "workspace", nbytes, dev)
-    _dense(bufs["lse"], "lse", torch.float32, (n, hq), dev)
-    if "weights" in bufs:
-        _dense(bufs["weights"], "weights", torch.float32, cache.slot_shape, dev)
-        _dense(bufs["positions"], "positions", torch.int32, cache.slot_shape, dev)
-    _kv4_starts(cache, starts, dev)
-    if at % 16:
-        _check(ZL_ERR_ALIGN, "o, workspace")
-    s, f = ctypes.c_float(scale).value, ctypes.c_float(decay).value
-    if not 2.0 ** -126 <= s < float("inf") or f - f != 0.0 or (starts is None and n != cache.slot_shape[0]):
-        _check(ZL_ERR_INVALID_ARG, "scale, decay, tokens without starts")
 
 
 def qkv_attention_cached(cache: Kv4Cache, qkv, positions, table: Optional[RotaryTable], scale: float, bufs: dict, q_weight=None,
@@ -1186,30 +1159,46 @@ def qkv_attention_cached(cache: Kv4Cache, qkv, positions, table: Optional[Rotary
         raise ValueError("keep: needs buffers that were allocated with evicts=True")
     if w is not None and (not isinstance(positions, torch.Tensor) or positions.numel() != qkv.shape[0]):
         raise ValueError("buffers with weights: need one position a token")
-    hq = qkv.shape[1] - 2 * heads
-    _kv4_check_step(cache, qkv.shape[0], hq, scale, bufs, starts, max_new, keep, recent, decay)
+    n, hq, dev = qkv.shape[0], qkv.shape[1] - 2 * heads, _kv4_dev(cache)
     q, k, v = qkv[:, :hq], qkv[:, hq:hq + heads], qkv[:, hq + heads:]
+    # all that one of the calls would refuse is refused here, before the first of them changes anything
+    nbytes = zl_kv4_attn_workspace_bytes(cache, hq, max_new, keep is not None)
+    if keep is not None:
+        _kv4_check_budget(keep, recent)
+        nbytes = max(nbytes, zl_kv4_evict_workspace_bytes(cache))
+        if cache.slot_shape[0] > 65535:
+            _check(ZL_ERR_UNSUPPORTED, "keep, more than 65535 sequences")
+    (pq, nq), (pk, nk) = _heads(bufs["q"], "q", (n, hq, d), dev), _heads(bufs["k"], "k", (n, heads, d), dev)
+    pv, nv = _heads(v, "qkv", (n, heads, d), dev)
+    po, plse = _dense(bufs["o"], "o", torch.bfloat16, (n, hq, d), dev), _dense(bufs["lse"], "lse", torch.float32, (n, hq), dev)
+    ws, ps = _scratch(bufs["workspace"], "workspace", nbytes, dev), _kv4_starts(cache, starts, dev)
+    pw = pat = ppos = pzero = None
+    if w is not None:
+        pw = _dense(w, "weights", torch.float32, cache.slot_shape, dev)
+        pat = _dense(at, "positions", torch.int32, cache.slot_shape, dev)
+        ppos = _dense(positions.view(-1), "positions", torch.int32, (n,), dev)
+        pzero = _dense(bufs["zeros"], "zeros", torch.int32, (n,), dev) if keep is None else None
+    if n and (pq | pk | pv | po | ws | 2 * nq | 2 * nk | 2 * nv) % 16:
+        _check(ZL_ERR_ALIGN, "qkv, q, k, o, workspace")
+    scale32, decay32 = ctypes.c_float(scale).value, ctypes.c_float(decay).value
+    if not 2.0 ** -126 <= scale32 < float("inf") or decay32 - decay32 != 0.0 or (starts is None and n != cache.slot_shape[0]):
+        _check(ZL_ERR_INVALID_ARG, "scale, decay, tokens without starts")
     for of_q, of_k, norm in _sides(q_weight, k_weight):
         zl_qk_rope_fwd(q if of_q else None, k if of_k else None, bufs["q"] if of_q else None, bufs["k"] if of_k else None,
                        positions, table, norm, q_weight if of_q else None, k_weight if of_k else None, eps, stream)
-    if w is None:
-        zl_kv4_write(cache, bufs["k"], v, starts, stream=stream)
-    else:
-        zl_kv4_write(cache, bufs["k"], v, starts, positions.view(-1), at, stream)
+    lib, raw, desc = load_library(), _raw_stream(stream, dev), cache.desc
+    _check(lib.zl_kv4_write(desc, pk, nk, pv, nv, n, ps, ppos, pat, raw), "zl_kv4_write")
     if keep is None:
-        zl_kv4_attn_fwd(cache, bufs["q"], bufs["o"], bufs["lse"], bufs["workspace"], scale, starts, max_new, stream=stream)
-    else:
-        zl_kv4_attn_fwd(cache, bufs["q"], bufs["o"], bufs["lse"], bufs["workspace"], scale, starts, max_new, w, w, decay, stream)
-        zl_kv4_evict(cache, w, at, keep, recent, bufs["workspace"], stream=stream)
-    if w is None:
+        if w is not None:  # the same tokens' slots of the weights: 0, which has the bits of the position 0
+            _check(lib.zl_kv4_write(cache.no_rows, pk, nk, pv, nv, n, ps, pzero, pw, raw), "zl_kv4_write")
+        _check(lib.zl_kv4_attn_fwd(desc, pq, nq, n, hq, ps, max_new, po, plse, None, None, 1.0, ws, scale, raw), "zl_kv4_attn_fwd")
         return bufs
+    _check(lib.zl_kv4_attn_fwd(desc, pq, nq, n, hq, ps, max_new, po, plse, pw, pw, decay, ws, scale, raw), "zl_kv4_attn_fwd")
+    _check(lib.zl_kv4_evict(desc, pw, pat, keep, recent, pw, pat, ws, raw), "zl_kv4_evict")
     if stream is not None and not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_raw_stream(stream, cache.device), cache.data.device)
+        stream = torch.cuda.ExternalStream(raw, cache.data.device)
     with torch.cuda.stream(stream):  # None: the current one
-        if keep is None:
-            _kv4_zero_new(cache, w, starts)
-        else:
-            cache.lens.clamp_(max=keep)
+        cache.lens.clamp_(max=keep)
     return bufs
 
 

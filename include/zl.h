@@ -574,7 +574,7 @@ typedef struct {
  * below 0 and tokens of no sequence are left out.  Each block of 16 channels takes the scale nearest to its
  * largest magnitude / 6 and each channel the nearest code, ties to even; NaN is held as 0, infinities as the largest
  * magnitude, 6 * 2^13.  positions (device int32 [n_tokens]) and slot_positions (int32 [n_seqs, n_kv_heads,
- * max_pages * page]), both or neither: the slot's position becomes the token's, for eviction.
+ * max_pages * page]), both or neither: the slot's position becomes the token's, for eviction (also where its page is bad).
  * Accumulated weights are not its own: zl_kv4_attn_fwd with weights begins new tokens' slots at 0, and after an
  * attention without weights the caller sets theirs.
  * Pages that it writes belong to one sequence alone. */

@@ -408,3 +408,21 @@ def test_steps_without_tokens_and_on_streams_of_either_kind(keep):
         results.append([bufs[x].clone() for x in ("o", "lse", "weights", "positions")] + [c.data])
     for other in results[1:]:
         assert all(torch.equal(x, y) for x, y in zip(results[0], other))
+
+
+def test_a_sequence_whose_tokens_do_not_fit_keeps_its_weights_and_positions():
+    import torch
+    heads, hq, d = 2, 4, 64
+    c = zl.allocate_kv4(2, 2, heads, d, page=16)
+    bufs = zl.allocate_kv4_attention(c, 4, hq, max_new=9, evicts=True)
+    bufs["weights"].fill_(2.0)
+    bufs["positions"].fill_(5)
+    c.lens.fill_(20)
+    qkv, at = torch.ones(4, hq + 2 * heads, d).bfloat16().cuda(), torch.arange(4, dtype=torch.int32).cuda()
+    starts = torch.tensor([0, 2, 9], dtype=torch.int32).cuda()
+    zl.qkv_attention_cached(c, qkv, at, zl.rotary_table(zl.rotary_frequencies(d)[0]), 0.1, bufs, starts=starts, max_new=9)
+    assert zl.zl_kv4_get_device_status(c) == zl.ZL_KV4_BAD_STARTS
+    w, pos = bufs["weights"].cpu(), bufs["positions"].cpu()
+    assert (w[1] == 2.0).all() and (pos[1] == 5).all()
+    assert (w[0, :, 18:20] == 0).all() and (w[0, :, :18] == 2.0).all() and (w[0, :, 20:] == 2.0).all()
+    assert (pos[0, :, 18:20] == torch.tensor([0, 1])).all() and (pos[0, :, :18] == 5).all()
